@@ -12,11 +12,10 @@
 #include <atomic>
 #include <mutex>
 
+#include "api.h"
 #include "gbattn.h"
 #include "internal.h"
 #include "ptx.cuh"
-
-#define GBATTN_API extern "C" __attribute__((visibility("default")))
 
 namespace gbattn {
 
@@ -26,13 +25,6 @@ __device__ unsigned int g_flags_word;
 namespace {
 
 constexpr int kMaxDevices = 64;
-
-struct DeviceState {
-  bool initialized = false;
-  int status = ATTN_OK;
-  int num_sms = 0;
-  unsigned* flags = nullptr;
-};
 
 std::mutex g_mutex;
 DeviceState g_dev[kMaxDevices];
@@ -53,7 +45,8 @@ void init_encode() {
   g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
 }
 
-// One-time per-device checks and kernel attributes; returns a status.
+}  // namespace
+
 int device_state(DeviceState** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return ATTN_ERR_CUDA;
@@ -87,9 +80,6 @@ int encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
   return g_encode_status;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Tiled map over a bf16 tensor of `rank` dims (innermost first), 128-byte swizzle.
 int encode_bf16(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* base,
                 int rank, const uint64_t* dims, const uint64_t* strides_bytes,
                 const uint32_t* box) {
@@ -108,8 +98,6 @@ int encode_bf16(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const v
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
-
-constexpr uint64_t kMaxDim = 1ull << 31;  // keeps every TMA coordinate inside int32
 
 // Limit of every pipeline wait inside the kernels (ns); see attn_test_set_failure.
 std::atomic<unsigned long long> g_wait_limit_ns{kWaitLimitNs};
@@ -140,7 +128,6 @@ FwdParams fwd_params(void* o, float* lse, int B, int Hq, int Hkv, int Tq, int Tk
   return p;
 }
 
-}  // namespace
 }  // namespace gbattn
 
 using namespace gbattn;

@@ -1,0 +1,353 @@
+// api_rope.cu -- C entry points of the norm + rotation pass, of the cache appends built
+// on it, and of the 4-bit cache (include/gbattn.h): argument checks and launches, under
+// the rules of api.cu.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "api.h"
+#include "gbattn.h"
+#include "internal.h"
+#include "norm_rope.h"
+
+using namespace gbattn;
+
+namespace {
+
+constexpr int64_t kMaxStride = 1ll << 48;
+
+bool good_strides(const int64_t* s) {
+  if (!s) return false;
+  for (int i = 0; i < 3; ++i)
+    if (s[i] < 0 || s[i] > kMaxStride || s[i] % 8 != 0) return false;
+  return true;
+}
+
+// Whether a written [B, T, H, D] layout gives every element a place of its own: taken
+// from the smallest stride up, each dimension steps past everything below it.
+bool distinct_places(const int64_t* s, int B, int T, int H, int D) {
+  struct Dim {
+    int64_t stride, size;
+  } d[3] = {{s[0], B}, {s[1], T}, {s[2], H}};
+  std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  __int128 extent = D;
+  for (const Dim& x : d) {
+    if (x.size <= 1) continue;
+    if (x.stride < extent) return false;
+    extent += static_cast<__int128>(x.stride) * (x.size - 1);
+  }
+  return true;
+}
+
+Heads heads(const void* p, const int64_t* s) {
+  Heads h{};
+  h.p = static_cast<uint16_t*>(const_cast<void*>(p));
+  if (p) {
+    h.sb = s[0];
+    h.st = s[1];
+    h.sh = s[2];
+  }
+  return h;
+}
+
+// Checks that need no sizes of the batch: ATTN_OK, or what is wrong.
+int check_rope(const void* q_weight, const void* k_weight, const float* cos_sin,
+               const int32_t* positions, int D, int rot_dim, int max_pos, int interleaved,
+               float eps) {
+  if (interleaved != 0 && interleaved != 1) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || !(eps > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > D || (rot_dim > 0 && max_pos <= 0)) return ATTN_ERR_INVALID_ARG;
+  if (rot_dim % 8 != 0) return ATTN_ERR_UNSUPPORTED;
+  if ((rot_dim > 0) != (cos_sin != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(cos_sin, 16) ||
+      !aligned(positions, 4))
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+RopeParams rope_params(const void* q_weight, const void* k_weight, const float* cos_sin,
+                       const int32_t* positions, int rot_dim, int max_pos, int interleaved,
+                       float eps) {
+  RopeParams r{};
+  r.q_weight = static_cast<const uint16_t*>(q_weight);
+  r.k_weight = static_cast<const uint16_t*>(k_weight);
+  r.cos_sin = cos_sin;
+  r.positions = positions;
+  r.eps = eps;
+  r.rot = rot_dim;
+  r.max_pos = max_pos;
+  r.interleaved = interleaved;
+  return r;
+}
+
+// An input operand: present with good strides and a 16-byte aligned base.
+bool good_input(const void* p, const int64_t* s) { return p && aligned(p, 16) && good_strides(s); }
+
+bool too_many_rows(int B, int T, int Hq, int Hkv) {
+  const unsigned __int128 n = static_cast<unsigned __int128>(B) * T;
+  return n >= kMaxDim * 8 || n * (static_cast<uint64_t>(Hq) + 2ull * Hkv) >= (1ull << 34);
+}
+
+bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bytes && y < x + bytes;
+}
+
+// The two appends: four = into the 4-bit pool (k_pool), else into the bf16 pools.
+int append(bool four, const void* q, const void* k, const void* v, const int64_t* q_strides,
+           const int64_t* k_strides, const int64_t* v_strides, const void* q_weight,
+           const void* k_weight, const float* cos_sin, const int32_t* positions, void* k_pool,
+           void* v_pool, const int32_t* block_table, const int32_t* seq_lens,
+           int32_t* new_seq_lens, int block_size, int num_seqs, int Tn, int Hq, int Hkv, int D,
+           int max_blocks_per_seq, int num_pool_blocks, int rot_dim, int max_pos, int interleaved,
+           float eps, void* q_out, void* stream) {
+  if (num_seqs < 0 || Tn < 0 || Hq < 0 || Hkv <= 0 || max_blocks_per_seq <= 0 ||
+      num_pool_blocks <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (block_size != 16 || (D != 64 && D != 128)) return ATTN_ERR_UNSUPPORTED;
+  int st = check_rope(q_weight, k_weight, cos_sin, positions, D, rot_dim, max_pos, interleaved,
+                      eps);
+  if (st != ATTN_OK) return st;
+  if (num_seqs == 0 || Tn == 0) return ATTN_OK;
+  if ((q != nullptr) != (q_out != nullptr) || (q && Hq == 0)) return ATTN_ERR_INVALID_ARG;
+  if (q && (!good_input(q, q_strides) || !aligned(q_out, 16))) return ATTN_ERR_INVALID_ARG;
+  if (!good_input(k, k_strides) || !good_input(v, v_strides)) return ATTN_ERR_INVALID_ARG;
+  if (!k_pool || !aligned(k_pool, 16) || (!four && (!v_pool || !aligned(v_pool, 16))) ||
+      !block_table || !aligned(block_table, 4) || !seq_lens || !aligned(seq_lens, 4) ||
+      !aligned(new_seq_lens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  // the lengths are read by every CTA while one of them writes the new ones
+  if (new_seq_lens && overlap(seq_lens, new_seq_lens, sizeof(int32_t) * num_seqs))
+    return ATTN_ERR_INVALID_ARG;
+  if (too_many_rows(num_seqs, Tn, q ? Hq : 0, Hkv) ||
+      static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim ||
+      static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim)
+    return ATTN_ERR_UNSUPPORTED;
+  DeviceState* ds = nullptr;
+  if ((st = device_state(&ds)) != ATTN_OK) return st;
+  NormRopeParams p{};
+  p.q = heads(q, q_strides);
+  p.k = heads(k, k_strides);
+  p.v = heads(v, v_strides);
+  p.rope = rope_params(q_weight, k_weight, cos_sin, positions, rot_dim, max_pos, interleaved, eps);
+  p.B = num_seqs;
+  p.T = Tn;
+  p.nq = q ? Hq : 0;
+  p.nk = p.nv = Hkv;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  if (four) {
+    p.kv4_pool = static_cast<uint8_t*>(k_pool);
+  } else {
+    p.k_pool = static_cast<uint16_t*>(k_pool);
+    p.v_pool = static_cast<uint16_t*>(v_pool);
+  }
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.new_seq_lens = new_seq_lens;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_pool_blocks = num_pool_blocks;
+  p.flags = ds->flags;
+  return launch_norm_rope(p, D, four ? RowSink::kPaged4 : RowSink::kPaged, ds->num_sms,
+                          static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+GBATTN_API int qkv_norm_rope(const void* q, const void* k, const void* v, const int64_t* q_strides,
+                             const int64_t* k_strides, const int64_t* v_strides,
+                             const void* q_weight, const void* k_weight, const float* cos_sin,
+                             const int32_t* positions, int B, int T, int Hq, int Hkv, int D,
+                             int rot_dim, int max_pos, int interleaved, float eps, void* q_out,
+                             void* k_out, void* v_out, void* stream) {
+  if (B < 0 || T < 0 || Hq < 0 || Hkv < 0) return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  int st = check_rope(q_weight, k_weight, cos_sin, positions, D, rot_dim, max_pos, interleaved,
+                      eps);
+  if (st != ATTN_OK) return st;
+  if (B == 0 || T == 0) return ATTN_OK;
+  const struct {
+    const void* in;
+    const int64_t* strides;
+    const void* out;
+    int n;
+  } ops[3] = {{q, q_strides, q_out, Hq}, {k, k_strides, k_out, Hkv}, {v, v_strides, v_out, Hkv}};
+  if (!q && !k && !v) return ATTN_ERR_INVALID_ARG;
+  for (const auto& o : ops) {
+    if ((o.in != nullptr) != (o.out != nullptr)) return ATTN_ERR_INVALID_ARG;
+    if (o.in && (o.n == 0 || !good_input(o.in, o.strides) || !aligned(o.out, 16)))
+      return ATTN_ERR_INVALID_ARG;
+  }
+  if (too_many_rows(B, T, Hq, Hkv)) return ATTN_ERR_UNSUPPORTED;
+  DeviceState* ds = nullptr;
+  if ((st = device_state(&ds)) != ATTN_OK) return st;
+  NormRopeParams p{};
+  p.q = heads(q, q_strides);
+  p.k = heads(k, k_strides);
+  p.v = heads(v, v_strides);
+  p.rope = rope_params(q_weight, k_weight, cos_sin, positions, rot_dim, max_pos, interleaved, eps);
+  p.B = B;
+  p.T = T;
+  p.nq = q ? Hq : 0;
+  p.nk = k ? Hkv : 0;
+  p.nv = v ? Hkv : 0;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.v_out = static_cast<uint16_t*>(v_out);
+  p.flags = ds->flags;
+  return launch_norm_rope(p, D, RowSink::kContiguous, ds->num_sms,
+                          static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+GBATTN_API size_t qkv_norm_rope_bwd_workspace_size(int B, int T, int D) {
+  if (B <= 0 || T <= 0 || D <= 0) return 0;
+  return norm_rope_bwd_workspace_bytes(B, T, D);
+}
+
+GBATTN_API int qkv_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* dv_out,
+                                 const void* q, const void* k, const int64_t* q_strides,
+                                 const int64_t* k_strides, const void* q_weight,
+                                 const void* k_weight, const float* cos_sin,
+                                 const int32_t* positions, int B, int T, int Hq, int Hkv, int D,
+                                 int rot_dim, int max_pos, int interleaved, float eps, void* dq,
+                                 void* dk, void* dv, const int64_t* dq_strides,
+                                 const int64_t* dk_strides, const int64_t* dv_strides,
+                                 float* dq_weight, float* dk_weight, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (B < 0 || T < 0 || Hq < 0 || Hkv < 0) return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  int st = check_rope(q_weight, k_weight, cos_sin, positions, D, rot_dim, max_pos, interleaved,
+                      eps);
+  if (st != ATTN_OK) return st;
+  if ((q_weight != nullptr) != (dq_weight != nullptr) ||
+      (k_weight != nullptr) != (dk_weight != nullptr) || !aligned(dq_weight, 4) ||
+      !aligned(dk_weight, 4))
+    return ATTN_ERR_INVALID_ARG;
+  const bool empty = B == 0 || T == 0;
+  const bool weights = q_weight || k_weight;
+  if (empty && !weights) return ATTN_OK;
+  if (!empty) {
+    const struct {
+      const void* g;
+      const void* d;
+      const int64_t* strides;
+      int n;
+    } ops[3] = {{dq_out, dq, dq_strides, Hq}, {dk_out, dk, dk_strides, Hkv},
+                {dv_out, dv, dv_strides, Hkv}};
+    if (!dq_out && !dk_out && !dv_out) return ATTN_ERR_INVALID_ARG;
+    for (const auto& o : ops) {
+      if ((o.g != nullptr) != (o.d != nullptr)) return ATTN_ERR_INVALID_ARG;
+      if (!o.g) continue;
+      if (o.n == 0 || !aligned(o.g, 16) || !good_input(o.d, o.strides) ||
+          !distinct_places(o.strides, B, T, o.n, D))
+        return ATTN_ERR_INVALID_ARG;
+    }
+    if (q_weight && (!dq_out || !good_input(q, q_strides))) return ATTN_ERR_INVALID_ARG;
+    if (k_weight && (!dk_out || !good_input(k, k_strides))) return ATTN_ERR_INVALID_ARG;
+    if (too_many_rows(B, T, Hq, Hkv)) return ATTN_ERR_UNSUPPORTED;
+    if (weights && (!workspace || !aligned(workspace, 16) ||
+                    workspace_bytes < norm_rope_bwd_workspace_bytes(B, T, D)))
+      return ATTN_ERR_INVALID_ARG;
+  }
+  DeviceState* ds = nullptr;
+  if ((st = device_state(&ds)) != ATTN_OK) return st;
+  NormRopeBwdParams p{};
+  if (!empty) {
+    if (q_weight) p.q = heads(q, q_strides);
+    if (k_weight) p.k = heads(k, k_strides);
+    p.gq = static_cast<const uint16_t*>(dq_out);
+    p.gk = static_cast<const uint16_t*>(dk_out);
+    p.gv = static_cast<const uint16_t*>(dv_out);
+    p.dq = heads(dq, dq_strides);
+    p.dk = heads(dk, dk_strides);
+    p.dv = heads(dv, dv_strides);
+    p.nq = dq_out ? Hq : 0;
+    p.nk = dk_out ? Hkv : 0;
+    p.nv = dv_out ? Hkv : 0;
+    p.part = weights ? static_cast<float*>(workspace) : nullptr;
+  }
+  p.rope = rope_params(q_weight, k_weight, cos_sin, positions, rot_dim, max_pos, interleaved, eps);
+  p.B = B;
+  p.T = T;
+  p.dwq = dq_weight;
+  p.dwk = dk_weight;
+  p.flags = ds->flags;
+  return launch_norm_rope_bwd(p, D, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+GBATTN_API int paged_qkv_append(const void* q, const void* k, const void* v,
+                                const int64_t* q_strides, const int64_t* k_strides,
+                                const int64_t* v_strides, const void* q_weight,
+                                const void* k_weight, const float* cos_sin,
+                                const int32_t* positions, void* k_pool, void* v_pool,
+                                const int32_t* block_table, const int32_t* seq_lens,
+                                int32_t* new_seq_lens, int block_size, int num_seqs, int Tn,
+                                int Hq, int Hkv, int D, int max_blocks_per_seq,
+                                int num_pool_blocks, int rot_dim, int max_pos, int interleaved,
+                                float eps, void* q_out, void* stream) {
+  return append(false, q, k, v, q_strides, k_strides, v_strides, q_weight, k_weight, cos_sin,
+                positions, k_pool, v_pool, block_table, seq_lens, new_seq_lens, block_size,
+                num_seqs, Tn, Hq, Hkv, D, max_blocks_per_seq, num_pool_blocks, rot_dim, max_pos,
+                interleaved, eps, q_out, stream);
+}
+
+GBATTN_API int paged_kv4_append(const void* q, const void* k, const void* v,
+                                const int64_t* q_strides, const int64_t* k_strides,
+                                const int64_t* v_strides, const void* q_weight,
+                                const void* k_weight, const float* cos_sin,
+                                const int32_t* positions, void* kv_pool,
+                                const int32_t* block_table, const int32_t* seq_lens,
+                                int32_t* new_seq_lens, int block_size, int num_seqs, int Tn,
+                                int Hq, int Hkv, int D, int max_blocks_per_seq,
+                                int num_pool_blocks, int rot_dim, int max_pos, int interleaved,
+                                float eps, void* q_out, void* stream) {
+  return append(true, q, k, v, q_strides, k_strides, v_strides, q_weight, k_weight, cos_sin,
+                positions, kv_pool, nullptr, block_table, seq_lens, new_seq_lens, block_size,
+                num_seqs, Tn, Hq, Hkv, D, max_blocks_per_seq, num_pool_blocks, rot_dim, max_pos,
+                interleaved, eps, q_out, stream);
+}
+
+GBATTN_API int paged_kv4_gather(const void* kv_pool, const int32_t* block_table,
+                                const int32_t* seq_lens, int block_size, int num_seqs, int Hkv,
+                                int D, int max_blocks_per_seq, int num_pool_blocks,
+                                int max_seq_len, void* k_out, void* v_out, void* stream) {
+  if (num_seqs < 0 || Hkv <= 0 || max_blocks_per_seq <= 0 || num_pool_blocks <= 0 ||
+      max_seq_len < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (block_size != 16 || (D != 64 && D != 128)) return ATTN_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || max_seq_len == 0) return ATTN_OK;
+  if (!kv_pool || !block_table || !seq_lens || !k_out || !v_out) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(kv_pool, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  const uint64_t blocks = (static_cast<uint64_t>(max_seq_len) + 15) / 16;
+  if (static_cast<unsigned __int128>(num_seqs) * Hkv * blocks >= kMaxDim ||
+      static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim ||
+      static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim)
+    return ATTN_ERR_UNSUPPORTED;
+  DeviceState* ds = nullptr;
+  const int st = device_state(&ds);
+  if (st != ATTN_OK) return st;
+  Gather4Params p{};
+  p.pool = static_cast<const uint8_t*>(kv_pool);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.v_out = static_cast<uint16_t*>(v_out);
+  p.S = num_seqs;
+  p.Hkv = Hkv;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_pool_blocks = num_pool_blocks;
+  p.max_seq_len = max_seq_len;
+  p.flags = ds->flags;
+  return launch_kv4_gather(p, D, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}

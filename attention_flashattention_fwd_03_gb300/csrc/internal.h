@@ -115,5 +115,19 @@ cudaError_t launch_kv_gather(const CUtensorMap& tmPool, const GatherParams& p,
                              cudaStream_t stream);
 cudaError_t prepare_kv_cache();
 
+struct Gather4Params {
+  const uint8_t* pool;         // [num_pool_blocks, Hkv, 18 D]
+  const int32_t* block_table;  // [S, max_blocks]
+  const int32_t* seq_lens;     // [S]
+  uint16_t *k_out, *v_out;     // [S, Hkv, max_seq_len, D] bf16
+  int S, Hkv;
+  int max_blocks;
+  int num_pool_blocks;
+  int max_seq_len;
+  unsigned* flags;
+};
+
+// History of the 4-bit cache as bf16 rows.
+cudaError_t launch_kv4_gather(const Gather4Params& p, int D, cudaStream_t stream);
 
 }  // namespace gbattn

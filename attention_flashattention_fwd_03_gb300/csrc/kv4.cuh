@@ -1,0 +1,62 @@
+// kv4.cuh -- the 4-bit paged KV cache: format and quantiser, shared by every kernel
+// that writes or reads it.
+//
+// Format.  32 consecutive channels of one (token, KV head) share a scale
+//   s = amax / 7 rounded to 5 significant bits (ties to even), held as bf16
+//   n = clamp(round(x / s), -7, 7), held as the code n + 8
+// and stand for n s.  |n| takes 3 bits and s 5, so n s has at most 8 significant bits:
+// every value the cache stands for is a bf16, which lets the prefill kernel hand exact
+// operands to the tensor cores while the decode kernel keeps n and s apart, and both
+// compute the same attention.  A group that holds a NaN or an infinity gets s = NaN and
+// reads as NaN throughout; a group of zeros reads as zeros.
+//
+// A pool is [num_pool_blocks, Hkv, 18 D] bytes.  One (block, KV head) chunk holds
+//   K codes  [16 tokens][D / 2]     K scales [16][D / 32] bf16
+//   V codes  [16 tokens][D / 2]     V scales [16][D / 32] bf16
+// contiguously (2304 bytes at D = 128, 1152 at D = 64, 28 % of the bf16 cache), so a
+// block arrives with one untiled bulk copy.  Two codes share a byte, the even position
+// low.  The order of the codes of a row is the order in which the decode kernel's
+// matrix fragments take them straight from shared memory:
+//   K: channel c at position ((c % 32) / 8 * (D / 32) + c / 32) * 8 + c % 8
+//      -- the thread t = 0..3 of a row reads its D / 32 words (one a group) in one load
+//   V: channel c at position ((c % 32) / 4 * (D / 32) + c / 32) * 4 + c % 4
+//      -- the thread g = 0..7 of a dim reads 4 channels of every group in one load
+#pragma once
+
+#include <cstdint>
+
+#include "paged.cuh"
+
+namespace gbattn {
+
+template <int D>
+struct Kv4 {
+  static constexpr int kGroup = 32;                      // channels that share a scale
+  static constexpr int kGroups = D / kGroup;
+  static constexpr int kCodeRow = D / 2;                 // bytes of a row's codes
+  static constexpr int kScaleRow = kGroups * 2;          // bytes of a row's scales
+  static constexpr int kOffKCodes = 0;
+  static constexpr int kOffKScales = kPagedBlock * kCodeRow;
+  static constexpr int kOffVCodes = kOffKScales + kPagedBlock * kScaleRow;
+  static constexpr int kOffVScales = kOffVCodes + kPagedBlock * kCodeRow;
+  static constexpr int kChunk = kOffVScales + kPagedBlock * kScaleRow;
+  static_assert(kChunk == 18 * D, "the pool's last dimension");
+};
+
+// Scale of a group whose largest magnitude is amax (amax_bits = its bf16 bits without
+// the sign; NaN and infinity compare above every finite value): fp32 bits whose low 16
+// are zero, so the bf16 is the high half.
+__device__ __forceinline__ uint32_t kv4_scale_bits(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f80u) return 0x7fc00000u;
+  const uint32_t t = __float_as_uint(__fdiv_rn(__uint_as_float(amax_bits << 16), 7.f));
+  return (t + 0x3ffffu + ((t >> 19) & 1u)) & 0xfff80000u;  // 1 + 4 mantissa bits
+}
+
+// Code of one channel for a scale (code 8, i.e. zero, where the scale is 0 or NaN).
+__device__ __forceinline__ uint32_t kv4_code(float x, float s) {
+  if (!(s > 0.f)) return 8u;
+  const float n = fminf(fmaxf(rintf(__fdiv_rn(x, s)), -7.f), 7.f);
+  return static_cast<uint32_t>(static_cast<int>(n) + 8);
+}
+
+}  // namespace gbattn

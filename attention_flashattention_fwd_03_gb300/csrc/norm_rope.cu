@@ -1,0 +1,392 @@
+// norm_rope.cu -- from a model's QKV projection to what the attention kernels read:
+// per-head RMS norm, position rotation and relayout in one pass, with its gradients, and
+// the same pass writing K and V straight into the paged caches (bf16 or 4 bits).
+// The mathematics and the lane layout are in norm_rope.cuh, the 4-bit format in kv4.cuh.
+//
+// Forward and appends: memory-bound, each value read and written once.  A warp takes a
+// run of the rows (q, k and v heads) of one token, 32 / (D / 8) rows at a time, so its
+// table row and weights are read once and every row moves as whole 128- or 256-byte
+// segments.
+#include <cuda_runtime.h>
+
+#include "kv4.cuh"
+#include "norm_rope.cuh"
+#include "norm_rope.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace gbattn {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+
+__device__ __forceinline__ uint2 ld8(const uint16_t* p) { return *reinterpret_cast<const uint2*>(p); }
+__device__ __forceinline__ void st8(uint16_t* p, uint2 v) { *reinterpret_cast<uint2*>(p) = v; }
+
+// Table entries of the lane's four planes (1 and 0 for a lane that does not rotate).
+__device__ __forceinline__ void load_planes(const RopeParams& r, int pos, int l, bool rotates,
+                                            float4& co, float4& si) {
+  co = make_float4(1.f, 1.f, 1.f, 1.f);
+  si = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (rotates) {
+    const float* row = r.cos_sin + static_cast<size_t>(pos) * r.rot;
+    co = *reinterpret_cast<const float4*>(row + 4 * l);
+    si = *reinterpret_cast<const float4*>(row + r.rot / 2 + 4 * l);
+  }
+}
+
+// Quantises one row of D bf16 (the lane's 8 channels from 8 l on, packed) into a chunk
+// of the 4-bit pool, as a K or a V row of token slot `slot`.  All lanes take part;
+// `write` is the same over a row.
+template <int D, bool IS_V>
+__device__ __forceinline__ void quantise_row(uint4 w, uint8_t* chunk, int slot, int l, bool write) {
+  using F = Kv4<D>;
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t amax = 0;  // bf16 magnitudes order like their bits, NaN and infinity on top
+#pragma unroll
+  for (int i = 0; i < 4; ++i) amax = max(amax, max(in[i] & 0x7fffu, (in[i] >> 16) & 0x7fffu));
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const uint32_t sbits = kv4_scale_bits(amax);
+  const float s = __uint_as_float(sbits);
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    codes |= kv4_code(bf16_lo(in[i]), s) << (8 * i);
+    codes |= kv4_code(bf16_hi(in[i]), s) << (8 * i + 4);
+  }
+  if (!write) return;
+  const int group = l >> 2, part = l & 3;  // channels 8 l .. 8 l + 7 of group l / 4
+  uint8_t* row = chunk + (IS_V ? F::kOffVCodes : F::kOffKCodes) + slot * F::kCodeRow;
+  if constexpr (IS_V) {
+    uint16_t* h = reinterpret_cast<uint16_t*>(row);
+    h[(2 * part) * F::kGroups + group] = static_cast<uint16_t>(codes & 0xffffu);
+    h[(2 * part + 1) * F::kGroups + group] = static_cast<uint16_t>(codes >> 16);
+  } else {
+    reinterpret_cast<uint32_t*>(row)[part * F::kGroups + group] = codes;
+  }
+  if (part == 0) {
+    uint8_t* sc = chunk + (IS_V ? F::kOffVScales : F::kOffKScales) + slot * F::kScaleRow;
+    reinterpret_cast<uint16_t*>(sc)[group] = static_cast<uint16_t>(sbits >> 16);
+  }
+}
+
+template <int D, RowSink SINK>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p) {
+  constexpr int LANES = D / 8;       // lanes of one row
+  constexpr int ROWS = 32 / LANES;   // rows of one pass
+  constexpr bool PAGED = SINK != RowSink::kContiguous;
+  // the 4-bit cache takes a K row in channel order: rows pass through shared memory
+  __shared__ __align__(16) uint16_t stage[SINK == RowSink::kPaged4 ? kWarps * ROWS * D : 8];
+  if (PAGED) {
+    // a decode launched next as a programmatic dependent may start its set-up now; it
+    // waits for this grid's writes before it reads anything
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
+  const int lane = threadIdx.x & 31;
+  const long long wid = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const long long tok = wid / p.chunks;
+  const int chunk = static_cast<int>(wid - tok * p.chunks);
+  if (tok >= static_cast<long long>(p.B) * p.T) return;
+  const int b = static_cast<int>(tok / p.T), t = static_cast<int>(tok - static_cast<long long>(b) * p.T);
+  const int l = lane % LANES, sub = lane / LANES;
+  const LaneChannels ch = lane_channels(l, p.rope.rot, p.rope.interleaved);
+
+  // ---- where this token goes, and its rotation ----
+  int pos = t;
+  bool write_kv = true;   // K and V reach the cache
+  bool live = true;       // false: the query row is NaN
+  int slot = 0;           // paged: token slot within its block
+  long long block = 0;    // paged: physical block
+  const bool first = chunk == 0 && lane == 0;
+  if constexpr (PAGED) {
+    const int L = p.seq_lens[b];
+    if (L < 0 || L > p.max_blocks * kPagedBlock - p.T) {
+      if (first && t == 0) {
+        raise_flag(p.flags, DEVFLAG_BAD_SEQLEN);
+        if (p.new_seq_lens) p.new_seq_lens[b] = L;
+      }
+      live = write_kv = false;
+    } else {
+      if (first && t == 0 && p.new_seq_lens) p.new_seq_lens[b] = L + p.T;
+      pos = L + t;
+      slot = pos % kPagedBlock;
+      block = p.block_table[static_cast<size_t>(b) * p.max_blocks + pos / kPagedBlock];
+      if (block < 0 || block >= p.num_pool_blocks) {
+        if (first) raise_flag(p.flags, DEVFLAG_BAD_BLOCK);
+        write_kv = false;
+      }
+    }
+  }
+  if (p.rope.rot > 0 && live) {
+    if (p.rope.positions) pos = p.rope.positions[tok];
+    if (pos < 0 || pos >= p.rope.max_pos) {
+      if (first) raise_flag(p.flags, DEVFLAG_BAD_POSITION);
+      live = false;
+      if (PAGED) write_kv = false;
+    }
+  }
+  float4 co, si;
+  load_planes(p.rope, pos, l, ch.rotates && live, co, si);
+
+  const int rows = p.nq + p.nk + p.nv;
+  const int row_end = min(rows, (chunk + 1) * p.rows_per_warp);
+  for (int row0 = chunk * p.rows_per_warp; row0 < row_end; row0 += ROWS) {
+    const int row = row0 + sub;
+    const bool in = row < row_end;
+    const bool is_q = row < p.nq;
+    const bool is_v = row >= p.nq + p.nk;
+    const int h = is_q ? row : (is_v ? row - p.nq - p.nk : row - p.nq);
+    const Heads& src = is_q ? p.q : (is_v ? p.v : p.k);
+    // V rows are taken in channel order
+    const int c0 = is_v ? 8 * l : ch.c0, c1 = is_v ? 8 * l + 4 : ch.c1;
+    uint2 a = make_uint2(0, 0), c = make_uint2(0, 0);
+    if (in) {
+      const uint16_t* x = src.p + b * src.sb + t * src.st + h * src.sh;
+      a = ld8(x + c0);
+      c = ld8(x + c1);
+    }
+    float x[8];
+    widen8(a, c, x);
+    const float r = row_rrms<D>(x, p.rope.eps);
+    const uint16_t* w = is_q ? p.rope.q_weight : p.rope.k_weight;
+    if (!is_v) {
+      if (w) {
+        float wf[8];
+        widen8(ld8(w + c0), ld8(w + c1), wf);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wf[i];
+      }
+      if (ch.rotates) rotate8<false>(x, co, si, p.rope.interleaved);
+      round8(x, a, c);
+      if (!live) a = c = make_uint2(kBf16NanPair, kBf16NanPair);
+    }
+    if (is_q || !PAGED) {
+      if (in) {
+        uint16_t* base = is_q ? p.q_out : (is_v ? p.v_out : p.k_out);
+        const int heads = is_q ? p.nq : (is_v ? p.nv : p.nk);
+        uint16_t* y = base + ((static_cast<long long>(b) * heads + h) * p.T + t) * D;
+        st8(y + c0, a);
+        st8(y + c1, c);
+      }
+    } else if constexpr (SINK == RowSink::kPaged) {
+      if (in && write_kv) {
+        uint16_t* y = (is_v ? p.v_pool : p.k_pool) +
+                      ((block * p.nk + h) * kPagedBlock + slot) * static_cast<long long>(D);
+        st8(y + c0, a);
+        st8(y + c1, c);
+      }
+    }
+    if constexpr (SINK == RowSink::kPaged4) {
+      // every lane of the warp takes part: the quantiser exchanges between lanes
+      const bool any_kv = __any_sync(0xffffffffu, in && !is_q);
+      if (any_kv) {
+        uint16_t* mine = stage + ((threadIdx.x >> 5) * ROWS + sub) * D;
+        st8(mine + c0, a);
+        st8(mine + c1, c);
+        __syncwarp();
+        const uint4 w8 = *reinterpret_cast<const uint4*>(mine + 8 * l);
+        uint8_t* dst = p.kv4_pool + (block * p.nk + h) * Kv4<D>::kChunk;
+        quantise_row<D, false>(w8, dst, slot, l, in && write_kv && !is_q && !is_v);
+        quantise_row<D, true>(w8, dst, slot, l, in && write_kv && is_v);
+        __syncwarp();
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(NormRopeParams p, int D, RowSink sink, int num_sms,
+                             cudaStream_t stream) {
+  const int rows = p.nq + p.nk + p.nv;
+  const long long tokens = static_cast<long long>(p.B) * p.T;
+  if (tokens <= 0 || rows <= 0) return cudaSuccess;
+  const int per_pass = 256 / D;
+  p.rows_per_warp = per_pass * 8;
+  p.chunks = (rows + p.rows_per_warp - 1) / p.rows_per_warp;
+  const long long grid = (tokens * p.chunks + kWarps - 1) / kWarps;
+  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  const dim3 g(static_cast<unsigned>(grid));
+  auto run = [&](auto d) {
+    constexpr int DD = decltype(d)::value;
+    if (sink == RowSink::kContiguous)
+      norm_rope_kernel<DD, RowSink::kContiguous><<<g, kThreads, 0, stream>>>(p);
+    else if (sink == RowSink::kPaged)
+      norm_rope_kernel<DD, RowSink::kPaged><<<g, kThreads, 0, stream>>>(p);
+    else
+      norm_rope_kernel<DD, RowSink::kPaged4><<<g, kThreads, 0, stream>>>(p);
+  };
+  if (D == 64)
+    run(std::integral_constant<int, 64>{});
+  else
+    run(std::integral_constant<int, 128>{});
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+// With dy = R^T g (g the gradient of the rotated row), xh = x r and u = dy * w:
+//   dx = r (u - xh mean(u xh))      dw = sum over tokens and heads of dy xh
+// (no weight: dx = dy).  One warp a token at a time; the lane's eight channels are the
+// same in every row, so the weight gradients stay in registers until the CTA has seen
+// all of its tokens.  They are then summed over the CTA in shared memory and written as
+// one partial per CTA; a second kernel adds the partials.  No atomics: the order of
+// every sum depends on the sizes alone.
+namespace {
+
+constexpr int kBwdMaxGrid = 456;  // three CTAs on each of 152 SMs
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
+  constexpr int LANES = D / 8;
+  constexpr int ROWS = 32 / LANES;
+  __shared__ float red[kWarps * ROWS][2][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int l = lane % LANES, sub = lane / LANES;
+  const LaneChannels ch = lane_channels(l, p.rope.rot, p.rope.interleaved);
+  const long long tokens = static_cast<long long>(p.B) * p.T;
+  const int rows = p.nq + p.nk + p.nv;
+  float dwq[8], dwk[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
+
+  for (long long tok = static_cast<long long>(blockIdx.x) * kWarps + warp; tok < tokens;
+       tok += static_cast<long long>(gridDim.x) * kWarps) {
+    const int b = static_cast<int>(tok / p.T);
+    const int t = static_cast<int>(tok - static_cast<long long>(b) * p.T);
+    int pos = t;
+    bool live = true;
+    if (p.rope.rot > 0) {
+      if (p.rope.positions) pos = p.rope.positions[tok];
+      if (pos < 0 || pos >= p.rope.max_pos) {
+        if (lane == 0) raise_flag(p.flags, DEVFLAG_BAD_POSITION);
+        live = false;
+      }
+    }
+    float4 co, si;
+    load_planes(p.rope, pos, l, ch.rotates && live, co, si);
+    for (int row0 = 0; row0 < rows; row0 += ROWS) {
+      const int row = row0 + sub;
+      const bool in = row < rows;
+      const bool is_q = row < p.nq;
+      const bool is_v = row >= p.nq + p.nk;
+      const int h = is_q ? row : (is_v ? row - p.nq - p.nk : row - p.nq);
+      const int heads = is_q ? p.nq : (is_v ? p.nv : p.nk);
+      const Heads& dst = is_q ? p.dq : (is_v ? p.dv : p.dk);
+      const int c0 = is_v ? 8 * l : ch.c0, c1 = is_v ? 8 * l + 4 : ch.c1;
+      uint2 ga = make_uint2(0, 0), gc = make_uint2(0, 0), xa = ga, xc = ga;
+      const uint16_t* w = is_v ? nullptr : (is_q ? p.rope.q_weight : p.rope.k_weight);
+      if (in) {
+        const uint16_t* gsrc = is_q ? p.gq : (is_v ? p.gv : p.gk);
+        const uint16_t* g = gsrc + ((static_cast<long long>(b) * heads + h) * p.T + t) * D;
+        ga = ld8(g + c0);
+        gc = ld8(g + c1);
+        if (w) {
+          const Heads& src = is_q ? p.q : p.k;
+          const uint16_t* x = src.p + b * src.sb + t * src.st + h * src.sh;
+          xa = ld8(x + c0);
+          xc = ld8(x + c1);
+        }
+      }
+      float g[8], x[8], wf[8];
+      widen8(ga, gc, g);
+      widen8(xa, xc, x);
+      if (!is_v && ch.rotates) rotate8<true>(g, co, si, p.rope.interleaved);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) wf[i] = 1.f;
+      if (w) widen8(ld8(w + c0), ld8(w + c1), wf);
+      const float r = row_rrms<D>(x, p.rope.eps);
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dot = fmaf(g[i] * wf[i], x[i] * r, dot);
+      dot = row_sum<LANES>(dot) * (1.f / D);
+      if (w) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float xh = x[i] * r;
+          const float dw = g[i] * xh;  // 0 for a row past the end: its g is 0
+          if (is_q)
+            dwq[i] += dw;
+          else
+            dwk[i] += dw;
+          g[i] = r * (g[i] * wf[i] - xh * dot);
+        }
+      }
+      if (in) {
+        if (!is_v) {
+          round8(g, ga, gc);
+          if (!live) ga = gc = make_uint2(kBf16NanPair, kBf16NanPair);
+        }
+        uint16_t* y = dst.p + b * dst.sb + t * dst.st + h * dst.sh;
+        st8(y + c0, ga);
+        st8(y + c1, gc);
+      }
+    }
+    if (!live) {  // a gradient through an unknown rotation is unknown
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = __int_as_float(0x7fc00000);
+    }
+  }
+  if (p.part == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = i < 4 ? ch.c0 + i : ch.c1 + i - 4;
+    red[warp * ROWS + sub][0][c] = dwq[i];
+    red[warp * ROWS + sub][1][c] = dwk[i];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < 2 * D; e += kThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps * ROWS; ++i) s += red[i][e / D][e % D];
+    p.part[static_cast<size_t>(blockIdx.x) * 2 * D + e] = s;
+  }
+}
+
+// Adds the partials: 32 channels a CTA, 32 strided runs of partials each (n = 0: zeros).
+__global__ void __launch_bounds__(1024)
+    norm_rope_dw_kernel(const float* part, int n, int D, float* dwq, float* dwk) {
+  __shared__ float red[32][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float s = 0.f;
+  for (int i = threadIdx.y; i < n; i += 32) s += part[static_cast<size_t>(i) * 2 * D + c];
+  red[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y != 0) return;
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
+  float* out = c < D ? dwq : dwk;
+  if (out) out[c < D ? c : c - D] = s;
+}
+
+}  // namespace
+
+int norm_rope_bwd_grid(int B, int T) {
+  const long long want = (static_cast<long long>(B) * T + kWarps - 1) / kWarps;
+  return static_cast<int>(want < kBwdMaxGrid ? want : kBwdMaxGrid);
+}
+
+size_t norm_rope_bwd_workspace_bytes(int B, int T, int D) {
+  return static_cast<size_t>(norm_rope_bwd_grid(B, T)) * 2 * D * sizeof(float);
+}
+
+cudaError_t launch_norm_rope_bwd(const NormRopeBwdParams& p, int D, cudaStream_t stream) {
+  const int grid = norm_rope_bwd_grid(p.B, p.T);
+  if (grid > 0 && p.nq + p.nk + p.nv > 0) {
+    if (D == 64)
+      norm_rope_bwd_kernel<64><<<grid, kThreads, 0, stream>>>(p);
+    else
+      norm_rope_bwd_kernel<128><<<grid, kThreads, 0, stream>>>(p);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || (p.dwq == nullptr && p.dwk == nullptr)) return e;
+  norm_rope_dw_kernel<<<2 * D / 32, dim3(32, 32), 0, stream>>>(p.part, grid, D, p.dwq, p.dwk);
+  return cudaGetLastError();
+}
+
+}  // namespace gbattn

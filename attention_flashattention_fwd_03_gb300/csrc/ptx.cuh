@@ -17,6 +17,7 @@ enum : unsigned {
   DEVFLAG_TIMEOUT = 1u << 0,      // a bounded wait gave up
   DEVFLAG_BAD_SEQLEN = 1u << 1,   // decode: seq_len < 0 or beyond the table / max_seq_len
   DEVFLAG_BAD_BLOCK = 1u << 2,    // decode: block id outside the pool
+  DEVFLAG_BAD_POSITION = 1u << 3, // rotation: position outside the table
 };
 
 // The flag word lives in the library's one device-global (api.cu); kernels get

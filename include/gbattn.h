@@ -191,7 +191,7 @@ int paged_attn_decode_noalloc(const void *q, const void *k_pool, const void *v_p
  * kernel of this library on that device stays set until the next call of this
  * function, which reports and clears it for everyone.  *flags (if not NULL) receives the raw bits: 1 = a bounded wait in
  * a kernel timed out, 2 = a decode request had an invalid length, 4 = a decode
- * block id was out of range.  Returns ATTN_ERR_DEVICE if any bit was set,
+ * block id was out of range, 8 = a position lay outside the rotation table.  Returns ATTN_ERR_DEVICE if any bit was set,
  * ATTN_ERR_CUDA if the synchronisation failed, else ATTN_OK.
  */
 int attn_device_status(unsigned int *flags);
@@ -238,6 +238,144 @@ int paged_kv_append(const void *k_new, const void *v_new, void *k_pool, void *v_
 int paged_kv_gather(const void *pool, const int32_t *block_table, const int32_t *seq_lens,
                     int block_size, int num_seqs, int Hkv, int D, int max_blocks_per_seq,
                     int num_pool_blocks, int max_seq_len, void *out, void *stream);
+
+/*
+ * qkv_norm_rope -- from the rows of a QKV projection to the operands of attn_fwd:
+ * RMS norm of every query and key head, rotation by position, and the move to
+ * [B, H, T, D], in one pass.
+ *
+ *   q [B, T, Hq, D], k, v [B, T, Hkv, D] bf16, strided: *_strides points at three
+ *                 HOST values, the batch, token and head strides in elements
+ *                 (the channels are contiguous).  Views of one fused projection
+ *                 buffer are the usual case; a stride of 0 repeats an input.
+ *   q_weight, k_weight [D] bf16, or NULL: that operand is not normalised
+ *   cos_sin       [max_pos, rot_dim] fp32, or NULL with rot_dim = 0: no rotation.
+ *                 Row p holds the rot_dim / 2 cosines, then the sines, of position
+ *                 p (any factor that scales them is applied with them)
+ *   positions     [B, T] int32, or NULL: token t sits at position t
+ *   q_out [B, Hq, T, D], k_out, v_out [B, Hkv, T, D] bf16 (written)
+ *
+ * Per row x of D channels: x * rsqrt(mean(x^2) + eps) * weight, then the first
+ * rot_dim channels turn as rot_dim / 2 planes, (i, i + rot_dim / 2) or, with
+ * interleaved = 1, (2 i, 2 i + 1): a, b -> a cos - b sin, b cos + a sin.  fp32
+ * throughout, rounded to bf16 once.  v is copied.  Any of q, k and v may be NULL
+ * together with its output; that operand is left out.  Outputs must not overlap
+ * inputs.  D must be 64 or 128, rot_dim a multiple of 8 in [0, D], eps finite and
+ * > 0, strides non-negative multiples of 8.  B = 0 or T = 0 is a no-op.
+ * A position outside [0, max_pos) makes that token's q_out and k_out rows NaN and
+ * sets flag bit 8.
+ */
+int qkv_norm_rope(const void *q, const void *k, const void *v, const int64_t *q_strides,
+                  const int64_t *k_strides, const int64_t *v_strides, const void *q_weight,
+                  const void *k_weight, const float *cos_sin, const int32_t *positions, int B,
+                  int T, int Hq, int Hkv, int D, int rot_dim, int max_pos, int interleaved,
+                  float eps, void *q_out, void *k_out, void *v_out, void *stream);
+
+/* Bytes of scratch qkv_norm_rope_bwd needs for these sizes (0 when B or T is 0). */
+size_t qkv_norm_rope_bwd_workspace_size(int B, int T, int D);
+
+/*
+ * qkv_norm_rope_bwd -- gradients of qkv_norm_rope.
+ *
+ *   dq_out [B, Hq, T, D], dk_out, dv_out [B, Hkv, T, D] bf16: gradients of the
+ *                 outputs; NULL leaves that operand out
+ *   q, k          the forward's inputs with their strides; read only where there is
+ *                 a weight, and may be NULL otherwise
+ *   dq, dk, dv    gradients of the inputs (written), [B, T, H, D] bf16 with strides
+ *                 as above; the layout must give every element a place of its own
+ *   dq_weight, dk_weight [D] fp32 (written), required with the weight and NULL
+ *                 without it: summed over tokens and heads in an order that depends
+ *                 on the sizes and on which operands take part, so they are the
+ *                 same bits on every run.  They
+ *                 are written (as zeros) for B = 0 or T = 0 too
+ *   workspace     >= qkv_norm_rope_bwd_workspace_size(...) bytes of device memory,
+ *                 16-byte aligned, needed when there is a weight; no initialisation
+ *
+ * Everything else as in qkv_norm_rope.  A position outside the table makes that
+ * token's dq and dk rows and the weight gradients NaN and sets flag bit 8.
+ */
+int qkv_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *dv_out, const void *q,
+                      const void *k, const int64_t *q_strides, const int64_t *k_strides,
+                      const void *q_weight, const void *k_weight, const float *cos_sin,
+                      const int32_t *positions, int B, int T, int Hq, int Hkv, int D, int rot_dim,
+                      int max_pos, int interleaved, float eps, void *dq, void *dk, void *dv,
+                      const int64_t *dq_strides, const int64_t *dk_strides,
+                      const int64_t *dv_strides, float *dq_weight, float *dk_weight,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * paged_qkv_append -- paged_kv_append with qkv_norm_rope on the way: the Tn new
+ * tokens of each request are normalised and rotated, K and V go into the paged
+ * cache, and the queries come out as the attention entry points read them.
+ *
+ *   q [num_seqs, Tn, Hq, D] (NULL together with q_out: no queries), k, v
+ *                 [num_seqs, Tn, Hkv, D] bf16, strided as in qkv_norm_rope
+ *   positions     [num_seqs, Tn] int32, or NULL: token t of request r is rotated by
+ *                 its place in the cache, seq_lens[r] + t
+ *   q_out         [num_seqs, Hq, Tn, D] bf16 (written); for Tn = 1 that is
+ *                 paged_attn_decode's q
+ *   k_pool/v_pool, block_table, seq_lens, new_seq_lens, block_size as in
+ *                 paged_kv_append; the rest as in qkv_norm_rope
+ *
+ * Device-side checks: a length with no room for Tn more tokens skips the request
+ * (its q_out rows become NaN, new_seq_lens keeps the length) and sets flag bit 2; a
+ * block id outside the pool skips that token's K and V and sets flag bit 4; a
+ * position outside the table skips that token's K and V, makes its q_out rows NaN
+ * and sets flag bit 8.  The slots written in one call must be distinct: two requests
+ * may share blocks only where neither appends.
+ */
+int paged_qkv_append(const void *q, const void *k, const void *v, const int64_t *q_strides,
+                     const int64_t *k_strides, const int64_t *v_strides, const void *q_weight,
+                     const void *k_weight, const float *cos_sin, const int32_t *positions,
+                     void *k_pool, void *v_pool, const int32_t *block_table,
+                     const int32_t *seq_lens, int32_t *new_seq_lens, int block_size, int num_seqs,
+                     int Tn, int Hq, int Hkv, int D, int max_blocks_per_seq, int num_pool_blocks,
+                     int rot_dim, int max_pos, int interleaved, float eps, void *q_out,
+                     void *stream);
+
+/*
+ * The 4-bit paged KV cache.  A pool is [num_pool_blocks, Hkv, 18 D] bytes, 16-byte
+ * aligned; one chunk of 18 D bytes holds a block's 16 tokens of one KV head:
+ *
+ *   K codes [16][D / 2], K scales [16][D / 32] bf16, V codes, V scales alike
+ *
+ * 32 consecutive channels share a scale s: the largest magnitude / 7 rounded to 5
+ * significant bits.  A channel x is held as n + 8 with n = x / s rounded to even and
+ * kept in [-7, 7], and stands for n * s, which is a bf16 exactly (code 0 reads as
+ * -8).  A NaN or infinity makes its group read as NaN.  Two codes share a byte, the
+ * even position in the low half; channel c of a K row is at position
+ * (c % 32 / 8 * (D / 32) + c / 32) * 8 + c % 8, of a V row at position
+ * (c % 32 / 4 * (D / 32) + c / 32) * 4 + c % 4.
+ * A block takes 28 % of the memory of its bf16 form (2304 bytes at D = 128).
+ */
+
+/*
+ * paged_kv4_append -- paged_qkv_append into the 4-bit cache: keys are normalised,
+ * rotated and rounded to bf16, then quantised; values are quantised as they are.
+ * With rot_dim = 0 and no weights it quantises keys that are ready.  kv_pool takes
+ * the place of the two bf16 pools; everything else as in paged_qkv_append.
+ */
+int paged_kv4_append(const void *q, const void *k, const void *v, const int64_t *q_strides,
+                     const int64_t *k_strides, const int64_t *v_strides, const void *q_weight,
+                     const void *k_weight, const float *cos_sin, const int32_t *positions,
+                     void *kv_pool, const int32_t *block_table, const int32_t *seq_lens,
+                     int32_t *new_seq_lens, int block_size, int num_seqs, int Tn, int Hq, int Hkv,
+                     int D, int max_blocks_per_seq, int num_pool_blocks, int rot_dim, int max_pos,
+                     int interleaved, float eps, void *q_out, void *stream);
+
+/*
+ * paged_kv4_gather -- the values the 4-bit cache holds, in logical order.
+ *
+ *   kv_pool       [num_pool_blocks, Hkv, 18 D] bytes
+ *   k_out, v_out  [num_seqs, Hkv, max_seq_len, D] bf16: row t < seq_lens[r] of
+ *                 request r; rows past it are not written
+ *
+ * Everything else, the device-side checks included, as in paged_kv_gather.
+ */
+int paged_kv4_gather(const void *kv_pool, const int32_t *block_table, const int32_t *seq_lens,
+                     int block_size, int num_seqs, int Hkv, int D, int max_blocks_per_seq,
+                     int num_pool_blocks, int max_seq_len, void *k_out, void *v_out,
+                     void *stream);
 
 /*
  * Test hook for the kernels' failure detection (not for production use).

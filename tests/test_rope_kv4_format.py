@@ -1,0 +1,238 @@
+"""The 4-bit cache's format and the norm + rotation formulas on the CPU: what the
+references the GPU tests use must satisfy, and the argument checks of the entry points."""
+
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import pytest
+
+import attention_flashattention_fwd_03_gb300 as gb
+import rope_ref as ref
+import synth
+
+A16 = 0x100000  # an aligned address that no check dereferences
+
+
+# --------------------------------------------------------------------------- #
+# format
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("per", [8, 4])
+def test_every_channel_has_a_nibble_of_its_own(D, per):
+    assert sorted(ref.nibble(c, D, per) for c in range(D)) == list(range(D))
+
+
+def test_values_are_bf16_and_within_half_a_step():
+    bits = synth.normal_bf16(71, (400, 128), 3.0)
+    x = synth.bf16_bits_to_float(bits).astype(np.float64)
+    codes, scales = ref.quantise(bits)
+    v = ref.values(codes, scales)
+    assert np.array_equal(synth.bf16_bits_to_float(synth.float_to_bf16_bits(v.astype(np.float32))), v)
+    assert codes.min() >= 1 and codes.max() <= 15
+    s = np.repeat(synth.bf16_bits_to_float(scales).astype(np.float64), 32, -1)
+    # half a step, and what the largest channel loses where 7 s fell short of it: the
+    # scale is off by at most 2^-5 of itself
+    assert np.all(np.abs(v - x) <= s * (0.5 + 7 * 2.0 ** -5) + 1e-300)
+    inner = np.abs(x) <= 7 * s
+    assert np.all(np.abs(v - x)[inner] <= 0.5 * s[inner])
+
+
+def test_special_groups():
+    x = np.zeros((5, 64), np.float32)
+    x[1, 3] = np.nan
+    x[2, 40] = -np.inf
+    x[3, :] = 3e38
+    x[4, 0] = 1e-39  # a subnormal
+    codes, scales = ref.quantise(synth.float_to_bf16_bits(x))
+    v = ref.values(codes, scales)
+    assert np.all(v[0] == 0)
+    assert np.all(np.isnan(v[1, :32])) and np.all(v[1, 32:] == 0)
+    assert np.all(v[2, :32] == 0) and np.all(np.isnan(v[2, 32:]))
+    assert np.all(np.isfinite(v[3])) and np.allclose(v[3], 3e38, rtol=0.05)
+    assert np.all(np.isfinite(v[4]))
+
+
+# --------------------------------------------------------------------------- #
+# gradient formula against differences
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+def test_gradient_formula_matches_differences(interleaved, norm):
+    B, T, H, D, rot = 1, 2, 2, 64, 32
+    x = synth.normals(81, B * T * H * D).reshape(B, T, H, D)
+    g = synth.normals(82, B * T * H * D).reshape(B, T, H, D)
+    w = 1 + 0.1 * synth.normals(83, D) if norm else None
+    cs = ref.table(40, rot)[np.array([[5, 39]])]
+    dx, dw, _ = ref.norm_rope_bwd(g, x, w, cs, interleaved)
+    h = 1e-6
+
+    def loss(xx, ww):
+        return float((ref.norm_rope(xx, ww, cs, interleaved) * g).sum())
+
+    for i in range(0, x.size, 17):
+        e = np.zeros(x.size)
+        e[i] = h
+        e = e.reshape(x.shape)
+        d = (loss(x + e, w) - loss(x - e, w)) / (2 * h)
+        assert abs(d - dx.flat[i]) <= 1e-7 * (1 + abs(d))
+    if norm:
+        for i in range(0, D, 7):
+            e = np.zeros(D)
+            e[i] = h
+            d = (loss(x, w + e) - loss(x, w - e)) / (2 * h)
+            assert abs(d - dw[i]) <= 1e-7 * (1 + abs(d))
+
+
+# --------------------------------------------------------------------------- #
+# argument checks of the C entry points
+# --------------------------------------------------------------------------- #
+def st(*s):
+    return (ctypes.c_int64 * 3)(*s)
+
+
+GOOD = dict(q=A16, k=A16, v=A16, qs=(2048, 1024, 64), ks=(2048, 1024, 64), vs=(2048, 1024, 64),
+            qw=A16, kw=A16, cs=A16, pos=None, B=2, T=2, Hq=4, Hkv=2, D=64, rot=64, mp=100, il=0,
+            eps=1e-6)
+INV, UNS, OK = gb.ATTN_ERR_INVALID_ARG, gb.ATTN_ERR_UNSUPPORTED, gb.ATTN_OK
+
+ROPE_BAD = [
+    (dict(D=96), UNS), (dict(rot=20), UNS), (dict(rot=72), INV), (dict(rot=-8), INV),
+    (dict(rot=0), INV), (dict(cs=None), INV), (dict(cs=A16 + 4), INV), (dict(mp=0), INV),
+    (dict(il=2), INV), (dict(eps=0.0), INV), (dict(eps=float("nan")), INV),
+    (dict(eps=float("inf")), INV), (dict(qw=A16 + 2), INV), (dict(pos=A16 + 2), INV),
+    (dict(B=-1), INV), (dict(T=-1), INV), (dict(Hq=-1), INV), (dict(k=A16 + 2), INV),
+    (dict(qs=(2048, 1024, 60)), INV), (dict(ks=(-2048, 1024, 64)), INV), (dict(vs=None), INV),
+    (dict(B=0), OK), (dict(T=0), OK), (dict(B=1 << 20, T=1 << 15), UNS),
+]
+
+
+def call_fwd(kw):
+    a = GOOD | dict(qo=A16, ko=A16, vo=A16) | kw
+    s = {n: st(*a[n]) if a[n] else None for n in ("qs", "ks", "vs")}
+    return gb.lib().qkv_norm_rope(a["q"], a["k"], a["v"], s["qs"], s["ks"], s["vs"], a["qw"],
+                                  a["kw"], a["cs"], a["pos"], a["B"], a["T"], a["Hq"], a["Hkv"],
+                                  a["D"], a["rot"], a["mp"], a["il"], a["eps"], a["qo"], a["ko"],
+                                  a["vo"], None)
+
+
+@pytest.mark.parametrize("kw,code", ROPE_BAD + [
+    (dict(q=None), INV), (dict(ko=None), INV), (dict(vo=A16 + 8), INV), (dict(Hq=0), INV),
+    (dict(q=None, k=None, v=None, qo=None, ko=None, vo=None), INV),
+])
+def test_qkv_norm_rope_refusals(kw, code):
+    assert call_fwd(kw) == code
+
+
+def call_bwd(kw):
+    a = GOOD | dict(gq=A16, gk=A16, gv=A16, dq=A16, dk=A16, dv=A16, ds=(2048, 1024, 64), dqw=A16,
+                    dkw=A16, ws=A16, wsb=1 << 20) | kw
+    s = {n: st(*a[n]) if a[n] else None for n in ("qs", "ks", "ds")}
+    return gb.lib().qkv_norm_rope_bwd(a["gq"], a["gk"], a["gv"], a["q"], a["k"], s["qs"], s["ks"],
+                                      a["qw"], a["kw"], a["cs"], a["pos"], a["B"], a["T"],
+                                      a["Hq"], a["Hkv"], a["D"], a["rot"], a["mp"], a["il"],
+                                      a["eps"], a["dq"], a["dk"], a["dv"], s["ds"], s["ds"],
+                                      s["ds"], a["dqw"], a["dkw"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,code", [x for x in ROPE_BAD if "vs" not in x[0] and x[1] != OK][:-1] + [
+    (dict(B=1 << 20, T=1 << 15, ds=(1 << 25, 1024, 64)), UNS), (dict(dqw=None), INV), (dict(kw=None), INV), (dict(ws=None), INV), (dict(wsb=511), INV),
+    (dict(q=None), INV), (dict(gq=None, dq=None), INV), (dict(gv=None), INV),
+    (dict(dk=A16 + 2), INV),
+    (dict(ds=(0, 1024, 64)), INV),      # two batches in one place
+    (dict(ds=(2048, 64, 64)), INV),     # tokens over heads
+    (dict(ds=(2048, 1024, 32)), INV),   # heads over channels
+    (dict(B=0, qw=None, kw=None, dqw=None, dkw=None), OK),
+])
+def test_qkv_norm_rope_bwd_refusals(kw, code):
+    assert call_bwd(kw) == code
+
+
+def call_append(four, kw):
+    a = GOOD | dict(pool=A16, vpool=A16, bt=A16, sl=A16, nsl=None, bs=16, mb=10, nb=30,
+                    qo=A16) | kw
+    s = {n: st(*a[n]) if a[n] else None for n in ("qs", "ks", "vs")}
+    pools = (a["pool"],) if four else (a["pool"], a["vpool"])
+    f = gb.lib().paged_kv4_append if four else gb.lib().paged_qkv_append
+    return f(a["q"], a["k"], a["v"], s["qs"], s["ks"], s["vs"], a["qw"], a["kw"], a["cs"],
+             a["pos"], *pools, a["bt"], a["sl"], a["nsl"], a["bs"], a["B"], a["T"], a["Hq"],
+             a["Hkv"], a["D"], a["mb"], a["nb"], a["rot"], a["mp"], a["il"], a["eps"], a["qo"],
+             None)
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("kw,code", ROPE_BAD + [
+    (dict(bs=8), UNS), (dict(mb=0), INV), (dict(nb=0), INV), (dict(Hkv=0), INV),
+    (dict(pool=None), INV), (dict(pool=A16 + 8), INV), (dict(bt=None), INV), (dict(sl=None), INV),
+    (dict(sl=A16 + 2), INV), (dict(nsl=A16 + 4), INV), (dict(k=None), INV), (dict(v=None), INV),
+    (dict(q=None), INV), (dict(qo=None), INV), (dict(nb=1 << 28), UNS), (dict(mb=1 << 28), UNS),
+])
+def test_append_refusals(four, kw, code):
+    assert call_append(four, kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(bs=32), UNS), (dict(D=32), UNS), (dict(S=-1), INV), (dict(ml=-1), INV),
+    (dict(pool=None), INV), (dict(pool=A16 + 4), INV), (dict(ko=None), INV), (dict(vo=A16 + 2), INV),
+    (dict(sl=None), INV), (dict(S=0), OK), (dict(ml=0), OK), (dict(S=1 << 30, ml=64), UNS),
+])
+def test_kv4_gather_refusals(kw, code):
+    a = dict(pool=A16, bt=A16, sl=A16, bs=16, S=2, Hkv=2, D=64, mb=4, nb=9, ml=64, ko=A16,
+             vo=A16) | kw
+    assert gb.lib().paged_kv4_gather(a["pool"], a["bt"], a["sl"], a["bs"], a["S"], a["Hkv"],
+                                     a["D"], a["mb"], a["nb"], a["ml"], a["ko"], a["vo"],
+                                     None) == code
+
+
+# --------------------------------------------------------------------------- #
+# argument checks of the binding
+# --------------------------------------------------------------------------- #
+torch = pytest.importorskip("torch")
+
+
+def bf(*s):
+    return torch.zeros(s, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q=bf(2, 3, 4, 32)), dict(q=bf(2, 3, 4, 64).float()), dict(k=bf(2, 4, 2, 64)),
+    dict(v=bf(2, 3, 3, 64)), dict(q=bf(2, 3, 4, 128)[..., ::2]), dict(cos_sin=torch.zeros(9)),
+    dict(cos_sin=torch.zeros(9, 64, dtype=torch.float64)), dict(q_weight=torch.ones(64)),
+    dict(k_weight=bf(32)), dict(positions=torch.zeros(2, 3)),
+    dict(positions=torch.zeros(3, 2, dtype=torch.int32)), dict(q_out=bf(2, 3, 4, 64)),
+    dict(v=None, v_out=bf(2, 2, 3, 64)), dict(q=None, k=None, v=None), {},
+])
+def test_binding_refuses_bad_rope_operands(bad):
+    a = dict(q=bf(2, 3, 4, 64), k=bf(2, 3, 2, 64), v=bf(2, 3, 2, 64), cos_sin=torch.zeros(9, 64))
+    with pytest.raises(ValueError):  # with nothing bad: the tensors are not on a GPU
+        gb.qkv_norm_rope(**(a | bad))
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dk_out=bf(2, 2, 4, 64)), dict(q=None), dict(q=bf(2, 3, 5, 64)), dict(dq=bf(2, 4, 3, 64)),
+    dict(dq_weight=bf(64)), dict(k_weight=None, dk_weight=torch.zeros(64)),
+    dict(dv_out=None, dv=bf(2, 3, 2, 64)), dict(workspace=torch.zeros(8)), {},
+])
+def test_binding_refuses_bad_gradients(bad):
+    a = dict(dq_out=bf(2, 4, 3, 64), dk_out=bf(2, 2, 3, 64), dv_out=bf(2, 2, 3, 64),
+             q=bf(2, 3, 4, 64), k=bf(2, 3, 2, 64), q_weight=bf(64), k_weight=bf(64),
+             cos_sin=torch.zeros(9, 64))
+    with pytest.raises(ValueError):
+        gb.qkv_norm_rope_bwd(**(a | bad))
+
+
+@pytest.mark.parametrize("bad", [
+    dict(kv_pool=torch.zeros(9, 2, 18 * 32, dtype=torch.uint8)), dict(kv_pool=bf(9, 2, 18 * 64)),
+    dict(kv_pool=torch.zeros(9, 2, 16, 64, dtype=torch.uint8)),
+    dict(seq_lens=torch.zeros(3, dtype=torch.int32)), dict(seq_lens=torch.zeros(2)),
+    dict(block_table=torch.zeros(3, 4, dtype=torch.int32)), dict(q_out=bf(2, 4, 3, 64)),
+    dict(q=None, q_out=bf(2, 4, 1, 64)), dict(new_seq_lens=torch.zeros(3, dtype=torch.int32)), {},
+])
+def test_binding_refuses_bad_appends(bad):
+    a = dict(q=bf(2, 1, 4, 64), k=bf(2, 1, 2, 64), v=bf(2, 1, 2, 64),
+             kv_pool=torch.zeros(9, 2, 18 * 64, dtype=torch.uint8),
+             block_table=torch.zeros(2, 4, dtype=torch.int32),
+             seq_lens=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        gb.paged_kv4_append(**(a | bad))
