@@ -49,6 +49,8 @@ EXPORTS = (
     "paged_qkv_append",
     "paged_kv4_append",
     "paged_kv4_gather",
+    "paged_kv4_attn_decode_workspace_size",
+    "paged_kv4_attn_decode",
     "attn_test_set_failure",
     "attn_device_status",
     "attn_version",
@@ -115,6 +117,10 @@ def _bind(h):
     h.paged_kv4_append.restype = I
     h.paged_kv4_gather.argtypes = [P, P, P, I, I, I, I, I, I, I, P, P, P]
     h.paged_kv4_gather.restype = I
+    h.paged_kv4_attn_decode_workspace_size.argtypes = [I, I, I, I]
+    h.paged_kv4_attn_decode_workspace_size.restype = Z
+    h.paged_kv4_attn_decode.argtypes = [P] * 4 + [I] * 8 + [F, P, P, P, Z, P]
+    h.paged_kv4_attn_decode.restype = I
     h.attn_test_set_failure.argtypes = [ctypes.c_ulonglong, I]
     h.attn_test_set_failure.restype = I
     h.attn_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -655,6 +661,56 @@ def paged_kv4_gather(kv_pool, block_table, seq_lens, max_seq_len: int, k_out=Non
     if st != ATTN_OK:
         raise GbAttnError("paged_kv4_gather", st)
     return k_out, v_out
+
+
+def paged_kv4_attn_decode_workspace_size(num_seqs: int, Hq: int, D: int, max_seq_len: int) -> int:
+    return int(lib().paged_kv4_attn_decode_workspace_size(num_seqs, Hq, D, max_seq_len))
+
+
+def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
+                          scale: float | None = None, out=None, lse=None, workspace=None,
+                          return_lse: bool = True, stream=None):
+    """Single-token decode against the 4-bit paged cache through the C ABI.
+
+    q [S,Hq,D] bf16, kv_pool [NB,Hkv,18*D] uint8, block_table [S,max_blocks] int32,
+    seq_lens [S] int32 (all CUDA) -> (o [S,Hq,D] bf16, lse [S,Hq] fp32).
+    ``workspace`` (uint8 CUDA tensor) is allocated here when not given.
+    """
+    import torch
+    device = q.device if isinstance(q, torch.Tensor) else None
+    _check_bf16("q", q, 3, device)
+    S, Hq, D = q.shape
+    NB = _check_kv4("kv_pool", kv_pool, None, None, device)
+    for name, t in (("block_table", block_table), ("seq_lens", seq_lens)):
+        _check_tensor(name, t, torch.int32, None, device)
+    if kv_pool.shape[2] != 18 * D or block_table.dim() != 2 or block_table.shape[0] != S or \
+            tuple(seq_lens.shape) != (S,):
+        raise ValueError("inconsistent paged-decode shapes")
+    if out is not None:
+        _check_tensor("out", out, torch.bfloat16, (S, Hq, D), device)
+    if lse is not None:
+        _check_tensor("lse", lse, torch.float32, (S, Hq), device)
+    if workspace is not None:
+        _check_tensor("workspace", workspace, torch.uint8, None, device)
+    _require_cuda(device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        if workspace is None:
+            need = paged_kv4_attn_decode_workspace_size(S, Hq, D, max_seq_len)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        if out is None:
+            out = torch.empty_like(q)
+        if return_lse and lse is None:
+            lse = torch.empty((S, Hq), dtype=torch.float32, device=device)
+        st = lib().paged_kv4_attn_decode(q.data_ptr(), kv_pool.data_ptr(), block_table.data_ptr(),
+                                         seq_lens.data_ptr(), 16, S, Hq, kv_pool.shape[1], D,
+                                         block_table.shape[1], NB, int(max_seq_len), float(scale),
+                                         out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+                                         workspace.numel(), _stream_handle(stream, device))
+    if st != ATTN_OK:
+        raise GbAttnError("paged_kv4_attn_decode", st)
+    return out, lse
 
 
 def test_set_failure(wait_limit_ns: int = 0, withhold_copy: bool = False) -> None:

@@ -351,3 +351,43 @@ GBATTN_API int paged_kv4_gather(const void* kv_pool, const int32_t* block_table,
              ? ATTN_OK
              : ATTN_ERR_CUDA;
 }
+
+GBATTN_API size_t paged_kv4_attn_decode_workspace_size(int num_seqs, int Hq, int D,
+                                                       int max_seq_len) {
+  if (num_seqs < 0 || Hq <= 0 || D <= 0 || max_seq_len < 0) return 0;
+  return decode_workspace_bytes(num_seqs, Hq, D, max_seq_len);
+}
+
+GBATTN_API int paged_kv4_attn_decode(const void* q, const void* kv_pool,
+                                     const int32_t* block_table, const int32_t* seq_lens,
+                                     int block_size, int num_seqs, int Hq, int Hkv, int D,
+                                     int max_blocks_per_seq, int num_pool_blocks,
+                                     int max_seq_len, float scale, void* o, float* lse,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  if (num_seqs < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_blocks_per_seq <= 0 ||
+      num_pool_blocks <= 0 || max_seq_len < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if (block_size != 16 || (D != 64 && D != 128) || Hq / Hkv > 16) return ATTN_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return ATTN_OK;
+  if (!q || !kv_pool || !block_table || !seq_lens || !o || !workspace) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(o, 16) || !aligned(block_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return ATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < decode_workspace_bytes(num_seqs, Hq, D, max_seq_len))
+    return ATTN_ERR_INVALID_ARG;
+  if (static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim ||
+      static_cast<uint64_t>(num_seqs) * Hq >= kMaxDim ||
+      static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim)
+    return ATTN_ERR_UNSUPPORTED;
+  DeviceState* ds = nullptr;
+  const int st = device_state(&ds);
+  if (st != ATTN_OK) return st;
+  const DecodeParams p =
+      decode_params(q, block_table, seq_lens, num_seqs, Hq, Hkv, D, max_blocks_per_seq,
+                    num_pool_blocks, max_seq_len, scale, o, lse, workspace, ds->flags);
+  return launch_kv4_decode(static_cast<const uint8_t*>(kv_pool), p, ds->num_sms,
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}

@@ -79,6 +79,15 @@ cudaError_t launch_paged_decode(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                 const DecodeParams& p, int num_sms, cudaStream_t stream);
 cudaError_t prepare_paged_decode();
 
+// Joins the pieces in the workspace into O and LSE; a programmatic dependent of the
+// split kernel launched just before it.
+cudaError_t launch_decode_merge(const DecodeParams& p, cudaStream_t stream);
+
+// Decode over the 4-bit pool [num_pool_blocks, Hkv, 18 D] (kv4.cuh).
+cudaError_t launch_kv4_decode(const uint8_t* pool, const DecodeParams& p, int num_sms,
+                              cudaStream_t stream);
+cudaError_t prepare_kv4_decode();
+
 size_t decode_workspace_bytes(int S, int Hq, int D, int max_seq_len);
 
 struct AppendParams {

@@ -1,0 +1,531 @@
+// kv4_decode.cu -- single-token attention against the 4-bit paged cache, sm_103a.
+//
+// For a query q and a token whose K group w has codes u_c = n_c + 8 and scale s_w, and
+// whose V group has codes and scale t_w:
+//   score  = scale * sum_w s_w (sum_{c in w} q_c u_c - 8 sum_{c in w} q_c)
+//   O_c    = sum_tokens (p t_w) (u_c - 8) / sum_tokens p,    p = exp(score - max)
+// so the codes go through the matrix units as the exact bf16 numbers 128 + u (their bits
+// OR 0x4300), the scales multiply the few score and probability values instead of the
+// many cache values, and the offset 136 leaves as a constant: the score products start
+// from -136 sum q, the output products are preceded by -136 sum p t.  The offset is
+// taken out once per step of kStepBlocks blocks, before that step's products are added,
+// so no accumulator drifts to 136 times its result.  Scores, softmax statistics and
+// outputs are fp32; p t is rounded to bf16 for its product (half a step of 2^-8, as the
+// probabilities of the bf16 kernels are).
+//
+// Bound by HBM: a token and KV head take 9 D / 8 bytes, read once.  Every warp streams a
+// range of the batch's blocks by itself (decode_split.cuh): lane j of the warp copies
+// block j of a step, one untiled bulk copy of the whole chunk (codes and scales of K and
+// V), into the warp's own ring in shared memory; the table entries of a step are read one
+// step ahead of its copies.  The fragments of m16n8k16 come out of shared memory by plain
+// loads in the order the format lays down, two codes a register after one shift and one
+// three-input logic operation.  The pieces are joined by the merge kernel of
+// paged_decode.cu.
+#include <cuda_runtime.h>
+
+#include "decode_split.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+#include "norm_rope.cuh"
+#include "ptx.cuh"
+
+namespace gbattn {
+
+namespace {
+
+constexpr int kBS = kPagedBlock;
+constexpr int kMinBlocks = kDecodeMinRange / kBS;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStepBlocks = 4;  // blocks of one step: 64 tokens share a softmax update
+constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16 pair
+
+// Ring depth and CTAs per SM by query tiles (NQT = 1: groups of up to 8 query heads,
+// 2: up to 16, which needs the registers of two CTAs).
+template <int D, int NQT>
+struct Shape {
+  static constexpr int kStageBytes = kStepBlocks * Kv4<D>::kChunk;
+  static constexpr int kCtasPerSm = NQT == 1 ? 3 : 2;
+  static constexpr int kStages = (D == 64 ? 2 : 1) * (NQT == 1 ? 2 : 3);
+  static constexpr int kOffBar = kWarps * kStages * kStageBytes;
+  static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
+  static constexpr int kSmem = kOffAbort + kWarps * 4 + 128;  // slack for 128-byte alignment
+};
+
+// D = A * B + C with C left as it is.
+__device__ __forceinline__ void mma_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+        "f"(c3));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit values held across the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Nibbles i and i + 4 of w as the bf16 pair (128 + low, 128 + high).
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
+  return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+}
+
+// Token of a 16-token block that row `row` of a score tile holds.  Neighbouring rows are
+// swapped in every other pair, so that both the K loads (rows 2 a, 2 a + 1 together) and
+// the V loads (rows 0, 2, 4, 6 together) meet tokens of either parity, i.e. both halves
+// of the shared-memory banks.
+__device__ __forceinline__ int token_of_row(int row) { return row ^ ((row >> 1) & 1); }
+
+template <int N>
+__device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&r)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "4, 8 or 16 bytes");
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r[0] = v.x, r[1] = v.y;
+  } else {
+    r[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+// Scale w of a row's packed scales.
+template <int N>
+__device__ __forceinline__ float scale_of(const uint32_t (&r)[N], int w) {
+  return (w & 1) ? bf16_hi(r[w >> 1]) : bf16_lo(r[w >> 1]);
+}
+
+// One step: up to kStepBlocks consecutive blocks of one (request, KV head).
+struct Step {
+  int r, h, b, n;
+};
+
+// The step at the cursor, no longer than the segment and `left` blocks allow.
+__device__ __forceinline__ Step step_at(const Cursor& c, int left) {
+  return Step{c.r, c.h, c.b, min(kStepBlocks, min(c.nb - c.b, left))};
+}
+
+template <int D, int NQT>
+__global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
+    kv4_decode_split_kernel(const uint8_t* __restrict__ pool, const DecodeParams p) {
+  using F = Kv4<D>;
+  using C = Shape<D, NQT>;
+  constexpr int G = F::kGroups;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 127u) & ~127u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
+  const uint32_t ring_addr = sbase + warp * C::kStages * C::kStageBytes;
+  const uint32_t bars = sbase + C::kOffBar + warp * C::kStages * 8;
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kOffAbort) + warp;
+
+  // the merge kernel may be scheduled now; it waits for this grid's results
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) mbar_init(bars + 8 * s, 1);
+    *abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncwarp();
+  // the preceding kernel's writes (an append's) are complete and visible past this point
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---------------- plan: total blocks, range count, this warp's range ----------------
+  long long nbr = 0;
+  for (int r0 = 0; r0 < p.S; r0 += 32)
+    if (r0 + lane < p.S) nbr += blocks_of(p, p.seq_lens[r0 + lane]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) nbr += __shfl_xor_sync(0xffffffffu, nbr, o);
+  const long long NB = nbr * p.Hkv;
+  const long long w_cap = static_cast<long long>(gridDim.x) * kWarps;
+  const int W = NB == 0 ? 0 : static_cast<int>(max(1ll, min(w_cap, NB / kMinBlocks)));
+  const int k_w = blockIdx.x * kWarps + warp;
+  if (k_w == 0 && lane == 0) {
+    p.plan[0] = NB;
+    p.plan[1] = W;
+  }
+  if (k_w >= W) return;  // warps are independent: no barrier of the CTA follows
+  const long long lo = k_w * NB / W;
+  const int n_w = static_cast<int>((k_w + 1) * NB / W - lo);
+  Cursor at{0, 0, 0, 0, 1};
+  {
+    long long before = 0;  // blocks of requests r0 - 1 and earlier
+    bool found = false;
+    for (int r0 = 0; r0 < p.S && !found; r0 += 32) {
+      const int r = r0 + lane;
+      const int nb = r < p.S ? blocks_of(p, p.seq_lens[r]) : 0;
+      long long incl = static_cast<long long>(nb) * p.Hkv;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      incl += before;
+      const long long excl = incl - static_cast<long long>(nb) * p.Hkv;
+      const unsigned hit = __ballot_sync(0xffffffffu, nb > 0 && excl <= lo && lo < incl);
+      if (hit) {
+        found = true;
+        const int src = __ffs(hit) - 1;
+        const long long e = __shfl_sync(0xffffffffu, excl, src);
+        at.nb = __shfl_sync(0xffffffffu, nb, src);
+        at.r = r0 + src;
+        at.h = static_cast<int>((lo - e) / at.nb);
+        at.b = static_cast<int>((lo - e) % at.nb);
+        at.first = e + static_cast<long long>(at.h) * at.nb;
+      }
+      before = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (!found) return;  // lengths changed under the kernel
+  }
+
+  // ---------------- copies: one step ahead in table entries, kStages in data ----------------
+  Cursor pc = at;
+  int p_left = n_w, issued = 0;
+  const uint64_t policy = l2_policy_evict_first();  // every cache byte is read once
+  Step ps = step_at(pc, p_left);
+  auto entry = [&](const Step& s) -> int {
+    return lane < s.n ? p.block_table[static_cast<size_t>(s.r) * p.max_blocks + s.b + lane] : 0;
+  };
+  int phys = entry(ps);
+  uint32_t stage_bad = 0;  // bit s: stage s holds a block the table could not translate
+  auto issue = [&]() {     // copies step ps, then reads the table entries of the next one
+    const int s = issued % C::kStages;
+    const bool bad = lane < ps.n && (phys < 0 || phys >= p.num_pool_blocks);
+    if (bad) raise_flag(p.flags, DEVFLAG_BAD_BLOCK);
+    stage_bad = (stage_bad & ~(1u << s)) | (__any_sync(0xffffffffu, bad) ? 1u << s : 0u);
+    if (!(p.withhold_copy && issued == 0)) {  // test hook: the first step never arrives
+      if (lane == 0) mbar_arrive_expect_tx(bars + 8 * s, ps.n * F::kChunk);
+      __syncwarp();
+      if (lane < ps.n)
+        bulk_load_hint(ring_addr + s * C::kStageBytes + lane * F::kChunk,
+                       pool + (static_cast<size_t>(bad ? 0 : phys) * p.Hkv + ps.h) * F::kChunk,
+                       F::kChunk, bars + 8 * s, policy);
+    }
+    ++issued;
+    p_left -= ps.n;
+    if (p_left > 0) {
+      advance(pc, ps.n, p);
+      if (pc.r >= p.S) {
+        p_left = 0;  // lengths changed under the kernel: nothing valid to read
+      } else {
+        ps = step_at(pc, p_left);
+        phys = entry(ps);
+      }
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; i < C::kStages && p_left > 0; ++i) issue();
+
+  // ---------------- the range, step by step ----------------
+  const int g = lane >> 2, t4 = lane & 3;
+  const int group = p.group;
+  const float sl2 = p.scale_log2;
+  const uint32_t minus136[4] = {kMinus136, kMinus136, kMinus136, kMinus136};
+  uint32_t qb[D / 16][NQT][2];   // Q^T fragments in the order of the K codes
+  float q136[G][NQT][2];         // -136 sum of q over group w, queries 2 t4 (+ 1)
+  float m_q[NQT][2], l_q[NQT][2];
+  float acc[D / 16][NQT][4];     // O^T: channels 32 w + 4 g + 2 x (+ 1) of tile 2 w + x
+  Cursor c = at;
+  int c_left = n_w, taken = 0, L = 0, piece_b0 = 0;
+  bool pbad = false, ok = true;
+
+  auto begin_piece = [&]() {
+    L = p.seq_lens[c.r];
+    piece_b0 = c.b;
+    pbad = false;
+    const uint16_t* q =
+        static_cast<const uint16_t*>(p.q) + (static_cast<size_t>(c.r) * p.Hq + c.h * group) * D;
+#pragma unroll
+    for (int nt = 0; nt < NQT; ++nt) {
+      const int row = 8 * nt + g;
+#pragma unroll
+      for (int w = 0; w < G; ++w) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row < group) x = *reinterpret_cast<const uint4*>(q + row * D + 32 * w + 8 * t4);
+        // code_pair(., i) holds channels i and i + 4 of the lane's eight
+        qb[2 * w][nt][0] = __byte_perm(x.x, x.z, 0x5410);
+        qb[2 * w][nt][1] = __byte_perm(x.x, x.z, 0x7632);
+        qb[2 * w + 1][nt][0] = __byte_perm(x.y, x.w, 0x5410);
+        qb[2 * w + 1][nt][1] = __byte_perm(x.y, x.w, 0x7632);
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_bf16_16816(d, minus136, qb[2 * w][nt][0], qb[2 * w][nt][1]);
+        mma_bf16_16816(d, minus136, qb[2 * w + 1][nt][0], qb[2 * w + 1][nt][1]);
+        q136[w][nt][0] = d[0];
+        q136[w][nt][1] = d[1];
+      }
+      m_q[nt][0] = m_q[nt][1] = -INFINITY;
+      l_q[nt][0] = l_q[nt][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+        acc[j][nt][0] = acc[j][nt][1] = acc[j][nt][2] = acc[j][nt][3] = 0.f;
+    }
+  };
+  begin_piece();
+
+  while (c_left > 0) {
+    const int s = taken % C::kStages;
+    const Step st = step_at(c, c_left);
+    if (!mbar_wait_warp(bars + 8 * s, (taken / C::kStages) & 1, abort, p.flags, p.wait_limit_ns)) {
+      ok = false;
+      break;
+    }
+    pbad |= (stage_bad >> s) & 1u;
+    const uint8_t* stage = ring + s * C::kStageBytes;
+    const int n_tok = min(kBS * st.n, L - st.b * kBS);  // valid tokens of the step
+    const int row0 = token_of_row(g);                   // rows g and g + 8 of a score tile
+
+    // ---- S^T = K Q^T, group by group ----
+    float sc[kStepBlocks][NQT][4];
+#pragma unroll
+    for (int j = 0; j < kStepBlocks; ++j) {
+      if (j < st.n) {
+        const uint8_t* blk = stage + j * F::kChunk;
+        uint32_t k0[G], k1[G], s0[G / 2], s1[G / 2];
+        lds(blk + F::kOffKCodes + row0 * F::kCodeRow + t4 * (4 * G), k0);
+        lds(blk + F::kOffKCodes + (row0 + 8) * F::kCodeRow + t4 * (4 * G), k1);
+        lds(blk + F::kOffKScales + row0 * F::kScaleRow, s0);
+        lds(blk + F::kOffKScales + (row0 + 8) * F::kScaleRow, s1);
+#pragma unroll
+        for (int w = 0; w < G; ++w) {
+          const uint32_t a0[4] = {code_pair(k0[w], 0), code_pair(k1[w], 0), code_pair(k0[w], 1),
+                                  code_pair(k1[w], 1)};
+          const uint32_t a1[4] = {code_pair(k0[w], 2), code_pair(k1[w], 2), code_pair(k0[w], 3),
+                                  code_pair(k1[w], 3)};
+          const float f0 = scale_of(s0, w), f1 = scale_of(s1, w);
+#pragma unroll
+          for (int nt = 0; nt < NQT; ++nt) {
+            float d[4];
+            const float c0 = q136[w][nt][0], c1 = q136[w][nt][1];
+            mma_from(d, a0, qb[2 * w][nt][0], qb[2 * w][nt][1], c0, c1, c0, c1);
+            mma_bf16_16816(d, a1, qb[2 * w + 1][nt][0], qb[2 * w + 1][nt][1]);
+            if (w == 0) {
+              sc[j][nt][0] = f0 * d[0];
+              sc[j][nt][1] = f0 * d[1];
+              sc[j][nt][2] = f1 * d[2];
+              sc[j][nt][3] = f1 * d[3];
+            } else {
+              sc[j][nt][0] = fmaf(f0, d[0], sc[j][nt][0]);
+              sc[j][nt][1] = fmaf(f0, d[1], sc[j][nt][1]);
+              sc[j][nt][2] = fmaf(f1, d[2], sc[j][nt][2]);
+              sc[j][nt][3] = fmaf(f1, d[3], sc[j][nt][3]);
+            }
+          }
+        }
+      }
+      // tokens past the end: their codes and scales may be anything
+      const bool in0 = kBS * j + row0 < n_tok, in1 = kBS * j + row0 + 8 < n_tok;
+#pragma unroll
+      for (int nt = 0; nt < NQT; ++nt) {
+        if (!in0) sc[j][nt][0] = sc[j][nt][1] = -INFINITY;
+        if (!in1) sc[j][nt][2] = sc[j][nt][3] = -INFINITY;
+      }
+    }
+
+    // ---- softmax update (one per step) ----
+    float al[NQT][2];
+#pragma unroll
+    for (int nt = 0; nt < NQT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float bm = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]);
+#pragma unroll
+        for (int j = 1; j < kStepBlocks; ++j) bm = fmax3(bm, sc[j][nt][e], sc[j][nt][2 + e]);
+        // lanes with the same t4 hold the step's other tokens
+        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
+        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
+        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
+        const float mn = fmaxf(m_q[nt][e], bm);  // finite: every step has a valid token
+        const float ms = mn * sl2;
+        al[nt][e] = ex2(m_q[nt][e] * sl2 - ms);
+        m_q[nt][e] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < kStepBlocks; ++j) {
+#pragma unroll
+          for (int x = e; x < 4; x += 2) {
+            sc[j][nt][x] = ex2(fmaf(sc[j][nt][x], sl2, -ms));
+            sum += sc[j][nt][x];
+          }
+        }
+        l_q[nt][e] = l_q[nt][e] * al[nt][e] + sum;
+      }
+    }
+
+    // ---- O^T = al O^T + V^T (P t)^T, two groups (one word of V codes) at a time ----
+#pragma unroll
+    for (int u = 0; u < G / 2; ++u) {
+      uint32_t pb[kStepBlocks][2][NQT][2];  // (p t)^T fragments of groups 2 u, 2 u + 1
+#pragma unroll
+      for (int j = 0; j < kStepBlocks; ++j) {
+        if (j < st.n) {
+          const uint8_t* sv = stage + j * F::kChunk + F::kOffVScales + 4 * u;
+          uint32_t t0 = *reinterpret_cast<const uint32_t*>(sv + row0 * F::kScaleRow);
+          uint32_t t1 = *reinterpret_cast<const uint32_t*>(sv + (row0 + 8) * F::kScaleRow);
+          if (kBS * j + row0 >= n_tok) t0 = 0;  // p is 0 there, but 0 * NaN is not
+          if (kBS * j + row0 + 8 >= n_tok) t1 = 0;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float f0 = x ? bf16_hi(t0) : bf16_lo(t0), f1 = x ? bf16_hi(t1) : bf16_lo(t1);
+#pragma unroll
+            for (int nt = 0; nt < NQT; ++nt) {
+              pb[j][x][nt][0] =
+                  transpose8x8(pack_bf16x2(sc[j][nt][0] * f0, sc[j][nt][1] * f0));
+              pb[j][x][nt][1] =
+                  transpose8x8(pack_bf16x2(sc[j][nt][2] * f1, sc[j][nt][3] * f1));
+            }
+          }
+        }
+      }
+      // the offset of the codes leaves before the step's products come in
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int nt = 0; nt < NQT; ++nt) {
+          float off[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < kStepBlocks; ++j)
+            if (j < st.n) mma_bf16_16816(off, minus136, pb[j][x][nt][0], pb[j][x][nt][1]);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float(&o)[4] = acc[4 * u + 2 * x + y][nt];
+            o[0] = fmaf(o[0], al[nt][0], off[0]);
+            o[1] = fmaf(o[1], al[nt][1], off[1]);
+            o[2] = fmaf(o[2], al[nt][0], off[0]);
+            o[3] = fmaf(o[3], al[nt][1], off[1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kStepBlocks; ++j) {
+        if (j < st.n) {
+          // V^T fragments: channels 4 g .. of each group, score rows 2 t4, 2 t4 + 1 (+ 8)
+          const uint8_t* v = stage + j * F::kChunk + F::kOffVCodes + g * (2 * G) + 4 * u;
+          const int ta = token_of_row(2 * t4), tb = token_of_row(2 * t4 + 1);
+          const uint32_t va = *reinterpret_cast<const uint32_t*>(v + ta * F::kCodeRow);
+          const uint32_t vb = *reinterpret_cast<const uint32_t*>(v + tb * F::kCodeRow);
+          const uint32_t vc = *reinterpret_cast<const uint32_t*>(v + (ta + 8) * F::kCodeRow);
+          const uint32_t vd = *reinterpret_cast<const uint32_t*>(v + (tb + 8) * F::kCodeRow);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t ab = __byte_perm(va, vb, x ? 0x7632 : 0x5410);
+            const uint32_t cd = __byte_perm(vc, vd, x ? 0x7632 : 0x5410);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t a[4] = {code_pair(ab, 2 * y), code_pair(ab, 2 * y + 1),
+                                     code_pair(cd, 2 * y), code_pair(cd, 2 * y + 1)};
+#pragma unroll
+              for (int nt = 0; nt < NQT; ++nt)
+                mma_bf16_16816(acc[4 * u + 2 * x + y][nt], a, pb[j][x][nt][0], pb[j][x][nt][1]);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();  // every lane has read the stage: the next step may be copied over it
+    ++taken;
+    if (p_left > 0) issue();
+
+    c_left -= st.n;
+    c.b += st.n;
+    if (c.b < c.nb && c_left > 0) continue;
+    // ---- the piece ends: write its normalised O and LSE ----
+    {
+      const int j = k_w - range_of(c.first, NB, W);  // piece index within the segment
+      const float nan = __int_as_float(0x7fc00000);
+      const size_t hq0 = static_cast<size_t>(c.r) * p.Hq + c.h * group;
+      if (j >= 0 && j < p.max_pieces) {
+#pragma unroll
+        for (int nt = 0; nt < NQT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float lsum = l_q[nt][e];
+            lsum += __shfl_xor_sync(0xffffffffu, lsum, 4);
+            lsum += __shfl_xor_sync(0xffffffffu, lsum, 8);
+            lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
+            const int q = 8 * nt + 2 * t4 + e;
+            if (q >= group) continue;
+            const float inv = pbad ? nan : 1.f / lsum;
+            const size_t base = (hq0 + q) * p.max_pieces + j;
+            float* dst = p.part_o + base * D + 4 * g;
+#pragma unroll
+            for (int w = 0; w < G; ++w)
+              *reinterpret_cast<float4*>(dst + 32 * w) =
+                  make_float4(acc[2 * w][nt][e] * inv, acc[2 * w][nt][2 + e] * inv,
+                              acc[2 * w + 1][nt][e] * inv, acc[2 * w + 1][nt][2 + e] * inv);
+            if (g == 0) p.part_lse[base] = pbad ? nan : m_q[nt][e] * p.scale + logf(lsum);
+          }
+        }
+        if (piece_b0 == 0 && lane == 0) p.seg_first[static_cast<size_t>(c.r) * p.Hkv + c.h] = c.first;
+      }
+    }
+    if (c_left == 0) break;
+    // the range continues in the next segment
+    advance(c, 0, p);
+    if (c.r >= p.S) break;  // lengths changed under the kernel: nothing valid to read
+    begin_piece();
+  }
+  // Copies still in flight land before the CTA's shared memory goes away.
+  if (!ok || taken < issued)
+    for (int i = taken; i < issued; ++i)
+      if (!(p.withhold_copy && i == 0))
+        mbar_wait_quiet(bars + 8 * (i % C::kStages), (i / C::kStages) & 1, 500000000ull);
+}
+
+template <int D, int NQT>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(kv4_decode_split_kernel<D, NQT>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D, NQT>::kSmem);
+}
+
+template <int D, int NQT>
+cudaError_t launch(const uint8_t* pool, const DecodeParams& p, int num_sms, cudaStream_t stream) {
+  // kCtasPerSm CTAs per SM, fewer when even the shortest ranges would not fill them
+  const long long most_blocks =
+      static_cast<long long>(p.S) * p.Hkv * ((p.max_seq_len + kBS - 1) / kBS);
+  const long long want = (most_blocks / kMinBlocks + kWarps - 1) / kWarps;
+  const long long cap = static_cast<long long>(num_sms) * Shape<D, NQT>::kCtasPerSm;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(want < 1 ? 1 : (want < cap ? want : cap)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<D, NQT>::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_decode_split_kernel<D, NQT>, pool, p);
+}
+
+}  // namespace
+
+cudaError_t prepare_kv4_decode() {
+  cudaError_t e;
+  if ((e = prepare<64, 1>()) != cudaSuccess) return e;
+  if ((e = prepare<64, 2>()) != cudaSuccess) return e;
+  if ((e = prepare<128, 1>()) != cudaSuccess) return e;
+  return prepare<128, 2>();
+}
+
+cudaError_t launch_kv4_decode(const uint8_t* pool, const DecodeParams& p, int num_sms,
+                              cudaStream_t stream) {
+  if (p.S <= 0) return cudaSuccess;
+  cudaError_t e;
+  if (p.D == 64)
+    e = p.group <= 8 ? launch<64, 1>(pool, p, num_sms, stream) : launch<64, 2>(pool, p, num_sms, stream);
+  else
+    e = p.group <= 8 ? launch<128, 1>(pool, p, num_sms, stream)
+                     : launch<128, 2>(pool, p, num_sms, stream);
+  return e != cudaSuccess ? e : launch_decode_merge(p, stream);
+}
+
+}  // namespace gbattn

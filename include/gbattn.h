@@ -377,6 +377,26 @@ int paged_kv4_gather(const void *kv_pool, const int32_t *block_table, const int3
                      int num_pool_blocks, int max_seq_len, void *k_out, void *v_out,
                      void *stream);
 
+/* Bytes of scratch workspace paged_kv4_attn_decode needs for these sizes. */
+size_t paged_kv4_attn_decode_workspace_size(int num_seqs, int Hq, int D, int max_seq_len);
+
+/*
+ * paged_kv4_attn_decode -- paged_attn_decode over the 4-bit cache: the attention of
+ * one query token per request over the values that paged_kv4_gather returns.
+ *
+ *   kv_pool       [num_pool_blocks, Hkv, 18 D] bytes
+ *   workspace     >= paged_kv4_attn_decode_workspace_size(...) bytes, 256-byte aligned
+ *
+ * Everything else, the device-side checks included, as in paged_attn_decode.  A NaN in
+ * a key of the cache makes that request's O and LSE NaN for the heads that read it, a
+ * NaN in a value the 32 channels of O that share its scale.
+ */
+int paged_kv4_attn_decode(const void *q, const void *kv_pool, const int32_t *block_table,
+                          const int32_t *seq_lens, int block_size, int num_seqs, int Hq, int Hkv,
+                          int D, int max_blocks_per_seq, int num_pool_blocks, int max_seq_len,
+                          float scale, void *o, float *lse, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
 /*
  * Test hook for the kernels' failure detection (not for production use).
  * Kernels launched after this call use wait_limit_ns as the limit, in
