@@ -51,6 +51,7 @@ EXPORTS = (
     "paged_kv4_gather",
     "paged_kv4_attn_decode_workspace_size",
     "paged_kv4_attn_decode",
+    "paged_kv4_attn_prefill",
     "attn_test_set_failure",
     "attn_device_status",
     "attn_version",
@@ -121,6 +122,8 @@ def _bind(h):
     h.paged_kv4_attn_decode_workspace_size.restype = Z
     h.paged_kv4_attn_decode.argtypes = [P] * 4 + [I] * 8 + [F, P, P, P, Z, P]
     h.paged_kv4_attn_decode.restype = I
+    h.paged_kv4_attn_prefill.argtypes = [P] * 4 + [I] * 10 + [F, P, P, P]
+    h.paged_kv4_attn_prefill.restype = I
     h.attn_test_set_failure.argtypes = [ctypes.c_ulonglong, I]
     h.attn_test_set_failure.restype = I
     h.attn_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -710,6 +713,49 @@ def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
                                          workspace.numel(), _stream_handle(stream, device))
     if st != ATTN_OK:
         raise GbAttnError("paged_kv4_attn_decode", st)
+    return out, lse
+
+
+def paged_kv4_attn_prefill(q, kv_pool, block_table, kv_lens, max_kv_len: int,
+                           causal: bool = True, scale: float | None = None, out=None, lse=None,
+                           return_lse: bool = True, stream=None):
+    """Chunked prefill against the 4-bit paged cache through the C ABI.
+
+    q [B,Hq,Tq,D] bf16 (the Tq newest tokens of each item), kv_pool [NB,Hkv,18*D]
+    uint8, block_table [B,max_blocks] int32, kv_lens [B] int32 (all CUDA) -> (o
+    [B,Hq,Tq,D] bf16, lse [B,Hq,Tq] fp32).  Query i of item b sits at logical
+    position kv_lens[b] - Tq + i.
+    """
+    import torch
+    device = q.device if isinstance(q, torch.Tensor) else None
+    _check_bf16("q", q, 4, device)
+    B, Hq, Tq, D = q.shape
+    NB = _check_kv4("kv_pool", kv_pool, None, None, device)
+    for name, t in (("block_table", block_table), ("kv_lens", kv_lens)):
+        _check_tensor(name, t, torch.int32, None, device)
+    if kv_pool.shape[2] != 18 * D or block_table.dim() != 2 or block_table.shape[0] != B or \
+            tuple(kv_lens.shape) != (B,):
+        raise ValueError("inconsistent paged-prefill shapes")
+    if out is not None:
+        _check_tensor("out", out, torch.bfloat16, (B, Hq, Tq, D), device)
+    if lse is not None:
+        _check_tensor("lse", lse, torch.float32, (B, Hq, Tq), device)
+    _require_cuda(device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if return_lse and lse is None:
+            lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=device)
+        st = lib().paged_kv4_attn_prefill(q.data_ptr(), kv_pool.data_ptr(),
+                                          block_table.data_ptr(), kv_lens.data_ptr(), 16, B, Hq,
+                                          kv_pool.shape[1], Tq, D, block_table.shape[1], NB,
+                                          int(max_kv_len), int(bool(causal)), float(scale),
+                                          out.data_ptr(), _ptr(lse),
+                                          _stream_handle(stream, device))
+    if st != ATTN_OK:
+        raise GbAttnError("paged_kv4_attn_prefill", st)
     return out, lse
 
 

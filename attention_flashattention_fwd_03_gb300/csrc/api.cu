@@ -125,6 +125,7 @@ FwdParams fwd_params(void* o, float* lse, int B, int Hq, int Hkv, int Tq, int Tk
   p.withhold_copy = g_withhold_copy.load(std::memory_order_relaxed);
   p.block_table = nullptr;
   p.kv_lens = nullptr;
+  p.kv4_pool = nullptr;
   return p;
 }
 

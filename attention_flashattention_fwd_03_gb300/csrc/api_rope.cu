@@ -391,3 +391,49 @@ GBATTN_API int paged_kv4_attn_decode(const void* q, const void* kv_pool,
              ? ATTN_OK
              : ATTN_ERR_CUDA;
 }
+
+GBATTN_API int paged_kv4_attn_prefill(const void* q, const void* kv_pool,
+                                      const int32_t* block_table, const int32_t* kv_lens,
+                                      int block_size, int B, int Hq, int Hkv, int Tq, int D,
+                                      int max_blocks_per_seq, int num_pool_blocks, int max_kv_len,
+                                      int causal, float scale, void* o, float* lse, void* stream) {
+  if (B < 0 || Tq < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_blocks_per_seq <= 0 ||
+      num_pool_blocks <= 0 || max_kv_len < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if (block_size != 16 || (D != 64 && D != 128)) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || Tq == 0) return ATTN_OK;
+  if (!q || !kv_pool || !block_table || !kv_lens || !o) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(o, 16) || !aligned(block_table, 4) ||
+      !aligned(kv_lens, 4) || !aligned(lse, 4))
+    return ATTN_ERR_INVALID_ARG;
+  const uint64_t bhq = static_cast<uint64_t>(B) * Hq;
+  const uint64_t n_qpairs = (static_cast<uint64_t>(Tq) + 255) / 256;
+  if (bhq >= kMaxDim || bhq * n_qpairs >= kMaxDim || bhq * Tq >= (1ull << 40) ||
+      static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim ||
+      static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim)
+    return ATTN_ERR_UNSUPPORTED;
+  DeviceState* ds = nullptr;
+  int st = device_state(&ds);
+  if (st != ATTN_OK) return st;
+  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+  if ((st = encoder(&enc)) != ATTN_OK) return st;
+  CUtensorMap tmQ;
+  const uint64_t row_bytes = static_cast<uint64_t>(D) * 2;
+  const uint64_t strides[2] = {row_bytes, row_bytes * Tq};
+  const uint32_t box[3] = {64, 128, 1};
+  const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(Tq), bhq};
+  if ((st = encode_bf16(enc, &tmQ, q, 3, dims, strides, box)) != ATTN_OK) return st;
+  FwdParams p = fwd_params(o, lse, B, Hq, Hkv, Tq, max_kv_len, D, causal, scale, ds->flags);
+  p.block_table = block_table;
+  p.kv_lens = kv_lens;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_pool_blocks = num_pool_blocks;
+  p.max_kv_len = max_kv_len;
+  p.kv4_pool = static_cast<const uint8_t*>(kv_pool);
+  return launch_attn_fwd(tmQ, tmQ, tmQ, p, ds->num_sms, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}

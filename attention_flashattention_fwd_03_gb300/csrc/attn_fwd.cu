@@ -6,9 +6,10 @@
 // is computed, the softmax statistics are updated, and the matching output is
 // accumulated in on-chip memory, so the Tq x Tk score matrix never reaches HBM.
 // The same section describes the paged KV cache (fixed 16-token blocks, every
-// logical position translated through a block table); with PAGED the key/value
-// tiles are gathered block by block through that table, which is what chunked
-// prefill against a paged cache needs.
+// logical position translated through a block table); from a paged source the
+// key/value tiles are gathered block by block through that table, which is what
+// chunked prefill against a paged cache needs.  The paged cache may be held in 4
+// bits (kv4.cuh).
 //
 // GB300 realisation.  One CTA per SM, persistent over work units; a unit is two
 // 128-row query tiles of one (batch, head) that share every K/V tile:
@@ -16,7 +17,11 @@
 //                 into one ring of 128-key slots (128-byte swizzle); in paged
 //                 mode lanes 0-7 read the tile's block-table entries (the next
 //                 tile's while this one is copied) and each copies its block's
-//                 16 rows
+//                 16 rows (of the 4-bit cache: its block's codes and scales, into
+//                 a ring of raw half chunks)
+//   warps 2, 3    4-bit cache: turn a raw K or V tile into the bf16 slot the MMA
+//                 warp reads.  Every value n s is a bf16 exactly, so these are the
+//                 operands themselves, not an approximation of them
 //   warp 1        MMA warp (the converged warp runs the issue code; elect.sync
 //                 picks the lane that issues): S_i = Q_i K_j^T into TMEM (fp32),
 //                 then O_i += P_i V_j with P_i read from TMEM (tcgen05 A operand
@@ -38,7 +43,10 @@
 // the rescale of O_i never waits for the tensor core.
 #include <cuda_runtime.h>
 
+#include <cuda_bf16.h>
+
 #include "internal.h"
+#include "kv4.cuh"
 #include "ptx.cuh"
 
 // With GBATTN_EXP2_POLY_PAIRS = n > 0, one key pair in every n of an unmasked
@@ -65,16 +73,24 @@ constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by
 constexpr int kRegsLaunch = 168, kRegsWg0 = 104, kRegsSoftmax = 200;
 static_assert(kRegsWg0 + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split exceeds the launch");
 
-template <int D>
+// Where keys and values come from: contiguous tensors, the bf16 pools or the 4-bit pool.
+enum class Src { kContiguous, kPaged, kPaged4 };
+
+template <int D, Src SRC>
 struct Cfg {
   static constexpr int KB = D / 64;                   // 64-column (128-byte) boxes per row
   static constexpr int BOX_BYTES = 128 * 128;         // 128 rows x 128 bytes
   static constexpr int TILE_BYTES = BM * D * 2;       // one Q, K or V tile
-  static constexpr int NSLOT = (D == 64) ? 8 : 5;     // K/V ring slots
+  // K/V ring slots; the raw tiles of the 4-bit cache take the place of one
+  static constexpr int NSLOT = (D == 64) ? 8 : (SRC == Src::kPaged4 ? 4 : 5);
+  static constexpr int NRAW = SRC == Src::kPaged4 ? 3 : 0;  // raw K or V tiles in flight
+  static constexpr int RAW_BLOCK = 9 * D;             // codes and scales of K or V of a block
+  static constexpr int RAW_BYTES = (BN / kBS) * RAW_BLOCK;
   static constexpr int OFF_Q = 0;                     // the unit's two Q tiles
   static constexpr int OFF_RING = 2 * TILE_BYTES;
-  static constexpr int OFF_BAR = OFF_RING + NSLOT * TILE_BYTES;
-  static constexpr int NBAR = 2 + 2 * NSLOT + 6 + 1;
+  static constexpr int OFF_RAW = OFF_RING + NSLOT * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_RAW + NRAW * RAW_BYTES;
+  static constexpr int NBAR = 2 + 2 * NSLOT + 6 + 1 + 2 * NRAW;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // + slack for 1024-byte alignment
   static constexpr uint32_t TMEM_COLS = 512;
@@ -84,20 +100,24 @@ struct Cfg {
   __device__ static constexpr uint32_t p_col(int i) { return 128u * i + 64u; }
   __device__ static constexpr uint32_t o_col(int i) { return 256u + static_cast<uint32_t>(D) * i; }
 };
-static_assert(Cfg<128>::SMEM_BYTES <= 232448, "shared memory budget");
-static_assert(Cfg<64>::SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(Cfg<128, Src::kPaged>::SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(Cfg<128, Src::kPaged4>::SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(Cfg<64, Src::kPaged4>::SMEM_BYTES <= 232448, "shared memory budget");
 
-template <int D>
+template <int D, Src SRC>
 struct Bars {
+  using C = Cfg<D, SRC>;
   uint32_t base;
   __device__ uint32_t q_full() const { return base; }
   __device__ uint32_t q_empty() const { return base + 8; }
   __device__ uint32_t slot_full(int s) const { return base + 8 * (2 + s); }
-  __device__ uint32_t slot_empty(int s) const { return base + 8 * (2 + Cfg<D>::NSLOT + s); }
-  __device__ uint32_t s_full(int i) const { return base + 8 * (2 + 2 * Cfg<D>::NSLOT + i); }
-  __device__ uint32_t s_free(int i) const { return base + 8 * (4 + 2 * Cfg<D>::NSLOT + i); }
-  __device__ uint32_t p_full(int i) const { return base + 8 * (6 + 2 * Cfg<D>::NSLOT + i); }
-  __device__ uint32_t teardown() const { return base + 8 * (8 + 2 * Cfg<D>::NSLOT); }
+  __device__ uint32_t slot_empty(int s) const { return base + 8 * (2 + C::NSLOT + s); }
+  __device__ uint32_t s_full(int i) const { return base + 8 * (2 + 2 * C::NSLOT + i); }
+  __device__ uint32_t s_free(int i) const { return base + 8 * (4 + 2 * C::NSLOT + i); }
+  __device__ uint32_t p_full(int i) const { return base + 8 * (6 + 2 * C::NSLOT + i); }
+  __device__ uint32_t teardown() const { return base + 8 * (8 + 2 * C::NSLOT); }
+  __device__ uint32_t raw_full(int s) const { return base + 8 * (9 + 2 * C::NSLOT + s); }
+  __device__ uint32_t raw_empty(int s) const { return base + 8 * (9 + 2 * C::NSLOT + C::NRAW + s); }
 };
 
 // One work unit: query rows [256 qp, 256 qp + 256) of one (batch, head).
@@ -181,13 +201,18 @@ __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
 // ---------------------------------------------------------------------------
 // producer warp: TMA loads
 // ---------------------------------------------------------------------------
-template <int D, bool PAGED>
+template <int D, Src SRC>
 __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
                               const CUtensorMap* tmV, const FwdParams& p, uint32_t sbase,
-                              const Bars<D>& bar, volatile int* abort) {
-  using C = Cfg<D>;
+                              const Bars<D, SRC>& bar, volatile int* abort) {
+  using C = Cfg<D, SRC>;
+  constexpr bool PAGED = SRC != Src::kContiguous;
+  constexpr bool RAW = SRC == Src::kPaged4;
+  constexpr int NRING = RAW ? C::NRAW : C::NSLOT;  // the ring this warp fills
   const int lane = threadIdx.x & 31;
-  const uint32_t sQ = sbase + C::OFF_Q, sR = sbase + C::OFF_RING;
+  const uint32_t sQ = sbase + C::OFF_Q, sR = sbase + (RAW ? C::OFF_RAW : C::OFF_RING);
+  auto full = [&](int s) { return RAW ? bar.raw_full(s) : bar.slot_full(s); };
+  auto empty = [&](int s) { return RAW ? bar.raw_empty(s) : bar.slot_empty(s); };
   const unsigned long long lim = p.wait_limit_ns;
   int rc = 0, uc = 0;
   bool ok = true, last_q_issued = false;
@@ -235,29 +260,35 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const CUtensorMap* map = kv == 0 ? tmK : tmV;
-        const int s = rc % C::NSLOT;
-        if (!mbar_wait_warp(bar.slot_empty(s), ((rc / C::NSLOT) & 1) ^ 1, abort, p.flags, lim)) {
+        const int s = rc % NRING;
+        if (!mbar_wait_warp(empty(s), ((rc / NRING) & 1) ^ 1, abort, p.flags, lim)) {
           ok = false;
           break;
         }
-        const uint32_t dst = sR + s * C::TILE_BYTES;
+        const uint32_t dst = sR + s * (RAW ? C::RAW_BYTES : C::TILE_BYTES);
         if (!PAGED) {
           if (lane == 0) {
-            mbar_arrive_expect_tx(bar.slot_full(s), C::TILE_BYTES);
+            mbar_arrive_expect_tx(full(s), C::TILE_BYTES);
 #pragma unroll
             for (int kb = 0; kb < C::KB; ++kb)
-              tma_load_3d(dst + kb * C::BOX_BYTES, map, bar.slot_full(s), kb * 64, j * BN, U.bkv);
+              tma_load_3d(dst + kb * C::BOX_BYTES, map, full(s), kb * 64, j * BN, U.bkv);
           }
         } else {
           // lane 0 posts the byte count first; then lanes 0..nblk-1 copy their
-          // block's 16 rows, one box per 64-column half
-          if (lane == 0) mbar_arrive_expect_tx(bar.slot_full(s), nblk * kBS * D * 2);
+          // block: 16 rows, one box per 64-column half, or its raw half chunk
+          if (lane == 0) mbar_arrive_expect_tx(full(s), nblk * (RAW ? C::RAW_BLOCK : kBS * D * 2));
           __syncwarp();
           if (lane < nblk) {
+            if constexpr (RAW) {
+              const uint8_t* src =
+                  p.kv4_pool + static_cast<size_t>(row_of_lane / kBS) * Kv4<D>::kChunk;
+              bulk_load(dst + lane * C::RAW_BLOCK, src + kv * C::RAW_BLOCK, C::RAW_BLOCK, full(s));
+            } else {
 #pragma unroll
-            for (int kb = 0; kb < C::KB; ++kb)
-              tma_load_2d(dst + kb * C::BOX_BYTES + lane * kBS * 128, map, bar.slot_full(s),
-                          kb * 64, row_of_lane);
+              for (int kb = 0; kb < C::KB; ++kb)
+                tma_load_2d(dst + kb * C::BOX_BYTES + lane * kBS * 128, map, full(s), kb * 64,
+                            row_of_lane);
+            }
           }
           __syncwarp();
         }
@@ -268,9 +299,108 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
   if (!ok && lane == 0) {
     // Let the copies still in flight land before the CTA's shared memory goes away.
     const unsigned long long quiet = 500000000ull;
-    for (int n = (rc > C::NSLOT ? rc - C::NSLOT : 0); n < rc; ++n)
-      mbar_wait_quiet(bar.slot_full(n % C::NSLOT), (n / C::NSLOT) & 1, quiet);
+    for (int n = (rc > NRING ? rc - NRING : 0); n < rc; ++n)
+      mbar_wait_quiet(full(n % NRING), (n / NRING) & 1, quiet);
     if (uc > 0 && last_q_issued) mbar_wait_quiet(bar.q_full(), (uc - 1) & 1, quiet);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 4-bit cache: warps 2 and 3 turn raw K and V tiles into bf16 slots, 64 keys each
+// ---------------------------------------------------------------------------
+
+// Eight codes of one word (low nibble first) times a scale pair (s, s), as four bf16
+// pairs in channel order.  Nibbles i and i + 4 become the pair 128 + u after one shift
+// and one logic operation; taking off 136 and the product with s are both exact.
+__device__ __forceinline__ uint4 dequantise_word(uint32_t w, __nv_bfloat162 s) {
+  const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    __nv_bfloat162 x;
+    memcpy(&x, &u, 4);
+    x = __hmul2(__hsub2(x, off), s);
+    memcpy(&v[i], &x, 4);
+  }
+  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                    __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+}
+
+template <int D, Src SRC>
+__device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SRC>& bar,
+                             volatile int* abort) {
+  using C = Cfg<D, SRC>;
+  using F = Kv4<D>;
+  constexpr int G = F::kGroups;
+  const int lane = threadIdx.x & 31;
+  const int half = (threadIdx.x >> 5) & 1;  // warp 2: keys 0..63 of a tile, warp 3: 64..127
+  const unsigned long long lim = p.wait_limit_ns;
+  int rc = 0;
+  for (int r = 0; r * static_cast<int>(gridDim.x) < p.num_units; ++r) {
+    const int u = unit_of_round(r);
+    if (u >= p.num_units) continue;
+    const Unit U = unit_at(u, p, true);
+    for (int j = 0; j < U.nkv; ++j) {
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv, ++rc) {
+        const int rs = rc % C::NRAW, s = rc % C::NSLOT;
+        if (!mbar_wait_warp(bar.raw_full(rs), (rc / C::NRAW) & 1, abort, p.flags, lim)) return;
+        if (!mbar_wait_warp(bar.slot_empty(s), ((rc / C::NSLOT) & 1) ^ 1, abort, p.flags, lim))
+          return;
+        const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW_BYTES;
+        uint8_t* tile = smem + C::OFF_RING + s * C::TILE_BYTES;
+        const int valid = U.L - j * BN;  // keys past the cache's end become zeros
+        // a lane takes a quarter of a key's codes: 8 channels of every group
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+          const int key = half * 64 + i * 8 + (lane >> 2), t = lane & 3;
+          const uint8_t* blk = raw + (key / kBS) * C::RAW_BLOCK;
+          const uint8_t* cp = blk + (key % kBS) * F::kCodeRow + t * (4 * G);
+          const uint8_t* sp = blk + kBS * F::kCodeRow + (key % kBS) * F::kScaleRow;
+          uint32_t w[G], sc[G / 2];
+          if constexpr (G == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(cp);
+            const uint2 y = *reinterpret_cast<const uint2*>(sp);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+            sc[0] = y.x, sc[1] = y.y;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(cp);
+            w[0] = x.x, w[1] = x.y;
+            sc[0] = *reinterpret_cast<const uint32_t*>(sp);
+          }
+          if (kv == 1) {
+            // a V row holds 4 channels of every group in turn: bring the two runs of 4
+            // of a group together
+            uint32_t y[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+              y[g] = __byte_perm(w[g / 2], w[G / 2 + g / 2], (g & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+            for (int g = 0; g < G; ++g) w[g] = y[g];
+          }
+          if (key >= valid) {
+#pragma unroll
+            for (int g = 0; g < G / 2; ++g) sc[g] = 0;
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const uint32_t ss = __byte_perm(sc[g / 2], 0, (g & 1) ? 0x3232 : 0x1010);
+            __nv_bfloat162 s2;
+            memcpy(&s2, &ss, 4);
+            const int chunk = 4 * (g & 1) + t;  // 16-byte chunk of the 64-channel box g / 2
+            *reinterpret_cast<uint4*>(tile + (g / 2) * C::BOX_BYTES + key * 128 +
+                                      ((chunk ^ (key & 7)) << 4)) = dequantise_word(w[g], s2);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar.slot_full(s));
+          mbar_arrive(bar.raw_empty(rs));
+        }
+      }
+    }
   }
 }
 
@@ -280,15 +410,16 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
 // also clears key rows past the sequence end in the last V tile).  Shared-memory
 // descriptors are built once; an MMA only adds constant offsets to them.
 // ---------------------------------------------------------------------------
-template <int D, bool PAGED>
+template <int D, Src SRC>
 struct MmaWarp {
-  using C = Cfg<D>;
+  using C = Cfg<D, SRC>;
+  static constexpr bool PAGED = SRC != Src::kContiguous;
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(BM, BN, 0, 0);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(BM, D, 0, 1);  // A (P) in TMEM, V MN-major
   static constexpr uint64_t kTileStep = C::TILE_BYTES >> 4;  // descriptor address units
 
   const FwdParams& p;
-  const Bars<D>& bar;
+  const Bars<D, SRC>& bar;
   volatile int* abort;
   uint32_t sR, tmem;
   uint64_t dq, dk, dv;   // descriptors of Q tile 0 and of ring slot 0 read as K and as V
@@ -298,7 +429,7 @@ struct MmaWarp {
   int s_left = 0;        // S products of the unit not yet issued
   int zeroed_j = -1;     // paged: the unit's last V tile has had its dead rows cleared
 
-  __device__ MmaWarp(const FwdParams& p_, const Bars<D>& b_, volatile int* a_, uint32_t sbase,
+  __device__ MmaWarp(const FwdParams& p_, const Bars<D, SRC>& b_, volatile int* a_, uint32_t sbase,
                      uint32_t tmem_)
       : p(p_), bar(b_), abort(a_), sR(sbase + C::OFF_RING), tmem(tmem_),
         dq(smem_desc_sw128(sbase + C::OFF_Q, 16, 1024)),
@@ -340,7 +471,7 @@ struct MmaWarp {
   __device__ bool issue_pv(int j, int nkv, int L, bool ring_seen) {
     const int vs = slot(2 * j + 1);
     if (!ring_seen && !wait(bar.slot_full(vs), par(2 * j + 1))) return false;
-    if (PAGED && j == nkv - 1 && zeroed_j != j) {
+    if (SRC == Src::kPaged && j == nkv - 1 && zeroed_j != j) {
       zeroed_j = j;
       // Key rows past the sequence end hold stale or arbitrary data (even NaN);
       // their probabilities are 0, but 0 * NaN would reach O.  Clear those rows.
@@ -429,10 +560,11 @@ __device__ __forceinline__ void write_p(const float (&s)[128], float sl2, float 
 // warpgroups run this one copy of the code, which keeps the instruction cache
 // footprint of the two warpgroups shared
 // ---------------------------------------------------------------------------
-template <int D, bool PAGED>
-__device__ void softmax_wg(const FwdParams& p, uint32_t tmem, const Bars<D>& bar,
+template <int D, Src SRC>
+__device__ void softmax_wg(const FwdParams& p, uint32_t tmem, const Bars<D, SRC>& bar,
                            volatile int* abort, const int I) {
-  using C = Cfg<D>;
+  using C = Cfg<D, SRC>;
+  constexpr bool PAGED = SRC != Src::kContiguous;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sp = warp & 3;  // TMEM sub-partition this warp may access
   const int r = sp * 32 + lane;
@@ -526,7 +658,8 @@ __device__ void softmax_wg(const FwdParams& p, uint32_t tmem, const Bars<D>& bar
     // epilogue: wait for the last P V, then O / l -> bf16 and LSE
     uint16_t* orow = static_cast<uint16_t*>(p.o) + (static_cast<size_t>(U.bh) * p.Tq + qpos) * D;
     const float nan = __int_as_float(0x7fc00000);
-    const bool empty = !(l > 0.f);  // no visible key (or none processed)
+    // no visible key (or none processed); a NaN from the 4-bit cache is a result
+    const bool empty = SRC == Src::kPaged4 ? l == 0.f : !(l > 0.f);
     const float inv_l = empty ? 0.f : 1.f / l;
     if (n > 0) {
       if (!mbar_wait_warp(bar.s_free(I), (sc - 1) & 1, abort, p.flags, lim)) return;
@@ -565,16 +698,16 @@ __device__ void softmax_wg(const FwdParams& p, uint32_t tmem, const Bars<D>& bar
   }
 }
 
-template <int D, bool PAGED>
+template <int D, Src SRC>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, SRC>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
-  const Bars<D> bar{sbase + C::OFF_BAR};
+  const Bars<D, SRC> bar{sbase + C::OFF_BAR};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -583,8 +716,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar.q_full(), 1);
     mbar_init(bar.q_empty(), 1);
     for (int s = 0; s < C::NSLOT; ++s) {
-      mbar_init(bar.slot_full(s), 1);
+      mbar_init(bar.slot_full(s), SRC == Src::kPaged4 ? 2 : 1);
       mbar_init(bar.slot_empty(s), 1);
+    }
+    for (int s = 0; s < C::NRAW; ++s) {
+      mbar_init(bar.raw_full(s), 1);
+      mbar_init(bar.raw_empty(s), 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar.s_full(i), 1);
@@ -613,18 +750,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     regs_decrease<kRegsWg0>();
     if (warp == 0) {
-      producer_warp<D, PAGED>(&tmQ, &tmK, &tmV, p, sbase, bar, abort);
+      producer_warp<D, SRC>(&tmQ, &tmK, &tmV, p, sbase, bar, abort);
     } else if (warp == 1) {
-      MmaWarp<D, PAGED> mma(p, bar, abort, sbase, tmem);
+      MmaWarp<D, SRC> mma(p, bar, abort, sbase, tmem);
       mma.run();
       // Every MMA this warp issued has finished once the teardown barrier flips.
       mma_commit_warp(bar.teardown());
       if (lane == 0) mbar_wait_quiet(bar.teardown(), 0, 1000000000ull);
       __syncwarp();
+    } else if constexpr (SRC == Src::kPaged4) {
+      dequant_warp<D, SRC>(p, smem, bar, abort);
     }
   } else {
     regs_increase<kRegsSoftmax>();
-    softmax_wg<D, PAGED>(p, tmem, bar, abort, warp < 8 ? 0 : 1);
+    softmax_wg<D, SRC>(p, tmem, bar, abort, warp < 8 ? 0 : 1);
   }
 
   tc_fence_before();
@@ -635,40 +774,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool PAGED>
+template <int D, Src SRC>
 cudaError_t set_smem() {
-  return cudaFuncSetAttribute(attn_fwd_kernel<D, PAGED>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM_BYTES);
+  return cudaFuncSetAttribute(attn_fwd_kernel<D, SRC>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, (Cfg<D, SRC>::SMEM_BYTES));
 }
 
-template <int D, bool PAGED>
+template <int D, Src SRC>
 void launch(int grid, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
             const FwdParams& p, cudaStream_t stream) {
-  attn_fwd_kernel<D, PAGED><<<grid, kThreads, Cfg<D>::SMEM_BYTES, stream>>>(tmQ, tmK, tmV, p);
+  attn_fwd_kernel<D, SRC><<<grid, kThreads, (Cfg<D, SRC>::SMEM_BYTES), stream>>>(tmQ, tmK, tmV, p);
 }
 
 }  // namespace
 
 cudaError_t prepare_attn_fwd() {
   cudaError_t e;
-  if ((e = set_smem<64, false>()) != cudaSuccess) return e;
-  if ((e = set_smem<128, false>()) != cudaSuccess) return e;
-  if ((e = set_smem<64, true>()) != cudaSuccess) return e;
-  return set_smem<128, true>();
+  if ((e = set_smem<64, Src::kContiguous>()) != cudaSuccess) return e;
+  if ((e = set_smem<128, Src::kContiguous>()) != cudaSuccess) return e;
+  if ((e = set_smem<64, Src::kPaged>()) != cudaSuccess) return e;
+  if ((e = set_smem<128, Src::kPaged>()) != cudaSuccess) return e;
+  if ((e = set_smem<64, Src::kPaged4>()) != cudaSuccess) return e;
+  return set_smem<128, Src::kPaged4>();
 }
 
 cudaError_t launch_attn_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                             const FwdParams& p, int num_sms, cudaStream_t stream) {
   const int grid = p.num_units < num_sms ? p.num_units : num_sms;
   if (grid <= 0) return cudaSuccess;
-  const bool paged = p.block_table != nullptr;
-  if (p.D == 64) {
-    if (paged) launch<64, true>(grid, tmQ, tmK, tmV, p, stream);
-    else launch<64, false>(grid, tmQ, tmK, tmV, p, stream);
-  } else {
-    if (paged) launch<128, true>(grid, tmQ, tmK, tmV, p, stream);
-    else launch<128, false>(grid, tmQ, tmK, tmV, p, stream);
-  }
+  auto run = [&](auto d) {
+    constexpr int DD = decltype(d)::value;
+    if (p.kv4_pool != nullptr)
+      launch<DD, Src::kPaged4>(grid, tmQ, tmK, tmV, p, stream);
+    else if (p.block_table != nullptr)
+      launch<DD, Src::kPaged>(grid, tmQ, tmK, tmV, p, stream);
+    else
+      launch<DD, Src::kContiguous>(grid, tmQ, tmK, tmV, p, stream);
+  };
+  if (p.D == 64)
+    run(std::integral_constant<int, 64>{});
+  else
+    run(std::integral_constant<int, 128>{});
   return cudaGetLastError();
 }
 

@@ -29,6 +29,7 @@ struct FwdParams {
   int max_blocks;
   int num_pool_blocks;
   int max_kv_len;
+  const uint8_t* kv4_pool;     // 4-bit pool (K and V; tmK and tmV unused), or nullptr
 };
 
 // Prefill / full attention.  Contiguous: tmK/tmV are 3-D tiled maps over

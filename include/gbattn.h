@@ -398,6 +398,23 @@ int paged_kv4_attn_decode(const void *q, const void *kv_pool, const int32_t *blo
                           size_t workspace_bytes, void *stream);
 
 /*
+ * paged_kv4_attn_prefill -- paged_attn_prefill over the 4-bit cache: the attention of
+ * the Tq newest tokens of each item over the values that paged_kv4_gather returns.
+ * The values are bf16 exactly, so the kernel computes with them as they are.
+ *
+ *   kv_pool       [num_pool_blocks, Hkv, 18 D] bytes
+ *
+ * Everything else, the device-side checks included, as in paged_attn_prefill.  Slots
+ * past kv_lens[b] may hold any bits.  A NaN in a key of the cache makes O and LSE NaN
+ * for the queries that see it; a NaN in a value may reach O of every query of its item
+ * and KV head, of those too that causal hides it from.
+ */
+int paged_kv4_attn_prefill(const void *q, const void *kv_pool, const int32_t *block_table,
+                           const int32_t *kv_lens, int block_size, int B, int Hq, int Hkv, int Tq,
+                           int D, int max_blocks_per_seq, int num_pool_blocks, int max_kv_len,
+                           int causal, float scale, void *o, float *lse, void *stream);
+
+/*
  * Test hook for the kernels' failure detection (not for production use).
  * Kernels launched after this call use wait_limit_ns as the limit, in
  * nanoseconds, of every pipeline wait (0 restores the default of 2 s).  With

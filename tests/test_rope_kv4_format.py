@@ -185,6 +185,41 @@ def test_kv4_gather_refusals(kw, code):
                                      None) == code
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(bs=8), UNS), (dict(D=96), UNS), (dict(Hq=34), UNS), (dict(Hq=5), INV), (dict(Hkv=0), INV),
+    (dict(q=None), INV), (dict(pool=None), INV), (dict(pool=A16 + 8), INV), (dict(o=None), INV),
+    (dict(bt=None), INV), (dict(sl=A16 + 2), INV), (dict(lse=A16 + 1), INV), (dict(ws=None), INV),
+    (dict(ws=A16 + 16), INV), (dict(wsb=-1), INV), (dict(scale=0.0), INV),
+    (dict(scale=float("nan")), INV), (dict(msl=-1), INV), (dict(mb=0), INV), (dict(nb=0), INV),
+    (dict(nb=1 << 27), UNS), (dict(mb=1 << 28), UNS), (dict(S=-1), INV), (dict(S=0), OK),
+])
+def test_kv4_decode_refusals(kw, code):
+    a = dict(q=A16, pool=A16, bt=A16, sl=A16, bs=16, S=4, Hq=12, Hkv=2, D=128, mb=512, nb=1000,
+             msl=8192, scale=0.088, o=A16, lse=None, ws=A16, wsb=0) | kw
+    need = gb.paged_kv4_attn_decode_workspace_size(a["S"], a["Hq"], a["D"], a["msl"])
+    assert gb.lib().paged_kv4_attn_decode(a["q"], a["pool"], a["bt"], a["sl"], a["bs"], a["S"],
+                                          a["Hq"], a["Hkv"], a["D"], a["mb"], a["nb"], a["msl"],
+                                          a["scale"], a["o"], a["lse"], a["ws"],
+                                          max(0, need + a["wsb"]), None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(bs=8), UNS), (dict(D=96), UNS), (dict(Hq=5), INV), (dict(Hkv=0), INV), (dict(Tq=-1), INV),
+    (dict(q=None), INV), (dict(q=A16 + 8), INV), (dict(pool=None), INV), (dict(pool=A16 + 8), INV),
+    (dict(o=None), INV), (dict(bt=None), INV), (dict(sl=A16 + 2), INV), (dict(lse=A16 + 1), INV),
+    (dict(causal=2), INV), (dict(scale=-1.0), INV), (dict(scale=float("inf")), INV),
+    (dict(ml=-1), INV), (dict(mb=0), INV), (dict(nb=0), INV), (dict(nb=1 << 27), UNS),
+    (dict(mb=1 << 28), UNS), (dict(B=0), OK), (dict(Tq=0), OK),
+])
+def test_kv4_prefill_refusals(kw, code):
+    a = dict(q=A16, pool=A16, bt=A16, sl=A16, bs=16, B=4, Hq=12, Hkv=2, Tq=9, D=128, mb=512,
+             nb=1000, ml=8192, causal=1, scale=0.088, o=A16, lse=None) | kw
+    assert gb.lib().paged_kv4_attn_prefill(a["q"], a["pool"], a["bt"], a["sl"], a["bs"], a["B"],
+                                           a["Hq"], a["Hkv"], a["Tq"], a["D"], a["mb"], a["nb"],
+                                           a["ml"], a["causal"], a["scale"], a["o"], a["lse"],
+                                           None) == code
+
+
 # --------------------------------------------------------------------------- #
 # argument checks of the binding
 # --------------------------------------------------------------------------- #
@@ -236,3 +271,22 @@ def test_binding_refuses_bad_appends(bad):
              seq_lens=torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError):
         gb.paged_kv4_append(**(a | bad))
+
+
+@pytest.mark.parametrize("bad", [
+    dict(kv_pool=torch.zeros(9, 2, 18 * 32, dtype=torch.uint8)), dict(kv_pool=bf(9, 2, 16, 64)),
+    dict(kv_pool=torch.zeros(9, 2, 100, dtype=torch.uint8)), dict(q=torch.zeros(2, 4, 64)),
+    dict(out=bf(2, 5, 64)), dict(lse=bf(2, 4)), dict(block_table=torch.zeros(2, 4)),
+    dict(seq_lens=torch.zeros(3, dtype=torch.int32)), {},
+])
+def test_binding_refuses_bad_kv4_attention(bad):
+    a = dict(q=bf(2, 4, 64), kv_pool=torch.zeros(9, 2, 18 * 64, dtype=torch.uint8),
+             block_table=torch.zeros(2, 4, dtype=torch.int32),
+             seq_lens=torch.zeros(2, dtype=torch.int32), max_seq_len=64)
+    with pytest.raises(ValueError):
+        gb.paged_kv4_attn_decode(**(a | bad))
+    a |= bad
+    a["kv_lens"], a["max_kv_len"] = a.pop("seq_lens"), a.pop("max_seq_len")
+    a = {n: t.unsqueeze(2) if n in ("q", "out", "lse") else t for n, t in a.items()}
+    with pytest.raises(ValueError):
+        gb.paged_kv4_attn_prefill(**a)
