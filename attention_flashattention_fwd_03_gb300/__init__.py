@@ -21,6 +21,7 @@ From a projection's rows to those calls, norm and rotation included, and the cac
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -59,6 +60,7 @@ EXPORTS = (
 
 _lock = threading.Lock()
 _lib = None
+_Tensor = None  # torch.Tensor, once an operator below has been called
 
 
 class GbAttnError(RuntimeError):
@@ -368,9 +370,54 @@ def paged_kv_gather(pool, block_table, seq_lens, max_seq_len: int, out=None, str
     return out
 
 
+# The operators below are called between kernels of a few microseconds, so their
+# argument checks first test everything at once and go into detail only to name what is
+# wrong (measured on the GPU's host, a call of paged_qkv_append took 43 us before and
+# takes @APP@ us now; its kernel runs for 5).
+
+class _On:
+    """The device, and the stream if one is given, current for allocations and launches
+    (outputs and workspaces then belong to that stream's memory pool)."""
+
+    __slots__ = ("device", "stream", "inner")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.inner = device, stream, None
+
+    def __enter__(self):
+        import torch
+        if self.stream is not None or torch.cuda.current_device() != self.device.index:
+            self.inner = (torch.cuda.device(self.device), torch.cuda.stream(self.stream))
+            for c in self.inner:
+                c.__enter__()
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            for c in reversed(self.inner):
+                c.__exit__(*exc)
+        return False
+
+
+def _check(name, t, dtype, shape, device):
+    """_check_tensor, quick where all is well."""
+    if t.__class__ is _Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous() and \
+            t.device == device:
+        return
+    _check_tensor(name, t, dtype, shape, device)
+
+
+def _is_rows(t, bf16, device):
+    """Whether t is a [B, T, H, D] bf16 operand: any strides but contiguous channels."""
+    return (t.__class__ is _Tensor and t.dtype is bf16 and t.dim() == 4 and
+            (t.stride(3) == 1 or t.shape[3] == 1) and t.device == device)
+
+
 def _check_rows(name, t, shape, device):
-    """A [B, T, H, D] bf16 operand with any strides but contiguous channels; `shape` may
-    hold None for a free dimension.  Metadata checks only."""
+    """Raises for what is wrong with a [B, T, H, D] operand; `shape` may hold None for a
+    free dimension.  Metadata checks only."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -384,11 +431,18 @@ def _check_rows(name, t, shape, device):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
+@functools.lru_cache(maxsize=1024)
+def _stride_array(b, t, h):
+    return (ctypes.c_int64 * 3)(b, t, h)
+
+
 def _strides(t):
     """Batch, token and head strides for the C ABI (0 where a dimension has one entry)."""
     if t is None:
         return None
-    return (ctypes.c_int64 * 3)(*(st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride()[:3])))
+    B, T, H, _ = t.shape
+    b, s, h, _ = t.stride()
+    return _stride_array(b if B > 1 else 0, s if T > 1 else 0, h if H > 1 else 0)
 
 
 def _ptr(t):
@@ -398,22 +452,30 @@ def _ptr(t):
 def _check_rope(cos_sin, q_weight, k_weight, positions, B, T, D, device):
     """Checks the norm and rotation operands; returns (rot_dim, max_pos)."""
     import torch
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check_tensor(name, w, torch.bfloat16, (D,), device)
+    if q_weight is not None:
+        _check("q_weight", q_weight, torch.bfloat16, (D,), device)
+    if k_weight is not None:
+        _check("k_weight", k_weight, torch.bfloat16, (D,), device)
     if positions is not None:
-        _check_tensor("positions", positions, torch.int32, (B, T), device)
+        _check("positions", positions, torch.int32, (B, T), device)
     if cos_sin is None:
         return 0, 0
     _check_tensor("cos_sin", cos_sin, torch.float32, None, device)
-    if cos_sin.dim() != 2 or cos_sin.shape[0] == 0 or cos_sin.shape[1] == 0:
+    if cos_sin.dim() != 2 or cos_sin.numel() == 0:
         raise ValueError("cos_sin must be a non-empty [max_pos, rot_dim] table")
-    return cos_sin.shape[1], cos_sin.shape[0]
+    max_pos, rot = cos_sin.shape
+    return rot, max_pos
 
 
 def _first(*tensors):
+    """The first operand given, after making sure that it is a tensor."""
+    import torch
+    global _Tensor
+    _Tensor = torch.Tensor
     for t in tensors:
         if t is not None:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"operands must be torch.Tensor, got {type(t)}")
             return t
     raise ValueError("at least one operand is needed")
 
@@ -431,42 +493,46 @@ def qkv_norm_rope(q, k, v=None, cos_sin=None, q_weight=None, k_weight=None, eps:
     norm); ``positions`` [B,T] int32 (None: 0 .. T-1).
     """
     import torch
+    bf16 = torch.bfloat16
     some = _first(q, k, v)
-    device = some.device if isinstance(some, torch.Tensor) else None
-    kv = k if k is not None else v
+    device = some.device
     for name, t in (("q", q), ("k", k), ("v", v)):
-        if t is not None:
+        if t is not None and not _is_rows(t, bf16, device):
             _check_rows(name, t, (None,) * 4, device)
     B, T, _, D = some.shape
-    for name, t, heads in (("q", q, None), ("k", k, None), ("v", v, None if kv is v else kv.shape[2])):
-        if t is not None:
+    Hq = q.shape[2] if q is not None else 0
+    kv = k if k is not None else v
+    Hkv = kv.shape[2] if kv is not None else 0
+    outs = []
+    for name, t, heads, out in (("q", q, Hq, q_out), ("k", k, Hkv, k_out), ("v", v, Hkv, v_out)):
+        if t is None:
+            if out is not None:
+                raise ValueError(f"{name}_out is given without its input")
+            continue
+        if t.shape != (B, T, heads, D):
             _check_rows(name, t, (B, T, heads, D), device)
+        if out is not None:
+            _check(name + "_out", out, bf16, (B, heads, T, D), device)
     rot, max_pos = _check_rope(cos_sin, q_weight, k_weight, positions, B, T, D, device)
-    for name, t, src in (("q_out", q_out, q), ("k_out", k_out, k), ("v_out", v_out, v)):
-        if t is not None:
-            if src is None:
-                raise ValueError(f"{name} is given without its input")
-            _check_tensor(name, t, torch.bfloat16, (B, src.shape[2], T, D), device)
     _require_cuda(device)
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        def out(t, src):
-            if t is not None or src is None:
-                return t
-            return torch.empty((B, src.shape[2], T, D), dtype=torch.bfloat16, device=device)
-        q_out, k_out, v_out = out(q_out, q), out(k_out, k), out(v_out, v)
-        st = lib().qkv_norm_rope(_ptr(q), _ptr(k), _ptr(v), _strides(q), _strides(k), _strides(v),
-                                 _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), _ptr(positions),
-                                 B, T, q.shape[2] if q is not None else 0,
-                                 kv.shape[2] if kv is not None else 0, D, rot, max_pos,
-                                 int(bool(interleaved)), float(eps), _ptr(q_out), _ptr(k_out),
-                                 _ptr(v_out), _stream_handle(stream, device))
+    with _On(device, stream) as handle:
+        if q_out is None and q is not None:
+            q_out = q.new_empty((B, Hq, T, D))
+        if k_out is None and k is not None:
+            k_out = k.new_empty((B, Hkv, T, D))
+        if v_out is None and v is not None:
+            v_out = v.new_empty((B, Hkv, T, D))
+        st = (_lib or lib()).qkv_norm_rope(
+            _ptr(q), _ptr(k), _ptr(v), _strides(q), _strides(k), _strides(v), _ptr(q_weight),
+            _ptr(k_weight), _ptr(cos_sin), _ptr(positions), B, T, Hq, Hkv, D, rot, max_pos,
+            1 if interleaved else 0, eps, _ptr(q_out), _ptr(k_out), _ptr(v_out), handle)
     if st != ATTN_OK:
         raise GbAttnError("qkv_norm_rope", st)
     return q_out, k_out, v_out
 
 
 def qkv_norm_rope_bwd_workspace_size(B: int, T: int, D: int) -> int:
-    return int(lib().qkv_norm_rope_bwd_workspace_size(B, T, D))
+    return (_lib or lib()).qkv_norm_rope_bwd_workspace_size(B, T, D)
 
 
 def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None, q_weight=None,
@@ -482,36 +548,37 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
     operand without a weight.
     """
     import torch
+    bf16 = torch.bfloat16
     some = _first(dq_out, dk_out, dv_out)
-    device = some.device if isinstance(some, torch.Tensor) else None
-    for name, t in (("dq_out", dq_out), ("dk_out", dk_out), ("dv_out", dv_out)):
-        if t is not None:
-            _check_bf16(name, t, 4, device)
+    device = some.device
+    if some.dim() != 4:
+        raise ValueError("gradients must be 4-d tensors")
     B, _, T, D = some.shape
-    kv = dk_out if dk_out is not None else dv_out
     Hq = dq_out.shape[1] if dq_out is not None else 0
-    Hkv = kv.shape[1] if kv is not None else 0
-    for name, t, heads in (("dq_out", dq_out, Hq), ("dk_out", dk_out, Hkv), ("dv_out", dv_out, Hkv)):
-        if t is not None and tuple(t.shape) != (B, heads, T, D):
-            raise ValueError(f"{name} must have shape {(B, heads, T, D)}, got {tuple(t.shape)}")
+    kv = dk_out if dk_out is not None else dv_out
+    Hkv = kv.shape[1] if kv is not None and kv.dim() > 1 else 0
+    for name, g, d, heads in (("dq", dq_out, dq, Hq), ("dk", dk_out, dk, Hkv),
+                              ("dv", dv_out, dv, Hkv)):
+        if g is None:
+            if d is not None:
+                raise ValueError(f"{name} is given without the gradient of its output")
+            continue
+        _check(name + "_out", g, bf16, (B, heads, T, D), device)
+        if d is not None:
+            _check_rows(name, d, (B, T, heads, D), device)
     rot, max_pos = _check_rope(cos_sin, q_weight, k_weight, positions, B, T, D, device)
-    for name, x, w, heads in (("q", q, q_weight, Hq), ("k", k, k_weight, Hkv)):
+    for name, x, w, dw, heads in (("q", q, q_weight, dq_weight, Hq),
+                                  ("k", k, k_weight, dk_weight, Hkv)):
         if w is None:
+            if dw is not None:
+                raise ValueError(f"d{name}_weight is given without its weight")
             continue
         if x is None:
             raise ValueError(f"{name} is needed for the gradient of its norm")
-        _check_rows(name, x, (B, T, heads, D), device)
-    for name, t, heads, g in (("dq", dq, Hq, dq_out), ("dk", dk, Hkv, dk_out),
-                              ("dv", dv, Hkv, dv_out)):
-        if t is not None:
-            if g is None:
-                raise ValueError(f"{name} is given without the gradient of its output")
-            _check_rows(name, t, (B, T, heads, D), device)
-    for name, t, w in (("dq_weight", dq_weight, q_weight), ("dk_weight", dk_weight, k_weight)):
-        if t is not None:
-            if w is None:
-                raise ValueError(f"{name} is given without its weight")
-            _check_tensor(name, t, torch.float32, (D,), device)
+        if not _is_rows(x, bf16, device) or x.shape != (B, T, heads, D):
+            _check_rows(name, x, (B, T, heads, D), device)
+        if dw is not None:
+            _check(f"d{name}_weight", dw, torch.float32, (D,), device)
     if workspace is not None:
         _check_tensor("workspace", workspace, torch.uint8, None, device)
     _require_cuda(device)
@@ -519,35 +586,31 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
         q = None
     if k_weight is None:
         k = None
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+    with _On(device, stream) as handle:
         if dq is None and dk is None and dv is None:
-            sizes = [Hq if dq_out is not None else 0, Hkv if dk_out is not None else 0,
-                     Hkv if dv_out is not None else 0]
-            fused = torch.empty((B, T, sum(sizes), D), dtype=torch.bfloat16, device=device)
-            dq, dk, dv = (t if n else None for t, n in zip(fused.split(sizes, 2), sizes))
-
-        def rows(t, g):
-            if t is not None or g is None:
-                return t
-            return torch.empty((B, T, g.shape[1], D), dtype=torch.bfloat16, device=device)
-
-        def vector(t, w):
-            if t is not None or w is None:
-                return t
-            return torch.empty((D,), dtype=torch.float32, device=device)
-        dq, dk, dv = rows(dq, dq_out), rows(dk, dk_out), rows(dv, dv_out)
-        dq_weight, dk_weight = vector(dq_weight, q_weight), vector(dk_weight, k_weight)
+            nq, nk = (Hq if dq_out is not None else 0), (Hkv if dk_out is not None else 0)
+            nv = Hkv if dv_out is not None else 0
+            fused = some.new_empty((B, T, nq + nk + nv, D))
+            dq = fused[:, :, :nq] if nq else None
+            dk = fused[:, :, nq:nq + nk] if nk else None
+            dv = fused[:, :, nq + nk:] if nv else None
+        else:
+            dq, dk, dv = (d if d is not None or g is None else
+                          g.new_empty((B, T, g.shape[1], D))
+                          for d, g in ((dq, dq_out), (dk, dk_out), (dv, dv_out)))
+        if dq_weight is None and q_weight is not None:
+            dq_weight = torch.empty((D,), dtype=torch.float32, device=device)
+        if dk_weight is None and k_weight is not None:
+            dk_weight = torch.empty((D,), dtype=torch.float32, device=device)
         if workspace is None and (q_weight is not None or k_weight is not None):
             need = qkv_norm_rope_bwd_workspace_size(B, T, D)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-        st = lib().qkv_norm_rope_bwd(_ptr(dq_out), _ptr(dk_out), _ptr(dv_out), _ptr(q), _ptr(k),
-                                     _strides(q), _strides(k), _ptr(q_weight), _ptr(k_weight),
-                                     _ptr(cos_sin), _ptr(positions), B, T, Hq, Hkv, D, rot,
-                                     max_pos, int(bool(interleaved)), float(eps), _ptr(dq),
-                                     _ptr(dk), _ptr(dv), _strides(dq), _strides(dk), _strides(dv),
-                                     _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
-                                     workspace.numel() if workspace is not None else 0,
-                                     _stream_handle(stream, device))
+            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=device)
+        st = (_lib or lib()).qkv_norm_rope_bwd(
+            _ptr(dq_out), _ptr(dk_out), _ptr(dv_out), _ptr(q), _ptr(k), _strides(q), _strides(k),
+            _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), _ptr(positions), B, T, Hq, Hkv, D, rot,
+            max_pos, 1 if interleaved else 0, eps, _ptr(dq), _ptr(dk), _ptr(dv), _strides(dq),
+            _strides(dk), _strides(dv), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
+            workspace.numel() if workspace is not None else 0, handle)
     if st != ATTN_OK:
         raise GbAttnError("qkv_norm_rope_bwd", st)
     return dq, dk, dv, dq_weight, dk_weight
@@ -556,16 +619,24 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
 def _append(op, pools, q, k, v, block_table, seq_lens, cos_sin, q_weight, k_weight, eps,
             interleaved, positions, q_out, new_seq_lens, stream):
     import torch
-    device = k.device if isinstance(k, torch.Tensor) else None
-    _check_rows("k", k, (None,) * 4, device)
+    bf16, i32 = torch.bfloat16, torch.int32
+    _first(k)
+    device = k.device
+    if not _is_rows(k, bf16, device):
+        _check_rows("k", k, (None,) * 4, device)
     S, Tn, Hkv, D = k.shape
-    _check_rows("v", v, (S, Tn, Hkv, D), device)
+    if not _is_rows(v, bf16, device) or v.shape != (S, Tn, Hkv, D):
+        _check_rows("v", v, (S, Tn, Hkv, D), device)
+    Hq = 0
     if q is not None:
-        _check_rows("q", q, (S, Tn, None, D), device)
-    Hq = q.shape[2] if q is not None else 0
-    for name, t in (("block_table", block_table), ("seq_lens", seq_lens)):
-        _check_tensor(name, t, torch.int32, None, device)
-    if block_table.dim() != 2 or block_table.shape[0] != S or tuple(seq_lens.shape) != (S,):
+        if not _is_rows(q, bf16, device):
+            _check_rows("q", q, (S, Tn, None, D), device)
+        Hq = q.shape[2]
+        if q.shape != (S, Tn, Hq, D):
+            _check_rows("q", q, (S, Tn, None, D), device)
+    _check("seq_lens", seq_lens, i32, (S,), device)
+    _check_tensor("block_table", block_table, i32, None, device)
+    if block_table.dim() != 2 or block_table.shape[0] != S:
         raise ValueError("inconsistent append shapes")
     if len(pools) == 2:
         for name, t in zip(("k_pool", "v_pool"), pools):
@@ -579,19 +650,19 @@ def _append(op, pools, q, k, v, block_table, seq_lens, cos_sin, q_weight, k_weig
     if q_out is not None:
         if q is None:
             raise ValueError("q_out is given without q")
-        _check_tensor("q_out", q_out, torch.bfloat16, (S, Hq, Tn, D), device)
+        _check("q_out", q_out, bf16, (S, Hq, Tn, D), device)
     if new_seq_lens is not None:
-        _check_tensor("new_seq_lens", new_seq_lens, torch.int32, (S,), device)
+        _check("new_seq_lens", new_seq_lens, i32, (S,), device)
     _require_cuda(device)
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+    with _On(device, stream) as handle:
         if q is not None and q_out is None:
-            q_out = torch.empty((S, Hq, Tn, D), dtype=torch.bfloat16, device=device)
-        st = getattr(lib(), op)(_ptr(q), _ptr(k), _ptr(v), _strides(q), _strides(k), _strides(v),
-                                _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), _ptr(positions),
-                                *(_ptr(t) for t in pools), block_table.data_ptr(),
-                                seq_lens.data_ptr(), _ptr(new_seq_lens), bs, S, Tn, Hq, Hkv, D,
-                                block_table.shape[1], NB, rot, max_pos, int(bool(interleaved)),
-                                float(eps), _ptr(q_out), _stream_handle(stream, device))
+            q_out = q.new_empty((S, Hq, Tn, D))
+        st = getattr(_lib or lib(), op)(
+            _ptr(q), k.data_ptr(), v.data_ptr(), _strides(q), _strides(k), _strides(v),
+            _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), _ptr(positions),
+            *[t.data_ptr() for t in pools], block_table.data_ptr(), seq_lens.data_ptr(),
+            _ptr(new_seq_lens), bs, S, Tn, Hq, Hkv, D, block_table.shape[1], NB, rot, max_pos,
+            1 if interleaved else 0, eps, _ptr(q_out), handle)
     if st != ATTN_OK:
         raise GbAttnError(op, st)
     return q_out, new_seq_lens
@@ -618,11 +689,12 @@ def _check_kv4(name, pool, Hkv, D, device):
     if isinstance(pool, torch.Tensor) and pool.dim() != 3:
         raise ValueError(f"{name} must be a 3-d tensor")
     _check_tensor(name, pool, torch.uint8, None, device)
-    if Hkv is not None and (pool.shape[1] != Hkv or pool.shape[2] != 18 * D):
+    NB, heads, chunk = pool.shape
+    if Hkv is not None and (heads != Hkv or chunk != 18 * D):
         raise ValueError(f"{name} must have shape (blocks, {Hkv}, {18 * D}), got {tuple(pool.shape)}")
-    if pool.shape[2] % 18 != 0:
-        raise ValueError(f"{name} must have 18 D bytes per block and head, got {pool.shape[2]}")
-    return pool.shape[0]
+    if chunk % 18 != 0:
+        raise ValueError(f"{name} must have 18 D bytes per block and head, got {chunk}")
+    return NB
 
 
 def paged_kv4_append(q, k, v, kv_pool, block_table, seq_lens, cos_sin=None, q_weight=None,
@@ -639,35 +711,60 @@ def paged_kv4_gather(kv_pool, block_table, seq_lens, max_seq_len: int, k_out=Non
     """The values the 4-bit cache holds, in logical order: k_out, v_out
     [S,Hkv,max_seq_len,D] bf16 (rows past a request's length are left as they were)."""
     import torch
-    device = kv_pool.device if isinstance(kv_pool, torch.Tensor) else None
+    _first(kv_pool)
+    device = kv_pool.device
     NB = _check_kv4("kv_pool", kv_pool, None, None, device)
+    _, Hkv, chunk = kv_pool.shape
+    D = chunk // 18
     for name, t in (("block_table", block_table), ("seq_lens", seq_lens)):
         _check_tensor(name, t, torch.int32, None, device)
-    Hkv, D = kv_pool.shape[1], kv_pool.shape[2] // 18
-    S = seq_lens.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != S or seq_lens.dim() != 1:
+    if seq_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != seq_lens.shape[0]:
         raise ValueError("inconsistent gather shapes")
+    S = seq_lens.shape[0]
+    shape = (S, Hkv, max_seq_len, D)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
-            _check_tensor(name, t, torch.bfloat16, (S, Hkv, max_seq_len, D), device)
+            _check(name, t, torch.bfloat16, shape, device)
     _require_cuda(device)
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        def out(t):
-            if t is not None:
-                return t
-            return torch.zeros((S, Hkv, max_seq_len, D), dtype=torch.bfloat16, device=device)
-        k_out, v_out = out(k_out), out(v_out)
-        st = lib().paged_kv4_gather(kv_pool.data_ptr(), block_table.data_ptr(),
-                                    seq_lens.data_ptr(), 16, S, Hkv, D, block_table.shape[1], NB,
-                                    int(max_seq_len), k_out.data_ptr(), v_out.data_ptr(),
-                                    _stream_handle(stream, device))
+    with _On(device, stream) as handle:
+        if k_out is None:
+            k_out = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+        if v_out is None:
+            v_out = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+        st = (_lib or lib()).paged_kv4_gather(
+            kv_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), 16, S, Hkv, D,
+            block_table.shape[1], NB, max_seq_len, k_out.data_ptr(), v_out.data_ptr(), handle)
     if st != ATTN_OK:
         raise GbAttnError("paged_kv4_gather", st)
     return k_out, v_out
 
 
+def _check_kv4_attention(q, kv_pool, block_table, lens, rows, out, lse):
+    """The operands that the two attention calls share: q is [S, Hq, *rows, D]."""
+    import torch
+    _first(q)
+    device = q.device
+    ndim = 3 + rows
+    if q.dim() != ndim:
+        raise ValueError(f"q must be a {ndim}-d tensor")
+    shape = q.shape
+    _check("q", q, torch.bfloat16, shape, device)
+    NB = _check_kv4("kv_pool", kv_pool, None, None, device)
+    _check_tensor("block_table", block_table, torch.int32, None, device)
+    _check("the lengths", lens, torch.int32, shape[:1], device)
+    if kv_pool.shape[2] != 18 * shape[-1] or block_table.dim() != 2 or \
+            block_table.shape[0] != shape[0]:
+        raise ValueError("inconsistent paged attention shapes")
+    if out is not None:
+        _check("out", out, torch.bfloat16, shape, device)
+    if lse is not None:
+        _check("lse", lse, torch.float32, shape[:-1], device)
+    _require_cuda(device)
+    return device, NB
+
+
 def paged_kv4_attn_decode_workspace_size(num_seqs: int, Hq: int, D: int, max_seq_len: int) -> int:
-    return int(lib().paged_kv4_attn_decode_workspace_size(num_seqs, Hq, D, max_seq_len))
+    return (_lib or lib()).paged_kv4_attn_decode_workspace_size(num_seqs, Hq, D, max_seq_len)
 
 
 def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
@@ -680,37 +777,24 @@ def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
     ``workspace`` (uint8 CUDA tensor) is allocated here when not given.
     """
     import torch
-    device = q.device if isinstance(q, torch.Tensor) else None
-    _check_bf16("q", q, 3, device)
+    device, NB = _check_kv4_attention(q, kv_pool, block_table, seq_lens, 0, out, lse)
     S, Hq, D = q.shape
-    NB = _check_kv4("kv_pool", kv_pool, None, None, device)
-    for name, t in (("block_table", block_table), ("seq_lens", seq_lens)):
-        _check_tensor(name, t, torch.int32, None, device)
-    if kv_pool.shape[2] != 18 * D or block_table.dim() != 2 or block_table.shape[0] != S or \
-            tuple(seq_lens.shape) != (S,):
-        raise ValueError("inconsistent paged-decode shapes")
-    if out is not None:
-        _check_tensor("out", out, torch.bfloat16, (S, Hq, D), device)
-    if lse is not None:
-        _check_tensor("lse", lse, torch.float32, (S, Hq), device)
     if workspace is not None:
         _check_tensor("workspace", workspace, torch.uint8, None, device)
-    _require_cuda(device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+    with _On(device, stream) as handle:
         if workspace is None:
             need = paged_kv4_attn_decode_workspace_size(S, Hq, D, max_seq_len)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=device)
         if out is None:
-            out = torch.empty_like(q)
+            out = q.new_empty((S, Hq, D))
         if return_lse and lse is None:
             lse = torch.empty((S, Hq), dtype=torch.float32, device=device)
-        st = lib().paged_kv4_attn_decode(q.data_ptr(), kv_pool.data_ptr(), block_table.data_ptr(),
-                                         seq_lens.data_ptr(), 16, S, Hq, kv_pool.shape[1], D,
-                                         block_table.shape[1], NB, int(max_seq_len), float(scale),
-                                         out.data_ptr(), _ptr(lse), workspace.data_ptr(),
-                                         workspace.numel(), _stream_handle(stream, device))
+        st = (_lib or lib()).paged_kv4_attn_decode(
+            q.data_ptr(), kv_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), 16, S,
+            Hq, kv_pool.shape[1], D, block_table.shape[1], NB, max_seq_len, scale, out.data_ptr(),
+            _ptr(lse), workspace.data_ptr(), workspace.numel(), handle)
     if st != ATTN_OK:
         raise GbAttnError("paged_kv4_attn_decode", st)
     return out, lse
@@ -727,33 +811,19 @@ def paged_kv4_attn_prefill(q, kv_pool, block_table, kv_lens, max_kv_len: int,
     position kv_lens[b] - Tq + i.
     """
     import torch
-    device = q.device if isinstance(q, torch.Tensor) else None
-    _check_bf16("q", q, 4, device)
+    device, NB = _check_kv4_attention(q, kv_pool, block_table, kv_lens, 1, out, lse)
     B, Hq, Tq, D = q.shape
-    NB = _check_kv4("kv_pool", kv_pool, None, None, device)
-    for name, t in (("block_table", block_table), ("kv_lens", kv_lens)):
-        _check_tensor(name, t, torch.int32, None, device)
-    if kv_pool.shape[2] != 18 * D or block_table.dim() != 2 or block_table.shape[0] != B or \
-            tuple(kv_lens.shape) != (B,):
-        raise ValueError("inconsistent paged-prefill shapes")
-    if out is not None:
-        _check_tensor("out", out, torch.bfloat16, (B, Hq, Tq, D), device)
-    if lse is not None:
-        _check_tensor("lse", lse, torch.float32, (B, Hq, Tq), device)
-    _require_cuda(device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+    with _On(device, stream) as handle:
         if out is None:
-            out = torch.empty_like(q)
+            out = q.new_empty((B, Hq, Tq, D))
         if return_lse and lse is None:
             lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=device)
-        st = lib().paged_kv4_attn_prefill(q.data_ptr(), kv_pool.data_ptr(),
-                                          block_table.data_ptr(), kv_lens.data_ptr(), 16, B, Hq,
-                                          kv_pool.shape[1], Tq, D, block_table.shape[1], NB,
-                                          int(max_kv_len), int(bool(causal)), float(scale),
-                                          out.data_ptr(), _ptr(lse),
-                                          _stream_handle(stream, device))
+        st = (_lib or lib()).paged_kv4_attn_prefill(
+            q.data_ptr(), kv_pool.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), 16, B,
+            Hq, kv_pool.shape[1], Tq, D, block_table.shape[1], NB, max_kv_len,
+            1 if causal else 0, scale, out.data_ptr(), _ptr(lse), handle)
     if st != ATTN_OK:
         raise GbAttnError("paged_kv4_attn_prefill", st)
     return out, lse
