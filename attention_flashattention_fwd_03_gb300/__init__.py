@@ -60,7 +60,7 @@ EXPORTS = (
 
 _lock = threading.Lock()
 _lib = None
-_Tensor = None  # torch.Tensor, once an operator below has been called
+_torch = _Tensor = None  # torch and torch.Tensor, once an operator that needs them is called
 
 
 class GbAttnError(RuntimeError):
@@ -385,14 +385,13 @@ class _On:
         self.device, self.stream, self.inner = device, stream, None
 
     def __enter__(self):
-        import torch
-        if self.stream is not None or torch.cuda.current_device() != self.device.index:
-            self.inner = (torch.cuda.device(self.device), torch.cuda.stream(self.stream))
+        if self.stream is not None or _torch.cuda.current_device() != self.device.index:
+            self.inner = (_torch.cuda.device(self.device), _torch.cuda.stream(self.stream))
             for c in self.inner:
                 c.__enter__()
         if self.stream is not None:
             return self.stream.cuda_stream
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return _torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def __exit__(self, *exc):
         if self.inner is not None:
@@ -418,11 +417,10 @@ def _is_rows(t, bf16, device):
 def _check_rows(name, t, shape, device):
     """Raises for what is wrong with a [B, T, H, D] operand; `shape` may hold None for a
     free dimension.  Metadata checks only."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dtype != _torch.bfloat16:
+        raise ValueError(f"{name} must be {_torch.bfloat16}, got {t.dtype}")
     if t.dim() != 4 or any(n is not None and n != m for n, m in zip(shape, t.shape)):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.shape[3] > 1 and t.stride(3) != 1:
@@ -451,30 +449,34 @@ def _ptr(t):
 
 def _check_rope(cos_sin, q_weight, k_weight, positions, B, T, D, device):
     """Checks the norm and rotation operands; returns (rot_dim, max_pos)."""
-    import torch
     if q_weight is not None:
-        _check("q_weight", q_weight, torch.bfloat16, (D,), device)
+        _check("q_weight", q_weight, _torch.bfloat16, (D,), device)
     if k_weight is not None:
-        _check("k_weight", k_weight, torch.bfloat16, (D,), device)
+        _check("k_weight", k_weight, _torch.bfloat16, (D,), device)
     if positions is not None:
-        _check("positions", positions, torch.int32, (B, T), device)
+        _check("positions", positions, _torch.int32, (B, T), device)
     if cos_sin is None:
         return 0, 0
-    _check_tensor("cos_sin", cos_sin, torch.float32, None, device)
-    if cos_sin.dim() != 2 or cos_sin.numel() == 0:
+    shape = cos_sin.shape if isinstance(cos_sin, _Tensor) else None
+    _check("cos_sin", cos_sin, _torch.float32, shape, device)
+    if len(shape) != 2 or shape[0] == 0 or shape[1] == 0:
         raise ValueError("cos_sin must be a non-empty [max_pos, rot_dim] table")
-    max_pos, rot = cos_sin.shape
-    return rot, max_pos
+    return shape[1], shape[0]
+
+
+def _load_torch():
+    global _torch, _Tensor
+    import torch
+    _torch, _Tensor = torch, torch.Tensor
 
 
 def _first(*tensors):
     """The first operand given, after making sure that it is a tensor."""
-    import torch
-    global _Tensor
-    _Tensor = torch.Tensor
+    if _torch is None:
+        _load_torch()
     for t in tensors:
         if t is not None:
-            if not isinstance(t, torch.Tensor):
+            if not isinstance(t, _Tensor):
                 raise TypeError(f"operands must be torch.Tensor, got {type(t)}")
             return t
     raise ValueError("at least one operand is needed")
@@ -492,9 +494,8 @@ def qkv_norm_rope(q, k, v=None, cos_sin=None, q_weight=None, k_weight=None, eps:
     each position (None: no rotation); ``q_weight``/``k_weight`` [D] bf16 (None: no
     norm); ``positions`` [B,T] int32 (None: 0 .. T-1).
     """
-    import torch
-    bf16 = torch.bfloat16
     some = _first(q, k, v)
+    bf16 = _torch.bfloat16
     device = some.device
     for name, t in (("q", q), ("k", k), ("v", v)):
         if t is not None and not _is_rows(t, bf16, device):
@@ -517,11 +518,11 @@ def qkv_norm_rope(q, k, v=None, cos_sin=None, q_weight=None, k_weight=None, eps:
     _require_cuda(device)
     with _On(device, stream) as handle:
         if q_out is None and q is not None:
-            q_out = q.new_empty((B, Hq, T, D))
+            q_out = _torch.empty((B, Hq, T, D), dtype=bf16, device=device)
         if k_out is None and k is not None:
-            k_out = k.new_empty((B, Hkv, T, D))
+            k_out = _torch.empty((B, Hkv, T, D), dtype=bf16, device=device)
         if v_out is None and v is not None:
-            v_out = v.new_empty((B, Hkv, T, D))
+            v_out = _torch.empty((B, Hkv, T, D), dtype=bf16, device=device)
         st = (_lib or lib()).qkv_norm_rope(
             _ptr(q), _ptr(k), _ptr(v), _strides(q), _strides(k), _strides(v), _ptr(q_weight),
             _ptr(k_weight), _ptr(cos_sin), _ptr(positions), B, T, Hq, Hkv, D, rot, max_pos,
@@ -547,9 +548,8 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
     the gradient of a fused projection.  The weight gradients [D] are fp32, None for an
     operand without a weight.
     """
-    import torch
-    bf16 = torch.bfloat16
     some = _first(dq_out, dk_out, dv_out)
+    bf16 = _torch.bfloat16
     device = some.device
     if some.dim() != 4:
         raise ValueError("gradients must be 4-d tensors")
@@ -578,9 +578,9 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
         if not _is_rows(x, bf16, device) or x.shape != (B, T, heads, D):
             _check_rows(name, x, (B, T, heads, D), device)
         if dw is not None:
-            _check(f"d{name}_weight", dw, torch.float32, (D,), device)
+            _check(f"d{name}_weight", dw, _torch.float32, (D,), device)
     if workspace is not None:
-        _check_tensor("workspace", workspace, torch.uint8, None, device)
+        _check_tensor("workspace", workspace, _torch.uint8, None, device)
     _require_cuda(device)
     if q_weight is None:
         q = None
@@ -590,21 +590,21 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
         if dq is None and dk is None and dv is None:
             nq, nk = (Hq if dq_out is not None else 0), (Hkv if dk_out is not None else 0)
             nv = Hkv if dv_out is not None else 0
-            fused = some.new_empty((B, T, nq + nk + nv, D))
+            fused = _torch.empty((B, T, nq + nk + nv, D), dtype=bf16, device=device)
             dq = fused[:, :, :nq] if nq else None
             dk = fused[:, :, nq:nq + nk] if nk else None
             dv = fused[:, :, nq + nk:] if nv else None
         else:
             dq, dk, dv = (d if d is not None or g is None else
-                          g.new_empty((B, T, g.shape[1], D))
+                          _torch.empty((B, T, g.shape[1], D), dtype=bf16, device=device)
                           for d, g in ((dq, dq_out), (dk, dk_out), (dv, dv_out)))
         if dq_weight is None and q_weight is not None:
-            dq_weight = torch.empty((D,), dtype=torch.float32, device=device)
+            dq_weight = _torch.empty((D,), dtype=_torch.float32, device=device)
         if dk_weight is None and k_weight is not None:
-            dk_weight = torch.empty((D,), dtype=torch.float32, device=device)
+            dk_weight = _torch.empty((D,), dtype=_torch.float32, device=device)
         if workspace is None and (q_weight is not None or k_weight is not None):
             need = qkv_norm_rope_bwd_workspace_size(B, T, D)
-            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=device)
+            workspace = _torch.empty((max(need, 256),), dtype=_torch.uint8, device=device)
         st = (_lib or lib()).qkv_norm_rope_bwd(
             _ptr(dq_out), _ptr(dk_out), _ptr(dv_out), _ptr(q), _ptr(k), _strides(q), _strides(k),
             _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), _ptr(positions), B, T, Hq, Hkv, D, rot,
@@ -618,9 +618,8 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
 
 def _append(op, pools, q, k, v, block_table, seq_lens, cos_sin, q_weight, k_weight, eps,
             interleaved, positions, q_out, new_seq_lens, stream):
-    import torch
-    bf16, i32 = torch.bfloat16, torch.int32
     _first(k)
+    bf16, i32 = _torch.bfloat16, _torch.int32
     device = k.device
     if not _is_rows(k, bf16, device):
         _check_rows("k", k, (None,) * 4, device)
@@ -639,10 +638,11 @@ def _append(op, pools, q, k, v, block_table, seq_lens, cos_sin, q_weight, k_weig
     if block_table.dim() != 2 or block_table.shape[0] != S:
         raise ValueError("inconsistent append shapes")
     if len(pools) == 2:
-        for name, t in zip(("k_pool", "v_pool"), pools):
-            _check_bf16(name, t, 4, device)
-        NB, Hkv2, bs, D2 = pools[0].shape
-        if pools[1].shape != pools[0].shape or Hkv2 != Hkv or D2 != D:
+        _check_bf16("k_pool", pools[0], 4, device)
+        shape = pools[0].shape
+        _check("v_pool", pools[1], bf16, shape, device)
+        NB, Hkv2, bs, D2 = shape
+        if Hkv2 != Hkv or D2 != D:
             raise ValueError("inconsistent append shapes")
     else:
         NB, bs = _check_kv4("kv_pool", pools[0], Hkv, D, device), 16
@@ -656,7 +656,7 @@ def _append(op, pools, q, k, v, block_table, seq_lens, cos_sin, q_weight, k_weig
     _require_cuda(device)
     with _On(device, stream) as handle:
         if q is not None and q_out is None:
-            q_out = q.new_empty((S, Hq, Tn, D))
+            q_out = _torch.empty((S, Hq, Tn, D), dtype=bf16, device=device)
         st = getattr(_lib or lib(), op)(
             _ptr(q), k.data_ptr(), v.data_ptr(), _strides(q), _strides(k), _strides(v),
             _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), _ptr(positions),
@@ -685,10 +685,9 @@ def paged_qkv_append(q, k, v, k_pool, v_pool, block_table, seq_lens, cos_sin=Non
 
 def _check_kv4(name, pool, Hkv, D, device):
     """A 4-bit pool [NB, Hkv, 18 D] uint8; returns NB."""
-    import torch
-    if isinstance(pool, torch.Tensor) and pool.dim() != 3:
+    if isinstance(pool, _Tensor) and pool.dim() != 3:
         raise ValueError(f"{name} must be a 3-d tensor")
-    _check_tensor(name, pool, torch.uint8, None, device)
+    _check_tensor(name, pool, _torch.uint8, None, device)
     NB, heads, chunk = pool.shape
     if Hkv is not None and (heads != Hkv or chunk != 18 * D):
         raise ValueError(f"{name} must have shape (blocks, {Hkv}, {18 * D}), got {tuple(pool.shape)}")
@@ -710,27 +709,26 @@ def paged_kv4_gather(kv_pool, block_table, seq_lens, max_seq_len: int, k_out=Non
                      stream=None):
     """The values the 4-bit cache holds, in logical order: k_out, v_out
     [S,Hkv,max_seq_len,D] bf16 (rows past a request's length are left as they were)."""
-    import torch
     _first(kv_pool)
     device = kv_pool.device
     NB = _check_kv4("kv_pool", kv_pool, None, None, device)
     _, Hkv, chunk = kv_pool.shape
     D = chunk // 18
     for name, t in (("block_table", block_table), ("seq_lens", seq_lens)):
-        _check_tensor(name, t, torch.int32, None, device)
+        _check_tensor(name, t, _torch.int32, None, device)
     if seq_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != seq_lens.shape[0]:
         raise ValueError("inconsistent gather shapes")
     S = seq_lens.shape[0]
     shape = (S, Hkv, max_seq_len, D)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
-            _check(name, t, torch.bfloat16, shape, device)
+            _check(name, t, _torch.bfloat16, shape, device)
     _require_cuda(device)
     with _On(device, stream) as handle:
         if k_out is None:
-            k_out = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+            k_out = _torch.zeros(shape, dtype=_torch.bfloat16, device=device)
         if v_out is None:
-            v_out = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+            v_out = _torch.zeros(shape, dtype=_torch.bfloat16, device=device)
         st = (_lib or lib()).paged_kv4_gather(
             kv_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), 16, S, Hkv, D,
             block_table.shape[1], NB, max_seq_len, k_out.data_ptr(), v_out.data_ptr(), handle)
@@ -741,24 +739,23 @@ def paged_kv4_gather(kv_pool, block_table, seq_lens, max_seq_len: int, k_out=Non
 
 def _check_kv4_attention(q, kv_pool, block_table, lens, rows, out, lse):
     """The operands that the two attention calls share: q is [S, Hq, *rows, D]."""
-    import torch
     _first(q)
     device = q.device
     ndim = 3 + rows
     if q.dim() != ndim:
         raise ValueError(f"q must be a {ndim}-d tensor")
     shape = q.shape
-    _check("q", q, torch.bfloat16, shape, device)
+    _check("q", q, _torch.bfloat16, shape, device)
     NB = _check_kv4("kv_pool", kv_pool, None, None, device)
-    _check_tensor("block_table", block_table, torch.int32, None, device)
-    _check("the lengths", lens, torch.int32, shape[:1], device)
+    _check_tensor("block_table", block_table, _torch.int32, None, device)
+    _check("the lengths", lens, _torch.int32, shape[:1], device)
     if kv_pool.shape[2] != 18 * shape[-1] or block_table.dim() != 2 or \
             block_table.shape[0] != shape[0]:
         raise ValueError("inconsistent paged attention shapes")
     if out is not None:
-        _check("out", out, torch.bfloat16, shape, device)
+        _check("out", out, _torch.bfloat16, shape, device)
     if lse is not None:
-        _check("lse", lse, torch.float32, shape[:-1], device)
+        _check("lse", lse, _torch.float32, shape[:-1], device)
     _require_cuda(device)
     return device, NB
 
@@ -776,21 +773,20 @@ def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
     seq_lens [S] int32 (all CUDA) -> (o [S,Hq,D] bf16, lse [S,Hq] fp32).
     ``workspace`` (uint8 CUDA tensor) is allocated here when not given.
     """
-    import torch
     device, NB = _check_kv4_attention(q, kv_pool, block_table, seq_lens, 0, out, lse)
     S, Hq, D = q.shape
     if workspace is not None:
-        _check_tensor("workspace", workspace, torch.uint8, None, device)
+        _check_tensor("workspace", workspace, _torch.uint8, None, device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     with _On(device, stream) as handle:
         if workspace is None:
             need = paged_kv4_attn_decode_workspace_size(S, Hq, D, max_seq_len)
-            workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=device)
+            workspace = _torch.empty((max(need, 256),), dtype=_torch.uint8, device=device)
         if out is None:
-            out = q.new_empty((S, Hq, D))
+            out = _torch.empty((S, Hq, D), dtype=_torch.bfloat16, device=device)
         if return_lse and lse is None:
-            lse = torch.empty((S, Hq), dtype=torch.float32, device=device)
+            lse = _torch.empty((S, Hq), dtype=_torch.float32, device=device)
         st = (_lib or lib()).paged_kv4_attn_decode(
             q.data_ptr(), kv_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), 16, S,
             Hq, kv_pool.shape[1], D, block_table.shape[1], NB, max_seq_len, scale, out.data_ptr(),
@@ -810,16 +806,15 @@ def paged_kv4_attn_prefill(q, kv_pool, block_table, kv_lens, max_kv_len: int,
     [B,Hq,Tq,D] bf16, lse [B,Hq,Tq] fp32).  Query i of item b sits at logical
     position kv_lens[b] - Tq + i.
     """
-    import torch
     device, NB = _check_kv4_attention(q, kv_pool, block_table, kv_lens, 1, out, lse)
     B, Hq, Tq, D = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     with _On(device, stream) as handle:
         if out is None:
-            out = q.new_empty((B, Hq, Tq, D))
+            out = _torch.empty((B, Hq, Tq, D), dtype=_torch.bfloat16, device=device)
         if return_lse and lse is None:
-            lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=device)
+            lse = _torch.empty((B, Hq, Tq), dtype=_torch.float32, device=device)
         st = (_lib or lib()).paged_kv4_attn_prefill(
             q.data_ptr(), kv_pool.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), 16, B,
             Hq, kv_pool.shape[1], Tq, D, block_table.shape[1], NB, max_kv_len,
