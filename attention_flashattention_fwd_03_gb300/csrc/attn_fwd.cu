@@ -19,8 +19,8 @@
 //                 tile's while this one is copied) and each copies its block's
 //                 16 rows (of the 4-bit cache: its block's codes and scales, into
 //                 a ring of raw half chunks)
-//   warps 2, 3    4-bit cache: turn a raw K or V tile into the bf16 slot the MMA
-//                 warp reads.  Every value n s is a bf16 exactly, so these are the
+//   warps 12-15   4-bit cache: turn a raw K or V tile into the bf16 slot the MMA
+//                 warp reads, 32 keys each.  Every value n s is a bf16 exactly, so these are the
 //                 operands themselves, not an approximation of them
 //   warp 1        MMA warp (the converged warp runs the issue code; elect.sync
 //                 picks the lane that issues): S_i = Q_i K_j^T into TMEM (fp32),
@@ -62,19 +62,25 @@ namespace gbattn {
 
 namespace {
 
+// Where keys and values come from: contiguous tensors, the bf16 pools or the 4-bit pool.
+enum class Src { kContiguous, kPaged, kPaged4 };
+
 constexpr int BM = 128;          // query rows per tile (= TMEM lanes)
 constexpr int BN = 128;          // keys per K/V tile
 constexpr int kBS = 16;          // tokens per paged KV block
-constexpr int kThreads = 384;    // warpgroup 0: producer, MMA, 2 idle warps; 1, 2: softmax
+// Warpgroup 0: producer, MMA, 2 idle warps; 1, 2: softmax; 3 (4-bit cache): dequantisers.
+template <Src SRC>
+constexpr int kThreads = SRC == Src::kPaged4 ? 512 : 384;
 constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by > 2^8
 // Registers per thread: the block launches with 168 (384 threads, one block per
 // SM); warpgroup 0 gives some up so the softmax warpgroups, which hold a whole
 // 128-key score row each, get more: 104 + 200 + 200 = 3 x 168.
 constexpr int kRegsLaunch = 168, kRegsWg0 = 104, kRegsSoftmax = 200;
 static_assert(kRegsWg0 + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split exceeds the launch");
-
-// Where keys and values come from: contiguous tensors, the bf16 pools or the 4-bit pool.
-enum class Src { kContiguous, kPaged, kPaged4 };
+// With the dequantisers the block launches with 128: 64 + 64 + 192 + 192 = 4 x 128.
+constexpr int kRegsLaunch4 = 128, kRegsWg0With4 = 64, kRegsDequant = 64, kRegsSoftmax4 = 192;
+static_assert(kRegsWg0With4 + kRegsDequant + 2 * kRegsSoftmax4 <= 4 * kRegsLaunch4,
+              "register split exceeds the launch");
 
 template <int D, Src SRC>
 struct Cfg {
@@ -306,7 +312,7 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
 }
 
 // ---------------------------------------------------------------------------
-// 4-bit cache: warps 2 and 3 turn raw K and V tiles into bf16 slots, 64 keys each
+// 4-bit cache: warps 12-15 turn raw K and V tiles into bf16 slots, 32 keys each
 // ---------------------------------------------------------------------------
 
 // Eight codes of one word (low nibble first) times a scale pair (s, s), as four bf16
@@ -334,7 +340,7 @@ __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SR
   using F = Kv4<D>;
   constexpr int G = F::kGroups;
   const int lane = threadIdx.x & 31;
-  const int half = (threadIdx.x >> 5) & 1;  // warp 2: keys 0..63 of a tile, warp 3: 64..127
+  const int part = (threadIdx.x >> 5) & 3;  // the warp's 32 keys of every tile
   const unsigned long long lim = p.wait_limit_ns;
   int rc = 0;
   for (int r = 0; r * static_cast<int>(gridDim.x) < p.num_units; ++r) {
@@ -353,8 +359,8 @@ __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SR
         const int valid = U.L - j * BN;  // keys past the cache's end become zeros
         // a lane takes a quarter of a key's codes: 8 channels of every group
 #pragma unroll 2
-        for (int i = 0; i < 8; ++i) {
-          const int key = half * 64 + i * 8 + (lane >> 2), t = lane & 3;
+        for (int i = 0; i < 4; ++i) {
+          const int key = part * 32 + i * 8 + (lane >> 2), t = lane & 3;
           const uint8_t* blk = raw + (key / kBS) * C::RAW_BLOCK;
           const uint8_t* cp = blk + (key % kBS) * F::kCodeRow + t * (4 * G);
           const uint8_t* sp = blk + kBS * F::kCodeRow + (key % kBS) * F::kScaleRow;
@@ -699,7 +705,7 @@ __device__ void softmax_wg(const FwdParams& p, uint32_t tmem, const Bars<D, SRC>
 }
 
 template <int D, Src SRC>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<SRC>, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
   using C = Cfg<D, SRC>;
@@ -716,12 +722,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar.q_full(), 1);
     mbar_init(bar.q_empty(), 1);
     for (int s = 0; s < C::NSLOT; ++s) {
-      mbar_init(bar.slot_full(s), SRC == Src::kPaged4 ? 2 : 1);
+      mbar_init(bar.slot_full(s), SRC == Src::kPaged4 ? 4 : 1);
       mbar_init(bar.slot_empty(s), 1);
     }
     for (int s = 0; s < C::NRAW; ++s) {
       mbar_init(bar.raw_full(s), 1);
-      mbar_init(bar.raw_empty(s), 2);
+      mbar_init(bar.raw_empty(s), 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar.s_full(i), 1);
@@ -748,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp < 4) {
-    regs_decrease<kRegsWg0>();
+    regs_decrease<SRC == Src::kPaged4 ? kRegsWg0With4 : kRegsWg0>();
     if (warp == 0) {
       producer_warp<D, SRC>(&tmQ, &tmK, &tmV, p, sbase, bar, abort);
     } else if (warp == 1) {
@@ -758,11 +764,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit_warp(bar.teardown());
       if (lane == 0) mbar_wait_quiet(bar.teardown(), 0, 1000000000ull);
       __syncwarp();
-    } else if constexpr (SRC == Src::kPaged4) {
+    }
+  } else if (SRC == Src::kPaged4 && warp >= 12) {
+    if constexpr (SRC == Src::kPaged4) {
+      regs_decrease<kRegsDequant>();
       dequant_warp<D, SRC>(p, smem, bar, abort);
     }
   } else {
-    regs_increase<kRegsSoftmax>();
+    regs_increase<SRC == Src::kPaged4 ? kRegsSoftmax4 : kRegsSoftmax>();
     softmax_wg<D, SRC>(p, tmem, bar, abort, warp < 8 ? 0 : 1);
   }
 
@@ -783,7 +792,7 @@ cudaError_t set_smem() {
 template <int D, Src SRC>
 void launch(int grid, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
             const FwdParams& p, cudaStream_t stream) {
-  attn_fwd_kernel<D, SRC><<<grid, kThreads, (Cfg<D, SRC>::SMEM_BYTES), stream>>>(tmQ, tmK, tmV, p);
+  attn_fwd_kernel<D, SRC><<<grid, kThreads<SRC>, (Cfg<D, SRC>::SMEM_BYTES), stream>>>(tmQ, tmK, tmV, p);
 }
 
 }  // namespace
