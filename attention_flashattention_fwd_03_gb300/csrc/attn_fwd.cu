@@ -315,11 +315,14 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
 // 4-bit cache: warps 12-15 turn raw K and V tiles into bf16 slots, 32 keys each
 // ---------------------------------------------------------------------------
 
-// Eight codes of one word (low nibble first) times a scale pair (s, s), as four bf16
-// pairs in channel order.  Nibbles i and i + 4 become the pair 128 + u after one shift
+// Eight codes of one word (low nibble first) times a scale pair (s, s; bf16 bits), as four
+// bf16 pairs in channel order.  Nibbles i and i + 4 become the pair 128 + u after one shift
 // and one logic operation; taking off 136 and the product with s are both exact.
-__device__ __forceinline__ uint4 dequantise_word(uint32_t w, __nv_bfloat162 s) {
-  const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
+__device__ __forceinline__ uint4 dequantise_word(uint32_t w, uint32_t s_bits) {
+  const uint32_t off_bits = 0x43084308u;  // 136
+  __nv_bfloat162 s, off;
+  memcpy(&s, &s_bits, 4);
+  memcpy(&off, &off_bits, 4);
   uint32_t v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -341,6 +344,16 @@ __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SR
   constexpr int G = F::kGroups;
   const int lane = threadIdx.x & 31;
   const int part = (threadIdx.x >> 5) & 3;  // the warp's 32 keys of every tile
+  // A lane takes a quarter t of the codes of key `row` of every 8: 8 channels of each
+  // group, one 16-byte chunk of the tile.  Lanes of odd rows take the groups of a
+  // 64-channel box in the other order, so that the 8 lanes that store together meet all
+  // eight chunk positions of the swizzle.
+  const int row = lane >> 2, t = lane & 3;
+  const bool odd = row & 1;
+  const int out_at = (part * 32 + row) * 128 + (((4 * (odd ? 1 : 0) + t) ^ row) << 4);
+  const int other = (out_at ^ 64) - out_at;  // to the group of the other parity
+  const uint32_t sel_s = odd ? 0x3232 : 0x1010;
+  const uint32_t sel_k = odd ? 0x7654 : 0x3210, sel_v = odd ? 0x7632 : 0x5410;
   const unsigned long long lim = p.wait_limit_ns;
   int rc = 0;
   for (int r = 0; r * static_cast<int>(gridDim.x) < p.num_units; ++r) {
@@ -355,48 +368,40 @@ __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SR
         if (!mbar_wait_warp(bar.slot_empty(s), ((rc / C::NSLOT) & 1) ^ 1, abort, p.flags, lim))
           return;
         const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW_BYTES;
-        uint8_t* tile = smem + C::OFF_RING + s * C::TILE_BYTES;
+        uint8_t* tile = smem + C::OFF_RING + s * C::TILE_BYTES + out_at;
         const int valid = U.L - j * BN;  // keys past the cache's end become zeros
-        // a lane takes a quarter of a key's codes: 8 channels of every group
-#pragma unroll 2
+        // A V row holds 4 channels of every group in turn: a word is put together from the
+        // two runs of 4 of its group
+        const uint32_t sel = kv == 0 ? sel_k : sel_v;
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-          const int key = part * 32 + i * 8 + (lane >> 2), t = lane & 3;
-          const uint8_t* blk = raw + (key / kBS) * C::RAW_BLOCK;
-          const uint8_t* cp = blk + (key % kBS) * F::kCodeRow + t * (4 * G);
-          const uint8_t* sp = blk + kBS * F::kCodeRow + (key % kBS) * F::kScaleRow;
+          const int key = part * 32 + 8 * i + row;
+          const uint8_t* cp = raw + (key / kBS) * C::RAW_BLOCK + (key % kBS) * F::kCodeRow + t * (4 * G);
+          const uint8_t* sp =
+              raw + (key / kBS) * C::RAW_BLOCK + kBS * F::kCodeRow + (key % kBS) * F::kScaleRow;
           uint32_t w[G], sc[G / 2];
           if constexpr (G == 4) {
             const uint4 x = *reinterpret_cast<const uint4*>(cp);
             const uint2 y = *reinterpret_cast<const uint2*>(sp);
-            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+            w[0] = x.x, w[1] = kv == 0 ? x.y : x.z, w[2] = kv == 0 ? x.z : x.y, w[3] = x.w;
             sc[0] = y.x, sc[1] = y.y;
           } else {
             const uint2 x = *reinterpret_cast<const uint2*>(cp);
             w[0] = x.x, w[1] = x.y;
             sc[0] = *reinterpret_cast<const uint32_t*>(sp);
           }
-          if (kv == 1) {
-            // a V row holds 4 channels of every group in turn: bring the two runs of 4
-            // of a group together
-            uint32_t y[G];
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-              y[g] = __byte_perm(w[g / 2], w[G / 2 + g / 2], (g & 1) ? 0x7632 : 0x5410);
-#pragma unroll
-            for (int g = 0; g < G; ++g) w[g] = y[g];
-          }
           if (key >= valid) {
 #pragma unroll
             for (int g = 0; g < G / 2; ++g) sc[g] = 0;
           }
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            const uint32_t ss = __byte_perm(sc[g / 2], 0, (g & 1) ? 0x3232 : 0x1010);
-            __nv_bfloat162 s2;
-            memcpy(&s2, &ss, 4);
-            const int chunk = 4 * (g & 1) + t;  // 16-byte chunk of the 64-channel box g / 2
-            *reinterpret_cast<uint4*>(tile + (g / 2) * C::BOX_BYTES + key * 128 +
-                                      ((chunk ^ (key & 7)) << 4)) = dequantise_word(w[g], s2);
+          for (int g = 0; g < G / 2; ++g) {
+            uint8_t* out = tile + g * C::BOX_BYTES + i * 1024;
+            *reinterpret_cast<uint4*>(out) = dequantise_word(
+                __byte_perm(w[2 * g], w[2 * g + 1], sel), __byte_perm(sc[g], 0, sel_s));
+            *reinterpret_cast<uint4*>(out + other) =
+                dequantise_word(__byte_perm(w[2 * g], w[2 * g + 1], sel ^ (kv == 0 ? 0x4444u : 0x2222u)),
+                                __byte_perm(sc[g], 0, sel_s ^ 0x2222u));
           }
         }
         fence_proxy_async_smem();
