@@ -20,8 +20,12 @@
 //                 16 rows (of the 4-bit cache: its block's codes and scales, into
 //                 a ring of raw half chunks)
 //   warps 12-15   4-bit cache: turn a raw K or V tile into the bf16 slot the MMA
-//                 warp reads, 32 keys each.  Every value n s is a bf16 exactly, so these are the
-//                 operands themselves, not an approximation of them
+//                 warp reads, 32 keys each.  Every value n s is a bf16 exactly, so
+//                 these are the operands themselves, not an approximation of them.
+//                 On the 16 x 512 workload the 4-bit source takes 668 us where the
+//                 bf16 pools take 571; with the four warps passing the slots on
+//                 without work it is 610, so 39 us are the second hand-over and the
+//                 ring's missing slot, 58 the issue slots that the softmax warps lose
 //   warp 1        MMA warp (the converged warp runs the issue code; elect.sync
 //                 picks the lane that issues): S_i = Q_i K_j^T into TMEM (fp32),
 //                 then O_i += P_i V_j with P_i read from TMEM (tcgen05 A operand
@@ -77,8 +81,10 @@ constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by
 // 128-key score row each, get more: 104 + 200 + 200 = 3 x 168.
 constexpr int kRegsLaunch = 168, kRegsWg0 = 104, kRegsSoftmax = 200;
 static_assert(kRegsWg0 + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split exceeds the launch");
-// With the dequantisers the block launches with 128: 64 + 64 + 192 + 192 = 4 x 128.
-constexpr int kRegsLaunch4 = 128, kRegsWg0With4 = 64, kRegsDequant = 64, kRegsSoftmax4 = 192;
+// With the dequantisers the block launches with 128: 88 + 40 + 192 + 192 = 4 x 128, the one
+// split of those tried that spills nothing (64 + 64: 698 us on the 16 x 512 workload, 80 +
+// 48: 691, this one: 668).
+constexpr int kRegsLaunch4 = 128, kRegsWg0With4 = 88, kRegsDequant = 40, kRegsSoftmax4 = 192;
 static_assert(kRegsWg0With4 + kRegsDequant + 2 * kRegsSoftmax4 <= 4 * kRegsLaunch4,
               "register split exceeds the launch");
 
@@ -315,25 +321,33 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
 // 4-bit cache: warps 12-15 turn raw K and V tiles into bf16 slots, 32 keys each
 // ---------------------------------------------------------------------------
 
-// Eight codes of one word (low nibble first) times a scale pair (s, s; bf16 bits), as four
-// bf16 pairs in channel order.  Nibbles i and i + 4 become the pair 128 + u after one shift
-// and one logic operation; taking off 136 and the product with s are both exact.
+// Eight codes u of one word (low nibble first) times a scale pair (s, s; bf16 bits): the
+// bf16 values (u - 8) s / 64 in channel order.  A code alone in 16 bits is the subnormal
+// bf16 u 2^-133; one fused multiply-add makes it (u - 8) / 64 and one product scales it,
+// both exact.  The factor 64 goes into the softmax scale for keys and into 1 / l for
+// values, where it is exact too.  (The other way, 128 + u by an OR into the mantissa, then
+// - 136, times s, delivers channels i and i + 4 in one register and takes four more
+// permutes a word on the pipe that the softmax warps need: 784 us against 698 on the
+// 16 x 512 workload.)
 __device__ __forceinline__ uint4 dequantise_word(uint32_t w, uint32_t s_bits) {
-  const uint32_t off_bits = 0x43084308u;  // 136
-  __nv_bfloat162 s, off;
+  const uint32_t big_bits = 0x7f007f00u, off_bits = 0xbe00be00u;  // 2^127, -2^-3
+  __nv_bfloat162 s, big, off;
   memcpy(&s, &s_bits, 4);
+  memcpy(&big, &big_bits, 4);
   memcpy(&off, &off_bits, 4);
+  const uint32_t lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
   uint32_t v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t u = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    // bytes: low code, its sign (0), high code, its sign
+    uint32_t u;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(u) : "r"(lo), "r"(hi), "r"(0xc480 + 0x1111 * i));
     __nv_bfloat162 x;
     memcpy(&x, &u, 4);
-    x = __hmul2(__hsub2(x, off), s);
+    x = __hmul2(__hfma2(x, big, off), s);
     memcpy(&v[i], &x, 4);
   }
-  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
-                    __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 template <int D, Src SRC>
@@ -345,15 +359,12 @@ __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SR
   const int lane = threadIdx.x & 31;
   const int part = (threadIdx.x >> 5) & 3;  // the warp's 32 keys of every tile
   // A lane takes a quarter t of the codes of key `row` of every 8: 8 channels of each
-  // group, one 16-byte chunk of the tile.  Lanes of odd rows take the groups of a
-  // 64-channel box in the other order, so that the 8 lanes that store together meet all
-  // eight chunk positions of the swizzle.
-  const int row = lane >> 2, t = lane & 3;
-  const bool odd = row & 1;
-  const int out_at = (part * 32 + row) * 128 + (((4 * (odd ? 1 : 0) + t) ^ row) << 4);
-  const int other = (out_at ^ 64) - out_at;  // to the group of the other parity
-  const uint32_t sel_s = odd ? 0x3232 : 0x1010;
-  const uint32_t sel_k = odd ? 0x7654 : 0x3210, sel_v = odd ? 0x7632 : 0x5410;
+  // group, one 16-byte chunk of the tile.  Rows r and r + 4 are neighbours among the
+  // lanes, so that the 8 lanes that store together meet all eight chunk positions of the
+  // swizzle.
+  const int row = ((lane >> 2) & 1) * 4 + (lane >> 3), t = lane & 3;
+  const int out0 = (part * 32 + row) * 128 + ((t ^ row) << 4);  // even groups
+  const int out1 = out0 ^ 64;                                   // odd groups
   const unsigned long long lim = p.wait_limit_ns;
   int rc = 0;
   for (int r = 0; r * static_cast<int>(gridDim.x) < p.num_units; ++r) {
@@ -361,29 +372,28 @@ __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SR
     if (u >= p.num_units) continue;
     const Unit U = unit_at(u, p, true);
     for (int j = 0; j < U.nkv; ++j) {
-#pragma unroll 1
+#pragma unroll
       for (int kv = 0; kv < 2; ++kv, ++rc) {
         const int rs = rc % C::NRAW, s = rc % C::NSLOT;
         if (!mbar_wait_warp(bar.raw_full(rs), (rc / C::NRAW) & 1, abort, p.flags, lim)) return;
         if (!mbar_wait_warp(bar.slot_empty(s), ((rc / C::NSLOT) & 1) ^ 1, abort, p.flags, lim))
           return;
         const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW_BYTES;
-        uint8_t* tile = smem + C::OFF_RING + s * C::TILE_BYTES + out_at;
+        uint8_t* tile = smem + C::OFF_RING + s * C::TILE_BYTES;
         const int valid = U.L - j * BN;  // keys past the cache's end become zeros
-        // A V row holds 4 channels of every group in turn: a word is put together from the
-        // two runs of 4 of its group
-        const uint32_t sel = kv == 0 ? sel_k : sel_v;
+        // (unrolled by four, the two loops overflow the instruction cache beside the
+        // softmax code: 1042 us against 784)
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
           const int key = part * 32 + 8 * i + row;
-          const uint8_t* cp = raw + (key / kBS) * C::RAW_BLOCK + (key % kBS) * F::kCodeRow + t * (4 * G);
-          const uint8_t* sp =
-              raw + (key / kBS) * C::RAW_BLOCK + kBS * F::kCodeRow + (key % kBS) * F::kScaleRow;
+          const uint8_t* blk = raw + (key / kBS) * C::RAW_BLOCK;
+          const uint8_t* cp = blk + (key % kBS) * F::kCodeRow + t * (4 * G);
+          const uint8_t* sp = blk + kBS * F::kCodeRow + (key % kBS) * F::kScaleRow;
           uint32_t w[G], sc[G / 2];
           if constexpr (G == 4) {
             const uint4 x = *reinterpret_cast<const uint4*>(cp);
             const uint2 y = *reinterpret_cast<const uint2*>(sp);
-            w[0] = x.x, w[1] = kv == 0 ? x.y : x.z, w[2] = kv == 0 ? x.z : x.y, w[3] = x.w;
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
             sc[0] = y.x, sc[1] = y.y;
           } else {
             const uint2 x = *reinterpret_cast<const uint2*>(cp);
@@ -395,13 +405,14 @@ __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SR
             for (int g = 0; g < G / 2; ++g) sc[g] = 0;
           }
 #pragma unroll
-          for (int g = 0; g < G / 2; ++g) {
-            uint8_t* out = tile + g * C::BOX_BYTES + i * 1024;
-            *reinterpret_cast<uint4*>(out) = dequantise_word(
-                __byte_perm(w[2 * g], w[2 * g + 1], sel), __byte_perm(sc[g], 0, sel_s));
-            *reinterpret_cast<uint4*>(out + other) =
-                dequantise_word(__byte_perm(w[2 * g], w[2 * g + 1], sel ^ (kv == 0 ? 0x4444u : 0x2222u)),
-                                __byte_perm(sc[g], 0, sel_s ^ 0x2222u));
+          for (int g = 0; g < G; ++g) {
+            // a V row holds 4 channels of every group in turn: a word is put together
+            // from the two runs of 4 of its group
+            const uint32_t word =
+                kv == 0 ? w[g] : __byte_perm(w[g / 2], w[G / 2 + g / 2], (g & 1) ? 0x7632 : 0x5410);
+            uint8_t* out = tile + ((g & 1) ? out1 : out0) + (g / 2) * C::BOX_BYTES + i * 1024;
+            *reinterpret_cast<uint4*>(out) =
+                dequantise_word(word, __byte_perm(sc[g / 2], 0, (g & 1) ? 0x3232 : 0x1010));
           }
         }
         fence_proxy_async_smem();
@@ -580,7 +591,9 @@ __device__ void softmax_wg(const FwdParams& p, uint32_t tmem, const Bars<D, SRC>
   const int sp = warp & 3;  // TMEM sub-partition this warp may access
   const int r = sp * 32 + lane;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
-  const float sl2 = p.scale_log2;
+  // (the 4-bit cache's keys come divided by 64)
+  const float sl2 = p.scale_log2 * (SRC == Src::kPaged4 ? 64.f : 1.f);
+  const float scale = p.scale * (SRC == Src::kPaged4 ? 64.f : 1.f);
   const unsigned long long lim = p.wait_limit_ns;
   int sc = 0;  // S tiles consumed (= P tiles produced), all units
 
@@ -671,7 +684,8 @@ __device__ void softmax_wg(const FwdParams& p, uint32_t tmem, const Bars<D, SRC>
     const float nan = __int_as_float(0x7fc00000);
     // no visible key (or none processed); a NaN from the 4-bit cache is a result
     const bool empty = SRC == Src::kPaged4 ? l == 0.f : !(l > 0.f);
-    const float inv_l = empty ? 0.f : 1.f / l;
+    // (the 4-bit cache's values come divided by 64)
+    const float inv_l = empty ? 0.f : (SRC == Src::kPaged4 ? 64.f : 1.f) / l;
     if (n > 0) {
       if (!mbar_wait_warp(bar.s_free(I), (sc - 1) & 1, abort, p.flags, lim)) return;
       tc_fence_after();
@@ -705,7 +719,7 @@ __device__ void softmax_wg(const FwdParams& p, uint32_t tmem, const Bars<D, SRC>
     }
     if (p.lse != nullptr && row_valid)
       p.lse[static_cast<size_t>(U.bh) * p.Tq + qpos] =
-          U.bad ? nan : (empty ? -INFINITY : m * p.scale + logf(l));
+          U.bad ? nan : (empty ? -INFINITY : m * scale + logf(l));
   }
 }
 
