@@ -2,24 +2,33 @@
 //
 // For a query q and a token whose K group w has codes u_c = n_c + 8 and scale s_w, and
 // whose V group has codes and scale t_w:
-//   score  = scale * sum_w s_w (sum_{c in w} q_c u_c - 8 sum_{c in w} q_c)
+//   score  = scale * sum_w s_w sum_{c in w} q_c (u_c - 8)
 //   O_c    = sum_tokens (p t_w) (u_c - 8) / sum_tokens p,    p = exp(score - max)
-// so the codes go through the matrix units as the exact bf16 numbers 128 + u (their bits
-// OR 0x4300), the scales multiply the few score and probability values instead of the
-// many cache values, and the offset 136 leaves as a constant: the score products start
-// from -136 sum q, the output products are preceded by -136 sum p t.  The offset is
-// taken out once per step of kStepBlocks blocks, before that step's products are added,
-// so no accumulator drifts to 136 times its result.  Scores, softmax statistics and
-// outputs are fp32; p t is rounded to bf16 for its product (half a step of 2^-8, as the
-// probabilities of the bf16 kernels are).
+// so the codes go through the matrix units by themselves and the scales multiply the few
+// score and probability values instead of the many cache values.
+//
+// A nibble becomes a matrix operand without any conversion of its bits, because the
+// smallest floating-point numbers are equally spaced: a nibble alone in 16 bits, in
+// either half of the low byte, is the fp16 number u 2^-24 or 16 u 2^-24 and the bf16 number
+// u 2^-133 or 16 u 2^-133.  Two masks give four codes of a word, a shift by 8 the rest.
+//   K: fp16 products take subnormal operands as they are.  The query's row is brought to
+//      fp16 by a power of two that puts its largest element in [2^14, 2^15): bf16 has 8
+//      bits, so nothing within 2^-29 of that element is rounded.  Channels whose code sits
+//      in the upper half of a byte take q / 16.  The products start from -8 sum q, which
+//      the same unit computes once a piece.  The power of two goes into the softmax scale.
+//   V: p t needs the range of bf16, whose products do not take 2^-133; one fused
+//      multiply-add on the pair makes it n / 64, exactly.
+// Scores, softmax statistics and outputs are fp32; p t is rounded to bf16 for its product
+// (2^-8 of itself at most, as the probabilities of the bf16 kernels are).  The running
+// maximum only moves when it grows by more than 2^8, so outputs are rarely rescaled; p
+// stays below 2^8.
 //
 // Bound by HBM: a token and KV head take 9 D / 8 bytes, read once.  Every warp streams a
 // range of the batch's blocks by itself (decode_split.cuh): lane j of the warp copies
 // block j of a step, one untiled bulk copy of the whole chunk (codes and scales of K and
 // V), into the warp's own ring in shared memory; the table entries of a step are read one
 // step ahead of its copies.  The fragments of m16n8k16 come out of shared memory by plain
-// loads in the order the format lays down, two codes a register after one shift and one
-// three-input logic operation.  The pieces are joined by the merge kernel of
+// loads in the order the format lays down.  The pieces are joined by the merge kernel of
 // paged_decode.cu.
 #include <cuda_runtime.h>
 
@@ -38,7 +47,7 @@ constexpr int kMinBlocks = kDecodeMinRange / kBS;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStepBlocks = 4;  // blocks of one step: 64 tokens share a softmax update
-constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16 pair
+constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by > 2^8
 
 // Ring depth and CTAs per SM by query tiles (NQT = 1: groups of up to 8 query heads,
 // 2: up to 16, which needs the registers of two CTAs).
@@ -52,11 +61,11 @@ struct Shape {
   static constexpr int kSmem = kOffAbort + kWarps * 4 + 128;  // slack for 128-byte alignment
 };
 
-// D = A * B + C with C left as it is.
-__device__ __forceinline__ void mma_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1, float c0, float c1, float c2, float c3) {
+// D = A * B + C (C may be D), m16n8k16, fp16 inputs, fp32 accumulators.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1, float c0, float c1, float c2, float c3) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
@@ -70,9 +79,22 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// Nibbles i and i + 4 of w as the bf16 pair (128 + low, 128 + high).
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
-  return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+constexpr uint32_t kLowNibbles = 0x000f000fu, kHighNibbles = 0x00f000f0u;
+
+// The masked codes of a pair, u 2^-133 or 16 u 2^-133, as bf16 (u - 8) / 64.
+__device__ __forceinline__ uint32_t centre(uint32_t codes, uint32_t factor) {
+  const uint32_t off = 0xbe00be00u;  // -2^-3
+  uint32_t y;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(codes), "r"(factor), "r"(off));
+  return y;
+}
+constexpr uint32_t kLowFactor = 0x7f007f00u, kHighFactor = 0x7d007d00u;  // 2^127, 2^123
+
+// Two fp32 as an fp16 pair: lo -> bits 0-15.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // Token of a 16-token block that row `row` of a score tile holds.  Neighbouring rows are
@@ -228,12 +250,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   // ---------------- the range, step by step ----------------
   const int g = lane >> 2, t4 = lane & 3;
   const int group = p.group;
-  const float sl2 = p.scale_log2;
-  const uint32_t minus136[4] = {kMinus136, kMinus136, kMinus136, kMinus136};
-  uint32_t qb[D / 16][NQT][2];   // Q^T fragments in the order of the K codes
-  float q136[G][NQT][2];         // -136 sum of q over group w, queries 2 t4 (+ 1)
+  const int row0 = token_of_row(g);  // rows g and g + 8 of a score tile: tokens row0 (+ 8)
+  uint32_t qb[D / 16][NQT][2];       // Q^T fragments (fp16) in the order of the K codes
+  float q8[G][NQT][2];               // -8 sum of q over group w, queries 2 t4 (+ 1)
+  float sl2[NQT][2], sl[NQT][2];     // softmax scale (times log2 e) over the query's 2^x
   float m_q[NQT][2], l_q[NQT][2];
-  float acc[D / 16][NQT][4];     // O^T: channels 32 w + 4 g + 2 x (+ 1) of tile 2 w + x
+  float acc[D / 16][NQT][4];         // O^T / 64: channels 32 w + 4 g + 2 x (+ 1) of tile 2 w + x
   Cursor c = at;
   int c_left = n_w, taken = 0, L = 0, piece_b0 = 0;
   bool pbad = false, ok = true;
@@ -244,26 +266,50 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     pbad = false;
     const uint16_t* q =
         static_cast<const uint16_t*>(p.q) + (static_cast<size_t>(c.r) * p.Hq + c.h * group) * D;
+    // A fragment of -8 in both forms of a code
+    const uint32_t minus8[4] = {0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u};
 #pragma unroll
     for (int nt = 0; nt < NQT; ++nt) {
       const int row = 8 * nt + g;
+      uint4 x[G];
+      uint32_t big = 0;  // largest magnitude of the row, as bf16 bits in either half
 #pragma unroll
       for (int w = 0; w < G; ++w) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (row < group) x = *reinterpret_cast<const uint4*>(q + row * D + 32 * w + 8 * t4);
-        // code_pair(., i) holds channels i and i + 4 of the lane's eight
-        qb[2 * w][nt][0] = __byte_perm(x.x, x.z, 0x5410);
-        qb[2 * w][nt][1] = __byte_perm(x.x, x.z, 0x7632);
-        qb[2 * w + 1][nt][0] = __byte_perm(x.y, x.w, 0x5410);
-        qb[2 * w + 1][nt][1] = __byte_perm(x.y, x.w, 0x7632);
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_bf16_16816(d, minus136, qb[2 * w][nt][0], qb[2 * w][nt][1]);
-        mma_bf16_16816(d, minus136, qb[2 * w + 1][nt][0], qb[2 * w + 1][nt][1]);
-        q136[w][nt][0] = d[0];
-        q136[w][nt][1] = d[1];
+        x[w] = make_uint4(0, 0, 0, 0);
+        if (row < group) x[w] = *reinterpret_cast<const uint4*>(q + row * D + 32 * w + 8 * t4);
+        big = __vmaxu2(big, __vmaxu2(__vmaxu2(x[w].x & 0x7fff7fffu, x[w].y & 0x7fff7fffu),
+                                     __vmaxu2(x[w].z & 0x7fff7fffu, x[w].w & 0x7fff7fffu)));
       }
-      m_q[nt][0] = m_q[nt][1] = -INFINITY;
-      l_q[nt][0] = l_q[nt][1] = 0.f;
+      big = max(big & 0xffffu, big >> 16);
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // q = q' 2^(e - 14): e the exponent of the largest element (kept where all powers of
+      // two below are normal numbers)
+      const int e = min(max(static_cast<int>(big >> 7) - 127, -100), 100);
+      const float f0 = __int_as_float((127 + 14 - e) << 23), f1 = f0 * 0.0625f;
+#pragma unroll
+      for (int w = 0; w < G; ++w) {
+        // masks of a word give channels 0, 4 (low) and 1, 5 (high); shifted by 8: 2, 6 and 3, 7
+        qb[2 * w][nt][0] = pack_f16x2(bf16_lo(x[w].x) * f0, bf16_lo(x[w].z) * f0);
+        qb[2 * w][nt][1] = pack_f16x2(bf16_hi(x[w].x) * f1, bf16_hi(x[w].z) * f1);
+        qb[2 * w + 1][nt][0] = pack_f16x2(bf16_lo(x[w].y) * f0, bf16_lo(x[w].w) * f0);
+        qb[2 * w + 1][nt][1] = pack_f16x2(bf16_hi(x[w].y) * f1, bf16_hi(x[w].w) * f1);
+        float d[4];
+        mma_f16(d, minus8, qb[2 * w][nt][0], qb[2 * w][nt][1], 0.f, 0.f, 0.f, 0.f);
+        mma_f16(d, minus8, qb[2 * w + 1][nt][0], qb[2 * w + 1][nt][1], d[0], d[1], d[2], d[3]);
+        q8[w][nt][0] = d[0];
+        q8[w][nt][1] = d[1];
+      }
+#pragma unroll
+      for (int x2 = 0; x2 < 2; ++x2) {
+        // lane 4 k holds the exponent of query k: this lane's columns are 2 t4 and 2 t4 + 1
+        const int eq = __shfl_sync(0xffffffffu, e, 4 * (2 * t4 + x2));
+        const float f = __int_as_float((127 + 24 - 14 + eq) << 23);
+        sl[nt][x2] = p.scale * f;
+        sl2[nt][x2] = p.scale_log2 * f;
+        m_q[nt][x2] = -INFINITY;
+        l_q[nt][x2] = 0.f;
+      }
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
         acc[j][nt][0] = acc[j][nt][1] = acc[j][nt][2] = acc[j][nt][3] = 0.f;
@@ -280,58 +326,64 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     }
     pbad |= (stage_bad >> s) & 1u;
     const uint8_t* stage = ring + s * C::kStageBytes;
-    const int n_tok = min(kBS * st.n, L - st.b * kBS);  // valid tokens of the step
-    const int row0 = token_of_row(g);                   // rows g and g + 8 of a score tile
+    // Valid tokens of the step.  The blocks past them are computed with whatever the stage
+    // holds (codes are finite whatever their bits) and masked with the tail.
+    const int n_tok = min(kBS * st.n, L - st.b * kBS);
 
     // ---- S^T = K Q^T, group by group ----
     float sc[kStepBlocks][NQT][4];
 #pragma unroll
     for (int j = 0; j < kStepBlocks; ++j) {
-      if (j < st.n) {
-        const uint8_t* blk = stage + j * F::kChunk;
-        uint32_t k0[G], k1[G], s0[G / 2], s1[G / 2];
-        lds(blk + F::kOffKCodes + row0 * F::kCodeRow + t4 * (4 * G), k0);
-        lds(blk + F::kOffKCodes + (row0 + 8) * F::kCodeRow + t4 * (4 * G), k1);
-        lds(blk + F::kOffKScales + row0 * F::kScaleRow, s0);
-        lds(blk + F::kOffKScales + (row0 + 8) * F::kScaleRow, s1);
+      const uint8_t* blk = stage + j * F::kChunk;
+      uint32_t k0[G], k1[G], s0[G / 2], s1[G / 2];
+      lds(blk + F::kOffKCodes + row0 * F::kCodeRow + t4 * (4 * G), k0);
+      lds(blk + F::kOffKCodes + (row0 + 8) * F::kCodeRow + t4 * (4 * G), k1);
+      lds(blk + F::kOffKScales + row0 * F::kScaleRow, s0);
+      lds(blk + F::kOffKScales + (row0 + 8) * F::kScaleRow, s1);
 #pragma unroll
-        for (int w = 0; w < G; ++w) {
-          const uint32_t a0[4] = {code_pair(k0[w], 0), code_pair(k1[w], 0), code_pair(k0[w], 1),
-                                  code_pair(k1[w], 1)};
-          const uint32_t a1[4] = {code_pair(k0[w], 2), code_pair(k1[w], 2), code_pair(k0[w], 3),
-                                  code_pair(k1[w], 3)};
-          const float f0 = scale_of(s0, w), f1 = scale_of(s1, w);
+      for (int w = 0; w < G; ++w) {
+        const uint32_t h0 = k0[w] >> 8, h1 = k1[w] >> 8;
+        const uint32_t a0[4] = {k0[w] & kLowNibbles, k1[w] & kLowNibbles, k0[w] & kHighNibbles,
+                                k1[w] & kHighNibbles};
+        const uint32_t a1[4] = {h0 & kLowNibbles, h1 & kLowNibbles, h0 & kHighNibbles,
+                                h1 & kHighNibbles};
+        const float f0 = scale_of(s0, w), f1 = scale_of(s1, w);
 #pragma unroll
-          for (int nt = 0; nt < NQT; ++nt) {
-            float d[4];
-            const float c0 = q136[w][nt][0], c1 = q136[w][nt][1];
-            mma_from(d, a0, qb[2 * w][nt][0], qb[2 * w][nt][1], c0, c1, c0, c1);
-            mma_bf16_16816(d, a1, qb[2 * w + 1][nt][0], qb[2 * w + 1][nt][1]);
-            if (w == 0) {
-              sc[j][nt][0] = f0 * d[0];
-              sc[j][nt][1] = f0 * d[1];
-              sc[j][nt][2] = f1 * d[2];
-              sc[j][nt][3] = f1 * d[3];
-            } else {
-              sc[j][nt][0] = fmaf(f0, d[0], sc[j][nt][0]);
-              sc[j][nt][1] = fmaf(f0, d[1], sc[j][nt][1]);
-              sc[j][nt][2] = fmaf(f1, d[2], sc[j][nt][2]);
-              sc[j][nt][3] = fmaf(f1, d[3], sc[j][nt][3]);
-            }
+        for (int nt = 0; nt < NQT; ++nt) {
+          float d[4];
+          const float c0 = q8[w][nt][0], c1 = q8[w][nt][1];
+          mma_f16(d, a0, qb[2 * w][nt][0], qb[2 * w][nt][1], c0, c1, c0, c1);
+          mma_f16(d, a1, qb[2 * w + 1][nt][0], qb[2 * w + 1][nt][1], d[0], d[1], d[2], d[3]);
+          if (w == 0) {
+            sc[j][nt][0] = f0 * d[0];
+            sc[j][nt][1] = f0 * d[1];
+            sc[j][nt][2] = f1 * d[2];
+            sc[j][nt][3] = f1 * d[3];
+          } else {
+            sc[j][nt][0] = fmaf(f0, d[0], sc[j][nt][0]);
+            sc[j][nt][1] = fmaf(f0, d[1], sc[j][nt][1]);
+            sc[j][nt][2] = fmaf(f1, d[2], sc[j][nt][2]);
+            sc[j][nt][3] = fmaf(f1, d[3], sc[j][nt][3]);
           }
         }
       }
-      // tokens past the end: their codes and scales may be anything
-      const bool in0 = kBS * j + row0 < n_tok, in1 = kBS * j + row0 + 8 < n_tok;
+    }
+    const bool tail = n_tok < kBS * kStepBlocks;
+    if (tail) {  // tokens past the end: their codes and scales may be anything
 #pragma unroll
-      for (int nt = 0; nt < NQT; ++nt) {
-        if (!in0) sc[j][nt][0] = sc[j][nt][1] = -INFINITY;
-        if (!in1) sc[j][nt][2] = sc[j][nt][3] = -INFINITY;
+      for (int j = 0; j < kStepBlocks; ++j) {
+        const bool in0 = kBS * j + row0 < n_tok, in1 = kBS * j + row0 + 8 < n_tok;
+#pragma unroll
+        for (int nt = 0; nt < NQT; ++nt) {
+          if (!in0) sc[j][nt][0] = sc[j][nt][1] = -INFINITY;
+          if (!in1) sc[j][nt][2] = sc[j][nt][3] = -INFINITY;
+        }
       }
     }
 
     // ---- softmax update (one per step) ----
     float al[NQT][2];
+    bool grown = false;
 #pragma unroll
     for (int nt = 0; nt < NQT; ++nt) {
 #pragma unroll
@@ -343,89 +395,75 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
-        const float mn = fmaxf(m_q[nt][e], bm);  // finite: every step has a valid token
-        const float ms = mn * sl2;
-        al[nt][e] = ex2(m_q[nt][e] * sl2 - ms);
-        m_q[nt][e] = mn;
+        // finite from the first step on: every step has a valid token
+        const bool grow = (bm - m_q[nt][e]) * sl2[nt][e] > kRescaleLog2;
+        al[nt][e] = grow ? ex2((m_q[nt][e] - bm) * sl2[nt][e]) : 1.f;
+        m_q[nt][e] = grow ? bm : m_q[nt][e];
+        grown |= grow;
+        const float ms = m_q[nt][e] * sl2[nt][e];
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < kStepBlocks; ++j) {
 #pragma unroll
           for (int x = e; x < 4; x += 2) {
-            sc[j][nt][x] = ex2(fmaf(sc[j][nt][x], sl2, -ms));
+            sc[j][nt][x] = ex2(fmaf(sc[j][nt][x], sl2[nt][e], -ms));
             sum += sc[j][nt][x];
           }
         }
         l_q[nt][e] = l_q[nt][e] * al[nt][e] + sum;
       }
     }
+    if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int nt = 0; nt < NQT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[j][nt][x] *= al[nt][x & 1];
+    }
 
-    // ---- O^T = al O^T + V^T (P t)^T, two groups (one word of V codes) at a time ----
+    // ---- O^T += V^T (P t)^T, two groups (one word of V codes) at a time ----
 #pragma unroll
-    for (int u = 0; u < G / 2; ++u) {
-      uint32_t pb[kStepBlocks][2][NQT][2];  // (p t)^T fragments of groups 2 u, 2 u + 1
+    for (int j = 0; j < kStepBlocks; ++j) {
+      const uint8_t* blk = stage + j * F::kChunk;
+      const int ta = token_of_row(2 * t4), tb = token_of_row(2 * t4 + 1);
 #pragma unroll
-      for (int j = 0; j < kStepBlocks; ++j) {
-        if (j < st.n) {
-          const uint8_t* sv = stage + j * F::kChunk + F::kOffVScales + 4 * u;
-          uint32_t t0 = *reinterpret_cast<const uint32_t*>(sv + row0 * F::kScaleRow);
-          uint32_t t1 = *reinterpret_cast<const uint32_t*>(sv + (row0 + 8) * F::kScaleRow);
-          if (kBS * j + row0 >= n_tok) t0 = 0;  // p is 0 there, but 0 * NaN is not
+      for (int u = 0; u < G / 2; ++u) {
+        // (p t)^T fragments of groups 2 u and 2 u + 1
+        const uint8_t* sv = blk + F::kOffVScales + 4 * u;
+        uint32_t t0 = *reinterpret_cast<const uint32_t*>(sv + row0 * F::kScaleRow);
+        uint32_t t1 = *reinterpret_cast<const uint32_t*>(sv + (row0 + 8) * F::kScaleRow);
+        if (tail) {  // p is 0 there, but 0 * NaN is not
+          if (kBS * j + row0 >= n_tok) t0 = 0;
           if (kBS * j + row0 + 8 >= n_tok) t1 = 0;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float f0 = x ? bf16_hi(t0) : bf16_lo(t0), f1 = x ? bf16_hi(t1) : bf16_lo(t1);
-#pragma unroll
-            for (int nt = 0; nt < NQT; ++nt) {
-              pb[j][x][nt][0] =
-                  transpose8x8(pack_bf16x2(sc[j][nt][0] * f0, sc[j][nt][1] * f0));
-              pb[j][x][nt][1] =
-                  transpose8x8(pack_bf16x2(sc[j][nt][2] * f1, sc[j][nt][3] * f1));
-            }
-          }
         }
-      }
-      // the offset of the codes leaves before the step's products come in
+        // V^T fragments: channels 4 g .. of each group, score rows 2 t4, 2 t4 + 1 (+ 8)
+        const uint8_t* v = blk + F::kOffVCodes + g * (2 * G) + 4 * u;
+        const uint32_t va = *reinterpret_cast<const uint32_t*>(v + ta * F::kCodeRow);
+        const uint32_t vb = *reinterpret_cast<const uint32_t*>(v + tb * F::kCodeRow);
+        const uint32_t vc = *reinterpret_cast<const uint32_t*>(v + (ta + 8) * F::kCodeRow);
+        const uint32_t vd = *reinterpret_cast<const uint32_t*>(v + (tb + 8) * F::kCodeRow);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < 2; ++x) {
+          const float f0 = x ? bf16_hi(t0) : bf16_lo(t0), f1 = x ? bf16_hi(t1) : bf16_lo(t1);
+          uint32_t pb[NQT][2];
 #pragma unroll
-        for (int nt = 0; nt < NQT; ++nt) {
-          float off[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < kStepBlocks; ++j)
-            if (j < st.n) mma_bf16_16816(off, minus136, pb[j][x][nt][0], pb[j][x][nt][1]);
+          for (int nt = 0; nt < NQT; ++nt) {
+            pb[nt][0] = transpose8x8(pack_bf16x2(sc[j][nt][0] * f0, sc[j][nt][1] * f0));
+            pb[nt][1] = transpose8x8(pack_bf16x2(sc[j][nt][2] * f1, sc[j][nt][3] * f1));
+          }
+          const uint32_t ab = __byte_perm(va, vb, x ? 0x7632 : 0x5410);
+          const uint32_t cd = __byte_perm(vc, vd, x ? 0x7632 : 0x5410);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            float(&o)[4] = acc[4 * u + 2 * x + y][nt];
-            o[0] = fmaf(o[0], al[nt][0], off[0]);
-            o[1] = fmaf(o[1], al[nt][1], off[1]);
-            o[2] = fmaf(o[2], al[nt][0], off[0]);
-            o[3] = fmaf(o[3], al[nt][1], off[1]);
-          }
-        }
-      }
+            const uint32_t ab8 = y ? ab >> 8 : ab, cd8 = y ? cd >> 8 : cd;
+            const uint32_t a[4] = {centre(ab8 & kLowNibbles, kLowFactor),
+                                   centre(ab8 & kHighNibbles, kHighFactor),
+                                   centre(cd8 & kLowNibbles, kLowFactor),
+                                   centre(cd8 & kHighNibbles, kHighFactor)};
 #pragma unroll
-      for (int j = 0; j < kStepBlocks; ++j) {
-        if (j < st.n) {
-          // V^T fragments: channels 4 g .. of each group, score rows 2 t4, 2 t4 + 1 (+ 8)
-          const uint8_t* v = stage + j * F::kChunk + F::kOffVCodes + g * (2 * G) + 4 * u;
-          const int ta = token_of_row(2 * t4), tb = token_of_row(2 * t4 + 1);
-          const uint32_t va = *reinterpret_cast<const uint32_t*>(v + ta * F::kCodeRow);
-          const uint32_t vb = *reinterpret_cast<const uint32_t*>(v + tb * F::kCodeRow);
-          const uint32_t vc = *reinterpret_cast<const uint32_t*>(v + (ta + 8) * F::kCodeRow);
-          const uint32_t vd = *reinterpret_cast<const uint32_t*>(v + (tb + 8) * F::kCodeRow);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t ab = __byte_perm(va, vb, x ? 0x7632 : 0x5410);
-            const uint32_t cd = __byte_perm(vc, vd, x ? 0x7632 : 0x5410);
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t a[4] = {code_pair(ab, 2 * y), code_pair(ab, 2 * y + 1),
-                                     code_pair(cd, 2 * y), code_pair(cd, 2 * y + 1)};
-#pragma unroll
-              for (int nt = 0; nt < NQT; ++nt)
-                mma_bf16_16816(acc[4 * u + 2 * x + y][nt], a, pb[j][x][nt][0], pb[j][x][nt][1]);
-            }
+            for (int nt = 0; nt < NQT; ++nt)
+              mma_bf16_16816(acc[2 * (2 * u + x) + y][nt], a, pb[nt][0], pb[nt][1]);
           }
         }
       }
@@ -453,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
             lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
             const int q = 8 * nt + 2 * t4 + e;
             if (q >= group) continue;
-            const float inv = pbad ? nan : 1.f / lsum;
+            const float inv = pbad ? nan : 64.f / lsum;
             const size_t base = (hq0 + q) * p.max_pieces + j;
             float* dst = p.part_o + base * D + 4 * g;
 #pragma unroll
@@ -461,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
               *reinterpret_cast<float4*>(dst + 32 * w) =
                   make_float4(acc[2 * w][nt][e] * inv, acc[2 * w][nt][2 + e] * inv,
                               acc[2 * w + 1][nt][e] * inv, acc[2 * w + 1][nt][2 + e] * inv);
-            if (g == 0) p.part_lse[base] = pbad ? nan : m_q[nt][e] * p.scale + logf(lsum);
+            if (g == 0) p.part_lse[base] = pbad ? nan : m_q[nt][e] * sl[nt][e] + logf(lsum);
           }
         }
         if (piece_b0 == 0 && lane == 0) p.seg_first[static_cast<size_t>(c.r) * p.Hkv + c.h] = c.first;
