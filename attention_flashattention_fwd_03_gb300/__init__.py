@@ -120,7 +120,7 @@ def _bind(h):
     h.paged_kv4_append.restype = I
     h.paged_kv4_gather.argtypes = [P, P, P, I, I, I, I, I, I, I, P, P, P]
     h.paged_kv4_gather.restype = I
-    h.paged_kv4_attn_decode_workspace_size.argtypes = [I, I, I, I]
+    h.paged_kv4_attn_decode_workspace_size.argtypes = [I, I, I, I, I]
     h.paged_kv4_attn_decode_workspace_size.restype = Z
     h.paged_kv4_attn_decode.argtypes = [P] * 4 + [I] * 8 + [F, P, P, P, Z, P]
     h.paged_kv4_attn_decode.restype = I
@@ -760,8 +760,9 @@ def _check_kv4_attention(q, kv_pool, block_table, lens, rows, out, lse):
     return device, NB
 
 
-def paged_kv4_attn_decode_workspace_size(num_seqs: int, Hq: int, D: int, max_seq_len: int) -> int:
-    return (_lib or lib()).paged_kv4_attn_decode_workspace_size(num_seqs, Hq, D, max_seq_len)
+def paged_kv4_attn_decode_workspace_size(num_seqs: int, Hq: int, Hkv: int, D: int,
+                                         max_seq_len: int) -> int:
+    return (_lib or lib()).paged_kv4_attn_decode_workspace_size(num_seqs, Hq, Hkv, D, max_seq_len)
 
 
 def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
@@ -781,7 +782,7 @@ def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
         scale = 1.0 / math.sqrt(D)
     with _On(device, stream) as handle:
         if workspace is None:
-            need = paged_kv4_attn_decode_workspace_size(S, Hq, D, max_seq_len)
+            need = paged_kv4_attn_decode_workspace_size(S, Hq, kv_pool.shape[1], D, max_seq_len)
             workspace = _torch.empty((max(need, 256),), dtype=_torch.uint8, device=device)
         if out is None:
             out = _torch.empty((S, Hq, D), dtype=_torch.bfloat16, device=device)

@@ -352,10 +352,10 @@ GBATTN_API int paged_kv4_gather(const void* kv_pool, const int32_t* block_table,
              : ATTN_ERR_CUDA;
 }
 
-GBATTN_API size_t paged_kv4_attn_decode_workspace_size(int num_seqs, int Hq, int D,
+GBATTN_API size_t paged_kv4_attn_decode_workspace_size(int num_seqs, int Hq, int Hkv, int D,
                                                        int max_seq_len) {
-  if (num_seqs < 0 || Hq <= 0 || D <= 0 || max_seq_len < 0) return 0;
-  return decode_workspace_bytes(num_seqs, Hq, D, max_seq_len);
+  if (num_seqs < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_seq_len < 0) return 0;
+  return kv4_decode_workspace(num_seqs, Hq, Hkv, D, max_seq_len).bytes;
 }
 
 GBATTN_API int paged_kv4_attn_decode(const void* q, const void* kv_pool,
@@ -374,8 +374,8 @@ GBATTN_API int paged_kv4_attn_decode(const void* q, const void* kv_pool,
   if (!aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(o, 16) || !aligned(block_table, 4) ||
       !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
     return ATTN_ERR_INVALID_ARG;
-  if (workspace_bytes < decode_workspace_bytes(num_seqs, Hq, D, max_seq_len))
-    return ATTN_ERR_INVALID_ARG;
+  const Kv4DecodeWorkspace wl = kv4_decode_workspace(num_seqs, Hq, Hkv, D, max_seq_len);
+  if (workspace_bytes < wl.bytes) return ATTN_ERR_INVALID_ARG;
   if (static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim ||
       static_cast<uint64_t>(num_seqs) * Hq >= kMaxDim ||
       static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim)
@@ -383,9 +383,15 @@ GBATTN_API int paged_kv4_attn_decode(const void* q, const void* kv_pool,
   DeviceState* ds = nullptr;
   const int st = device_state(&ds);
   if (st != ATTN_OK) return st;
-  const DecodeParams p =
-      decode_params(q, block_table, seq_lens, num_seqs, Hq, Hkv, D, max_blocks_per_seq,
-                    num_pool_blocks, max_seq_len, scale, o, lse, workspace, ds->flags);
+  DecodeParams p = decode_params(q, block_table, seq_lens, num_seqs, Hq, Hkv, D,
+                                 max_blocks_per_seq, num_pool_blocks, max_seq_len, scale, o, lse,
+                                 ds->flags);
+  char* ws = static_cast<char*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_lse = reinterpret_cast<float*>(ws + wl.off_part_lse);
+  p.seg_first = reinterpret_cast<long long*>(ws + wl.off_seg_first);
+  p.plan = reinterpret_cast<long long*>(ws + wl.off_plan);
+  p.max_pieces = static_cast<int>(wl.pieces);
   return launch_kv4_decode(static_cast<const uint8_t*>(kv_pool), p, ds->num_sms,
                            static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ATTN_OK

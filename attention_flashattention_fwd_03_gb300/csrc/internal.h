@@ -56,6 +56,7 @@ struct DecodeParams {
   int num_pool_blocks;
   int max_seq_len;
   int max_pieces;              // bound on the pieces of one (request, KV head) segment
+                               // (4-bit cache: of the batch)
   float scale;
   float scale_log2;
   unsigned* flags;             // device flag word (DEVFLAG_*)
@@ -80,11 +81,16 @@ cudaError_t launch_paged_decode(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                 const DecodeParams& p, int num_sms, cudaStream_t stream);
 cudaError_t prepare_paged_decode();
 
-// Joins the pieces in the workspace into O and LSE; a programmatic dependent of the
-// split kernel launched just before it.
-cudaError_t launch_decode_merge(const DecodeParams& p, cudaStream_t stream);
-
-// Decode over the 4-bit pool [num_pool_blocks, Hkv, 18 D] (kv4.cuh).
+// Decode over the 4-bit pool [num_pool_blocks, Hkv, 18 D] (kv4.cuh).  Its workspace:
+// part_o [pieces, group, D], part_lse [pieces, group], seg_first [S, Hkv], plan [2]; in
+// DecodeParams max_pieces is the number of pieces of the whole batch.
+constexpr int kKv4MaxRanges = 2048;  // warp ranges of one launch (152 SMs x 12 warps and some)
+struct Kv4DecodeWorkspace {
+  long long pieces;
+  size_t off_part_lse, off_seg_first, off_plan, bytes;
+};
+Kv4DecodeWorkspace kv4_decode_workspace(int S, int Hq, int Hkv, int D, int max_seq_len);
+long long kv4_max_ranges(int S, int Hkv, int max_seq_len);  // ranges a launch may use
 cudaError_t launch_kv4_decode(const uint8_t* pool, const DecodeParams& p, int num_sms,
                               cudaStream_t stream);
 cudaError_t prepare_kv4_decode();

@@ -28,8 +28,14 @@
 // block j of a step, one untiled bulk copy of the whole chunk (codes and scales of K and
 // V), into the warp's own ring in shared memory; the table entries of a step are read one
 // step ahead of its copies.  The fragments of m16n8k16 come out of shared memory by plain
-// loads in the order the format lays down.  The pieces are joined by the merge kernel of
-// paged_decode.cu.
+// loads in the order the format lays down.
+//
+// The shortest range is one step, so that a small batch spreads over many SMs; ranges are
+// dealt to the CTAs in turn for the same reason.  The piece of range k and segment s (both
+// counted along the batch) is k + s: no two pieces share that number and those of one
+// segment are consecutive, so the workspace holds ranges + segments pieces whatever the
+// lengths.  The merge kernel gives every (request, query head) a CTA whose warps take its
+// pieces in turn.
 #include <cuda_runtime.h>
 
 #include "decode_split.cuh"
@@ -43,7 +49,6 @@ namespace gbattn {
 namespace {
 
 constexpr int kBS = kPagedBlock;
-constexpr int kMinBlocks = kDecodeMinRange / kBS;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStepBlocks = 4;  // blocks of one step: 64 tokens share a softmax update
@@ -169,8 +174,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   for (int o = 16; o > 0; o >>= 1) nbr += __shfl_xor_sync(0xffffffffu, nbr, o);
   const long long NB = nbr * p.Hkv;
   const long long w_cap = static_cast<long long>(gridDim.x) * kWarps;
-  const int W = NB == 0 ? 0 : static_cast<int>(max(1ll, min(w_cap, NB / kMinBlocks)));
-  const int k_w = blockIdx.x * kWarps + warp;
+  const int W = NB == 0 ? 0 : static_cast<int>(max(1ll, min(w_cap, NB / kStepBlocks)));
+  const int k_w = warp * gridDim.x + blockIdx.x;
   if (k_w == 0 && lane == 0) {
     p.plan[0] = NB;
     p.plan[1] = W;
@@ -477,10 +482,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     if (c.b < c.nb && c_left > 0) continue;
     // ---- the piece ends: write its normalised O and LSE ----
     {
-      const int j = k_w - range_of(c.first, NB, W);  // piece index within the segment
       const float nan = __int_as_float(0x7fc00000);
-      const size_t hq0 = static_cast<size_t>(c.r) * p.Hq + c.h * group;
-      if (j >= 0 && j < p.max_pieces) {
+      const long long seg = static_cast<long long>(c.r) * p.Hkv + c.h;
+      const long long piece = k_w + seg;
+      if (piece < p.max_pieces) {
 #pragma unroll
         for (int nt = 0; nt < NQT; ++nt) {
 #pragma unroll
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
             const int q = 8 * nt + 2 * t4 + e;
             if (q >= group) continue;
             const float inv = pbad ? nan : 64.f / lsum;
-            const size_t base = (hq0 + q) * p.max_pieces + j;
+            const size_t base = piece * group + q;
             float* dst = p.part_o + base * D + 4 * g;
 #pragma unroll
             for (int w = 0; w < G; ++w)
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
             if (g == 0) p.part_lse[base] = pbad ? nan : m_q[nt][e] * sl[nt][e] + logf(lsum);
           }
         }
-        if (piece_b0 == 0 && lane == 0) p.seg_first[static_cast<size_t>(c.r) * p.Hkv + c.h] = c.first;
+        if (piece_b0 == 0 && lane == 0) p.seg_first[seg] = c.first;
       }
     }
     if (c_left == 0) break;
@@ -518,6 +523,115 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
         mbar_wait_quiet(bars + 8 * (i % C::kStages), (i / C::kStages) & 1, 500000000ull);
 }
 
+// LSE = M + ln sum_j e^{LSE_j - M}, O = sum_j e^{LSE_j - LSE} O_j over the pieces of one
+// (request, query head): a CTA, whose eight warps take every eighth piece, four of them in
+// flight at a time, and are joined in shared memory.  A NaN of a piece goes through.
+constexpr int kMergeWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) kv4_decode_merge_kernel(const DecodeParams p) {
+  constexpr int PER = D / 32;  // dims per lane
+  constexpr float kLog2e = 1.4426950408889634f;
+  __shared__ float part[kMergeWarps][D];
+  __shared__ float part_m[kMergeWarps], part_sum[kMergeWarps];
+  // launched as a programmatic dependent: the split kernel's results are complete and
+  // visible once this returns
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int r = blockIdx.x / p.Hq, hq = blockIdx.x - r * p.Hq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = hq / p.group;
+  const long long seg = static_cast<long long>(r) * p.Hkv + kvh;
+  const int L = p.seq_lens[r];
+  const long long NB = p.plan[0];
+  const int W = static_cast<int>(p.plan[1]);
+  const long long first = p.seg_first[seg];
+  const int nb = blocks_of(p, L);
+  const bool valid_len = L == 0 || nb > 0;
+  // (the plan always covers a valid nonempty request; the guard keeps every read in
+  // bounds should the lengths have changed between the two kernels)
+  const bool planned = nb > 0 && NB > 0 && W > 0 && first >= 0 && first + nb <= NB;
+  const int k0 = planned ? range_of(first, NB, W) : 0;
+  const int ns = planned ? range_of(first + nb - 1, NB, W) - k0 + 1 : 0;
+  const bool bad = !valid_len || (L > 0 && (ns < 1 || k0 + seg + ns > p.max_pieces));
+  const int n = bad ? 0 : ns;
+  const size_t base = static_cast<size_t>(k0 + seg) * p.group + (hq - kvh * p.group);
+  const float* pl = p.part_lse + base;
+  const float* po = p.part_o + base * D + lane * PER;
+
+  float m = -INFINITY, sum = 0.f, o[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) o[i] = 0.f;
+  for (int j0 = warp; j0 < n; j0 += 4 * kMergeWarps) {
+    float lse[4], v[4][PER];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int j = j0 + s * kMergeWarps;
+      lse[s] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[s][i] = 0.f;
+      if (j < n) {
+        lse[s] = pl[static_cast<size_t>(j) * p.group];
+        const float* src = po + static_cast<size_t>(j) * p.group * D;
+        if constexpr (PER == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          v[s][0] = x.x, v[s][1] = x.y, v[s][2] = x.z, v[s][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          v[s][0] = x.x, v[s][1] = x.y;
+        }
+      }
+    }
+    const float mn = fmaxf(fmaxf(m, lse[0]), fmax3(lse[1], lse[2], lse[3]));
+    const float ms = mn == -INFINITY ? 0.f : mn;  // (all four NaN)
+    const float al = ex2((m - ms) * kLog2e);
+    m = mn;
+    sum *= al;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] *= al;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const float w = ex2((lse[s] - ms) * kLog2e);
+      sum += w;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] = fmaf(w, v[s][i], o[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) part[warp][lane * PER + i] = o[i];
+  if (lane == 0) {
+    part_m[warp] = m;
+    part_sum[warp] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x >= D / 2) return;
+  float M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, part_m[w]);
+  const float Ms = M == -INFINITY ? 0.f : M;
+  float tot = 0.f, x0 = 0.f, x1 = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float f = ex2((part_m[w] - Ms) * kLog2e);
+    tot = fmaf(f, part_sum[w], tot);
+    x0 = fmaf(f, part[w][2 * threadIdx.x], x0);
+    x1 = fmaf(f, part[w][2 * threadIdx.x + 1], x1);
+  }
+  float lse_out = Ms + logf(tot);
+  const float inv = 1.f / tot;
+  x0 *= inv;
+  x1 *= inv;
+  if (L == 0) {
+    x0 = x1 = 0.f;
+    lse_out = -INFINITY;
+  } else if (bad) {
+    if (threadIdx.x == 0) raise_flag(p.flags, DEVFLAG_BAD_SEQLEN);
+    x0 = x1 = lse_out = __int_as_float(0x7fc00000);
+  }
+  reinterpret_cast<uint32_t*>(p.o)[static_cast<size_t>(blockIdx.x) * (D / 2) + threadIdx.x] =
+      pack_bf16x2(x0, x1);
+  if (p.lse != nullptr && threadIdx.x == 0) p.lse[blockIdx.x] = lse_out;
+}
+
 template <int D, int NQT>
 cudaError_t prepare() {
   return cudaFuncSetAttribute(kv4_decode_split_kernel<D, NQT>,
@@ -525,17 +639,17 @@ cudaError_t prepare() {
 }
 
 template <int D, int NQT>
-cudaError_t launch(const uint8_t* pool, const DecodeParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_split(const uint8_t* pool, const DecodeParams& p, int num_sms,
+                         cudaStream_t stream) {
   // kCtasPerSm CTAs per SM, fewer when even the shortest ranges would not fill them
-  const long long most_blocks =
-      static_cast<long long>(p.S) * p.Hkv * ((p.max_seq_len + kBS - 1) / kBS);
-  const long long want = (most_blocks / kMinBlocks + kWarps - 1) / kWarps;
-  const long long cap = static_cast<long long>(num_sms) * Shape<D, NQT>::kCtasPerSm;
+  const int ctas = num_sms * Shape<D, NQT>::kCtasPerSm;
+  const int cap = ctas < kKv4MaxRanges / kWarps ? ctas : kKv4MaxRanges / kWarps;
+  const long long want = (kv4_max_ranges(p.S, p.Hkv, p.max_seq_len) + kWarps - 1) / kWarps;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(want < 1 ? 1 : (want < cap ? want : cap)));
+  cfg.gridDim = dim3(static_cast<unsigned>(want < cap ? want : cap));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Shape<D, NQT>::kSmem;
   cfg.stream = stream;
@@ -544,7 +658,42 @@ cudaError_t launch(const uint8_t* pool, const DecodeParams& p, int num_sms, cuda
   return cudaLaunchKernelEx(&cfg, kv4_decode_split_kernel<D, NQT>, pool, p);
 }
 
+template <int D>
+cudaError_t launch(const uint8_t* pool, const DecodeParams& p, int num_sms, cudaStream_t stream) {
+  const cudaError_t e = p.group <= 8 ? launch_split<D, 1>(pool, p, num_sms, stream)
+                                     : launch_split<D, 2>(pool, p, num_sms, stream);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.S) * p.Hq);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_decode_merge_kernel<D>, p);
+}
+
 }  // namespace
+
+long long kv4_max_ranges(int S, int Hkv, int max_seq_len) {
+  const long long blocks = static_cast<long long>(S) * Hkv * ((max_seq_len + kBS - 1) / kBS);
+  const long long n = blocks / kStepBlocks;
+  return n < 1 ? 1 : (n < kKv4MaxRanges ? n : kKv4MaxRanges);
+}
+
+Kv4DecodeWorkspace kv4_decode_workspace(int S, int Hq, int Hkv, int D, int max_seq_len) {
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  Kv4DecodeWorkspace w;
+  w.pieces = kv4_max_ranges(S, Hkv, max_seq_len) + static_cast<long long>(S) * Hkv;
+  const size_t n = static_cast<size_t>(w.pieces) * (Hq / Hkv);
+  w.off_part_lse = up(n * D * sizeof(float));
+  w.off_seg_first = w.off_part_lse + up(n * sizeof(float));
+  w.off_plan = w.off_seg_first + up(static_cast<size_t>(S) * Hkv * sizeof(long long));
+  w.bytes = w.off_plan + up(2 * sizeof(long long));
+  return w;
+}
 
 cudaError_t prepare_kv4_decode() {
   cudaError_t e;
@@ -557,13 +706,7 @@ cudaError_t prepare_kv4_decode() {
 cudaError_t launch_kv4_decode(const uint8_t* pool, const DecodeParams& p, int num_sms,
                               cudaStream_t stream) {
   if (p.S <= 0) return cudaSuccess;
-  cudaError_t e;
-  if (p.D == 64)
-    e = p.group <= 8 ? launch<64, 1>(pool, p, num_sms, stream) : launch<64, 2>(pool, p, num_sms, stream);
-  else
-    e = p.group <= 8 ? launch<128, 1>(pool, p, num_sms, stream)
-                     : launch<128, 2>(pool, p, num_sms, stream);
-  return e != cudaSuccess ? e : launch_decode_merge(p, stream);
+  return p.D == 64 ? launch<64>(pool, p, num_sms, stream) : launch<128>(pool, p, num_sms, stream);
 }
 
 }  // namespace gbattn

@@ -709,15 +709,6 @@ cudaError_t launch_pair(const CUtensorMap& tmK, const CUtensorMap& tmV, const De
     e = cudaLaunchKernelEx(&split, paged_decode_split_kernel<D, 2>, tmK, tmV, p);
   }
   if (e != cudaSuccess) return e;
-  return launch_decode_merge(p, stream);
-}
-
-}  // namespace
-
-cudaError_t launch_decode_merge(const DecodeParams& p, cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.S * p.Hq + 3) / 4);
   cfg.blockDim = dim3(128);
@@ -725,9 +716,10 @@ cudaError_t launch_decode_merge(const DecodeParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.D == 64 ? cudaLaunchKernelEx(&cfg, paged_decode_merge_kernel<64>, p)
-                   : cudaLaunchKernelEx(&cfg, paged_decode_merge_kernel<128>, p);
+  return cudaLaunchKernelEx(&cfg, paged_decode_merge_kernel<D>, p);
 }
+
+}  // namespace
 
 cudaError_t launch_paged_decode(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                 const DecodeParams& p, int num_sms, cudaStream_t stream) {

@@ -377,8 +377,13 @@ int paged_kv4_gather(const void *kv_pool, const int32_t *block_table, const int3
                      int num_pool_blocks, int max_seq_len, void *k_out, void *v_out,
                      void *stream);
 
-/* Bytes of scratch workspace paged_kv4_attn_decode needs for these sizes. */
-size_t paged_kv4_attn_decode_workspace_size(int num_seqs, int Hq, int D, int max_seq_len);
+/*
+ * Bytes of scratch workspace paged_kv4_attn_decode needs for these sizes: one partial
+ * output (D fp32) and LSE per query head for each of at most 2048 + num_seqs * Hkv
+ * pieces of the batch.
+ */
+size_t paged_kv4_attn_decode_workspace_size(int num_seqs, int Hq, int Hkv, int D,
+                                            int max_seq_len);
 
 /*
  * paged_kv4_attn_decode -- paged_attn_decode over the 4-bit cache: the attention of

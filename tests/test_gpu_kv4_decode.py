@@ -218,7 +218,7 @@ def test_decode_steps_from_projections_replayed_as_a_graph(gb):
             self.qr = torch.empty((S, Hq, 1, D), dtype=torch.bfloat16, device="cuda")
             self.o = torch.empty((S, Hq, D), dtype=torch.bfloat16, device="cuda")
             self.lse = torch.empty((S, Hq), dtype=torch.float32, device="cuda")
-            n = gb.paged_kv4_attn_decode_workspace_size(S, Hq, D, room)
+            n = gb.paged_kv4_attn_decode_workspace_size(S, Hq, Hkv, D, room)
             self.ws = torch.empty(max(n, 256), dtype=torch.uint8, device="cuda")
 
         def step(self):

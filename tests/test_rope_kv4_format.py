@@ -196,7 +196,7 @@ def test_kv4_gather_refusals(kw, code):
 def test_kv4_decode_refusals(kw, code):
     a = dict(q=A16, pool=A16, bt=A16, sl=A16, bs=16, S=4, Hq=12, Hkv=2, D=128, mb=512, nb=1000,
              msl=8192, scale=0.088, o=A16, lse=None, ws=A16, wsb=0) | kw
-    need = gb.paged_kv4_attn_decode_workspace_size(a["S"], a["Hq"], a["D"], a["msl"])
+    need = gb.paged_kv4_attn_decode_workspace_size(a["S"], a["Hq"], a["Hkv"], a["D"], a["msl"])
     assert gb.lib().paged_kv4_attn_decode(a["q"], a["pool"], a["bt"], a["sl"], a["bs"], a["S"],
                                           a["Hq"], a["Hkv"], a["D"], a["mb"], a["nb"], a["msl"],
                                           a["scale"], a["o"], a["lse"], a["ws"],
