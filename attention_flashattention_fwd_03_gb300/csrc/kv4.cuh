@@ -52,11 +52,34 @@ __device__ __forceinline__ uint32_t kv4_scale_bits(uint32_t amax_bits) {
   return (t + 0x3ffffu + ((t >> 19) & 1u)) & 0xfff80000u;  // 1 + 4 mantissa bits
 }
 
-// Code of one channel for a scale (code 8, i.e. zero, where the scale is 0 or NaN).
-__device__ __forceinline__ uint32_t kv4_code(float x, float s) {
-  if (!(s > 0.f)) return 8u;
-  const float n = fminf(fmaxf(rintf(__fdiv_rn(x, s)), -7.f), 7.f);
-  return static_cast<uint32_t>(static_cast<int>(n) + 8);
+// Codes of the eight channels of a lane for their group's scale (code 8, i.e. zero, where
+// the scale is 0 or NaN), the first in the lowest nibble.
+//
+// n = round(x / s), ties to even, without a division: x has 8 significant bits and s 5,
+// so a quotient that is not exactly k + 1/2 keeps a distance of at least 1/992 from it,
+// while x (1 / s) is within 2^-21 of the quotient.  Adding 6144 rounds that product to a
+// multiple of 2^-11, which puts exact ties back in place; adding 3 * 2^22 + 8 then rounds
+// to an integer, whose low bits are the code.  (Checked against exact division for every
+// pair of significands.)  |n| <= 7 holds by itself: s >= amax / 7 * 31 / 32.  Scales near
+// the ends of the fp32 range, where 1 / s is not a normal number, take a division.
+__device__ __forceinline__ uint32_t kv4_codes(const float (&x)[8], float s) {
+  uint32_t w = 0;
+  if (s > 1e-30f && s < 1e30f) {
+    const float inv = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = __fadd_rn(__fmaf_rn(x[i], inv, 6144.f), -6144.f);
+      const uint32_t bits = __float_as_uint(__fadd_rn(q, 12582920.f));
+      w += (bits - 0x4b400000u) << (4 * i);
+    }
+    return w;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float n = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -7.f), 7.f) : 0.f;
+    w |= static_cast<uint32_t>(static_cast<int>(n) + 8) << (4 * i);
+  }
+  return w;
 }
 
 }  // namespace gbattn

@@ -4,9 +4,9 @@
 // The mathematics and the lane layout are in norm_rope.cuh, the 4-bit format in kv4.cuh.
 //
 // Forward and appends: memory-bound, each value read and written once.  A warp takes a
-// run of the rows (q, k and v heads) of one token, 32 / (D / 8) rows at a time, so its
-// table row and weights are read once and every row moves as whole 128- or 256-byte
-// segments.
+// run of the rows (q, k and v heads) of one token, 32 / (D / 8) rows a pass, so its table
+// row and weights are read once and every row moves as whole 128- or 256-byte segments;
+// the loads of four passes are in flight together.
 #include <cuda_runtime.h>
 
 #include "kv4.cuh"
@@ -44,19 +44,19 @@ template <int D, bool IS_V>
 __device__ __forceinline__ void quantise_row(uint4 w, uint8_t* chunk, int slot, int l, bool write) {
   using F = Kv4<D>;
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-  uint32_t amax = 0;  // bf16 magnitudes order like their bits, NaN and infinity on top
-#pragma unroll
-  for (int i = 0; i < 4; ++i) amax = max(amax, max(in[i] & 0x7fffu, (in[i] >> 16) & 0x7fffu));
-  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  const uint32_t sbits = kv4_scale_bits(amax);
-  const float s = __uint_as_float(sbits);
-  uint32_t codes = 0;
+  // bf16 magnitudes order like their bits, NaN and infinity on top
+  uint32_t pair = __vmaxu2(__vmaxu2(in[0] & 0x7fff7fffu, in[1] & 0x7fff7fffu),
+                           __vmaxu2(in[2] & 0x7fff7fffu, in[3] & 0x7fff7fffu));
+  pair = __vmaxu2(pair, __shfl_xor_sync(0xffffffffu, pair, 1));
+  pair = __vmaxu2(pair, __shfl_xor_sync(0xffffffffu, pair, 2));
+  const uint32_t sbits = kv4_scale_bits(max(pair & 0xffffu, pair >> 16));
+  float x[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    codes |= kv4_code(bf16_lo(in[i]), s) << (8 * i);
-    codes |= kv4_code(bf16_hi(in[i]), s) << (8 * i + 4);
+    x[2 * i] = bf16_lo(in[i]);
+    x[2 * i + 1] = bf16_hi(in[i]);
   }
+  const uint32_t codes = kv4_codes(x, __uint_as_float(sbits));
   if (!write) return;
   const int group = l >> 2, part = l & 3;  // channels 8 l .. 8 l + 7 of group l / 4
   uint8_t* row = chunk + (IS_V ? F::kOffVCodes : F::kOffKCodes) + slot * F::kCodeRow;
@@ -73,13 +73,112 @@ __device__ __forceinline__ void quantise_row(uint4 w, uint8_t* chunk, int slot, 
   }
 }
 
+constexpr int kUnroll = 4;  // passes whose loads are in flight together
+
+// What the rows of one token share.
+struct TokenCtx {
+  LaneChannels ch;
+  float4 co, si;
+  int l, sub;       // lane within its row, row within the pass
+  int interleaved;
+  float eps;
+  bool live;        // false: q and k rows are NaN
+  bool write_kv;    // paged: K and V reach the cache
+  int slot;
+};
+
+// Query or key rows h0 .. h1 - 1: x[h * sh] -> y[h * oh] (QUANT: the 4-bit chunk at
+// y4 + h * kChunk, through the warp's rows of shared memory, which bring the lane's two
+// runs of channels into order).  LD lanes past h1 take part with zeros.
+template <int D, bool QUANT>
+__device__ __forceinline__ void norm_rope_rows(const TokenCtx& t, const uint16_t* x, long long sh,
+                                               const uint16_t* w, int h0, int h1, uint16_t* y,
+                                               long long oh, uint8_t* y4, uint16_t* stage,
+                                               bool write) {
+  constexpr int LANES = D / 8;
+  constexpr int ROWS = 32 / LANES;
+  float wf[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) wf[i] = 1.f;
+  if (w) widen8(ld8(w + t.ch.c0), ld8(w + t.ch.c1), wf);
+  for (int r0 = h0; r0 < h1; r0 += ROWS * kUnroll) {
+    uint2 a[kUnroll], c[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = r0 + u * ROWS + t.sub;
+      a[u] = c[u] = make_uint2(0, 0);
+      if (h < h1) {
+        a[u] = ld8(x + h * sh + t.ch.c0);
+        c[u] = ld8(x + h * sh + t.ch.c1);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (r0 + u * ROWS >= h1) break;
+      const int h = r0 + u * ROWS + t.sub;
+      float v[8];
+      widen8(a[u], c[u], v);
+      if (w) {
+        const float r = row_rrms<D>(v, t.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * r * wf[i];
+      }
+      if (t.ch.rotates) rotate8<false>(v, t.co, t.si, t.interleaved);
+      round8(v, a[u], c[u]);
+      if (!t.live) a[u] = c[u] = make_uint2(kBf16NanPair, kBf16NanPair);
+      if constexpr (QUANT) {
+        uint16_t* mine = stage + t.sub * D;
+        __syncwarp();
+        st8(mine + t.ch.c0, a[u]);
+        st8(mine + t.ch.c1, c[u]);
+        __syncwarp();
+        quantise_row<D, false>(*reinterpret_cast<const uint4*>(mine + 8 * t.l),
+                               y4 + h * static_cast<long long>(Kv4<D>::kChunk), t.slot, t.l,
+                               write && h < h1);
+      } else if (write && h < h1) {
+        st8(y + h * oh + t.ch.c0, a[u]);
+        st8(y + h * oh + t.ch.c1, c[u]);
+      }
+    }
+  }
+}
+
+// Value rows h0 .. h1 - 1, taken in channel order.
+template <int D, bool QUANT>
+__device__ __forceinline__ void value_rows(const TokenCtx& t, const uint16_t* x, long long sh,
+                                           int h0, int h1, uint16_t* y, long long oh, uint8_t* y4,
+                                           bool write) {
+  constexpr int LANES = D / 8;
+  constexpr int ROWS = 32 / LANES;
+  for (int r0 = h0; r0 < h1; r0 += ROWS * kUnroll) {
+    uint4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = r0 + u * ROWS + t.sub;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (h < h1) v[u] = *reinterpret_cast<const uint4*>(x + h * sh + 8 * t.l);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (r0 + u * ROWS >= h1) break;
+      const int h = r0 + u * ROWS + t.sub;
+      if constexpr (QUANT) {
+        quantise_row<D, true>(v[u], y4 + h * static_cast<long long>(Kv4<D>::kChunk), t.slot, t.l,
+                              write && h < h1);
+      } else if (write && h < h1) {
+        *reinterpret_cast<uint4*>(y + h * oh + 8 * t.l) = v[u];
+      }
+    }
+  }
+}
+
 template <int D, RowSink SINK>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p) {
   constexpr int LANES = D / 8;       // lanes of one row
   constexpr int ROWS = 32 / LANES;   // rows of one pass
   constexpr bool PAGED = SINK != RowSink::kContiguous;
-  // the 4-bit cache takes a K row in channel order: rows pass through shared memory
-  __shared__ __align__(16) uint16_t stage[SINK == RowSink::kPaged4 ? kWarps * ROWS * D : 8];
+  constexpr bool QUANT = SINK == RowSink::kPaged4;
+  __shared__ __align__(16) uint16_t stage[QUANT ? kWarps * ROWS * D : 8];
   if (PAGED) {
     // a decode launched next as a programmatic dependent may start its set-up now; it
     // waits for this grid's writes before it reads anything
@@ -90,110 +189,83 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
   const long long tok = wid / p.chunks;
   const int chunk = static_cast<int>(wid - tok * p.chunks);
   if (tok >= static_cast<long long>(p.B) * p.T) return;
-  const int b = static_cast<int>(tok / p.T), t = static_cast<int>(tok - static_cast<long long>(b) * p.T);
-  const int l = lane % LANES, sub = lane / LANES;
-  const LaneChannels ch = lane_channels(l, p.rope.rot, p.rope.interleaved);
+  const int b = static_cast<int>(tok / p.T), ti = static_cast<int>(tok - static_cast<long long>(b) * p.T);
+  TokenCtx t;
+  t.l = lane % LANES;
+  t.sub = lane / LANES;
+  t.interleaved = p.rope.interleaved;
+  t.eps = p.rope.eps;
+  t.ch = lane_channels(t.l, p.rope.rot, p.rope.interleaved);
+  t.live = t.write_kv = true;
+  t.slot = 0;
 
   // ---- where this token goes, and its rotation ----
-  int pos = t;
-  bool write_kv = true;   // K and V reach the cache
-  bool live = true;       // false: the query row is NaN
-  int slot = 0;           // paged: token slot within its block
+  int pos = ti;
   long long block = 0;    // paged: physical block
   const bool first = chunk == 0 && lane == 0;
   if constexpr (PAGED) {
     const int L = p.seq_lens[b];
     if (L < 0 || L > p.max_blocks * kPagedBlock - p.T) {
-      if (first && t == 0) {
+      if (first && ti == 0) {
         raise_flag(p.flags, DEVFLAG_BAD_SEQLEN);
         if (p.new_seq_lens) p.new_seq_lens[b] = L;
       }
-      live = write_kv = false;
+      t.live = t.write_kv = false;
     } else {
-      if (first && t == 0 && p.new_seq_lens) p.new_seq_lens[b] = L + p.T;
-      pos = L + t;
-      slot = pos % kPagedBlock;
+      if (first && ti == 0 && p.new_seq_lens) p.new_seq_lens[b] = L + p.T;
+      pos = L + ti;
+      t.slot = pos % kPagedBlock;
       block = p.block_table[static_cast<size_t>(b) * p.max_blocks + pos / kPagedBlock];
       if (block < 0 || block >= p.num_pool_blocks) {
         if (first) raise_flag(p.flags, DEVFLAG_BAD_BLOCK);
-        write_kv = false;
+        t.write_kv = false;
+        block = 0;
       }
     }
   }
-  if (p.rope.rot > 0 && live) {
+  if (p.rope.rot > 0 && t.live) {
     if (p.rope.positions) pos = p.rope.positions[tok];
     if (pos < 0 || pos >= p.rope.max_pos) {
       if (first) raise_flag(p.flags, DEVFLAG_BAD_POSITION);
-      live = false;
-      if (PAGED) write_kv = false;
+      t.live = false;
+      if (PAGED) t.write_kv = false;
     }
   }
-  float4 co, si;
-  load_planes(p.rope, pos, l, ch.rotates && live, co, si);
+  load_planes(p.rope, pos, t.l, t.ch.rotates && t.live, t.co, t.si);
 
+  // ---- this warp's share of the token's query, key and value rows ----
   const int rows = p.nq + p.nk + p.nv;
-  const int row_end = min(rows, (chunk + 1) * p.rows_per_warp);
-  for (int row0 = chunk * p.rows_per_warp; row0 < row_end; row0 += ROWS) {
-    const int row = row0 + sub;
-    const bool in = row < row_end;
-    const bool is_q = row < p.nq;
-    const bool is_v = row >= p.nq + p.nk;
-    const int h = is_q ? row : (is_v ? row - p.nq - p.nk : row - p.nq);
-    const Heads& src = is_q ? p.q : (is_v ? p.v : p.k);
-    // V rows are taken in channel order
-    const int c0 = is_v ? 8 * l : ch.c0, c1 = is_v ? 8 * l + 4 : ch.c1;
-    uint2 a = make_uint2(0, 0), c = make_uint2(0, 0);
-    if (in) {
-      const uint16_t* x = src.p + b * src.sb + t * src.st + h * src.sh;
-      a = ld8(x + c0);
-      c = ld8(x + c1);
-    }
-    float x[8];
-    widen8(a, c, x);
-    const float r = row_rrms<D>(x, p.rope.eps);
-    const uint16_t* w = is_q ? p.rope.q_weight : p.rope.k_weight;
-    if (!is_v) {
-      if (w) {
-        float wf[8];
-        widen8(ld8(w + c0), ld8(w + c1), wf);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wf[i];
-      }
-      if (ch.rotates) rotate8<false>(x, co, si, p.rope.interleaved);
-      round8(x, a, c);
-      if (!live) a = c = make_uint2(kBf16NanPair, kBf16NanPair);
-    }
-    if (is_q || !PAGED) {
-      if (in) {
-        uint16_t* base = is_q ? p.q_out : (is_v ? p.v_out : p.k_out);
-        const int heads = is_q ? p.nq : (is_v ? p.nv : p.nk);
-        uint16_t* y = base + ((static_cast<long long>(b) * heads + h) * p.T + t) * D;
-        st8(y + c0, a);
-        st8(y + c1, c);
-      }
-    } else if constexpr (SINK == RowSink::kPaged) {
-      if (in && write_kv) {
-        uint16_t* y = (is_v ? p.v_pool : p.k_pool) +
-                      ((block * p.nk + h) * kPagedBlock + slot) * static_cast<long long>(D);
-        st8(y + c0, a);
-        st8(y + c1, c);
-      }
-    }
-    if constexpr (SINK == RowSink::kPaged4) {
-      // every lane of the warp takes part: the quantiser exchanges between lanes
-      const bool any_kv = __any_sync(0xffffffffu, in && !is_q);
-      if (any_kv) {
-        uint16_t* mine = stage + ((threadIdx.x >> 5) * ROWS + sub) * D;
-        st8(mine + c0, a);
-        st8(mine + c1, c);
-        __syncwarp();
-        const uint4 w8 = *reinterpret_cast<const uint4*>(mine + 8 * l);
-        uint8_t* dst = p.kv4_pool + (block * p.nk + h) * Kv4<D>::kChunk;
-        quantise_row<D, false>(w8, dst, slot, l, in && write_kv && !is_q && !is_v);
-        quantise_row<D, true>(w8, dst, slot, l, in && write_kv && is_v);
-        __syncwarp();
-      }
-    }
+  const int c0 = chunk * p.rows_per_warp, c1 = min(rows, c0 + p.rows_per_warp);
+  auto in = [&](const Heads& x) { return x.p + b * x.sb + ti * x.st; };
+  auto out = [&](uint16_t* y, int heads) {
+    return y + (static_cast<long long>(b) * heads * p.T + ti) * D;
+  };
+  const long long oh = static_cast<long long>(p.T) * D;
+  if (c0 < p.nq)
+    norm_rope_rows<D, false>(t, in(p.q), p.q.sh, p.rope.q_weight, c0, min(c1, p.nq),
+                             out(p.q_out, p.nq), oh, nullptr, nullptr, true);
+  const int k0 = max(c0 - p.nq, 0), k1 = min(c1 - p.nq, p.nk);
+  const int v0 = max(c0 - p.nq - p.nk, 0), v1 = c1 - p.nq - p.nk;
+  if constexpr (!PAGED) {
+    if (k0 < k1)
+      norm_rope_rows<D, false>(t, in(p.k), p.k.sh, p.rope.k_weight, k0, k1, out(p.k_out, p.nk), oh,
+                               nullptr, nullptr, true);
+    if (v0 < v1) value_rows<D, false>(t, in(p.v), p.v.sh, v0, v1, out(p.v_out, p.nv), oh, nullptr, true);
+  } else if constexpr (!QUANT) {
+    const long long at = (block * p.nk * kPagedBlock + t.slot) * D;  // pool row of head 0
+    constexpr long long ph = kPagedBlock * D;
+    if (k0 < k1)
+      norm_rope_rows<D, false>(t, in(p.k), p.k.sh, p.rope.k_weight, k0, k1, p.k_pool + at, ph,
+                               nullptr, nullptr, t.write_kv);
+    if (v0 < v1)
+      value_rows<D, false>(t, in(p.v), p.v.sh, v0, v1, p.v_pool + at, ph, nullptr, t.write_kv);
+  } else {
+    uint8_t* chunk4 = p.kv4_pool + block * p.nk * Kv4<D>::kChunk;
+    if (k0 < k1)
+      norm_rope_rows<D, true>(t, in(p.k), p.k.sh, p.rope.k_weight, k0, k1, nullptr, 0, chunk4,
+                              stage + (threadIdx.x >> 5) * ROWS * D, t.write_kv);
+    if (v0 < v1)
+      value_rows<D, true>(t, in(p.v), p.v.sh, v0, v1, nullptr, 0, chunk4, t.write_kv);
   }
 }
 
@@ -204,8 +276,10 @@ cudaError_t launch_norm_rope(NormRopeParams p, int D, RowSink sink, int num_sms,
   const int rows = p.nq + p.nk + p.nv;
   const long long tokens = static_cast<long long>(p.B) * p.T;
   if (tokens <= 0 || rows <= 0) return cudaSuccess;
-  const int per_pass = 256 / D;
-  p.rows_per_warp = per_pass * 8;
+  // A warp takes whole tokens where there are enough of them to fill the SMs (the table
+  // row and the weights are then read once), else one unrolled pass of a token.
+  const int pass = 256 / D * kUnroll;
+  p.rows_per_warp = tokens >= 32ll * num_sms ? rows : pass;
   p.chunks = (rows + p.rows_per_warp - 1) / p.rows_per_warp;
   const long long grid = (tokens * p.chunks + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
