@@ -87,7 +87,7 @@ bool good_input(const void* p, const int64_t* s) { return p && aligned(p, 16) &&
 
 bool too_many_rows(int B, int T, int Hq, int Hkv) {
   const unsigned __int128 n = static_cast<unsigned __int128>(B) * T;
-  return n >= kMaxDim * 8 || n * (static_cast<uint64_t>(Hq) + 2ull * Hkv) >= (1ull << 34);
+  return n >= kMaxDim || n * (static_cast<uint64_t>(Hq) + 2ull * Hkv) >= (1ull << 34);
 }
 
 bool overlap(const void* a, const void* b, size_t bytes) {

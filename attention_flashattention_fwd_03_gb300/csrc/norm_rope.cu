@@ -19,8 +19,12 @@ namespace gbattn {
 
 namespace {
 
-constexpr int kWarps = 8;
+// One warp a CTA: a token's rows leave an SM as they end, without waiting for others.
+// (16k prompt, four passes unrolled: 1 warp 66.1 us, 2 68.4, 4 68.6, 8 69.6, each held to
+// 64 registers; two passes unrolled 77.5, three 75.0, six 74.3, eight 91.8.)
+constexpr int kWarps = 1;
 constexpr int kThreads = kWarps * 32;
+constexpr int kCtasPerSm = 32;
 
 __device__ __forceinline__ uint2 ld8(const uint16_t* p) { return *reinterpret_cast<const uint2*>(p); }
 __device__ __forceinline__ void st8(uint16_t* p, uint2 v) { *reinterpret_cast<uint2*>(p) = v; }
@@ -173,7 +177,7 @@ __device__ __forceinline__ void value_rows(const TokenCtx& t, const uint16_t* x,
 }
 
 template <int D, RowSink SINK>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const NormRopeParams p) {
   constexpr int LANES = D / 8;       // lanes of one row
   constexpr int ROWS = 32 / LANES;   // rows of one pass
   constexpr bool PAGED = SINK != RowSink::kContiguous;
@@ -277,9 +281,10 @@ cudaError_t launch_norm_rope(NormRopeParams p, int D, RowSink sink, int num_sms,
   const long long tokens = static_cast<long long>(p.B) * p.T;
   if (tokens <= 0 || rows <= 0) return cudaSuccess;
   // A warp takes whole tokens where there are enough of them to fill the SMs (the table
-  // row and the weights are then read once), else one unrolled pass of a token.
-  const int pass = 256 / D * kUnroll;
-  p.rows_per_warp = tokens >= 32ll * num_sms ? rows : pass;
+  // row and the weights are then read once), else four passes of a token, or two where
+  // there are so few tokens that only the depth of the work counts.
+  const int pass = 256 / D;
+  p.rows_per_warp = tokens >= 32ll * num_sms ? rows : (tokens >= 4ll * num_sms ? 4 : 2) * pass;
   p.chunks = (rows + p.rows_per_warp - 1) / p.rows_per_warp;
   const long long grid = (tokens * p.chunks + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -312,95 +317,123 @@ cudaError_t launch_norm_rope(NormRopeParams p, int D, RowSink sink, int num_sms,
 // every sum depends on the sizes alone.
 namespace {
 
-constexpr int kBwdMaxGrid = 456;  // three CTAs on each of 152 SMs
+constexpr int kBwdWarps = 8;
+constexpr int kBwdThreads = kBwdWarps * 32;
+constexpr int kBwdMaxGrid = 304;  // two CTAs on each of 152 SMs
+constexpr int kBwdUnroll = 4;     // passes whose loads are in flight together
 
+// Query or key rows of one token: dx from the gradient g (head stride gh) and, with a
+// weight, the input x; adds this lane's terms of the weight gradient to dw.
 template <int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
+__device__ __forceinline__ void norm_rope_bwd_rows(const TokenCtx& t, const uint16_t* g,
+                                                   long long gh, const uint16_t* x, long long sh,
+                                                   const uint16_t* w, int heads, uint16_t* dx,
+                                                   long long dh, float (&dw)[8]) {
   constexpr int LANES = D / 8;
   constexpr int ROWS = 32 / LANES;
-  __shared__ float red[kWarps * ROWS][2][D];
+  float wf[8];
+  if (w) widen8(ld8(w + t.ch.c0), ld8(w + t.ch.c1), wf);
+  for (int r0 = 0; r0 < heads; r0 += ROWS * kBwdUnroll) {
+    uint2 ga[kBwdUnroll], gc[kBwdUnroll], xa[kBwdUnroll], xc[kBwdUnroll];
+#pragma unroll
+    for (int u = 0; u < kBwdUnroll; ++u) {
+      const int h = r0 + u * ROWS + t.sub;
+      ga[u] = gc[u] = xa[u] = xc[u] = make_uint2(0, 0);
+      if (h < heads) {
+        ga[u] = ld8(g + h * gh + t.ch.c0);
+        gc[u] = ld8(g + h * gh + t.ch.c1);
+        if (w) {
+          xa[u] = ld8(x + h * sh + t.ch.c0);
+          xc[u] = ld8(x + h * sh + t.ch.c1);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBwdUnroll; ++u) {
+      if (r0 + u * ROWS >= heads) break;
+      const int h = r0 + u * ROWS + t.sub;
+      float v[8];
+      widen8(ga[u], gc[u], v);
+      if (t.ch.rotates) rotate8<true>(v, t.co, t.si, t.interleaved);
+      if (w) {
+        float xh[8];
+        widen8(xa[u], xc[u], xh);
+        // both sums of the row at once: x^2 and (dy w) x
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ss = fmaf(xh[i], xh[i], ss);
+          dot = fmaf(v[i] * wf[i], xh[i], dot);
+        }
+        ss = row_sum<LANES>(ss);
+        dot = row_sum<LANES>(dot);
+        const float r = rsqrtf(ss * (1.f / D) + t.eps);
+        const float mean = dot * r * (1.f / D);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          xh[i] *= r;
+          dw[i] = fmaf(v[i], xh[i], dw[i]);  // 0 for a row past the end: its g is 0
+          v[i] = r * (v[i] * wf[i] - xh[i] * mean);
+        }
+      }
+      round8(v, ga[u], gc[u]);
+      if (!t.live) ga[u] = gc[u] = make_uint2(kBf16NanPair, kBf16NanPair);
+      if (h < heads) {
+        st8(dx + h * dh + t.ch.c0, ga[u]);
+        st8(dx + h * dh + t.ch.c1, gc[u]);
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
+  constexpr int LANES = D / 8;
+  constexpr int ROWS = 32 / LANES;
+  __shared__ float red[kBwdWarps * ROWS][2][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int l = lane % LANES, sub = lane / LANES;
-  const LaneChannels ch = lane_channels(l, p.rope.rot, p.rope.interleaved);
-  const long long tokens = static_cast<long long>(p.B) * p.T;
-  const int rows = p.nq + p.nk + p.nv;
+  TokenCtx t;
+  t.l = lane % LANES;
+  t.sub = lane / LANES;
+  t.interleaved = p.rope.interleaved;
+  t.eps = p.rope.eps;
+  t.ch = lane_channels(t.l, p.rope.rot, p.rope.interleaved);
+  // a unit of work is one operand of one token, so that the warps end together
+  const long long units = static_cast<long long>(p.B) * p.T * 3;
+  const long long gh = static_cast<long long>(p.T) * D;
   float dwq[8], dwk[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
 
-  for (long long tok = static_cast<long long>(blockIdx.x) * kWarps + warp; tok < tokens;
-       tok += static_cast<long long>(gridDim.x) * kWarps) {
+  for (long long unit = static_cast<long long>(blockIdx.x) * kBwdWarps + warp; unit < units;
+       unit += static_cast<long long>(gridDim.x) * kBwdWarps) {
+    const long long tok = unit / 3;
+    const int op = static_cast<int>(unit - 3 * tok);
     const int b = static_cast<int>(tok / p.T);
-    const int t = static_cast<int>(tok - static_cast<long long>(b) * p.T);
-    int pos = t;
-    bool live = true;
+    const int ti = static_cast<int>(tok - static_cast<long long>(b) * p.T);
+    int pos = ti;
+    t.live = true;
     if (p.rope.rot > 0) {
       if (p.rope.positions) pos = p.rope.positions[tok];
       if (pos < 0 || pos >= p.rope.max_pos) {
         if (lane == 0) raise_flag(p.flags, DEVFLAG_BAD_POSITION);
-        live = false;
+        t.live = false;
       }
     }
-    float4 co, si;
-    load_planes(p.rope, pos, l, ch.rotates && live, co, si);
-    for (int row0 = 0; row0 < rows; row0 += ROWS) {
-      const int row = row0 + sub;
-      const bool in = row < rows;
-      const bool is_q = row < p.nq;
-      const bool is_v = row >= p.nq + p.nk;
-      const int h = is_q ? row : (is_v ? row - p.nq - p.nk : row - p.nq);
-      const int heads = is_q ? p.nq : (is_v ? p.nv : p.nk);
-      const Heads& dst = is_q ? p.dq : (is_v ? p.dv : p.dk);
-      const int c0 = is_v ? 8 * l : ch.c0, c1 = is_v ? 8 * l + 4 : ch.c1;
-      uint2 ga = make_uint2(0, 0), gc = make_uint2(0, 0), xa = ga, xc = ga;
-      const uint16_t* w = is_v ? nullptr : (is_q ? p.rope.q_weight : p.rope.k_weight);
-      if (in) {
-        const uint16_t* gsrc = is_q ? p.gq : (is_v ? p.gv : p.gk);
-        const uint16_t* g = gsrc + ((static_cast<long long>(b) * heads + h) * p.T + t) * D;
-        ga = ld8(g + c0);
-        gc = ld8(g + c1);
-        if (w) {
-          const Heads& src = is_q ? p.q : p.k;
-          const uint16_t* x = src.p + b * src.sb + t * src.st + h * src.sh;
-          xa = ld8(x + c0);
-          xc = ld8(x + c1);
-        }
-      }
-      float g[8], x[8], wf[8];
-      widen8(ga, gc, g);
-      widen8(xa, xc, x);
-      if (!is_v && ch.rotates) rotate8<true>(g, co, si, p.rope.interleaved);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) wf[i] = 1.f;
-      if (w) widen8(ld8(w + c0), ld8(w + c1), wf);
-      const float r = row_rrms<D>(x, p.rope.eps);
-      float dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) dot = fmaf(g[i] * wf[i], x[i] * r, dot);
-      dot = row_sum<LANES>(dot) * (1.f / D);
-      if (w) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xh = x[i] * r;
-          const float dw = g[i] * xh;  // 0 for a row past the end: its g is 0
-          if (is_q)
-            dwq[i] += dw;
-          else
-            dwk[i] += dw;
-          g[i] = r * (g[i] * wf[i] - xh * dot);
-        }
-      }
-      if (in) {
-        if (!is_v) {
-          round8(g, ga, gc);
-          if (!live) ga = gc = make_uint2(kBf16NanPair, kBf16NanPair);
-        }
-        uint16_t* y = dst.p + b * dst.sb + t * dst.st + h * dst.sh;
-        st8(y + c0, ga);
-        st8(y + c1, gc);
-      }
-    }
-    if (!live) {  // a gradient through an unknown rotation is unknown
+    load_planes(p.rope, pos, t.l, t.ch.rotates && t.live, t.co, t.si);
+    auto grad = [&](const uint16_t* g, int heads) {
+      return g + (static_cast<long long>(b) * heads * p.T + ti) * D;
+    };
+    auto at = [&](const Heads& x) { return x.p + b * x.sb + ti * x.st; };
+    if (op == 0 && p.nq > 0)
+      norm_rope_bwd_rows<D>(t, grad(p.gq, p.nq), gh, at(p.q), p.q.sh, p.rope.q_weight, p.nq,
+                            at(p.dq), p.dq.sh, dwq);
+    if (op == 1 && p.nk > 0)
+      norm_rope_bwd_rows<D>(t, grad(p.gk, p.nk), gh, at(p.k), p.k.sh, p.rope.k_weight, p.nk,
+                            at(p.dk), p.dk.sh, dwk);
+    if (op == 2 && p.nv > 0)
+      value_rows<D, false>(t, grad(p.gv, p.nv), gh, 0, p.nv, at(p.dv), p.dv.sh, nullptr, true);
+    if (!t.live) {  // a gradient through an unknown rotation is unknown
 #pragma unroll
       for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = __int_as_float(0x7fc00000);
     }
@@ -408,15 +441,15 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeB
   if (p.part == nullptr) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int c = i < 4 ? ch.c0 + i : ch.c1 + i - 4;
-    red[warp * ROWS + sub][0][c] = dwq[i];
-    red[warp * ROWS + sub][1][c] = dwk[i];
+    const int c = i < 4 ? t.ch.c0 + i : t.ch.c1 + i - 4;
+    red[warp * ROWS + t.sub][0][c] = dwq[i];
+    red[warp * ROWS + t.sub][1][c] = dwk[i];
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < 2 * D; e += kThreads) {
+  for (int e = threadIdx.x; e < 2 * D; e += kBwdThreads) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWarps * ROWS; ++i) s += red[i][e / D][e % D];
+    for (int i = 0; i < kBwdWarps * ROWS; ++i) s += red[i][e / D][e % D];
     p.part[static_cast<size_t>(blockIdx.x) * 2 * D + e] = s;
   }
 }
@@ -441,7 +474,7 @@ __global__ void __launch_bounds__(1024)
 }  // namespace
 
 int norm_rope_bwd_grid(int B, int T) {
-  const long long want = (static_cast<long long>(B) * T + kWarps - 1) / kWarps;
+  const long long want = (static_cast<long long>(B) * T + kBwdWarps - 1) / kBwdWarps;
   return static_cast<int>(want < kBwdMaxGrid ? want : kBwdMaxGrid);
 }
 
@@ -453,9 +486,9 @@ cudaError_t launch_norm_rope_bwd(const NormRopeBwdParams& p, int D, cudaStream_t
   const int grid = norm_rope_bwd_grid(p.B, p.T);
   if (grid > 0 && p.nq + p.nk + p.nv > 0) {
     if (D == 64)
-      norm_rope_bwd_kernel<64><<<grid, kThreads, 0, stream>>>(p);
+      norm_rope_bwd_kernel<64><<<grid, kBwdThreads, 0, stream>>>(p);
     else
-      norm_rope_bwd_kernel<128><<<grid, kThreads, 0, stream>>>(p);
+      norm_rope_bwd_kernel<128><<<grid, kBwdThreads, 0, stream>>>(p);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (p.dwq == nullptr && p.dwk == nullptr)) return e;
