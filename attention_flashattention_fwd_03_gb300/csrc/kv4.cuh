@@ -48,7 +48,10 @@ struct Kv4 {
 // are zero, so the bf16 is the high half.
 __device__ __forceinline__ uint32_t kv4_scale_bits(uint32_t amax_bits) {
   if (amax_bits >= 0x7f80u) return 0x7fc00000u;
-  const uint32_t t = __float_as_uint(__fdiv_rn(__uint_as_float(amax_bits << 16), 7.f));
+  // a product with fp32(1 / 7) rounds to the same 5 bits as the quotient for each of the 128
+  // significands of a bf16; subnormal quotients take the division
+  const float a = __uint_as_float(amax_bits << 16);
+  const uint32_t t = __float_as_uint(amax_bits >= 0x0400u ? a * (1.f / 7.f) : __fdiv_rn(a, 7.f));
   return (t + 0x3ffffu + ((t >> 19) & 1u)) & 0xfff80000u;  // 1 + 4 mantissa bits
 }
 

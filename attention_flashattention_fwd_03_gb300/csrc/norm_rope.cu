@@ -29,16 +29,19 @@ constexpr int kCtasPerSm = 32;
 __device__ __forceinline__ uint2 ld8(const uint16_t* p) { return *reinterpret_cast<const uint2*>(p); }
 __device__ __forceinline__ void st8(uint16_t* p, uint2 v) { *reinterpret_cast<uint2*>(p) = v; }
 
-// Table entries of the lane's four planes (1 and 0 for a lane that does not rotate).
-__device__ __forceinline__ void load_planes(const RopeParams& r, int pos, int l, bool rotates,
-                                            float4& co, float4& si) {
-  co = make_float4(1.f, 1.f, 1.f, 1.f);
-  si = make_float4(0.f, 0.f, 0.f, 0.f);
+// Table entries of the lane's four planes (1 and 0 for a lane that does not rotate);
+// BACK: of the transposed rotation.
+template <bool BACK>
+__device__ __forceinline__ Planes load_planes(const RopeParams& r, int pos, int l, bool rotates) {
+  float4 co = make_float4(1.f, 1.f, 1.f, 1.f), si = make_float4(0.f, 0.f, 0.f, 0.f);
   if (rotates) {
     const float* row = r.cos_sin + static_cast<size_t>(pos) * r.rot;
     co = *reinterpret_cast<const float4*>(row + 4 * l);
     si = *reinterpret_cast<const float4*>(row + r.rot / 2 + 4 * l);
   }
+  const float f = BACK ? -1.f : 1.f;
+  return Planes{{make_float2(co.x, co.y), make_float2(co.z, co.w)},
+                {make_float2(f * si.x, f * si.y), make_float2(f * si.z, f * si.w)}};
 }
 
 // Quantises one row of D bf16 (the lane's 8 channels from 8 l on, packed) into a chunk
@@ -82,7 +85,7 @@ constexpr int kUnroll = 4;  // passes whose loads are in flight together
 // What the rows of one token share.
 struct TokenCtx {
   LaneChannels ch;
-  float4 co, si;
+  Planes planes;
   int l, sub;       // lane within its row, row within the pass
   int interleaved;
   float eps;
@@ -101,10 +104,8 @@ __device__ __forceinline__ void norm_rope_rows(const TokenCtx& t, const uint16_t
                                                bool write) {
   constexpr int LANES = D / 8;
   constexpr int ROWS = 32 / LANES;
-  float wf[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) wf[i] = 1.f;
-  if (w) widen8(ld8(w + t.ch.c0), ld8(w + t.ch.c1), wf);
+  Lane8 wf{};
+  if (w) wf = widen8(ld8(w + t.ch.c0), ld8(w + t.ch.c1));
   for (int r0 = h0; r0 < h1; r0 += ROWS * kUnroll) {
     uint2 a[kUnroll], c[kUnroll];
 #pragma unroll
@@ -120,14 +121,12 @@ __device__ __forceinline__ void norm_rope_rows(const TokenCtx& t, const uint16_t
     for (int u = 0; u < kUnroll; ++u) {
       if (r0 + u * ROWS >= h1) break;
       const int h = r0 + u * ROWS + t.sub;
-      float v[8];
-      widen8(a[u], c[u], v);
+      Lane8 v = widen8(a[u], c[u]);
       if (w) {
-        const float r = row_rrms<D>(v, t.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * r * wf[i];
+        const float r = rsqrtf(row_sum<LANES>(dot8(v, v)) * (1.f / D) + t.eps);
+        v = mul8(scale8(v, r), wf);
       }
-      if (t.ch.rotates) rotate8<false>(v, t.co, t.si, t.interleaved);
+      if (t.ch.rotates) rotate8(v, t.planes, t.interleaved);
       round8(v, a[u], c[u]);
       if (!t.live) a[u] = c[u] = make_uint2(kBf16NanPair, kBf16NanPair);
       if constexpr (QUANT) {
@@ -235,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
       if (PAGED) t.write_kv = false;
     }
   }
-  load_planes(p.rope, pos, t.l, t.ch.rotates && t.live, t.co, t.si);
+  t.planes = load_planes<false>(p.rope, pos, t.l, t.ch.rotates && t.live);
 
   // ---- this warp's share of the token's query, key and value rows ----
   const int rows = p.nq + p.nk + p.nv;
@@ -328,11 +327,11 @@ template <int D>
 __device__ __forceinline__ void norm_rope_bwd_rows(const TokenCtx& t, const uint16_t* g,
                                                    long long gh, const uint16_t* x, long long sh,
                                                    const uint16_t* w, int heads, uint16_t* dx,
-                                                   long long dh, float (&dw)[8]) {
+                                                   long long dh, Lane8& dw) {
   constexpr int LANES = D / 8;
   constexpr int ROWS = 32 / LANES;
-  float wf[8];
-  if (w) widen8(ld8(w + t.ch.c0), ld8(w + t.ch.c1), wf);
+  Lane8 wf{};
+  if (w) wf = widen8(ld8(w + t.ch.c0), ld8(w + t.ch.c1));
   for (int r0 = 0; r0 < heads; r0 += ROWS * kBwdUnroll) {
     uint2 ga[kBwdUnroll], gc[kBwdUnroll], xa[kBwdUnroll], xc[kBwdUnroll];
 #pragma unroll
@@ -352,29 +351,22 @@ __device__ __forceinline__ void norm_rope_bwd_rows(const TokenCtx& t, const uint
     for (int u = 0; u < kBwdUnroll; ++u) {
       if (r0 + u * ROWS >= heads) break;
       const int h = r0 + u * ROWS + t.sub;
-      float v[8];
-      widen8(ga[u], gc[u], v);
-      if (t.ch.rotates) rotate8<true>(v, t.co, t.si, t.interleaved);
+      Lane8 v = widen8(ga[u], gc[u]);
+      if (t.ch.rotates) rotate8(v, t.planes, t.interleaved);
       if (w) {
-        float xh[8];
-        widen8(xa[u], xc[u], xh);
+        const Lane8 x8 = widen8(xa[u], xc[u]);
+        const Lane8 vw = mul8(v, wf);
         // both sums of the row at once: x^2 and (dy w) x
-        float ss = 0.f, dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(xh[i], xh[i], ss);
-          dot = fmaf(v[i] * wf[i], xh[i], dot);
-        }
-        ss = row_sum<LANES>(ss);
-        dot = row_sum<LANES>(dot);
+        const float ss = row_sum<LANES>(dot8(x8, x8)), dot = row_sum<LANES>(dot8(vw, x8));
         const float r = rsqrtf(ss * (1.f / D) + t.eps);
-        const float mean = dot * r * (1.f / D);
+        const float m = -dot * r * (1.f / D);
+        const Lane8 xh = scale8(x8, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          xh[i] *= r;
-          dw[i] = fmaf(v[i], xh[i], dw[i]);  // 0 for a row past the end: its g is 0
-          v[i] = r * (v[i] * wf[i] - xh[i] * mean);
+        for (int i = 0; i < 4; ++i) {
+          dw.v[i] = __ffma2_rn(v.v[i], xh.v[i], dw.v[i]);  // 0 for a row past the end: its g is 0
+          v.v[i] = __ffma2_rn(xh.v[i], make_float2(m, m), vw.v[i]);
         }
+        v = scale8(v, r);
       }
       round8(v, ga[u], gc[u]);
       if (!t.live) ga[u] = gc[u] = make_uint2(kBf16NanPair, kBf16NanPair);
@@ -401,9 +393,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const Nor
   // a unit of work is one operand of one token, so that the warps end together
   const long long units = static_cast<long long>(p.B) * p.T * 3;
   const long long gh = static_cast<long long>(p.T) * D;
-  float dwq[8], dwk[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
+  Lane8 dwq{}, dwk{};
 
   for (long long unit = static_cast<long long>(blockIdx.x) * kBwdWarps + warp; unit < units;
        unit += static_cast<long long>(gridDim.x) * kBwdWarps) {
@@ -420,7 +410,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const Nor
         t.live = false;
       }
     }
-    load_planes(p.rope, pos, t.l, t.ch.rotates && t.live, t.co, t.si);
+    t.planes = load_planes<true>(p.rope, pos, t.l, t.ch.rotates && t.live);
     auto grad = [&](const uint16_t* g, int heads) {
       return g + (static_cast<long long>(b) * heads * p.T + ti) * D;
     };
@@ -434,16 +424,16 @@ __global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const Nor
     if (op == 2 && p.nv > 0)
       value_rows<D, false>(t, grad(p.gv, p.nv), gh, 0, p.nv, at(p.dv), p.dv.sh, nullptr, true);
     if (!t.live) {  // a gradient through an unknown rotation is unknown
-#pragma unroll
-      for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = __int_as_float(0x7fc00000);
+      const float nan = __int_as_float(0x7fc00000);
+      dwq = dwk = Lane8{{{nan, nan}, {nan, nan}, {nan, nan}, {nan, nan}}};
     }
   }
   if (p.part == nullptr) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int c = i < 4 ? t.ch.c0 + i : t.ch.c1 + i - 4;
-    red[warp * ROWS + t.sub][0][c] = dwq[i];
-    red[warp * ROWS + t.sub][1][c] = dwk[i];
+    red[warp * ROWS + t.sub][0][c] = (i & 1) ? dwq.v[i / 2].y : dwq.v[i / 2].x;
+    red[warp * ROWS + t.sub][1][c] = (i & 1) ? dwk.v[i / 2].y : dwk.v[i / 2].x;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < 2 * D; e += kBwdThreads) {

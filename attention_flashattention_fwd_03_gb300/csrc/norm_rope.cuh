@@ -46,15 +46,43 @@ __device__ __forceinline__ LaneChannels lane_channels(int l, int rot, int interl
   return c;
 }
 
-// Eight packed bf16 of a lane (two runs of 4) -> fp32.
-__device__ __forceinline__ void widen8(uint2 a, uint2 b, float (&x)[8]) {
-  x[0] = bf16_lo(a.x), x[1] = bf16_hi(a.x), x[2] = bf16_lo(a.y), x[3] = bf16_hi(a.y);
-  x[4] = bf16_lo(b.x), x[5] = bf16_hi(b.x), x[6] = bf16_lo(b.y), x[7] = bf16_hi(b.y);
+// A lane's eight channels as fp32 pairs, for the packed fp32x2 instructions: the first
+// run of 4 in v[0], v[1], the second in v[2], v[3].
+struct Lane8 {
+  float2 v[4];
+};
+
+__device__ __forceinline__ float2 widen2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+
+__device__ __forceinline__ Lane8 widen8(uint2 a, uint2 b) {
+  return Lane8{{widen2(a.x), widen2(a.y), widen2(b.x), widen2(b.y)}};
 }
 
-__device__ __forceinline__ void round8(const float (&x)[8], uint2& a, uint2& b) {
-  a = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-  b = make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ void round8(const Lane8& x, uint2& a, uint2& b) {
+  a = make_uint2(pack_bf16x2(x.v[0].x, x.v[0].y), pack_bf16x2(x.v[1].x, x.v[1].y));
+  b = make_uint2(pack_bf16x2(x.v[2].x, x.v[2].y), pack_bf16x2(x.v[3].x, x.v[3].y));
+}
+
+__device__ __forceinline__ Lane8 mul8(const Lane8& x, const Lane8& y) {
+  Lane8 z;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z.v[i] = __fmul2_rn(x.v[i], y.v[i]);
+  return z;
+}
+
+__device__ __forceinline__ Lane8 scale8(const Lane8& x, float f) {
+  Lane8 z;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z.v[i] = __fmul2_rn(x.v[i], make_float2(f, f));
+  return z;
+}
+
+// This lane's part of the dot product of two rows.
+__device__ __forceinline__ float dot8(const Lane8& x, const Lane8& y) {
+  float2 s = __fmul2_rn(x.v[0], y.v[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = __ffma2_rn(x.v[i], y.v[i], s);
+  return s.x + s.y;
 }
 
 // Sum over the LANES lanes that share a row; every lane gets the same bits.
@@ -65,31 +93,27 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// 1 / rms of a row from this lane's 8 channels.
-template <int D>
-__device__ __forceinline__ float row_rrms(const float (&x)[8], float eps) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
-  return rsqrtf(row_sum<D / 8>(s) * (1.f / D) + eps);
-}
+// cos and sin of a lane's four planes (BACK: of the transposed rotation).
+struct Planes {
+  float2 c[2], s[2];
+};
 
-// Turns the lane's four planes by cos / sin (BACK: by the transpose).
-template <bool BACK>
-__device__ __forceinline__ void rotate8(float (&x)[8], float4 co, float4 si, int interleaved) {
-  const float c[4] = {co.x, co.y, co.z, co.w};
-  const float s[4] = {si.x, si.y, si.z, si.w};
+// Turns the lane's four planes.
+__device__ __forceinline__ void rotate8(Lane8& x, const Planes& p, int interleaved) {
+  if (!interleaved) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float sn = BACK ? -s[i] : s[i];
-    if (interleaved) {
-      const float a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = a * c[i] - b * sn;
-      x[2 * i + 1] = b * c[i] + a * sn;
-    } else {
-      const float a = x[i], b = x[4 + i];
-      x[i] = a * c[i] - b * sn;
-      x[4 + i] = b * c[i] + a * sn;
+    for (int i = 0; i < 2; ++i) {
+      const float2 a = x.v[i], b = x.v[2 + i];
+      const float2 ns = make_float2(-p.s[i].x, -p.s[i].y);
+      x.v[i] = __ffma2_rn(b, ns, __fmul2_rn(a, p.c[i]));
+      x.v[2 + i] = __ffma2_rn(a, p.s[i], __fmul2_rn(b, p.c[i]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float c = (i & 1) ? p.c[i / 2].y : p.c[i / 2].x, s = (i & 1) ? p.s[i / 2].y : p.s[i / 2].x;
+      const float a = x.v[i].x, b = x.v[i].y;
+      x.v[i] = make_float2(fmaf(b, -s, a * c), fmaf(a, s, b * c));
     }
   }
 }
