@@ -321,35 +321,8 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
 // 4-bit cache: warps 12-15 turn raw K and V tiles into bf16 slots, 32 keys each
 // ---------------------------------------------------------------------------
 
-// Eight codes u of one word (low nibble first) times a scale pair (s, s; bf16 bits): the
-// bf16 values (u - 8) s / 64 in channel order.  A code alone in 16 bits is the subnormal
-// bf16 u 2^-133; one fused multiply-add makes it (u - 8) / 64 and one product scales it,
-// both exact.  The factor 64 goes into the softmax scale for keys and into 1 / l for
-// values, where it is exact too.  (The other way, 128 + u by an OR into the mantissa, then
-// - 136, times s, delivers channels i and i + 4 in one register and takes four more
-// permutes a word on the pipe that the softmax warps need: 784 us against 698 on the
-// 16 x 512 workload.)
-__device__ __forceinline__ uint4 dequantise_word(uint32_t w, uint32_t s_bits) {
-  const uint32_t big_bits = 0x7f007f00u, off_bits = 0xbe00be00u;  // 2^127, -2^-3
-  __nv_bfloat162 s, big, off;
-  memcpy(&s, &s_bits, 4);
-  memcpy(&big, &big_bits, 4);
-  memcpy(&off, &off_bits, 4);
-  const uint32_t lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
-  uint32_t v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // bytes: low code, its sign (0), high code, its sign
-    uint32_t u;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(u) : "r"(lo), "r"(hi), "r"(0xc480 + 0x1111 * i));
-    __nv_bfloat162 x;
-    memcpy(&x, &u, 4);
-    x = __hmul2(__hfma2(x, big, off), s);
-    memcpy(&v[i], &x, 4);
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
+// The tiles hold the cache's values / 64 (one operation a pair less, kv4.cuh): the factor
+// goes into the softmax scale for keys and into 1 / l for values, exactly.
 template <int D, Src SRC>
 __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SRC>& bar,
                              volatile int* abort) {
@@ -412,7 +385,7 @@ __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SR
                 kv == 0 ? w[g] : __byte_perm(w[g / 2], w[G / 2 + g / 2], (g & 1) ? 0x7632 : 0x5410);
             uint8_t* out = tile + ((g & 1) ? out1 : out0) + (g / 2) * C::BOX_BYTES + i * 1024;
             *reinterpret_cast<uint4*>(out) =
-                dequantise_word(word, __byte_perm(sc[g / 2], 0, (g & 1) ? 0x3232 : 0x1010));
+                kv4_values<1>(word, __byte_perm(sc[g / 2], 0, (g & 1) ? 0x3232 : 0x1010));
           }
         }
         fence_proxy_async_smem();

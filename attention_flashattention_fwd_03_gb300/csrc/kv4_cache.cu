@@ -15,18 +15,6 @@ namespace gbattn {
 
 namespace {
 
-// Eight codes (low nibble first) times a scale, as bf16.
-__device__ __forceinline__ uint4 dequantise8(uint32_t codes, float s) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = static_cast<float>(static_cast<int>((codes >> (8 * i)) & 15u) - 8) * s;
-    const float b = static_cast<float>(static_cast<int>((codes >> (8 * i + 4)) & 15u) - 8) * s;
-    w[i] = pack_bf16x2(a, b);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 template <int D>
 __global__ void __launch_bounds__(2 * D) paged_kv4_gather_kernel(const Gather4Params p) {
   using F = Kv4<D>;
@@ -53,7 +41,7 @@ __global__ void __launch_bounds__(2 * D) paged_kv4_gather_kernel(const Gather4Pa
     const int group = l >> 2, part = l & 3;
     auto scale = [&](int off) {
       const uint16_t* s = reinterpret_cast<const uint16_t*>(chunk + off + slot * F::kScaleRow);
-      return __uint_as_float(static_cast<uint32_t>(s[group]) << 16);
+      return s[group] * 0x10001u;
     };
     const uint32_t kc = reinterpret_cast<const uint32_t*>(
         chunk + F::kOffKCodes + slot * F::kCodeRow)[part * F::kGroups + group];
@@ -61,8 +49,8 @@ __global__ void __launch_bounds__(2 * D) paged_kv4_gather_kernel(const Gather4Pa
         reinterpret_cast<const uint16_t*>(chunk + F::kOffVCodes + slot * F::kCodeRow);
     const uint32_t vc = vrow[2 * part * F::kGroups + group] |
                         (static_cast<uint32_t>(vrow[(2 * part + 1) * F::kGroups + group]) << 16);
-    k4 = dequantise8(kc, scale(F::kOffKScales));
-    v4 = dequantise8(vc, scale(F::kOffVScales));
+    k4 = kv4_values<64>(kc, scale(F::kOffKScales));
+    v4 = kv4_values<64>(vc, scale(F::kOffVScales));
   }
   const size_t at = (static_cast<size_t>(rh) * p.max_seq_len + t) * D + 8 * l;
   *reinterpret_cast<uint4*>(p.k_out + at) = k4;

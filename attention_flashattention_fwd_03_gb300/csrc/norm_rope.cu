@@ -383,6 +383,8 @@ __global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const Nor
   constexpr int LANES = D / 8;
   constexpr int ROWS = 32 / LANES;
   __shared__ float red[kBwdWarps * ROWS][2][D];
+  // the sum over the partials may be scheduled now; it waits for this grid's results
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   TokenCtx t;
   t.l = lane % LANES;
@@ -448,6 +450,8 @@ __global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const Nor
 __global__ void __launch_bounds__(1024)
     norm_rope_dw_kernel(const float* part, int n, int D, float* dwq, float* dwk) {
   __shared__ float red[32][33];
+  // launched as a programmatic dependent: the partials are complete once this returns
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
   for (int i = threadIdx.y; i < n; i += 32) s += part[static_cast<size_t>(i) * 2 * D + c];
@@ -482,8 +486,17 @@ cudaError_t launch_norm_rope_bwd(const NormRopeBwdParams& p, int D, cudaStream_t
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (p.dwq == nullptr && p.dwk == nullptr)) return e;
-  norm_rope_dw_kernel<<<2 * D / 32, dim3(32, 32), 0, stream>>>(p.part, grid, D, p.dwq, p.dwk);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * D / 32);
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(p.part), grid, D,
+                            p.dwq, p.dwk);
 }
 
 }  // namespace gbattn
