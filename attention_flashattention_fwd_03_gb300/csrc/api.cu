@@ -129,33 +129,6 @@ FwdParams fwd_params(void* o, float* lse, int B, int Hq, int Hkv, int Tq, int Tk
   return p;
 }
 
-DecodeParams decode_params(const void* q, const int32_t* block_table, const int32_t* seq_lens,
-                           int num_seqs, int Hq, int Hkv, int D, int max_blocks_per_seq,
-                           int num_pool_blocks, int max_seq_len, float scale, void* o, float* lse,
-                           unsigned* flags) {
-  DecodeParams p{};
-  p.q = q;
-  p.block_table = block_table;
-  p.seq_lens = seq_lens;
-  p.o = o;
-  p.lse = lse;
-  p.S = num_seqs;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.D = D;
-  p.group = Hq / Hkv;
-  p.block_size = 16;
-  p.max_blocks = max_blocks_per_seq;
-  p.num_pool_blocks = num_pool_blocks;
-  p.max_seq_len = max_seq_len;
-  p.scale = scale;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.flags = flags;
-  p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
-  p.withhold_copy = g_withhold_copy.load(std::memory_order_relaxed);
-  return p;
-}
-
 }  // namespace gbattn
 
 using namespace gbattn;
@@ -310,16 +283,33 @@ GBATTN_API int paged_attn_decode(const void* q, const void* k_pool, const void* 
   if ((st = encode_bf16(enc, &tmK, k_pool, 2, dims, strides, box)) != ATTN_OK) return st;
   if ((st = encode_bf16(enc, &tmV, v_pool, 2, dims, strides, box)) != ATTN_OK) return st;
 
-  DecodeParams p = decode_params(q, block_table, seq_lens, num_seqs, Hq, Hkv, D,
-                                 max_blocks_per_seq, num_pool_blocks, max_seq_len, scale, o, lse,
-                                 ds->flags);
+  DecodeParams p;
+  p.q = q;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.o = o;
+  p.lse = lse;
   const DecodeWorkspace wl = decode_workspace_layout(num_seqs, Hq, D, max_seq_len);
   char* ws = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_lse = reinterpret_cast<float*>(ws + wl.off_part_lse);
   p.seg_first = reinterpret_cast<long long*>(ws + wl.off_seg_first);
   p.plan = reinterpret_cast<long long*>(ws + wl.off_plan);
+  p.S = num_seqs;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.group = Hq / Hkv;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_pool_blocks = num_pool_blocks;
+  p.max_seq_len = max_seq_len;
   p.max_pieces = decode_max_pieces(max_seq_len);
+  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.flags = ds->flags;
+  p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  p.withhold_copy = g_withhold_copy.load(std::memory_order_relaxed);
   if (launch_paged_decode(tmK, tmV, p, ds->num_sms, static_cast<cudaStream_t>(stream)) !=
       cudaSuccess)
     return ATTN_ERR_CUDA;

@@ -44,12 +44,6 @@ constexpr uint64_t kMaxDim = 1ull << 31;  // keeps every TMA coordinate inside i
 extern std::atomic<unsigned long long> g_wait_limit_ns;  // limit of every wait in the kernels
 extern std::atomic<int> g_withhold_copy;
 
-// Parameters of a paged decode but for its workspace.
-DecodeParams decode_params(const void* q, const int32_t* block_table, const int32_t* seq_lens,
-                           int num_seqs, int Hq, int Hkv, int D, int max_blocks_per_seq,
-                           int num_pool_blocks, int max_seq_len, float scale, void* o, float* lse,
-                           unsigned* flags);
-
 FwdParams fwd_params(void* o, float* lse, int B, int Hq, int Hkv, int Tq, int Tk, int D,
                      int causal, float scale, unsigned* flags);
 

@@ -377,21 +377,38 @@ GBATTN_API int paged_kv4_attn_decode(const void* q, const void* kv_pool,
   const Kv4DecodeWorkspace wl = kv4_decode_workspace(num_seqs, Hq, Hkv, D, max_seq_len);
   if (workspace_bytes < wl.bytes) return ATTN_ERR_INVALID_ARG;
   if (static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim ||
-      static_cast<uint64_t>(num_seqs) * Hq >= kMaxDim ||
-      static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim)
+      static_cast<uint64_t>(num_seqs) * Hq >= kMaxDim / 2 ||
+      static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim ||
+      static_cast<uint64_t>(kv4_max_steps(num_seqs, Hkv, max_seq_len)) >= kMaxDim)
     return ATTN_ERR_UNSUPPORTED;
   DeviceState* ds = nullptr;
   const int st = device_state(&ds);
   if (st != ATTN_OK) return st;
-  DecodeParams p = decode_params(q, block_table, seq_lens, num_seqs, Hq, Hkv, D,
-                                 max_blocks_per_seq, num_pool_blocks, max_seq_len, scale, o, lse,
-                                 ds->flags);
+  Kv4DecodeParams p{};
+  p.q = q;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.o = o;
+  p.lse = lse;
   char* ws = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_lse = reinterpret_cast<float*>(ws + wl.off_part_lse);
-  p.seg_first = reinterpret_cast<long long*>(ws + wl.off_seg_first);
-  p.plan = reinterpret_cast<long long*>(ws + wl.off_plan);
+  p.seg_first = reinterpret_cast<int*>(ws + wl.off_seg_first);
+  p.seg_last = reinterpret_cast<int*>(ws + wl.off_seg_last);
+  p.S = num_seqs;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.group = Hq / Hkv;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_pool_blocks = num_pool_blocks;
+  p.max_seq_len = max_seq_len;
   p.max_pieces = static_cast<int>(wl.pieces);
+  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.flags = ds->flags;
+  p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  p.withhold_copy = g_withhold_copy.load(std::memory_order_relaxed);
   return launch_kv4_decode(static_cast<const uint8_t*>(kv_pool), p, ds->num_sms,
                            static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ATTN_OK

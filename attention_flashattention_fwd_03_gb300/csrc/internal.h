@@ -56,7 +56,6 @@ struct DecodeParams {
   int num_pool_blocks;
   int max_seq_len;
   int max_pieces;              // bound on the pieces of one (request, KV head) segment
-                               // (4-bit cache: of the batch)
   float scale;
   float scale_log2;
   unsigned* flags;             // device flag word (DEVFLAG_*)
@@ -81,17 +80,38 @@ cudaError_t launch_paged_decode(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                 const DecodeParams& p, int num_sms, cudaStream_t stream);
 cudaError_t prepare_paged_decode();
 
-// Decode over the 4-bit pool [num_pool_blocks, Hkv, 18 D] (kv4.cuh).  Its workspace:
-// part_o [pieces, group, D], part_lse [pieces, group], seg_first [S, Hkv], plan [2]; in
-// DecodeParams max_pieces is the number of pieces of the whole batch.
-constexpr int kKv4MaxRanges = 2048;  // warp ranges of one launch (152 SMs x 12 warps and some)
+struct Kv4DecodeParams {
+  const void* q;               // [S, Hq, D] bf16
+  const int32_t* block_table;  // [S, max_blocks]
+  const int32_t* seq_lens;     // [S]
+  void* o;                     // [S, Hq, D] bf16
+  float* lse;                  // [S, Hq] or nullptr
+  float* part_o;               // [pieces, group, D] fp32 (workspace)
+  float* part_lse;             // [pieces, group] fp32 (workspace)
+  int *seg_first, *seg_last;   // [S, Hkv] first and last range of each segment (workspace)
+  int S, Hq, Hkv, D, group;
+  int max_blocks;
+  int num_pool_blocks;
+  int max_seq_len;
+  int max_pieces;              // pieces the workspace holds
+  float scale;
+  float scale_log2;
+  unsigned* flags;             // device flag word (DEVFLAG_*)
+  unsigned long long wait_limit_ns;  // limit of every pipeline wait
+  int withhold_copy;           // test hook: the first copy of every warp is not issued
+};
+
+// Warp ranges of one 4-bit decode (152 SMs x 12 warps and some).
+constexpr int kKv4MaxRanges = 2048;
 struct Kv4DecodeWorkspace {
   long long pieces;
-  size_t off_part_lse, off_seg_first, off_plan, bytes;
+  size_t off_part_lse, off_seg_first, off_seg_last, bytes;  // part_o at 0
 };
 Kv4DecodeWorkspace kv4_decode_workspace(int S, int Hq, int Hkv, int D, int max_seq_len);
-long long kv4_max_ranges(int S, int Hkv, int max_seq_len);  // ranges a launch may use
-cudaError_t launch_kv4_decode(const uint8_t* pool, const DecodeParams& p, int num_sms,
+long long kv4_max_steps(int S, int Hkv, int max_seq_len);  // steps of 64 tokens of a batch
+
+// Decode over the 4-bit pool [num_pool_blocks, Hkv, 18 D] (kv4.cuh).
+cudaError_t launch_kv4_decode(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms,
                               cudaStream_t stream);
 cudaError_t prepare_kv4_decode();
 

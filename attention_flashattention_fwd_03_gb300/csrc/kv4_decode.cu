@@ -23,11 +23,12 @@
 // maximum only moves when it grows by more than 2^8, so outputs are rarely rescaled; p
 // stays below 2^8.
 //
-// Bound by HBM: a token and KV head take 9 D / 8 bytes, read once.  Every warp streams a
-// range of the batch's blocks by itself (decode_split.cuh): lane j of the warp copies
-// block j of a step, one untiled bulk copy of the whole chunk (codes and scales of K and
-// V), into the warp's own ring in shared memory; the table entries of a step are read one
-// step ahead of its copies.  The fragments of m16n8k16 come out of shared memory by plain
+// Bound by HBM: a token and KV head take 9 D / 8 bytes, read once.  The batch is one
+// sequence of steps, 64 tokens (4 blocks) of one (request, KV head) each, request-major;
+// it is cut into equal ranges, and every warp streams a range by itself: lane j of the
+// warp copies block j of a step, one untiled bulk copy of the whole chunk (codes and
+// scales of K and V), into the warp's own ring in shared memory; the table entries of a
+// step are read one step ahead of its copies.  The fragments of m16n8k16 come out of shared memory by plain
 // loads in the order the format lays down.
 //
 // The shortest range is one step, so that a small batch spreads over many SMs; ranges are
@@ -38,7 +39,6 @@
 // pieces in turn.
 #include <cuda_runtime.h>
 
-#include "decode_split.cuh"
 #include "internal.h"
 #include "kv4.cuh"
 #include "norm_rope.cuh"
@@ -75,6 +75,16 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
         "f"(c3));
+}
+
+// D = A * B + D, m16n8k16, bf16 inputs, fp32 accumulators.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // Transposes an 8 x 8 matrix of 16-bit values held across the warp.
@@ -128,19 +138,37 @@ __device__ __forceinline__ float scale_of(const uint32_t (&r)[N], int w) {
   return (w & 1) ? bf16_hi(r[w >> 1]) : bf16_lo(r[w >> 1]);
 }
 
-// One step: up to kStepBlocks consecutive blocks of one (request, KV head).
+// Blocks per KV head of a request of L tokens; 0 for a length outside its bounds (the
+// merge kernel reports that request).
+__device__ __forceinline__ int blocks_of(const Kv4DecodeParams& p, int L) {
+  return (L < 0 || L > p.max_seq_len || L > p.max_blocks * kBS) ? 0 : (L + kBS - 1) / kBS;
+}
+
+__device__ __forceinline__ int steps_of(int blocks) { return (blocks + kStepBlocks - 1) / kStepBlocks; }
+
+// A step of the batch: step i of request r, KV head h, whose segment has nb blocks.
 struct Step {
-  int r, h, b, n;
+  int r, h, i, nb;
+  __device__ int blocks() const { return min(kStepBlocks, nb - i * kStepBlocks); }
+  __device__ bool last() const { return (i + 1) * kStepBlocks >= nb; }
 };
 
-// The step at the cursor, no longer than the segment and `left` blocks allow.
-__device__ __forceinline__ Step step_at(const Cursor& c, int left) {
-  return Step{c.r, c.h, c.b, min(kStepBlocks, min(c.nb - c.b, left))};
+// The next step of the batch; r stops at S, should the lengths have changed.
+__device__ __forceinline__ void advance(Step& s, const Kv4DecodeParams& p) {
+  if (!s.last()) {
+    ++s.i;
+    return;
+  }
+  s.i = 0;
+  if (++s.h < p.Hkv) return;
+  s.h = 0;
+  s.nb = 0;
+  while (s.nb == 0 && ++s.r < p.S) s.nb = blocks_of(p, p.seq_lens[s.r]);
 }
 
 template <int D, int NQT>
 __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
-    kv4_decode_split_kernel(const uint8_t* __restrict__ pool, const DecodeParams p) {
+    kv4_decode_split_kernel(const uint8_t* __restrict__ pool, const Kv4DecodeParams p) {
   using F = Kv4<D>;
   using C = Shape<D, NQT>;
   constexpr int G = F::kGroups;
@@ -166,48 +194,43 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   // the preceding kernel's writes (an append's) are complete and visible past this point
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // ---------------- plan: total blocks, range count, this warp's range ----------------
-  long long nbr = 0;
+  // ---------------- plan: total steps, range count, this warp's range ----------------
+  int total = 0;
   for (int r0 = 0; r0 < p.S; r0 += 32)
-    if (r0 + lane < p.S) nbr += blocks_of(p, p.seq_lens[r0 + lane]);
+    if (r0 + lane < p.S) total += steps_of(blocks_of(p, p.seq_lens[r0 + lane]));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) nbr += __shfl_xor_sync(0xffffffffu, nbr, o);
-  const long long NB = nbr * p.Hkv;
-  const long long w_cap = static_cast<long long>(gridDim.x) * kWarps;
-  const int W = NB == 0 ? 0 : static_cast<int>(max(1ll, min(w_cap, NB / kStepBlocks)));
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= p.Hkv;  // below 2^31 for every length within max_seq_len
+  const int W = min(static_cast<int>(gridDim.x) * kWarps, total);
   const int k_w = warp * gridDim.x + blockIdx.x;
-  if (k_w == 0 && lane == 0) {
-    p.plan[0] = NB;
-    p.plan[1] = W;
-  }
   if (k_w >= W) return;  // warps are independent: no barrier of the CTA follows
-  const long long lo = k_w * NB / W;
-  const int n_w = static_cast<int>((k_w + 1) * NB / W - lo);
-  Cursor at{0, 0, 0, 0, 1};
+  const int share = total / W, extra = total - share * W;  // the first `extra` take one more
+  const int lo = k_w * share + min(k_w, extra);
+  const int n_w = share + (k_w < extra ? 1 : 0);
+  Step at{0, 0, 0, 0};
   {
-    long long before = 0;  // blocks of requests r0 - 1 and earlier
+    int before = 0;  // steps of requests r0 - 1 and earlier
     bool found = false;
     for (int r0 = 0; r0 < p.S && !found; r0 += 32) {
       const int r = r0 + lane;
       const int nb = r < p.S ? blocks_of(p, p.seq_lens[r]) : 0;
-      long long incl = static_cast<long long>(nb) * p.Hkv;
+      const int own = steps_of(nb) * p.Hkv;
+      int incl = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
       incl += before;
-      const long long excl = incl - static_cast<long long>(nb) * p.Hkv;
-      const unsigned hit = __ballot_sync(0xffffffffu, nb > 0 && excl <= lo && lo < incl);
+      const unsigned hit = __ballot_sync(0xffffffffu, incl - own <= lo && lo < incl);
       if (hit) {
         found = true;
         const int src = __ffs(hit) - 1;
-        const long long e = __shfl_sync(0xffffffffu, excl, src);
+        const int rest = lo - __shfl_sync(0xffffffffu, incl - own, src);
         at.nb = __shfl_sync(0xffffffffu, nb, src);
         at.r = r0 + src;
-        at.h = static_cast<int>((lo - e) / at.nb);
-        at.b = static_cast<int>((lo - e) % at.nb);
-        at.first = e + static_cast<long long>(at.h) * at.nb;
+        at.h = rest / steps_of(at.nb);
+        at.i = rest - at.h * steps_of(at.nb);
       }
       before = __shfl_sync(0xffffffffu, incl, 31);
     }
@@ -215,38 +238,37 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   }
 
   // ---------------- copies: one step ahead in table entries, kStages in data ----------------
-  Cursor pc = at;
-  int p_left = n_w, issued = 0;
+  Step ps = at;
+  int p_left = n_w, issued = 0, p_stage = 0;
   const uint64_t policy = l2_policy_evict_first();  // every cache byte is read once
-  Step ps = step_at(pc, p_left);
-  auto entry = [&](const Step& s) -> int {
-    return lane < s.n ? p.block_table[static_cast<size_t>(s.r) * p.max_blocks + s.b + lane] : 0;
+  auto entry = [&]() -> int {
+    return lane < ps.blocks()
+               ? p.block_table[static_cast<size_t>(ps.r) * p.max_blocks + ps.i * kStepBlocks + lane]
+               : 0;
   };
-  int phys = entry(ps);
+  int phys = entry();
   uint32_t stage_bad = 0;  // bit s: stage s holds a block the table could not translate
   auto issue = [&]() {     // copies step ps, then reads the table entries of the next one
-    const int s = issued % C::kStages;
-    const bool bad = lane < ps.n && (phys < 0 || phys >= p.num_pool_blocks);
+    const int s = p_stage, n = ps.blocks();
+    const bool bad = lane < n && (phys < 0 || phys >= p.num_pool_blocks);
     if (bad) raise_flag(p.flags, DEVFLAG_BAD_BLOCK);
     stage_bad = (stage_bad & ~(1u << s)) | (__any_sync(0xffffffffu, bad) ? 1u << s : 0u);
     if (!(p.withhold_copy && issued == 0)) {  // test hook: the first step never arrives
-      if (lane == 0) mbar_arrive_expect_tx(bars + 8 * s, ps.n * F::kChunk);
+      if (lane == 0) mbar_arrive_expect_tx(bars + 8 * s, n * F::kChunk);
       __syncwarp();
-      if (lane < ps.n)
+      if (lane < n)
         bulk_load_hint(ring_addr + s * C::kStageBytes + lane * F::kChunk,
                        pool + (static_cast<size_t>(bad ? 0 : phys) * p.Hkv + ps.h) * F::kChunk,
                        F::kChunk, bars + 8 * s, policy);
     }
     ++issued;
-    p_left -= ps.n;
-    if (p_left > 0) {
-      advance(pc, ps.n, p);
-      if (pc.r >= p.S) {
+    p_stage = s + 1 == C::kStages ? 0 : s + 1;
+    if (--p_left > 0) {
+      advance(ps, p);
+      if (ps.r >= p.S)
         p_left = 0;  // lengths changed under the kernel: nothing valid to read
-      } else {
-        ps = step_at(pc, p_left);
-        phys = entry(ps);
-      }
+      else
+        phys = entry();
     }
   };
 #pragma unroll 1
@@ -261,14 +283,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   float sl2[NQT][2], sl[NQT][2];     // softmax scale (times log2 e) over the query's 2^x
   float m_q[NQT][2], l_q[NQT][2];
   float acc[D / 16][NQT][4];         // O^T / 64: channels 32 w + 4 g + 2 x (+ 1) of tile 2 w + x
-  Cursor c = at;
-  int c_left = n_w, taken = 0, L = 0, piece_b0 = 0;
+  Step c = at;
+  int c_left = n_w, taken = 0, c_stage = 0, L = 0;
+  uint32_t phase = 0;
   bool pbad = false, ok = true;
 
   auto begin_piece = [&]() {
     L = p.seq_lens[c.r];
-    piece_b0 = c.b;
     pbad = false;
+    if (c.i == 0 && lane == 0) p.seg_first[c.r * p.Hkv + c.h] = k_w;
     const uint16_t* q =
         static_cast<const uint16_t*>(p.q) + (static_cast<size_t>(c.r) * p.Hq + c.h * group) * D;
     // A fragment of -8 in both forms of a code
@@ -323,9 +346,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   begin_piece();
 
   while (c_left > 0) {
-    const int s = taken % C::kStages;
-    const Step st = step_at(c, c_left);
-    if (!mbar_wait_warp(bars + 8 * s, (taken / C::kStages) & 1, abort, p.flags, p.wait_limit_ns)) {
+    const int s = c_stage;
+    if (!mbar_wait_warp(bars + 8 * s, phase, abort, p.flags, p.wait_limit_ns)) {
       ok = false;
       break;
     }
@@ -333,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     const uint8_t* stage = ring + s * C::kStageBytes;
     // Valid tokens of the step.  The blocks past them are computed with whatever the stage
     // holds (codes are finite whatever their bits) and masked with the tail.
-    const int n_tok = min(kBS * st.n, L - st.b * kBS);
+    const int n_tok = min(kBS * kStepBlocks, L - c.i * (kBS * kStepBlocks));
 
     // ---- S^T = K Q^T, group by group ----
     float sc[kStepBlocks][NQT][4];
@@ -468,23 +490,28 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
                                    centre(cd8 & kHighNibbles, kHighFactor)};
 #pragma unroll
             for (int nt = 0; nt < NQT; ++nt)
-              mma_bf16_16816(acc[2 * (2 * u + x) + y][nt], a, pb[nt][0], pb[nt][1]);
+              mma_bf16(acc[2 * (2 * u + x) + y][nt], a, pb[nt][0], pb[nt][1]);
           }
         }
       }
     }
     __syncwarp();  // every lane has read the stage: the next step may be copied over it
     ++taken;
+    if (++c_stage == C::kStages) {
+      c_stage = 0;
+      phase ^= 1;
+    }
     if (p_left > 0) issue();
 
-    c_left -= st.n;
-    c.b += st.n;
-    if (c.b < c.nb && c_left > 0) continue;
+    --c_left;
+    if (!c.last() && c_left > 0) {
+      ++c.i;
+      continue;
+    }
     // ---- the piece ends: write its normalised O and LSE ----
     {
       const float nan = __int_as_float(0x7fc00000);
-      const long long seg = static_cast<long long>(c.r) * p.Hkv + c.h;
-      const long long piece = k_w + seg;
+      const int seg = c.r * p.Hkv + c.h, piece = k_w + seg;
       if (piece < p.max_pieces) {
 #pragma unroll
         for (int nt = 0; nt < NQT; ++nt) {
@@ -497,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
             const int q = 8 * nt + 2 * t4 + e;
             if (q >= group) continue;
             const float inv = pbad ? nan : 64.f / lsum;
-            const size_t base = piece * group + q;
+            const size_t base = static_cast<size_t>(piece) * group + q;
             float* dst = p.part_o + base * D + 4 * g;
 #pragma unroll
             for (int w = 0; w < G; ++w)
@@ -507,12 +534,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
             if (g == 0) p.part_lse[base] = pbad ? nan : m_q[nt][e] * sl[nt][e] + logf(lsum);
           }
         }
-        if (piece_b0 == 0 && lane == 0) p.seg_first[seg] = c.first;
+        if (c.last() && lane == 0) p.seg_last[seg] = k_w;
       }
     }
     if (c_left == 0) break;
     // the range continues in the next segment
-    advance(c, 0, p);
+    advance(c, p);
     if (c.r >= p.S) break;  // lengths changed under the kernel: nothing valid to read
     begin_piece();
   }
@@ -529,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
 constexpr int kMergeWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) kv4_decode_merge_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32) kv4_decode_merge_kernel(const Kv4DecodeParams p) {
   constexpr int PER = D / 32;  // dims per lane
   constexpr float kLog2e = 1.4426950408889634f;
   __shared__ float part[kMergeWarps][D];
@@ -540,21 +567,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv4_decode_merge_kernel(cons
   const int r = blockIdx.x / p.Hq, hq = blockIdx.x - r * p.Hq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kvh = hq / p.group;
-  const long long seg = static_cast<long long>(r) * p.Hkv + kvh;
-  const int L = p.seq_lens[r];
-  const long long NB = p.plan[0];
-  const int W = static_cast<int>(p.plan[1]);
-  const long long first = p.seg_first[seg];
-  const int nb = blocks_of(p, L);
-  const bool valid_len = L == 0 || nb > 0;
-  // (the plan always covers a valid nonempty request; the guard keeps every read in
-  // bounds should the lengths have changed between the two kernels)
-  const bool planned = nb > 0 && NB > 0 && W > 0 && first >= 0 && first + nb <= NB;
-  const int k0 = planned ? range_of(first, NB, W) : 0;
-  const int ns = planned ? range_of(first + nb - 1, NB, W) - k0 + 1 : 0;
-  const bool bad = !valid_len || (L > 0 && (ns < 1 || k0 + seg + ns > p.max_pieces));
-  const int n = bad ? 0 : ns;
-  const size_t base = static_cast<size_t>(k0 + seg) * p.group + (hq - kvh * p.group);
+  const int seg = r * p.Hkv + kvh;
+  const int L = p.seq_lens[r], k0 = p.seg_first[seg], k1 = p.seg_last[seg];
+  // (the split kernel has noted the ranges of every valid nonempty request; the check keeps
+  // every read in bounds should the lengths have changed between the two kernels)
+  const bool good = blocks_of(p, L) > 0 && k0 >= 0 && k0 <= k1 && k1 + seg < p.max_pieces;
+  const bool bad = L != 0 && !good;
+  const int n = good ? k1 - k0 + 1 : 0;
+  const size_t base = good ? static_cast<size_t>(k0 + seg) * p.group + (hq - kvh * p.group) : 0;
   const float* pl = p.part_lse + base;
   const float* po = p.part_o + base * D + lane * PER;
 
@@ -639,12 +659,14 @@ cudaError_t prepare() {
 }
 
 template <int D, int NQT>
-cudaError_t launch_split(const uint8_t* pool, const DecodeParams& p, int num_sms,
+cudaError_t launch_split(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms,
                          cudaStream_t stream) {
   // kCtasPerSm CTAs per SM, fewer when even the shortest ranges would not fill them
   const int ctas = num_sms * Shape<D, NQT>::kCtasPerSm;
   const int cap = ctas < kKv4MaxRanges / kWarps ? ctas : kKv4MaxRanges / kWarps;
-  const long long want = (kv4_max_ranges(p.S, p.Hkv, p.max_seq_len) + kWarps - 1) / kWarps;
+  // a CTA a range first, then more ranges a CTA (the kernel deals them in that order)
+  const long long steps = kv4_max_steps(p.S, p.Hkv, p.max_seq_len);
+  const long long want = steps < 1 ? 1 : (steps < num_sms ? steps : num_sms + (steps - num_sms) / kWarps);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -659,7 +681,7 @@ cudaError_t launch_split(const uint8_t* pool, const DecodeParams& p, int num_sms
 }
 
 template <int D>
-cudaError_t launch(const uint8_t* pool, const DecodeParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms, cudaStream_t stream) {
   const cudaError_t e = p.group <= 8 ? launch_split<D, 1>(pool, p, num_sms, stream)
                                      : launch_split<D, 2>(pool, p, num_sms, stream);
   if (e != cudaSuccess) return e;
@@ -677,21 +699,21 @@ cudaError_t launch(const uint8_t* pool, const DecodeParams& p, int num_sms, cuda
 
 }  // namespace
 
-long long kv4_max_ranges(int S, int Hkv, int max_seq_len) {
-  const long long blocks = static_cast<long long>(S) * Hkv * ((max_seq_len + kBS - 1) / kBS);
-  const long long n = blocks / kStepBlocks;
-  return n < 1 ? 1 : (n < kKv4MaxRanges ? n : kKv4MaxRanges);
+long long kv4_max_steps(int S, int Hkv, int max_seq_len) {
+  return static_cast<long long>(S) * Hkv *
+         ((max_seq_len + kBS * kStepBlocks - 1ll) / (kBS * kStepBlocks));
 }
 
 Kv4DecodeWorkspace kv4_decode_workspace(int S, int Hq, int Hkv, int D, int max_seq_len) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   Kv4DecodeWorkspace w;
-  w.pieces = kv4_max_ranges(S, Hkv, max_seq_len) + static_cast<long long>(S) * Hkv;
+  const long long steps = kv4_max_steps(S, Hkv, max_seq_len), segs = static_cast<long long>(S) * Hkv;
+  w.pieces = (steps < kKv4MaxRanges ? steps : kKv4MaxRanges) + segs;
   const size_t n = static_cast<size_t>(w.pieces) * (Hq / Hkv);
   w.off_part_lse = up(n * D * sizeof(float));
   w.off_seg_first = w.off_part_lse + up(n * sizeof(float));
-  w.off_plan = w.off_seg_first + up(static_cast<size_t>(S) * Hkv * sizeof(long long));
-  w.bytes = w.off_plan + up(2 * sizeof(long long));
+  w.off_seg_last = w.off_seg_first + up(static_cast<size_t>(segs) * sizeof(int));
+  w.bytes = w.off_seg_last + up(static_cast<size_t>(segs) * sizeof(int));
   return w;
 }
 
@@ -703,7 +725,7 @@ cudaError_t prepare_kv4_decode() {
   return prepare<128, 2>();
 }
 
-cudaError_t launch_kv4_decode(const uint8_t* pool, const DecodeParams& p, int num_sms,
+cudaError_t launch_kv4_decode(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms,
                               cudaStream_t stream) {
   if (p.S <= 0) return cudaSuccess;
   return p.D == 64 ? launch<64>(pool, p, num_sms, stream) : launch<128>(pool, p, num_sms, stream);
