@@ -19,13 +19,6 @@
 //                 tile's while this one is copied) and each copies its block's
 //                 16 rows (of the 4-bit cache: its block's codes and scales, into
 //                 a ring of raw half chunks)
-//   warps 12-15   4-bit cache: turn a raw K or V tile into the bf16 slot the MMA
-//                 warp reads, 32 keys each.  Every value n s is a bf16 exactly, so
-//                 these are the operands themselves, not an approximation of them.
-//                 On the 16 x 512 workload the 4-bit source takes 668 us where the
-//                 bf16 pools take 571; with the four warps passing the slots on
-//                 without work it is 610, so 39 us are the second hand-over and the
-//                 ring's missing slot, 58 the issue slots that the softmax warps lose
 //   warp 1        MMA warp (the converged warp runs the issue code; elect.sync
 //                 picks the lane that issues): S_i = Q_i K_j^T into TMEM (fp32),
 //                 then O_i += P_i V_j with P_i read from TMEM (tcgen05 A operand
@@ -38,6 +31,13 @@
 //                 P = 2^(c s - c m) as bf16 back into the S_i columns (c =
 //                 scale * log2 e folds the softmax scale into exp2), and at the
 //                 end writes O / l (bf16) and LSE = scale m + ln l.
+//   warps 12-15   4-bit cache: turn a raw K or V tile into the bf16 slot the MMA
+//                 warp reads, 32 keys each.  Every value n s is a bf16 exactly, so
+//                 these are the operands themselves, not an approximation of them.
+//                 On the 16 x 512 workload the 4-bit source takes 436 us where the
+//                 bf16 pools take 368 (398 with the four warps passing the slots on
+//                 without work: the second hand-over and the ring's missing slot; the
+//                 rest are issue slots that the softmax warps lose)
 // The two tiles ping-pong: while the softmax warps of one tile work, the tensor
 // core computes the other tile's S and P V.  The running max is only moved
 // (and O rescaled in TMEM) when a row's max grows by more than 2^8 in exp2
@@ -76,15 +76,15 @@ constexpr int kBS = 16;          // tokens per paged KV block
 template <Src SRC>
 constexpr int kThreads = SRC == Src::kPaged4 ? 512 : 384;
 constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by > 2^8
+constexpr int kMaxSorted = 384;  // (item, query pair) classes whose units are sorted by length
 // Registers per thread: the block launches with 168 (384 threads, one block per
 // SM); warpgroup 0 gives some up so the softmax warpgroups, which hold a whole
 // 128-key score row each, get more: 104 + 200 + 200 = 3 x 168.
 constexpr int kRegsLaunch = 168, kRegsWg0 = 104, kRegsSoftmax = 200;
 static_assert(kRegsWg0 + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split exceeds the launch");
-// With the dequantisers the block launches with 128: 88 + 40 + 192 + 192 = 4 x 128, the one
-// split of those tried that spills nothing (64 + 64: 698 us on the 16 x 512 workload, 80 +
-// 48: 691, this one: 668).
-constexpr int kRegsLaunch4 = 128, kRegsWg0With4 = 88, kRegsDequant = 40, kRegsSoftmax4 = 192;
+// With the dequantisers the block launches with 128: 80 + 48 + 192 + 192 = 4 x 128 (436 us
+// on the 16 x 512 workload; 72 + 56: 440, 88 + 40: 445, 96 + 32: 439).
+constexpr int kRegsLaunch4 = 128, kRegsWg0With4 = 80, kRegsDequant = 48, kRegsSoftmax4 = 192;
 static_assert(kRegsWg0With4 + kRegsDequant + 2 * kRegsSoftmax4 <= 4 * kRegsLaunch4,
               "register split exceeds the launch");
 
@@ -104,7 +104,11 @@ struct Cfg {
   static constexpr int OFF_BAR = OFF_RAW + NRAW * RAW_BYTES;
   static constexpr int NBAR = 2 + 2 * NSLOT + 6 + 1 + 2 * NRAW;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // + slack for 1024-byte alignment
+  // paged sources: tile counts and sorted order of the (item, query pair) classes
+  static constexpr int OFF_COST = OFF_MISC + 16;
+  static constexpr int OFF_ORDER = OFF_COST + (SRC == Src::kContiguous ? 0 : 2 * kMaxSorted);
+  static constexpr int OFF_END = OFF_ORDER + (SRC == Src::kContiguous ? 0 : 2 * kMaxSorted);
+  static constexpr int SMEM_BYTES = OFF_END + 1024;  // + slack for 1024-byte alignment
   static constexpr uint32_t TMEM_COLS = 512;
   // TMEM columns: S_0 [0,128), S_1 [128,256), O_0 and O_1 from 256 (D each).
   // P_i (bf16 pairs, 64 columns) overwrites the upper half of S_i.
@@ -112,6 +116,7 @@ struct Cfg {
   __device__ static constexpr uint32_t p_col(int i) { return 128u * i + 64u; }
   __device__ static constexpr uint32_t o_col(int i) { return 256u + static_cast<uint32_t>(D) * i; }
 };
+static_assert(kMaxSorted <= kThreads<Src::kPaged>, "a thread a class");
 static_assert(Cfg<128, Src::kPaged>::SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(Cfg<128, Src::kPaged4>::SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(Cfg<64, Src::kPaged4>::SMEM_BYTES <= 232448, "shared memory budget");
@@ -128,6 +133,7 @@ struct Bars {
   __device__ uint32_t s_free(int i) const { return base + 8 * (4 + 2 * C::NSLOT + i); }
   __device__ uint32_t p_full(int i) const { return base + 8 * (6 + 2 * C::NSLOT + i); }
   __device__ uint32_t teardown() const { return base + 8 * (8 + 2 * C::NSLOT); }
+  __device__ uint32_t order() const { return base - C::OFF_BAR + C::OFF_ORDER; }
   __device__ uint32_t raw_full(int s) const { return base + 8 * (9 + 2 * C::NSLOT + s); }
   __device__ uint32_t raw_empty(int s) const { return base + 8 * (9 + 2 * C::NSLOT + C::NRAW + s); }
 };
@@ -149,38 +155,54 @@ __device__ __forceinline__ int kv_end_of(int qpos, int L, const FwdParams& p) {
   return e < 0 ? 0 : (e > L ? L : e);
 }
 
-// Unit u: query-pair index decreasing (the longest causal rows first); within
-// one pair index, heads of a batch item are adjacent so heads that share K/V run
-// at the same time.
-__device__ __forceinline__ Unit unit_at(int u, const FwdParams& p, bool paged) {
-  const int BH = p.B * p.Hq;
-  const int qi = u / BH;
+// Keys of batch item b, and whether its key count is outside its bounds (then 0).
+__device__ __forceinline__ int keys_of(int b, const FwdParams& p, bool paged, bool& bad) {
+  bad = false;
+  if (!paged) return p.Tk;
+  const int L = p.kv_lens[b];
+  bad = L < 0 || L > p.max_kv_len || L > p.max_blocks * kBS;
+  return bad ? 0 : L;
+}
+
+// K/V tiles that query tile i of pair qp visits in an item of L keys.
+__device__ __forceinline__ int tiles_of(int qp, int i, int L, const FwdParams& p) {
+  const int r0 = 256 * qp + 128 * i;
+  if (r0 >= p.Tq) return 0;
+  return (kv_end_of(min(r0 + 127, p.Tq - 1), L, p) + BN - 1) / BN;
+}
+
+// Unit u.  Contiguous K and V: query-pair index decreasing (the longest causal rows
+// first); within one pair index, heads of a batch item are adjacent so heads that share
+// K/V run at the same time.  Paged, where the items' lengths differ: the list at `order`
+// in shared memory holds the classes (qi, b) by decreasing tile count, each with its heads
+// adjacent (batches of more classes than it holds keep the order of the items).  (On 16 items of
+// 1024 .. 8192 keys, 1024 units on 152 CTAs, the busiest CTA had 1.61 times the mean work
+// in the order of the items and has 1.04 times it in this one; bf16 pools 571 -> 368 us,
+// 4-bit 663 -> 438 us.)
+__device__ __forceinline__ Unit unit_at(int u, const FwdParams& p, bool paged,
+                                        uint32_t order) {
   Unit U;
-  U.bh = u - qi * BH;
+  int qi;
+  if (paged && p.B * p.n_qpairs <= kMaxSorted) {
+    const int i = u / p.Hq, h = u - i * p.Hq;
+    uint16_t cls;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(cls) : "r"(order + 2 * i));
+    qi = cls / p.B;
+    U.b = cls - qi * p.B;
+    U.bh = U.b * p.Hq + h;
+    U.kvh = h / p.group;
+  } else {
+    const int BH = p.B * p.Hq;
+    qi = u / BH;
+    U.bh = u - qi * BH;
+    U.b = U.bh / p.Hq;
+    U.kvh = (U.bh - U.b * p.Hq) / p.group;
+  }
   U.qp = p.n_qpairs - 1 - qi;
-  U.b = U.bh / p.Hq;
-  const int h = U.bh - U.b * p.Hq;
-  U.kvh = h / p.group;
   U.bkv = U.b * p.Hkv + U.kvh;
-  U.bad = false;
-  U.L = p.Tk;
-  if (paged) {
-    U.L = p.kv_lens[U.b];
-    if (U.L < 0 || U.L > p.max_kv_len || U.L > p.max_blocks * kBS) {
-      U.bad = true;
-      U.L = 0;
-    }
-  }
+  U.L = keys_of(U.b, p, paged, U.bad);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r0 = 256 * U.qp + 128 * i;
-    if (r0 >= p.Tq) {
-      U.n[i] = 0;
-    } else {
-      const int r1 = min(r0 + 127, p.Tq - 1);
-      U.n[i] = (kv_end_of(r1, U.L, p) + BN - 1) / BN;
-    }
-  }
+  for (int i = 0; i < 2; ++i) U.n[i] = tiles_of(U.qp, i, U.L, p);
   U.nkv = max(U.n[0], U.n[1]);
   return U;
 }
@@ -231,7 +253,7 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
   for (int r = 0; ok && r * static_cast<int>(gridDim.x) < p.num_units; ++r) {
     const int u = unit_of_round(r);
     if (u >= p.num_units) continue;
-    const Unit U = unit_at(u, p, PAGED);
+    const Unit U = unit_at(u, p, PAGED, bar.order());
     if (PAGED && U.bad && lane == 0) raise_flag(p.flags, DEVFLAG_BAD_SEQLEN);
     if (!mbar_wait_warp(bar.q_empty(), (uc & 1) ^ 1, abort, p.flags, lim)) { ok = false; break; }
     last_q_issued = !(p.withhold_copy && uc == 0);  // test hook: withhold the first Q
@@ -343,7 +365,7 @@ __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SR
   for (int r = 0; r * static_cast<int>(gridDim.x) < p.num_units; ++r) {
     const int u = unit_of_round(r);
     if (u >= p.num_units) continue;
-    const Unit U = unit_at(u, p, true);
+    const Unit U = unit_at(u, p, true, bar.order());
     for (int j = 0; j < U.nkv; ++j) {
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ++rc) {
@@ -354,8 +376,8 @@ __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SR
         const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW_BYTES;
         uint8_t* tile = smem + C::OFF_RING + s * C::TILE_BYTES;
         const int valid = U.L - j * BN;  // keys past the cache's end become zeros
-        // (unrolled by four, the two loops overflow the instruction cache beside the
-        // softmax code: 1042 us against 784)
+        // (small loops: unrolled by two they take 464 us against 436, as the code of the
+        // roles shares one instruction cache)
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
           const int key = part * 32 + 8 * i + row;
@@ -424,8 +446,8 @@ struct MmaWarp {
   int s_left = 0;        // S products of the unit not yet issued
   int zeroed_j = -1;     // paged: the unit's last V tile has had its dead rows cleared
 
-  __device__ MmaWarp(const FwdParams& p_, const Bars<D, SRC>& b_, volatile int* a_, uint32_t sbase,
-                     uint32_t tmem_)
+  __device__ MmaWarp(const FwdParams& p_, const Bars<D, SRC>& b_, volatile int* a_,
+                     uint32_t sbase, uint32_t tmem_)
       : p(p_), bar(b_), abort(a_), sR(sbase + C::OFF_RING), tmem(tmem_),
         dq(smem_desc_sw128(sbase + C::OFF_Q, 16, 1024)),
         dk(smem_desc_sw128(sbase + C::OFF_RING, 16, 1024)),
@@ -497,7 +519,7 @@ struct MmaWarp {
     for (int r = 0; r * static_cast<int>(gridDim.x) < p.num_units; ++r) {
       const int u = unit_of_round(r);
       if (u >= p.num_units) continue;
-      const Unit U = unit_at(u, p, PAGED);
+      const Unit U = unit_at(u, p, PAGED, bar.order());
       if (!wait(bar.q_full(), uc & 1)) return;
       ++uc;
       const int n0 = U.n[0], n1 = U.n[1], nkv = U.nkv;
@@ -573,7 +595,7 @@ __device__ void softmax_wg(const FwdParams& p, uint32_t tmem, const Bars<D, SRC>
   for (int rr = 0; rr * static_cast<int>(gridDim.x) < p.num_units; ++rr) {
     const int u = unit_of_round(rr);
     if (u >= p.num_units) continue;
-    const Unit U = unit_at(u, p, PAGED);
+    const Unit U = unit_at(u, p, PAGED, bar.order());
     const int n = I ? U.n[1] : U.n[0];
     const int qpos = 256 * U.qp + 128 * I + r;
     const bool row_valid = qpos < p.Tq;
@@ -739,6 +761,30 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1)
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
+  }
+  if constexpr (SRC != Src::kContiguous) {
+    // every CTA sorts the classes for itself: a class's place is the number of classes
+    // before it, by tiles and then by index
+    const int classes = p.B * p.n_qpairs;
+    if (classes <= kMaxSorted) {
+      uint16_t* cost = reinterpret_cast<uint16_t*>(smem + C::OFF_COST);
+      uint16_t* places = reinterpret_cast<uint16_t*>(smem + C::OFF_ORDER);
+      const int c = threadIdx.x;
+      int mine = 0;
+      if (c < classes) {
+        const int qi = c / p.B, qp = p.n_qpairs - 1 - qi;
+        bool bad;
+        const int L = keys_of(c - qi * p.B, p, true, bad);
+        mine = min(tiles_of(qp, 0, L, p) + tiles_of(qp, 1, L, p), 65535);
+        cost[c] = static_cast<uint16_t>(mine);
+      }
+      __syncthreads();
+      if (c < classes) {
+        int place = 0;
+        for (int i = 0; i < classes; ++i) place += cost[i] > mine || (cost[i] == mine && i < c);
+        places[place] = static_cast<uint16_t>(c);
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
