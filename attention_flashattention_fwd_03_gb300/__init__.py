@@ -52,6 +52,7 @@ EXPORTS = (
     "paged_kv4_gather",
     "paged_kv4_attn_decode_workspace_size",
     "paged_kv4_attn_decode",
+    "paged_kv4_attn_prefill_workspace_size",
     "paged_kv4_attn_prefill",
     "attn_test_set_failure",
     "attn_device_status",
@@ -124,7 +125,9 @@ def _bind(h):
     h.paged_kv4_attn_decode_workspace_size.restype = Z
     h.paged_kv4_attn_decode.argtypes = [P] * 4 + [I] * 8 + [F, P, P, P, Z, P]
     h.paged_kv4_attn_decode.restype = I
-    h.paged_kv4_attn_prefill.argtypes = [P] * 4 + [I] * 10 + [F, P, P, P]
+    h.paged_kv4_attn_prefill_workspace_size.argtypes = [I, I, I, I, I, I]
+    h.paged_kv4_attn_prefill_workspace_size.restype = Z
+    h.paged_kv4_attn_prefill.argtypes = [P] * 4 + [I] * 10 + [F, P, P, P, Z, P]
     h.paged_kv4_attn_prefill.restype = I
     h.attn_test_set_failure.argtypes = [ctypes.c_ulonglong, I]
     h.attn_test_set_failure.restype = I
@@ -797,29 +800,43 @@ def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
     return out, lse
 
 
+def paged_kv4_attn_prefill_workspace_size(B: int, Hq: int, Hkv: int, Tq: int, D: int,
+                                          max_kv_len: int) -> int:
+    return (_lib or lib()).paged_kv4_attn_prefill_workspace_size(B, Hq, Hkv, Tq, D, max_kv_len)
+
+
 def paged_kv4_attn_prefill(q, kv_pool, block_table, kv_lens, max_kv_len: int,
                            causal: bool = True, scale: float | None = None, out=None, lse=None,
-                           return_lse: bool = True, stream=None):
+                           workspace=None, return_lse: bool = True, stream=None):
     """Chunked prefill against the 4-bit paged cache through the C ABI.
 
     q [B,Hq,Tq,D] bf16 (the Tq newest tokens of each item), kv_pool [NB,Hkv,18*D]
     uint8, block_table [B,max_blocks] int32, kv_lens [B] int32 (all CUDA) -> (o
     [B,Hq,Tq,D] bf16, lse [B,Hq,Tq] fp32).  Query i of item b sits at logical
-    position kv_lens[b] - Tq + i.
+    position kv_lens[b] - Tq + i.  ``workspace`` (uint8 CUDA tensor, needed for short
+    chunks) is allocated here when not given.
     """
     device, NB = _check_kv4_attention(q, kv_pool, block_table, kv_lens, 1, out, lse)
     B, Hq, Tq, D = q.shape
+    Hkv = kv_pool.shape[1]
+    if workspace is not None:
+        _check_tensor("workspace", workspace, _torch.uint8, None, device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     with _On(device, stream) as handle:
+        if workspace is None:
+            need = paged_kv4_attn_prefill_workspace_size(B, Hq, Hkv, Tq, D, max_kv_len)
+            if need:
+                workspace = _torch.empty((need,), dtype=_torch.uint8, device=device)
         if out is None:
             out = _torch.empty((B, Hq, Tq, D), dtype=_torch.bfloat16, device=device)
         if return_lse and lse is None:
             lse = _torch.empty((B, Hq, Tq), dtype=_torch.float32, device=device)
         st = (_lib or lib()).paged_kv4_attn_prefill(
             q.data_ptr(), kv_pool.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), 16, B,
-            Hq, kv_pool.shape[1], Tq, D, block_table.shape[1], NB, max_kv_len,
-            1 if causal else 0, scale, out.data_ptr(), _ptr(lse), handle)
+            Hq, Hkv, Tq, D, block_table.shape[1], NB, max_kv_len, 1 if causal else 0, scale,
+            out.data_ptr(), _ptr(lse), _ptr(workspace),
+            workspace.numel() if workspace is not None else 0, handle)
     if st != ATTN_OK:
         raise GbAttnError("paged_kv4_attn_prefill", st)
     return out, lse

@@ -352,10 +352,88 @@ GBATTN_API int paged_kv4_gather(const void* kv_pool, const int32_t* block_table,
              : ATTN_ERR_CUDA;
 }
 
+namespace {
+
+// Attention of Tq query tokens a request by the row kernels of kv4_decode.cu.
+int attend_rows(const void* q, const void* kv_pool, const int32_t* block_table,
+                const int32_t* seq_lens, int S, int Hq, int Hkv, int Tq, int D, int max_blocks,
+                int num_pool_blocks, int max_seq_len, int causal, float scale, void* o, float* lse,
+                void* workspace, size_t workspace_bytes, void* stream) {
+  if (!workspace || !aligned(workspace, 256)) return ATTN_ERR_INVALID_ARG;
+  const Kv4DecodeWorkspace wl = kv4_decode_workspace(S, Hq, Hkv, Tq, D, max_seq_len);
+  if (workspace_bytes < wl.bytes) return ATTN_ERR_INVALID_ARG;
+  const Kv4Rows rows = kv4_rows(Hq, Hkv, Tq);
+  if (static_cast<uint64_t>(kv4_max_steps(S, Hkv * rows.chunks, max_seq_len)) >= kMaxDim ||
+      static_cast<uint64_t>(S) * Hkv * rows.rows >= kMaxDim / 2)
+    return ATTN_ERR_UNSUPPORTED;
+  DeviceState* ds = nullptr;
+  const int st = device_state(&ds);
+  if (st != ATTN_OK) return st;
+  Kv4DecodeParams p{};
+  p.q = q;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.o = o;
+  p.lse = lse;
+  char* ws = static_cast<char*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_lse = reinterpret_cast<float*>(ws + wl.off_part_lse);
+  p.seg_first = reinterpret_cast<int*>(ws + wl.off_seg_first);
+  p.seg_last = reinterpret_cast<int*>(ws + wl.off_seg_last);
+  p.S = S;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.Tq = Tq;
+  p.causal = causal;
+  p.rows = rows.rows;
+  p.piece_rows = rows.piece_rows;
+  p.chunks = rows.chunks;
+  p.segs = Hkv * rows.chunks;
+  p.max_blocks = max_blocks;
+  p.num_pool_blocks = num_pool_blocks;
+  p.max_seq_len = max_seq_len;
+  p.max_pieces = static_cast<int>(wl.pieces);
+  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.flags = ds->flags;
+  p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  p.withhold_copy = g_withhold_copy.load(std::memory_order_relaxed);
+  return launch_kv4_decode(static_cast<const uint8_t*>(kv_pool), p, ds->num_sms,
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+// Whether a chunk of Tq tokens goes to the row kernels instead of the tile kernel.  The row
+// kernels' time grows with Tq and is spread over the SMs along the cache; the tile kernel
+// takes the same time for 1 and for 256 tokens (one unit a query head), on as many SMs as
+// there are query heads in the batch.  Measured on GB300 (us, rows / tiles):
+//   16 x 32/8 heads, 6000 keys, D 128:  Tq 1: 30 / 312   16: 141 / 312   32: 266 / 312   48: 392 / 313
+//   64 x 12/2 heads, 4000 keys, D 128:  Tq 1: 24 / 320   16: 146 / 321   32: 277 / 321   48: 409 / 324
+//   64 x 32/8 heads, 1000 keys, D 128:  Tq 24: 194 / 212 32: 254 / 212
+//   8 x 8/8 heads, 3000 keys, D 128:    Tq 16: 22 / 44   48: 38 / 44     64: 46 / 45
+//   4 x 16/1 heads, 2000 keys, D 64:    Tq 16: 12 / 27   64: 26 / 27     96: 36 / 27
+//   1 x 32/8 heads, 100000 keys, D 128: Tq 1: 32 / 1235  64: 499 / 1236  128: 974 / 1236  192: 1462 / 1403
+// i.e. the crossing is near Tq = 30 with every SM busy and moves up as query heads are
+// fewer than the 152 SMs.
+bool by_rows(int B, int Hq, int Tq) {
+  const int64_t units = static_cast<int64_t>(B) * Hq;
+  return Tq <= 256 && Tq * (units < 152 ? units : 152) <= 4500;
+}
+
+}  // namespace
+
 GBATTN_API size_t paged_kv4_attn_decode_workspace_size(int num_seqs, int Hq, int Hkv, int D,
                                                        int max_seq_len) {
   if (num_seqs < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_seq_len < 0) return 0;
-  return kv4_decode_workspace(num_seqs, Hq, Hkv, D, max_seq_len).bytes;
+  return kv4_decode_workspace(num_seqs, Hq, Hkv, 1, D, max_seq_len).bytes;
+}
+
+GBATTN_API size_t paged_kv4_attn_prefill_workspace_size(int B, int Hq, int Hkv, int Tq, int D,
+                                                        int max_kv_len) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Tq <= 0 || D <= 0 || max_kv_len < 0)
+    return 0;
+  return by_rows(B, Hq, Tq) ? kv4_decode_workspace(B, Hq, Hkv, Tq, D, max_kv_len).bytes : 0;
 }
 
 GBATTN_API int paged_kv4_attn_decode(const void* q, const void* kv_pool,
@@ -374,52 +452,21 @@ GBATTN_API int paged_kv4_attn_decode(const void* q, const void* kv_pool,
   if (!aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(o, 16) || !aligned(block_table, 4) ||
       !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
     return ATTN_ERR_INVALID_ARG;
-  const Kv4DecodeWorkspace wl = kv4_decode_workspace(num_seqs, Hq, Hkv, D, max_seq_len);
-  if (workspace_bytes < wl.bytes) return ATTN_ERR_INVALID_ARG;
   if (static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim ||
       static_cast<uint64_t>(num_seqs) * Hq >= kMaxDim / 2 ||
-      static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim ||
-      static_cast<uint64_t>(kv4_max_steps(num_seqs, Hkv, max_seq_len)) >= kMaxDim)
+      static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim)
     return ATTN_ERR_UNSUPPORTED;
-  DeviceState* ds = nullptr;
-  const int st = device_state(&ds);
-  if (st != ATTN_OK) return st;
-  Kv4DecodeParams p{};
-  p.q = q;
-  p.block_table = block_table;
-  p.seq_lens = seq_lens;
-  p.o = o;
-  p.lse = lse;
-  char* ws = static_cast<char*>(workspace);
-  p.part_o = reinterpret_cast<float*>(ws);
-  p.part_lse = reinterpret_cast<float*>(ws + wl.off_part_lse);
-  p.seg_first = reinterpret_cast<int*>(ws + wl.off_seg_first);
-  p.seg_last = reinterpret_cast<int*>(ws + wl.off_seg_last);
-  p.S = num_seqs;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.D = D;
-  p.group = Hq / Hkv;
-  p.max_blocks = max_blocks_per_seq;
-  p.num_pool_blocks = num_pool_blocks;
-  p.max_seq_len = max_seq_len;
-  p.max_pieces = static_cast<int>(wl.pieces);
-  p.scale = scale;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.flags = ds->flags;
-  p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
-  p.withhold_copy = g_withhold_copy.load(std::memory_order_relaxed);
-  return launch_kv4_decode(static_cast<const uint8_t*>(kv_pool), p, ds->num_sms,
-                           static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? ATTN_OK
-             : ATTN_ERR_CUDA;
+  return attend_rows(q, kv_pool, block_table, seq_lens, num_seqs, Hq, Hkv, 1, D,
+                     max_blocks_per_seq, num_pool_blocks, max_seq_len, 0, scale, o, lse, workspace,
+                     workspace_bytes, stream);
 }
 
 GBATTN_API int paged_kv4_attn_prefill(const void* q, const void* kv_pool,
                                       const int32_t* block_table, const int32_t* kv_lens,
                                       int block_size, int B, int Hq, int Hkv, int Tq, int D,
                                       int max_blocks_per_seq, int num_pool_blocks, int max_kv_len,
-                                      int causal, float scale, void* o, float* lse, void* stream) {
+                                      int causal, float scale, void* o, float* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
   if (B < 0 || Tq < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_blocks_per_seq <= 0 ||
       num_pool_blocks <= 0 || max_kv_len < 0)
     return ATTN_ERR_INVALID_ARG;
@@ -437,6 +484,10 @@ GBATTN_API int paged_kv4_attn_prefill(const void* q, const void* kv_pool,
       static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim ||
       static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim)
     return ATTN_ERR_UNSUPPORTED;
+  if (by_rows(B, Hq, Tq))
+    return attend_rows(q, kv_pool, block_table, kv_lens, B, Hq, Hkv, Tq, D, max_blocks_per_seq,
+                       num_pool_blocks, max_kv_len, causal, scale, o, lse, workspace,
+                       workspace_bytes, stream);
   DeviceState* ds = nullptr;
   int st = device_state(&ds);
   if (st != ATTN_OK) return st;

@@ -81,15 +81,20 @@ cudaError_t launch_paged_decode(const CUtensorMap& tmK, const CUtensorMap& tmV,
 cudaError_t prepare_paged_decode();
 
 struct Kv4DecodeParams {
-  const void* q;               // [S, Hq, D] bf16
+  const void* q;               // [S, Hq, Tq, D] bf16
   const int32_t* block_table;  // [S, max_blocks]
   const int32_t* seq_lens;     // [S]
-  void* o;                     // [S, Hq, D] bf16
-  float* lse;                  // [S, Hq] or nullptr
-  float* part_o;               // [pieces, group, D] fp32 (workspace)
-  float* part_lse;             // [pieces, group] fp32 (workspace)
-  int *seg_first, *seg_last;   // [S, Hkv] first and last range of each segment (workspace)
-  int S, Hq, Hkv, D, group;
+  void* o;                     // [S, Hq, Tq, D] bf16
+  float* lse;                  // [S, Hq, Tq] or nullptr
+  float* part_o;               // [pieces, piece_rows, D] fp32 (workspace)
+  float* part_lse;             // [pieces, piece_rows] fp32 (workspace)
+  int *seg_first, *seg_last;   // [S, segs] first and last range of each segment (workspace)
+  int S, Hkv, D;
+  int Tq;                      // query tokens a request
+  int causal;                  // token i sees the keys up to position L - Tq + i
+  int rows;                    // query rows of a KV head: Hq / Hkv * Tq
+  int piece_rows, chunks;      // rows handled together, and how often that many make `rows`
+  int segs;                    // segments of a request: Hkv * chunks
   int max_blocks;
   int num_pool_blocks;
   int max_seq_len;
@@ -107,8 +112,12 @@ struct Kv4DecodeWorkspace {
   long long pieces;
   size_t off_part_lse, off_seg_first, off_seg_last, bytes;  // part_o at 0
 };
-Kv4DecodeWorkspace kv4_decode_workspace(int S, int Hq, int Hkv, int D, int max_seq_len);
-long long kv4_max_steps(int S, int Hkv, int max_seq_len);  // steps of 64 tokens of a batch
+Kv4DecodeWorkspace kv4_decode_workspace(int S, int Hq, int Hkv, int Tq, int D, int max_seq_len);
+long long kv4_max_steps(int S, int segs, int max_seq_len);  // steps of 64 tokens of a batch
+struct Kv4Rows {
+  int rows, piece_rows, chunks;
+};
+Kv4Rows kv4_rows(int Hq, int Hkv, int Tq);
 
 // Decode over the 4-bit pool [num_pool_blocks, Hkv, 18 D] (kv4.cuh).
 cudaError_t launch_kv4_decode(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms,

@@ -1,4 +1,5 @@
-// kv4_decode.cu -- single-token attention against the 4-bit paged cache, sm_103a.
+// kv4_decode.cu -- attention of single tokens and of short chunks against the 4-bit paged
+// cache, sm_103a.
 //
 // For a query q and a token whose K group w has codes u_c = n_c + 8 and scale s_w, and
 // whose V group has codes and scale t_w:
@@ -30,6 +31,10 @@
 // scales of K and V), into the warp's own ring in shared memory; the table entries of a
 // step are read one step ahead of its copies.  The fragments of m16n8k16 come out of shared memory by plain
 // loads in the order the format lays down.
+//
+// A chunk of Tq tokens is the same computation with group * Tq query rows on every KV head
+// ([Hq, Tq, D] keeps them together); row x sees the keys up to its own position.  Rows are
+// taken 8 or 16 at a time, each such chunk of rows as a segment of its own (MULTI).
 //
 // The shortest range is one step, so that a small batch spreads over many SMs; ranges are
 // dealt to the CTAs in turn for the same reason.  The piece of range k and segment s (both
@@ -146,7 +151,8 @@ __device__ __forceinline__ int blocks_of(const Kv4DecodeParams& p, int L) {
 
 __device__ __forceinline__ int steps_of(int blocks) { return (blocks + kStepBlocks - 1) / kStepBlocks; }
 
-// A step of the batch: step i of request r, KV head h, whose segment has nb blocks.
+// A step of the batch: step i of request r, segment h (a KV head, or MULTI a KV head and a
+// chunk of rows), which has nb blocks.
 struct Step {
   int r, h, i, nb;
   __device__ int blocks() const { return min(kStepBlocks, nb - i * kStepBlocks); }
@@ -160,13 +166,13 @@ __device__ __forceinline__ void advance(Step& s, const Kv4DecodeParams& p) {
     return;
   }
   s.i = 0;
-  if (++s.h < p.Hkv) return;
+  if (++s.h < p.segs) return;
   s.h = 0;
   s.nb = 0;
   while (s.nb == 0 && ++s.r < p.S) s.nb = blocks_of(p, p.seq_lens[s.r]);
 }
 
-template <int D, int NQT>
+template <int D, int NQT, bool MULTI>
 __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     kv4_decode_split_kernel(const uint8_t* __restrict__ pool, const Kv4DecodeParams p) {
   using F = Kv4<D>;
@@ -200,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     if (r0 + lane < p.S) total += steps_of(blocks_of(p, p.seq_lens[r0 + lane]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  total *= p.Hkv;  // below 2^31 for every length within max_seq_len
+  total *= p.segs;  // below 2^31 for every length within max_seq_len
   const int W = min(static_cast<int>(gridDim.x) * kWarps, total);
   const int k_w = warp * gridDim.x + blockIdx.x;
   if (k_w >= W) return;  // warps are independent: no barrier of the CTA follows
@@ -214,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     for (int r0 = 0; r0 < p.S && !found; r0 += 32) {
       const int r = r0 + lane;
       const int nb = r < p.S ? blocks_of(p, p.seq_lens[r]) : 0;
-      const int own = steps_of(nb) * p.Hkv;
+      const int own = steps_of(nb) * p.segs;
       int incl = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -241,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   Step ps = at;
   int p_left = n_w, issued = 0, p_stage = 0;
   const uint64_t policy = l2_policy_evict_first();  // every cache byte is read once
+  auto kv_head = [&](int h) { return MULTI ? h / p.chunks : h; };
   auto entry = [&]() -> int {
     return lane < ps.blocks()
                ? p.block_table[static_cast<size_t>(ps.r) * p.max_blocks + ps.i * kStepBlocks + lane]
@@ -258,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
       __syncwarp();
       if (lane < n)
         bulk_load_hint(ring_addr + s * C::kStageBytes + lane * F::kChunk,
-                       pool + (static_cast<size_t>(bad ? 0 : phys) * p.Hkv + ps.h) * F::kChunk,
+                       pool + (static_cast<size_t>(bad ? 0 : phys) * p.Hkv + kv_head(ps.h)) * F::kChunk,
                        F::kChunk, bars + 8 * s, policy);
     }
     ++issued;
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
 
   // ---------------- the range, step by step ----------------
   const int g = lane >> 2, t4 = lane & 3;
-  const int group = p.group;
+  int n_rows = p.rows;               // query rows of the segment
   const int row0 = token_of_row(g);  // rows g and g + 8 of a score tile: tokens row0 (+ 8)
   uint32_t qb[D / 16][NQT][2];       // Q^T fragments (fp16) in the order of the K codes
   float q8[G][NQT][2];               // -8 sum of q over group w, queries 2 t4 (+ 1)
@@ -291,9 +298,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   auto begin_piece = [&]() {
     L = p.seq_lens[c.r];
     pbad = false;
-    if (c.i == 0 && lane == 0) p.seg_first[c.r * p.Hkv + c.h] = k_w;
-    const uint16_t* q =
-        static_cast<const uint16_t*>(p.q) + (static_cast<size_t>(c.r) * p.Hq + c.h * group) * D;
+    if (c.i == 0 && lane == 0) p.seg_first[c.r * p.segs + c.h] = k_w;
+    size_t q0 = static_cast<size_t>(c.r) * p.Hkv * p.rows + static_cast<size_t>(c.h) * p.rows;
+    if constexpr (MULTI) {
+      const int h = c.h / p.chunks, x0 = (c.h - h * p.chunks) * (8 * NQT);
+      n_rows = min(8 * NQT, p.rows - x0);
+      q0 = (static_cast<size_t>(c.r) * p.Hkv + h) * p.rows + x0;
+    }
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) + q0 * D;
     // A fragment of -8 in both forms of a code
     const uint32_t minus8[4] = {0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u};
 #pragma unroll
@@ -304,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
 #pragma unroll
       for (int w = 0; w < G; ++w) {
         x[w] = make_uint4(0, 0, 0, 0);
-        if (row < group) x[w] = *reinterpret_cast<const uint4*>(q + row * D + 32 * w + 8 * t4);
+        if (row < n_rows) x[w] = *reinterpret_cast<const uint4*>(q + row * D + 32 * w + 8 * t4);
         big = __vmaxu2(big, __vmaxu2(__vmaxu2(x[w].x & 0x7fff7fffu, x[w].y & 0x7fff7fffu),
                                      __vmaxu2(x[w].z & 0x7fff7fffu, x[w].w & 0x7fff7fffu)));
       }
@@ -355,7 +367,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     const uint8_t* stage = ring + s * C::kStageBytes;
     // Valid tokens of the step.  The blocks past them are computed with whatever the stage
     // holds (codes are finite whatever their bits) and masked with the tail.
-    const int n_tok = min(kBS * kStepBlocks, L - c.i * (kBS * kStepBlocks));
+    const int here = L - c.i * (kBS * kStepBlocks);  // keys from the step's first on
+    const int n_tok = min(kBS * kStepBlocks, here);
 
     // ---- S^T = K Q^T, group by group ----
     float sc[kStepBlocks][NQT][4];
@@ -395,8 +408,24 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
         }
       }
     }
-    const bool tail = n_tok < kBS * kStepBlocks;
-    if (tail) {  // tokens past the end: their codes and scales may be anything
+    // MULTI, causal: row x sees the keys before its own position and its own
+    const int hidden = MULTI && p.causal ? p.Tq - 1 : 0;  // keys that row 0 does not see
+    const bool tail = here - hidden < kBS * kStepBlocks;
+    if (MULTI && tail) {
+      const int x0 = (c.h % p.chunks) * (8 * NQT) + 2 * t4;
+#pragma unroll
+      for (int nt = 0; nt < NQT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int n = min(here, here - hidden + (p.causal ? (x0 + 8 * nt + e) % p.Tq : 0));
+#pragma unroll
+          for (int j = 0; j < kStepBlocks; ++j) {
+            if (kBS * j + row0 >= n) sc[j][nt][e] = -INFINITY;
+            if (kBS * j + row0 + 8 >= n) sc[j][nt][2 + e] = -INFINITY;
+          }
+        }
+      }
+    } else if (tail) {  // tokens past the end: their codes and scales may be anything
 #pragma unroll
       for (int j = 0; j < kStepBlocks; ++j) {
         const bool in0 = kBS * j + row0 < n_tok, in1 = kBS * j + row0 + 8 < n_tok;
@@ -422,12 +451,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
-        // finite from the first step on: every step has a valid token
+        // (finite from the first step on: every step has a valid token, but MULTI rows may
+        // not see it)
         const bool grow = (bm - m_q[nt][e]) * sl2[nt][e] > kRescaleLog2;
         al[nt][e] = grow ? ex2((m_q[nt][e] - bm) * sl2[nt][e]) : 1.f;
         m_q[nt][e] = grow ? bm : m_q[nt][e];
         grown |= grow;
-        const float ms = m_q[nt][e] * sl2[nt][e];
+        const float ms = MULTI && m_q[nt][e] == -INFINITY ? 0.f : m_q[nt][e] * sl2[nt][e];
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < kStepBlocks; ++j) {
@@ -511,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     // ---- the piece ends: write its normalised O and LSE ----
     {
       const float nan = __int_as_float(0x7fc00000);
-      const int seg = c.r * p.Hkv + c.h, piece = k_w + seg;
+      const int seg = c.r * p.segs + c.h, piece = k_w + seg;
       if (piece < p.max_pieces) {
 #pragma unroll
         for (int nt = 0; nt < NQT; ++nt) {
@@ -522,16 +552,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
             lsum += __shfl_xor_sync(0xffffffffu, lsum, 8);
             lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
             const int q = 8 * nt + 2 * t4 + e;
-            if (q >= group) continue;
-            const float inv = pbad ? nan : 64.f / lsum;
-            const size_t base = static_cast<size_t>(piece) * group + q;
+            if (q >= n_rows) continue;
+            const bool none = MULTI && lsum == 0.f;  // no key of the piece is visible
+            const float inv = pbad ? nan : (none ? 0.f : 64.f / lsum);
+            const size_t base = static_cast<size_t>(piece) * p.piece_rows + q;
             float* dst = p.part_o + base * D + 4 * g;
 #pragma unroll
             for (int w = 0; w < G; ++w)
               *reinterpret_cast<float4*>(dst + 32 * w) =
                   make_float4(acc[2 * w][nt][e] * inv, acc[2 * w][nt][2 + e] * inv,
                               acc[2 * w + 1][nt][e] * inv, acc[2 * w + 1][nt][2 + e] * inv);
-            if (g == 0) p.part_lse[base] = pbad ? nan : m_q[nt][e] * sl[nt][e] + logf(lsum);
+            if (g == 0)
+              p.part_lse[base] =
+                  pbad ? nan : (none ? -INFINITY : m_q[nt][e] * sl[nt][e] + logf(lsum));
           }
         }
         if (c.last() && lane == 0) p.seg_last[seg] = k_w;
@@ -562,17 +595,20 @@ __global__ void __launch_bounds__(MW * 32) kv4_decode_merge_kernel(const Kv4Deco
   // launched as a programmatic dependent: the split kernel's results are complete and
   // visible once this returns
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int r = blockIdx.x / p.Hq, hq = blockIdx.x - r * p.Hq;
+  // the CTA's row: row x of KV head kvh of request r
+  const int kv = blockIdx.x / p.rows, x = blockIdx.x - kv * p.rows;
+  const int r = kv / p.Hkv, kvh = kv - r * p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = hq / p.group;
-  const int seg = r * p.Hkv + kvh;
+  const int chunk = x / p.piece_rows;
+  const int seg = r * p.segs + kvh * p.chunks + chunk;
   const int L = p.seq_lens[r], k0 = p.seg_first[seg], k1 = p.seg_last[seg];
   // (the split kernel has noted the ranges of every valid nonempty request; the check keeps
   // every read in bounds should the lengths have changed between the two kernels)
   const bool good = blocks_of(p, L) > 0 && k0 >= 0 && k0 <= k1 && k1 + seg < p.max_pieces;
   const bool bad = L != 0 && !good;
   const int n = good ? k1 - k0 + 1 : 0;
-  const size_t base = good ? static_cast<size_t>(k0 + seg) * p.group + (hq - kvh * p.group) : 0;
+  const size_t base =
+      good ? static_cast<size_t>(k0 + seg) * p.piece_rows + (x - chunk * p.piece_rows) : 0;
   const float* pl = p.part_lse + base;
   const float* po = p.part_o + base * D + lane * PER;
 
@@ -588,8 +624,8 @@ __global__ void __launch_bounds__(MW * 32) kv4_decode_merge_kernel(const Kv4Deco
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[s][i] = 0.f;
       if (j < n) {
-        lse[s] = pl[static_cast<size_t>(j) * p.group];
-        const float* src = po + static_cast<size_t>(j) * p.group * D;
+        lse[s] = pl[static_cast<size_t>(j) * p.piece_rows];
+        const float* src = po + static_cast<size_t>(j) * p.piece_rows * D;
         if constexpr (PER == 4) {
           const float4 x = *reinterpret_cast<const float4*>(src);
           v[s][0] = x.x, v[s][1] = x.y, v[s][2] = x.z, v[s][3] = x.w;
@@ -635,7 +671,7 @@ __global__ void __launch_bounds__(MW * 32) kv4_decode_merge_kernel(const Kv4Deco
     x1 = fmaf(f, part[w][2 * threadIdx.x + 1], x1);
   }
   float lse_out = Ms + logf(tot);
-  const float inv = 1.f / tot;
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;  // (no key is visible to the row)
   x0 *= inv;
   x1 *= inv;
   if (L == 0) {
@@ -652,18 +688,22 @@ __global__ void __launch_bounds__(MW * 32) kv4_decode_merge_kernel(const Kv4Deco
 
 template <int D, int NQT>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(kv4_decode_split_kernel<D, NQT>,
+  const cudaError_t e =
+      cudaFuncSetAttribute(kv4_decode_split_kernel<D, NQT, false>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D, NQT>::kSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(kv4_decode_split_kernel<D, NQT, true>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D, NQT>::kSmem);
 }
 
-template <int D, int NQT>
+template <int D, int NQT, bool MULTI>
 cudaError_t launch_split(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms,
                          cudaStream_t stream) {
   // kCtasPerSm CTAs per SM, fewer when even the shortest ranges would not fill them
   const int ctas = num_sms * Shape<D, NQT>::kCtasPerSm;
   const int cap = ctas < kKv4MaxRanges / kWarps ? ctas : kKv4MaxRanges / kWarps;
   // a CTA a range first, then more ranges a CTA (the kernel deals them in that order)
-  const long long steps = kv4_max_steps(p.S, p.Hkv, p.max_seq_len);
+  const long long steps = kv4_max_steps(p.S, p.segs, p.max_seq_len);
   const long long want = steps < 1 ? 1 : (steps < num_sms ? steps : num_sms + (steps - num_sms) / kWarps);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -675,26 +715,32 @@ cudaError_t launch_split(const uint8_t* pool, const Kv4DecodeParams& p, int num_
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_decode_split_kernel<D, NQT>, pool, p);
+  return cudaLaunchKernelEx(&cfg, kv4_decode_split_kernel<D, NQT, MULTI>, pool, p);
 }
 
 template <int D>
 cudaError_t launch(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms, cudaStream_t stream) {
-  const cudaError_t e = p.group <= 8 ? launch_split<D, 1>(pool, p, num_sms, stream)
-                                     : launch_split<D, 2>(pool, p, num_sms, stream);
+  const bool multi = p.Tq > 1 || p.chunks > 1;
+  cudaError_t e;
+  if (p.piece_rows <= 8)
+    e = multi ? launch_split<D, 1, true>(pool, p, num_sms, stream)
+              : launch_split<D, 1, false>(pool, p, num_sms, stream);
+  else
+    e = multi ? launch_split<D, 2, true>(pool, p, num_sms, stream)
+              : launch_split<D, 2, false>(pool, p, num_sms, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.S) * p.Hq);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.S) * p.Hkv * p.rows);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // Few segments share the ranges among many pieces each: 16 warps a head then (one request
   // of 131000 tokens, 228 pieces a head: 36.7 us a call against 40.6 with 8), else 4, one
   // round trip for the ~15 pieces a head of 64 requests.
-  const long long pieces = p.max_pieces / (static_cast<long long>(p.S) * p.Hkv);
+  const long long pieces = p.max_pieces / (static_cast<long long>(p.S) * p.segs);
   if (pieces > 48) {
     cfg.blockDim = dim3(16 * 32);
     return cudaLaunchKernelEx(&cfg, kv4_decode_merge_kernel<D, 16>, p);
@@ -705,17 +751,27 @@ cudaError_t launch(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms, c
 
 }  // namespace
 
-long long kv4_max_steps(int S, int Hkv, int max_seq_len) {
-  return static_cast<long long>(S) * Hkv *
+long long kv4_max_steps(int S, int segs, int max_seq_len) {
+  return static_cast<long long>(S) * segs *
          ((max_seq_len + kBS * kStepBlocks - 1ll) / (kBS * kStepBlocks));
 }
 
-Kv4DecodeWorkspace kv4_decode_workspace(int S, int Hq, int Hkv, int D, int max_seq_len) {
+Kv4Rows kv4_rows(int Hq, int Hkv, int Tq) {
+  Kv4Rows r;
+  r.rows = Hq / Hkv * Tq;
+  r.piece_rows = r.rows < 16 ? r.rows : 16;
+  r.chunks = (r.rows + 15) / 16;
+  return r;
+}
+
+Kv4DecodeWorkspace kv4_decode_workspace(int S, int Hq, int Hkv, int Tq, int D, int max_seq_len) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   Kv4DecodeWorkspace w;
-  const long long steps = kv4_max_steps(S, Hkv, max_seq_len), segs = static_cast<long long>(S) * Hkv;
+  const Kv4Rows r = kv4_rows(Hq, Hkv, Tq);
+  const long long segs = static_cast<long long>(S) * Hkv * r.chunks;
+  const long long steps = kv4_max_steps(S, Hkv * r.chunks, max_seq_len);
   w.pieces = (steps < kKv4MaxRanges ? steps : kKv4MaxRanges) + segs;
-  const size_t n = static_cast<size_t>(w.pieces) * (Hq / Hkv);
+  const size_t n = static_cast<size_t>(w.pieces) * r.piece_rows;
   w.off_part_lse = up(n * D * sizeof(float));
   w.off_seg_first = w.off_part_lse + up(n * sizeof(float));
   w.off_seg_last = w.off_seg_first + up(static_cast<size_t>(segs) * sizeof(int));

@@ -386,6 +386,13 @@ size_t paged_kv4_attn_decode_workspace_size(int num_seqs, int Hq, int Hkv, int D
                                             int max_seq_len);
 
 /*
+ * Bytes of scratch workspace paged_kv4_attn_prefill needs for these sizes: 0 for
+ * chunks long enough for its tile kernel, else partial results as in the decode.
+ */
+size_t paged_kv4_attn_prefill_workspace_size(int B, int Hq, int Hkv, int Tq, int D,
+                                             int max_kv_len);
+
+/*
  * paged_kv4_attn_decode -- paged_attn_decode over the 4-bit cache: the attention of
  * one query token per request over the values that paged_kv4_gather returns.
  *
@@ -408,7 +415,12 @@ int paged_kv4_attn_decode(const void *q, const void *kv_pool, const int32_t *blo
  * The values are bf16 exactly, so the kernel computes with them as they are.
  *
  *   kv_pool       [num_pool_blocks, Hkv, 18 D] bytes
+ *   workspace     >= paged_kv4_attn_prefill_workspace_size(...) bytes, 256-byte
+ *                 aligned (may be NULL where that is 0); no initialisation
  *
+ * Short chunks (a few drafted tokens) run as a decode of group * Tq query rows a KV
+ * head, split along the cache; longer ones as 128-row tiles.  An invalid block id makes
+ * that item's O unspecified (NaN in short chunks) and sets flag bit 4.
  * Everything else, the device-side checks included, as in paged_attn_prefill.  Slots
  * past kv_lens[b] may hold any bits.  A NaN in a key of the cache makes O and LSE NaN
  * for the queries that see it; a NaN in a value may reach O of every query of its item
@@ -417,7 +429,8 @@ int paged_kv4_attn_decode(const void *q, const void *kv_pool, const int32_t *blo
 int paged_kv4_attn_prefill(const void *q, const void *kv_pool, const int32_t *block_table,
                            const int32_t *kv_lens, int block_size, int B, int Hq, int Hkv, int Tq,
                            int D, int max_blocks_per_seq, int num_pool_blocks, int max_kv_len,
-                           int causal, float scale, void *o, float *lse, void *stream);
+                           int causal, float scale, void *o, float *lse, void *workspace,
+                           size_t workspace_bytes, void *stream);
 
 /*
  * Test hook for the kernels' failure detection (not for production use).

@@ -1,5 +1,7 @@
-"""paged_kv4_attn_prefill against the bf16 paged prefill over the same values (equal bits:
-every value the 4-bit cache holds is a bf16) and against the fp64 oracle."""
+"""paged_kv4_attn_prefill: its tile kernel against the bf16 paged prefill over the same
+values (equal bits: every value the 4-bit cache holds is a bf16), its row kernels (short
+chunks) against the fp64 oracle, with the tolerances of the 4-bit decode, and both on the
+inputs where they could go wrong."""
 
 from __future__ import annotations
 
@@ -41,23 +43,41 @@ class Item:
                                          causal=causal, scale=self.scale, **kw)
 
 
-CASES = [
+def uses_rows(gb, c):
+    B, Hq, Tq, D = c.q.shape
+    return gb.paged_kv4_attn_prefill_workspace_size(B, Hq, c.p.k_pool.shape[1], Tq, D,
+                                                    c.p.max_seq_len) > 0
+
+
+TILES = [
     # Hq, Hkv, D, Tq, kv_lens
-    (8, 2, 128, 1, [1, 17, 4096, 8192]),
-    (8, 2, 128, 127, [127, 300, 2049, 8192]),
     (8, 2, 128, 512, [512, 700, 5000, 8192]),
     (12, 2, 128, 300, [300, 301, 1024, 2999]),
     (4, 4, 64, 257, [257, 640, 1000, 4096]),
     (16, 2, 64, 512, [600, 8192]),
-    (2, 1, 128, 37, [0, 5, 36, 37, 128, 129]),   # chunks longer than their cache
+    (32, 4, 128, 64, [64, 100, 2049, 4000, 129, 128]),
+    (32, 2, 128, 70, [0, 5, 69, 70, 128, 129]),   # chunks longer than their cache
+    (24, 1, 64, 130, [0, 1, 15, 16, 17, 127]),
+]
+
+ROWS = [
+    (8, 2, 128, 1, [1, 17, 4096, 8192]),
+    (8, 2, 128, 4, [4, 5, 63, 64, 65, 300]),      # 16 rows on a KV head
+    (3, 1, 128, 3, [3, 70, 700]),                 # 9 rows
+    (5, 5, 64, 7, [7, 8, 1000]),                  # 7 rows, no sharing
+    (8, 2, 64, 5, [100, 0, 3, 4, 5, 129]),        # 20 rows: two chunks, caches below Tq
+    (32, 2, 128, 6, [6, 900]),                    # 96 rows
+    (2, 1, 128, 37, [0, 5, 36, 37, 128, 129]),
     (2, 1, 64, 130, [0, 1, 15, 16, 17, 127]),
+    (4, 2, 128, 200, [200, 333]),
 ]
 
 
-@pytest.mark.parametrize("Hq,Hkv,D,Tq,lens", CASES)
+@pytest.mark.parametrize("Hq,Hkv,D,Tq,lens", TILES)
 @pytest.mark.parametrize("causal", [True, False])
-def test_equals_the_bf16_prefill_over_the_same_values(gb, Hq, Hkv, D, Tq, lens, causal):
+def test_tiles_equal_the_bf16_prefill_over_the_same_values(gb, Hq, Hkv, D, Tq, lens, causal):
     c = Item(Hq, Hkv, D, Tq, lens, 60000 + Tq)
+    assert not uses_rows(gb, c)
     o, lse = c.run(gb, causal)
     o2, lse2 = gb.paged_attn_prefill(c.q, to_dev(c.k), to_dev(c.v), c.table, c.kv_lens,
                                      c.p.max_seq_len, causal=causal, scale=c.scale)
@@ -66,8 +86,8 @@ def test_equals_the_bf16_prefill_over_the_same_values(gb, Hq, Hkv, D, Tq, lens, 
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
-@pytest.mark.parametrize("Hq,Hkv,D,Tq,lens", [CASES[3], CASES[4], CASES[6], CASES[7]])
-def test_matches_the_oracle(gb, Hq, Hkv, D, Tq, lens):
+@pytest.mark.parametrize("Hq,Hkv,D,Tq,lens", [TILES[1], TILES[2], TILES[5], TILES[6]])
+def test_tiles_match_the_oracle(gb, Hq, Hkv, D, Tq, lens):
     c = Item(Hq, Hkv, D, Tq, lens, 61000 + Tq)
     o, lse = c.run(gb, True)
     o_ref, l_ref = oracle.paged_prefill(c.q_bits, c.k, c.v, c.p.block_table, c.p.seq_lens, True,
@@ -76,6 +96,61 @@ def test_matches_the_oracle(gb, Hq, Hkv, D, Tq, lens):
     empty = np.isneginf(l_ref)
     assert np.array_equal(np.isneginf(lg), empty) and np.all(og[empty] == 0)
     check_close(og[~empty], lg[~empty], o_ref[~empty], l_ref[~empty], "kv4 prefill")
+
+
+def check_rows(c, o, lse, causal, items=None):
+    """Tolerances as derived in test_gpu_kv4_decode.py."""
+    p = c.p
+    args = (p.block_table, p.seq_lens, causal, c.scale)
+    want, wl = oracle.paged_prefill(c.q_bits, c.k, c.v, *args)
+    mag, _ = oracle.paged_prefill(c.q_bits, c.k, c.v & 0x7FFF, *args)
+    B, Hq, Tq, D = c.q_bits.shape
+    Hkv = p.k_pool.shape[1]
+    scales = synth.bf16_bits_to_float(ref.quantise(p.k_pool)[1]).astype(np.float64)
+    big = np.nanmax(np.where(np.isnan(scales), 0, scales), (0, 2))  # [Hkv, groups]
+    qs = np.abs(synth.bf16_bits_to_float(c.q_bits).astype(np.float64))
+    qs = qs.reshape(B, Hq, Tq, -1, 32).sum(-1)
+    s = (qs * np.repeat(big, Hq // Hkv, 0)[None, :, None]).sum(-1)
+    fin = np.where(np.isfinite(wl), np.abs(wl), 0)
+    ltol = 2.0 ** -20 * 23 * c.scale * s + 2.0 ** -20 * fin + 2.0 ** -18
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -16) * mag
+    got, gl = from_dev(o), from_dev(lse)
+    empty = np.isneginf(wl)
+    for b in range(B) if items is None else items:
+        e = empty[b]
+        assert np.array_equal(np.isneginf(gl[b]), e) and np.all(got[b][e] == 0), b
+        assert np.all(np.abs(got[b] - want[b])[~e] <= tol[b][~e]), b
+        assert np.all(np.abs(gl[b][~e] - wl[b][~e]) <= ltol[b][~e]), b
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,Tq,lens", ROWS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_match_the_oracle(gb, Hq, Hkv, D, Tq, lens, causal):
+    c = Item(Hq, Hkv, D, Tq, lens, 60500 + Tq)
+    assert uses_rows(gb, c)
+    o, lse = c.run(gb, causal)
+    torch.cuda.synchronize()
+    assert gb.attn_device_status() == (gb.ATTN_OK, 0)
+    check_rows(c, o, lse, causal)
+
+
+def test_one_drafted_token_equals_the_decode(gb):
+    c = Item(12, 2, 128, 1, [1, 300, 4000], 61500)
+    o, lse = c.run(gb, True)
+    o2, lse2 = gb.paged_kv4_attn_decode(c.q.squeeze(2), c.pool, c.table, c.kv_lens, 4000,
+                                        scale=c.scale)
+    assert torch.equal(o.squeeze(2), o2) and torch.equal(lse.squeeze(2), lse2)
+
+
+def test_more_classes_than_the_sorted_list_holds(gb):
+    """More (item, query pair) classes than are sorted: the items' own order."""
+    lens = list(synth.uniform_ints(61600, 400, 0, 90))
+    c = Item(2, 1, 64, 40, lens, 61601)
+    assert not uses_rows(gb, c)
+    o, lse = c.run(gb, True)
+    o2, lse2 = gb.paged_attn_prefill(c.q, to_dev(c.k), to_dev(c.v), c.table, c.kv_lens,
+                                     c.p.max_seq_len, causal=True, scale=c.scale)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 def test_outputs_streams_and_graphs(gb):
@@ -97,12 +172,13 @@ def test_outputs_streams_and_graphs(gb):
         assert torch.equal(out, o) and torch.equal(l2, lse)
 
 
-def test_nan_keys_reach_the_queries_that_see_them(gb):
-    Tq, D = 20, 128
-    c = Item(4, 2, D, Tq, [40, 40], 63000)
+@pytest.mark.parametrize("Tq", [20, 300])  # by rows, by tiles
+def test_nan_keys_reach_the_queries_that_see_them(gb, Tq):
+    D = 128
+    c = Item(4, 2, D, Tq, [Tq + 20] * 2, 63000)
     host = c.pool_host.copy()
     blk = c.p.block_table
-    # token 30 of item 0: its key in head 0 (seen by queries 10..19)
+    # token 30 of item 0: its key in head 0 (seen by queries 10 and on)
     host[blk[0, 1], 0, 8 * D + 14 * 8:8 * D + 14 * 8 + 2] = [0xC0, 0x7F]
     o, lse = c.run(gb, True, pool=torch.from_numpy(host).cuda())
     good, _ = c.run(gb, True)
@@ -115,8 +191,9 @@ def test_nan_keys_reach_the_queries_that_see_them(gb):
     assert torch.equal(o[keep], good[keep])
 
 
-def test_bad_requests_are_flagged(gb):
-    c = Item(4, 2, 64, 30, [100, 200, 300, 100], 64000)
+@pytest.mark.parametrize("Tq", [30, 300])
+def test_bad_requests_are_flagged(gb, Tq):
+    c = Item(4, 2, 64, Tq, [100, 200, 300, 100], 64000)
     table = c.p.block_table.copy()
     table[1, 5] = c.p.num_pool_blocks
     lens = c.p.seq_lens.copy()
@@ -126,10 +203,13 @@ def test_bad_requests_are_flagged(gb):
     assert torch.isnan(o[2:]).all() and torch.isnan(lse[2:]).all()
     good, _ = c.run(gb, True)
     assert torch.equal(o[0], good[0])  # item 1 read another block: unspecified
+    if uses_rows(gb, c):
+        assert torch.isnan(o[1]).all() and torch.isnan(lse[1]).all()
 
 
-def test_a_wait_that_runs_out_is_reported(gb):
-    c = Item(4, 2, 128, 30, [100, 200], 65000)
+@pytest.mark.parametrize("Tq", [30, 300])
+def test_a_wait_that_runs_out_is_reported(gb, Tq):
+    c = Item(4, 2, 128, Tq, [100, 200], 65000)
     gb.test_set_failure(2_000_000, True)
     try:
         c.run(gb, True)
@@ -144,36 +224,34 @@ def test_a_wait_that_runs_out_is_reported(gb):
 
 
 def test_a_prompt_in_chunks_then_decode(gb):
-    """A prompt through the whole path in two chunks and one token more -- projection
-    rows, norm, rotation, quantised append, attention -- equals the prompt in one chunk."""
-    Hq, Hkv, D, T = 8, 2, 128, 200
+    """A prompt through the whole path in chunks -- projection rows, norm, rotation,
+    quantised append, attention -- against the prompt in one chunk."""
+    Hq, Hkv, D, T = 8, 2, 128, 320
     rows = to_dev(synth.normal_bf16(66000, (2, T + 1, Hq + 2 * Hkv, D)))
     cs = torch.from_numpy(ref.table(T + 1, D)).cuda()
     w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
-    table = to_dev_i32(synth.permutation(9, 28).reshape(2, 14))
+    table = to_dev_i32(synth.permutation(9, 44).reshape(2, 22))
+    v_max = float(rows[:, :, Hq + Hkv:].abs().max())
 
     def run(cuts):
-        pool = torch.zeros((28, Hkv, 18 * D), dtype=torch.uint8, device="cuda")
+        pool = torch.zeros((44, Hkv, 18 * D), dtype=torch.uint8, device="cuda")
         lens = torch.zeros(2, dtype=torch.int32, device="cuda")
         out = []
         for a, b in zip(cuts, cuts[1:]):
             q, k, v = rows[:, a:b].split([Hq, Hkv, Hkv], 2)
             new = torch.empty_like(lens)
             q, _ = gb.paged_kv4_append(q, k, v, pool, table, lens, cs, w, w, new_seq_lens=new)
-            o, lse = gb.paged_kv4_attn_prefill(q, pool, table, new, T + 1)
-            if b - a == 1:
-                o1, lse1 = gb.paged_kv4_attn_decode(q.squeeze(2), pool, table, new, T + 1)
-                # the two kernels round probabilities at different points: half a step
-                # of 2^-8 of sum p |v| each, |v| being at most 5.3 here
-                assert torch.all((o1 - o.squeeze(2)).abs() <= 5.3 * 2 ** -7)
-                assert torch.all((lse1 - lse.squeeze(2)).abs() <= 1e-3)
-            out.append((o, lse))
+            out.append(gb.paged_kv4_attn_prefill(q, pool, table, new, T + 1))
             lens = new
         return pool, torch.cat([o for o, _ in out], 2), torch.cat([l for _, l in out], 2)
 
-    pool, o, lse = run([0, T + 1])
-    pool2, o2, lse2 = run([0, 77, T, T + 1])
+    pool, o, lse = run([0, T + 1])                 # tiles
+    pool2, o2, lse2 = run([0, 270, T - 3, T, T + 1])  # tiles, rows, rows, one row
     assert gb.attn_device_status() == (gb.ATTN_OK, 0)
     assert torch.equal(pool, pool2)
-    # rows of a chunk see the same tiles in the same order
-    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    # tile rows see the same tiles in the same order
+    assert torch.equal(o[:, :, :270], o2[:, :, :270]) and torch.equal(lse[:, :, :270], lse2[:, :, :270])
+    # the kernels round probabilities and results at different points: 2^-8 of sum p |v| and
+    # of |O| each, twice; values are at most v_max (1 + 2^-5) in the cache
+    assert torch.all((o - o2).abs() <= 4 * 2.0 ** -8 * v_max * (1 + 2.0 ** -5))
+    assert torch.all((lse - lse2).abs() <= 1e-4)

@@ -209,15 +209,18 @@ def test_kv4_decode_refusals(kw, code):
     (dict(o=None), INV), (dict(bt=None), INV), (dict(sl=A16 + 2), INV), (dict(lse=A16 + 1), INV),
     (dict(causal=2), INV), (dict(scale=-1.0), INV), (dict(scale=float("inf")), INV),
     (dict(ml=-1), INV), (dict(mb=0), INV), (dict(nb=0), INV), (dict(nb=1 << 27), UNS),
-    (dict(mb=1 << 28), UNS), (dict(B=0), OK), (dict(Tq=0), OK),
+    (dict(mb=1 << 28), UNS), (dict(B=0), OK), (dict(Tq=0), OK), (dict(ws=None), INV),
+    (dict(ws=A16 + 16), INV), (dict(wsb=-1), INV),
 ])
 def test_kv4_prefill_refusals(kw, code):
     a = dict(q=A16, pool=A16, bt=A16, sl=A16, bs=16, B=4, Hq=12, Hkv=2, Tq=9, D=128, mb=512,
-             nb=1000, ml=8192, causal=1, scale=0.088, o=A16, lse=None) | kw
+             nb=1000, ml=8192, causal=1, scale=0.088, o=A16, lse=None, ws=A16, wsb=0) | kw
+    need = gb.paged_kv4_attn_prefill_workspace_size(a["B"], a["Hq"], a["Hkv"], a["Tq"], a["D"],
+                                                    a["ml"])
     assert gb.lib().paged_kv4_attn_prefill(a["q"], a["pool"], a["bt"], a["sl"], a["bs"], a["B"],
                                            a["Hq"], a["Hkv"], a["Tq"], a["D"], a["mb"], a["nb"],
                                            a["ml"], a["causal"], a["scale"], a["o"], a["lse"],
-                                           None) == code
+                                           a["ws"], max(0, need + a["wsb"]), None) == code
 
 
 # --------------------------------------------------------------------------- #
