@@ -415,9 +415,12 @@ int attend_rows(const void* q, const void* kv_pool, const int32_t* block_table,
 //   4 x 16/1 heads, 2000 keys, D 64:    Tq 16: 12 / 27   64: 26 / 27     96: 36 / 27
 //   1 x 32/8 heads, 100000 keys, D 128: Tq 1: 32 / 1235  64: 499 / 1236  128: 974 / 1236  192: 1462 / 1403
 // i.e. the crossing is near Tq = 30 with every SM busy and moves up as query heads are
-// fewer than the 152 SMs.
-bool by_rows(int B, int Hq, int Tq) {
+// fewer than the 152 SMs.  On short caches (3 x 8/2 heads, 500 keys, D 64: Tq 4: 7.2 / 11.3,
+// 37: 9.0 / 11.3; 300 keys: 7.2 / 9.9, 9.0 / 10.1) the rows' few microseconds do not pay for
+// their second launch and workspace on the host, unless the tiles need several rounds.
+bool by_rows(int B, int Hq, int Tq, int max_kv_len) {
   const int64_t units = static_cast<int64_t>(B) * Hq;
+  if (max_kv_len <= 512 && units <= 152) return false;
   return Tq <= 256 && Tq * (units < 152 ? units : 152) <= 4500;
 }
 
@@ -433,7 +436,7 @@ GBATTN_API size_t paged_kv4_attn_prefill_workspace_size(int B, int Hq, int Hkv, 
                                                         int max_kv_len) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Tq <= 0 || D <= 0 || max_kv_len < 0)
     return 0;
-  return by_rows(B, Hq, Tq) ? kv4_decode_workspace(B, Hq, Hkv, Tq, D, max_kv_len).bytes : 0;
+  return by_rows(B, Hq, Tq, max_kv_len) ? kv4_decode_workspace(B, Hq, Hkv, Tq, D, max_kv_len).bytes : 0;
 }
 
 GBATTN_API int paged_kv4_attn_decode(const void* q, const void* kv_pool,
@@ -484,7 +487,7 @@ GBATTN_API int paged_kv4_attn_prefill(const void* q, const void* kv_pool,
       static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim ||
       static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim)
     return ATTN_ERR_UNSUPPORTED;
-  if (by_rows(B, Hq, Tq))
+  if (by_rows(B, Hq, Tq, max_kv_len))
     return attend_rows(q, kv_pool, block_table, kv_lens, B, Hq, Hkv, Tq, D, max_blocks_per_seq,
                        num_pool_blocks, max_kv_len, causal, scale, o, lse, workspace,
                        workspace_bytes, stream);

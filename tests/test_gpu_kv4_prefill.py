@@ -26,9 +26,9 @@ def gb():
 
 
 class Item:
-    def __init__(self, Hq, Hkv, D, Tq, lens, seed):
+    def __init__(self, Hq, Hkv, D, Tq, lens, seed, max_len=0):
         cfg = synth.DecodeConfig("kv4p", len(lens), Hq, Hkv, D, 0, 1, 16, seed)
-        p = synth.paged_inputs(cfg, seq_lens=lens, max_seq_len=max(max(lens), 1))
+        p = synth.paged_inputs(cfg, seq_lens=lens, max_seq_len=max(max(lens), 1, max_len))
         self.p, self.scale, self.lens = p, cfg.softmax_scale, lens
         self.q_bits = synth.normal_bf16(seed + 11, (len(lens), Hq, Tq, D))
         self.q = to_dev(self.q_bits)
@@ -126,7 +126,7 @@ def check_rows(c, o, lse, causal, items=None):
 @pytest.mark.parametrize("Hq,Hkv,D,Tq,lens", ROWS)
 @pytest.mark.parametrize("causal", [True, False])
 def test_rows_match_the_oracle(gb, Hq, Hkv, D, Tq, lens, causal):
-    c = Item(Hq, Hkv, D, Tq, lens, 60500 + Tq)
+    c = Item(Hq, Hkv, D, Tq, lens, 60500 + Tq, max_len=1000)
     assert uses_rows(gb, c)
     o, lse = c.run(gb, causal)
     torch.cuda.synchronize()
@@ -172,10 +172,14 @@ def test_outputs_streams_and_graphs(gb):
         assert torch.equal(out, o) and torch.equal(l2, lse)
 
 
-@pytest.mark.parametrize("Tq", [20, 300])  # by rows, by tiles
-def test_nan_keys_reach_the_queries_that_see_them(gb, Tq):
+PATHS = [(20, 1000), (20, 0), (300, 0)]  # Tq, max_len: by rows, by tiles, by tiles
+
+
+@pytest.mark.parametrize("Tq,max_len", PATHS)
+def test_nan_keys_reach_the_queries_that_see_them(gb, Tq, max_len):
     D = 128
-    c = Item(4, 2, D, Tq, [Tq + 20] * 2, 63000)
+    c = Item(4, 2, D, Tq, [Tq + 20] * 2, 63000, max_len)
+    assert uses_rows(gb, c) == (max_len > 0)
     host = c.pool_host.copy()
     blk = c.p.block_table
     # token 30 of item 0: its key in head 0 (seen by queries 10 and on)
@@ -191,13 +195,13 @@ def test_nan_keys_reach_the_queries_that_see_them(gb, Tq):
     assert torch.equal(o[keep], good[keep])
 
 
-@pytest.mark.parametrize("Tq", [30, 300])
-def test_bad_requests_are_flagged(gb, Tq):
-    c = Item(4, 2, 64, Tq, [100, 200, 300, 100], 64000)
+@pytest.mark.parametrize("Tq,max_len", PATHS)
+def test_bad_requests_are_flagged(gb, Tq, max_len):
+    c = Item(4, 2, 64, Tq, [100, 200, 300, 100], 64000, max_len)
     table = c.p.block_table.copy()
     table[1, 5] = c.p.num_pool_blocks
     lens = c.p.seq_lens.copy()
-    lens[2], lens[3] = 301, -1
+    lens[2], lens[3] = c.p.max_seq_len + 1, -1
     o, lse = c.run(gb, True, table=to_dev_i32(table), lens=to_dev_i32(lens))
     assert gb.attn_device_status() == (gb.ATTN_ERR_DEVICE, 2 | 4)
     assert torch.isnan(o[2:]).all() and torch.isnan(lse[2:]).all()
@@ -207,9 +211,9 @@ def test_bad_requests_are_flagged(gb, Tq):
         assert torch.isnan(o[1]).all() and torch.isnan(lse[1]).all()
 
 
-@pytest.mark.parametrize("Tq", [30, 300])
-def test_a_wait_that_runs_out_is_reported(gb, Tq):
-    c = Item(4, 2, 128, Tq, [100, 200], 65000)
+@pytest.mark.parametrize("Tq,max_len", PATHS)
+def test_a_wait_that_runs_out_is_reported(gb, Tq, max_len):
+    c = Item(4, 2, 128, Tq, [100, 200], 65000, max_len)
     gb.test_set_failure(2_000_000, True)
     try:
         c.run(gb, True)
@@ -230,7 +234,7 @@ def test_a_prompt_in_chunks_then_decode(gb):
     rows = to_dev(synth.normal_bf16(66000, (2, T + 1, Hq + 2 * Hkv, D)))
     cs = torch.from_numpy(ref.table(T + 1, D)).cuda()
     w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
-    table = to_dev_i32(synth.permutation(9, 44).reshape(2, 22))
+    table = to_dev_i32(np.pad(synth.permutation(9, 44).reshape(2, 22), ((0, 0), (0, 48))))
     v_max = float(rows[:, :, Hq + Hkv:].abs().max())
 
     def run(cuts):
@@ -241,7 +245,7 @@ def test_a_prompt_in_chunks_then_decode(gb):
             q, k, v = rows[:, a:b].split([Hq, Hkv, Hkv], 2)
             new = torch.empty_like(lens)
             q, _ = gb.paged_kv4_append(q, k, v, pool, table, lens, cs, w, w, new_seq_lens=new)
-            out.append(gb.paged_kv4_attn_prefill(q, pool, table, new, T + 1))
+            out.append(gb.paged_kv4_attn_prefill(q, pool, table, new, 1000))
             lens = new
         return pool, torch.cat([o for o, _ in out], 2), torch.cat([l for _, l in out], 2)
 
