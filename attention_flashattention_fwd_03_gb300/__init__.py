@@ -786,7 +786,8 @@ def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
     with _On(device, stream) as handle:
         if workspace is None:
             need = paged_kv4_attn_decode_workspace_size(S, Hq, kv_pool.shape[1], D, max_seq_len)
-            workspace = _torch.empty((max(need, 256),), dtype=_torch.uint8, device=device)
+            if need:
+                workspace = _torch.empty((need,), dtype=_torch.uint8, device=device)
         if out is None:
             out = _torch.empty((S, Hq, D), dtype=_torch.bfloat16, device=device)
         if return_lse and lse is None:
@@ -794,7 +795,7 @@ def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
         st = (_lib or lib()).paged_kv4_attn_decode(
             q.data_ptr(), kv_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), 16, S,
             Hq, kv_pool.shape[1], D, block_table.shape[1], NB, max_seq_len, scale, out.data_ptr(),
-            _ptr(lse), workspace.data_ptr(), workspace.numel(), handle)
+            _ptr(lse), _ptr(workspace), workspace.numel() if workspace is not None else 0, handle)
     if st != ATTN_OK:
         raise GbAttnError("paged_kv4_attn_decode", st)
     return out, lse

@@ -359,9 +359,9 @@ int attend_rows(const void* q, const void* kv_pool, const int32_t* block_table,
                 const int32_t* seq_lens, int S, int Hq, int Hkv, int Tq, int D, int max_blocks,
                 int num_pool_blocks, int max_seq_len, int causal, float scale, void* o, float* lse,
                 void* workspace, size_t workspace_bytes, void* stream) {
-  if (!workspace || !aligned(workspace, 256)) return ATTN_ERR_INVALID_ARG;
   const Kv4DecodeWorkspace wl = kv4_decode_workspace(S, Hq, Hkv, Tq, D, max_seq_len);
-  if (workspace_bytes < wl.bytes) return ATTN_ERR_INVALID_ARG;
+  if (wl.bytes > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < wl.bytes))
+    return ATTN_ERR_INVALID_ARG;
   const Kv4Rows rows = kv4_rows(Hq, Hkv, Tq);
   if (static_cast<uint64_t>(kv4_max_steps(S, Hkv * rows.chunks, max_seq_len)) >= kMaxDim ||
       static_cast<uint64_t>(S) * Hkv * rows.rows >= kMaxDim / 2)
@@ -451,9 +451,9 @@ GBATTN_API int paged_kv4_attn_decode(const void* q, const void* kv_pool,
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   if (block_size != 16 || (D != 64 && D != 128) || Hq / Hkv > 16) return ATTN_ERR_UNSUPPORTED;
   if (num_seqs == 0) return ATTN_OK;
-  if (!q || !kv_pool || !block_table || !seq_lens || !o || !workspace) return ATTN_ERR_INVALID_ARG;
+  if (!q || !kv_pool || !block_table || !seq_lens || !o) return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(o, 16) || !aligned(block_table, 4) ||
-      !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+      !aligned(seq_lens, 4) || !aligned(lse, 4))
     return ATTN_ERR_INVALID_ARG;
   if (static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim ||
       static_cast<uint64_t>(num_seqs) * Hq >= kMaxDim / 2 ||

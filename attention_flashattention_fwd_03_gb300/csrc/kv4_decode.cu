@@ -57,6 +57,11 @@ constexpr int kBS = kPagedBlock;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStepBlocks = 4;  // blocks of one step: 64 tokens share a softmax update
+// Deal::kDirect up to this max_seq_len.  Device time in us, direct / split, by max_seq_len
+// (lengths from half of it): 5 x 16/1 heads, D 64: 256: 3.9 / 6.8, 1024: 7.6 / 6.8, 2048: 12.3
+// / 7.6; 64 x 12/2, D 128: 256: 5.2 / 9.2, 1024: 11.3 / 10.5, 2048: 18.8 / 15.5; 200 x 8/2, D
+// 128: 1024: 15.2 / 18.9, 4096: 48 / 43.  An eager call takes 20 us of host time instead of 25.
+constexpr int kDirectMaxLen = 1024;
 constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by > 2^8
 
 // Ring depth and CTAs per SM by query tiles (NQT = 1: groups of up to 8 query heads,
@@ -172,11 +177,18 @@ __device__ __forceinline__ void advance(Step& s, const Kv4DecodeParams& p) {
   while (s.nb == 0 && ++s.r < p.S) s.nb = blocks_of(p, p.seq_lens[s.r]);
 }
 
-template <int D, int NQT, bool MULTI>
+// How the work is dealt.  kSplit and kMulti (the rows of a chunk in several segments): the
+// batch's steps in equal ranges, a merge kernel after.  kDirect, for short caches: a CTA a
+// segment, whose warps take its steps in turn and join their results in shared memory; no
+// workspace and one launch.
+enum class Deal { kSplit, kMulti, kDirect };
+
+template <int D, int NQT, Deal DEAL>
 __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     kv4_decode_split_kernel(const uint8_t* __restrict__ pool, const Kv4DecodeParams p) {
   using F = Kv4<D>;
   using C = Shape<D, NQT>;
+  constexpr bool MULTI = DEAL == Deal::kMulti, DIRECT = DEAL == Deal::kDirect;
   constexpr int G = F::kGroups;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -188,7 +200,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   const uint32_t bars = sbase + C::kOffBar + warp * C::kStages * 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kOffAbort) + warp;
 
-  // the merge kernel may be scheduled now; it waits for this grid's results
+  // the merge kernel (or what else follows as a programmatic dependent) may be scheduled
+  // now; it waits for this grid's results
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (lane == 0) {
     for (int s = 0; s < C::kStages; ++s) mbar_init(bars + 8 * s, 1);
@@ -200,48 +213,63 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   // the preceding kernel's writes (an append's) are complete and visible past this point
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // ---------------- plan: total steps, range count, this warp's range ----------------
-  int total = 0;
-  for (int r0 = 0; r0 < p.S; r0 += 32)
-    if (r0 + lane < p.S) total += steps_of(blocks_of(p, p.seq_lens[r0 + lane]));
+  Step at{0, 0, 0, 0};  // this warp's first step, and how many steps it takes
+  int n_w = 0, k_w = 0;
+  if constexpr (DIRECT) {
+    at.r = blockIdx.x / p.segs;
+    at.h = blockIdx.x - at.r * p.segs;
+    at.i = warp;
+    at.nb = blocks_of(p, p.seq_lens[at.r]);
+    n_w = (steps_of(at.nb) - warp + kWarps - 1) / kWarps;
+  } else {
+    // ---------------- plan: total steps, range count, this warp's range ----------------
+    int total = 0;
+    for (int r0 = 0; r0 < p.S; r0 += 32)
+      if (r0 + lane < p.S) total += steps_of(blocks_of(p, p.seq_lens[r0 + lane]));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  total *= p.segs;  // below 2^31 for every length within max_seq_len
-  const int W = min(static_cast<int>(gridDim.x) * kWarps, total);
-  const int k_w = warp * gridDim.x + blockIdx.x;
-  if (k_w >= W) return;  // warps are independent: no barrier of the CTA follows
-  const int share = total / W, extra = total - share * W;  // the first `extra` take one more
-  const int lo = k_w * share + min(k_w, extra);
-  const int n_w = share + (k_w < extra ? 1 : 0);
-  Step at{0, 0, 0, 0};
-  {
-    int before = 0;  // steps of requests r0 - 1 and earlier
-    bool found = false;
-    for (int r0 = 0; r0 < p.S && !found; r0 += 32) {
-      const int r = r0 + lane;
-      const int nb = r < p.S ? blocks_of(p, p.seq_lens[r]) : 0;
-      const int own = steps_of(nb) * p.segs;
-      int incl = own;
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total *= p.segs;  // below 2^31 for every length within max_seq_len
+    const int W = min(static_cast<int>(gridDim.x) * kWarps, total);
+    k_w = warp * gridDim.x + blockIdx.x;
+    if (k_w >= W) return;  // warps are independent: no barrier of the CTA follows
+    const int share = total / W, extra = total - share * W;  // the first `extra` take one more
+    const int lo = k_w * share + min(k_w, extra);
+    n_w = share + (k_w < extra ? 1 : 0);
+    {
+      int before = 0;  // steps of requests r0 - 1 and earlier
+      bool found = false;
+      for (int r0 = 0; r0 < p.S && !found; r0 += 32) {
+        const int r = r0 + lane;
+        const int nb = r < p.S ? blocks_of(p, p.seq_lens[r]) : 0;
+        const int own = steps_of(nb) * p.segs;
+        int incl = own;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        incl += before;
+        const unsigned hit = __ballot_sync(0xffffffffu, incl - own <= lo && lo < incl);
+        if (hit) {
+          found = true;
+          const int src = __ffs(hit) - 1;
+          const int rest = lo - __shfl_sync(0xffffffffu, incl - own, src);
+          at.nb = __shfl_sync(0xffffffffu, nb, src);
+          at.r = r0 + src;
+          at.h = rest / steps_of(at.nb);
+          at.i = rest - at.h * steps_of(at.nb);
+        }
+        before = __shfl_sync(0xffffffffu, incl, 31);
       }
-      incl += before;
-      const unsigned hit = __ballot_sync(0xffffffffu, incl - own <= lo && lo < incl);
-      if (hit) {
-        found = true;
-        const int src = __ffs(hit) - 1;
-        const int rest = lo - __shfl_sync(0xffffffffu, incl - own, src);
-        at.nb = __shfl_sync(0xffffffffu, nb, src);
-        at.r = r0 + src;
-        at.h = rest / steps_of(at.nb);
-        at.i = rest - at.h * steps_of(at.nb);
-      }
-      before = __shfl_sync(0xffffffffu, incl, 31);
+      if (!found) return;  // lengths changed under the kernel
     }
-    if (!found) return;  // lengths changed under the kernel
   }
+  auto next = [&](Step& st) {
+    if constexpr (DIRECT)
+      st.i += kWarps;
+    else
+      advance(st, p);
+  };
 
   // ---------------- copies: one step ahead in table entries, kStages in data ----------------
   Step ps = at;
@@ -253,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
                ? p.block_table[static_cast<size_t>(ps.r) * p.max_blocks + ps.i * kStepBlocks + lane]
                : 0;
   };
-  int phys = entry();
+  int phys = p_left > 0 ? entry() : 0;
   uint32_t stage_bad = 0;  // bit s: stage s holds a block the table could not translate
   auto issue = [&]() {     // copies step ps, then reads the table entries of the next one
     const int s = p_stage, n = ps.blocks();
@@ -271,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     ++issued;
     p_stage = s + 1 == C::kStages ? 0 : s + 1;
     if (--p_left > 0) {
-      advance(ps, p);
+      next(ps);
       if (ps.r >= p.S)
         p_left = 0;  // lengths changed under the kernel: nothing valid to read
       else
@@ -298,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   auto begin_piece = [&]() {
     L = p.seq_lens[c.r];
     pbad = false;
-    if (c.i == 0 && lane == 0) p.seg_first[c.r * p.segs + c.h] = k_w;
+    if (!DIRECT && c.i == 0 && lane == 0) p.seg_first[c.r * p.segs + c.h] = k_w;
     size_t q0 = static_cast<size_t>(c.r) * p.Hkv * p.rows + static_cast<size_t>(c.h) * p.rows;
     if constexpr (MULTI) {
       const int h = c.h / p.chunks, x0 = (c.h - h * p.chunks) * (8 * NQT);
@@ -355,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
         acc[j][nt][0] = acc[j][nt][1] = acc[j][nt][2] = acc[j][nt][3] = 0.f;
     }
   };
-  begin_piece();
+  begin_piece();  // (DIRECT: also by a warp without a step, whose sums stay empty)
 
   while (c_left > 0) {
     const int s = c_stage;
@@ -534,6 +562,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     if (p_left > 0) issue();
 
     --c_left;
+    if constexpr (DIRECT) {
+      c.i += kWarps;
+      continue;
+    }
     if (!c.last() && c_left > 0) {
       ++c.i;
       continue;
@@ -581,6 +613,63 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     for (int i = taken; i < issued; ++i)
       if (!(p.withhold_copy && i == 0))
         mbar_wait_quiet(bars + 8 * (i % C::kStages), (i / C::kStages) & 1, 500000000ull);
+  if constexpr (DIRECT) {
+    // ---- join the warps' sums; the rings are done with ----
+    constexpr int R = 8 * NQT;
+    float* po = reinterpret_cast<float*>(smem);       // [kWarps][R][D] O / 64, not normalised
+    float* pm = po + kWarps * R * D;                  // [kWarps][R] maximum, in log2 units
+    float* pl = pm + kWarps * R;                      // [kWarps][R] sum
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NQT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float lsum = l_q[nt][e];
+        lsum += __shfl_xor_sync(0xffffffffu, lsum, 4);
+        lsum += __shfl_xor_sync(0xffffffffu, lsum, 8);
+        lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
+        const int q = warp * R + 8 * nt + 2 * t4 + e;
+#pragma unroll
+        for (int w = 0; w < G; ++w)
+          *reinterpret_cast<float4*>(po + q * D + 4 * g + 32 * w) =
+              make_float4(acc[2 * w][nt][e], acc[2 * w][nt][2 + e], acc[2 * w + 1][nt][e],
+                          acc[2 * w + 1][nt][2 + e]);
+        if (g == 0) {
+          // a block that the table could not translate makes the whole request NaN
+          pm[q] = m_q[nt][e] == -INFINITY ? -INFINITY : m_q[nt][e] * sl2[nt][e];
+          pl[q] = pbad ? __int_as_float(0x7fc00000) : lsum;
+        }
+      }
+    }
+    __syncthreads();
+    const bool bad_len = at.nb == 0 && L != 0;
+    if (bad_len && threadIdx.x == 0) raise_flag(p.flags, DEVFLAG_BAD_SEQLEN);
+    constexpr int TPR = D / 2;  // threads of a row, two channels each
+    const size_t row0_out = (static_cast<size_t>(at.r) * p.segs + at.h) * p.rows;
+    for (int q = threadIdx.x / TPR; q < p.rows; q += kThreads / TPR) {
+      const int d = threadIdx.x % TPR * 2;
+      float M = pm[q];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) M = fmaxf(M, pm[w * R + q]);
+      const float Ms = M == -INFINITY ? 0.f : M;
+      float tot = 0.f, x0 = 0.f, x1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(pm[w * R + q] - Ms);
+        const float2 v = *reinterpret_cast<const float2*>(po + (w * R + q) * D + d);
+        tot = fmaf(f, pl[w * R + q], tot);
+        x0 = fmaf(f, v.x, x0);
+        x1 = fmaf(f, v.y, x1);
+      }
+      const float inv = tot == 0.f ? 0.f : 64.f / tot;
+      float lse = Ms * 0.6931471805599453f + logf(tot);  // (log 0 = -inf: an empty cache)
+      x0 *= inv;
+      x1 *= inv;
+      if (bad_len) x0 = x1 = lse = __int_as_float(0x7fc00000);
+      reinterpret_cast<uint32_t*>(p.o)[((row0_out + q) * D + d) / 2] = pack_bf16x2(x0, x1);
+      if (p.lse != nullptr && d == 0) p.lse[row0_out + q] = lse;
+    }
+  }
 }
 
 // LSE = M + ln sum_j e^{LSE_j - M}, O = sum_j e^{LSE_j - LSE} O_j over the pieces of one
@@ -688,15 +777,19 @@ __global__ void __launch_bounds__(MW * 32) kv4_decode_merge_kernel(const Kv4Deco
 
 template <int D, int NQT>
 cudaError_t prepare() {
-  const cudaError_t e =
-      cudaFuncSetAttribute(kv4_decode_split_kernel<D, NQT, false>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D, NQT>::kSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(kv4_decode_split_kernel<D, NQT, true>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D, NQT>::kSmem);
+  cudaError_t e = cudaSuccess;
+  auto set = [&](const void* fn) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Shape<D, NQT>::kSmem);
+  };
+  set(reinterpret_cast<const void*>(kv4_decode_split_kernel<D, NQT, Deal::kSplit>));
+  set(reinterpret_cast<const void*>(kv4_decode_split_kernel<D, NQT, Deal::kMulti>));
+  set(reinterpret_cast<const void*>(kv4_decode_split_kernel<D, NQT, Deal::kDirect>));
+  return e;
 }
 
-template <int D, int NQT, bool MULTI>
+template <int D, int NQT, Deal DEAL>
 cudaError_t launch_split(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms,
                          cudaStream_t stream) {
   // kCtasPerSm CTAs per SM, fewer when even the shortest ranges would not fill them
@@ -705,29 +798,34 @@ cudaError_t launch_split(const uint8_t* pool, const Kv4DecodeParams& p, int num_
   // a CTA a range first, then more ranges a CTA (the kernel deals them in that order)
   const long long steps = kv4_max_steps(p.S, p.segs, p.max_seq_len);
   const long long want = steps < 1 ? 1 : (steps < num_sms ? steps : num_sms + (steps - num_sms) / kWarps);
+  const unsigned grid = DEAL == Deal::kDirect ? static_cast<unsigned>(p.S) * p.segs
+                                              : static_cast<unsigned>(want < cap ? want : cap);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(want < cap ? want : cap));
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Shape<D, NQT>::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_decode_split_kernel<D, NQT, MULTI>, pool, p);
+  return cudaLaunchKernelEx(&cfg, kv4_decode_split_kernel<D, NQT, DEAL>, pool, p);
 }
 
 template <int D>
 cudaError_t launch(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms, cudaStream_t stream) {
   const bool multi = p.Tq > 1 || p.chunks > 1;
   cudaError_t e;
+  if (kv4_direct(p.Tq, p.max_seq_len))
+    return p.piece_rows <= 8 ? launch_split<D, 1, Deal::kDirect>(pool, p, num_sms, stream)
+                             : launch_split<D, 2, Deal::kDirect>(pool, p, num_sms, stream);
   if (p.piece_rows <= 8)
-    e = multi ? launch_split<D, 1, true>(pool, p, num_sms, stream)
-              : launch_split<D, 1, false>(pool, p, num_sms, stream);
+    e = multi ? launch_split<D, 1, Deal::kMulti>(pool, p, num_sms, stream)
+              : launch_split<D, 1, Deal::kSplit>(pool, p, num_sms, stream);
   else
-    e = multi ? launch_split<D, 2, true>(pool, p, num_sms, stream)
-              : launch_split<D, 2, false>(pool, p, num_sms, stream);
+    e = multi ? launch_split<D, 2, Deal::kMulti>(pool, p, num_sms, stream)
+              : launch_split<D, 2, Deal::kSplit>(pool, p, num_sms, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -764,9 +862,12 @@ Kv4Rows kv4_rows(int Hq, int Hkv, int Tq) {
   return r;
 }
 
+bool kv4_direct(int Tq, int max_seq_len) { return Tq == 1 && max_seq_len <= kDirectMaxLen; }
+
 Kv4DecodeWorkspace kv4_decode_workspace(int S, int Hq, int Hkv, int Tq, int D, int max_seq_len) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  Kv4DecodeWorkspace w;
+  Kv4DecodeWorkspace w{};
+  if (kv4_direct(Tq, max_seq_len)) return w;
   const Kv4Rows r = kv4_rows(Hq, Hkv, Tq);
   const long long segs = static_cast<long long>(S) * Hkv * r.chunks;
   const long long steps = kv4_max_steps(S, Hkv * r.chunks, max_seq_len);

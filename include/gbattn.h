@@ -380,7 +380,7 @@ int paged_kv4_gather(const void *kv_pool, const int32_t *block_table, const int3
 /*
  * Bytes of scratch workspace paged_kv4_attn_decode needs for these sizes: one partial
  * output (D fp32) and LSE per query head for each of at most 2048 + num_seqs * Hkv
- * pieces of the batch.
+ * pieces of the batch; 0 for short caches, which need none.
  */
 size_t paged_kv4_attn_decode_workspace_size(int num_seqs, int Hq, int Hkv, int D,
                                             int max_seq_len);
@@ -398,6 +398,7 @@ size_t paged_kv4_attn_prefill_workspace_size(int B, int Hq, int Hkv, int Tq, int
  *
  *   kv_pool       [num_pool_blocks, Hkv, 18 D] bytes
  *   workspace     >= paged_kv4_attn_decode_workspace_size(...) bytes, 256-byte aligned
+ *                 (may be NULL where that is 0); no initialisation
  *
  * Everything else, the device-side checks included, as in paged_attn_decode.  A NaN in
  * a key of the cache makes that request's O and LSE NaN for the heads that read it, a

@@ -93,10 +93,14 @@ CASES = [
 @pytest.mark.parametrize("lens,Hq,Hkv,D", CASES)
 def test_decode_matches_the_oracle(gb, lens, Hq, Hkv, D):
     c = Cache(lens, Hq, Hkv, D, 50000 + sum(lens))
-    o, lse = gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, c.p.max_seq_len, scale=c.scale)
-    torch.cuda.synchronize()
-    assert gb.attn_device_status() == (gb.ATTN_OK, 0)
-    check(c, o, lse)
+    # up to 1024 tokens one launch without a workspace, above that the split and its merge
+    for bound in {c.p.max_seq_len, max(c.p.max_seq_len, 1025)}:
+        need = gb.paged_kv4_attn_decode_workspace_size(len(lens), Hq, Hkv, D, bound)
+        assert (need == 0) == (bound <= 1024)
+        o, lse = gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, bound, scale=c.scale)
+        torch.cuda.synchronize()
+        assert gb.attn_device_status() == (gb.ATTN_OK, 0)
+        check(c, o, lse)
 
 
 @pytest.mark.parametrize("gain", [0.01, 30.0])
@@ -128,8 +132,9 @@ def test_the_decode_workload(gb):
 def test_many_short_requests(gb):
     lens = list(synth.uniform_ints(52000, 300, 0, 40))
     c = Cache(lens, 4, 2, 64, 52001, max_len=512)
-    o, lse = gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, 512, scale=c.scale)
-    check(c, o, lse)
+    for bound in (512, 2000):
+        o, lse = gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, bound, scale=c.scale)
+        check(c, o, lse)
 
 
 def test_one_long_request_at_large_offsets(gb):
@@ -147,7 +152,8 @@ def test_one_long_request_at_large_offsets(gb):
     assert torch.equal(k, k0)
 
 
-def test_nan_in_the_cache_stays_where_it_is_read(gb):
+@pytest.mark.parametrize("bound", [70, 1100])
+def test_nan_in_the_cache_stays_where_it_is_read(gb, bound):
     lens = [50, 60, 70]
     c = Cache(lens, 4, 2, 128, 54000)
     host = c.pool_host.copy()
@@ -155,8 +161,8 @@ def test_nan_in_the_cache_stays_where_it_is_read(gb):
     blk = c.p.block_table
     host[blk[1, 2], 0, 8 * D + 3 * 8:8 * D + 3 * 8 + 2] = [0xC0, 0x7F]       # K, head 0, group 0
     host[blk[2, 1], 1, 17 * D + 5 * 8 + 2:17 * D + 5 * 8 + 4] = [0xC0, 0x7F]  # V, head 1, group 1
-    o, lse = gb.paged_kv4_attn_decode(c.q, torch.from_numpy(host).cuda(), c.table, c.lens,
-                                      c.p.max_seq_len, scale=c.scale)
+    o, lse = gb.paged_kv4_attn_decode(c.q, torch.from_numpy(host).cuda(), c.table, c.lens, bound,
+                                      scale=c.scale)
     check(c, o, lse, rows=[0])
     nan = from_dev(o) != from_dev(o)
     assert nan[1, :2].all() and not nan[1, 2:].any()
@@ -166,15 +172,16 @@ def test_nan_in_the_cache_stays_where_it_is_read(gb):
     assert ln == [[False] * 4, [True, True, False, False], [False] * 4]
 
 
-def test_bad_requests_are_flagged(gb):
+@pytest.mark.parametrize("bound", [400, 1100])
+def test_bad_requests_are_flagged(gb, bound):
     c = Cache([100, 200, 300, 400], 4, 2, 64, 55000)
     table = c.p.block_table.copy()
     table[1, 5] = c.p.num_pool_blocks
     table[1, 12] = -3
     lens = c.p.seq_lens.copy()
-    lens[2] = 401
+    lens[2] = bound + 1
     lens[3] = -1
-    o, lse = gb.paged_kv4_attn_decode(c.q, c.pool, to_dev_i32(table), to_dev_i32(lens), 400,
+    o, lse = gb.paged_kv4_attn_decode(c.q, c.pool, to_dev_i32(table), to_dev_i32(lens), bound,
                                       scale=c.scale)
     torch.cuda.synchronize()
     assert gb.attn_device_status() == (gb.ATTN_ERR_DEVICE, 2 | 4)
@@ -182,17 +189,18 @@ def test_bad_requests_are_flagged(gb):
     check(c, o, lse, rows=[0])
 
 
-def test_a_wait_that_runs_out_is_reported(gb):
+@pytest.mark.parametrize("bound", [200, 1100])
+def test_a_wait_that_runs_out_is_reported(gb, bound):
     c = Cache([100, 200], 4, 2, 64, 56000)
     gb.test_set_failure(2_000_000, True)
     try:
-        gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, 200, scale=c.scale)
+        gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, bound, scale=c.scale)
         torch.cuda.synchronize()
         st, flags = gb.attn_device_status()
     finally:
         gb.test_set_failure(0, False)
     assert st == gb.ATTN_ERR_DEVICE and flags & 1
-    o, lse = gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, 200, scale=c.scale)
+    o, lse = gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, bound, scale=c.scale)
     check(c, o, lse)
     assert gb.attn_device_status() == (gb.ATTN_OK, 0)
 

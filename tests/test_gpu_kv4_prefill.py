@@ -135,7 +135,7 @@ def test_rows_match_the_oracle(gb, Hq, Hkv, D, Tq, lens, causal):
 
 
 def test_one_drafted_token_equals_the_decode(gb):
-    c = Item(12, 2, 128, 1, [1, 300, 4000], 61500)
+    c = Item(12, 2, 128, 1, [1, 300, 4000], 61500)  # (past the decode's one-launch form)
     o, lse = c.run(gb, True)
     o2, lse2 = gb.paged_kv4_attn_decode(c.q.squeeze(2), c.pool, c.table, c.kv_lens, 4000,
                                         scale=c.scale)
