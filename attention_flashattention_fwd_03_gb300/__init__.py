@@ -61,7 +61,7 @@ EXPORTS = (
 
 _lock = threading.Lock()
 _lib = None
-_torch = _Tensor = None  # torch and torch.Tensor, once an operator that needs them is called
+_torch = _Tensor = _bf16 = _f32 = _i32 = _u8 = None  # set by _load_torch
 
 
 class GbAttnError(RuntimeError):
@@ -373,10 +373,10 @@ def paged_kv_gather(pool, block_table, seq_lens, max_seq_len: int, out=None, str
     return out
 
 
-# The operators below are called between kernels of a few microseconds, so their
-# argument checks first test everything at once and go into detail only to name what is
-# wrong (measured on the GPU's host, a call of paged_qkv_append took 43 us before and
-# takes @APP@ us now; its kernel runs for 5).
+# The operators below are called between kernels of a few microseconds, so a call looks
+# its arguments over with a few plain comparisons first and goes into detail only to name
+# what is wrong.  (Host time of a paged_qkv_append, whose kernel runs for 3 us: 43 us with
+# the checks written as above, 25 us as they are.)
 
 class _On:
     """The device, and the stream if one is given, current for allocations and launches
@@ -411,9 +411,9 @@ def _check(name, t, dtype, shape, device):
     _check_tensor(name, t, dtype, shape, device)
 
 
-def _is_rows(t, bf16, device):
+def _is_rows(t, device):
     """Whether t is a [B, T, H, D] bf16 operand: any strides but contiguous channels."""
-    return (t.__class__ is _Tensor and t.dtype is bf16 and t.dim() == 4 and
+    return (t.__class__ is _Tensor and t.dtype is _bf16 and t.dim() == 4 and
             (t.stride(3) == 1 or t.shape[3] == 1) and t.device == device)
 
 
@@ -422,8 +422,8 @@ def _check_rows(name, t, shape, device):
     free dimension.  Metadata checks only."""
     if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != _torch.bfloat16:
-        raise ValueError(f"{name} must be {_torch.bfloat16}, got {t.dtype}")
+    if t.dtype != _bf16:
+        raise ValueError(f"{name} must be {_bf16}, got {t.dtype}")
     if t.dim() != 4 or any(n is not None and n != m for n, m in zip(shape, t.shape)):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.shape[3] > 1 and t.stride(3) != 1:
@@ -433,17 +433,13 @@ def _check_rows(name, t, shape, device):
 
 
 @functools.lru_cache(maxsize=1024)
-def _stride_array(b, t, h):
-    return (ctypes.c_int64 * 3)(b, t, h)
+def _stride_array(shape, strides):
+    """Batch, token and head strides for the C ABI (0 where a dimension has one entry)."""
+    return (ctypes.c_int64 * 3)(*(st if n > 1 else 0 for n, st in zip(shape[:3], strides)))
 
 
 def _strides(t):
-    """Batch, token and head strides for the C ABI (0 where a dimension has one entry)."""
-    if t is None:
-        return None
-    B, T, H, _ = t.shape
-    b, s, h, _ = t.stride()
-    return _stride_array(b if B > 1 else 0, s if T > 1 else 0, h if H > 1 else 0)
+    return _stride_array(t.shape, t.stride()) if t is not None else None
 
 
 def _ptr(t):
@@ -453,24 +449,25 @@ def _ptr(t):
 def _check_rope(cos_sin, q_weight, k_weight, positions, B, T, D, device):
     """Checks the norm and rotation operands; returns (rot_dim, max_pos)."""
     if q_weight is not None:
-        _check("q_weight", q_weight, _torch.bfloat16, (D,), device)
+        _check("q_weight", q_weight, _bf16, (D,), device)
     if k_weight is not None:
-        _check("k_weight", k_weight, _torch.bfloat16, (D,), device)
+        _check("k_weight", k_weight, _bf16, (D,), device)
     if positions is not None:
-        _check("positions", positions, _torch.int32, (B, T), device)
+        _check("positions", positions, _i32, (B, T), device)
     if cos_sin is None:
         return 0, 0
     shape = cos_sin.shape if isinstance(cos_sin, _Tensor) else None
-    _check("cos_sin", cos_sin, _torch.float32, shape, device)
+    _check("cos_sin", cos_sin, _f32, shape, device)
     if len(shape) != 2 or shape[0] == 0 or shape[1] == 0:
         raise ValueError("cos_sin must be a non-empty [max_pos, rot_dim] table")
     return shape[1], shape[0]
 
 
 def _load_torch():
-    global _torch, _Tensor
+    global _torch, _Tensor, _bf16, _f32, _i32, _u8
     import torch
     _torch, _Tensor = torch, torch.Tensor
+    _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _first(*tensors):
@@ -498,10 +495,9 @@ def qkv_norm_rope(q, k, v=None, cos_sin=None, q_weight=None, k_weight=None, eps:
     norm); ``positions`` [B,T] int32 (None: 0 .. T-1).
     """
     some = _first(q, k, v)
-    bf16 = _torch.bfloat16
     device = some.device
     for name, t in (("q", q), ("k", k), ("v", v)):
-        if t is not None and not _is_rows(t, bf16, device):
+        if t is not None and not _is_rows(t, device):
             _check_rows(name, t, (None,) * 4, device)
     B, T, _, D = some.shape
     Hq = q.shape[2] if q is not None else 0
@@ -516,16 +512,16 @@ def qkv_norm_rope(q, k, v=None, cos_sin=None, q_weight=None, k_weight=None, eps:
         if t.shape != (B, T, heads, D):
             _check_rows(name, t, (B, T, heads, D), device)
         if out is not None:
-            _check(name + "_out", out, bf16, (B, heads, T, D), device)
+            _check(name + "_out", out, _bf16, (B, heads, T, D), device)
     rot, max_pos = _check_rope(cos_sin, q_weight, k_weight, positions, B, T, D, device)
     _require_cuda(device)
     with _On(device, stream) as handle:
         if q_out is None and q is not None:
-            q_out = _torch.empty((B, Hq, T, D), dtype=bf16, device=device)
+            q_out = _torch.empty((B, Hq, T, D), dtype=_bf16, device=device)
         if k_out is None and k is not None:
-            k_out = _torch.empty((B, Hkv, T, D), dtype=bf16, device=device)
+            k_out = _torch.empty((B, Hkv, T, D), dtype=_bf16, device=device)
         if v_out is None and v is not None:
-            v_out = _torch.empty((B, Hkv, T, D), dtype=bf16, device=device)
+            v_out = _torch.empty((B, Hkv, T, D), dtype=_bf16, device=device)
         st = (_lib or lib()).qkv_norm_rope(
             _ptr(q), _ptr(k), _ptr(v), _strides(q), _strides(k), _strides(v), _ptr(q_weight),
             _ptr(k_weight), _ptr(cos_sin), _ptr(positions), B, T, Hq, Hkv, D, rot, max_pos,
@@ -552,7 +548,6 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
     operand without a weight.
     """
     some = _first(dq_out, dk_out, dv_out)
-    bf16 = _torch.bfloat16
     device = some.device
     if some.dim() != 4:
         raise ValueError("gradients must be 4-d tensors")
@@ -566,7 +561,7 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
             if d is not None:
                 raise ValueError(f"{name} is given without the gradient of its output")
             continue
-        _check(name + "_out", g, bf16, (B, heads, T, D), device)
+        _check(name + "_out", g, _bf16, (B, heads, T, D), device)
         if d is not None:
             _check_rows(name, d, (B, T, heads, D), device)
     rot, max_pos = _check_rope(cos_sin, q_weight, k_weight, positions, B, T, D, device)
@@ -578,12 +573,12 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
             continue
         if x is None:
             raise ValueError(f"{name} is needed for the gradient of its norm")
-        if not _is_rows(x, bf16, device) or x.shape != (B, T, heads, D):
+        if not _is_rows(x, device) or x.shape != (B, T, heads, D):
             _check_rows(name, x, (B, T, heads, D), device)
         if dw is not None:
-            _check(f"d{name}_weight", dw, _torch.float32, (D,), device)
+            _check(f"d{name}_weight", dw, _f32, (D,), device)
     if workspace is not None:
-        _check_tensor("workspace", workspace, _torch.uint8, None, device)
+        _check_tensor("workspace", workspace, _u8, None, device)
     _require_cuda(device)
     if q_weight is None:
         q = None
@@ -593,21 +588,21 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
         if dq is None and dk is None and dv is None:
             nq, nk = (Hq if dq_out is not None else 0), (Hkv if dk_out is not None else 0)
             nv = Hkv if dv_out is not None else 0
-            fused = _torch.empty((B, T, nq + nk + nv, D), dtype=bf16, device=device)
+            fused = _torch.empty((B, T, nq + nk + nv, D), dtype=_bf16, device=device)
             dq = fused[:, :, :nq] if nq else None
             dk = fused[:, :, nq:nq + nk] if nk else None
             dv = fused[:, :, nq + nk:] if nv else None
         else:
             dq, dk, dv = (d if d is not None or g is None else
-                          _torch.empty((B, T, g.shape[1], D), dtype=bf16, device=device)
+                          _torch.empty((B, T, g.shape[1], D), dtype=_bf16, device=device)
                           for d, g in ((dq, dq_out), (dk, dk_out), (dv, dv_out)))
         if dq_weight is None and q_weight is not None:
-            dq_weight = _torch.empty((D,), dtype=_torch.float32, device=device)
+            dq_weight = _torch.empty((D,), dtype=_f32, device=device)
         if dk_weight is None and k_weight is not None:
-            dk_weight = _torch.empty((D,), dtype=_torch.float32, device=device)
+            dk_weight = _torch.empty((D,), dtype=_f32, device=device)
         if workspace is None and (q_weight is not None or k_weight is not None):
             need = qkv_norm_rope_bwd_workspace_size(B, T, D)
-            workspace = _torch.empty((max(need, 256),), dtype=_torch.uint8, device=device)
+            workspace = _torch.empty((max(need, 256),), dtype=_u8, device=device)
         st = (_lib or lib()).qkv_norm_rope_bwd(
             _ptr(dq_out), _ptr(dk_out), _ptr(dv_out), _ptr(q), _ptr(k), _strides(q), _strides(k),
             _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), _ptr(positions), B, T, Hq, Hkv, D, rot,
@@ -622,28 +617,27 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
 def _append(op, pools, q, k, v, block_table, seq_lens, cos_sin, q_weight, k_weight, eps,
             interleaved, positions, q_out, new_seq_lens, stream):
     _first(k)
-    bf16, i32 = _torch.bfloat16, _torch.int32
     device = k.device
-    if not _is_rows(k, bf16, device):
+    if not _is_rows(k, device):
         _check_rows("k", k, (None,) * 4, device)
     S, Tn, Hkv, D = k.shape
-    if not _is_rows(v, bf16, device) or v.shape != (S, Tn, Hkv, D):
+    if not _is_rows(v, device) or v.shape != (S, Tn, Hkv, D):
         _check_rows("v", v, (S, Tn, Hkv, D), device)
     Hq = 0
     if q is not None:
-        if not _is_rows(q, bf16, device):
+        if not _is_rows(q, device):
             _check_rows("q", q, (S, Tn, None, D), device)
         Hq = q.shape[2]
         if q.shape != (S, Tn, Hq, D):
             _check_rows("q", q, (S, Tn, None, D), device)
-    _check("seq_lens", seq_lens, i32, (S,), device)
-    _check_tensor("block_table", block_table, i32, None, device)
+    _check("seq_lens", seq_lens, _i32, (S,), device)
+    _check_tensor("block_table", block_table, _i32, None, device)
     if block_table.dim() != 2 or block_table.shape[0] != S:
         raise ValueError("inconsistent append shapes")
     if len(pools) == 2:
         _check_bf16("k_pool", pools[0], 4, device)
         shape = pools[0].shape
-        _check("v_pool", pools[1], bf16, shape, device)
+        _check("v_pool", pools[1], _bf16, shape, device)
         NB, Hkv2, bs, D2 = shape
         if Hkv2 != Hkv or D2 != D:
             raise ValueError("inconsistent append shapes")
@@ -653,13 +647,13 @@ def _append(op, pools, q, k, v, block_table, seq_lens, cos_sin, q_weight, k_weig
     if q_out is not None:
         if q is None:
             raise ValueError("q_out is given without q")
-        _check("q_out", q_out, bf16, (S, Hq, Tn, D), device)
+        _check("q_out", q_out, _bf16, (S, Hq, Tn, D), device)
     if new_seq_lens is not None:
-        _check("new_seq_lens", new_seq_lens, i32, (S,), device)
+        _check("new_seq_lens", new_seq_lens, _i32, (S,), device)
     _require_cuda(device)
     with _On(device, stream) as handle:
         if q is not None and q_out is None:
-            q_out = _torch.empty((S, Hq, Tn, D), dtype=bf16, device=device)
+            q_out = _torch.empty((S, Hq, Tn, D), dtype=_bf16, device=device)
         st = getattr(_lib or lib(), op)(
             _ptr(q), k.data_ptr(), v.data_ptr(), _strides(q), _strides(k), _strides(v),
             _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), _ptr(positions),
@@ -690,7 +684,7 @@ def _check_kv4(name, pool, Hkv, D, device):
     """A 4-bit pool [NB, Hkv, 18 D] uint8; returns NB."""
     if isinstance(pool, _Tensor) and pool.dim() != 3:
         raise ValueError(f"{name} must be a 3-d tensor")
-    _check_tensor(name, pool, _torch.uint8, None, device)
+    _check_tensor(name, pool, _u8, None, device)
     NB, heads, chunk = pool.shape
     if Hkv is not None and (heads != Hkv or chunk != 18 * D):
         raise ValueError(f"{name} must have shape (blocks, {Hkv}, {18 * D}), got {tuple(pool.shape)}")
@@ -718,20 +712,20 @@ def paged_kv4_gather(kv_pool, block_table, seq_lens, max_seq_len: int, k_out=Non
     _, Hkv, chunk = kv_pool.shape
     D = chunk // 18
     for name, t in (("block_table", block_table), ("seq_lens", seq_lens)):
-        _check_tensor(name, t, _torch.int32, None, device)
+        _check_tensor(name, t, _i32, None, device)
     if seq_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != seq_lens.shape[0]:
         raise ValueError("inconsistent gather shapes")
     S = seq_lens.shape[0]
     shape = (S, Hkv, max_seq_len, D)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
-            _check(name, t, _torch.bfloat16, shape, device)
+            _check(name, t, _bf16, shape, device)
     _require_cuda(device)
     with _On(device, stream) as handle:
         if k_out is None:
-            k_out = _torch.zeros(shape, dtype=_torch.bfloat16, device=device)
+            k_out = _torch.zeros(shape, dtype=_bf16, device=device)
         if v_out is None:
-            v_out = _torch.zeros(shape, dtype=_torch.bfloat16, device=device)
+            v_out = _torch.zeros(shape, dtype=_bf16, device=device)
         st = (_lib or lib()).paged_kv4_gather(
             kv_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), 16, S, Hkv, D,
             block_table.shape[1], NB, max_seq_len, k_out.data_ptr(), v_out.data_ptr(), handle)
@@ -748,17 +742,17 @@ def _check_kv4_attention(q, kv_pool, block_table, lens, rows, out, lse):
     if q.dim() != ndim:
         raise ValueError(f"q must be a {ndim}-d tensor")
     shape = q.shape
-    _check("q", q, _torch.bfloat16, shape, device)
+    _check("q", q, _bf16, shape, device)
     NB = _check_kv4("kv_pool", kv_pool, None, None, device)
-    _check_tensor("block_table", block_table, _torch.int32, None, device)
-    _check("the lengths", lens, _torch.int32, shape[:1], device)
+    _check_tensor("block_table", block_table, _i32, None, device)
+    _check("the lengths", lens, _i32, shape[:1], device)
     if kv_pool.shape[2] != 18 * shape[-1] or block_table.dim() != 2 or \
             block_table.shape[0] != shape[0]:
         raise ValueError("inconsistent paged attention shapes")
     if out is not None:
-        _check("out", out, _torch.bfloat16, shape, device)
+        _check("out", out, _bf16, shape, device)
     if lse is not None:
-        _check("lse", lse, _torch.float32, shape[:-1], device)
+        _check("lse", lse, _f32, shape[:-1], device)
     _require_cuda(device)
     return device, NB
 
@@ -773,25 +767,25 @@ def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
                           return_lse: bool = True, stream=None):
     """Single-token decode against the 4-bit paged cache through the C ABI.
 
-    q [S,Hq,D] bf16, kv_pool [NB,Hkv,18*D] uint8, block_table [S,max_blocks] int32,
-    seq_lens [S] int32 (all CUDA) -> (o [S,Hq,D] bf16, lse [S,Hq] fp32).
+    q [S,Hq,D] _bf16, kv_pool [NB,Hkv,18*D] uint8, block_table [S,max_blocks] int32,
+    seq_lens [S] int32 (all CUDA) -> (o [S,Hq,D] _bf16, lse [S,Hq] fp32).
     ``workspace`` (uint8 CUDA tensor) is allocated here when not given.
     """
     device, NB = _check_kv4_attention(q, kv_pool, block_table, seq_lens, 0, out, lse)
     S, Hq, D = q.shape
     if workspace is not None:
-        _check_tensor("workspace", workspace, _torch.uint8, None, device)
+        _check_tensor("workspace", workspace, _u8, None, device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     with _On(device, stream) as handle:
         if workspace is None:
             need = paged_kv4_attn_decode_workspace_size(S, Hq, kv_pool.shape[1], D, max_seq_len)
             if need:
-                workspace = _torch.empty((need,), dtype=_torch.uint8, device=device)
+                workspace = _torch.empty((need,), dtype=_u8, device=device)
         if out is None:
-            out = _torch.empty((S, Hq, D), dtype=_torch.bfloat16, device=device)
+            out = _torch.empty((S, Hq, D), dtype=_bf16, device=device)
         if return_lse and lse is None:
-            lse = _torch.empty((S, Hq), dtype=_torch.float32, device=device)
+            lse = _torch.empty((S, Hq), dtype=_f32, device=device)
         st = (_lib or lib()).paged_kv4_attn_decode(
             q.data_ptr(), kv_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), 16, S,
             Hq, kv_pool.shape[1], D, block_table.shape[1], NB, max_seq_len, scale, out.data_ptr(),
@@ -813,7 +807,7 @@ def paged_kv4_attn_prefill(q, kv_pool, block_table, kv_lens, max_kv_len: int,
 
     q [B,Hq,Tq,D] bf16 (the Tq newest tokens of each item), kv_pool [NB,Hkv,18*D]
     uint8, block_table [B,max_blocks] int32, kv_lens [B] int32 (all CUDA) -> (o
-    [B,Hq,Tq,D] bf16, lse [B,Hq,Tq] fp32).  Query i of item b sits at logical
+    [B,Hq,Tq,D] _bf16, lse [B,Hq,Tq] fp32).  Query i of item b sits at logical
     position kv_lens[b] - Tq + i.  ``workspace`` (uint8 CUDA tensor, needed for short
     chunks) is allocated here when not given.
     """
@@ -821,18 +815,18 @@ def paged_kv4_attn_prefill(q, kv_pool, block_table, kv_lens, max_kv_len: int,
     B, Hq, Tq, D = q.shape
     Hkv = kv_pool.shape[1]
     if workspace is not None:
-        _check_tensor("workspace", workspace, _torch.uint8, None, device)
+        _check_tensor("workspace", workspace, _u8, None, device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     with _On(device, stream) as handle:
         if workspace is None:
             need = paged_kv4_attn_prefill_workspace_size(B, Hq, Hkv, Tq, D, max_kv_len)
             if need:
-                workspace = _torch.empty((need,), dtype=_torch.uint8, device=device)
+                workspace = _torch.empty((need,), dtype=_u8, device=device)
         if out is None:
-            out = _torch.empty((B, Hq, Tq, D), dtype=_torch.bfloat16, device=device)
+            out = _torch.empty((B, Hq, Tq, D), dtype=_bf16, device=device)
         if return_lse and lse is None:
-            lse = _torch.empty((B, Hq, Tq), dtype=_torch.float32, device=device)
+            lse = _torch.empty((B, Hq, Tq), dtype=_f32, device=device)
         st = (_lib or lib()).paged_kv4_attn_prefill(
             q.data_ptr(), kv_pool.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), 16, B,
             Hq, Hkv, Tq, D, block_table.shape[1], NB, max_kv_len, 1 if causal else 0, scale,
