@@ -388,6 +388,8 @@ class _On:
         self.device, self.stream, self.inner = device, stream, None
 
     def __enter__(self):
+        if self.stream is not None and self.stream.device != self.device:
+            raise ValueError(f"stream must be on {self.device}, got {self.stream.device}")
         if self.stream is not None or _torch.cuda.current_device() != self.device.index:
             self.inner = (_torch.cuda.device(self.device), _torch.cuda.stream(self.stream))
             for c in self.inner:
@@ -503,7 +505,6 @@ def qkv_norm_rope(q, k, v=None, cos_sin=None, q_weight=None, k_weight=None, eps:
     Hq = q.shape[2] if q is not None else 0
     kv = k if k is not None else v
     Hkv = kv.shape[2] if kv is not None else 0
-    outs = []
     for name, t, heads, out in (("q", q, Hq, q_out), ("k", k, Hkv, k_out), ("v", v, Hkv, v_out)):
         if t is None:
             if out is not None:
@@ -525,7 +526,7 @@ def qkv_norm_rope(q, k, v=None, cos_sin=None, q_weight=None, k_weight=None, eps:
         st = (_lib or lib()).qkv_norm_rope(
             _ptr(q), _ptr(k), _ptr(v), _strides(q), _strides(k), _strides(v), _ptr(q_weight),
             _ptr(k_weight), _ptr(cos_sin), _ptr(positions), B, T, Hq, Hkv, D, rot, max_pos,
-            1 if interleaved else 0, eps, _ptr(q_out), _ptr(k_out), _ptr(v_out), handle)
+            1 if interleaved else 0, float(eps), _ptr(q_out), _ptr(k_out), _ptr(v_out), handle)
     if st != ATTN_OK:
         raise GbAttnError("qkv_norm_rope", st)
     return q_out, k_out, v_out
@@ -606,7 +607,7 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
         st = (_lib or lib()).qkv_norm_rope_bwd(
             _ptr(dq_out), _ptr(dk_out), _ptr(dv_out), _ptr(q), _ptr(k), _strides(q), _strides(k),
             _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), _ptr(positions), B, T, Hq, Hkv, D, rot,
-            max_pos, 1 if interleaved else 0, eps, _ptr(dq), _ptr(dk), _ptr(dv), _strides(dq),
+            max_pos, 1 if interleaved else 0, float(eps), _ptr(dq), _ptr(dk), _ptr(dv), _strides(dq),
             _strides(dk), _strides(dv), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
             workspace.numel() if workspace is not None else 0, handle)
     if st != ATTN_OK:
@@ -659,7 +660,7 @@ def _append(op, pools, q, k, v, block_table, seq_lens, cos_sin, q_weight, k_weig
             _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), _ptr(positions),
             *[t.data_ptr() for t in pools], block_table.data_ptr(), seq_lens.data_ptr(),
             _ptr(new_seq_lens), bs, S, Tn, Hq, Hkv, D, block_table.shape[1], NB, rot, max_pos,
-            1 if interleaved else 0, eps, _ptr(q_out), handle)
+            1 if interleaved else 0, float(eps), _ptr(q_out), handle)
     if st != ATTN_OK:
         raise GbAttnError(op, st)
     return q_out, new_seq_lens
@@ -715,7 +716,7 @@ def paged_kv4_gather(kv_pool, block_table, seq_lens, max_seq_len: int, k_out=Non
         _check_tensor(name, t, _i32, None, device)
     if seq_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != seq_lens.shape[0]:
         raise ValueError("inconsistent gather shapes")
-    S = seq_lens.shape[0]
+    S, max_seq_len = seq_lens.shape[0], _length(max_seq_len)
     shape = (S, Hkv, max_seq_len, D)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
@@ -732,6 +733,14 @@ def paged_kv4_gather(kv_pool, block_table, seq_lens, max_seq_len: int, k_out=Non
     if st != ATTN_OK:
         raise GbAttnError("paged_kv4_gather", st)
     return k_out, v_out
+
+
+def _length(n):
+    """A bound on lengths as the C ABI's int."""
+    n = int(n)
+    if not 0 <= n < 1 << 31:
+        raise ValueError(f"length bound out of range: {n}")
+    return n
 
 
 def _check_kv4_attention(q, kv_pool, block_table, lens, rows, out, lse):
@@ -767,16 +776,16 @@ def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
                           return_lse: bool = True, stream=None):
     """Single-token decode against the 4-bit paged cache through the C ABI.
 
-    q [S,Hq,D] _bf16, kv_pool [NB,Hkv,18*D] uint8, block_table [S,max_blocks] int32,
-    seq_lens [S] int32 (all CUDA) -> (o [S,Hq,D] _bf16, lse [S,Hq] fp32).
+    q [S,Hq,D] bf16, kv_pool [NB,Hkv,18*D] uint8, block_table [S,max_blocks] int32,
+    seq_lens [S] int32 (all CUDA) -> (o [S,Hq,D] bf16, lse [S,Hq] fp32).
     ``workspace`` (uint8 CUDA tensor) is allocated here when not given.
     """
     device, NB = _check_kv4_attention(q, kv_pool, block_table, seq_lens, 0, out, lse)
     S, Hq, D = q.shape
+    max_seq_len = _length(max_seq_len)
     if workspace is not None:
         _check_tensor("workspace", workspace, _u8, None, device)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     with _On(device, stream) as handle:
         if workspace is None:
             need = paged_kv4_attn_decode_workspace_size(S, Hq, kv_pool.shape[1], D, max_seq_len)
@@ -807,17 +816,16 @@ def paged_kv4_attn_prefill(q, kv_pool, block_table, kv_lens, max_kv_len: int,
 
     q [B,Hq,Tq,D] bf16 (the Tq newest tokens of each item), kv_pool [NB,Hkv,18*D]
     uint8, block_table [B,max_blocks] int32, kv_lens [B] int32 (all CUDA) -> (o
-    [B,Hq,Tq,D] _bf16, lse [B,Hq,Tq] fp32).  Query i of item b sits at logical
+    [B,Hq,Tq,D] bf16, lse [B,Hq,Tq] fp32).  Query i of item b sits at logical
     position kv_lens[b] - Tq + i.  ``workspace`` (uint8 CUDA tensor, needed for short
     chunks) is allocated here when not given.
     """
     device, NB = _check_kv4_attention(q, kv_pool, block_table, kv_lens, 1, out, lse)
     B, Hq, Tq, D = q.shape
-    Hkv = kv_pool.shape[1]
+    Hkv, max_kv_len = kv_pool.shape[1], _length(max_kv_len)
     if workspace is not None:
         _check_tensor("workspace", workspace, _u8, None, device)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     with _On(device, stream) as handle:
         if workspace is None:
             need = paged_kv4_attn_prefill_workspace_size(B, Hq, Hkv, Tq, D, max_kv_len)
