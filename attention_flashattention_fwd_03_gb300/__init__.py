@@ -1,6 +1,7 @@
 """GB300 (sm_103a) fused attention: Python binding of the C ABI in include/gbattn.h.
 
-Only argument marshalling happens here; every step of the computation runs in
+Only argument marshalling happens here (for the usual call of the newer operators in
+_binding, compiled from csrc/binding.cpp); every step of the computation runs in
 the library's CUDA kernels.  torch is used for device memory and streams.  If
 the library is missing or cannot be loaded, or an operation reports an error,
 an exception is raised -- there is no fallback implementation.
@@ -22,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import math
 import os
 import threading
@@ -61,7 +63,7 @@ EXPORTS = (
 
 _lock = threading.Lock()
 _lib = None
-_torch = _Tensor = _bf16 = _f32 = _i32 = _u8 = None  # set by _load_torch
+_torch = _Tensor = _bf16 = _f32 = _i32 = _u8 = _quick = None  # set by _load_torch
 
 
 class GbAttnError(RuntimeError):
@@ -373,10 +375,11 @@ def paged_kv_gather(pool, block_table, seq_lens, max_seq_len: int, out=None, str
     return out
 
 
-# The operators below are called between kernels of a few microseconds, so a call looks
-# its arguments over with a few plain comparisons first and goes into detail only to name
-# what is wrong.  (Host time of a paged_qkv_append, whose kernel runs for 3 us: 43 us with
-# the checks written as above, 25 us as they are.)
+# The operators below are called between kernels of a few microseconds.  The usual call
+# therefore goes through _binding (csrc/binding.cpp), which makes the same checks in compiled
+# code and returns None for everything else: other streams and devices, and whatever is
+# wrong with the arguments, which the Python code then handles and names.  (Host time of a
+# paged_qkv_append, whose kernel runs for 3 us: 8.5 us, and 25 us the long way.)
 
 class _On:
     """The device, and the stream if one is given, current for allocations and launches
@@ -470,6 +473,34 @@ def _load_torch():
     import torch
     _torch, _Tensor = torch, torch.Tensor
     _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+    _load_quick()
+
+
+def _load_quick():
+    """Binds _quick, the module _binding, to the library and torch's current device
+    and stream, if it was built."""
+    global _quick
+    h, _quick = lib(), None
+    if not hasattr(_torch._C, "_cuda_getDevice"):  # a torch without CUDA
+        return
+    try:
+        m = importlib.import_module("._binding", __name__)
+        names = ("qkv_norm_rope", "qkv_norm_rope_bwd", "qkv_norm_rope_bwd_workspace_size",
+                 "paged_qkv_append", "paged_kv4_append", "paged_kv4_gather",
+                 "paged_kv4_attn_decode", "paged_kv4_attn_decode_workspace_size",
+                 "paged_kv4_attn_prefill", "paged_kv4_attn_prefill_workspace_size")
+        m.setup(_torch.__version__, _torch._C._cuda_getDevice, _torch._C._cuda_getCurrentRawStream,
+                *(ctypes.cast(getattr(h, n), ctypes.c_void_p).value for n in names))
+    except ImportError:  # not built, or against another torch
+        return
+    _quick = m
+
+
+def _done(op, r):
+    """The result of a quick call that was made."""
+    if r.__class__ is tuple:
+        return r
+    raise GbAttnError(op, r)
 
 
 def _first(*tensors):
@@ -496,6 +527,13 @@ def qkv_norm_rope(q, k, v=None, cos_sin=None, q_weight=None, k_weight=None, eps:
     each position (None: no rotation); ``q_weight``/``k_weight`` [D] bf16 (None: no
     norm); ``positions`` [B,T] int32 (None: 0 .. T-1).
     """
+    if _torch is None:
+        _load_torch()
+    if _quick is not None and stream is None:
+        r = _quick.rope(q, k, v, cos_sin, q_weight, k_weight, eps, interleaved, positions, q_out,
+                        k_out, v_out)
+        if r is not None:
+            return _done("qkv_norm_rope", r)
     some = _first(q, k, v)
     device = some.device
     for name, t in (("q", q), ("k", k), ("v", v)):
@@ -548,6 +586,14 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
     the gradient of a fused projection.  The weight gradients [D] are fp32, None for an
     operand without a weight.
     """
+    if _torch is None:
+        _load_torch()
+    if _quick is not None and stream is None and dq is None and dk is None and \
+            dv is None and dq_weight is None and dk_weight is None and workspace is None:
+        r = _quick.rope_bwd(dq_out, dk_out, dv_out, q, k, cos_sin, q_weight, k_weight, eps,
+                            interleaved, positions)
+        if r is not None:
+            return _done("qkv_norm_rope_bwd", r)
     some = _first(dq_out, dk_out, dv_out)
     device = some.device
     if some.dim() != 4:
@@ -617,6 +663,16 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
 
 def _append(op, pools, q, k, v, block_table, seq_lens, cos_sin, q_weight, k_weight, eps,
             interleaved, positions, q_out, new_seq_lens, stream):
+    if _torch is None:
+        _load_torch()
+    if _quick is not None and stream is None:
+        quick = _quick.append4 if op == "paged_kv4_append" else _quick.append
+        r = quick(q, k, v, pools[0], pools[1], block_table, seq_lens, cos_sin, q_weight, k_weight,
+                  eps, interleaved, positions, q_out, new_seq_lens)
+        if r is not None:
+            return _done(op, r)
+    if op == "paged_kv4_append":
+        pools = pools[:1]
     _first(k)
     device = k.device
     if not _is_rows(k, device):
@@ -699,7 +755,7 @@ def paged_kv4_append(q, k, v, kv_pool, block_table, seq_lens, cos_sin=None, q_we
                      q_out=None, new_seq_lens=None, stream=None):
     """paged_qkv_append into the 4-bit cache: kv_pool [NB,Hkv,18*D] uint8 is written in
     place (the format is described in include/gbattn.h)."""
-    return _append("paged_kv4_append", (kv_pool,), q, k, v, block_table, seq_lens, cos_sin,
+    return _append("paged_kv4_append", (kv_pool, None), q, k, v, block_table, seq_lens, cos_sin,
                    q_weight, k_weight, eps, interleaved, positions, q_out, new_seq_lens, stream)
 
 
@@ -707,6 +763,12 @@ def paged_kv4_gather(kv_pool, block_table, seq_lens, max_seq_len: int, k_out=Non
                      stream=None):
     """The values the 4-bit cache holds, in logical order: k_out, v_out
     [S,Hkv,max_seq_len,D] bf16 (rows past a request's length are left as they were)."""
+    if _torch is None:
+        _load_torch()
+    if _quick is not None and stream is None:
+        r = _quick.gather(kv_pool, block_table, seq_lens, max_seq_len, k_out, v_out)
+        if r is not None:
+            return _done("paged_kv4_gather", r)
     _first(kv_pool)
     device = kv_pool.device
     NB = _check_kv4("kv_pool", kv_pool, None, None, device)
@@ -780,6 +842,13 @@ def paged_kv4_attn_decode(q, kv_pool, block_table, seq_lens, max_seq_len: int,
     seq_lens [S] int32 (all CUDA) -> (o [S,Hq,D] bf16, lse [S,Hq] fp32).
     ``workspace`` (uint8 CUDA tensor) is allocated here when not given.
     """
+    if _torch is None:
+        _load_torch()
+    if _quick is not None and stream is None:
+        r = _quick.decode(q, kv_pool, block_table, seq_lens, max_seq_len, scale, out, lse,
+                          workspace, return_lse)
+        if r is not None:
+            return _done("paged_kv4_attn_decode", r)
     device, NB = _check_kv4_attention(q, kv_pool, block_table, seq_lens, 0, out, lse)
     S, Hq, D = q.shape
     max_seq_len = _length(max_seq_len)
@@ -820,6 +889,13 @@ def paged_kv4_attn_prefill(q, kv_pool, block_table, kv_lens, max_kv_len: int,
     position kv_lens[b] - Tq + i.  ``workspace`` (uint8 CUDA tensor, needed for short
     chunks) is allocated here when not given.
     """
+    if _torch is None:
+        _load_torch()
+    if _quick is not None and stream is None:
+        r = _quick.prefill(q, kv_pool, block_table, kv_lens, max_kv_len, scale, out, lse, workspace,
+                           return_lse, causal)
+        if r is not None:
+            return _done("paged_kv4_attn_prefill", r)
     device, NB = _check_kv4_attention(q, kv_pool, block_table, kv_lens, 1, out, lse)
     B, Hq, Tq, D = q.shape
     Hkv, max_kv_len = kv_pool.shape[1], _length(max_kv_len)

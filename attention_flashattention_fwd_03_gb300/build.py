@@ -3,6 +3,10 @@
 Each .cu under csrc/ compiles in its own nvcc process (in parallel); the objects
 link into one shared library with the CUDA runtime linked statically, so the
 library only needs the NVIDIA driver at run time.  No torch, no cmake.
+
+_binding, an extension module built beside it with the host compiler against the installed torch, is the
+quick way from Python into the library (csrc/binding.cpp).  The package works without it,
+at the interpreter's pace, so a machine on which it does not build gets a warning.
 """
 
 from __future__ import annotations
@@ -12,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +26,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgbattn.so")
 SOURCES = ["attn_fwd.cu", "paged_decode.cu", "kv_cache.cu", "norm_rope.cu", "kv4_cache.cu", "kv4_decode.cu",
            "api.cu", "api_rope.cu", "decode_noalloc.cu"]
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,10 +51,38 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files if os.path.isfile(f))
 
 
+def build_binding() -> str | None:
+    """Compiles _binding; returns what went wrong, or None."""
+    try:
+        import torch
+    except ImportError as e:
+        return str(e)
+    root = os.path.dirname(torch.__file__)
+    inc, libs = os.path.join(root, "include"), os.path.join(root, "lib")
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
+           f'-DBUILT_FOR_TORCH="{torch.__version__}"',
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", BINDING_SOURCE, "-o",
+           tmp, "-L", libs, "-lc10", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{libs}"]
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        return str(e)
+    if res.returncode != 0:
+        return res.stderr
+    os.replace(tmp, BINDING)
+    return None
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
+    if os.path.exists(BINDING):
+        os.remove(BINDING)  # never older than the library it calls
     cc = nvcc()
 
     def compile_one(src):
@@ -57,13 +92,17 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
         return src, obj, res
 
     objs = []
-    with concurrent.futures.ThreadPoolExecutor(max_workers=jobs or len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=jobs or len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding)
         for src, obj, res in ex.map(compile_one, SOURCES):
             if res.returncode != 0:
                 raise RuntimeError(f"nvcc failed on {src}:\n{res.stdout}\n{res.stderr}")
             if verbose_ptxas:
                 sys.stderr.write(res.stderr)
             objs.append(obj)
+        wrong = binding.result()
+        if wrong:
+            sys.stderr.write(f"warning: _binding was not built, calls go the slower way:\n{wrong}\n")
     tmp = LIB + ".tmp"
     cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static", "-ldl", "-lpthread",
                                                          "-lrt"]

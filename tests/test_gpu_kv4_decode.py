@@ -264,3 +264,52 @@ def test_decode_steps_from_projections_replayed_as_a_graph(gb):
         mag = np.einsum("hgt,htd->hgd", p, np.abs(vf)).reshape(Hq, D)
         tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -16) * mag
         assert np.all(np.abs(from_dev(eager.o)[r] - want) <= tol)
+
+
+def test_both_bindings_give_the_same_bits(gb, monkeypatch):
+    """The compiled way into the library and the Python code behind it, with what may be
+    given and what may be left out; refused calls name the fault either way."""
+    gb._load_torch()
+    assert gb._quick is not None
+    S, Hq, Hkv, D, L = 4, 8, 2, 128, 1500
+    c = Cache([1, 700, 1500, 33], Hq, Hkv, D, 58000)
+    q4 = to_dev(synth.normal_bf16(58100, (S, Hq, 3, D)))
+    out, lse = torch.empty_like(c.q), torch.empty((S, Hq), device="cuda")
+    ws = torch.empty(gb.paged_kv4_attn_decode_workspace_size(S, Hq, Hkv, D, L), dtype=torch.uint8,
+                     device="cuda")
+    cache = (c.pool, c.table, c.lens, L)
+
+    def calls():
+        yield gb.paged_kv4_attn_decode(c.q, *cache)
+        yield gb.paged_kv4_attn_decode(c.q, *cache, scale=0.2, return_lse=False)
+        yield gb.paged_kv4_attn_decode(c.q, *cache, scale=1, out=out, lse=lse, workspace=ws)
+        yield gb.paged_kv4_attn_prefill(q4, *cache, causal=True)
+        yield gb.paged_kv4_attn_prefill(q4, *cache, causal=False, return_lse=False)
+        yield gb.paged_kv4_gather(*cache)
+        yield gb.paged_kv4_gather(*cache, k_out=torch.zeros((S, Hkv, L, D), dtype=torch.bfloat16,
+                                                            device="cuda"),
+                                  v_out=torch.zeros((S, Hkv, L, D), dtype=torch.bfloat16,
+                                                    device="cuda"))
+
+    def results():
+        return [tuple(None if t is None else t.clone() for t in r) for r in calls()]
+
+    quick = results()
+    with pytest.raises(ValueError):
+        gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens[:2], L)
+    with pytest.raises(ValueError):
+        gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, L, workspace=ws.float())
+    with pytest.raises(gb.GbAttnError):
+        gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, L, workspace=ws[:256])
+    with pytest.raises(gb.GbAttnError):
+        gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, L, scale=float("nan"))
+    with pytest.raises(TypeError):
+        gb.paged_kv4_attn_decode([1], c.pool, c.table, c.lens, L)
+    monkeypatch.setattr(gb, "_quick", None)
+    for a, b in zip(quick, results()):
+        assert len(a) == len(b)
+        for x, y in zip(a, b):
+            assert (x is None) == (y is None)
+            # (values past the end are left as they were: NaN keeps its bits)
+            assert x is None or torch.equal(x.view(torch.int16 if x.dtype == torch.bfloat16 else torch.int32),
+                                            y.view(torch.int16 if y.dtype == torch.bfloat16 else torch.int32))

@@ -28,10 +28,15 @@ torch = pytest.importorskip("torch")
 HALF = 2.0 ** -8
 
 
-@pytest.fixture(scope="module")
-def gb():
+@pytest.fixture(params=["compiled binding", "Python binding"])
+def gb(request, monkeypatch):
     import attention_flashattention_fwd_03_gb300 as gb
     gb.lib()
+    gb._load_torch()
+    if request.param == "Python binding":
+        monkeypatch.setattr(gb, "_quick", None)
+    elif gb._quick is None:
+        pytest.fail("_binding was not built")
     return gb
 
 
