@@ -15,6 +15,7 @@
 #include "api.h"
 #include "gbattn.h"
 #include "internal.h"
+#include "norm_rope.h"
 #include "ptx.cuh"
 
 namespace gbattn {
@@ -63,6 +64,7 @@ int device_state(DeviceState** out) {
       st.status = ATTN_ERR_UNSUPPORTED;  // kernels are built for sm_103a only
     } else if (prepare_attn_fwd() != cudaSuccess || prepare_paged_decode() != cudaSuccess ||
                prepare_kv_cache() != cudaSuccess || prepare_kv4_decode() != cudaSuccess ||
+               prepare_norm_rope() != cudaSuccess ||
                cudaGetSymbolAddress(reinterpret_cast<void**>(&st.flags), g_flags_word) !=
                    cudaSuccess) {
       st.status = ATTN_ERR_CUDA;

@@ -9,6 +9,8 @@
 // the loads of four passes are in flight together.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "kv4.cuh"
 #include "norm_rope.cuh"
 #include "norm_rope.h"
@@ -315,138 +317,264 @@ cudaError_t launch_norm_rope(NormRopeParams p, int D, RowSink sink, int num_sms,
 // summed over the CTA in shared memory and written as one partial per CTA; a second kernel
 // adds the partials.  No atomics: the order of every sum depends on the sizes alone.
 //
-// Memory-bound in kind (x and g read, dx written), but with 16 warps an SM the loads of a
-// unit do not all hide behind the sums of another: 57 us on 4 x 2048 tokens of 16/16 heads,
-// D 128 (269 MB; 40 us at the copy rate; the sum over the partials is about 3 of them).
-// Passes unrolled x CTAs an SM: 4 x 2 57 us, 6 x 2 64, 2 x 3 71, 1 x 4 71, 8 x 3 of four
-// warps 67; one token with all its operands a unit 59.
+// Memory-bound (x and g read, dx written).  A warp streams its units pass by pass, a pass
+// being 2 KB of g, 2 KB of x and the token's row of the table, through its own ring of
+// stages in shared memory: the copies of the next passes are in flight while one is
+// computed, which registers alone did not allow (57 us so).  4 x 2048 tokens of 16/16
+// heads, D 128: 46 us for 269 MB, 86 % of the copy rate, about 3 of them the sum over the
+// partials.  Two stages of four row sets 46.3 us, three 48.6; six stages of two sets 81,
+// two of six 59, both with a pass's set-up costing more than its rows.
 namespace {
 
 constexpr int kBwdWarps = 8;
 constexpr int kBwdThreads = kBwdWarps * 32;
+constexpr int kBwdCtasPerSm = 2;
 constexpr int kBwdMaxGrid = 304;  // two CTAs on each of 152 SMs
-constexpr int kBwdUnroll = 4;     // passes whose loads are in flight together
+constexpr int kBwdUnroll = 4;  // row sets of a pass
+constexpr int kBwdStages = 2;
 
-// Query or key rows of one token: dx from the gradient g (head stride gh) and, with a
-// weight, the input x; adds this lane's terms of the weight gradient to dw.
 template <int D>
-__device__ __forceinline__ void norm_rope_bwd_rows(const TokenCtx& t, const uint16_t* g,
-                                                   long long gh, const uint16_t* x, long long sh,
-                                                   const uint16_t* w, int heads, uint16_t* dx,
-                                                   long long dh, Lane8& dw) {
+struct BwdShape {
+  static constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a set
+  static constexpr int kHalf = kBwdUnroll * 512;             // bytes of a pass of g or of x
+  static constexpr int kStage = 2 * kHalf + 4 * D;           // and a row of the table
+  static constexpr int kSmem = kBwdWarps * kBwdStages * kStage;
+  static_assert(kSmem >= kBwdWarps * kRows * 2 * D * 4, "the ring also holds the warps' sums");
+};
+
+// A row set of queries or keys: dx from the gradient and, with a weight, the input (both in
+// shared memory); adds this lane's terms of the weight gradient to dw.
+template <int D, bool INTERLEAVED, bool NORM>
+__device__ __forceinline__ void norm_rope_bwd_set(const TokenCtx& t, const uint16_t* g,
+                                                  const uint16_t* x, const uint2 (&w)[2],
+                                                  uint16_t* dx, bool write, Lane8& dw) {
   constexpr int LANES = D / 8;
-  constexpr int ROWS = 32 / LANES;
-  Lane8 wf{};
-  if (w) wf = widen8(ld8(w + t.ch.c0), ld8(w + t.ch.c1));
-  for (int r0 = 0; r0 < heads; r0 += ROWS * kBwdUnroll) {
-    uint2 ga[kBwdUnroll], gc[kBwdUnroll], xa[kBwdUnroll], xc[kBwdUnroll];
+  Lane8 v = widen8(ld8(g + t.ch.c0), ld8(g + t.ch.c1));
+  if (t.ch.rotates) rotate8(v, t.planes, INTERLEAVED);
+  if constexpr (NORM) {
+    const Lane8 x8 = widen8(ld8(x + t.ch.c0), ld8(x + t.ch.c1));
+    const Lane8 vw = mul8(v, widen8(w[0], w[1]));
+    // both sums of the row at once: x^2 and (dy w) x
+    const float ss = row_sum<LANES>(dot8(x8, x8)), dot = row_sum<LANES>(dot8(vw, x8));
+    const float r = rsqrtf(ss * (1.f / D) + t.eps);
+    const float m = -dot * r * (1.f / D);
+    const Lane8 xh = scale8(x8, r);
 #pragma unroll
-    for (int u = 0; u < kBwdUnroll; ++u) {
-      const int h = r0 + u * ROWS + t.sub;
-      ga[u] = gc[u] = xa[u] = xc[u] = make_uint2(0, 0);
-      if (h < heads) {
-        ga[u] = ld8(g + h * gh + t.ch.c0);
-        gc[u] = ld8(g + h * gh + t.ch.c1);
-        if (w) {
-          xa[u] = ld8(x + h * sh + t.ch.c0);
-          xc[u] = ld8(x + h * sh + t.ch.c1);
-        }
-      }
+    for (int i = 0; i < 4; ++i) {
+      dw.v[i] = __ffma2_rn(v.v[i], xh.v[i], dw.v[i]);  // 0 for a row past the end: its g is 0
+      v.v[i] = __ffma2_rn(xh.v[i], make_float2(m, m), vw.v[i]);
     }
-#pragma unroll
-    for (int u = 0; u < kBwdUnroll; ++u) {
-      if (r0 + u * ROWS >= heads) break;
-      const int h = r0 + u * ROWS + t.sub;
-      Lane8 v = widen8(ga[u], gc[u]);
-      if (t.ch.rotates) rotate8(v, t.planes, t.interleaved);
-      if (w) {
-        const Lane8 x8 = widen8(xa[u], xc[u]);
-        const Lane8 vw = mul8(v, wf);
-        // both sums of the row at once: x^2 and (dy w) x
-        const float ss = row_sum<LANES>(dot8(x8, x8)), dot = row_sum<LANES>(dot8(vw, x8));
-        const float r = rsqrtf(ss * (1.f / D) + t.eps);
-        const float m = -dot * r * (1.f / D);
-        const Lane8 xh = scale8(x8, r);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dw.v[i] = __ffma2_rn(v.v[i], xh.v[i], dw.v[i]);  // 0 for a row past the end: its g is 0
-          v.v[i] = __ffma2_rn(xh.v[i], make_float2(m, m), vw.v[i]);
-        }
-        v = scale8(v, r);
-      }
-      round8(v, ga[u], gc[u]);
-      if (!t.live) ga[u] = gc[u] = make_uint2(kBf16NanPair, kBf16NanPair);
-      if (h < heads) {
-        st8(dx + h * dh + t.ch.c0, ga[u]);
-        st8(dx + h * dh + t.ch.c1, gc[u]);
-      }
-    }
+    v = scale8(v, r);
+  }
+  uint2 a, c;
+  round8(v, a, c);
+  if (!t.live) a = c = make_uint2(kBf16NanPair, kBf16NanPair);
+  if (write) {
+    st8(dx, a);
+    st8(dx + (t.ch.c1 - t.ch.c0), c);
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
-  constexpr int LANES = D / 8;
-  constexpr int ROWS = 32 / LANES;
-  __shared__ float red[kBwdWarps * ROWS][2][D];
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kBwdThreads, kBwdCtasPerSm)
+    norm_rope_bwd_kernel(const NormRopeBwdParams p) {
+  using C = BwdShape<D>;
+  constexpr int LANES = C::kLanes, ROWS = C::kRows, PASS = kBwdUnroll * ROWS;
+  extern __shared__ __align__(16) uint8_t smem[];
   // the sum over the partials may be scheduled now; it waits for this grid's results
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = smem + warp * kBwdStages * C::kStage;
+  const uint32_t ring_addr = smem_u32(ring) + lane * 16;
   TokenCtx t;
   t.l = lane % LANES;
   t.sub = lane / LANES;
-  t.interleaved = p.rope.interleaved;
+  t.interleaved = INTERLEAVED;
   t.eps = p.rope.eps;
-  t.ch = lane_channels(t.l, p.rope.rot, p.rope.interleaved);
-  const long long units = static_cast<long long>(p.B) * p.T * 3;
-  const long long gh = static_cast<long long>(p.T) * D;
+  t.ch = lane_channels(t.l, p.rope.rot, INTERLEAVED);
+  t.live = true;
+  uint2 wq[2] = {}, wk[2] = {};
+  if (p.rope.q_weight) wq[0] = ld8(p.rope.q_weight + t.ch.c0), wq[1] = ld8(p.rope.q_weight + t.ch.c1);
+  if (p.rope.k_weight) wk[0] = ld8(p.rope.k_weight + t.ch.c0), wk[1] = ld8(p.rope.k_weight + t.ch.c1);
   Lane8 dwq{}, dwk{};
 
-  for (long long unit = static_cast<long long>(blockIdx.x) * kBwdWarps + warp; unit < units;
-       unit += static_cast<long long>(gridDim.x) * kBwdWarps) {
-    const long long tok = unit / 3;
-    const int op = static_cast<int>(unit - 3 * tok);
-    const int b = static_cast<int>(tok / p.T);
-    const int ti = static_cast<int>(tok - static_cast<long long>(b) * p.T);
-    int pos = ti;
-    t.live = true;
-    if (p.rope.rot > 0) {
-      if (p.rope.positions) pos = p.rope.positions[tok];
-      if (pos < 0 || pos >= p.rope.max_pos) {
-        if (lane == 0) raise_flag(p.flags, DEVFLAG_BAD_POSITION);
-        t.live = false;
+  // Unit: operand op (0 q, 1 k, 2 v) of token ti of batch entry b; a warp takes every
+  // gridDim.x * kBwdWarps-th unit.
+  struct Unit {
+    int b, ti, op;
+  };
+  const unsigned stride = gridDim.x * kBwdWarps, T = p.T;
+  const int step_op = stride % 3, step_t = stride / 3 % T, step_b = stride / 3 / T;
+  auto heads_of = [&](int op) { return op == 0 ? p.nq : (op == 1 ? p.nk : p.nv); };
+  auto advance = [&](Unit& u) {  // to the warp's next unit that has rows
+    do {
+      u.op += step_op;
+      u.ti += step_t + (u.op >= 3 ? 1 : 0);  // at most T - 1 + 1 more
+      u.op -= u.op >= 3 ? 3 : 0;
+      u.b += step_b;
+      if (u.ti >= p.T) u.ti -= p.T, ++u.b;
+    } while (u.b < p.B && heads_of(u.op) == 0);
+  };
+  const unsigned first = blockIdx.x * kBwdWarps + warp;
+  Unit at{static_cast<int>(first / 3 / T), static_cast<int>(first / 3 % T), static_cast<int>(first % 3)};
+  if (at.b < p.B && heads_of(at.op) == 0) advance(at);
+
+  // ---------------- copies, kBwdStages passes ahead ----------------
+  auto position = [&](const Unit& u) -> int {  // rot > 0
+    if (p.rope.positions && u.b < p.B) return p.rope.positions[static_cast<long long>(u.b) * p.T + u.ti];
+    return u.ti;
+  };
+  Unit ps = at, pn = at;  // the unit being copied and the one after it
+  int p_row = 0, p_heads = 0, p_stage = 0, pos = 0, pos_ahead = 0;
+  const uint16_t *p_g = nullptr, *p_x = nullptr;  // this lane's channels of its first row
+  long long p_sh = 0;
+  const long long g_set = static_cast<long long>(p.T) * D * ROWS;
+  uint32_t live_bits = ~0u;  // bit s: the token of stage s has a row of the table
+  if (p.rope.rot > 0) pos_ahead = position(ps);
+  auto open = [&]() {  // addresses of unit ps; reads the position of the next
+    if (ps.b >= p.B) return;
+    p_heads = heads_of(ps.op);
+    p_g = (ps.op == 0 ? p.gq : (ps.op == 1 ? p.gk : p.gv)) +
+          ((static_cast<long long>(ps.b) * p_heads + t.sub) * p.T + ps.ti) * D + 8 * t.l;
+    const Heads& x = ps.op == 0 ? p.q : p.k;
+    const bool norm = ps.op == 0 ? p.rope.q_weight != nullptr : ps.op == 1 && p.rope.k_weight != nullptr;
+    p_x = norm ? x.p + ps.b * x.sb + ps.ti * x.st + t.sub * x.sh + 8 * t.l : nullptr;
+    p_sh = x.sh * ROWS;
+    pos = pos_ahead;
+    pn = ps;
+    advance(pn);
+    if (p.rope.rot > 0) pos_ahead = position(pn);
+  };
+  open();
+  auto issue = [&]() {
+    const int s = p_stage;
+    p_stage = s + 1 == kBwdStages ? 0 : s + 1;
+    if (ps.b < p.B) {
+      const uint32_t dst = ring_addr + s * C::kStage;
+      const bool more = p_row + PASS < p_heads;
+      if (p_row + PASS <= p_heads) {
+        const uint16_t* a = p_g;
+#pragma unroll
+        for (int u = 0; u < kBwdUnroll; ++u, a += g_set) copy16_async(dst + u * 512, a, true);
+        p_g = a;
+        if (p_x) {
+          const uint16_t* c = p_x;
+#pragma unroll
+          for (int u = 0; u < kBwdUnroll; ++u, c += p_sh)
+            copy16_async(dst + C::kHalf + u * 512, c, true);
+          p_x = c;
+        }
+      } else {  // the unit's last rows: zeros behind them (from the address of a row it has)
+#pragma unroll
+        for (int u = 0; u < kBwdUnroll; ++u) {
+          const int h = u * ROWS + t.sub, left = p_heads - p_row;
+          const bool take = h < left;
+          const long long set = take ? u : 0, back = take || t.sub < left ? 0 : t.sub;
+          copy16_async(dst + u * 512, p_g + set * g_set - back * (g_set / ROWS), take);
+          if (p_x) copy16_async(dst + C::kHalf + u * 512, p_x + set * p_sh - back * (p_sh / ROWS), take);
+        }
+      }
+      if (p_row == 0 && p.rope.rot > 0) {
+        const bool live = pos >= 0 && pos < p.rope.max_pos;
+        if (!live && lane == 0) raise_flag(p.flags, DEVFLAG_BAD_POSITION);
+        live_bits = (live_bits & ~(1u << s)) | (live ? 1u << s : 0u);
+        if (4 * lane < p.rope.rot)
+          copy16_async(dst + 2 * C::kHalf,
+                       p.rope.cos_sin + static_cast<size_t>(live ? pos : 0) * p.rope.rot + 4 * lane, true);
+      }
+      p_row += PASS;
+      if (!more) {
+        p_row = 0;
+        ps = pn;
+        open();
       }
     }
-    t.planes = load_planes<true>(p.rope, pos, t.l, t.ch.rotates && t.live);
-    auto grad = [&](const uint16_t* g, int heads) {
-      return g + (static_cast<long long>(b) * heads * p.T + ti) * D;
-    };
-    auto at = [&](const Heads& x) { return x.p + b * x.sb + ti * x.st; };
-    if (op == 0 && p.nq > 0)
-      norm_rope_bwd_rows<D>(t, grad(p.gq, p.nq), gh, at(p.q), p.q.sh, p.rope.q_weight, p.nq,
-                            at(p.dq), p.dq.sh, dwq);
-    if (op == 1 && p.nk > 0)
-      norm_rope_bwd_rows<D>(t, grad(p.gk, p.nk), gh, at(p.k), p.k.sh, p.rope.k_weight, p.nk,
-                            at(p.dk), p.dk.sh, dwk);
-    if (op == 2 && p.nv > 0)
-      value_rows<D, false>(t, grad(p.gv, p.nv), gh, 0, p.nv, at(p.dv), p.dv.sh, nullptr, true);
-    if (!t.live) {  // a gradient through an unknown rotation is unknown
-      const float nan = __int_as_float(0x7fc00000);
-      dwq = dwk = Lane8{{{nan, nan}, {nan, nan}, {nan, nan}, {nan, nan}}};
+    copy16_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kBwdStages; ++i) issue();
+
+  // ---------------- pass by pass ----------------
+  int left = 0, c_stage = 0;  // rows of the unit that are left; 0: a unit begins
+  uint16_t* dx = nullptr;     // this lane's first channel of its first row
+  long long dx_set = 0;
+  while (at.b < p.B) {
+    copy16_wait<kBwdStages - 1>();
+    __syncwarp();
+    const uint8_t* stage = ring + c_stage * C::kStage;
+    const uint16_t* g = reinterpret_cast<const uint16_t*>(stage) + t.sub * D;
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(stage + C::kHalf) + t.sub * D;
+    if (left == 0) {
+      left = heads_of(at.op);
+      const Heads& d = at.op == 0 ? p.dq : (at.op == 1 ? p.dk : p.dv);
+      dx = d.p + at.b * d.sb + at.ti * d.st + t.sub * d.sh + (at.op == 2 ? 8 * t.l : t.ch.c0);
+      dx_set = d.sh * ROWS;
+      if (p.rope.rot > 0) {
+        t.live = (live_bits >> c_stage) & 1u;
+        float4 co = make_float4(1.f, 1.f, 1.f, 1.f), si = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t.ch.rotates && t.live) {
+          const float* tab = reinterpret_cast<const float*>(stage + 2 * C::kHalf);
+          co = *reinterpret_cast<const float4*>(tab + 4 * t.l);
+          si = *reinterpret_cast<const float4*>(tab + p.rope.rot / 2 + 4 * t.l);
+        }
+        t.planes = Planes{{make_float2(co.x, co.y), make_float2(co.z, co.w)},
+                          {make_float2(-si.x, -si.y), make_float2(-si.z, -si.w)}};
+        if (!t.live) {  // a gradient through an unknown rotation is unknown
+          const float nan = __int_as_float(0x7fc00000);
+          dwq = dwk = Lane8{{{nan, nan}, {nan, nan}, {nan, nan}, {nan, nan}}};
+        }
+      }
     }
+    // (sets past the last row compute with zeros: no branch keeps the sets apart)
+    auto sets = [&](auto norm, const uint2(&w)[2], Lane8& dw) {
+#pragma unroll(decltype(norm)::value ? 2 : 1)
+      for (int u = 0; u < kBwdUnroll; ++u)
+        norm_rope_bwd_set<D, INTERLEAVED, decltype(norm)::value>(
+            t, g + u * ROWS * D, x + u * ROWS * D, w, dx + u * dx_set, u * ROWS + t.sub < left, dw);
+    };
+    if (at.op == 2) {
+#pragma unroll
+      for (int u = 0; u < kBwdUnroll; ++u)
+        if (u * ROWS + t.sub < left)
+          *reinterpret_cast<uint4*>(dx + u * dx_set) =
+              *reinterpret_cast<const uint4*>(g + u * ROWS * D + 8 * t.l);
+    } else if (at.op == 0) {
+      if (p.rope.q_weight)
+        sets(std::true_type{}, wq, dwq);
+      else
+        sets(std::false_type{}, wq, dwq);
+    } else {
+      if (p.rope.k_weight)
+        sets(std::true_type{}, wk, dwk);
+      else
+        sets(std::false_type{}, wk, dwk);
+    }
+    left -= PASS;
+    dx += kBwdUnroll * dx_set;
+    if (left <= 0) {
+      left = 0;
+      advance(at);
+    }
+    __syncwarp();  // every lane has read the stage: the next pass may be copied over it
+    c_stage = c_stage + 1 == kBwdStages ? 0 : c_stage + 1;
+    issue();
   }
   if (p.part == nullptr) return;
+  copy16_wait<0>();
+  __syncthreads();  // the rings are done with
+  float* red = reinterpret_cast<float*>(smem);  // [kBwdWarps * ROWS][2][D]
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int c = i < 4 ? t.ch.c0 + i : t.ch.c1 + i - 4;
-    red[warp * ROWS + t.sub][0][c] = (i & 1) ? dwq.v[i / 2].y : dwq.v[i / 2].x;
-    red[warp * ROWS + t.sub][1][c] = (i & 1) ? dwk.v[i / 2].y : dwk.v[i / 2].x;
+    float* mine = red + (warp * ROWS + t.sub) * 2 * D + c;
+    mine[0] = (i & 1) ? dwq.v[i / 2].y : dwq.v[i / 2].x;
+    mine[D] = (i & 1) ? dwk.v[i / 2].y : dwk.v[i / 2].x;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < 2 * D; e += kBwdThreads) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kBwdWarps * ROWS; ++i) s += red[i][e / D][e % D];
+    for (int i = 0; i < kBwdWarps * ROWS; ++i) s += red[i * 2 * D + e];
     p.part[static_cast<size_t>(blockIdx.x) * 2 * D + e] = s;
   }
 }
@@ -481,13 +609,29 @@ size_t norm_rope_bwd_workspace_bytes(int B, int T, int D) {
   return static_cast<size_t>(norm_rope_bwd_grid(B, T)) * 2 * D * sizeof(float);
 }
 
+cudaError_t prepare_norm_rope() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](const void* fn, int bytes) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  set(reinterpret_cast<const void*>(norm_rope_bwd_kernel<64, false>), BwdShape<64>::kSmem);
+  set(reinterpret_cast<const void*>(norm_rope_bwd_kernel<64, true>), BwdShape<64>::kSmem);
+  set(reinterpret_cast<const void*>(norm_rope_bwd_kernel<128, false>), BwdShape<128>::kSmem);
+  set(reinterpret_cast<const void*>(norm_rope_bwd_kernel<128, true>), BwdShape<128>::kSmem);
+  return e;
+}
+
 cudaError_t launch_norm_rope_bwd(const NormRopeBwdParams& p, int D, cudaStream_t stream) {
   const int grid = norm_rope_bwd_grid(p.B, p.T);
   if (grid > 0 && p.nq + p.nk + p.nv > 0) {
+    auto launch = [&](auto* kernel, int smem) { kernel<<<grid, kBwdThreads, smem, stream>>>(p); };
     if (D == 64)
-      norm_rope_bwd_kernel<64><<<grid, kBwdThreads, 0, stream>>>(p);
+      launch(p.rope.interleaved ? norm_rope_bwd_kernel<64, true> : norm_rope_bwd_kernel<64, false>,
+             BwdShape<64>::kSmem);
     else
-      norm_rope_bwd_kernel<128><<<grid, kBwdThreads, 0, stream>>>(p);
+      launch(p.rope.interleaved ? norm_rope_bwd_kernel<128, true> : norm_rope_bwd_kernel<128, false>,
+             BwdShape<128>::kSmem);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (p.dwq == nullptr && p.dwk == nullptr)) return e;

@@ -42,6 +42,7 @@ struct NormRopeParams {
   unsigned* flags;
 };
 
+cudaError_t prepare_norm_rope();  // per-device one-time attributes
 cudaError_t launch_norm_rope(NormRopeParams p, int D, RowSink sink, int num_sms,
                              cudaStream_t stream);
 

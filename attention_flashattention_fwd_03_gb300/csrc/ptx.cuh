@@ -466,4 +466,22 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                : "memory");
 }
 
+// 16 bytes from global to shared memory without passing registers (zeros when !take, from
+// whatever address), in groups that are waited for by age.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(take ? 16 : 0)
+               : "memory");
+}
+
+__device__ __forceinline__ void copy16_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Until at most N of this thread's groups are in flight.
+template <int N>
+__device__ __forceinline__ void copy16_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 }  // namespace gbattn

@@ -259,6 +259,43 @@ APPENDS = [
 ]
 
 
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,il,ops", [
+    (600, 3, 9, 1, 128, False, "qkv"),   # more tokens than warps, T far below a warp's stride
+    (2500, 1, 3, 2, 64, True, "qkv"),
+    (2, 1500, 17, 2, 64, False, "qkv"),  # rows behind the last full pass
+    (3, 811, 33, 1, 128, True, "qk"),    # T of the very stride of the warps
+    (1, 2000, 8, 20, 128, False, "kv"),
+    (700, 2, 16, 4, 128, False, "q"),
+    (5, 400, 1, 24, 64, False, "v"),
+])
+def test_backward_of_many_tokens(gb, B, T, Hq, Hkv, D, il, ops):
+    """Warps that take many tokens, of all, two and one of the operands."""
+    c = Case(B, T, Hq, Hkv, D, D, True, il, 64000 + T)
+    bits = [synth.normal_bf16(65000 + i, (B, h, T, D)) for i, h in enumerate((Hq, Hkv, Hkv))]
+    g = [to_dev(x) if o in ops else None for x, o in zip(bits, "qkv")]
+    how = dict(c.how, q_weight=c.wq if "q" in ops else None, k_weight=c.wk if "k" in ops else None)
+    out = gb.qkv_norm_rope_bwd(*g, c.q, c.k, positions=c.positions, **how)
+    torch.cuda.synchronize()
+    assert gb.attn_device_status() == (gb.ATTN_OK, 0)
+    assert [x is not None for x in out] == [o in ops for o in "qkvqk"]
+    if "v" in ops:
+        assert torch.equal(out[2], g[2].transpose(1, 2))
+    for i, o in enumerate("qk"):
+        if o not in ops:
+            continue
+        gf = synth.bf16_bits_to_float(bits[i]).astype(np.float64).transpose(0, 2, 1, 3)
+        x, w = c.x(i), c.w(i)
+        want, ww, mags = ref.norm_rope_bwd(gf, x, w, c.rows_of_table(), il)
+        size = np.abs(gf).max(-1, keepdims=True)
+        size = size * np.abs(w).max() / np.sqrt((x * x).mean(-1, keepdims=True) + ref.EPS)
+        assert np.all(np.abs(from_dev(out[i]) - want) <= HALF * np.abs(want) + 2.0 ** -16 * size)
+        # a lane adds its share of the rows, then at most 32 rows of a CTA, 10 CTAs and 32 sums
+        # follow, each addition off by half a step of the sum so far
+        share = (B * T // 810 + 1) * ((Hq, Hkv)[i] * D // 256 + 1)
+        tol = ((share + 32 + 10 + 32) * 2.0 ** -24 + 2.0 ** -19) * mags
+        assert np.all(np.abs(from_dev(out[3 + i]) - ww) <= tol)
+
+
 @pytest.mark.parametrize("four", [False, True])
 @pytest.mark.parametrize("lens,Tn,Hq,Hkv,D,rot,norm,il,explicit", APPENDS)
 def test_append_matches_the_forward_bit_for_bit(gb, four, lens, Tn, Hq, Hkv, D, rot, norm, il,
