@@ -90,7 +90,7 @@ struct TokenCtx {
   Planes planes;
   int l, sub;       // lane within its row, row within the pass
   int interleaved;
-  float eps;
+  float eps, one;   // (one: for rounded_sum2)
   bool live;        // false: q and k rows are NaN
   bool write_kv;    // paged: K and V reach the cache
   int slot;
@@ -99,7 +99,7 @@ struct TokenCtx {
 // Query or key rows h0 .. h1 - 1: x[h * sh] -> y[h * oh] (QUANT: the 4-bit chunk at
 // y4 + h * kChunk, through the warp's rows of shared memory, which bring the lane's two
 // runs of channels into order).  Lanes whose row lies past h1 take part with zeros.
-template <int D, bool QUANT>
+template <int D, bool QUANT, bool FULL>
 __device__ __forceinline__ void norm_rope_rows(const TokenCtx& t, const uint16_t* x, long long sh,
                                                const uint16_t* w, int h0, int h1, uint16_t* y,
                                                long long oh, uint8_t* y4, uint16_t* stage,
@@ -125,10 +125,10 @@ __device__ __forceinline__ void norm_rope_rows(const TokenCtx& t, const uint16_t
       const int h = r0 + u * ROWS + t.sub;
       Lane8 v = widen8(a[u], c[u]);
       if (w) {
-        const float r = rsqrtf(row_sum<LANES>(dot8(v, v)) * (1.f / D) + t.eps);
+        const float r = rsqrtf(row_squares<D, FULL>(v, t.l) * (1.f / D) + t.eps);
         v = mul8(scale8(v, r), wf);
       }
-      if (t.ch.rotates) rotate8(v, t.planes, t.interleaved);
+      if (FULL || t.ch.rotates) rotate8_stepwise(v, t.planes, FULL ? 0 : t.interleaved, t.one);
       round8(v, a[u], c[u]);
       if (!t.live) a[u] = c[u] = make_uint2(kBf16NanPair, kBf16NanPair);
       if constexpr (QUANT) {
@@ -177,7 +177,7 @@ __device__ __forceinline__ void value_rows(const TokenCtx& t, const uint16_t* x,
   }
 }
 
-template <int D, RowSink SINK>
+template <int D, RowSink SINK, bool FULL>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const NormRopeParams p) {
   constexpr int LANES = D / 8;       // lanes of one row
   constexpr int ROWS = 32 / LANES;   // rows of one pass
@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
   t.sub = lane / LANES;
   t.interleaved = p.rope.interleaved;
   t.eps = p.rope.eps;
+  t.one = p.one;
   t.ch = lane_channels(t.l, p.rope.rot, p.rope.interleaved);
   t.live = t.write_kv = true;
   t.slot = 0;
@@ -247,27 +248,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
   };
   const long long oh = static_cast<long long>(p.T) * D;
   if (c0 < p.nq)
-    norm_rope_rows<D, false>(t, in(p.q), p.q.sh, p.rope.q_weight, c0, min(c1, p.nq),
+    norm_rope_rows<D, false, FULL>(t, in(p.q), p.q.sh, p.rope.q_weight, c0, min(c1, p.nq),
                              out(p.q_out, p.nq), oh, nullptr, nullptr, true);
   const int k0 = max(c0 - p.nq, 0), k1 = min(c1 - p.nq, p.nk);
   const int v0 = max(c0 - p.nq - p.nk, 0), v1 = c1 - p.nq - p.nk;
   if constexpr (!PAGED) {
     if (k0 < k1)
-      norm_rope_rows<D, false>(t, in(p.k), p.k.sh, p.rope.k_weight, k0, k1, out(p.k_out, p.nk), oh,
+      norm_rope_rows<D, false, FULL>(t, in(p.k), p.k.sh, p.rope.k_weight, k0, k1, out(p.k_out, p.nk), oh,
                                nullptr, nullptr, true);
     if (v0 < v1) value_rows<D, false>(t, in(p.v), p.v.sh, v0, v1, out(p.v_out, p.nv), oh, nullptr, true);
   } else if constexpr (!QUANT) {
     const long long at = (block * p.nk * kPagedBlock + t.slot) * D;  // pool row of head 0
     constexpr long long ph = kPagedBlock * D;
     if (k0 < k1)
-      norm_rope_rows<D, false>(t, in(p.k), p.k.sh, p.rope.k_weight, k0, k1, p.k_pool + at, ph,
+      norm_rope_rows<D, false, FULL>(t, in(p.k), p.k.sh, p.rope.k_weight, k0, k1, p.k_pool + at, ph,
                                nullptr, nullptr, t.write_kv);
     if (v0 < v1)
       value_rows<D, false>(t, in(p.v), p.v.sh, v0, v1, p.v_pool + at, ph, nullptr, t.write_kv);
   } else {
     uint8_t* chunk4 = p.kv4_pool + block * p.nk * Kv4<D>::kChunk;
     if (k0 < k1)
-      norm_rope_rows<D, true>(t, in(p.k), p.k.sh, p.rope.k_weight, k0, k1, nullptr, 0, chunk4,
+      norm_rope_rows<D, true, FULL>(t, in(p.k), p.k.sh, p.rope.k_weight, k0, k1, nullptr, 0, chunk4,
                               stage + (threadIdx.x >> 5) * ROWS * D, t.write_kv);
     if (v0 < v1)
       value_rows<D, true>(t, in(p.v), p.v.sh, v0, v1, nullptr, 0, chunk4, t.write_kv);
@@ -287,22 +288,30 @@ cudaError_t launch_norm_rope(NormRopeParams p, int D, RowSink sink, int num_sms,
   const int pass = 256 / D;
   p.rows_per_warp = tokens >= 32ll * num_sms ? rows : (tokens >= 4ll * num_sms ? 4 : 2) * pass;
   p.chunks = (rows + p.rows_per_warp - 1) / p.rows_per_warp;
+  p.one = 1.f;
   const long long grid = (tokens * p.chunks + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
   const dim3 g(static_cast<unsigned>(grid));
-  auto run = [&](auto d) {
+  auto run = [&](auto d, auto f) {
     constexpr int DD = decltype(d)::value;
+    constexpr bool FULL = decltype(f)::value;
     if (sink == RowSink::kContiguous)
-      norm_rope_kernel<DD, RowSink::kContiguous><<<g, kThreads, 0, stream>>>(p);
+      norm_rope_kernel<DD, RowSink::kContiguous, FULL><<<g, kThreads, 0, stream>>>(p);
     else if (sink == RowSink::kPaged)
-      norm_rope_kernel<DD, RowSink::kPaged><<<g, kThreads, 0, stream>>>(p);
+      norm_rope_kernel<DD, RowSink::kPaged, FULL><<<g, kThreads, 0, stream>>>(p);
     else
-      norm_rope_kernel<DD, RowSink::kPaged4><<<g, kThreads, 0, stream>>>(p);
+      norm_rope_kernel<DD, RowSink::kPaged4, FULL><<<g, kThreads, 0, stream>>>(p);
   };
-  if (D == 64)
-    run(std::integral_constant<int, 64>{});
+  auto sized = [&](auto f) {
+    if (D == 64)
+      run(std::integral_constant<int, 64>{}, f);
+    else
+      run(std::integral_constant<int, 128>{}, f);
+  };
+  if (p.rope.rot == D && !p.rope.interleaved)
+    sized(std::true_type{});
   else
-    run(std::integral_constant<int, 128>{});
+    sized(std::false_type{});
   return cudaGetLastError();
 }
 

@@ -1,5 +1,5 @@
 // norm_rope.cuh -- RMS norm and position rotation of one head's row, shared by the
-// forward, backward and cache-append kernels so they agree bit for bit.
+// forward and cache-append kernels so they agree bit for bit, and the backward kernel.
 //
 //   xh = x * rsqrt(mean(x^2) + eps)      y = R(pos) (xh * w)
 // over the D channels of one (token, head); without a weight y = R(pos) x.  R turns the
@@ -16,7 +16,12 @@
 // part 8 l.. and 8 l + 4...  Either way a rotating lane uses planes 4 l .. 4 l + 3, and
 // the rotation needs no exchange between lanes.  rot is a multiple of 8 for this.
 //
-// All arithmetic is fp32; a row is rounded to bf16 once, after the rotation.
+// All arithmetic is fp32; a row is rounded to bf16 once, after the rotation.  Up to there
+// the forward takes the formula's operations one by one, x r, times w, two products and
+// their sum, each rounded, as a program that evaluates it tensor by tensor does: a fused
+// product would differ in the last bit of one value in some ten thousand, which the 4-bit
+// cache can turn into a whole step.  (Costs 0.4 of 66 us on a 16k prompt, 1 of 50 on an
+// append to the 4-bit cache and its gather.)
 #pragma once
 
 #include <cstdint>
@@ -97,6 +102,67 @@ __device__ __forceinline__ float row_sum(float v) {
 struct Planes {
   float2 c[2], s[2];
 };
+
+// x y + z u with both products and the sum rounded.  The sum is a multiply-add by a one that
+// the compiler does not know: it joins a packed product and a packed sum to one operation.
+__device__ __forceinline__ float2 rounded_sum2(float2 x, float2 y, float2 z, float2 u, float one) {
+  return __ffma2_rn(__fmul2_rn(z, u), make_float2(one, one), __fmul2_rn(x, y));
+}
+
+// Turns the lane's four planes, every operation rounded by itself.
+__device__ __forceinline__ void rotate8_stepwise(Lane8& x, const Planes& p, int interleaved,
+                                                 float one) {
+  if (!interleaved) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 a = x.v[i], b = x.v[2 + i];
+      const float2 ns = make_float2(-p.s[i].x, -p.s[i].y);
+      x.v[i] = rounded_sum2(a, p.c[i], b, ns, one);
+      x.v[2 + i] = rounded_sum2(b, p.c[i], a, p.s[i], one);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float c = (i & 1) ? p.c[i / 2].y : p.c[i / 2].x, s = (i & 1) ? p.s[i / 2].y : p.s[i / 2].x;
+      const float a = x.v[i].x, b = x.v[i].y;
+      x.v[i] = make_float2(__fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)),
+                           __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s)));
+    }
+  }
+}
+
+// Sum of the squares of a row.  FULL (every channel rotates, planes of halves): 32 columns
+// c, c + 32, .. are added first, then neighbouring columns in pairs, the order in which a
+// reduction over a row of 128 or 64 values by a warp goes, for the reason given above.
+template <int D, bool FULL>
+__device__ __forceinline__ float row_squares(const Lane8& x, int l) {
+  if constexpr (!FULL) {
+    return row_sum<D / 8>(dot8(x, x));
+  } else {
+    const Lane8 q = mul8(x, x);  // exact: x is bf16
+    float s;
+    if constexpr (D == 64) {
+      const float2 z0 = __fadd2_rn(q.v[0], q.v[2]), z1 = __fadd2_rn(q.v[1], q.v[3]);
+      s = (z0.x + z0.y) + (z1.x + z1.y);
+    } else {
+      // lanes l and l + 8 hold quarters 0, 2 and 1, 3 of the same four columns: each adds two
+      const bool up = l & 8;
+      const float2 give0 = up ? q.v[0] : q.v[1], give1 = up ? q.v[2] : q.v[3];
+      const float2 own0 = up ? q.v[1] : q.v[0], own1 = up ? q.v[3] : q.v[2];
+      float2 got0, got1;
+      got0.x = __shfl_xor_sync(0xffffffffu, give0.x, 8);
+      got0.y = __shfl_xor_sync(0xffffffffu, give0.y, 8);
+      got1.x = __shfl_xor_sync(0xffffffffu, give1.x, 8);
+      got1.y = __shfl_xor_sync(0xffffffffu, give1.y, 8);
+      const float2 z = __fadd2_rn(__fadd2_rn(__fadd2_rn(own0, got0), up ? got1 : own1), up ? own1 : got1);
+      s = z.x + z.y;
+      s += __shfl_xor_sync(0xffffffffu, s, 8);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  }
+}
 
 // Turns the lane's four planes.
 __device__ __forceinline__ void rotate8(Lane8& x, const Planes& p, int interleaved) {

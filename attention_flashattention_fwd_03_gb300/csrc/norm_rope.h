@@ -39,6 +39,7 @@ struct NormRopeParams {
   int32_t* new_seq_lens;       // [B] or nullptr
   int max_blocks, num_pool_blocks;
   int chunks, rows_per_warp;   // a token's nq + nk + nv rows are cut into chunks (launcher)
+  float one;                   // 1, which the compiler must not know (launcher)
   unsigned* flags;
 };
 

@@ -114,6 +114,22 @@ def test_forward(gb, B, T, Hq, Hkv, D, rot, norm, il, start, explicit):
     assert torch.equal(q, q1) and torch.equal(k, k1) and torch.equal(v, v1)
 
 
+@pytest.mark.parametrize("D,rot,il", [(128, 128, False), (64, 64, False), (128, 40, False),
+                                      (64, 64, True), (128, 32, True)])
+def test_rotation_rounds_every_operation(gb, D, rot, il):
+    """Without a norm the rows are what eager fp32 operations give, bit for bit."""
+    c = Case(3, 50, 5, 2, D, rot, False, il, 66000 + rot, 7)
+    cs = c.cs[c.positions.long()][:, :, None]
+    cos, sin = cs.chunk(2, -1)
+    for x, y in zip((c.q, c.k), gb.qkv_norm_rope(c.q, c.k, positions=c.positions, **c.how)):
+        r = x[..., :rot].float()
+        a, b = (r[..., 0::2], r[..., 1::2]) if il else r.chunk(2, -1)
+        want = (a * cos - b * sin, b * cos + a * sin)
+        want = torch.stack(want, -1).flatten(-2) if il else torch.cat(want, -1)
+        want = torch.cat([want.bfloat16(), x[..., rot:]], -1)
+        assert torch.equal(y, want.transpose(1, 2))
+
+
 @pytest.mark.parametrize("B,T,Hq,Hkv,D,rot,norm,il,start,explicit", CASES)
 def test_backward(gb, B, T, Hq, Hkv, D, rot, norm, il, start, explicit):
     c = Case(B, T, Hq, Hkv, D, rot, norm, il, 32000 + T, start, explicit)
