@@ -65,21 +65,24 @@ __device__ __forceinline__ uint32_t kv4_scale_bits(uint32_t amax_bits) {
 // to an integer, whose low bits are the code.  (Checked against exact division for every
 // pair of significands.)  |n| <= 7 holds by itself: s >= amax / 7 * 31 / 32.  Scales near
 // the ends of the fp32 range, where 1 / s is not a normal number, take a division.
-__device__ __forceinline__ uint32_t kv4_codes(const float (&x)[8], float s) {
+__device__ __forceinline__ uint32_t kv4_codes(const float2 (&x)[4], float s) {
   uint32_t w = 0;
   if (s > 1e-30f && s < 1e30f) {
     const float inv = __frcp_rn(s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q = __fadd_rn(__fmaf_rn(x[i], inv, 6144.f), -6144.f);
-      const uint32_t bits = __float_as_uint(__fadd_rn(q, 12582920.f));
-      w += (bits - 0x4b400000u) << (4 * i);
+    for (int i = 3; i >= 0; --i) {
+      float2 q = __ffma2_rn(x[i], make_float2(inv, inv), make_float2(6144.f, 6144.f));
+      q = __fadd2_rn(q, make_float2(-6144.f, -6144.f));
+      q = __fadd2_rn(q, make_float2(12582920.f, 12582920.f));
+      w = 16 * w + __float_as_uint(q.y);
+      w = 16 * w + __float_as_uint(q.x);
     }
-    return w;
+    return w - 0x3f400000u;  // the sum of 0x4b400000 16^i
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float n = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -7.f), 7.f) : 0.f;
+    const float v = (i & 1) ? x[i / 2].y : x[i / 2].x;
+    const float n = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(v, s)), -7.f), 7.f) : 0.f;
     w |= static_cast<uint32_t>(static_cast<int>(n) + 8) << (4 * i);
   }
   return w;

@@ -23,10 +23,12 @@ namespace {
 
 // One warp a CTA: a token's rows leave an SM as they end, without waiting for others.
 // (16k prompt, four passes unrolled: 1 warp 66.1 us, 2 68.4, 4 68.6, 8 69.6, each held to
-// 64 registers; two passes unrolled 77.5, three 75.0, six 74.3, eight 91.8.)
+// 64 registers; two passes unrolled 77.5, three 75.0, six 74.3, eight 91.8.)  CTAs an SM
+// (registers), 16k prompt / bf16 append / 4-bit append and gather of 16 x 512 tokens: 32 (64)
+// 66.4 / 36.0 / 49.9 us, 28 (72) 66.1 / 36.3 / 48.7, 24 (80) 67.9 / 36.1 / 53.7, 20 78.9 / 41.8 / 54.6.
 constexpr int kWarps = 1;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtasPerSm = 32;
+constexpr int kCtasPerSm = 28;
 
 __device__ __forceinline__ uint2 ld8(const uint16_t* p) { return *reinterpret_cast<const uint2*>(p); }
 __device__ __forceinline__ void st8(uint16_t* p, uint2 v) { *reinterpret_cast<uint2*>(p) = v; }
@@ -59,12 +61,9 @@ __device__ __forceinline__ void quantise_row(uint4 w, uint8_t* chunk, int slot, 
   pair = __vmaxu2(pair, __shfl_xor_sync(0xffffffffu, pair, 1));
   pair = __vmaxu2(pair, __shfl_xor_sync(0xffffffffu, pair, 2));
   const uint32_t sbits = kv4_scale_bits(max(pair & 0xffffu, pair >> 16));
-  float x[8];
+  float2 x[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(in[i]);
-    x[2 * i + 1] = bf16_hi(in[i]);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = widen2(in[i]);
   const uint32_t codes = kv4_codes(x, __uint_as_float(sbits));
   if (!write) return;
   const int group = l >> 2, part = l & 3;  // channels 8 l .. 8 l + 7 of group l / 4
