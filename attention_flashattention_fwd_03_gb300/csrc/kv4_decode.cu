@@ -24,13 +24,23 @@
 // maximum only moves when it grows by more than 2^8, so outputs are rarely rescaled; p
 // stays below 2^8.
 //
-// Bound by HBM: a token and KV head take 9 D / 8 bytes, read once.  The batch is one
-// sequence of steps, 64 tokens (4 blocks) of one (request, KV head) each, request-major;
-// it is cut into equal ranges, and every warp streams a range by itself: lane j of the
-// warp copies block j of a step, one untiled bulk copy of the whole chunk (codes and
-// scales of K and V), into the warp's own ring in shared memory; the table entries of a
-// step are read one step ahead of its copies.  The fragments of m16n8k16 come out of shared memory by plain
-// loads in the order the format lays down.
+// A token and KV head take 9 D / 8 bytes, read once.  The batch is one sequence of steps, 64
+// tokens (4 blocks) of one (request, KV head) each, request-major; it is cut into equal
+// ranges, and every warp streams a range by itself: lane j of the warp copies block j of a
+// step, one untiled bulk copy of the whole chunk (codes and scales of K and V), into the
+// warp's own ring in shared memory; the table entries of a step are read one step ahead of
+// its copies.  The fragments of m16n8k16 come out of shared memory by plain loads in the
+// order the format lays down.
+//
+// What bounds it: 64 requests of 512 to 8192 tokens, 12/2 heads, D 128 (80 MB, 11.8 us at
+// the copy rate) take 25 us, one of 131000 tokens, 32/8 heads (151 MB, 22.2 us) 37 us.  The
+// copies alone would take 12 and 30: at 28 % of its size the cache arrives faster than the
+// ALU takes nibbles apart (busy 49 % of the long case, issue slots 55 %, with the 12 warps an
+// SM that 168 registers and two stages a warp leave room for).  Set-up before the first
+// copy lands is about 3 us, the merge kernel 5.  Steps of 2 blocks 27 and 41 us; 4 CTAs an SM
+// (128 registers, spills) 31 and 47; V scales multiplied into transposed bf16 probabilities
+// (22 of 230 instructions a block fewer, one more rounding) 25.4 and 37.2; V codes by 8-byte
+// loads no change.
 //
 // A chunk of Tq tokens is the same computation with group * Tq query rows on every KV head
 // ([Hq, Tq, D] keeps them together); row x sees the keys up to its own position.  Rows are
@@ -835,13 +845,13 @@ cudaError_t launch(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms, c
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // Few segments share the ranges among many pieces each: 16 warps a head then (one request
-  // of 131000 tokens, 228 pieces a head: 36.7 us a call against 40.6 with 8), else 4, one
+  // Few segments share the ranges among many pieces each: 32 warps a head then (one request
+  // of 131000 tokens, 228 pieces a head: 36.7 us a call, 16 warps 37.2, 8 40.6), else 4, one
   // round trip for the ~15 pieces a head of 64 requests.
   const long long pieces = p.max_pieces / (static_cast<long long>(p.S) * p.segs);
   if (pieces > 48) {
-    cfg.blockDim = dim3(16 * 32);
-    return cudaLaunchKernelEx(&cfg, kv4_decode_merge_kernel<D, 16>, p);
+    cfg.blockDim = dim3(32 * 32);
+    return cudaLaunchKernelEx(&cfg, kv4_decode_merge_kernel<D, 32>, p);
   }
   cfg.blockDim = dim3(4 * 32);
   return cudaLaunchKernelEx(&cfg, kv4_decode_merge_kernel<D, 4>, p);
