@@ -33,11 +33,11 @@
 // order the format lays down.
 //
 // What bounds it: 64 requests of 512 to 8192 tokens, 12/2 heads, D 128 (80 MB, 11.8 us at
-// the copy rate) take 25 us, one of 131000 tokens, 32/8 heads (151 MB, 22.2 us) 37 us.  The
+// the copy rate) take 25 us, one of 131000 tokens, 32/8 heads (151 MB, 22.2 us) 36 us.  The
 // copies alone would take 12 and 30: at 28 % of its size the cache arrives faster than the
 // ALU takes nibbles apart (busy 49 % of the long case, issue slots 55 %, with the 12 warps an
 // SM that 168 registers and two stages a warp leave room for).  Set-up before the first
-// copy lands is about 3 us, the merge kernel 5.  Steps of 2 blocks 27 and 41 us; 4 CTAs an SM
+// copy lands is about 3 us, the merge kernel 4.  Steps of 2 blocks 27 and 41 us; 4 CTAs an SM
 // (128 registers, spills) 31 and 47; V scales multiplied into transposed bf16 probabilities
 // (22 of 230 instructions a block fewer, one more rounding) 25.4 and 37.2; V codes by 8-byte
 // loads no change.
@@ -233,9 +233,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     n_w = (steps_of(at.nb) - warp + kWarps - 1) / kWarps;
   } else {
     // ---------------- plan: total steps, range count, this warp's range ----------------
-    int total = 0;
-    for (int r0 = 0; r0 < p.S; r0 += 32)
-      if (r0 + lane < p.S) total += steps_of(blocks_of(p, p.seq_lens[r0 + lane]));
+    // (128 requests a round: a lane's four lengths are read at once)
+    int total = 0, nb4[4];
+    auto read4 = [&](int r0) {
+      int L[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) L[i] = r0 + 32 * i + lane < p.S ? p.seq_lens[r0 + 32 * i + lane] : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) nb4[i] = blocks_of(p, L[i]);
+    };
+    for (int r0 = 0; r0 < p.S; r0 += 128) {
+      read4(r0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total += steps_of(nb4[i]);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     total *= p.segs;  // below 2^31 for every length within max_seq_len
@@ -249,8 +260,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
       int before = 0;  // steps of requests r0 - 1 and earlier
       bool found = false;
       for (int r0 = 0; r0 < p.S && !found; r0 += 32) {
-        const int r = r0 + lane;
-        const int nb = r < p.S ? blocks_of(p, p.seq_lens[r]) : 0;
+        if (p.S > 128 && r0 % 128 == 0) read4(r0);
+        const int i = r0 / 32 % 4;
+        const int nb = i < 2 ? (i == 0 ? nb4[0] : nb4[1]) : (i == 2 ? nb4[2] : nb4[3]);
         const int own = steps_of(nb) * p.segs;
         int incl = own;
 #pragma unroll
@@ -685,104 +697,120 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
 // LSE = M + ln sum_j e^{LSE_j - M}, O = sum_j e^{LSE_j - LSE} O_j over the pieces of one
 // (request, query head): a CTA, whose MW warps take every MW-th piece, four of them in
 // flight at a time, and are joined in shared memory.  A NaN of a piece goes through.
+//
+// The whole takes some 4 us, more than its two round trips of reads: a first run of the code
+// is slow.  With many warps a head, i.e. few CTAs, each goes through it once over no pieces
+// before it waits for the split kernel, which then still runs (36.6 -> 35.9 us a call on
+// 131000 tokens, 19.1 -> 18.5 on 40000; the 768 CTAs of 64 requests would take issue slots
+// from the split kernel: 25.0 -> 25.3).
 template <int D, int MW>
 __global__ void __launch_bounds__(MW * 32) kv4_decode_merge_kernel(const Kv4DecodeParams p) {
   constexpr int PER = D / 32;  // dims per lane
   constexpr float kLog2e = 1.4426950408889634f;
   __shared__ float part[MW][D];
   __shared__ float part_m[MW], part_sum[MW];
-  // launched as a programmatic dependent: the split kernel's results are complete and
-  // visible once this returns
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   // the CTA's row: row x of KV head kvh of request r
   const int kv = blockIdx.x / p.rows, x = blockIdx.x - kv * p.rows;
   const int r = kv / p.Hkv, kvh = kv - r * p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunk = x / p.piece_rows;
   const int seg = r * p.segs + kvh * p.chunks + chunk;
-  const int L = p.seq_lens[r], k0 = p.seg_first[seg], k1 = p.seg_last[seg];
-  // (the split kernel has noted the ranges of every valid nonempty request; the check keeps
-  // every read in bounds should the lengths have changed between the two kernels)
-  const bool good = blocks_of(p, L) > 0 && k0 >= 0 && k0 <= k1 && k1 + seg < p.max_pieces;
-  const bool bad = L != 0 && !good;
-  const int n = good ? k1 - k0 + 1 : 0;
-  const size_t base =
-      good ? static_cast<size_t>(k0 + seg) * p.piece_rows + (x - chunk * p.piece_rows) : 0;
-  const float* pl = p.part_lse + base;
-  const float* po = p.part_o + base * D + lane * PER;
+#pragma unroll 1
+  for (int pass = MW > 4 ? 0 : 1; pass < 2; ++pass) {
+    int L = 0, k0 = 0, k1 = -1;
+    if (pass == 1) {
+      // launched as a programmatic dependent: the split kernel's results are complete and
+      // visible once this returns
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      L = p.seq_lens[r];
+      k0 = p.seg_first[seg];
+      k1 = p.seg_last[seg];
+    }
+    // (the split kernel has noted the ranges of every valid nonempty request; the check keeps
+    // every read in bounds should the lengths have changed between the two kernels)
+    const bool good = blocks_of(p, L) > 0 && k0 >= 0 && k0 <= k1 && k1 + seg < p.max_pieces;
+    const bool bad = L != 0 && !good;
+    const int n = good ? k1 - k0 + 1 : 0;
+    const size_t base =
+        good ? static_cast<size_t>(k0 + seg) * p.piece_rows + (x - chunk * p.piece_rows) : 0;
+    const float* pl = p.part_lse + base;
+    const float* po = p.part_o + base * D + lane * PER;
 
-  float m = -INFINITY, sum = 0.f, o[PER];
+    float m = -INFINITY, sum = 0.f, o[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) o[i] = 0.f;
-  for (int j0 = warp; j0 < n; j0 += 4 * MW) {
-    float lse[4], v[4][PER];
+    for (int i = 0; i < PER; ++i) o[i] = 0.f;
+    // (a first round without pieces is taken too, for the reason above)
+    for (int j0 = warp; j0 < n || (pass == 0 && j0 == warp); j0 += 4 * MW) {
+      float lse[4], v[4][PER];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int j = j0 + s * MW;
-      lse[s] = -INFINITY;
+      for (int s = 0; s < 4; ++s) {
+        const int j = j0 + s * MW;
+        lse[s] = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) v[s][i] = 0.f;
-      if (j < n) {
-        lse[s] = pl[static_cast<size_t>(j) * p.piece_rows];
-        const float* src = po + static_cast<size_t>(j) * p.piece_rows * D;
-        if constexpr (PER == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(src);
-          v[s][0] = x.x, v[s][1] = x.y, v[s][2] = x.z, v[s][3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(src);
-          v[s][0] = x.x, v[s][1] = x.y;
+        for (int i = 0; i < PER; ++i) v[s][i] = 0.f;
+        if (j < n) {
+          lse[s] = pl[static_cast<size_t>(j) * p.piece_rows];
+          const float* src = po + static_cast<size_t>(j) * p.piece_rows * D;
+          if constexpr (PER == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            v[s][0] = x.x, v[s][1] = x.y, v[s][2] = x.z, v[s][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            v[s][0] = x.x, v[s][1] = x.y;
+          }
         }
       }
+      const float mn = fmaxf(fmaxf(m, lse[0]), fmax3(lse[1], lse[2], lse[3]));
+      const float ms = mn == -INFINITY ? 0.f : mn;  // (all four NaN, or no piece)
+      const float al = ex2((m - ms) * kLog2e);
+      m = mn;
+      sum *= al;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] *= al;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const float w = ex2((lse[s] - ms) * kLog2e);
+        sum += w;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) o[i] = fmaf(w, v[s][i], o[i]);
+      }
     }
-    const float mn = fmaxf(fmaxf(m, lse[0]), fmax3(lse[1], lse[2], lse[3]));
-    const float ms = mn == -INFINITY ? 0.f : mn;  // (all four NaN)
-    const float al = ex2((m - ms) * kLog2e);
-    m = mn;
-    sum *= al;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] *= al;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const float w = ex2((lse[s] - ms) * kLog2e);
-      sum += w;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) o[i] = fmaf(w, v[s][i], o[i]);
+    for (int i = 0; i < PER; ++i) part[warp][lane * PER + i] = o[i];
+    if (lane == 0) {
+      part_m[warp] = m;
+      part_sum[warp] = sum;
     }
-  }
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+      float M = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) part[warp][lane * PER + i] = o[i];
-  if (lane == 0) {
-    part_m[warp] = m;
-    part_sum[warp] = sum;
-  }
-  __syncthreads();
-  if (threadIdx.x >= D / 2) return;
-  float M = -INFINITY;
+      for (int w = 0; w < MW; ++w) M = fmaxf(M, part_m[w]);
+      const float Ms = M == -INFINITY ? 0.f : M;
+      float tot = 0.f, x0 = 0.f, x1 = 0.f;
 #pragma unroll
-  for (int w = 0; w < MW; ++w) M = fmaxf(M, part_m[w]);
-  const float Ms = M == -INFINITY ? 0.f : M;
-  float tot = 0.f, x0 = 0.f, x1 = 0.f;
-#pragma unroll
-  for (int w = 0; w < MW; ++w) {
-    const float f = ex2((part_m[w] - Ms) * kLog2e);
-    tot = fmaf(f, part_sum[w], tot);
-    x0 = fmaf(f, part[w][2 * threadIdx.x], x0);
-    x1 = fmaf(f, part[w][2 * threadIdx.x + 1], x1);
+      for (int w = 0; w < MW; ++w) {
+        const float f = ex2((part_m[w] - Ms) * kLog2e);
+        tot = fmaf(f, part_sum[w], tot);
+        x0 = fmaf(f, part[w][2 * threadIdx.x], x0);
+        x1 = fmaf(f, part[w][2 * threadIdx.x + 1], x1);
+      }
+      float lse_out = Ms + logf(tot);
+      const float inv = tot == 0.f ? 0.f : 1.f / tot;  // (no key is visible to the row)
+      x0 *= inv;
+      x1 *= inv;
+      if (bad) {
+        if (threadIdx.x == 0) raise_flag(p.flags, DEVFLAG_BAD_SEQLEN);
+        x0 = x1 = lse_out = __int_as_float(0x7fc00000);
+      }
+      if (pass == 1) {
+        reinterpret_cast<uint32_t*>(p.o)[static_cast<size_t>(blockIdx.x) * (D / 2) + threadIdx.x] =
+            pack_bf16x2(x0, x1);
+        if (p.lse != nullptr && threadIdx.x == 0) p.lse[blockIdx.x] = lse_out;
+      }
+    }
+    if (pass == 0) __syncthreads();  // the first pass's sums have been read
   }
-  float lse_out = Ms + logf(tot);
-  const float inv = tot == 0.f ? 0.f : 1.f / tot;  // (no key is visible to the row)
-  x0 *= inv;
-  x1 *= inv;
-  if (L == 0) {
-    x0 = x1 = 0.f;
-    lse_out = -INFINITY;
-  } else if (bad) {
-    if (threadIdx.x == 0) raise_flag(p.flags, DEVFLAG_BAD_SEQLEN);
-    x0 = x1 = lse_out = __int_as_float(0x7fc00000);
-  }
-  reinterpret_cast<uint32_t*>(p.o)[static_cast<size_t>(blockIdx.x) * (D / 2) + threadIdx.x] =
-      pack_bf16x2(x0, x1);
-  if (p.lse != nullptr && threadIdx.x == 0) p.lse[blockIdx.x] = lse_out;
 }
 
 template <int D, int NQT>
@@ -846,8 +874,8 @@ cudaError_t launch(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms, c
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // Few segments share the ranges among many pieces each: 32 warps a head then (one request
-  // of 131000 tokens, 228 pieces a head: 36.7 us a call, 16 warps 37.2, 8 40.6), else 4, one
-  // round trip for the ~15 pieces a head of 64 requests.
+  // of 131000 tokens, 228 pieces a head: 36.6 us a call, 16 warps 37.2, 8 40.6, before the
+  // first pass above), else 4, one round trip for the ~15 pieces a head of 64 requests.
   const long long pieces = p.max_pieces / (static_cast<long long>(p.S) * p.segs);
   if (pieces > 48) {
     cfg.blockDim = dim3(32 * 32);

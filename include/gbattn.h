@@ -191,7 +191,8 @@ int paged_attn_decode_noalloc(const void *q, const void *k_pool, const void *v_p
  * kernel of this library on that device stays set until the next call of this
  * function, which reports and clears it for everyone.  *flags (if not NULL) receives the raw bits: 1 = a bounded wait in
  * a kernel timed out, 2 = a decode request had an invalid length, 4 = a decode
- * block id was out of range, 8 = a position lay outside the rotation table.  Returns ATTN_ERR_DEVICE if any bit was set,
+ * block id was out of range, 8 = a position lay outside the rotation table.  Returns
+ * ATTN_ERR_DEVICE if any bit was set,
  * ATTN_ERR_CUDA if the synchronisation failed, else ATTN_OK.
  */
 int attn_device_status(unsigned int *flags);
