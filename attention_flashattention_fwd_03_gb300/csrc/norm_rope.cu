@@ -332,8 +332,8 @@ cudaError_t launch_norm_rope(NormRopeParams p, int D, RowSink sink, int num_sms,
 // being 2 KB of g, 2 KB of x and the token's row of the table, through its own ring of
 // stages in shared memory: the copies of the next passes are in flight while one is
 // computed, which registers alone did not allow (57 us so).  4 x 2048 tokens of 16/16
-// heads, D 128: 46 us for 269 MB, 86 % of the copy rate, about 3 of them the sum over the
-// partials.  Two stages of four row sets 46.3 us, three 48.6; six stages of two sets 81,
+// heads, D 128: 45.7 us for 269 MB, 87 % of the copy rate, about 2 of them the sum over the
+// partials (read one after the other they took one more).  Two stages of four row sets 46.3 us, three 48.6; six stages of two sets 81,
 // two of six 59, both with a pass's set-up costing more than its rows.
 namespace {
 
@@ -590,15 +590,23 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtasPerSm)
   }
 }
 
-// Adds the partials: 32 channels a CTA, 32 strided runs of partials each (n = 0: zeros).
+// Adds the partials: 32 channels a CTA, 32 strided runs of partials each, a run's values all
+// read at once (n = 0: zeros).
 __global__ void __launch_bounds__(1024)
     norm_rope_dw_kernel(const float* part, int n, int D, float* dwq, float* dwk) {
   __shared__ float red[32][33];
   // launched as a programmatic dependent: the partials are complete once this returns
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x * 32 + threadIdx.x;
-  float s = 0.f;
-  for (int i = threadIdx.y; i < n; i += 32) s += part[static_cast<size_t>(i) * 2 * D + c];
+  constexpr int RUN = (kBwdMaxGrid + 31) / 32;
+  float v[RUN], s = 0.f;
+#pragma unroll
+  for (int k = 0; k < RUN; ++k) {
+    const int i = threadIdx.y + 32 * k;
+    v[k] = i < n ? part[static_cast<size_t>(i) * 2 * D + c] : 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < RUN; ++k) s += v[k];
   red[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y != 0) return;
