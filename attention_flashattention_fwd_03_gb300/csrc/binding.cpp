@@ -11,6 +11,8 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/Allocator.h>
+#include <c10/core/TensorImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -191,6 +193,20 @@ at::Tensor make(at::IntArrayRef sizes, const at::Tensor& like, at::ScalarType ty
   return at::empty(sizes, like.options().dtype(type).requires_grad(false));
 }
 
+// Heads h0 .. h0 + n - 1 of a fused [B, T, H, D] buffer, without the dispatcher's way there.
+at::Tensor heads_of(const at::Tensor& fused, int64_t h0, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::TensorImpl::VIEW, c10::Storage(fused.storage()), fused.key_set(), fused.dtype());
+  const int64_t sizes[4] = {fused.size(0), fused.size(1), n, fused.size(3)};
+  t.unsafeGetTensorImpl()->set_storage_offset(h0 * fused.size(3));
+  t.unsafeGetTensorImpl()->set_sizes_and_strides(sizes, fused.strides());
+  return t;
+}
+
+// Device memory of a call's own, given back to the allocator (which reuses it in stream
+// order) when the call returns.
+c10::DataPtr scratch(size_t bytes) { return c10::GetAllocator(at::kCUDA)->allocate(bytes); }
+
 // The norm and rotation operands from argument i on: cos_sin, q_weight, k_weight, eps,
 // interleaved, positions.
 struct Rope {
@@ -289,16 +305,17 @@ PyObject* rope_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int64_t nq = g[0] ? Hq : 0, nk = g[1] ? Hkv : 0, nv = g[2] ? Hkv : 0;
     if (B == 0 || T == 0 || nq + nk + nv == 0) return nullptr;
     const at::Tensor fused = make({B, T, nq + nk + nv, D}, *some, at::kBFloat16);
-    at::Tensor d[3], dw[2], ws;
-    if (nq) d[0] = fused.narrow(2, 0, nq);
-    if (nk) d[1] = fused.narrow(2, nq, nk);
-    if (nv) d[2] = fused.narrow(2, nq + nk, nv);
+    at::Tensor d[3], dw[2];
+    if (nq) d[0] = heads_of(fused, 0, nq);
+    if (nk) d[1] = heads_of(fused, nq, nk);
+    if (nv) d[2] = heads_of(fused, nq + nk, nv);
     if (r.qw) dw[0] = make({D}, *some, at::kFloat);
     if (r.kw) dw[1] = make({D}, *some, at::kFloat);
     size_t bytes = 0;
+    c10::DataPtr ws;
     if (r.qw || r.kw) {
       bytes = g_entry.rope_bwd_ws(B, T, D);
-      ws = make({static_cast<int64_t>(bytes)}, *some, at::kByte);
+      ws = scratch(bytes);
     }
     const at::Tensor* dp[3];
     for (int i = 0; i < 3; ++i) dp[i] = d[i].defined() ? &d[i] : nullptr;
@@ -308,7 +325,7 @@ PyObject* rope_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
         static_cast<const float*>(ptr(r.cs)), static_cast<const int32_t*>(ptr(r.pos)), B, T, Hq,
         Hkv, D, r.rot, r.max_pos, r.interleaved, r.eps, ptr(dp[0]), ptr(dp[1]), ptr(dp[2]), s0.s,
         s1.s, s2.s, r.qw ? dw[0].data_ptr<float>() : nullptr,
-        r.kw ? dw[1].data_ptr<float>() : nullptr, bytes ? ws.data_ptr() : nullptr, bytes, c.stream); });
+        r.kw ? dw[1].data_ptr<float>() : nullptr, ws.get(), bytes, c.stream); });
     if (st != ATTN_OK) return PyLong_FromLong(st);
     return pack({result(Py_None, d[0]), result(Py_None, d[1]), result(Py_None, d[2]),
                  result(Py_None, dw[0]), result(Py_None, dw[1])});
@@ -420,13 +437,15 @@ PyObject* attend(PyObject* const* args, Py_ssize_t n, bool prefill) {
     const int causal = prefill ? c.truth(10) : 0;
     if (!c.ok) return nullptr;
     const int64_t Hkv = pool->size(1);
-    at::Tensor made_out, made_lse, made_ws;
+    at::Tensor made_out, made_lse;
+    c10::DataPtr own_ws;
     size_t bytes = ws ? static_cast<size_t>(ws->numel()) : 0;
+    void* work = ptr(ws);
     if (!ws) {
       bytes = prefill ? g_entry.prefill_ws(S, Hq, Hkv, Tq, D, len) : g_entry.decode_ws(S, Hq, Hkv, D, len);
       if (bytes) {
-        made_ws = make({static_cast<int64_t>(bytes)}, *q, at::kByte);
-        ws = &made_ws;
+        own_ws = scratch(bytes);
+        work = own_ws.get();
       }
     }
     if (!out) {
@@ -443,9 +462,9 @@ PyObject* attend(PyObject* const* args, Py_ssize_t n, bool prefill) {
     const int st = released([&] { return
         prefill ? g_entry.prefill(ptr(q), ptr(pool), table, lens, 16, S, Hq, Hkv, Tq, D,
                                   bt->size(1), pool->size(0), len, causal, scale, ptr(out), lse_p,
-                                  ptr(ws), bytes, c.stream)
+                                  work, bytes, c.stream)
                 : g_entry.decode(ptr(q), ptr(pool), table, lens, 16, S, Hq, Hkv, D, bt->size(1),
-                                 pool->size(0), len, scale, ptr(out), lse_p, ptr(ws), bytes,
+                                 pool->size(0), len, scale, ptr(out), lse_p, work, bytes,
                                  c.stream); });
     if (st != ATTN_OK) return PyLong_FromLong(st);
     return pack({result(args[6], made_out), result(args[7], made_lse)});
