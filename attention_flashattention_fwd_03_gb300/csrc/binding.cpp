@@ -9,8 +9,8 @@
 // for everything it does not know, which the wrapper then handles, errors included.
 #include <Python.h>
 
+#include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
 #include <c10/core/Allocator.h>
 #include <c10/core/TensorImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -19,6 +19,7 @@
 #include <cstring>
 #include <exception>
 #include <initializer_list>
+#include <optional>
 
 #include "gbattn.h"
 
@@ -189,11 +190,16 @@ int released(F call) {
   return status;
 }
 
-at::Tensor make(at::IntArrayRef sizes, const at::Tensor& like, at::ScalarType type) {
-  return at::empty(sizes, like.options().dtype(type).requires_grad(false));
+// Device memory comes from torch's allocator for the current device, without the
+// dispatcher's way there.
+c10::Allocator* allocator() { return c10::GetAllocator(at::kCUDA); }
+
+at::Tensor make(at::IntArrayRef sizes, at::ScalarType type) {
+  return at::detail::empty_generic(sizes, allocator(), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                   type, std::nullopt);
 }
 
-// Heads h0 .. h0 + n - 1 of a fused [B, T, H, D] buffer, without the dispatcher's way there.
+// Heads h0 .. h0 + n - 1 of a fused [B, T, H, D] buffer.
 at::Tensor heads_of(const at::Tensor& fused, int64_t h0, int64_t n) {
   at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
       c10::TensorImpl::VIEW, c10::Storage(fused.storage()), fused.key_set(), fused.dtype());
@@ -203,9 +209,9 @@ at::Tensor heads_of(const at::Tensor& fused, int64_t h0, int64_t n) {
   return t;
 }
 
-// Device memory of a call's own, given back to the allocator (which reuses it in stream
-// order) when the call returns.
-c10::DataPtr scratch(size_t bytes) { return c10::GetAllocator(at::kCUDA)->allocate(bytes); }
+// Memory of a call's own, given back to the allocator (which reuses it in stream order) when
+// the call returns.
+c10::DataPtr scratch(size_t bytes) { return allocator()->allocate(bytes); }
 
 // The norm and rotation operands from argument i on: cos_sin, q_weight, k_weight, eps,
 // interleaved, positions.
@@ -269,7 +275,7 @@ PyObject* rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
     for (int i = 0; i < 3; ++i) {
       if (!in[i] && out[i]) return nullptr;
       if (in[i] && !out[i]) {
-        made[i] = make({B, i == 0 ? Hq : Hkv, T, D}, *some, at::kBFloat16);
+        made[i] = make({B, i == 0 ? Hq : Hkv, T, D}, at::kBFloat16);
         out[i] = &made[i];
       }
     }
@@ -304,13 +310,13 @@ PyObject* rope_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
       return nullptr;
     const int64_t nq = g[0] ? Hq : 0, nk = g[1] ? Hkv : 0, nv = g[2] ? Hkv : 0;
     if (B == 0 || T == 0 || nq + nk + nv == 0) return nullptr;
-    const at::Tensor fused = make({B, T, nq + nk + nv, D}, *some, at::kBFloat16);
+    const at::Tensor fused = make({B, T, nq + nk + nv, D}, at::kBFloat16);
     at::Tensor d[3], dw[2];
     if (nq) d[0] = heads_of(fused, 0, nq);
     if (nk) d[1] = heads_of(fused, nq, nk);
     if (nv) d[2] = heads_of(fused, nq + nk, nv);
-    if (r.qw) dw[0] = make({D}, *some, at::kFloat);
-    if (r.kw) dw[1] = make({D}, *some, at::kFloat);
+    if (r.qw) dw[0] = make({D}, at::kFloat);
+    if (r.kw) dw[1] = make({D}, at::kFloat);
     size_t bytes = 0;
     c10::DataPtr ws;
     if (r.qw || r.kw) {
@@ -359,7 +365,7 @@ PyObject* append_to(PyObject* const* args, Py_ssize_t n, bool four) {
     if (!c.ok || (qo && !q)) return nullptr;
     at::Tensor made;
     if (q && !qo) {
-      made = make({S, Hq, Tn, D}, *k, at::kBFloat16);
+      made = make({S, Hq, Tn, D}, at::kBFloat16);
       qo = &made;
     }
     const Strides sq(q), sk(k), sv(v);
@@ -449,11 +455,11 @@ PyObject* attend(PyObject* const* args, Py_ssize_t n, bool prefill) {
       }
     }
     if (!out) {
-      made_out = make(q->sizes(), *q, at::kBFloat16);
+      made_out = make(q->sizes(), at::kBFloat16);
       out = &made_out;
     }
     if (!lse && want_lse) {
-      made_lse = make(q->sizes().slice(0, q->dim() - 1), *q, at::kFloat);
+      made_lse = make(q->sizes().slice(0, q->dim() - 1), at::kFloat);
       lse = &made_lse;
     }
     const int32_t* table = static_cast<const int32_t*>(ptr(bt));
