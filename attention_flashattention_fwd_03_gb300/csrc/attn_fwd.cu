@@ -762,6 +762,11 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1)
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
+  if constexpr (SRC == Src::kPaged4) {
+    // launched as a programmatic dependent: the preceding kernel's writes (an append's) are
+    // complete and visible past this point
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
   if constexpr (SRC != Src::kContiguous) {
     // every CTA sorts the classes for itself: a class's place is the number of classes
     // before it, by tiles and then by index
@@ -828,9 +833,19 @@ cudaError_t set_smem() {
 }
 
 template <int D, Src SRC>
-void launch(int grid, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
-            const FwdParams& p, cudaStream_t stream) {
-  attn_fwd_kernel<D, SRC><<<grid, kThreads<SRC>, (Cfg<D, SRC>::SMEM_BYTES), stream>>>(tmQ, tmK, tmV, p);
+cudaError_t launch(int grid, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                   const CUtensorMap& tmV, const FwdParams& p, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads<SRC>);
+  cfg.dynamicSmemBytes = Cfg<D, SRC>::SMEM_BYTES;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = SRC == Src::kPaged4 ? 1 : 0;  // the others do not wait for the grid before
+  return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<D, SRC>, tmQ, tmK, tmV, p);
 }
 
 }  // namespace
@@ -851,18 +866,11 @@ cudaError_t launch_attn_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, cons
   if (grid <= 0) return cudaSuccess;
   auto run = [&](auto d) {
     constexpr int DD = decltype(d)::value;
-    if (p.kv4_pool != nullptr)
-      launch<DD, Src::kPaged4>(grid, tmQ, tmK, tmV, p, stream);
-    else if (p.block_table != nullptr)
-      launch<DD, Src::kPaged>(grid, tmQ, tmK, tmV, p, stream);
-    else
-      launch<DD, Src::kContiguous>(grid, tmQ, tmK, tmV, p, stream);
+    if (p.kv4_pool != nullptr) return launch<DD, Src::kPaged4>(grid, tmQ, tmK, tmV, p, stream);
+    if (p.block_table != nullptr) return launch<DD, Src::kPaged>(grid, tmQ, tmK, tmV, p, stream);
+    return launch<DD, Src::kContiguous>(grid, tmQ, tmK, tmV, p, stream);
   };
-  if (p.D == 64)
-    run(std::integral_constant<int, 64>{});
-  else
-    run(std::integral_constant<int, 128>{});
-  return cudaGetLastError();
+  return p.D == 64 ? run(std::integral_constant<int, 64>{}) : run(std::integral_constant<int, 128>{});
 }
 
 }  // namespace gbattn

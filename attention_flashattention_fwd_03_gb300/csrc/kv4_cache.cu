@@ -28,6 +28,9 @@ __global__ void __launch_bounds__(2 * D) paged_kv4_gather_kernel(const Gather4Pa
   const unsigned set = blockIdx.x % n_sets, rb = blockIdx.x / n_sets;
   const int lb = rb % n_blocks, r = rb / n_blocks;
   const int h0 = set * kHeads;
+  // launched as a programmatic dependent: the preceding kernel's writes (an append's) are
+  // complete and visible past this point
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // (both loads at once; an entry past the table's row is not read)
   const int L = p.seq_lens[r];
   const long long phys =
@@ -74,11 +77,16 @@ cudaError_t launch_kv4_gather(const Gather4Params& p, int D, cudaStream_t stream
   const long long n_blocks = (p.max_seq_len + kPagedBlock - 1) / kPagedBlock;
   const long long grid = static_cast<long long>(p.S) * ((p.Hkv + kHeads - 1) / kHeads) * n_blocks;
   if (grid <= 0) return cudaSuccess;
-  if (D == 64)
-    paged_kv4_gather_kernel<64><<<static_cast<unsigned>(grid), 128, 0, stream>>>(p);
-  else
-    paged_kv4_gather_kernel<128><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(2 * D);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, D == 64 ? paged_kv4_gather_kernel<64> : paged_kv4_gather_kernel<128>, p);
 }
 
 }  // namespace gbattn
