@@ -178,7 +178,7 @@ __device__ __forceinline__ int tiles_of(int qp, int i, int L, const FwdParams& p
 // adjacent (batches of more classes than it holds keep the order of the items).  (On 16 items of
 // 1024 .. 8192 keys, 1024 units on 152 CTAs, the busiest CTA had 1.61 times the mean work
 // in the order of the items and has 1.04 times it in this one; bf16 pools 571 -> 368 us,
-// 4-bit 663 -> 438 us.)
+// 4-bit 663 -> 438 us, 432 with its launch as a programmatic dependent.)
 __device__ __forceinline__ Unit unit_at(int u, const FwdParams& p, bool paged,
                                         uint32_t order) {
   Unit U;

@@ -702,7 +702,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
 // is slow.  With many warps a head, i.e. few CTAs, each goes through it once over no pieces
 // before it waits for the split kernel, which then still runs (36.6 -> 35.9 us a call on
 // 131000 tokens, 19.1 -> 18.5 on 40000; the 768 CTAs of 64 requests would take issue slots
-// from the split kernel: 25.0 -> 25.3).
+// from the split kernel: 25.0 -> 25.3).  It does not let the next call's split kernel in
+// early: that one takes the room its own CTAs need (64 requests in a row 24.6 -> 29.0 us).
 template <int D, int MW>
 __global__ void __launch_bounds__(MW * 32) kv4_decode_merge_kernel(const Kv4DecodeParams p) {
   constexpr int PER = D / 32;  // dims per lane

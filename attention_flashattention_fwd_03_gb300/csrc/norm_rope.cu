@@ -8,7 +8,7 @@
 // row and weights are read once and every row moves as whole 128- or 256-byte segments;
 // the loads of four passes are in flight together.  D 128: a 16k prompt of 32/8 heads (411
 // MB) 66 us, 91 % of the copy rate; 16 x 512 tokens appended to the bf16 cache (202 MB) 36 us,
-// 82 %; to the 4-bit cache (187 MB) 40 us, 68 %, its quantiser taking a quarter of the
+// 83 %; to the 4-bit cache (187 MB) 40 us, 69 %, its quantiser taking a quarter of the
 // instructions at 65 % of the issue slots.
 #include <cuda_runtime.h>
 
