@@ -259,3 +259,71 @@ def test_a_prompt_in_chunks_then_decode(gb):
     # of |O| each, twice; values are at most v_max (1 + 2^-5) in the cache
     assert torch.all((o - o2).abs() <= 4 * 2.0 ** -8 * v_max * (1 + 2.0 ** -5))
     assert torch.all((lse - lse2).abs() <= 1e-4)
+
+
+def test_calls_in_a_row_equal_calls_apart(gb):
+    """The kernels let their successors be set up before they end.  A chain of calls in the
+    same buffers, each reading or overwriting what the one before wrote, gives the bits of
+    the same chain with a synchronisation after every call."""
+    S, Hq, Hkv, D, Tn, rounds, first = 16, 8, 2, 128, 64, 6, 1500
+    room = first + 16 * S + rounds * (Tn + 1)
+    bt = np.random.default_rng(9).permutation(S * (room // 16 + 1)).reshape(S, -1).astype(np.int32)
+    kb, vb = synth.normal_bf16(59000, (2, bt.size, Hkv, 16, D))
+    start = first + 16 * np.arange(S)
+    lens = [to_dev_i32(start + i * (Tn + 1)) for i in range(rounds)]
+    more = [to_dev_i32(start + i * (Tn + 1) + Tn) for i in range(rounds)]
+    last = [to_dev_i32(start + i * (Tn + 1) + Tn + 1) for i in range(rounds)]
+    rows = [to_dev(synth.normal_bf16(59100 + i, (S, Tn, Hq + 2 * Hkv, D))) for i in range(rounds)]
+    cs = torch.from_numpy(ref.table(room, D)).cuda()
+    w = to_dev(synth.float_to_bf16_bits((1 + 0.2 * synth.normals(59200, D)).astype(np.float32)))
+    how = dict(cos_sin=cs, q_weight=w, k_weight=w)
+
+    def chain(wait):
+        dev = dict(device="cuda")
+        pool = torch.from_numpy(ref.pool_from_bf16(kb, vb)).cuda()
+        table = to_dev_i32(bt)
+        new = torch.empty(S, dtype=torch.int32, **dev)
+        qkv = [torch.empty((S, h, Tn, D), dtype=torch.bfloat16, **dev) for h in (Hq, Hkv, Hkv)]
+        d = [torch.empty((S, Tn, h, D), dtype=torch.bfloat16, **dev) for h in (Hq, Hkv, Hkv)]
+        dw = torch.empty((2, D), **dev)
+        wsb = torch.empty(gb.qkv_norm_rope_bwd_workspace_size(S, Tn, D), dtype=torch.uint8, **dev)
+        ws = torch.empty(gb.paged_kv4_attn_decode_workspace_size(S, Hq, Hkv, D, room),
+                         dtype=torch.uint8, **dev)
+        assert ws.numel() > 0 and gb.paged_kv4_attn_prefill_workspace_size(S, Hq, Hkv, Tn, D, room) == 0
+        q1 = torch.empty((S, Hq, 1, D), dtype=torch.bfloat16, **dev)
+        hist = [torch.zeros((S, Hkv, room, D), dtype=torch.bfloat16, **dev) for _ in range(2)]
+        o, lse = torch.empty_like(qkv[0]), torch.empty((S, Hq, Tn), **dev)
+        o1, lse1 = torch.empty((S, Hq, D), dtype=torch.bfloat16, **dev), torch.empty((S, Hq), **dev)
+        out = []
+        for i in range(rounds):
+            q, k, v = rows[i].split([Hq, Hkv, Hkv], 2)
+            calls = [
+                lambda: gb.qkv_norm_rope(q, k, v, q_out=qkv[0], k_out=qkv[1], v_out=qkv[2], **how),
+                lambda: gb.qkv_norm_rope_bwd(*qkv, q, k, dq=d[0], dk=d[1], dv=d[2], dq_weight=dw[0],
+                                             dk_weight=dw[1], workspace=wsb, **how),
+                lambda: gb.paged_kv4_append(d[0], d[1], d[2], pool, table, lens[i], q_out=qkv[0],
+                                            new_seq_lens=new, **how),
+                lambda: gb.paged_kv4_gather(pool, table, new, room, k_out=hist[0], v_out=hist[1]),
+                lambda: gb.paged_kv4_attn_prefill(qkv[0], pool, table, more[i], room, out=o, lse=lse),
+                lambda: gb.paged_kv4_append(q[:, :1], k[:, :1], v[:, :1], pool, table, new, q_out=q1,
+                                            **how),
+                lambda: gb.paged_kv4_attn_decode(q1[:, :, 0], pool, table, last[i], room, out=o1,
+                                                 lse=lse1, workspace=ws),
+                lambda: gb.paged_kv4_append(None, k[:, :1], v[:, :1], pool, table, new, **how),
+                lambda: gb.paged_kv4_attn_decode(q1[:, :, 0], pool, table, last[i], room, out=o1,
+                                                 lse=lse1, workspace=ws),
+            ]
+            for call in calls:
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            out += [t.clone() for t in (*qkv, *d, dw, pool, *hist, o, lse, o1, lse1)]
+        torch.cuda.synchronize()
+        assert gb.attn_device_status() == (gb.ATTN_OK, 0)
+        return out
+
+    apart = chain(True)
+    for _ in range(3):
+        for a, b in zip(apart, chain(False)):
+            assert torch.equal(a, b)
+    assert all(t.isfinite().all() for t in apart if t.is_floating_point())
