@@ -113,7 +113,7 @@ struct Kv4DecodeWorkspace {
   size_t off_part_lse, off_seg_first, off_seg_last, bytes;  // part_o at 0
 };
 Kv4DecodeWorkspace kv4_decode_workspace(int S, int Hq, int Hkv, int Tq, int D, int max_seq_len);
-bool kv4_direct(int Tq, int max_seq_len);  // one launch without a workspace
+bool kv4_direct(int Tq, int chunks, int max_seq_len);  // one launch without a workspace
 long long kv4_max_steps(int S, int segs, int max_seq_len);  // steps of 64 tokens of a batch
 struct Kv4Rows {
   int rows, piece_rows, chunks;

@@ -856,7 +856,7 @@ template <int D>
 cudaError_t launch(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms, cudaStream_t stream) {
   const bool multi = p.Tq > 1 || p.chunks > 1;
   cudaError_t e;
-  if (kv4_direct(p.Tq, p.max_seq_len))
+  if (kv4_direct(p.Tq, p.chunks, p.max_seq_len))
     return p.piece_rows <= 8 ? launch_split<D, 1, Deal::kDirect>(pool, p, num_sms, stream)
                              : launch_split<D, 2, Deal::kDirect>(pool, p, num_sms, stream);
   if (p.piece_rows <= 8)
@@ -901,13 +901,16 @@ Kv4Rows kv4_rows(int Hq, int Hkv, int Tq) {
   return r;
 }
 
-bool kv4_direct(int Tq, int max_seq_len) { return Tq == 1 && max_seq_len <= kDirectMaxLen; }
+// (a CTA of that form is a whole KV head: rows in several chunks are kMulti's)
+bool kv4_direct(int Tq, int chunks, int max_seq_len) {
+  return Tq == 1 && chunks == 1 && max_seq_len <= kDirectMaxLen;
+}
 
 Kv4DecodeWorkspace kv4_decode_workspace(int S, int Hq, int Hkv, int Tq, int D, int max_seq_len) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   Kv4DecodeWorkspace w{};
-  if (kv4_direct(Tq, max_seq_len)) return w;
   const Kv4Rows r = kv4_rows(Hq, Hkv, Tq);
+  if (kv4_direct(Tq, r.chunks, max_seq_len)) return w;
   const long long segs = static_cast<long long>(S) * Hkv * r.chunks;
   const long long steps = kv4_max_steps(S, Hkv * r.chunks, max_seq_len);
   w.pieces = (steps < kKv4MaxRanges ? steps : kKv4MaxRanges) + segs;

@@ -134,6 +134,30 @@ def test_rows_match_the_oracle(gb, Hq, Hkv, D, Tq, lens, causal):
     check_rows(c, o, lse, causal)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(17, 1, 128), (24, 1, 64), (32, 1, 128), (34, 2, 64), (16, 1, 128)])
+@pytest.mark.parametrize("max_len", [512, 513, 1024, 1025])
+def test_one_token_of_wide_groups(gb, Hq, Hkv, D, max_len):
+    """Single tokens of more than 16 query heads on a KV head, on both sides of every length
+    bound at which the kernels change; what lies around the outputs stays as it was."""
+    c = Item(Hq, Hkv, D, 1, [1, 0, 17, 64, 65, 300, 500, 512, 511], 61400 + Hq + max_len, max_len=max_len)
+    B = len(c.lens)
+    # (16 heads are one pass: a single launch without a workspace up to 1024 keys)
+    wide = Hq // Hkv > 16
+    assert uses_rows(gb, c) == ((max_len > 512 or B * Hq > 152) if wide else max_len > 1024)
+    n = B * Hq
+    for causal in (True, False):
+        around = torch.full((3 * n * D,), 7.0, dtype=torch.bfloat16, device="cuda")
+        around_lse = torch.full((3 * n,), 7.0, device="cuda")
+        o = around[n * D:2 * n * D].view(B, Hq, 1, D)
+        lse = around_lse[n:2 * n].view(B, Hq, 1)
+        c.run(gb, causal, out=o, lse=lse)
+        torch.cuda.synchronize()
+        assert gb.attn_device_status() == (gb.ATTN_OK, 0)
+        check_rows(c, o, lse, causal)
+        assert torch.all(around[:n * D] == 7) and torch.all(around[2 * n * D:] == 7)
+        assert torch.all(around_lse[:n] == 7) and torch.all(around_lse[2 * n:] == 7)
+
+
 def test_one_drafted_token_equals_the_decode(gb):
     c = Item(12, 2, 128, 1, [1, 300, 4000], 61500)  # (past the decode's one-launch form)
     o, lse = c.run(gb, True)

@@ -223,6 +223,19 @@ def test_kv4_prefill_refusals(kw, code):
                                            a["ws"], max(0, need + a["wsb"]), None) == code
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group,Hkv,B", [(17, 1, 1), (17, 2, 9), (24, 1, 1), (32, 1, 8), (40, 3, 2)])
+def test_single_tokens_of_wide_groups_have_a_workspace(group, Hkv, B, D):
+    """More query heads on a KV head than one pass takes (16) are several segments, whose
+    results meet in the workspace: one-launch decoding, a CTA a KV head, is not for them."""
+    size = gb.paged_kv4_attn_prefill_workspace_size
+    for ml in (513, 1024, 1025, 100000):
+        assert size(B, group * Hkv, Hkv, 1, D, ml) > 0
+    if B * group * Hkv > 152:  # (fewer units on so short a cache: tiles)
+        assert size(B, group * Hkv, Hkv, 1, D, 512) > 0
+    assert size(B, 16 * Hkv, Hkv, 1, D, 1024) == 0
+
+
 # --------------------------------------------------------------------------- #
 # argument checks of the binding
 # --------------------------------------------------------------------------- #
