@@ -43,6 +43,12 @@ PyObject *g_get_device = nullptr, *g_get_stream = nullptr;
 
 constexpr int64_t kMaxSize = 0x7fffffff;  // the C ABI's sizes are ints
 
+// What a plain CUDA tensor is made of.  Others (those that a function transform wraps or
+// batches, zeros without memory, values kept negated) have no memory, or hold something
+// else in it.
+const c10::DispatchKeySet kPlain({c10::DispatchKey::CUDA, c10::DispatchKey::AutogradCUDA,
+                                  c10::DispatchKey::ADInplaceOrView, c10::DispatchKey::AutocastCUDA});
+
 // The arguments of one call; `ok` falls when something is not the usual.
 struct Call {
   PyObject* const* args;
@@ -59,7 +65,8 @@ struct Call {
       return nullptr;
     }
     const at::Tensor& t = THPVariable_Unpack(o);
-    if (!t.defined() || t.layout() != at::kStrided || !t.is_cuda()) {
+    if (!t.defined() || t.layout() != at::kStrided || !t.is_cuda() || !t.has_storage() ||
+        !kPlain.has_all(t.key_set())) {
       ok = false;
       return nullptr;
     }
@@ -180,14 +187,20 @@ PyObject* pack(std::initializer_list<PyObject*> items) {
   return nullptr;
 }
 
-// Calls into the library without the interpreter's lock: a launch waits when the GPU's
-// queue is full, and what it waits for may need another thread.
-template <typename F>
-int released(F call) {
+// Calls an entry point without the interpreter's lock: a launch waits when the GPU's queue
+// is full, and what it waits for may need another thread.  The arguments, which may throw,
+// are made before the lock is given up, and it is taken back however the call ends.
+struct Unlocked {
   PyThreadState* state = PyEval_SaveThread();
-  const int status = call();
-  PyEval_RestoreThread(state);
-  return status;
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+template <typename... P, typename... A>
+int released(int (*entry)(P...), A... args) {
+  const Unlocked unlocked;
+  return entry(static_cast<P>(args)...);
 }
 
 // Device memory comes from torch's allocator for the current device, without the
@@ -280,11 +293,9 @@ PyObject* rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
       }
     }
     const Strides sq(q), sk(k), sv(v);
-    const int st = released([&] { return g_entry.rope(ptr(q), ptr(k), ptr(v), sq.s, sk.s, sv.s, ptr(r.qw), ptr(r.kw),
-                                static_cast<const float*>(ptr(r.cs)),
-                                static_cast<const int32_t*>(ptr(r.pos)), B, T, Hq, Hkv, D, r.rot,
-                                r.max_pos, r.interleaved, r.eps, ptr(out[0]), ptr(out[1]),
-                                ptr(out[2]), c.stream); });
+    const int st = released(g_entry.rope, ptr(q), ptr(k), ptr(v), sq.s, sk.s, sv.s, ptr(r.qw),
+                            ptr(r.kw), ptr(r.cs), ptr(r.pos), B, T, Hq, Hkv, D, r.rot, r.max_pos,
+                            r.interleaved, r.eps, ptr(out[0]), ptr(out[1]), ptr(out[2]), c.stream);
     if (st != ATTN_OK) return PyLong_FromLong(st);
     return pack({result(args[9], made[0]), result(args[10], made[1]), result(args[11], made[2])});
   });
@@ -326,12 +337,11 @@ PyObject* rope_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor* dp[3];
     for (int i = 0; i < 3; ++i) dp[i] = d[i].defined() ? &d[i] : nullptr;
     const Strides sq(q), sk(k), s0(dp[0]), s1(dp[1]), s2(dp[2]);
-    const int st = released([&] { return g_entry.rope_bwd(
-        ptr(g[0]), ptr(g[1]), ptr(g[2]), ptr(q), ptr(k), sq.s, sk.s, ptr(r.qw), ptr(r.kw),
-        static_cast<const float*>(ptr(r.cs)), static_cast<const int32_t*>(ptr(r.pos)), B, T, Hq,
-        Hkv, D, r.rot, r.max_pos, r.interleaved, r.eps, ptr(dp[0]), ptr(dp[1]), ptr(dp[2]), s0.s,
-        s1.s, s2.s, r.qw ? dw[0].data_ptr<float>() : nullptr,
-        r.kw ? dw[1].data_ptr<float>() : nullptr, ws.get(), bytes, c.stream); });
+    const int st = released(
+        g_entry.rope_bwd, ptr(g[0]), ptr(g[1]), ptr(g[2]), ptr(q), ptr(k), sq.s, sk.s, ptr(r.qw),
+        ptr(r.kw), ptr(r.cs), ptr(r.pos), B, T, Hq, Hkv, D, r.rot, r.max_pos, r.interleaved, r.eps,
+        ptr(dp[0]), ptr(dp[1]), ptr(dp[2]), s0.s, s1.s, s2.s, ptr(r.qw ? &dw[0] : nullptr),
+        ptr(r.kw ? &dw[1] : nullptr), ws.get(), bytes, c.stream);
     if (st != ATTN_OK) return PyLong_FromLong(st);
     return pack({result(Py_None, d[0]), result(Py_None, d[1]), result(Py_None, d[2]),
                  result(Py_None, dw[0]), result(Py_None, dw[1])});
@@ -369,20 +379,15 @@ PyObject* append_to(PyObject* const* args, Py_ssize_t n, bool four) {
       qo = &made;
     }
     const Strides sq(q), sk(k), sv(v);
-    const float* cs = static_cast<const float*>(ptr(r.cs));
-    const int32_t* pos = static_cast<const int32_t*>(ptr(r.pos));
-    const int32_t* table = static_cast<const int32_t*>(ptr(bt));
-    const int32_t* lens = static_cast<const int32_t*>(ptr(sl));
-    int32_t* after = static_cast<int32_t*>(ptr(nsl));
-    const int st = released([&] { return
-        four ? g_entry.append4(ptr(q), ptr(k), ptr(v), sq.s, sk.s, sv.s, ptr(r.qw), ptr(r.kw), cs,
-                               pos, ptr(kp), table, lens, after, 16, S, Tn, Hq, Hkv, D,
-                               bt->size(1), kp->size(0), r.rot, r.max_pos, r.interleaved, r.eps,
-                               ptr(qo), c.stream)
-             : g_entry.append(ptr(q), ptr(k), ptr(v), sq.s, sk.s, sv.s, ptr(r.qw), ptr(r.kw), cs,
-                              pos, ptr(kp), ptr(vp), table, lens, after, kp->size(2), S, Tn, Hq,
-                              Hkv, D, bt->size(1), kp->size(0), r.rot, r.max_pos, r.interleaved,
-                              r.eps, ptr(qo), c.stream); });
+    const int st =
+        four ? released(g_entry.append4, ptr(q), ptr(k), ptr(v), sq.s, sk.s, sv.s, ptr(r.qw),
+                        ptr(r.kw), ptr(r.cs), ptr(r.pos), ptr(kp), ptr(bt), ptr(sl), ptr(nsl), 16,
+                        S, Tn, Hq, Hkv, D, bt->size(1), kp->size(0), r.rot, r.max_pos,
+                        r.interleaved, r.eps, ptr(qo), c.stream)
+             : released(g_entry.append, ptr(q), ptr(k), ptr(v), sq.s, sk.s, sv.s, ptr(r.qw),
+                        ptr(r.kw), ptr(r.cs), ptr(r.pos), ptr(kp), ptr(vp), ptr(bt), ptr(sl),
+                        ptr(nsl), kp->size(2), S, Tn, Hq, Hkv, D, bt->size(1), kp->size(0), r.rot,
+                        r.max_pos, r.interleaved, r.eps, ptr(qo), c.stream);
     if (st != ATTN_OK) return PyLong_FromLong(st);
     PyObject* after_obj = args[14];
     Py_INCREF(after_obj);
@@ -408,9 +413,8 @@ PyObject* gather(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor* ko = c.need(c.dense(4, at::kBFloat16, {S, Hkv, len, D}));
     const at::Tensor* vo = c.need(c.dense(5, at::kBFloat16, {S, Hkv, len, D}));
     if (!c.ok) return nullptr;
-    const int st = released([&] { return g_entry.gather(ptr(pool), static_cast<const int32_t*>(ptr(bt)),
-                                  static_cast<const int32_t*>(ptr(sl)), 16, S, Hkv, D, bt->size(1),
-                                  pool->size(0), len, ptr(ko), ptr(vo), c.stream); });
+    const int st = released(g_entry.gather, ptr(pool), ptr(bt), ptr(sl), 16, S, Hkv, D,
+                            bt->size(1), pool->size(0), len, ptr(ko), ptr(vo), c.stream);
     if (st != ATTN_OK) return PyLong_FromLong(st);
     return pack({result(args[4], at::Tensor()), result(args[5], at::Tensor())});
   });
@@ -462,16 +466,13 @@ PyObject* attend(PyObject* const* args, Py_ssize_t n, bool prefill) {
       made_lse = make(q->sizes().slice(0, q->dim() - 1), at::kFloat);
       lse = &made_lse;
     }
-    const int32_t* table = static_cast<const int32_t*>(ptr(bt));
-    const int32_t* lens = static_cast<const int32_t*>(ptr(sl));
-    float* lse_p = static_cast<float*>(ptr(lse));
-    const int st = released([&] { return
-        prefill ? g_entry.prefill(ptr(q), ptr(pool), table, lens, 16, S, Hq, Hkv, Tq, D,
-                                  bt->size(1), pool->size(0), len, causal, scale, ptr(out), lse_p,
-                                  work, bytes, c.stream)
-                : g_entry.decode(ptr(q), ptr(pool), table, lens, 16, S, Hq, Hkv, D, bt->size(1),
-                                 pool->size(0), len, scale, ptr(out), lse_p, work, bytes,
-                                 c.stream); });
+    const int st =
+        prefill ? released(g_entry.prefill, ptr(q), ptr(pool), ptr(bt), ptr(sl), 16, S, Hq, Hkv, Tq,
+                           D, bt->size(1), pool->size(0), len, causal, scale, ptr(out), ptr(lse),
+                           work, bytes, c.stream)
+                : released(g_entry.decode, ptr(q), ptr(pool), ptr(bt), ptr(sl), 16, S, Hq, Hkv, D,
+                           bt->size(1), pool->size(0), len, scale, ptr(out), ptr(lse), work, bytes,
+                           c.stream);
     if (st != ATTN_OK) return PyLong_FromLong(st);
     return pack({result(args[6], made_out), result(args[7], made_lse)});
   });
