@@ -468,6 +468,19 @@ def _check_rope(cos_sin, q_weight, k_weight, positions, B, T, D, device):
     return shape[1], shape[0]
 
 
+def _check_no_gradients(op, **operands):
+    """Raises for an operand through which torch expects a derivative: outputs carry none."""
+    grad_mode, fwd = _torch.is_grad_enabled(), _torch.autograd.forward_ad
+    for name, t in operands.items():
+        if t is None:
+            continue
+        if (grad_mode and t.requires_grad) or fwd.unpack_dual(t).tangent is not None:
+            raise ValueError(
+                f"{op} records nothing for automatic differentiation, and {name} takes part in it: "
+                "call it under torch.no_grad() (or in an autograd.Function) and take the "
+                "gradients from qkv_norm_rope_bwd")
+
+
 def _load_torch():
     global _torch, _Tensor, _bf16, _f32, _i32, _u8
     import torch
@@ -526,6 +539,10 @@ def qkv_norm_rope(q, k, v=None, cos_sin=None, q_weight=None, k_weight=None, eps:
     ``cos_sin`` [max_pos, rot_dim] fp32 holds rot_dim / 2 cosines, then the sines, of
     each position (None: no rotation); ``q_weight``/``k_weight`` [D] bf16 (None: no
     norm); ``positions`` [B,T] int32 (None: 0 .. T-1).
+
+    Nothing is recorded for automatic differentiation: qkv_norm_rope_bwd computes the
+    gradients.  Where gradients are enabled, operands that require one (and the duals of
+    forward mode) are refused; call it under torch.no_grad() or in an autograd.Function.
     """
     if _torch is None:
         _load_torch()
@@ -553,6 +570,8 @@ def qkv_norm_rope(q, k, v=None, cos_sin=None, q_weight=None, k_weight=None, eps:
         if out is not None:
             _check(name + "_out", out, _bf16, (B, heads, T, D), device)
     rot, max_pos = _check_rope(cos_sin, q_weight, k_weight, positions, B, T, D, device)
+    _check_no_gradients("qkv_norm_rope", q=q, k=k, v=v, cos_sin=cos_sin, q_weight=q_weight,
+                        k_weight=k_weight)
     _require_cuda(device)
     with _On(device, stream) as handle:
         if q_out is None and q is not None:
@@ -584,7 +603,8 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
     (needed with a weight).  dq, dk, dv are [B,T,H,D] bf16 and may be strided views
     without overlap; when none is given they are views of one [B,T,all heads,D] buffer,
     the gradient of a fused projection.  The weight gradients [D] are fp32, None for an
-    operand without a weight.
+    operand without a weight.  Operands that take part in automatic differentiation are
+    refused as in qkv_norm_rope.
     """
     if _torch is None:
         _load_torch()
@@ -626,11 +646,13 @@ def qkv_norm_rope_bwd(dq_out, dk_out, dv_out=None, q=None, k=None, cos_sin=None,
             _check(f"d{name}_weight", dw, _f32, (D,), device)
     if workspace is not None:
         _check_tensor("workspace", workspace, _u8, None, device)
-    _require_cuda(device)
     if q_weight is None:
         q = None
     if k_weight is None:
         k = None
+    _check_no_gradients("qkv_norm_rope_bwd", dq_out=dq_out, dk_out=dk_out, dv_out=dv_out, q=q, k=k,
+                        cos_sin=cos_sin, q_weight=q_weight, k_weight=k_weight)
+    _require_cuda(device)
     with _On(device, stream) as handle:
         if dq is None and dk is None and dv is None:
             nq, nk = (Hq if dq_out is not None else 0), (Hkv if dk_out is not None else 0)

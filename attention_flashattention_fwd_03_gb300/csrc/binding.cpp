@@ -11,6 +11,7 @@
 
 #include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/core/Allocator.h>
 #include <c10/core/TensorImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -52,6 +53,7 @@ const c10::DispatchKeySet kPlain({c10::DispatchKey::CUDA, c10::DispatchKey::Auto
 // The arguments of one call; `ok` falls when something is not the usual.
 struct Call {
   PyObject* const* args;
+  bool differentiable = false;  // whether a gradient might be expected of the call
   bool ok = true;
   int dev = -1;
   void* stream = nullptr;
@@ -67,6 +69,11 @@ struct Call {
     const at::Tensor& t = THPVariable_Unpack(o);
     if (!t.defined() || t.layout() != at::kStrided || !t.is_cuda() || !t.has_storage() ||
         !kPlain.has_all(t.key_set())) {
+      ok = false;
+      return nullptr;
+    }
+    // (the wrapper refuses what the outputs would silently be cut off from)
+    if (differentiable && ((t.requires_grad() && at::GradMode::is_enabled()) || t._fw_grad(0).defined())) {
       ok = false;
       return nullptr;
     }
@@ -269,6 +276,7 @@ PyObject* guarded(PyObject* const* args, Py_ssize_t n, Py_ssize_t expected, F bo
 // q, k, v, cos_sin, q_weight, k_weight, eps, interleaved, positions, q_out, k_out, v_out
 PyObject* rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded(args, n, 12, [&](Call& c) -> PyObject* {
+    c.differentiable = true;
     const at::Tensor *q = c.rows(0), *k = c.rows(1), *v = c.rows(2);
     const at::Tensor* some = q ? q : (k ? k : v);
     if (!c.ok || !some || !c.on(*some)) return nullptr;
@@ -305,6 +313,7 @@ PyObject* rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // (gradient buffers and workspace made here)
 PyObject* rope_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded(args, n, 11, [&](Call& c) -> PyObject* {
+    c.differentiable = true;
     const at::Tensor* g[3] = {c.tensor(0), c.tensor(1), c.tensor(2)};
     const at::Tensor* some = g[0] ? g[0] : (g[1] ? g[1] : g[2]);
     if (!c.ok || !some || some->dim() != 4 || !c.on(*some)) return nullptr;

@@ -312,6 +312,56 @@ def test_backward_of_many_tokens(gb, B, T, Hq, Hkv, D, il, ops):
         assert np.all(np.abs(from_dev(out[3 + i]) - ww) <= tol)
 
 
+def test_no_gradient_is_lost_without_a_word(gb):
+    """Calls through which torch expects a derivative are refused by both bindings; the same
+    operands under no_grad, and in an autograd.Function, give what they give without."""
+    c = Case(2, 5, 4, 2, 64, 64, True, False, 47000)
+    good = gb.qkv_norm_rope(c.q, c.k, c.v, positions=c.positions, **c.how)
+    g = [torch.ones_like(x) for x in good]
+    good_bwd = gb.qkv_norm_rope_bwd(*g, c.q, c.k, positions=c.positions, **c.how)
+    wq, wk = (torch.nn.Parameter(c.how[n]) for n in ("q_weight", "k_weight"))
+    how = dict(c.how, positions=c.positions, q_weight=wq, k_weight=wk)
+    with pytest.raises(ValueError, match="records nothing"):
+        gb.qkv_norm_rope(c.q, c.k, c.v, **how)
+    with pytest.raises(ValueError, match="records nothing"):
+        gb.qkv_norm_rope_bwd(*g, c.q, c.k, **how)
+    x = c.q.clone().requires_grad_()
+    with pytest.raises(ValueError, match="records nothing"):
+        gb.qkv_norm_rope(x * 1, c.k, c.v, positions=c.positions, **c.how)
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(c.q, torch.ones_like(c.q))
+        with pytest.raises(ValueError, match="records nothing"):
+            gb.qkv_norm_rope(dual, c.k, c.v, positions=c.positions, **c.how)
+    with torch.no_grad():
+        for a, b in zip(good, gb.qkv_norm_rope(c.q, c.k, c.v, **how)):
+            assert torch.equal(a, b)
+        for a, b in zip(good_bwd, gb.qkv_norm_rope_bwd(*g, c.q, c.k, **how)):
+            assert torch.equal(a, b)
+
+    class Turn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, w, wk):
+            ctx.save_for_backward(q, k, w, wk)
+            return gb.qkv_norm_rope(q, k, None, positions=c.positions,
+                                    **dict(c.how, q_weight=w, k_weight=wk))[:2]
+
+        @staticmethod
+        def backward(ctx, dq, dk):
+            q, k, w, wk = ctx.saved_tensors
+            dq, dk, _, dw, dwk = gb.qkv_norm_rope_bwd(
+                dq.contiguous(), dk.contiguous(), None, q, k, positions=c.positions,
+                **dict(c.how, q_weight=w, k_weight=wk))
+            return dq, dk, dw.to(w.dtype), dwk.to(wk.dtype)
+
+    k = c.k.clone().requires_grad_()
+    q1, k1 = Turn.apply(x, k, wq, wk)
+    assert torch.equal(q1, good[0]) and torch.equal(k1, good[1])
+    torch.autograd.backward([q1, k1], g[:2])
+    same = gb.qkv_norm_rope_bwd(*g[:2], None, c.q, c.k, positions=c.positions, **c.how)
+    assert torch.equal(x.grad, same[0]) and torch.equal(k.grad, same[1])
+    assert torch.equal(wq.grad, same[3].bfloat16()) and torch.equal(wk.grad, same[4].bfloat16())
+
+
 @pytest.mark.parametrize("four", [False, True])
 @pytest.mark.parametrize("lens,Tn,Hq,Hkv,D,rot,norm,il,explicit", APPENDS)
 def test_append_matches_the_forward_bit_for_bit(gb, four, lens, Tn, Hq, Hkv, D, rot, norm, il,

@@ -260,6 +260,31 @@ def test_binding_refuses_bad_rope_operands(bad):
         gb.qkv_norm_rope(**(a | bad))
 
 
+ROPE = dict(q=(2, 3, 4, 64), k=(2, 3, 2, 64), v=(2, 3, 2, 64), cos_sin=(9, 64), q_weight=(64,),
+            k_weight=(64,))
+GRADS = dict(dq_out=(2, 4, 3, 64), dk_out=(2, 2, 3, 64), dv_out=(2, 2, 3, 64)) | {
+    n: ROPE[n] for n in ("q", "k", "cos_sin", "q_weight", "k_weight")}
+DIFFERENTIABLE = [(gb.qkv_norm_rope, ROPE, n) for n in ROPE] + [
+    (gb.qkv_norm_rope_bwd, GRADS, n) for n in GRADS]
+
+
+@pytest.mark.parametrize("op,shapes,name", DIFFERENTIABLE, ids=lambda x: getattr(x, "__name__", None) or str(x)[:9])
+def test_operands_of_automatic_differentiation_are_refused(op, shapes, name):
+    """Outputs have no way back to their operands, so a call that would lose a gradient
+    without a word is refused, in reverse and in forward mode."""
+    a = {n: torch.zeros(s, dtype=torch.float32 if n == "cos_sin" else torch.bfloat16)
+         for n, s in shapes.items()}
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(a[name], torch.ones_like(a[name]))
+        with pytest.raises(ValueError, match=f"{op.__name__} records nothing.*and {name} takes"):
+            op(**a | {name: dual})
+    a[name].requires_grad_()
+    with pytest.raises(ValueError, match=f"{op.__name__} records nothing.*and {name} takes"):
+        op(**a)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # as without a gradient
+        op(**a)
+
+
 @pytest.mark.parametrize("bad", [
     dict(dk_out=bf(2, 2, 4, 64)), dict(q=None), dict(q=bf(2, 3, 5, 64)), dict(dq=bf(2, 4, 3, 64)),
     dict(dq_weight=bf(64)), dict(k_weight=None, dk_weight=torch.zeros(64)),
