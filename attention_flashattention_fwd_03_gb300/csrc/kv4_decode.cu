@@ -13,10 +13,14 @@
 // either half of the low byte, is the fp16 number u 2^-24 or 16 u 2^-24 and the bf16 number
 // u 2^-133 or 16 u 2^-133.  Two masks give four codes of a word, a shift by 8 the rest.
 //   K: fp16 products take subnormal operands as they are.  The query's row is brought to
-//      fp16 by a power of two that puts its largest element in [2^14, 2^15): bf16 has 8
-//      bits, so nothing within 2^-29 of that element is rounded.  Channels whose code sits
-//      in the upper half of a byte take q / 16.  The products start from -8 sum q, which
-//      the same unit computes once a piece.  The power of two goes into the softmax scale.
+//      fp16 by a power of two that puts its largest element in [2^14, 2^15).  Channels whose
+//      code sits in the upper half of a byte take q / 16.  fp16 goes down to 2^-24 and a bf16
+//      has 8 bits, so elements down to 2^-27 of the largest (2^-31 without the / 16) are not
+//      rounded, and smaller ones by at most 2^-35 (2^-39) of it, which an fp32 sum of the
+//      row's products would not keep either.  (Rows below 2^-112 throughout lose more: they
+//      are only brought up by 2^126.)  The products start from -8 sum q, which the same unit
+//      computes once a piece.  The power of two goes into the softmax scale, and what that
+//      does not hold as an fp32 (rows from about 2^93 on) into the scores.
 //   V: p t needs the range of bf16, whose products do not take 2^-133; one fused
 //      multiply-add on the pair makes it n / 64, exactly.
 // Scores, softmax statistics and outputs are fp32; p t is rounded to bf16 for its product
@@ -83,7 +87,8 @@ struct Shape {
   static constexpr int kStages = (D == 64 ? 2 : 1) * (NQT == 1 ? 2 : 3);
   static constexpr int kOffBar = kWarps * kStages * kStageBytes;
   static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
-  static constexpr int kSmem = kOffAbort + kWarps * 4 + 128;  // slack for 128-byte alignment
+  static constexpr int kOffBoost = kOffAbort + kWarps * 4;  // [kWarps][8 NQT] floats
+  static constexpr int kSmem = kOffBoost + kWarps * 8 * NQT * 4 + 128;  // slack for 128-byte alignment
 };
 
 // D = A * B + C (C may be D), m16n8k16, fp16 inputs, fp32 accumulators.
@@ -131,6 +136,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+// 2^x as an fp32, -126 <= x <= 127.
+__device__ __forceinline__ float pow2(int x) { return __int_as_float((127 + x) << 23); }
 
 // Token of a 16-token block that row `row` of a score tile holds.  Neighbouring rows are
 // swapped in every other pair, so that both the K loads (rows 2 a, 2 a + 1 together) and
@@ -209,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   const uint32_t ring_addr = sbase + warp * C::kStages * C::kStageBytes;
   const uint32_t bars = sbase + C::kOffBar + warp * C::kStages * 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kOffAbort) + warp;
+  float* boost = reinterpret_cast<float*>(smem + C::kOffBoost) + warp * 8 * NQT;
 
   // the merge kernel (or what else follows as a programmatic dependent) may be scheduled
   // now; it waits for this grid's results
@@ -338,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
   uint32_t qb[D / 16][NQT][2];       // Q^T fragments (fp16) in the order of the K codes
   float q8[G][NQT][2];               // -8 sum of q over group w, queries 2 t4 (+ 1)
   float sl2[NQT][2], sl[NQT][2];     // softmax scale (times log2 e) over the query's 2^x
+  bool boosted = false;              // some query's scores take a factor (boost) first
   float m_q[NQT][2], l_q[NQT][2];
   float acc[D / 16][NQT][4];         // O^T / 64: channels 32 w + 4 g + 2 x (+ 1) of tile 2 w + x
   Step c = at;
@@ -358,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
     const uint16_t* q = static_cast<const uint16_t*>(p.q) + q0 * D;
     // A fragment of -8 in both forms of a code
     const uint32_t minus8[4] = {0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u};
+    bool big_scale = false;
 #pragma unroll
     for (int nt = 0; nt < NQT; ++nt) {
       const int row = 8 * nt + g;
@@ -373,10 +384,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
       big = max(big & 0xffffu, big >> 16);
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      // q = q' 2^(e - 14): e the exponent of the largest element (kept where all powers of
-      // two below are normal numbers)
-      const int e = min(max(static_cast<int>(big >> 7) - 127, -100), 100);
-      const float f0 = __int_as_float((127 + 14 - e) << 23), f1 = f0 * 0.0625f;
+      // q = q' 2^(e - 14): e the exponent of the largest element (128: an infinity or NaN),
+      // kept where the factor is a normal number
+      const int e = max(static_cast<int>(big >> 7) - 127, -112);
+      const float f0 = pow2(14 - e), f1 = f0 * 0.0625f;
 #pragma unroll
       for (int w = 0; w < G; ++w) {
         // masks of a word give channels 0, 4 (low) and 1, 5 (high); shifted by 8: 2, 6 and 3, 7
@@ -394,9 +405,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
       for (int x2 = 0; x2 < 2; ++x2) {
         // lane 4 k holds the exponent of query k: this lane's columns are 2 t4 and 2 t4 + 1
         const int eq = __shfl_sync(0xffffffffu, e, 4 * (2 * t4 + x2));
-        const float f = __int_as_float((127 + 24 - 14 + eq) << 23);
-        sl[nt][x2] = p.scale * f;
-        sl2[nt][x2] = p.scale_log2 * f;
+        // scale 2^(eq + 24 - 14), in two steps as the power alone may not be a number, and
+        // what it has above 2^100 as a factor of the scores
+        const int sx = static_cast<int>(__float_as_uint(p.scale_log2) >> 23) - 127;
+        const int over = min(max(eq + 10 + sx - 100, 0), 126), x = eq + 10 - over;
+        const float fa = pow2(x >> 1), fb = pow2(x - (x >> 1));
+        sl[nt][x2] = p.scale * fa * fb;
+        sl2[nt][x2] = fmaxf(p.scale_log2 * fa * fb, 1.17549435e-38f);  // (0 times the first -inf: NaN)
+        big_scale |= over > 0;
+        if (g == 0) boost[8 * nt + 2 * t4 + x2] = pow2(over);
         m_q[nt][x2] = -INFINITY;
         l_q[nt][x2] = 0.f;
       }
@@ -404,6 +421,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
       for (int j = 0; j < D / 16; ++j)
         acc[j][nt][0] = acc[j][nt][1] = acc[j][nt][2] = acc[j][nt][3] = 0.f;
     }
+    boosted = __any_sync(0xffffffffu, big_scale);
+    __syncwarp();
   };
   begin_piece();  // (DIRECT: also by a warp without a step, whose sums stay empty)
 
@@ -454,6 +473,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NQT>::kCtasPerSm)
             sc[j][nt][1] = fmaf(f0, d[1], sc[j][nt][1]);
             sc[j][nt][2] = fmaf(f1, d[2], sc[j][nt][2]);
             sc[j][nt][3] = fmaf(f1, d[3], sc[j][nt][3]);
+          }
+        }
+      }
+    }
+    if (boosted) {
+#pragma unroll
+      for (int nt = 0; nt < NQT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float f = boost[8 * nt + 2 * t4 + e];
+#pragma unroll
+          for (int j = 0; j < kStepBlocks; ++j) {
+            sc[j][nt][e] *= f;
+            sc[j][nt][2 + e] *= f;
           }
         }
       }

@@ -110,6 +110,55 @@ def test_small_and_large_cache_values(gb, gain):
     check(c, o, lse)
 
 
+def shifted(bits, k):
+    """bf16 bits times 2^k; zeros and NaN stay."""
+    e = (bits >> 7) & 0xFF
+    move = (e > 0) & (e < 0xFF)
+    assert not move.any() or 0 < int(e[move].min()) + k and int(e[move].max()) + k < 0xFF
+    return np.where(move, bits + np.uint16(k * 128 % 65536), bits).astype(np.uint16)
+
+
+def shift_keys(pool, D, k):
+    """A 4-bit pool whose keys are times 2^k (their scales are)."""
+    out = pool.copy()
+    scales = np.ascontiguousarray(out[..., 8 * D:9 * D]).view(np.uint16)
+    out[..., 8 * D:9 * D] = np.ascontiguousarray(shifted(scales, k)).view(np.uint8)
+    return out
+
+
+@pytest.mark.parametrize("k", [-104, 60, 95, 101, 107, 113, 118])
+@pytest.mark.parametrize("Hq,Hkv,D", [(6, 2, 128), (12, 1, 64), (16, 1, 128)])
+@pytest.mark.parametrize("bound", [700, 1100])
+def test_queries_of_any_magnitude(gb, Hq, Hkv, D, k, bound):
+    """Queries times 2^k on keys times 2^-k: the same scores, however large the queries.
+    (What fp32 sums below 2^-126 lose, 2^-150 of a key of 2^-118 against a query of 2^118,
+    is 2^-18 of a score, within the tolerances' 2^-16.)"""
+    c = Cache([700, 1, 90], Hq, Hkv, D, 51500 + Hq, max_len=bound)
+    bits = c.p.q.copy()
+    bits[((bits >> 7) & 0xFF) < 127 - 12] = 0  # (so that every element of the row can be shifted)
+    bits[1, 0] = 0                             # a row of zeros
+    c.p.q = bits
+    q, pool = to_dev(shifted(bits, k)), torch.from_numpy(shift_keys(c.pool_host, D, -k)).cuda()
+    o, lse = gb.paged_kv4_attn_decode(q, pool, c.table, c.lens, bound, scale=c.scale)
+    torch.cuda.synchronize()
+    assert gb.attn_device_status() == (gb.ATTN_OK, 0)
+    check(c, o, lse)
+    if k in (-104, 60, 95):  # (products and sums of 2^k times the fp32 values, none subnormal)
+        o1, lse1 = gb.paged_kv4_attn_decode(to_dev(bits), c.pool, c.table, c.lens, bound, scale=c.scale)
+        assert torch.equal(o, o1) and torch.equal(lse, lse1)
+
+
+@pytest.mark.parametrize("scale", [1e-44, 1e-30, 1e-12])
+@pytest.mark.parametrize("bound", [300, 1100])
+def test_tiny_softmax_scales(gb, scale, bound):
+    """Scores of nothing: the mean of the values, also of rows of zeros."""
+    c = Cache([300, 64, 1], 4, 2, 128, 51700, max_len=bound)
+    c.p.q[0] = 0
+    c.q, c.scale = to_dev(c.p.q), scale
+    o, lse = gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, bound, scale=scale)
+    check(c, o, lse)
+
+
 def test_the_decode_workload(gb):
     cfg = synth.CONFIGS["paged_decode"]
     lens = synth.uniform_ints(cfg.seed + 3, cfg.num_seqs, cfg.len_lo, cfg.len_hi)

@@ -12,6 +12,7 @@ import oracle
 import rope_ref as ref
 import synth
 from gpu_util import check_close, from_dev, to_dev, to_dev_i32
+from test_gpu_kv4_decode import shift_keys, shifted
 
 pytestmark = pytest.mark.gpu
 
@@ -132,6 +133,20 @@ def test_rows_match_the_oracle(gb, Hq, Hkv, D, Tq, lens, causal):
     torch.cuda.synchronize()
     assert gb.attn_device_status() == (gb.ATTN_OK, 0)
     check_rows(c, o, lse, causal)
+
+
+@pytest.mark.parametrize("k", [60, 101, 118])
+@pytest.mark.parametrize("Hq,Hkv,D,Tq", [(8, 2, 128, 4), (4, 2, 64, 2), (32, 1, 128, 1)])
+def test_row_queries_of_any_magnitude(gb, Hq, Hkv, D, Tq, k):
+    """Queries times 2^k on keys times 2^-k, as in test_gpu_kv4_decode.py."""
+    c = Item(Hq, Hkv, D, Tq, [Tq, 65, 700], 61300 + Tq, max_len=1000)
+    assert uses_rows(gb, c)
+    c.q_bits[((c.q_bits >> 7) & 0xFF) < 127 - 12] = 0
+    c.q = to_dev(shifted(c.q_bits, k))
+    o, lse = c.run(gb, True, pool=torch.from_numpy(shift_keys(c.pool_host, D, -k)).cuda())
+    torch.cuda.synchronize()
+    assert gb.attn_device_status() == (gb.ATTN_OK, 0)
+    check_rows(c, o, lse, True)
 
 
 @pytest.mark.parametrize("Hq,Hkv,D", [(17, 1, 128), (24, 1, 64), (32, 1, 128), (34, 2, 64), (16, 1, 128)])
