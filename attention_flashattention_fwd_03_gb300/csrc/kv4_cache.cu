@@ -23,7 +23,7 @@ template <int D>
 __global__ void __launch_bounds__(2 * D) paged_kv4_gather_kernel(const Gather4Params p) {
   using F = Kv4<D>;
   constexpr int LANES = D / 8;
-  const unsigned n_blocks = (p.max_seq_len + kPagedBlock - 1) / kPagedBlock;
+  const unsigned n_blocks = (p.max_seq_len + (kPagedBlock - 1u)) / kPagedBlock;
   const unsigned n_sets = (p.Hkv + kHeads - 1) / kHeads;
   const unsigned set = blockIdx.x % n_sets, rb = blockIdx.x / n_sets;
   const int lb = rb % n_blocks, r = rb / n_blocks;
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(2 * D) paged_kv4_gather_kernel(const Gather4Pa
 }  // namespace
 
 cudaError_t launch_kv4_gather(const Gather4Params& p, int D, cudaStream_t stream) {
-  const long long n_blocks = (p.max_seq_len + kPagedBlock - 1) / kPagedBlock;
+  const long long n_blocks = (p.max_seq_len + (kPagedBlock - 1ll)) / kPagedBlock;
   const long long grid = static_cast<long long>(p.S) * ((p.Hkv + kHeads - 1) / kHeads) * n_blocks;
   if (grid <= 0) return cudaSuccess;
   cudaLaunchAttribute attr[1];

@@ -923,7 +923,7 @@ cudaError_t launch(const uint8_t* pool, const Kv4DecodeParams& p, int num_sms, c
 
 long long kv4_max_steps(int S, int segs, int max_seq_len) {
   return static_cast<long long>(S) * segs *
-         ((max_seq_len + kBS * kStepBlocks - 1ll) / (kBS * kStepBlocks));
+         ((max_seq_len + (kBS * kStepBlocks - 1ll)) / (kBS * kStepBlocks));
 }
 
 Kv4Rows kv4_rows(int Hq, int Hkv, int Tq) {

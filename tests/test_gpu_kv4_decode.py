@@ -159,6 +159,14 @@ def test_tiny_softmax_scales(gb, scale, bound):
     check(c, o, lse)
 
 
+def test_the_largest_length_bound(gb):
+    """Any bound an int holds."""
+    c = Cache([700, 1, 90], 6, 2, 128, 51800, max_len=1100)
+    o, lse = gb.paged_kv4_attn_decode(c.q, c.pool, c.table, c.lens, 2 ** 31 - 1, scale=c.scale)
+    check(c, o, lse)
+    assert gb.attn_device_status() == (gb.ATTN_OK, 0)
+
+
 def test_the_decode_workload(gb):
     cfg = synth.CONFIGS["paged_decode"]
     lens = synth.uniform_ints(cfg.seed + 3, cfg.num_seqs, cfg.len_lo, cfg.len_hi)

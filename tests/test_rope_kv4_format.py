@@ -236,6 +236,15 @@ def test_single_tokens_of_wide_groups_have_a_workspace(group, Hkv, B, D):
     assert size(B, 16 * Hkv, Hkv, 1, D, 1024) == 0
 
 
+def test_workspace_sizes_at_the_largest_length_bound():
+    """At 2^31 - 1 tokens a batch has its most ranges (2048), and a piece more a segment."""
+    for ml in (2 ** 31 - 1, 2 ** 31 - 64, 1 << 20):
+        pieces = 2048 + 3 * 2
+        n = pieces * 2 * (128 + 1) * 4
+        need = gb.paged_kv4_attn_decode_workspace_size(3, 4, 2, 128, ml)
+        assert n <= need <= n + 2 * 4 * 6 + 4 * 256
+
+
 # --------------------------------------------------------------------------- #
 # argument checks of the binding
 # --------------------------------------------------------------------------- #
