@@ -354,6 +354,13 @@ GBATTN_API int paged_kv4_gather(const void* kv_pool, const int32_t* block_table,
 
 namespace {
 
+// Whether the row kernels' 32-bit counts of steps and rows hold a call of these sizes.
+bool rows_fit(int S, int Hq, int Hkv, int Tq, int max_seq_len) {
+  if (static_cast<unsigned __int128>(S) * Hq * Tq >= kMaxDim / 2) return false;
+  const int64_t steps = kv4_max_steps(S, Hkv * kv4_rows(Hq, Hkv, Tq).chunks, max_seq_len);
+  return static_cast<uint64_t>(steps) < kMaxDim;
+}
+
 // Attention of Tq query tokens a request by the row kernels of kv4_decode.cu.
 int attend_rows(const void* q, const void* kv_pool, const int32_t* block_table,
                 const int32_t* seq_lens, int S, int Hq, int Hkv, int Tq, int D, int max_blocks,
@@ -363,9 +370,6 @@ int attend_rows(const void* q, const void* kv_pool, const int32_t* block_table,
   if (wl.bytes > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < wl.bytes))
     return ATTN_ERR_INVALID_ARG;
   const Kv4Rows rows = kv4_rows(Hq, Hkv, Tq);
-  if (static_cast<uint64_t>(kv4_max_steps(S, Hkv * rows.chunks, max_seq_len)) >= kMaxDim ||
-      static_cast<uint64_t>(S) * Hkv * rows.rows >= kMaxDim / 2)
-    return ATTN_ERR_UNSUPPORTED;
   DeviceState* ds = nullptr;
   const int st = device_state(&ds);
   if (st != ATTN_OK) return st;
@@ -418,8 +422,10 @@ int attend_rows(const void* q, const void* kv_pool, const int32_t* block_table,
 // fewer than the 152 SMs.  On short caches (3 x 8/2 heads, 500 keys, D 64: Tq 4: 7.2 / 11.3,
 // 37: 9.0 / 11.3; 300 keys: 7.2 / 9.9, 9.0 / 10.1) the rows' few microseconds do not pay for
 // their second launch and workspace on the host, unless the tiles need several rounds.
-bool by_rows(int B, int Hq, int Tq, int max_kv_len) {
+// Sizes that the row kernels cannot count are the tile kernel's.
+bool by_rows(int B, int Hq, int Hkv, int Tq, int max_kv_len) {
   const int64_t units = static_cast<int64_t>(B) * Hq;
+  if (!rows_fit(B, Hq, Hkv, Tq, max_kv_len)) return false;
   if (max_kv_len <= 512 && units <= 152) return false;
   return Tq <= 256 && Tq * (units < 152 ? units : 152) <= 4500;
 }
@@ -436,7 +442,9 @@ GBATTN_API size_t paged_kv4_attn_prefill_workspace_size(int B, int Hq, int Hkv, 
                                                         int max_kv_len) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Tq <= 0 || D <= 0 || max_kv_len < 0)
     return 0;
-  return by_rows(B, Hq, Tq, max_kv_len) ? kv4_decode_workspace(B, Hq, Hkv, Tq, D, max_kv_len).bytes : 0;
+  return by_rows(B, Hq, Hkv, Tq, max_kv_len)
+             ? kv4_decode_workspace(B, Hq, Hkv, Tq, D, max_kv_len).bytes
+             : 0;
 }
 
 GBATTN_API int paged_kv4_attn_decode(const void* q, const void* kv_pool,
@@ -456,8 +464,8 @@ GBATTN_API int paged_kv4_attn_decode(const void* q, const void* kv_pool,
       !aligned(seq_lens, 4) || !aligned(lse, 4))
     return ATTN_ERR_INVALID_ARG;
   if (static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim ||
-      static_cast<uint64_t>(num_seqs) * Hq >= kMaxDim / 2 ||
-      static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim)
+      static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim ||
+      !rows_fit(num_seqs, Hq, Hkv, 1, max_seq_len))
     return ATTN_ERR_UNSUPPORTED;
   return attend_rows(q, kv_pool, block_table, seq_lens, num_seqs, Hq, Hkv, 1, D,
                      max_blocks_per_seq, num_pool_blocks, max_seq_len, 0, scale, o, lse, workspace,
@@ -487,7 +495,7 @@ GBATTN_API int paged_kv4_attn_prefill(const void* q, const void* kv_pool,
       static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim ||
       static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim)
     return ATTN_ERR_UNSUPPORTED;
-  if (by_rows(B, Hq, Tq, max_kv_len))
+  if (by_rows(B, Hq, Hkv, Tq, max_kv_len))
     return attend_rows(q, kv_pool, block_table, kv_lens, B, Hq, Hkv, Tq, D, max_blocks_per_seq,
                        num_pool_blocks, max_kv_len, causal, scale, o, lse, workspace,
                        workspace_bytes, stream);

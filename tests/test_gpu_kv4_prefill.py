@@ -192,6 +192,19 @@ def test_more_classes_than_the_sorted_list_holds(gb):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_a_length_bound_of_any_size(gb):
+    """Short chunks under the largest bound an int holds: more steps than the row kernels
+    count, so tiles."""
+    c = Item(4, 2, 128, 4, [4, 70, 333, 0] * 8, 61700)
+    top = 2 ** 31 - 1
+    o, lse = gb.paged_kv4_attn_prefill(c.q, c.pool, c.table, c.kv_lens, top, scale=c.scale)
+    o2, lse2 = gb.paged_attn_prefill(c.q, to_dev(c.k), to_dev(c.v), c.table, c.kv_lens, top,
+                                     scale=c.scale)
+    torch.cuda.synchronize()
+    assert gb.attn_device_status() == (gb.ATTN_OK, 0)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_outputs_streams_and_graphs(gb):
     c = Item(8, 2, 128, 130, [130, 999, 2048], 62000)
     o, lse = c.run(gb, True)

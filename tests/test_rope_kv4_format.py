@@ -236,6 +236,14 @@ def test_single_tokens_of_wide_groups_have_a_workspace(group, Hkv, B, D):
     assert size(B, 16 * Hkv, Hkv, 1, D, 1024) == 0
 
 
+def test_chunks_past_the_row_kernels_counts_are_the_tile_kernels():
+    """A length bound that makes 2^31 steps of 64 tokens or more: no rows, so no workspace."""
+    size, top = gb.paged_kv4_attn_prefill_workspace_size, 2 ** 31 - 1
+    assert size(31, 4, 2, 4, 128, top) > 0
+    assert size(32, 4, 2, 4, 128, top) == 0
+    assert size(1 << 20, 4, 2, 1, 128, 1 << 20) == 0
+
+
 def test_workspace_sizes_at_the_largest_length_bound():
     """At 2^31 - 1 tokens a batch has its most ranges (2048), and a piece more a segment."""
     for ml in (2 ** 31 - 1, 2 ** 31 - 64, 1 << 20):
