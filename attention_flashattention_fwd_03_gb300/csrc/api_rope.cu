@@ -85,9 +85,13 @@ RopeParams rope_params(const void* q_weight, const void* k_weight, const float* 
 // An input operand: present with good strides and a 16-byte aligned base.
 bool good_input(const void* p, const int64_t* s) { return p && aligned(p, 16) && good_strides(s); }
 
+// Sizes past the kernels' counts: 2^31 tokens or heads, or 2^32 rows (half a terabyte of
+// them at D = 64), with which a launch stays below 2^31 CTAs: a CTA has at least four rows of
+// its token.
 bool too_many_rows(int B, int T, int Hq, int Hkv) {
   const unsigned __int128 n = static_cast<unsigned __int128>(B) * T;
-  return n >= kMaxDim || n * (static_cast<uint64_t>(Hq) + 2ull * Hkv) >= (1ull << 34);
+  const uint64_t rows = static_cast<uint64_t>(Hq) + 2ull * Hkv;
+  return n >= kMaxDim || rows >= kMaxDim || n * rows >= (1ull << 32);
 }
 
 bool overlap(const void* a, const void* b, size_t bytes) {

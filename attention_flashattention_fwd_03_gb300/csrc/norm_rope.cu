@@ -312,8 +312,7 @@ cudaError_t launch_norm_rope(NormRopeParams p, int D, RowSink sink, int num_sms,
   p.rows_per_warp = tokens >= 32ll * num_sms ? rows : (tokens >= 4ll * num_sms ? 4 : 2) * pass;
   p.chunks = (rows + p.rows_per_warp - 1) / p.rows_per_warp;
   p.one = 1.f;
-  const long long grid = (tokens * p.chunks + kWarps - 1) / kWarps;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  const long long grid = (tokens * p.chunks + kWarps - 1) / kWarps;  // (its bound: too_many_rows)
   const dim3 g(static_cast<unsigned>(grid));
   auto run = [&](auto d, auto f) {
     constexpr int DD = decltype(d)::value;

@@ -161,6 +161,22 @@ def call_append(four, kw):
              None)
 
 
+@pytest.mark.parametrize("sizes", [
+    dict(B=1, T=1, Hq=1 << 30, Hkv=1 << 30),        # heads past an int
+    dict(B=1, T=1, Hq=(1 << 31) - 1, Hkv=1),
+    dict(B=1, T=300, Hq=1 << 24, Hkv=1),            # 2^32 rows and more
+    dict(B=50, T=50, Hq=64, Hkv=1 << 20),
+])
+def test_more_rows_than_a_launch_counts_are_refused(sizes):
+    """As a size that is not supported, not as a CUDA error and not as a call that does nothing."""
+    strides = dict(qs=(0, 0, 64), ks=(0, 0, 64), vs=(0, 0, 64))
+    assert call_fwd(sizes | strides) == UNS
+    assert call_append(False, sizes | strides) == UNS and call_append(True, sizes | strides) == UNS
+    rows = max(sizes["Hq"], sizes["Hkv"]) * 64
+    places = (rows * sizes["T"], rows, 64)
+    assert call_bwd(sizes | strides | dict(ds=places)) == UNS
+
+
 @pytest.mark.parametrize("four", [False, True])
 @pytest.mark.parametrize("kw,code", ROPE_BAD + [
     (dict(bs=8), UNS), (dict(mb=0), INV), (dict(nb=0), INV), (dict(Hkv=0), INV),
