@@ -484,17 +484,18 @@ def _check_no_gradients(op, **operands):
 def _load_torch():
     global _torch, _Tensor, _bf16, _f32, _i32, _u8
     import torch
-    _torch, _Tensor = torch, torch.Tensor
+    _Tensor = torch.Tensor
     _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-    _load_quick()
+    _load_quick(torch)
+    _torch = torch  # last: another thread that finds it set finds the rest too
 
 
-def _load_quick():
+def _load_quick(torch):
     """Binds _quick, the module _binding, to the library and torch's current device
     and stream, if it was built."""
     global _quick
-    h, _quick = lib(), None
-    if not hasattr(_torch._C, "_cuda_getDevice"):  # a torch without CUDA
+    h = lib()
+    if not hasattr(torch._C, "_cuda_getDevice"):  # a torch without CUDA
         return
     try:
         m = importlib.import_module("._binding", __name__)
@@ -502,7 +503,7 @@ def _load_quick():
                  "paged_qkv_append", "paged_kv4_append", "paged_kv4_gather",
                  "paged_kv4_attn_decode", "paged_kv4_attn_decode_workspace_size",
                  "paged_kv4_attn_prefill", "paged_kv4_attn_prefill_workspace_size")
-        m.setup(_torch.__version__, _torch._C._cuda_getDevice, _torch._C._cuda_getCurrentRawStream,
+        m.setup(torch.__version__, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
                 *(ctypes.cast(getattr(h, n), ctypes.c_void_p).value for n in names))
     except ImportError:  # not built, or against another torch
         return

@@ -364,3 +364,42 @@ def test_binding_refuses_bad_kv4_attention(bad):
     a = {n: t.unsqueeze(2) if n in ("q", "out", "lse") else t for n, t in a.items()}
     with pytest.raises(ValueError):
         gb.paged_kv4_attn_prefill(**a)
+
+
+def test_first_calls_of_two_threads(monkeypatch):
+    """A call that another thread makes at any point of the first one's loading of torch finds
+    all of what it uses (each line of the loader is such a point)."""
+    import sys
+    import threading
+
+    a = dict(q=bf(2, 3, 4, 64), k=bf(2, 3, 2, 64), v=bf(2, 3, 2, 64), cos_sin=torch.zeros(9, 64))
+    gb.lib()
+
+    def refusal():  # with all in place: the tensors are not on a GPU
+        try:
+            gb.qkv_norm_rope(**a)
+        except Exception as e:  # noqa: BLE001 -- whatever a half-loaded state leads to
+            seen.append(repr(e))
+
+    def trace(frame, event, arg):
+        if frame.f_code is gb._load_torch.__code__ and event != "return":
+            if events[0] == point:
+                t = threading.Thread(target=refusal)
+                t.start()
+                t.join(60)
+            events[0] += 1
+            return trace
+
+    point, last = 0, 1
+    while point < last:
+        for n in ("_torch", "_Tensor", "_bf16", "_f32", "_i32", "_u8", "_quick"):
+            monkeypatch.setattr(gb, n, None)
+        seen, events, before = [], [0], sys.gettrace()
+        sys.settrace(trace)
+        try:
+            refusal()
+        finally:
+            sys.settrace(before)
+        assert len(seen) == 2 and all("ValueError" in s and "CUDA" in s for s in seen), (point, seen)
+        point, last = point + 1, events[0]
+    assert last > 4
