@@ -114,16 +114,21 @@ int append(bool four, const void* q, const void* k, const void* v, const int64_t
   int st = check_rope(q_weight, k_weight, cos_sin, positions, D, rot_dim, max_pos, interleaved,
                       eps);
   if (st != ATTN_OK) return st;
-  if (num_seqs == 0 || Tn == 0) return ATTN_OK;
+  if (num_seqs == 0 || (Tn == 0 && !new_seq_lens)) return ATTN_OK;
+  // the lengths are read by every CTA while one of them writes the new ones
+  if (new_seq_lens && (!seq_lens || !aligned(seq_lens, 4) || !aligned(new_seq_lens, 4) ||
+                       overlap(seq_lens, new_seq_lens, sizeof(int32_t) * num_seqs)))
+    return ATTN_ERR_INVALID_ARG;
+  if (Tn == 0)  // nothing to append: the lengths stay
+    return cudaMemcpyAsync(new_seq_lens, seq_lens, sizeof(int32_t) * num_seqs,
+                           cudaMemcpyDeviceToDevice, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? ATTN_OK
+               : ATTN_ERR_CUDA;
   if ((q != nullptr) != (q_out != nullptr) || (q && Hq == 0)) return ATTN_ERR_INVALID_ARG;
   if (q && (!good_input(q, q_strides) || !aligned(q_out, 16))) return ATTN_ERR_INVALID_ARG;
   if (!good_input(k, k_strides) || !good_input(v, v_strides)) return ATTN_ERR_INVALID_ARG;
   if (!k_pool || !aligned(k_pool, 16) || (!four && (!v_pool || !aligned(v_pool, 16))) ||
-      !block_table || !aligned(block_table, 4) || !seq_lens || !aligned(seq_lens, 4) ||
-      !aligned(new_seq_lens, 4))
-    return ATTN_ERR_INVALID_ARG;
-  // the lengths are read by every CTA while one of them writes the new ones
-  if (new_seq_lens && overlap(seq_lens, new_seq_lens, sizeof(int32_t) * num_seqs))
+      !block_table || !aligned(block_table, 4) || !seq_lens || !aligned(seq_lens, 4))
     return ATTN_ERR_INVALID_ARG;
   if (too_many_rows(num_seqs, Tn, q ? Hq : 0, Hkv) ||
       static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim ||

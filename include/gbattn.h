@@ -316,7 +316,8 @@ int qkv_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *dv_out
  *   q_out         [num_seqs, Hq, Tn, D] bf16 (written); for Tn = 1 that is
  *                 paged_attn_decode's q
  *   k_pool/v_pool, block_table, seq_lens, new_seq_lens, block_size as in
- *                 paged_kv_append; the rest as in qkv_norm_rope
+ *                 paged_kv_append (Tn = 0 copies the lengths to new_seq_lens and does
+ *                 nothing else); the rest as in qkv_norm_rope
  *
  * Device-side checks: a length with no room for Tn more tokens skips the request
  * (its q_out rows become NaN, new_seq_lens keeps the length) and sets flag bit 2; a

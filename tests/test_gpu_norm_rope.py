@@ -432,6 +432,29 @@ def test_append_bad_requests_are_flagged_and_skipped(gb, four):
     assert nan == [False, False, True, True, True]
 
 
+@pytest.mark.parametrize("four", [False, True])
+def test_append_of_no_tokens_keeps_the_lengths(gb, four):
+    c = Case(3, 1, 4, 2, 64, 64, True, False, 40900)
+    none = [x[:, :0] for x in (c.q, c.k, c.v)]
+    bt, NB = table_for([4, 9, 20], 1, 42)
+    pools = [torch.full((NB, 2, 18 * 64), 3, dtype=torch.uint8, device="cuda")] if four else [
+        torch.full((NB, 2, 16, 64), 3.0, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    lens, new = to_dev_i32(np.array([4, 9, 20])), torch.full((3,), -9, dtype=torch.int32, device="cuda")
+    op = gb.paged_kv4_append if four else gb.paged_qkv_append
+    table = to_dev_i32(bt)
+    q, after = op(*none, *pools, table, lens, new_seq_lens=new, **c.how)
+    torch.cuda.synchronize()
+    assert q.shape == (3, 4, 0, 64) and after is new and torch.equal(new, lens)
+    assert all(torch.all(p == 3) for p in pools)
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=s):
+        op(*none, *pools, table, lens, new_seq_lens=new, **c.how)
+    lens += 7
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(new, lens)
+
+
 def test_append_without_queries(gb):
     c = Case(2, 3, 1, 2, 128, 128, True, False, 41000)
     bt, NB = table_for([4, 9], 3, 42)

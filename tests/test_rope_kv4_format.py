@@ -183,6 +183,7 @@ def test_more_rows_than_a_launch_counts_are_refused(sizes):
     (dict(pool=None), INV), (dict(pool=A16 + 8), INV), (dict(bt=None), INV), (dict(sl=None), INV),
     (dict(sl=A16 + 2), INV), (dict(nsl=A16 + 4), INV), (dict(k=None), INV), (dict(v=None), INV),
     (dict(q=None), INV), (dict(qo=None), INV), (dict(nb=1 << 28), UNS), (dict(mb=1 << 28), UNS),
+    (dict(T=0, nsl=A16 + 4), INV), (dict(T=0, nsl=A16, sl=None), INV), (dict(B=0, nsl=A16), OK),
 ])
 def test_append_refusals(four, kw, code):
     assert call_append(four, kw) == code
