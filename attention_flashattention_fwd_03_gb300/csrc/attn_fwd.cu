@@ -66,16 +66,21 @@ namespace gbattn {
 
 namespace {
 
-// Where keys and values come from: contiguous tensors, the bf16 pools or the 4-bit pool.
-enum class Src { kContiguous, kPaged, kPaged4 };
+// Where keys and values come from: contiguous tensors, the bf16 pools or the 4-bit pool
+// (kSorted..: with the units in order of length, see unit_at).
+enum class Src { kContiguous, kPaged, kPaged4, kSortedPaged, kSortedPaged4 };
+constexpr bool is_paged(Src s) { return s != Src::kContiguous; }
+constexpr bool is_kv4(Src s) { return s == Src::kPaged4 || s == Src::kSortedPaged4; }
+constexpr bool is_sorted(Src s) { return s == Src::kSortedPaged || s == Src::kSortedPaged4; }
 
 constexpr int BM = 128;          // query rows per tile (= TMEM lanes)
 constexpr int BN = 128;          // keys per K/V tile
 constexpr int kBS = 16;          // tokens per paged KV block
 // Warpgroup 0: producer, MMA, 2 idle warps; 1, 2: softmax; 3 (4-bit cache): dequantisers.
 template <Src SRC>
-constexpr int kThreads = SRC == Src::kPaged4 ? 512 : 384;
+constexpr int kThreads = is_kv4(SRC) ? 512 : 384;
 constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by > 2^8
+constexpr int kSortLen = 512;    // units are sorted where an item may have more keys than this
 constexpr int kMaxSorted = 384;  // (item, query pair) classes whose units are sorted by length
 // Registers per thread: the block launches with 168 (384 threads, one block per
 // SM); warpgroup 0 gives some up so the softmax warpgroups, which hold a whole
@@ -94,8 +99,8 @@ struct Cfg {
   static constexpr int BOX_BYTES = 128 * 128;         // 128 rows x 128 bytes
   static constexpr int TILE_BYTES = BM * D * 2;       // one Q, K or V tile
   // K/V ring slots; the raw tiles of the 4-bit cache take the place of one
-  static constexpr int NSLOT = (D == 64) ? 8 : (SRC == Src::kPaged4 ? 4 : 5);
-  static constexpr int NRAW = SRC == Src::kPaged4 ? 3 : 0;  // raw K or V tiles in flight
+  static constexpr int NSLOT = (D == 64) ? 8 : (is_kv4(SRC) ? 4 : 5);
+  static constexpr int NRAW = is_kv4(SRC) ? 3 : 0;  // raw K or V tiles in flight
   static constexpr int RAW_BLOCK = 9 * D;             // codes and scales of K or V of a block
   static constexpr int RAW_BYTES = (BN / kBS) * RAW_BLOCK;
   static constexpr int OFF_Q = 0;                     // the unit's two Q tiles
@@ -104,10 +109,10 @@ struct Cfg {
   static constexpr int OFF_BAR = OFF_RAW + NRAW * RAW_BYTES;
   static constexpr int NBAR = 2 + 2 * NSLOT + 6 + 1 + 2 * NRAW;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  // paged sources: tile counts and sorted order of the (item, query pair) classes
+  // sorted units: tile counts and order of the (item, query pair) classes
   static constexpr int OFF_COST = OFF_MISC + 16;
-  static constexpr int OFF_ORDER = OFF_COST + (SRC == Src::kContiguous ? 0 : 2 * kMaxSorted);
-  static constexpr int OFF_END = OFF_ORDER + (SRC == Src::kContiguous ? 0 : 2 * kMaxSorted);
+  static constexpr int OFF_ORDER = OFF_COST + (is_sorted(SRC) ? 2 * kMaxSorted : 0);
+  static constexpr int OFF_END = OFF_ORDER + (is_sorted(SRC) ? 2 * kMaxSorted : 0);
   static constexpr int SMEM_BYTES = OFF_END + 1024;  // + slack for 1024-byte alignment
   static constexpr uint32_t TMEM_COLS = 512;
   // TMEM columns: S_0 [0,128), S_1 [128,256), O_0 and O_1 from 256 (D each).
@@ -116,10 +121,10 @@ struct Cfg {
   __device__ static constexpr uint32_t p_col(int i) { return 128u * i + 64u; }
   __device__ static constexpr uint32_t o_col(int i) { return 256u + static_cast<uint32_t>(D) * i; }
 };
-static_assert(kMaxSorted <= kThreads<Src::kPaged>, "a thread a class");
-static_assert(Cfg<128, Src::kPaged>::SMEM_BYTES <= 232448, "shared memory budget");
-static_assert(Cfg<128, Src::kPaged4>::SMEM_BYTES <= 232448, "shared memory budget");
-static_assert(Cfg<64, Src::kPaged4>::SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(kMaxSorted <= kThreads<Src::kSortedPaged>, "a thread a class");
+static_assert(Cfg<128, Src::kSortedPaged>::SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(Cfg<128, Src::kSortedPaged4>::SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(Cfg<64, Src::kSortedPaged4>::SMEM_BYTES <= 232448, "shared memory budget");
 
 template <int D, Src SRC>
 struct Bars {
@@ -171,19 +176,29 @@ __device__ __forceinline__ int tiles_of(int qp, int i, int L, const FwdParams& p
   return (kv_end_of(min(r0 + 127, p.Tq - 1), L, p) + BN - 1) / BN;
 }
 
-// Unit u.  Contiguous K and V: query-pair index decreasing (the longest causal rows
-// first); within one pair index, heads of a batch item are adjacent so heads that share
-// K/V run at the same time.  Paged, where the items' lengths differ: the list at `order`
-// in shared memory holds the classes (qi, b) by decreasing tile count, each with its heads
-// adjacent (batches of more classes than it holds keep the order of the items).  (On 16 items of
-// 1024 .. 8192 keys, 1024 units on 152 CTAs, the busiest CTA had 1.61 times the mean work
-// in the order of the items and has 1.04 times it in this one; bf16 pools 571 -> 368 us,
-// 4-bit 663 -> 438 us, 432 with its launch as a programmatic dependent.)
-__device__ __forceinline__ Unit unit_at(int u, const FwdParams& p, bool paged,
-                                        uint32_t order) {
+// Unit u: query-pair index decreasing (the longest causal rows first); within one pair
+// index, heads of a batch item are adjacent so heads that share K/V run at the same time.
+// Sorted: the list at `order` in shared memory holds the classes (qi, b) by decreasing tile
+// count, each with its heads adjacent.
+//
+// Paged items have lengths of their own.  On 16 items of 1024 .. 8192 keys, 1024 units on
+// 152 CTAs, the busiest CTA had 1.61 times the mean work in the order of the items and has
+// 1.04 times it sorted: bf16 pools 571 -> 368 us, 4-bit 663 -> 438 us.  A unit then costs
+// some 0.5 us more to find, and the sort of 300 classes 4 us, so the sorted kernels are taken
+// where there is more than one unit a CTA and a bound on the keys above kSortLen; they leave
+// the order as it is where no item has more keys than that.  Us, items' order / sorted (D
+// 128, bf16 pools, lengths up to the bound): 300 items x 4 heads x 4 rows: 128 keys: 28.9 /
+// 37.3, 512: 51.8 / 51.9, 1024: 88.2 / 73.0, 2048: 153 / 116; 40 x 8 x 64: 128: 12.5 / 14.0,
+// 512: 21.4 / 18.4, 2048: 51.3 / 38.1; 100 x 16 x 100: 256: 59.8 / 64.1, 1024: 106 / 107,
+// 2048: 196 / 166.  Short items under a loose bound stay the dearer: 300 x 4 x 4 rows on up to
+// 100 keys 33.0 us with a bound of 8192, 28.6 with one of 100.  Batches of more classes than
+// kMaxSorted keep the items' order: 49 items of 2048 rows on 2048 .. 8192 keys (392 classes)
+// run at 1376 TFLOP/s, 47 of them (376) at 1473.
+template <Src SRC>
+__device__ __forceinline__ Unit unit_at(int u, const FwdParams& p, uint32_t order) {
   Unit U;
   int qi;
-  if (paged && p.B * p.n_qpairs <= kMaxSorted) {
+  if (is_sorted(SRC) && p.B * p.n_qpairs <= kMaxSorted) {
     const int i = u / p.Hq, h = u - i * p.Hq;
     uint16_t cls;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(cls) : "r"(order + 2 * i));
@@ -200,7 +215,7 @@ __device__ __forceinline__ Unit unit_at(int u, const FwdParams& p, bool paged,
   }
   U.qp = p.n_qpairs - 1 - qi;
   U.bkv = U.b * p.Hkv + U.kvh;
-  U.L = keys_of(U.b, p, paged, U.bad);
+  U.L = keys_of(U.b, p, is_paged(SRC), U.bad);
 #pragma unroll
   for (int i = 0; i < 2; ++i) U.n[i] = tiles_of(U.qp, i, U.L, p);
   U.nkv = max(U.n[0], U.n[1]);
@@ -240,8 +255,8 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
                               const CUtensorMap* tmV, const FwdParams& p, uint32_t sbase,
                               const Bars<D, SRC>& bar, volatile int* abort) {
   using C = Cfg<D, SRC>;
-  constexpr bool PAGED = SRC != Src::kContiguous;
-  constexpr bool RAW = SRC == Src::kPaged4;
+  constexpr bool PAGED = is_paged(SRC);
+  constexpr bool RAW = is_kv4(SRC);
   constexpr int NRING = RAW ? C::NRAW : C::NSLOT;  // the ring this warp fills
   const int lane = threadIdx.x & 31;
   const uint32_t sQ = sbase + C::OFF_Q, sR = sbase + (RAW ? C::OFF_RAW : C::OFF_RING);
@@ -253,7 +268,7 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
   for (int r = 0; ok && r * static_cast<int>(gridDim.x) < p.num_units; ++r) {
     const int u = unit_of_round(r);
     if (u >= p.num_units) continue;
-    const Unit U = unit_at(u, p, PAGED, bar.order());
+    const Unit U = unit_at<SRC>(u, p, bar.order());
     if (PAGED && U.bad && lane == 0) raise_flag(p.flags, DEVFLAG_BAD_SEQLEN);
     if (!mbar_wait_warp(bar.q_empty(), (uc & 1) ^ 1, abort, p.flags, lim)) { ok = false; break; }
     last_q_issued = !(p.withhold_copy && uc == 0);  // test hook: withhold the first Q
@@ -365,7 +380,7 @@ __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SR
   for (int r = 0; r * static_cast<int>(gridDim.x) < p.num_units; ++r) {
     const int u = unit_of_round(r);
     if (u >= p.num_units) continue;
-    const Unit U = unit_at(u, p, true, bar.order());
+    const Unit U = unit_at<SRC>(u, p, bar.order());
     for (int j = 0; j < U.nkv; ++j) {
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ++rc) {
@@ -430,7 +445,7 @@ __device__ void dequant_warp(const FwdParams& p, uint8_t* smem, const Bars<D, SR
 template <int D, Src SRC>
 struct MmaWarp {
   using C = Cfg<D, SRC>;
-  static constexpr bool PAGED = SRC != Src::kContiguous;
+  static constexpr bool PAGED = is_paged(SRC);
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(BM, BN, 0, 0);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(BM, D, 0, 1);  // A (P) in TMEM, V MN-major
   static constexpr uint64_t kTileStep = C::TILE_BYTES >> 4;  // descriptor address units
@@ -488,7 +503,7 @@ struct MmaWarp {
   __device__ bool issue_pv(int j, int nkv, int L, bool ring_seen) {
     const int vs = slot(2 * j + 1);
     if (!ring_seen && !wait(bar.slot_full(vs), par(2 * j + 1))) return false;
-    if (SRC == Src::kPaged && j == nkv - 1 && zeroed_j != j) {
+    if (is_paged(SRC) && !is_kv4(SRC) && j == nkv - 1 && zeroed_j != j) {
       zeroed_j = j;
       // Key rows past the sequence end hold stale or arbitrary data (even NaN);
       // their probabilities are 0, but 0 * NaN would reach O.  Clear those rows.
@@ -519,7 +534,7 @@ struct MmaWarp {
     for (int r = 0; r * static_cast<int>(gridDim.x) < p.num_units; ++r) {
       const int u = unit_of_round(r);
       if (u >= p.num_units) continue;
-      const Unit U = unit_at(u, p, PAGED, bar.order());
+      const Unit U = unit_at<SRC>(u, p, bar.order());
       if (!wait(bar.q_full(), uc & 1)) return;
       ++uc;
       const int n0 = U.n[0], n1 = U.n[1], nkv = U.nkv;
@@ -581,21 +596,21 @@ template <int D, Src SRC>
 __device__ void softmax_wg(const FwdParams& p, uint32_t tmem, const Bars<D, SRC>& bar,
                            volatile int* abort, const int I) {
   using C = Cfg<D, SRC>;
-  constexpr bool PAGED = SRC != Src::kContiguous;
+  constexpr bool PAGED = is_paged(SRC);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sp = warp & 3;  // TMEM sub-partition this warp may access
   const int r = sp * 32 + lane;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
   // (the 4-bit cache's keys come divided by 64)
-  const float sl2 = p.scale_log2 * (SRC == Src::kPaged4 ? 64.f : 1.f);
-  const float scale = p.scale * (SRC == Src::kPaged4 ? 64.f : 1.f);
+  const float sl2 = p.scale_log2 * (is_kv4(SRC) ? 64.f : 1.f);
+  const float scale = p.scale * (is_kv4(SRC) ? 64.f : 1.f);
   const unsigned long long lim = p.wait_limit_ns;
   int sc = 0;  // S tiles consumed (= P tiles produced), all units
 
   for (int rr = 0; rr * static_cast<int>(gridDim.x) < p.num_units; ++rr) {
     const int u = unit_of_round(rr);
     if (u >= p.num_units) continue;
-    const Unit U = unit_at(u, p, PAGED, bar.order());
+    const Unit U = unit_at<SRC>(u, p, bar.order());
     const int n = I ? U.n[1] : U.n[0];
     const int qpos = 256 * U.qp + 128 * I + r;
     const bool row_valid = qpos < p.Tq;
@@ -678,9 +693,9 @@ __device__ void softmax_wg(const FwdParams& p, uint32_t tmem, const Bars<D, SRC>
     uint16_t* orow = static_cast<uint16_t*>(p.o) + (static_cast<size_t>(U.bh) * p.Tq + qpos) * D;
     const float nan = __int_as_float(0x7fc00000);
     // no visible key (or none processed); a NaN from the 4-bit cache is a result
-    const bool empty = SRC == Src::kPaged4 ? l == 0.f : !(l > 0.f);
+    const bool empty = is_kv4(SRC) ? l == 0.f : !(l > 0.f);
     // (the 4-bit cache's values come divided by 64)
-    const float inv_l = empty ? 0.f : (SRC == Src::kPaged4 ? 64.f : 1.f) / l;
+    const float inv_l = empty ? 0.f : (is_kv4(SRC) ? 64.f : 1.f) / l;
     if (n > 0) {
       if (!mbar_wait_warp(bar.s_free(I), (sc - 1) & 1, abort, p.flags, lim)) return;
       tc_fence_after();
@@ -736,7 +751,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1)
     mbar_init(bar.q_full(), 1);
     mbar_init(bar.q_empty(), 1);
     for (int s = 0; s < C::NSLOT; ++s) {
-      mbar_init(bar.slot_full(s), SRC == Src::kPaged4 ? 4 : 1);
+      mbar_init(bar.slot_full(s), is_kv4(SRC) ? 4 : 1);
       mbar_init(bar.slot_empty(s), 1);
     }
     for (int s = 0; s < C::NRAW; ++s) {
@@ -762,12 +777,12 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1)
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
-  if constexpr (SRC == Src::kPaged4) {
+  if constexpr (is_kv4(SRC)) {
     // launched as a programmatic dependent: the preceding kernel's writes (an append's) are
     // complete and visible past this point
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }
-  if constexpr (SRC != Src::kContiguous) {
+  if constexpr (is_sorted(SRC)) {
     // every CTA sorts the classes for itself: a class's place is the number of classes
     // before it, by tiles and then by index
     const int classes = p.B * p.n_qpairs;
@@ -775,18 +790,19 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1)
       uint16_t* cost = reinterpret_cast<uint16_t*>(smem + C::OFF_COST);
       uint16_t* places = reinterpret_cast<uint16_t*>(smem + C::OFF_ORDER);
       const int c = threadIdx.x;
-      int mine = 0;
+      int mine = 0, L = 0;
       if (c < classes) {
         const int qi = c / p.B, qp = p.n_qpairs - 1 - qi;
         bool bad;
-        const int L = keys_of(c - qi * p.B, p, true, bad);
+        L = keys_of(c - qi * p.B, p, true, bad);
         mine = min(tiles_of(qp, 0, L, p) + tiles_of(qp, 1, L, p), 65535);
         cost[c] = static_cast<uint16_t>(mine);
       }
-      __syncthreads();
+      const bool sort = __syncthreads_or(L > kSortLen);
       if (c < classes) {
-        int place = 0;
-        for (int i = 0; i < classes; ++i) place += cost[i] > mine || (cost[i] == mine && i < c);
+        int place = sort ? 0 : c;
+        for (int i = 0; sort && i < classes; ++i)
+          place += cost[i] > mine || (cost[i] == mine && i < c);
         places[place] = static_cast<uint16_t>(c);
       }
     }
@@ -797,7 +813,7 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp < 4) {
-    regs_decrease<SRC == Src::kPaged4 ? kRegsWg0With4 : kRegsWg0>();
+    regs_decrease<is_kv4(SRC) ? kRegsWg0With4 : kRegsWg0>();
     if (warp == 0) {
       producer_warp<D, SRC>(&tmQ, &tmK, &tmV, p, sbase, bar, abort);
     } else if (warp == 1) {
@@ -808,13 +824,13 @@ __global__ void __launch_bounds__(kThreads<SRC>, 1)
       if (lane == 0) mbar_wait_quiet(bar.teardown(), 0, 1000000000ull);
       __syncwarp();
     }
-  } else if (SRC == Src::kPaged4 && warp >= 12) {
-    if constexpr (SRC == Src::kPaged4) {
+  } else if (is_kv4(SRC) && warp >= 12) {
+    if constexpr (is_kv4(SRC)) {
       regs_decrease<kRegsDequant>();
       dequant_warp<D, SRC>(p, smem, bar, abort);
     }
   } else {
-    regs_increase<SRC == Src::kPaged4 ? kRegsSoftmax4 : kRegsSoftmax>();
+    regs_increase<is_kv4(SRC) ? kRegsSoftmax4 : kRegsSoftmax>();
     softmax_wg<D, SRC>(p, tmem, bar, abort, warp < 8 ? 0 : 1);
   }
 
@@ -844,7 +860,7 @@ cudaError_t launch(int grid, const CUtensorMap& tmQ, const CUtensorMap& tmK,
   cfg.dynamicSmemBytes = Cfg<D, SRC>::SMEM_BYTES;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = SRC == Src::kPaged4 ? 1 : 0;  // the others do not wait for the grid before
+  cfg.numAttrs = is_kv4(SRC) ? 1 : 0;  // the others do not wait for the grid before
   return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<D, SRC>, tmQ, tmK, tmV, p);
 }
 
@@ -857,7 +873,11 @@ cudaError_t prepare_attn_fwd() {
   if ((e = set_smem<64, Src::kPaged>()) != cudaSuccess) return e;
   if ((e = set_smem<128, Src::kPaged>()) != cudaSuccess) return e;
   if ((e = set_smem<64, Src::kPaged4>()) != cudaSuccess) return e;
-  return set_smem<128, Src::kPaged4>();
+  if ((e = set_smem<128, Src::kPaged4>()) != cudaSuccess) return e;
+  if ((e = set_smem<64, Src::kSortedPaged>()) != cudaSuccess) return e;
+  if ((e = set_smem<128, Src::kSortedPaged>()) != cudaSuccess) return e;
+  if ((e = set_smem<64, Src::kSortedPaged4>()) != cudaSuccess) return e;
+  return set_smem<128, Src::kSortedPaged4>();
 }
 
 cudaError_t launch_attn_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
@@ -866,8 +886,13 @@ cudaError_t launch_attn_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, cons
   if (grid <= 0) return cudaSuccess;
   auto run = [&](auto d) {
     constexpr int DD = decltype(d)::value;
-    if (p.kv4_pool != nullptr) return launch<DD, Src::kPaged4>(grid, tmQ, tmK, tmV, p, stream);
-    if (p.block_table != nullptr) return launch<DD, Src::kPaged>(grid, tmQ, tmK, tmV, p, stream);
+    const bool sorted = p.num_units > grid && p.max_kv_len > kSortLen;
+    if (p.kv4_pool != nullptr)
+      return sorted ? launch<DD, Src::kSortedPaged4>(grid, tmQ, tmK, tmV, p, stream)
+                    : launch<DD, Src::kPaged4>(grid, tmQ, tmK, tmV, p, stream);
+    if (p.block_table != nullptr)
+      return sorted ? launch<DD, Src::kSortedPaged>(grid, tmQ, tmK, tmV, p, stream)
+                    : launch<DD, Src::kPaged>(grid, tmQ, tmK, tmV, p, stream);
     return launch<DD, Src::kContiguous>(grid, tmQ, tmK, tmV, p, stream);
   };
   return p.D == 64 ? run(std::integral_constant<int, 64>{}) : run(std::integral_constant<int, 128>{});

@@ -135,3 +135,41 @@ def test_paged_prefill_bad_length_is_flagged_not_fatal(gb):
                                           cfg.softmax_scale)
     for b in (0, 2):
         check_close(og[b], lg[b], o_ref[b], lse_ref[b], f"good item {b}")
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("B,Hq,Hkv,D,Tq", [(90, 4, 2, 128, 40), (90, 4, 2, 64, 300), (400, 2, 1, 64, 40)])
+def test_the_order_of_the_units_changes_nothing(gb, B, Hq, Hkv, D, Tq, four):
+    """More units than SMs in the items' order (bounds up to 512 keys), in the order of
+    their lengths (some item longer), under a loose bound (no item longer) and past the
+    classes that are sorted: the same bits."""
+    lens = list(synth.uniform_ints(23000 + B, B, 1, 512))
+    cfg = synth.DecodeConfig("order", B, Hq, Hkv, D, 1, 900, 16, 23100 + D)
+    p = synth.paged_inputs(cfg, seq_lens=lens + [900], max_seq_len=900)
+    q = to_dev(synth.normal_bf16(23200, (B + 1, Hq, Tq, D)))
+    table, n = to_dev_i32(p.block_table), to_dev_i32(p.seq_lens)
+    if four:
+        import rope_ref as ref
+        pool = torch.from_numpy(ref.pool_from_bf16(p.k_pool, p.v_pool)).cuda()
+        if gb.paged_kv4_attn_prefill_workspace_size(B, Hq, Hkv, Tq, D, 900):
+            pytest.skip("short chunks of this batch are rows, not tiles")
+
+        def call(m, bound):
+            return gb.paged_kv4_attn_prefill(q[:m], pool, table[:m], n[:m], bound, scale=0.1)
+    else:
+        pools = to_dev(p.k_pool), to_dev(p.v_pool)
+
+        def call(m, bound):
+            return gb.paged_attn_prefill(q[:m], *pools, table[:m], n[:m], bound, scale=0.1)
+
+    o, lse = call(B, 512)
+    for m, bound in ((B, 513), (B, 100000), (B + 1, 900)):
+        o2, lse2 = call(m, bound)
+        assert torch.equal(o, o2[:B]) and torch.equal(lse, lse2[:B])
+    torch.cuda.synchronize()
+    assert gb.attn_device_status()[1] == 0
+    if not four:
+        want, wl = oracle.paged_prefill(synth.normal_bf16(23200, (B + 1, Hq, Tq, D))[:4], p.k_pool,
+                                        p.v_pool, p.block_table[:4], p.seq_lens[:4], True, 0.1)
+        live = ~np.isneginf(wl)
+        check_close(from_dev(o[:4])[live], from_dev(lse[:4])[live], want[live], wl[live], "order")
