@@ -452,6 +452,13 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+def _check_table(block_table, S, device):
+    """A block table [S, blocks]; its width is an int of the C ABI."""
+    _check_tensor("block_table", block_table, _i32, None, device)
+    if block_table.dim() != 2 or block_table.shape[0] != S or block_table.shape[1] >= 1 << 31:
+        raise ValueError(f"block_table must have shape ({S}, blocks), got {tuple(block_table.shape)}")
+
+
 def _check_rope(cos_sin, q_weight, k_weight, positions, B, T, D, device):
     """Checks the norm and rotation operands; returns (rot_dim, max_pos)."""
     if q_weight is not None:
@@ -464,8 +471,8 @@ def _check_rope(cos_sin, q_weight, k_weight, positions, B, T, D, device):
         return 0, 0
     shape = cos_sin.shape if isinstance(cos_sin, _Tensor) else None
     _check("cos_sin", cos_sin, _f32, shape, device)
-    if len(shape) != 2 or shape[0] == 0 or shape[1] == 0:
-        raise ValueError("cos_sin must be a non-empty [max_pos, rot_dim] table")
+    if len(shape) != 2 or shape[0] == 0 or shape[1] == 0 or max(shape) >= 1 << 31:
+        raise ValueError("cos_sin must be a non-empty [max_pos, rot_dim] table of sizes below 2^31")
     return shape[1], shape[0]
 
 
@@ -714,9 +721,7 @@ def _append(op, pools, q, k, v, block_table, seq_lens, cos_sin, q_weight, k_weig
         if q.shape != (S, Tn, Hq, D):
             _check_rows("q", q, (S, Tn, None, D), device)
     _check("seq_lens", seq_lens, _i32, (S,), device)
-    _check_tensor("block_table", block_table, _i32, None, device)
-    if block_table.dim() != 2 or block_table.shape[0] != S:
-        raise ValueError("inconsistent append shapes")
+    _check_table(block_table, S, device)
     if len(pools) == 2:
         _check_bf16("k_pool", pools[0], 4, device)
         shape = pools[0].shape
@@ -800,11 +805,11 @@ def paged_kv4_gather(kv_pool, block_table, seq_lens, max_seq_len: int, k_out=Non
     NB = _check_kv4("kv_pool", kv_pool, None, None, device)
     _, Hkv, chunk = kv_pool.shape
     D = chunk // 18
-    for name, t in (("block_table", block_table), ("seq_lens", seq_lens)):
-        _check_tensor(name, t, _i32, None, device)
-    if seq_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != seq_lens.shape[0]:
-        raise ValueError("inconsistent gather shapes")
+    _check_tensor("seq_lens", seq_lens, _i32, None, device)
+    if seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be a 1-d tensor")
     S, max_seq_len = seq_lens.shape[0], _length(max_seq_len)
+    _check_table(block_table, S, device)
     shape = (S, Hkv, max_seq_len, D)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
@@ -841,10 +846,9 @@ def _check_kv4_attention(q, kv_pool, block_table, lens, rows, out, lse):
     shape = q.shape
     _check("q", q, _bf16, shape, device)
     NB = _check_kv4("kv_pool", kv_pool, None, None, device)
-    _check_tensor("block_table", block_table, _i32, None, device)
+    _check_table(block_table, shape[0], device)
     _check("the lengths", lens, _i32, shape[:1], device)
-    if kv_pool.shape[2] != 18 * shape[-1] or block_table.dim() != 2 or \
-            block_table.shape[0] != shape[0]:
+    if kv_pool.shape[2] != 18 * shape[-1]:
         raise ValueError("inconsistent paged attention shapes")
     if out is not None:
         _check("out", out, _bf16, shape, device)

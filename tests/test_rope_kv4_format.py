@@ -367,6 +367,29 @@ def test_binding_refuses_bad_kv4_attention(bad):
         gb.paged_kv4_attn_prefill(**a)
 
 
+def test_tables_past_an_int_are_refused():
+    """Sizes that the C ABI's ints would wrap (on the meta device: nothing is allocated)."""
+    def meta(*s, dtype=torch.bfloat16):
+        return torch.empty(s, dtype=dtype, device="meta")
+
+    i32, u8, wide = torch.int32, torch.uint8, (1 << 32) + 4
+    rows = dict(q=meta(2, 1, 4, 64), k=meta(2, 1, 2, 64), v=meta(2, 1, 2, 64))
+    table, lens, pool = meta(2, wide, dtype=i32), meta(2, dtype=i32), meta(9, 2, 18 * 64, dtype=u8)
+    with pytest.raises(ValueError, match="cos_sin"):
+        gb.qkv_norm_rope(**rows, cos_sin=meta(wide, 64, dtype=torch.float32))
+    calls = [
+        lambda: gb.paged_kv4_append(**rows, kv_pool=pool, block_table=table, seq_lens=lens),
+        lambda: gb.paged_qkv_append(**rows, k_pool=meta(9, 2, 16, 64), v_pool=meta(9, 2, 16, 64),
+                                    block_table=table, seq_lens=lens),
+        lambda: gb.paged_kv4_gather(pool, table, lens, 64),
+        lambda: gb.paged_kv4_attn_decode(meta(2, 4, 64), pool, table, lens, 64),
+        lambda: gb.paged_kv4_attn_prefill(meta(2, 4, 1, 64), pool, table, lens, 64),
+    ]
+    for call in calls:
+        with pytest.raises(ValueError, match="block_table"):
+            call()
+
+
 def test_first_calls_of_two_threads(monkeypatch):
     """A call that another thread makes at any point of the first one's loading of torch finds
     all of what it uses (each line of the loader is such a point)."""
