@@ -428,9 +428,16 @@ int attend_rows(const void* q, const void* kv_pool, const int32_t* block_table,
 //   4 x 16/1 heads, 2000 keys, D 64:    Tq 16: 12 / 27   64: 26 / 27     96: 36 / 27
 //   1 x 32/8 heads, 100000 keys, D 128: Tq 1: 32 / 1235  64: 499 / 1236  128: 974 / 1236  192: 1462 / 1403
 // i.e. the crossing is near Tq = 30 with every SM busy and moves up as query heads are
-// fewer than the 152 SMs.  On short caches (3 x 8/2 heads, 500 keys, D 64: Tq 4: 7.2 / 11.3,
-// 37: 9.0 / 11.3; 300 keys: 7.2 / 9.9, 9.0 / 10.1) the rows' few microseconds do not pay for
-// their second launch and workspace on the host, unless the tiles need several rounds.
+// fewer than the 152 SMs.  Caches of up to 512 keys stay with the tiles, unless those need
+// several rounds: one tile's chain is short then, and the rows take two launches and a
+// workspace.  Rows / tiles (us, lengths from half the bound):
+//   3 x 8/2 heads, D 64:    100 keys: Tq 4: 7.8 / 5.3   37: 9.2 / 5.3    300: 4: 7.3 / 7.9   37: 9.6 / 8.3
+//                           500 keys: Tq 4: 7.2 / 9.2   16: 8.0 / 9.1    37: 9.5 / 8.2
+//   1 x 32/8 heads, D 128:  300 keys: Tq 4: 8.6 / 7.8   16: 9.6 / 7.8    500: 4: 9.0 / 9.2   16: 10.4 / 9.6
+//   12 x 12/2 heads, D 128: 300 keys: Tq 4: 10.0 / 10.4 16: 12.8 / 10.6  500: 4: 11.1 / 12.0 16: 13.0 / 12.1
+// A few tokens on the longest of them are the exception, by up to a fifth, and single tokens
+// (2.6 to 5.4 us in the one launch of a decode against 5.3 to 12), which paged_kv4_attn_decode
+// is for.
 // Sizes that the row kernels cannot count are the tile kernel's.
 bool by_rows(int B, int Hq, int Hkv, int Tq, int max_kv_len) {
   const int64_t units = static_cast<int64_t>(B) * Hq;

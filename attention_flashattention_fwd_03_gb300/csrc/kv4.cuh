@@ -91,7 +91,8 @@ __device__ __forceinline__ uint32_t kv4_codes(const float2 (&x)[4], float s) {
 // Eight codes u of one word (low nibble first) times a scale pair (s, s; bf16 bits): the
 // bf16 values (u - 8) s TIMES / 64 in channel order, TIMES = 1 or 64.  A code alone in 16
 // bits is the subnormal bf16 u 2^-133; one fused multiply-add makes it (u - 8) / 64 and the
-// products scale it, all exact (TIMES = 1: where s >= 2^-120).  (The other way, 128 + u by an
+// products scale it, all exact.  (TIMES = 1: where s >= 2^-123; below that a value / 64 is a
+// subnormal bf16 and rounded to a multiple of 2^-133, so the value is off by 2^-128 at most.)  (The other way, 128 + u by an
 // OR into the mantissa, then - 136, times s, delivers channels i and i + 4 in one register
 // and takes four more permutes a word on the pipe that a softmax beside it needs: 784 us
 // against 698 on the prefill of 16 x 512 tokens.)

@@ -20,7 +20,7 @@
 //      row's products would not keep either.  (Rows below 2^-112 throughout lose more: they
 //      are only brought up by 2^126.)  The products start from -8 sum q, which the same unit
 //      computes once a piece.  The power of two goes into the softmax scale, and what that
-//      does not hold as an fp32 (rows from about 2^93 on) into the scores.
+//      does not hold as an fp32 (rows from about 2^93 on) into the scores (0.2 of 25 us).
 //   V: p t needs the range of bf16, whose products do not take 2^-133; one fused
 //      multiply-add on the pair makes it n / 64, exactly.
 // Scores, softmax statistics and outputs are fp32; p t is rounded to bf16 for its product
@@ -38,10 +38,11 @@
 //
 // What bounds it: 64 requests of 512 to 8192 tokens, 12/2 heads, D 128 (80 MB, 11.8 us at
 // the copy rate) take 25 us, one of 131000 tokens, 32/8 heads (151 MB, 22.2 us) 36 us.  The
-// copies alone would take 12 and 30: at 28 % of its size the cache arrives faster than the
-// ALU takes nibbles apart (busy 49 % of the long case, issue slots 55 %, with the 12 warps an
-// SM that 168 registers and two stages a warp leave room for).  Set-up before the first
-// copy lands is about 3 us, the merge kernel 4.  Steps of 2 blocks 27 and 41 us; 4 CTAs an SM
+// copies alone would take 12 and 30.  No pipe is full (issue slots 50 and 56 %, ALU 43 and
+// 51 %, tensor 15 and 20 %): a step is one chain of loads, products, shuffles, exponentials
+// and products, 3 us for the 12 warps an SM that 168 registers and two stages a warp leave
+// room for, and too few warps to hide its latencies.  Set-up before the first copy lands
+// is about 3 us, the merge kernel 4.  Steps of 2 blocks 27 and 41 us; 4 CTAs an SM
 // (128 registers, spills) 31 and 47; V scales multiplied into transposed bf16 probabilities
 // (22 of 230 instructions a block fewer, one more rounding) 25.4 and 37.2; V codes by 8-byte
 // loads no change.
@@ -72,9 +73,14 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStepBlocks = 4;  // blocks of one step: 64 tokens share a softmax update
 // Deal::kDirect up to this max_seq_len.  Device time in us, direct / split, by max_seq_len
-// (lengths from half of it): 5 x 16/1 heads, D 64: 256: 3.9 / 6.8, 1024: 7.6 / 6.8, 2048: 12.3
-// / 7.6; 64 x 12/2, D 128: 256: 5.2 / 9.2, 1024: 11.3 / 10.5, 2048: 18.8 / 15.5; 200 x 8/2, D
-// 128: 1024: 15.2 / 18.9, 4096: 48 / 43.  An eager call takes 20 us of host time instead of 25.
+// (lengths from half of it):
+//   5 x 16/1 heads, D 64:     256: 3.7 / 7.3    512: 4.8 / 7.4    768: 6.1 / 7.4    1024: 7.5 / 7.3
+//   1 x 12/2, D 128:          256: 3.7 / 6.6    512: 5.2 / 7.0    768: 5.0 / 7.1    1024: 6.7 / 7.2
+//   64 x 12/2, D 128:         256: 5.7 / 8.8    512: 8.3 / 10.0   768: 10.4 / 10.1  1024: 13.2 / 10.2
+//   200 x 8/2, D 128:         256: 6.5 / 11.0   512: 9.6 / 14.5   768: 12.4 / 15.9  1024: 15.1 / 18.2
+//   64 x 32/8, D 128:         256: 8.4 / 11.1   512: 12.6 / 15.4  768: 15.8 / 18.6  1024: 19.3 / 21.1
+// An eager call adds 0.2 to 2 us to either.  Batches of about one CTA an SM are the
+// exception above 700 tokens: their few steps a warp are a longer chain than the split's.
 constexpr int kDirectMaxLen = 1024;
 constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by > 2^8
 

@@ -8,8 +8,9 @@
 // row and weights are read once and every row moves as whole 128- or 256-byte segments;
 // the loads of four passes are in flight together.  D 128: a 16k prompt of 32/8 heads (411
 // MB) 66 us, 91 % of the copy rate; 16 x 512 tokens appended to the bf16 cache (202 MB) 36 us,
-// 83 %; to the 4-bit cache (187 MB) 40 us, 69 %, its quantiser taking a quarter of the
-// instructions at 65 % of the issue slots.
+// 83 %; to the 4-bit cache (187 MB) 40 us, 69 %: a quarter more instructions (64 % of the issue
+// slots), and K rows pass through shared memory between two warp barriers a row set, which
+// puts the passes in flight back in line.  Neither HBM nor the issue slots are full.
 #include <cuda_runtime.h>
 
 #include <type_traits>

@@ -21,7 +21,10 @@
 // their sum, each rounded, as a program that evaluates it tensor by tensor does: a fused
 // product would differ in the last bit of one value in some ten thousand, which the 4-bit
 // cache can turn into a whole step.  (Costs 0.4 of 66 us on a 16k prompt, 1 of 50 on an
-// append to the 4-bit cache and its gather.)
+// append to the 4-bit cache and its gather.)  The exception is the sum of squares behind r
+// where a row turns in part or interleaved: fused products, in the order of the lanes.  It is
+// as exact, but not the same bits: a row may differ in its last bit between such a rotation
+// and a full one of halves (row_squares).
 #pragma once
 
 #include <cstdint>
@@ -133,7 +136,8 @@ __device__ __forceinline__ void rotate8_stepwise(Lane8& x, const Planes& p, int 
 
 // Sum of the squares of a row.  FULL (every channel rotates, planes of halves): 32 columns
 // c, c + 32, .. are added first, then neighbouring columns in pairs, the order in which a
-// reduction over a row of 128 or 64 values by a warp goes, for the reason given above.
+// reduction over a row of 128 or 64 values by a warp goes, for the reason given above.  Else
+// a lane's eight are added with fused products, then the lanes.
 template <int D, bool FULL>
 __device__ __forceinline__ float row_squares(const Lane8& x, int l) {
   if constexpr (!FULL) {

@@ -415,7 +415,8 @@ int paged_kv4_attn_decode(const void *q, const void *kv_pool, const int32_t *blo
 /*
  * paged_kv4_attn_prefill -- paged_attn_prefill over the 4-bit cache: the attention of
  * the Tq newest tokens of each item over the values that paged_kv4_gather returns.
- * The values are bf16 exactly, so the kernel computes with them as they are.
+ * The values are bf16 exactly, so the kernel computes with them as they are (long chunks
+ * hold values of groups whose scale is below 2^-123 to within 2^-128).
  *
  *   kv_pool       [num_pool_blocks, Hkv, 18 D] bytes
  *   workspace     >= paged_kv4_attn_prefill_workspace_size(...) bytes, 256-byte
