@@ -70,10 +70,10 @@ def torch_version() -> str | None:
 
 
 def binding_is_current() -> bool:
-    """Whether _binding was built for the installed torch, or failed to be (another try
-    would end the same way)."""
+    """Whether there is nothing to do about _binding: built for the installed torch, failed to
+    be (another try would end the same way), or in a tree that cannot be written to."""
     version = torch_version()
-    if version is None:
+    if version is None or not os.access(os.path.dirname(BINDING), os.W_OK):
         return True
     try:
         with open(BINDING_STAMP) as f:

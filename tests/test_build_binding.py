@@ -70,6 +70,12 @@ def test_without_torch_there_is_nothing_to_build(tree, monkeypatch):
     assert tree.built == 0
 
 
+def test_a_tree_that_cannot_be_written_to_is_left_alone(tree, monkeypatch):
+    monkeypatch.setattr(build.os, "access", lambda path, mode: False)
+    build.build()
+    assert tree.built == 0
+
+
 def test_the_version_is_the_installed_torchs(monkeypatch):
     assert build.torch_version() == torch.__version__
     modules = {n: m for n, m in build.sys.modules.items() if n != "torch"}
