@@ -17,6 +17,12 @@ From a projection's rows to those calls, norm and rotation included, and the cac
                                    seq_lens, cos_sin, q_weight, k_weight)
     q, new_lens = paged_kv4_append(q_rows, k_rows, v_rows, kv_pool, block_table, seq_lens,
                                    cos_sin, q_weight, k_weight)
+
+A step with a tree of drafted tokens for each request, appended behind its cache:
+
+    o, lse = paged_attn_tree(q, k_pool, v_pool, block_table, seq_lens, parents, max_seq_len)
+    tokens, path, counts = draft_verify(target_probs, draft_probs, drafted, parents, uniforms)
+    new_lens = paged_kv_keep(k_pools, v_pools, block_table, seq_lens, path, counts, new_lens)
 """
 
 from __future__ import annotations
@@ -38,6 +44,8 @@ ATTN_ERR_UNSUPPORTED = 2
 ATTN_ERR_CUDA = 3
 ATTN_ERR_DEVICE = 4
 
+TREE_MAX_NODES = 256  # nodes of a tree of drafted tokens
+
 EXPORTS = (
     "attn_status_string",
     "attn_fwd",
@@ -57,6 +65,10 @@ EXPORTS = (
     "paged_kv4_attn_decode",
     "paged_kv4_attn_prefill_workspace_size",
     "paged_kv4_attn_prefill",
+    "paged_attn_tree_workspace_size",
+    "paged_attn_tree",
+    "draft_verify",
+    "paged_kv_keep",
     "attn_test_set_failure",
     "attn_device_status",
     "attn_version",
@@ -132,6 +144,15 @@ def _bind(h):
     h.paged_kv4_attn_prefill_workspace_size.restype = Z
     h.paged_kv4_attn_prefill.argtypes = [P] * 4 + [I] * 10 + [F, P, P, P, Z, P]
     h.paged_kv4_attn_prefill.restype = I
+    h.paged_attn_tree_workspace_size.argtypes = [I] * 6
+    h.paged_attn_tree_workspace_size.restype = Z
+    h.paged_attn_tree.argtypes = [P] * 7 + [I] * 9 + [F, P, P, P, Z, P]
+    h.paged_attn_tree.restype = I
+    h.draft_verify.argtypes = [P, P, S, S, I, P, P, P, P, I, I, I, P, P, P, P]
+    h.draft_verify.restype = I
+    pools = ctypes.POINTER(ctypes.c_void_p)  # a host array
+    h.paged_kv_keep.argtypes = [pools, pools, I, P, P, P, P, P, I, I, I, I, I, I, I, P]
+    h.paged_kv_keep.restype = I
     h.attn_test_set_failure.argtypes = [ctypes.c_ulonglong, I]
     h.attn_test_set_failure.restype = I
     h.attn_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -949,6 +970,216 @@ def paged_kv4_attn_prefill(q, kv_pool, block_table, kv_lens, max_kv_len: int,
     if st != ATTN_OK:
         raise GbAttnError("paged_kv4_attn_prefill", st)
     return out, lse
+
+
+def paged_attn_tree_workspace_size(num_seqs: int, Tn: int, Hq: int, Hkv: int, D: int,
+                                   max_seq_len: int) -> int:
+    return (_lib or lib()).paged_attn_tree_workspace_size(num_seqs, Tn, Hq, Hkv, D, max_seq_len)
+
+
+def paged_attn_tree(q, k_pool, v_pool, block_table, seq_lens, parents, max_seq_len: int,
+                    tree_lens=None, scale: float | None = None, out=None, lse=None,
+                    workspace=None, return_lse: bool = True, stream=None):
+    """Attention of a tree of drafted tokens per request against a paged KV cache.
+
+    q [S,Hq,Tn,D] bf16 (the tree's nodes), k_pool/v_pool [NB,Hkv,16,D] bf16, block_table
+    [S,max_blocks] int32, seq_lens [S] int32: tokens cached before the tree, behind which
+    node i's key and value stand at position seq_lens + i; parents [S,Tn] int32, -1 for a
+    root, each below its own index (all CUDA) -> (o [S,Hq,Tn,D] bf16, lse [S,Hq,Tn] fp32).
+    A node sees the cached tokens, its ancestors and itself.  ``tree_lens`` [S] int32 says
+    how many of the Tn (at most 256) places hold nodes (None: all); the others come back as
+    0 and -inf.  ``max_seq_len`` bounds seq_lens + tree_lens.  ``workspace`` (uint8 CUDA
+    tensor) is allocated here when not given.
+    """
+    if _torch is None:
+        _load_torch()
+    _first(q)
+    device = q.device
+    if q.dim() != 4:
+        raise ValueError("q must be a 4-d tensor")
+    S, Hq, Tn, D = shape = q.shape
+    _check("q", q, _bf16, shape, device)
+    _check_bf16("k_pool", k_pool, 4, device)
+    _check("v_pool", v_pool, _bf16, k_pool.shape, device)
+    NB, Hkv, bs, D2 = k_pool.shape
+    if D2 != D:
+        raise ValueError("inconsistent paged attention shapes")
+    _check_table(block_table, S, device)
+    _check("seq_lens", seq_lens, _i32, (S,), device)
+    _check("parents", parents, _i32, (S, Tn), device)
+    if tree_lens is not None:
+        _check("tree_lens", tree_lens, _i32, (S,), device)
+    if out is not None:
+        _check("out", out, _bf16, shape, device)
+    if lse is not None:
+        _check("lse", lse, _f32, shape[:3], device)
+    if workspace is not None:
+        _check_tensor("workspace", workspace, _u8, None, device)
+    max_seq_len = _length(max_seq_len)
+    _check_sizes(S=S, Hq=Hq, Tn=Tn, NB=NB, Hkv=Hkv)
+    _require_cuda(device)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    with _On(device, stream) as handle:
+        if workspace is None:
+            need = paged_attn_tree_workspace_size(S, Tn, Hq, Hkv, D, max_seq_len)
+            if need:
+                workspace = _torch.empty((need,), dtype=_u8, device=device)
+        if out is None:
+            out = _torch.empty(shape, dtype=_bf16, device=device)
+        if return_lse and lse is None:
+            lse = _torch.empty(shape[:3], dtype=_f32, device=device)
+        st = (_lib or lib()).paged_attn_tree(
+            q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
+            seq_lens.data_ptr(), parents.data_ptr(), _ptr(tree_lens), bs, S, Tn, Hq, Hkv, D,
+            block_table.shape[1], NB, max_seq_len, scale, out.data_ptr(), _ptr(lse),
+            _ptr(workspace), workspace.numel() if workspace is not None else 0, handle)
+    if st != ATTN_OK:
+        raise GbAttnError("paged_attn_tree", st)
+    return out, lse
+
+
+def _check_sizes(**sizes):
+    """Sizes that the C ABI takes as ints."""
+    for name, n in sizes.items():
+        if n >= 1 << 31:
+            raise ValueError(f"{name} = {n} is out of range")
+
+
+def _check_probs(name, t, shape, dtype, device):
+    """Probabilities [S, Tn, V] with contiguous rows and any other strides."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (_f32, _bf16) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape {tuple(shape or ('S', 'Tn', 'V'))}, got "
+                         f"{tuple(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def draft_verify(target_probs, draft_probs, draft_tokens, parents, uniforms, tree_lens=None,
+                 tokens_out=None, path=None, counts=None, stream=None):
+    """Which drafted tokens the target model accepts, and the token after them.
+
+    target_probs [S,Tn,V] fp32 or bf16: the target's distribution of the token after each
+    node of the tree; draft_probs, the same shape and type: the distribution each node's
+    children were drawn from, independently, or None if they were put forward without a
+    draw (rows contiguous, other strides as they come).  draft_tokens [S,Tn] int32: the
+    nodes' tokens; node 0 is the token that the tree hangs from and stands already.
+    parents [S,Tn] and tree_lens [S] (None: Tn nodes) int32 as in paged_attn_tree; uniforms
+    [S,Tn] fp32 random numbers in [0, 1).  What is put out is distributed as draws from the
+    target are (include/gbattn.h gives the rule).
+
+    Returns (tokens_out [S,Tn], path [S,Tn], counts [S]) int32: counts[r] tokens are put
+    out for request r, the accepted drafts and one more; path holds the counts[r] nodes
+    that stand, from node 0 down; both are filled up with -1.
+    """
+    if _torch is None:
+        _load_torch()
+    _first(target_probs)
+    device = target_probs.device
+    _check_probs("target_probs", target_probs, None, None, device)
+    S, Tn, V = shape = target_probs.shape
+    if draft_probs is not None:
+        _check_probs("draft_probs", draft_probs, shape, target_probs.dtype, device)
+    for name, t, dtype in (("draft_tokens", draft_tokens, _i32), ("parents", parents, _i32),
+                           ("uniforms", uniforms, _f32)):
+        _check(name, t, dtype, (S, Tn), device)
+    for name, t, size in (("tree_lens", tree_lens, (S,)), ("tokens_out", tokens_out, (S, Tn)),
+                          ("path", path, (S, Tn)), ("counts", counts, (S,))):
+        if t is not None:
+            _check(name, t, _i32, size, device)
+    _check_sizes(S=S, Tn=Tn, V=V)
+    _require_cuda(device)
+    with _On(device, stream) as handle:
+        if tokens_out is None:
+            tokens_out = _torch.empty((S, Tn), dtype=_i32, device=device)
+        if path is None:
+            path = _torch.empty((S, Tn), dtype=_i32, device=device)
+        if counts is None:
+            counts = _torch.empty((S,), dtype=_i32, device=device)
+        st = (_lib or lib()).draft_verify(
+            target_probs.data_ptr(), _ptr(draft_probs), _row_strides(target_probs),
+            _row_strides(draft_probs), 1 if target_probs.dtype == _bf16 else 0,
+            draft_tokens.data_ptr(), parents.data_ptr(), uniforms.data_ptr(), _ptr(tree_lens), S,
+            Tn, V, tokens_out.data_ptr(), path.data_ptr(), counts.data_ptr(), handle)
+    if st != ATTN_OK:
+        raise GbAttnError("draft_verify", st)
+    return tokens_out, path, counts
+
+
+def _row_strides(t):
+    """Strides of requests and nodes (0 where there is one)."""
+    if t is None:
+        return None
+    return (ctypes.c_int64 * 3)(*(st if n > 1 else 0 for n, st in zip(t.shape[:2], t.stride())))
+
+
+def _pools(name, pools, device):
+    """The pools of one or more layers: their pointers and the shape they share."""
+    if isinstance(pools, _Tensor) and pools.dim() == 5:
+        _check_tensor(name, pools, _bf16, None, device)
+        base, step = pools.data_ptr(), pools.stride(0) * 2
+        return [base + i * step for i in range(pools.shape[0])], pools.shape[1:]
+    if isinstance(pools, _Tensor):
+        pools = (pools,)
+    shape = None
+    for t in pools:
+        _check_bf16(name, t, 4, device)
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"the layers of {name} must have one shape")
+        shape = t.shape
+    return [t.data_ptr() for t in pools], shape
+
+
+def paged_kv_keep(k_pool, v_pool, block_table, seq_lens, path, counts, new_seq_lens=None,
+                  stream=None):
+    """Keeps chosen rows behind each request's cache and moves them together (in place).
+
+    The row at position seq_lens[r] + path[r,j] goes to seq_lens[r] + j for j < counts[r],
+    keys and values, in every layer: k_pool/v_pool are bf16 pools [NB,Hkv,16,D], sequences of
+    such pools (one a layer), or all layers' pools in one tensor [layers,NB,Hkv,16,D].
+    block_table [S,max_blocks] (shared by the layers), seq_lens [S] (lengths before those
+    rows), path [S,n] (strictly increasing, n at most 256), counts [S], all int32.  With
+    draft_verify's path and counts that leaves the accepted tokens in the cache.
+    new_seq_lens [S] int32, if given, receives seq_lens + counts; it is returned.
+    """
+    if _torch is None:
+        _load_torch()
+    _first(seq_lens)
+    device = seq_lens.device
+    kp, shape = _pools("k_pool", k_pool, device)
+    vp, v_shape = _pools("v_pool", v_pool, device)
+    if shape != v_shape or len(kp) != len(vp):
+        raise ValueError("k_pool and v_pool must have the same layers and shapes")
+    if not kp:
+        raise ValueError("at least one layer is needed")
+    if seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be a 1-d tensor")
+    S = seq_lens.shape[0]
+    _check("seq_lens", seq_lens, _i32, (S,), device)
+    _check_table(block_table, S, device)
+    _check("counts", counts, _i32, (S,), device)
+    if not isinstance(path, _Tensor) or path.dim() != 2:
+        raise ValueError("path must be a 2-d tensor")
+    _check("path", path, _i32, (S, path.shape[1]), device)
+    if new_seq_lens is not None:
+        _check("new_seq_lens", new_seq_lens, _i32, (S,), device)
+    NB, Hkv, bs, D = shape
+    _check_sizes(S=S, n=path.shape[1], NB=NB, Hkv=Hkv, layers=len(kp))
+    _require_cuda(device)
+    array = ctypes.c_void_p * len(kp)
+    with _On(device, stream) as handle:
+        st = (_lib or lib()).paged_kv_keep(
+            array(*kp), array(*vp), len(kp), block_table.data_ptr(), seq_lens.data_ptr(),
+            path.data_ptr(), counts.data_ptr(), _ptr(new_seq_lens), bs, S, path.shape[1], Hkv, D,
+            block_table.shape[1], NB, handle)
+    if st != ATTN_OK:
+        raise GbAttnError("paged_kv_keep", st)
+    return new_seq_lens
 
 
 def test_set_failure(wait_limit_ns: int = 0, withhold_copy: bool = False) -> None:

@@ -17,6 +17,7 @@
 #include "internal.h"
 #include "norm_rope.h"
 #include "ptx.cuh"
+#include "tree.h"
 
 namespace gbattn {
 
@@ -64,7 +65,8 @@ int device_state(DeviceState** out) {
       st.status = ATTN_ERR_UNSUPPORTED;  // kernels are built for sm_103a only
     } else if (prepare_attn_fwd() != cudaSuccess || prepare_paged_decode() != cudaSuccess ||
                prepare_kv_cache() != cudaSuccess || prepare_kv4_decode() != cudaSuccess ||
-               prepare_norm_rope() != cudaSuccess ||
+               prepare_norm_rope() != cudaSuccess || prepare_tree_attn() != cudaSuccess ||
+               prepare_draft_verify() != cudaSuccess ||
                cudaGetSymbolAddress(reinterpret_cast<void**>(&st.flags), g_flags_word) !=
                    cudaSuccess) {
       st.status = ATTN_ERR_CUDA;

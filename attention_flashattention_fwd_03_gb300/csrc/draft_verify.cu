@@ -1,0 +1,458 @@
+// draft_verify.cu -- which drafted tokens the target model accepts, from given random
+// numbers, and the token after them.
+//
+// At a node with the target's row p and the draft's row q (from which its children were
+// drawn independently), with w = p, W = 1: child x stands if u q(x) W < w(x), i.e. with
+// probability min(1, (w(x) / W) / q(x)).  When it falls, w becomes max(w - W q, 0) and W
+// its sum: w / W is the distribution that what is still to be drawn has to follow (the
+// residual), kept without divisions.  The last token is drawn from w by where u times its
+// sum falls in the running sum.
+//
+// A token hangs on which side of a border a random number lies, so sums must not depend on
+// an order and must be finer than fp32: probabilities are held as multiples of 2^-62 in 64-bit
+// integers (an fp32 from 2^-38 up exactly), whose sums are exact whatever the order, and
+// products of two are taken in 128 bits.  The kernel is bound by the rows that it reads; 64-bit
+// floating-point arithmetic, of which this GPU does two operations a clock and SM, would
+// be ten times slower than they are.
+//
+// A cluster of CTAs takes a request.  CTA 0 leads: it reads the tree and, for all nodes at
+// once, the two probabilities that a test of the node would need, and walks down the tree
+// in registers and shared memory.  Only where a child falls, or at the end, all V values of
+// a row (or two) are needed: CTA c then sums tokens [c chunk, (c + 1) chunk), a warp a tile
+// of them at a time, keeps the tiles' sums, and puts its sum into every CTA's shared memory.
+// The leader tells the others what to do next, so the control flow, and with it the number
+// of cluster barriers that each CTA meets, is decided in one place.  The last token's CTA is found from the CTAs' sums,
+// its tile from the tiles' sums, and only that tile is read again.
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+#include "gbattn.h"
+#include "ptx.cuh"
+#include "tree.h"
+
+namespace gbattn {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxNodes = GBATTN_TREE_MAX_NODES;
+static_assert(kThreads == kMaxNodes, "a thread a node");
+constexpr int kMaxCtas = 16;   // of a cluster
+constexpr int kPerLane = 16;   // values of a row that a lane reads at once
+constexpr int kSpan = 32 * kPerLane;
+constexpr int kMaxTiles = 256;
+
+using u64 = unsigned long long;
+constexpr u64 kOne = 1ull << 62;
+
+// A probability (or random number) as a multiple of 2^-62; NaN and negative values are 0.
+__device__ __forceinline__ u64 fixed(float v) {
+  return __float2ull_rz(__saturatef(v) * 0x1p62f);
+}
+__device__ __forceinline__ float value(float v) { return v; }
+__device__ __forceinline__ float value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+
+// a b 2^-62, rounded down.
+__device__ __forceinline__ u64 product(u64 a, u64 b) { return (__umul64hi(a, b) << 2) | ((a * b) >> 62); }
+__device__ __forceinline__ u64 minus(u64 a, u64 b) { return a > b ? a - b : 0; }
+// Whether a b 2^-62 < c, exactly.
+__device__ __forceinline__ bool product_below(u64 a, u64 b, u64 c) {
+  const u64 hi = __umul64hi(a, b), lo = a * b;
+  return hi < c >> 2 || (hi == c >> 2 && lo < c << 62);
+}
+
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ u64 warp_prefix(u64 v) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Address of this CTA's shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void store_remote(uint32_t a, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+
+// What the leader has the cluster do.
+enum : int { kDone, kScan, kRest, kDraw };  // rest: sum of what is left once W q is taken off
+struct Command {
+  int op, node, level, count;
+  u64 total;  // kRest: W; kDraw: where the random number falls in the running sum
+};
+static_assert(sizeof(Command) == 24, "three words");
+
+// w of one token at `level` falls, and less W q if `rest`.
+__device__ __forceinline__ u64 left(u64 w, u64 q, const u64* W, int level, bool rest) {
+  const int n = level + (rest ? 1 : 0);
+  for (int i = 0; i < n; ++i) w = minus(w, i == 0 ? q : product(q, W[i]));  // W[0] = 1
+  return w;
+}
+
+template <typename T, bool DRAWN>
+__global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyParams p) {
+  __shared__ int parent[kMaxNodes], token[kMaxNodes], path[kMaxNodes];
+  __shared__ u64 chance[kMaxNodes], pv[kMaxNodes], qv[kMaxNodes];  // u, p and q of every node
+  __shared__ u64 W[kMaxNodes];           // sums of w by level
+  __shared__ u64 sums[kMaxTiles];        // of this CTA's tiles
+  __shared__ u64 totals[kMaxCtas];       // of all CTAs
+  __shared__ u64 part[kWarps];
+  __shared__ Command cmd;
+  __shared__ u64 gone[DRAWN ? 1 : kMaxNodes], gone_w[DRAWN ? 1 : kMaxNodes];  // fallen tokens
+  const uint32_t ctas = cluster_size(), rank = cluster_rank();
+  const int r = blockIdx.x / ctas;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  cluster_arrive();  // every CTA's shared memory may be written once all are past the wait
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  const T* p_rows = static_cast<const T*>(p.p) + r * p.p_stride[0];
+  const T* q_rows = DRAWN ? static_cast<const T*>(p.q) + r * p.q_stride[0] : nullptr;
+  int n = 0;
+  if (rank == 0) {
+    n = p.tree_lens ? p.tree_lens[r] : p.Tn;
+    const bool bad_n = n < 0 || n > p.Tn;
+    if (bad_n) n = 0;
+    const size_t row = static_cast<size_t>(r) * p.Tn;
+    bool bad = false;
+    if (tid < n) {
+      const int up = p.parents[row + tid], x = p.tokens[row + tid];
+      parent[tid] = up;
+      token[tid] = x;
+      chance[tid] = fixed(p.uniforms[row + tid]);
+      bad = up < -1 || up >= tid;
+      u64 a = 0, b = 0;
+      if (!bad && up >= 0 && x >= 0 && x < p.V) {
+        a = fixed(value(p_rows[up * p.p_stride[1] + x]));
+        if (DRAWN) b = fixed(value(q_rows[up * p.q_stride[1] + x]));
+      }
+      pv[tid] = a;
+      qv[tid] = DRAWN ? b : kOne;
+    }
+    const bool bad_tree = __syncthreads_or(bad);
+    if ((bad_n || bad_tree) && tid == 0) raise_flag(p.flags, bad_n ? DEVFLAG_BAD_SEQLEN : DEVFLAG_BAD_TREE);
+    if (bad_tree) n = 0;
+    if (tid == 0) path[0] = 0;
+  }
+  cluster_wait();
+
+  // the leader's walk (warp 0 of CTA 0)
+  int cur = 0, at = 0, level = 0, fallen = 0, count = n > 0 ? 1 : 0;
+  u64 total = kOne;
+  enum { kNothing, kRested, kSummed, kLast } waiting = kNothing;
+  bool summed = false;  // the last sums are those of the present w
+  int op = kDone, s_level = 0, s_node = 0;
+  bool s_rest = false;
+  const int c0 = rank * p.chunk, c1 = min(p.V, c0 + p.chunk);  // (chunk * ctas < 2^31)
+
+  for (;;) {
+    if (rank == 0 && warp == 0) {
+      Command next{kDone, cur, 0, count, 0};
+      u64 all = 0;
+      if (waiting != kNothing) {
+        all = warp_sum(lane < static_cast<int>(ctas) ? totals[lane] : 0);
+        summed = true;
+        if (waiting == kRested) {
+          if (all > 0) {
+            total = all;
+            ++level;
+          } else {
+            summed = false;
+          }
+        }
+      }
+      bool again = waiting == kSummed;  // child `at` has been found to fall already
+      waiting = kNothing;
+      if (n > 0) {
+        for (;;) {
+          if (!again) {
+            // the next child of the node reached
+            int found = -1;
+            for (int b = (at + 1) & ~31; b < n && found < 0; b += 32) {
+              const int i = b + lane;
+              const unsigned hit = __ballot_sync(0xffffffffu, i > at && i < n && parent[i] == cur);
+              if (hit) found = b + __ffs(hit) - 1;
+            }
+            if (found < 0) {
+              next.op = summed ? kDraw : kScan;
+              waiting = kLast;
+              break;
+            }
+            at = found;
+          }
+          u64 w = pv[at];
+          const u64 q = qv[at];
+          if (DRAWN) {
+            w = left(w, q, W, level, false);
+          } else {
+            const u64 x = static_cast<u64>(token[at]);
+            bool hit = false;
+            for (int i = lane; i < fallen; i += 32) hit |= gone[i] == x;
+            if (__any_sync(0xffffffffu, hit)) w = 0;
+          }
+          if (!again && product_below(chance[at], product(q, total), w)) {
+            if (lane == 0) path[count] = at;
+            ++count;
+            cur = at;
+            level = fallen = 0;
+            total = kOne;
+            summed = false;
+            continue;
+          }
+          if (DRAWN) {
+            next.op = kRest;
+            waiting = kRested;
+            break;
+          }
+          if (!summed) {
+            next.op = kScan;
+            waiting = kSummed;
+            break;
+          }
+          // without a draft the token itself is what falls
+          again = false;
+          u64 out = 0;
+          for (int i = lane; i < fallen; i += 32) out += gone_w[i];
+          all = warp_sum(lane < static_cast<int>(ctas) ? totals[lane] : 0) - warp_sum(out);
+          if (all > w) {
+            total = all - w;
+            if (w > 0) {
+              if (lane < static_cast<int>(ctas)) {
+                store_remote(remote(&gone[fallen], lane), static_cast<u64>(token[at]));
+                store_remote(remote(&gone_w[fallen], lane), w);
+              }
+              __syncwarp();
+              ++fallen;
+            }
+          }
+        }
+      }
+      next.node = cur;
+      next.count = count;
+      next.level = DRAWN ? level : fallen;
+      next.total = total;
+      if (next.op == kDraw) {
+        all = warp_sum(lane < static_cast<int>(ctas) ? totals[lane] : 0);
+        if (!DRAWN) {
+          u64 out = 0;
+          for (int i = lane; i < fallen; i += 32) out += gone_w[i];
+          all -= warp_sum(out);
+        }
+        next.total = product(chance[0], all);
+        if (all == 0) next.op = kDone;
+        if (lane == 0 && all == 0) raise_flag(p.flags, DEVFLAG_NO_MASS);
+      }
+      if (lane < static_cast<int>(ctas)) {
+        u64 words[3];
+        memcpy(words, &next, sizeof words);
+        const uint32_t to = remote(&cmd, lane);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) store_remote(to + 8 * i, words[i]);
+      }
+    }
+    cluster_arrive();
+    cluster_wait();
+    const Command c = cmd;
+    op = c.op;
+    if (op == kDone || op == kDraw) break;
+
+    // ---- sums of this CTA's tokens ----
+    s_level = DRAWN ? c.level : 0;
+    s_node = c.node;
+    s_rest = op == kRest;
+    if (s_rest) {
+      if (tid == 0) W[c.level] = c.total;
+      __syncthreads();
+    }
+    const T* pr = p_rows + s_node * p.p_stride[1];
+    const T* qr = DRAWN ? q_rows + s_node * p.q_stride[1] : nullptr;
+    const bool both = DRAWN && (s_rest || s_level > 0);
+    u64 mine = 0;
+    for (int t = warp; c0 + t * p.tile < c1; t += kWarps) {
+      u64 sum = 0;
+      const int end = min(c1, c0 + (t + 1) * p.tile);
+      for (int b = c0 + t * p.tile; b < end; b += kSpan) {
+        T a[kPerLane], d[kPerLane];
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+          const int i = b + 32 * k + lane;
+          a[k] = d[k] = 0;
+          if (i < end) {
+            a[k] = pr[i];
+            if (both) d[k] = qr[i];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+          const u64 w = fixed(value(a[k]));
+          sum += both ? left(w, fixed(value(d[k])), W, s_level, s_rest) : w;
+        }
+      }
+      sum = warp_sum(sum);
+      if (lane == 0) sums[t] = sum;
+      mine += sum;
+    }
+    if (lane == 0) part[warp] = mine;
+    __syncthreads();
+    if (warp == 0) {
+      mine = warp_sum(lane < kWarps ? part[lane] : 0);
+      if (lane < static_cast<int>(ctas)) store_remote(remote(&totals[rank], lane), mine);
+    }
+    cluster_arrive();
+    cluster_wait();
+  }
+
+  // ---- results ----
+  const Command c = cmd;
+  const size_t row = static_cast<size_t>(r) * p.Tn;
+  if (rank == 0) {
+    for (int j = tid; j < p.Tn; j += kThreads) {
+      p.path[row + j] = j < c.count ? path[j] : -1;
+      if (op == kDone || j != c.count - 1)  // (the last token is written by its CTA)
+        p.tokens_out[row + j] = j < c.count - 1 ? token[path[j + 1]] : -1;
+    }
+    if (tid == 0) p.counts[r] = c.count;
+  }
+  if (op != kDraw || warp != 0) return;
+  // the CTA whose tokens the running sum passes c.total in
+  const int n_gone = DRAWN ? 0 : c.level;
+  u64 own = lane < static_cast<int>(ctas) ? totals[lane] : 0;
+  for (int i = 0; i < n_gone; ++i)
+    if (static_cast<int>(gone[i]) / p.chunk == lane) own -= gone_w[i];
+  u64 upto = warp_prefix(own);
+  const u64 begin = __shfl_sync(0xffffffffu, upto - own, rank);
+  const u64 stop = __shfl_sync(0xffffffffu, upto, rank);
+  if (c.total < begin || c.total >= stop) return;
+  u64 rest = c.total - begin;
+  // its tile
+  const int tiles = (c1 - c0 + p.tile - 1) / p.tile;
+  int t = -1;
+  for (int b = 0; b < tiles && t < 0; b += 32) {
+    u64 s = b + lane < tiles ? sums[b + lane] : 0;
+    for (int i = 0; i < n_gone; ++i) {
+      const int x = static_cast<int>(gone[i]) - c0;
+      if (x >= 0 && x < p.chunk && x / p.tile == b + lane) s -= gone_w[i];
+    }
+    const u64 incl = warp_prefix(s);
+    const unsigned hit = __ballot_sync(0xffffffffu, rest < incl);
+    if (hit) {
+      t = b + __ffs(hit) - 1;
+      rest -= __shfl_sync(0xffffffffu, incl - s, __ffs(hit) - 1);
+    } else {
+      rest -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  // its token: a lane's values are neighbours
+  const T* pr = p_rows + s_node * p.p_stride[1];
+  const T* qr = DRAWN ? q_rows + s_node * p.q_stride[1] : nullptr;
+  const bool both = DRAWN && (s_rest || s_level > 0);
+  const int end = min(c1, c0 + (t + 1) * p.tile);
+  for (int b = c0 + t * p.tile; t >= 0 && b < end; b += kSpan) {
+    u64 w[kPerLane], sum = 0;
+    const int i0 = b + kPerLane * lane;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      w[k] = 0;
+      if (i0 + k < end) {
+        w[k] = fixed(value(pr[i0 + k]));
+        if (both) w[k] = left(w[k], fixed(value(qr[i0 + k])), W, s_level, s_rest);
+        for (int i = 0; i < n_gone; ++i)
+          if (gone[i] == static_cast<u64>(i0 + k)) w[k] = 0;
+      }
+      sum += w[k];
+    }
+    const u64 incl = warp_prefix(sum);
+    const unsigned hit = __ballot_sync(0xffffffffu, rest < incl);
+    if (hit) {
+      if (lane == __ffs(hit) - 1) {
+        u64 s = incl - sum;
+        int x = i0 + kPerLane - 1;
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+          const bool before = s <= rest;
+          s += w[k];
+          if (before && s > rest) x = i0 + k;
+        }
+        p.tokens_out[row + c.count - 1] = x;
+      }
+      return;
+    }
+    rest -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+template <typename T, bool DRAWN>
+cudaError_t launch(const VerifyParams& p, int ctas, cudaStream_t stream) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.S) * ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, draft_verify_kernel<T, DRAWN>, p);
+}
+
+}  // namespace
+
+cudaError_t prepare_draft_verify() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](const void* fn) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  };
+  set(reinterpret_cast<const void*>(draft_verify_kernel<float, false>));
+  set(reinterpret_cast<const void*>(draft_verify_kernel<float, true>));
+  set(reinterpret_cast<const void*>(draft_verify_kernel<uint16_t, false>));
+  set(reinterpret_cast<const void*>(draft_verify_kernel<uint16_t, true>));
+  return e;
+}
+
+cudaError_t launch_draft_verify(VerifyParams p, bool bf16, int num_sms, cudaStream_t stream) {
+  if (p.S <= 0) return cudaSuccess;
+  int ctas = p.S * 8 <= num_sms ? kMaxCtas : 8;
+  while (ctas > 1 && p.V <= ctas / 2 * kSpan * kWarps) ctas /= 2;
+  auto up = [](long long x, long long m) { return (x + m - 1) / m * m; };
+  const long long share = (static_cast<long long>(p.V) + ctas - 1) / ctas;
+  p.tile = static_cast<int>(up((share + kMaxTiles - 1) / kMaxTiles, kSpan));
+  p.chunk = static_cast<int>(up(share, p.tile));
+  if (bf16)
+    return p.q ? launch<uint16_t, true>(p, ctas, stream) : launch<uint16_t, false>(p, ctas, stream);
+  return p.q ? launch<float, true>(p, ctas, stream) : launch<float, false>(p, ctas, stream);
+}
+
+}  // namespace gbattn

@@ -18,6 +18,8 @@ enum : unsigned {
   DEVFLAG_BAD_SEQLEN = 1u << 1,   // decode: seq_len < 0 or beyond the table / max_seq_len
   DEVFLAG_BAD_BLOCK = 1u << 2,    // decode: block id outside the pool
   DEVFLAG_BAD_POSITION = 1u << 3, // rotation: position outside the table
+  DEVFLAG_BAD_TREE = 1u << 4,     // a parent not before its child, a path that does not increase
+  DEVFLAG_NO_MASS = 1u << 5,      // a token to be drawn from a distribution without mass
 };
 
 // The flag word lives in the library's one device-global (api.cu); kernels get

@@ -191,8 +191,9 @@ int paged_attn_decode_noalloc(const void *q, const void *k_pool, const void *v_p
  * kernel of this library on that device stays set until the next call of this
  * function, which reports and clears it for everyone.  *flags (if not NULL) receives the raw bits: 1 = a bounded wait in
  * a kernel timed out, 2 = a decode request had an invalid length, 4 = a decode
- * block id was out of range, 8 = a position lay outside the rotation table.  Returns
- * ATTN_ERR_DEVICE if any bit was set,
+ * block id was out of range, 8 = a position lay outside the rotation table, 16 = a tree or
+ * a path was invalid, 32 = a token was to be drawn from a distribution without mass.
+ * Returns ATTN_ERR_DEVICE if any bit was set,
  * ATTN_ERR_CUDA if the synchronisation failed, else ATTN_OK.
  */
 int attn_device_status(unsigned int *flags);
@@ -435,6 +436,135 @@ int paged_kv4_attn_prefill(const void *q, const void *kv_pool, const int32_t *bl
                            int D, int max_blocks_per_seq, int num_pool_blocks, int max_kv_len,
                            int causal, float scale, void *o, float *lse, void *workspace,
                            size_t workspace_bytes, void *stream);
+
+/*
+ * Trees of drafted tokens.  A step of decoding with drafted tokens appends the nodes of a
+ * tree behind each request's cache (paged_qkv_append or paged_kv_append; a node's position
+ * for its rotation is the request's length + the node's depth), attends to them with
+ * paged_attn_tree, decides with draft_verify which of them the target model accepts, and
+ * moves the accepted nodes' rows together with paged_kv_keep.
+ *
+ * A tree has at most GBATTN_TREE_MAX_NODES nodes.  parents [num_seqs, Tn] int32 gives the
+ * parent of each node, -1 for a root; a parent comes before its children (parents[r][i] <
+ * i).  A chain of drafts is the tree with parents[r][i] = i - 1.  tree_lens [num_seqs]
+ * int32 (NULL: Tn for every request) says how many of the Tn places hold nodes.
+ */
+#define GBATTN_TREE_MAX_NODES 256
+
+/*
+ * Bytes of scratch workspace paged_attn_tree needs for these sizes (0 for sizes that need
+ * none): partial outputs (D fp32) and LSEs of the query rows that share a cache cut between
+ * two CTAs.
+ */
+size_t paged_attn_tree_workspace_size(int num_seqs, int Tn, int Hq, int Hkv, int D,
+                                      int max_seq_len);
+
+/*
+ * paged_attn_tree -- attention of the nodes of a tree of drafted tokens per request against
+ * the paged cache: paged_attn_prefill with the tree in the place of the causal chunk.
+ *
+ *   q             [num_seqs, Hq, Tn, D] bf16: the nodes' queries
+ *   k_pool/v_pool [num_pool_blocks, Hkv, block_size, D] bf16
+ *   block_table   [num_seqs, max_blocks_per_seq] int32
+ *   seq_lens      [num_seqs] int32 (device): tokens cached before the tree, L_r; node i's
+ *                 key and value are at logical position L_r + i
+ *   parents       [num_seqs, Tn] int32, tree_lens [num_seqs] int32 or NULL: see above
+ *   o             [num_seqs, Hq, Tn, D] bf16 (written)
+ *   lse           [num_seqs, Hq, Tn] fp32 (written; may be NULL)
+ *   workspace     >= paged_attn_tree_workspace_size(...) bytes, 256-byte aligned (may be
+ *                 NULL where that is 0); no initialisation
+ *
+ * Node i sees the L_r cached tokens, its ancestors and itself.  Places past a tree's nodes
+ * get O = 0 and LSE = -inf; what is cached for them is not read.  max_seq_len bounds every
+ * L_r + tree_lens[r].  Tn is at most GBATTN_TREE_MAX_NODES, block_size 16, D 64 or 128; any
+ * number of query heads may share a KV head.  The split of the work depends on the lengths
+ * of the whole batch, never on the blocks' places: the same inputs give the same bits.
+ *
+ * Device-side checks: a length or a number of nodes outside its bounds, or L_r +
+ * tree_lens[r] outside [0, min(max_seq_len, max_blocks_per_seq * block_size)], makes that
+ * request's O and LSE NaN and sets flag bit 2; a parent outside [-1, i) does so with flag
+ * bit 16.  A block id outside the pool is read as block 0 and sets flag bit 4 (that
+ * request's output is then unspecified).  Slots past the tree may hold any bits.  A NaN in a
+ * value may reach O of every node of its request, of those too that do not see it.
+ */
+int paged_attn_tree(const void *q, const void *k_pool, const void *v_pool,
+                    const int32_t *block_table, const int32_t *seq_lens, const int32_t *parents,
+                    const int32_t *tree_lens, int block_size, int num_seqs, int Tn, int Hq,
+                    int Hkv, int D, int max_blocks_per_seq, int num_pool_blocks, int max_seq_len,
+                    float scale, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/*
+ * draft_verify -- which drafted tokens the target model accepts, and the token after them,
+ * so that what is put out is distributed as the target's own draws would be.
+ *
+ *   target_probs  [num_seqs, Tn, V] fp32 (prob_type 0) or bf16 (1): row i is the target's
+ *                 distribution of the token after node i
+ *   draft_probs   the same type, or NULL: row i is the distribution that node i's children
+ *                 were drawn from, independently.  NULL: they were put forward without a
+ *                 draw (the likeliest few, say)
+ *   *_strides     two HOST values, the strides of requests and of nodes in elements; the V
+ *                 probabilities of a row are contiguous
+ *   tokens        [num_seqs, Tn] int32: the nodes' tokens.  Node 0 is the token that the
+ *                 tree hangs from: it stands already, and its entry is not read
+ *   parents, tree_lens  as above
+ *   uniforms      [num_seqs, Tn] fp32 random numbers in [0, 1): number i > 0 decides on
+ *                 node i, number 0 draws the last token
+ *   tokens_out    [num_seqs, Tn] int32 (written): the accepted nodes' tokens, root left out,
+ *                 then the last token, then -1
+ *   path          [num_seqs, Tn] int32 (written): the accepted nodes, from node 0 down, then
+ *                 -1
+ *   counts        [num_seqs] int32 (written): how many nodes stand, and so how many tokens
+ *                 are put out
+ *
+ * From node 0 on, with w = p (the target's row of the node reached), W = 1: the node's
+ * children are tried in the order of their numbers.  Child i with token x stands if
+ * u_i q(x) W < w(x) (q: the draft's row; without one q(x) = 1 and q = 0 elsewhere), and the
+ * search goes on from there.  If it falls, w becomes max(w - W q, 0) and W its sum, unless
+ * that is 0, in which case both stay.  Where no child stands, the last token is the first x
+ * whose w(0) + .. + w(x) is above u_0 times the sum of w (-1 and flag bit 32 if the sum is
+ * 0).  Probabilities and random numbers are taken to [0, 1] (NaN as 0) and held as multiples
+ * of 2^-62, so sums do not depend on an order; a row may sum to anything below 4.  Tokens
+ * outside [0, V) have probability 0.
+ *
+ * A request without nodes gets count 0.  Device-side checks: a number of nodes outside
+ * [0, Tn] (flag bit 2) or a parent outside [-1, i) (flag bit 16) gives count 0 as well.
+ * Tn is at most GBATTN_TREE_MAX_NODES; strides are non-negative.
+ */
+int draft_verify(const void *target_probs, const void *draft_probs, const int64_t *target_strides,
+                 const int64_t *draft_strides, int prob_type, const int32_t *tokens,
+                 const int32_t *parents, const float *uniforms, const int32_t *tree_lens,
+                 int num_seqs, int Tn, int V, int32_t *tokens_out, int32_t *path, int32_t *counts,
+                 void *stream);
+
+/*
+ * paged_kv_keep -- keeps chosen rows behind each request's cache and moves them together:
+ * the row at logical position L_r + path[r][j] goes to L_r + j for every j < counts[r], key
+ * and value, every KV head, in every layer.
+ *
+ *   k_pools, v_pools  HOST arrays of num_layers device pointers, each to a pool
+ *                 [num_pool_blocks, Hkv, block_size, D] bf16 (changed in place); the pools
+ *                 must not overlap
+ *   block_table   [num_seqs, max_blocks_per_seq] int32, shared by the layers
+ *   seq_lens      [num_seqs] int32 (device): L_r, the tokens before those rows
+ *   path          [num_seqs, path_len] int32: strictly increasing (entries past counts[r]
+ *                 are not read)
+ *   counts        [num_seqs] int32, at most path_len
+ *   new_seq_lens  [num_seqs] int32 (may be NULL): receives L_r + counts[r]; it must not
+ *                 overlap another operand
+ *
+ * Rows that stay in place are not touched, nor is any other row.  path_len is at most
+ * GBATTN_TREE_MAX_NODES.  Device-side checks: a length or count out of bounds, or a last row
+ * past max_blocks_per_seq * block_size (flag bit 2), or a path that does not increase (flag
+ * bit 16) skips the request and writes L_r unchanged to new_seq_lens; a move from or to a
+ * block id outside the pool is skipped and sets flag bit 4.  Two requests may share blocks
+ * only below their lengths.
+ */
+int paged_kv_keep(void *const *k_pools, void *const *v_pools, int num_layers,
+                  const int32_t *block_table, const int32_t *seq_lens, const int32_t *path,
+                  const int32_t *counts, int32_t *new_seq_lens, int block_size, int num_seqs,
+                  int path_len, int Hkv, int D, int max_blocks_per_seq, int num_pool_blocks,
+                  void *stream);
 
 /*
  * Test hook for the kernels' failure detection (not for production use).
