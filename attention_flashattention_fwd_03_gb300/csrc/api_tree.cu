@@ -73,12 +73,21 @@ GBATTN_API int paged_attn_tree(const void* q, const void* k_pool, const void* v_
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
     return ATTN_ERR_INVALID_ARG;
   DeviceState* ds = nullptr;
-  const int st = device_state(&ds);
+  int st = device_state(&ds);
   if (st != ATTN_OK) return st;
+  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+  if ((st = encoder(&enc)) != ATTN_OK) return st;
+  CUtensorMap tmQ, tmK, tmV;
+  const uint64_t row_bytes = static_cast<uint64_t>(D) * 2, rows = static_cast<uint64_t>(Hq / Hkv) * Tn;
+  const uint64_t q_strides[2] = {row_bytes, row_bytes * rows}, pool_strides[1] = {row_bytes};
+  const uint32_t q_box[3] = {64, 128, 1}, pool_box[2] = {64, 16};
+  const uint64_t dq[3] = {static_cast<uint64_t>(D), rows, static_cast<uint64_t>(num_seqs) * Hkv};
+  const uint64_t dpool[2] = {static_cast<uint64_t>(D),
+                             static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size};
+  if ((st = encode_bf16(enc, &tmQ, q, 3, dq, q_strides, q_box)) != ATTN_OK) return st;
+  if ((st = encode_bf16(enc, &tmK, k_pool, 2, dpool, pool_strides, pool_box)) != ATTN_OK) return st;
+  if ((st = encode_bf16(enc, &tmV, v_pool, 2, dpool, pool_strides, pool_box)) != ATTN_OK) return st;
   TreeParams p{};
-  p.q = q;
-  p.k_pool = k_pool;
-  p.v_pool = v_pool;
   p.block_table = block_table;
   p.seq_lens = seq_lens;
   p.parents = parents;
@@ -98,7 +107,8 @@ GBATTN_API int paged_attn_tree(const void* q, const void* k_pool, const void* v_
   p.flags = ds->flags;
   p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   p.withhold_copy = g_withhold_copy.load(std::memory_order_relaxed);
-  return launch_tree_attn(p, ds->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_tree_attn(tmQ, tmK, tmV, p, workspace, ds->num_sms,
+                          static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ATTN_OK
              : ATTN_ERR_CUDA;
 }

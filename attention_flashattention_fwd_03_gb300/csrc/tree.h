@@ -11,8 +11,6 @@
 namespace gbattn {
 
 struct TreeParams {
-  const void* q;               // [S, Hq, Tn, D] bf16
-  const void *k_pool, *v_pool; // [num_pool_blocks, Hkv, 16, D] bf16
   const int32_t* block_table;  // [S, max_blocks]
   const int32_t* seq_lens;     // [S]: tokens before the tree
   const int32_t* parents;      // [S, Tn]
@@ -32,7 +30,11 @@ struct TreeParams {
 
 size_t tree_attn_workspace_bytes(int S, int Tn, int Hq, int Hkv, int D, int max_seq_len);
 cudaError_t prepare_tree_attn();
-cudaError_t launch_tree_attn(const TreeParams& p, int num_sms, cudaStream_t stream);
+// tmQ is a 3-D map over [S * Hkv, Hq / Hkv * Tn, D] with a 64 x 128 x 1 box, tmK and tmV are the
+// decode kernels' 2-D maps over the pools (64 x 16 box); all with the 128-byte swizzle.
+cudaError_t launch_tree_attn(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                             const TreeParams& p, void* workspace, int num_sms,
+                             cudaStream_t stream);
 
 struct VerifyParams {
   const void *p, *q;           // rows of V probabilities; q may be nullptr

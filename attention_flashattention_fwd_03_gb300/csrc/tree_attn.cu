@@ -1,6 +1,36 @@
-// tree_attn.cu -- attention of the nodes of trees of drafted tokens over the paged cache.
+// tree_attn.cu -- attention of the nodes of trees of drafted tokens over the paged cache,
+// sm_103a.
+//
+// A tree's queries share almost all of their keys: the L cached tokens, which every node
+// sees, and up to 256 nodes behind them, of which node i sees its ancestors and itself.  So
+// the query heads of a KV head and the nodes are rows of one matrix product ([Hq, Tn, D] keeps
+// the group * Tn rows of a KV head together), every key and value is read once for all of
+// them, and only the last tiles of 128 keys need a mask, a bit a (row, node).
+//
+// The work is a sequence of segments, (request, KV head, 256 rows) each, of steps of 128
+// keys; a CTA an SM takes an equal range of it, so that one long cache and many short ones
+// alike keep every SM busy whatever the lengths.  A segment that is cut between CTAs is put
+// together from partial outputs by the merge kernel; whole ones are written at once.  Where
+// all caches are short, CTAs take whole segments in turn and there is no merge kernel and no
+// workspace.
+//
+// A CTA is a pipeline of warps, as in attn_fwd.cu:
+//   warp 0      producer: Q tiles, then K and V tiles through the block table (16-row TMA
+//               boxes) into a ring
+//   warp 1      issues the products: S = Q K^T into tensor memory, O += P V with P from
+//               tensor memory
+//   warp 2      ancestors of the segment's tree, as bit masks
+//   warps 4-7, 8-11  softmax, a row a thread, of two chains of tiles that alternate on the
+//               tensor cores
+// Up to 128 rows the two chains take every other key tile of the one row tile, each with its
+// own maximum, sum and output, and are joined when the piece ends; above, they take a row tile
+// each over the same keys.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
+#include "api.h"
+#include "attn_tile.cuh"
 #include "gbattn.h"
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -10,103 +40,1003 @@ namespace gbattn {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int BM = 128;  // query rows of a tile
+constexpr int BN = 128;  // keys of a step
+constexpr int kBS = kPagedBlock;
+constexpr int kThreads = 384;
+constexpr int kMaxNodes = GBATTN_TREE_MAX_NODES;
+constexpr int kWords = kMaxNodes / 32;
+constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by > 2^8
+constexpr int kDirectSteps = 4;      // caches of so many steps at most are not cut
+// (the block launches with 168 registers a thread)
+constexpr int kRegsLaunch = 168, kRegsWg0 = 104, kRegsSoftmax = 200;
+static_assert(kRegsWg0 + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split exceeds the launch");
+constexpr float kNan = __builtin_nanf("");
 
-__device__ __forceinline__ float bf16_value(uint16_t v) {
-  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+struct Plan {  // this CTA's range of steps
+  int lo, n;   // first step and how many
+  int r, s, j; // the first one's request, segment of the request and step of the segment
+  int share, extra;
+};
+
+// A segment that is cut after range k and begins in it: request, segment of the request,
+// number of pieces and the first one's slot (the others are their ranges' first slots).
+struct Cut {
+  int r, s, pieces, slot;
+};
+
+struct Work {  // what the kernels share besides the caller's operands
+  TreeParams p;
+  float* part_o;    // [2 grid][unit_rows][D]
+  float* part_lse;  // [2 grid][unit_rows]
+  Cut* cut;         // [grid]
+  int group_rows;   // query rows of a KV head
+  int pairs;        // units of rows of a KV head
+  int segs;         // Hkv * pairs
+  int unit_rows;    // rows of a partial output
+  int direct;       // CTAs take whole segments in turn
+};
+
+template <int D, bool SPLIT>
+struct Cfg {
+  static constexpr int KB = D / 64;              // 64-column (128-byte) boxes of a row
+  static constexpr int BOX_BYTES = BM * 128;
+  static constexpr int TILE_BYTES = BM * D * 2;
+  static constexpr int NQ = SPLIT ? 1 : 2;       // row tiles
+  static constexpr int NSLOT = D == 64 ? 8 : (SPLIT ? 5 : 4);
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_RING = NQ * TILE_BYTES;
+  static constexpr int OFF_MASK = OFF_RING + NSLOT * TILE_BYTES;  // [2][kWords][kMaxNodes]
+  static constexpr int OFF_UP = OFF_MASK + 2 * kWords * kMaxNodes * 4;
+  static constexpr int OFF_JOIN = OFF_UP + kMaxNodes * 4;         // [2][BM] float2: maximum and sum
+  static constexpr int OFF_BAR = OFF_JOIN + 2 * BM * 8;
+  static constexpr int NBAR = 2 + 2 * NSLOT + 6 + 1 + 4 + 2;
+  static constexpr int OFF_PLAN = OFF_BAR + NBAR * 8;
+  static constexpr int OFF_SUMS = OFF_PLAN + sizeof(Plan) + 4;    // [12] ints
+  static constexpr int OFF_MISC = (OFF_SUMS + 48 + 15) & ~15;     // TMEM address, abort, bad tree [2]
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;         // + slack for 1024-byte alignment
+  static constexpr uint32_t TMEM_COLS = 512;
+  // TMEM columns: S_0 [0,128), S_1 [128,256), O_0 and O_1 from 256 (D each).  P_i (bf16
+  // pairs, 64 columns) overwrites the upper half of S_i.
+  __device__ static constexpr uint32_t s_col(int i) { return 128u * i; }
+  __device__ static constexpr uint32_t p_col(int i) { return 128u * i + 64u; }
+  __device__ static constexpr uint32_t o_col(int i) { return 256u + static_cast<uint32_t>(D) * i; }
+};
+static_assert(Cfg<128, true>::SMEM_BYTES <= 232448 && Cfg<128, false>::SMEM_BYTES <= 232448,
+              "shared memory budget");
+
+template <int D, bool SPLIT>
+struct Bars {
+  using C = Cfg<D, SPLIT>;
+  uint32_t base;
+  __device__ uint32_t at(int i) const { return base + 8 * i; }
+  __device__ uint32_t q_full() const { return at(0); }
+  __device__ uint32_t q_empty() const { return at(1); }
+  __device__ uint32_t slot_full(int s) const { return at(2 + s); }
+  __device__ uint32_t slot_empty(int s) const { return at(2 + C::NSLOT + s); }
+  __device__ uint32_t s_full(int i) const { return at(2 + 2 * C::NSLOT + i); }
+  __device__ uint32_t s_free(int i) const { return at(4 + 2 * C::NSLOT + i); }
+  __device__ uint32_t p_full(int i) const { return at(6 + 2 * C::NSLOT + i); }
+  __device__ uint32_t teardown() const { return at(8 + 2 * C::NSLOT); }
+  __device__ uint32_t mask_full(int b) const { return at(9 + 2 * C::NSLOT + b); }
+  __device__ uint32_t mask_empty(int b) const { return at(11 + 2 * C::NSLOT + b); }
+  __device__ uint32_t joined(int i) const { return at(13 + 2 * C::NSLOT + i); }
+};
+
+// A request's sizes: tokens before the tree, nodes, and whether they are out of bounds (then
+// the request counts as empty).
+struct Sizes {
+  int L, n;
+  bool bad;
+  __device__ int keys() const { return L + n; }
+  __device__ int steps() const { return max(1, (L + n + BN - 1) / BN); }  // (empty: one, to be written)
+};
+__device__ __forceinline__ Sizes sizes_of(const TreeParams& p, int r) {
+  Sizes z{p.seq_lens[r], p.tree_lens ? p.tree_lens[r] : p.Tn, false};
+  const long long keys = static_cast<long long>(z.L) + z.n;
+  z.bad = z.L < 0 || z.n < 0 || z.n > p.Tn || keys > p.max_seq_len ||
+          keys > static_cast<long long>(p.max_blocks) * kBS;
+  if (z.bad) z.L = z.n = 0;
+  return z;
 }
 
-// One CTA a (request, query head, node); its warps take the keys in turn.
-template <int D>
-__global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p) {
-  constexpr int PER = D / 32;
-  __shared__ unsigned seen[GBATTN_TREE_MAX_NODES / 32];
-  __shared__ float part[kWarps][D], part_m[kWarps], part_l[kWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int node = blockIdx.x % p.Tn, rh = blockIdx.x / p.Tn;
-  const int r = rh / p.Hq, kvh = (rh - r * p.Hq) / (p.Hq / p.Hkv);
-  const int L = p.seq_lens[r], n = p.tree_lens ? p.tree_lens[r] : p.Tn;
-  const int32_t* parents = p.parents + static_cast<size_t>(r) * p.Tn;
-  const bool bad_len = L < 0 || n < 0 || n > p.Tn ||
-                       static_cast<long long>(L) + n > p.max_seq_len ||
-                       static_cast<long long>(L) + n > static_cast<long long>(p.max_blocks) * kPagedBlock;
-  bool bad_node = false;
-  for (int i = threadIdx.x; i < n && !bad_len; i += kThreads)
-    bad_node |= parents[i] < -1 || parents[i] >= i;
-  const bool bad_tree = __syncthreads_or(bad_node);
-  const bool bad = bad_len || bad_tree;
-  if (bad && threadIdx.x == 0) raise_flag(p.flags, bad_len ? DEVFLAG_BAD_SEQLEN : DEVFLAG_BAD_TREE);
-  if (threadIdx.x < GBATTN_TREE_MAX_NODES / 32) seen[threadIdx.x] = 0;
-  __syncthreads();
-  const bool live = !bad && node < n;
-  if (threadIdx.x == 0 && live)
-    for (int a = node; a >= 0; a = parents[a]) seen[a >> 5] |= 1u << (a & 31);
-  __syncthreads();
+// The part of a segment that a CTA takes.
+struct Piece {
+  Sizes z;
+  int r, kvh, pair;
+  int j0, n;          // first key tile and how many (0: no keys at all)
+  int slot;           // of its partial output; -1: the segment is whole
+  bool last;          // holds the segment's last tile
+  __device__ bool masked(int j) const { return (j + 1) * BN > z.L; }
+  __device__ bool tail() const { return n > 0 && masked(j0 + n - 1); }
+};
 
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + static_cast<size_t>(blockIdx.x) * D + lane * PER;
-  float x[PER], o[PER], m = -INFINITY, l = 0.f;
-  for (int i = 0; i < PER; ++i) {
-    x[i] = bf16_value(q[i]);
-    o[i] = 0.f;
+// Walks over this CTA's pieces; every role does so for itself.
+struct Walk {
+  const Work& w;
+  int left;  // steps, or (direct) the next segment
+  int r, s, j, index = 0;
+  Sizes z;
+  __device__ Walk(const Work& w_, const Plan& plan)
+      : w(w_), left(w_.direct ? static_cast<int>(blockIdx.x) : plan.n), r(w_.direct ? -1 : plan.r),
+        s(plan.s), j(plan.j) {
+    if (!w.direct && left > 0) z = sizes_of(w.p, r);
   }
-  const int keys = live ? L + node + 1 : 0;
-  for (int t = warp; t < keys; t += kWarps) {
-    if (t >= L && !(seen[(t - L) >> 5] >> ((t - L) & 31) & 1)) continue;
-    int row = paged_block_row(p.block_table, p.max_blocks, r, t / kPagedBlock, kvh, p.Hkv,
-                              p.num_pool_blocks);
-    if (row < 0) {
-      if (lane == 0) raise_flag(p.flags, DEVFLAG_BAD_BLOCK);
-      row = kvh * kPagedBlock;
+  __device__ bool next(Piece& x) {
+    if (w.direct) {
+      if (left >= w.p.S * w.segs) return false;
+      const int now = left / w.segs;
+      if (now != r) z = sizes_of(w.p, now);
+      r = now;
+      s = left - now * w.segs;
+      left += gridDim.x;
+      j = 0;
+    } else if (left <= 0) {
+      return false;
     }
-    const size_t at = static_cast<size_t>(row + t % kPagedBlock) * D + lane * PER;
-    const uint16_t* k = static_cast<const uint16_t*>(p.k_pool) + at;
-    const uint16_t* v = static_cast<const uint16_t*>(p.v_pool) + at;
-    float s = 0.f;
-    for (int i = 0; i < PER; ++i) s = fmaf(x[i], bf16_value(k[i]), s);
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const float mn = fmaxf(m, s);
-    const float al = ex2((m - mn) * p.scale_log2), e = ex2((s - mn) * p.scale_log2);
-    m = mn;
-    l = l * al + e;
-    for (int i = 0; i < PER; ++i) o[i] = o[i] * al + e * bf16_value(v[i]);
+    const int steps = z.steps();
+    const int n = w.direct ? steps : min(left, steps - j);
+    x.z = z;
+    x.r = r;
+    x.kvh = s / w.pairs;
+    x.pair = s - x.kvh * w.pairs;
+    x.j0 = j;
+    x.n = z.keys() > 0 ? n : 0;
+    x.last = j + n == steps;
+    x.slot = j == 0 && x.last ? -1 : 2 * static_cast<int>(blockIdx.x) + (index > 0 ? 1 : 0);
+    ++index;
+    if (!w.direct) {
+      left -= n;
+      j += n;
+      if (j == steps && left > 0) {
+        j = 0;
+        if (++s == w.segs) {
+          s = 0;
+          if (++r >= w.p.S) left = 0;  // (lengths changed under the kernel)
+          else z = sizes_of(w.p, r);
+        }
+      }
+    }
+    return true;
   }
-  for (int i = 0; i < PER; ++i) part[warp][lane * PER + i] = o[i];
-  if (lane == 0) {
-    part_m[warp] = m;
-    part_l[warp] = l;
+};
+
+// ---------------------------------------------------------------------------
+// producer warp
+// ---------------------------------------------------------------------------
+template <int D, bool SPLIT>
+__device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
+                              const CUtensorMap* tmV, const Work& w, const Plan& plan,
+                              uint32_t sbase, const Bars<D, SPLIT>& bar, volatile int* abort) {
+  using C = Cfg<D, SPLIT>;
+  const TreeParams& p = w.p;
+  const int lane = threadIdx.x & 31;
+  const uint32_t sQ = sbase + C::OFF_Q, sR = sbase + C::OFF_RING;
+  const unsigned long long lim = p.wait_limit_ns;
+  const uint64_t stream_policy = l2_policy_evict_first();
+  const bool once = w.pairs == 1;  // every K/V byte is read once
+  int rc = 0, uc = 0;
+  bool ok = true, last_q_issued = false;
+  Walk walk(w, plan);
+  Piece x;
+  while (ok && walk.next(x)) {
+    if (x.z.bad && lane == 0) raise_flag(p.flags, DEVFLAG_BAD_SEQLEN);
+    if (x.n == 0) continue;
+    if (!mbar_wait_warp(bar.q_empty(), (uc & 1) ^ 1, abort, p.flags, lim)) { ok = false; break; }
+    last_q_issued = !(p.withhold_copy && uc == 0);  // test hook: withhold the first Q
+    if (lane == 0 && last_q_issued) {
+      mbar_arrive_expect_tx(bar.q_full(), C::NQ * C::TILE_BYTES);
+#pragma unroll
+      for (int i = 0; i < C::NQ; ++i)
+#pragma unroll
+        for (int kb = 0; kb < C::KB; ++kb)
+          tma_load_3d(sQ + i * C::TILE_BYTES + kb * C::BOX_BYTES, tmQ, bar.q_full(), kb * 64,
+                      256 * x.pair + BM * i, x.r * p.Hkv + x.kvh);
+    }
+    ++uc;
+    const int blocks = (x.z.keys() + kBS - 1) / kBS;
+    // lane l < 8 reads the table entry of block l of a tile, one tile ahead of the copies
+    auto table_entry = [&](int j) -> int {
+      const int b = j * (BN / kBS) + lane;
+      return lane < BN / kBS && b < blocks
+                 ? p.block_table[static_cast<size_t>(x.r) * p.max_blocks + b]
+                 : 0;
+    };
+    int next_phys = table_entry(x.j0);
+    for (int j = x.j0; j < x.j0 + x.n && ok; ++j) {
+      const int nblk = min(BN / kBS, blocks - j * (BN / kBS));
+      int phys = next_phys, row = 0;
+      if (j + 1 < x.j0 + x.n) next_phys = table_entry(j + 1);
+      if (lane < nblk) {
+        if (phys < 0 || phys >= p.num_pool_blocks) {
+          raise_flag(p.flags, DEVFLAG_BAD_BLOCK);
+          phys = 0;
+        }
+        row = (phys * p.Hkv + x.kvh) * kBS;
+      }
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const CUtensorMap* map = kv == 0 ? tmK : tmV;
+        const int s = rc % C::NSLOT;
+        if (!mbar_wait_warp(bar.slot_empty(s), ((rc / C::NSLOT) & 1) ^ 1, abort, p.flags, lim)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = sR + s * C::TILE_BYTES;
+        // lane 0 posts the byte count first
+        if (lane == 0) mbar_arrive_expect_tx(bar.slot_full(s), nblk * kBS * D * 2);
+        __syncwarp();
+        if (lane < nblk) {
+#pragma unroll
+          for (int kb = 0; kb < C::KB; ++kb) {
+            if (once)
+              tma_load_2d_hint(dst + kb * C::BOX_BYTES + lane * kBS * 128, map, bar.slot_full(s),
+                               kb * 64, row, stream_policy);
+            else
+              tma_load_2d(dst + kb * C::BOX_BYTES + lane * kBS * 128, map, bar.slot_full(s),
+                          kb * 64, row);
+          }
+        }
+        __syncwarp();
+        ++rc;
+      }
+    }
   }
+  if (!ok && lane == 0) {
+    // Let the copies still in flight land before the CTA's shared memory goes away.
+    const unsigned long long quiet = 500000000ull;
+    for (int n = (rc > C::NSLOT ? rc - C::NSLOT : 0); n < rc; ++n)
+      mbar_wait_quiet(bar.slot_full(n % C::NSLOT), (n / C::NSLOT) & 1, quiet);
+    if (uc > 0 && last_q_issued) mbar_wait_quiet(bar.q_full(), (uc - 1) & 1, quiet);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// warp 2: which nodes each node sees; and where a segment is cut behind this CTA's range
+// ---------------------------------------------------------------------------
+// Word w of node i is at mask[w kMaxNodes + i].  A node's set is taken from its parent's by
+// pointer jumping: `up` is the first ancestor not in the set yet.  Nodes go 32 at a time,
+// so that parents in earlier groups are complete; inside a group the sets double with each
+// round.
+__device__ __forceinline__ void ancestors(const int32_t* parents, int n, int places, uint32_t* mask,
+                                          int* up, bool& bad) {
+  const int lane = threadIdx.x & 31;
+  bad = false;
+  for (int i = lane; i < places; i += 32) {
+    const int a = i < n ? parents[i] : -1;
+    bad |= a < -1 || a >= i;
+    up[i] = a;
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  for (int b = 0; 32 * b < places; ++b) {
+    const int i = 32 * b + lane;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) mask[w * kMaxNodes + i] = w == b && i < n && !bad ? 1u << lane : 0u;
+    int u = bad || i >= n ? -1 : up[i];
+    __syncwarp();
+    while (__any_sync(0xffffffffu, u >= 0)) {
+      uint32_t set[kWords];
+      int above = -1;
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) set[w] = u >= 0 && w <= b ? mask[w * kMaxNodes + u] : 0u;
+      if (u >= 0) above = up[u];
+      __syncwarp();
+      if (u >= 0) {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)
+          if (w <= b) mask[w * kMaxNodes + i] |= set[w];
+      }
+      u = above;
+      up[i] = u;
+      __syncwarp();
+    }
+    up[i] = -1;
+    __syncwarp();
+  }
+}
+
+template <int D, bool SPLIT>
+__device__ void mask_warp(const Work& w, const Plan& plan, uint8_t* smem, const Bars<D, SPLIT>& bar,
+                          volatile int* abort) {
+  using C = Cfg<D, SPLIT>;
+  const TreeParams& p = w.p;
+  const int lane = threadIdx.x & 31;
+  const int places = (p.Tn + 31) / 32 * 32;
+  volatile int* bad_tree = reinterpret_cast<volatile int*>(smem + C::OFF_MISC) + 2;
+  int* up = reinterpret_cast<int*>(smem + C::OFF_UP);
+  int mc = 0;
+  Walk walk(w, plan);
+  Piece x;
+  while (walk.next(x)) {
+    if (!x.tail()) continue;
+    const int b = mc & 1;
+    if (!mbar_wait_warp(bar.mask_empty(b), ((mc >> 1) & 1) ^ 1, abort, p.flags, p.wait_limit_ns)) return;
+    uint32_t* mask = reinterpret_cast<uint32_t*>(smem + C::OFF_MASK) + b * kWords * kMaxNodes;
+    bool bad;
+    ancestors(p.parents + static_cast<size_t>(x.r) * p.Tn, x.z.n, places, mask, up, bad);
+    if (lane == 0) {
+      bad_tree[b] = bad;
+      if (bad) raise_flag(p.flags, DEVFLAG_BAD_TREE);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar.mask_full(b));
+    ++mc;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// MMA warp (the converged warp runs the issue code, elect.sync picks the issuing lane)
+// ---------------------------------------------------------------------------
+template <int D, bool SPLIT>
+struct MmaWarp {
+  using C = Cfg<D, SPLIT>;
+  static constexpr uint32_t kIdescQK = idesc_bf16_f32(BM, BN, 0, 0);
+  static constexpr uint32_t kIdescPV = idesc_bf16_f32(BM, D, 0, 1);  // P in TMEM, V MN-major
+  static constexpr uint64_t kTileStep = C::TILE_BYTES >> 4;
+
+  const Work& w;
+  const Bars<D, SPLIT>& bar;
+  volatile int* abort;
+  uint32_t sR, tmem;
+  uint64_t dq, dk, dv;  // descriptors of Q tile 0 and of ring slot 0 read as K and as V
+  int lane;
+  int base = 0;          // ring index of the piece's first K tile
+  int n_pv[2] = {0, 0};  // P V products issued per chain, all pieces
+  int cleared = -1;      // the piece's last V tile has had its dead rows cleared
+
+  __device__ MmaWarp(const Work& w_, const Bars<D, SPLIT>& b_, volatile int* a_, uint32_t sbase,
+                     uint32_t tmem_)
+      : w(w_), bar(b_), abort(a_), sR(sbase + C::OFF_RING), tmem(tmem_),
+        dq(smem_desc_sw128(sbase + C::OFF_Q, 16, 1024)),
+        dk(smem_desc_sw128(sbase + C::OFF_RING, 16, 1024)),
+        dv(smem_desc_sw128(sbase + C::OFF_RING, C::BOX_BYTES, 1024)),
+        lane(threadIdx.x & 31) {}
+
+  __device__ bool wait(uint32_t b, uint32_t parity) {
+    return mbar_wait_warp(b, parity, abort, w.p.flags, w.p.wait_limit_ns);
+  }
+  __device__ int slot(int i) const { return (base + i) % C::NSLOT; }
+  __device__ uint32_t par(int i) const { return ((base + i) / C::NSLOT) & 1; }
+
+  // S_I = Q_I K_t^T (t counts the piece's tiles).  It overwrites the columns of P_I of the
+  // tile before, whose P V product was issued earlier by this same thread: one thread's
+  // products execute in issue order.
+  template <int I>
+  __device__ bool issue_s(int t, bool ring_seen) {
+    const int ks = slot(2 * t);
+    if (!ring_seen && !wait(bar.slot_full(ks), par(2 * t))) return false;
+    tc_fence_after();
+    const uint64_t a = dq + (SPLIT ? 0 : I) * kTileStep, b = dk + static_cast<uint64_t>(ks) * kTileStep;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint32_t off = ((kk >> 2) * C::BOX_BYTES + (kk & 3) * 32) >> 4;
+      mma_ss_warp(tmem + C::s_col(I), a + off, b + off, kIdescQK, kk > 0 ? 1u : 0u);
+    }
+    mma_commit_warp(bar.s_full(I));
+    return true;
+  }
+
+  // O_I += P_I V_t (P_I from TMEM); `add`: the chain has an earlier tile in this piece
+  template <int I>
+  __device__ bool issue_pv(int t, bool add, int dead_from, bool ring_seen) {
+    const int vs = slot(2 * t + 1);
+    if (!ring_seen && !wait(bar.slot_full(vs), par(2 * t + 1))) return false;
+    if (dead_from < BN && cleared != t) {
+      cleared = t;
+      // Rows past the last key hold stale or arbitrary data (even NaN); their probabilities
+      // are 0, but 0 * NaN would reach O.
+      uint8_t* gv = reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(sR + vs * C::TILE_BYTES));
+      for (int e = dead_from * 8 + lane; e < BN * 8; e += 32) {  // 8 x 16 bytes a 128-byte row
+#pragma unroll
+        for (int kb = 0; kb < C::KB; ++kb)
+          *reinterpret_cast<uint4*>(gv + kb * C::BOX_BYTES + e * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+    if (!wait(bar.p_full(I), n_pv[I] & 1)) return false;
+    tc_fence_after();
+    const uint64_t b = dv + static_cast<uint64_t>(vs) * kTileStep;
+#pragma unroll
+    for (int kk = 0; kk < BN / 16; ++kk)
+      mma_ts_warp(tmem + C::o_col(I), tmem + C::p_col(I) + 8 * kk, b + ((kk * 16 * 128) >> 4),
+                  kIdescPV, (add || kk > 0) ? 1u : 0u);
+    mma_commit_warp(bar.s_free(I));
+    ++n_pv[I];
+    return true;
+  }
+
+  __device__ void run(const Plan& plan) {
+    int uc = 0;
+    Walk walk(w, plan);
+    Piece x;
+    while (walk.next(x)) {
+      const int n = x.n;
+      if (n == 0) continue;
+      if (!wait(bar.q_full(), uc & 1)) return;
+      ++uc;
+      cleared = -1;
+      // row of the last tile from which on there are no keys
+      auto dead_from = [&](int t) { return x.z.keys() - (x.j0 + t) * BN; };
+      if (SPLIT) {
+        if (!issue_s<0>(0, false)) return;
+        mma_commit_warp(bar.slot_empty(slot(0)));
+        if (n > 1) {
+          if (!issue_s<1>(1, false)) return;
+          mma_commit_warp(bar.slot_empty(slot(2)));
+        }
+        if (n <= 2) mma_commit_warp(bar.q_empty());
+        for (int t = 0; t < n; ++t) {
+          if (!(t & 1 ? issue_pv<1>(t, t > 1, dead_from(t), false)
+                      : issue_pv<0>(t, t > 1, dead_from(t), false)))
+            return;
+          mma_commit_warp(bar.slot_empty(slot(2 * t + 1)));
+          if (t + 2 < n) {
+            if (!(t & 1 ? issue_s<1>(t + 2, false) : issue_s<0>(t + 2, false))) return;
+            mma_commit_warp(bar.slot_empty(slot(2 * t + 4)));
+            if (t + 3 == n) mma_commit_warp(bar.q_empty());  // the piece's last read of Q
+          }
+        }
+      } else {
+        const bool two = 256 * x.pair + BM < w.group_rows;  // the second row tile has rows
+        if (!issue_s<0>(0, false)) return;
+        if (two && !issue_s<1>(0, true)) return;
+        mma_commit_warp(bar.slot_empty(slot(0)));
+        if (n == 1) mma_commit_warp(bar.q_empty());
+        for (int t = 0; t < n; ++t) {
+          if (!issue_pv<0>(t, t > 0, dead_from(t), false)) return;
+          if (t + 1 < n && !issue_s<0>(t + 1, false)) return;
+          if (two && !issue_pv<1>(t, t > 0, dead_from(t), true)) return;
+          mma_commit_warp(bar.slot_empty(slot(2 * t + 1)));
+          if (t + 1 < n) {
+            if (two && !issue_s<1>(t + 1, true)) return;
+            mma_commit_warp(bar.slot_empty(slot(2 * t + 2)));
+            if (t + 2 == n) mma_commit_warp(bar.q_empty());
+          }
+        }
+      }
+      base += 2 * n;
+    }
+  }
+};
+
+// Bits x .. x + 31 of a node's set, those before node 0 (the cached tokens) set.
+__device__ __forceinline__ uint32_t seen_bits(const uint32_t* set, int x) {
+  if (x <= -32) return 0xffffffffu;
+  if (x >= kMaxNodes) return 0u;
+  if (x < 0) return (set[0] << -x) | ((1u << -x) - 1u);
+  const int i = x >> 5;
+  return __funnelshift_r(set[i * kMaxNodes], i + 1 < kWords ? set[(i + 1) * kMaxNodes] : 0u, x & 31);
+}
+
+// ---------------------------------------------------------------------------
+// softmax warpgroup of chain I (128 threads, one query row each)
+// ---------------------------------------------------------------------------
+template <int D, bool SPLIT>
+__device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint32_t tmem,
+                           const Bars<D, SPLIT>& bar, volatile int* abort, const int I) {
+  using C = Cfg<D, SPLIT>;
+  const TreeParams& p = w.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sp = warp & 3;  // TMEM sub-partition this warp may access
+  const int tile_row = sp * 32 + lane;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
+  const float sl2 = p.scale_log2;
+  const unsigned long long lim = p.wait_limit_ns;
+  volatile int* bad_trees = reinterpret_cast<volatile int*>(smem + C::OFF_MISC) + 2;
+  float2* join = reinterpret_cast<float2*>(smem + C::OFF_JOIN);
+  int sc = 0;  // tiles consumed by this chain, all pieces
+  int mc = 0;  // masks consumed
+  int jc = 0;  // pieces joined
+  // A meeting of both warpgroups, with a bounded wait like every other.
+  auto meet = [&](int i) {
+    tc_fence_before();
+    mbar_arrive(bar.joined(i));
+    if (!mbar_wait_warp(bar.joined(i), jc & 1, abort, p.flags, lim)) return false;
+    tc_fence_after();
+    return true;
+  };
+  Walk walk(w, plan);
+  Piece x;
+  while (walk.next(x)) {
+    const int row = 256 * x.pair + (SPLIT ? 0 : BM * I) + tile_row;  // of the KV head
+    const bool row_valid = row < w.group_rows;
+    const int node = row % p.Tn;
+    const bool live = __any_sync(0xffffffffu, row_valid);  // else the warp only keeps step
+    const int n = SPLIT ? (x.n + 1 - I) / 2
+                        : (256 * x.pair + BM * I < w.group_rows ? x.n : 0);
+    const bool tail = x.tail();
+    const int b = mc & 1;
+    const uint32_t* set = reinterpret_cast<const uint32_t*>(smem + C::OFF_MASK) +
+                          b * kWords * kMaxNodes + node;
+    bool have_mask = false;
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < n; ++i) {
+      const int j = x.j0 + (SPLIT ? 2 * i + I : i);
+      if (!mbar_wait_warp(bar.s_full(I), sc & 1, abort, p.flags, lim)) return;
+      if (live) {
+        tc_fence_after();
+        float s[128];
+        {
+          uint32_t u32[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(lane_base + C::s_col(I) + 32 * c, u32[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) reg_fence32(u32[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[32 * c + e] = __uint_as_float(u32[c][e]);
+        }
+        const bool masked = x.masked(j);
+        if (masked) {
+          if (!have_mask &&
+              !mbar_wait_warp(bar.mask_full(b), (mc >> 1) & 1, abort, p.flags, lim))
+            return;
+          have_mask = true;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t bits = seen_bits(set, j * BN - x.z.L + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(bits >> e & 1u)) s[32 * c + e] = -INFINITY;
+          }
+        }
+        const float m_tile = row_max(s);
+        // Move the running max only when it grows by more than 2^kRescaleLog2.
+        const bool grow = (m_tile - m) * sl2 > kRescaleLog2;
+        float alpha = 1.f;
+        if (grow) {
+          alpha = ex2((m - m_tile) * sl2);  // 0 for the first visible tile (m = -inf)
+          m = m_tile;
+          l *= alpha;
+        }
+        if (i > 0 && __any_sync(0xffffffffu, grow)) {
+          // O_I already holds the chain's earlier tiles (S_I was issued after their products
+          // completed): rescale it in TMEM.
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(lane_base + C::o_col(I) + 16 * c, o);
+            tmem_wait_ld();
+            reg_fence16(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(lane_base + C::o_col(I) + 16 * c, o);
+          }
+          tmem_wait_st();
+        }
+        const float ms = (m == -INFINITY) ? 0.f : m * sl2;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        if (masked)
+          write_p<false>(s, sl2, ms, lane_base + C::p_col(I), sum);
+        else
+          write_p<true>(s, sl2, ms, lane_base + C::p_col(I), sum);
+        l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      mbar_arrive(bar.p_full(I));
+      ++sc;
+    }
+    bool bad = x.z.bad;
+    if (tail) {
+      // (every warp meets every mask, so that none is a buffer ahead)
+      if (!have_mask && !mbar_wait_warp(bar.mask_full(b), (mc >> 1) & 1, abort, p.flags, lim)) return;
+      bad |= bad_trees[b] != 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.mask_empty(b));
+      ++mc;
+    }
+
+    // ---- results of the piece: O and LSE, or a partial output ----
+    const bool dead = node >= x.z.n;  // no node is in this place
+    float f0 = 0.f, f1 = 0.f;         // factors of O_0 and O_1 (one of them without SPLIT)
+    float M = m, sum = l;
+    bool two = false;
+    // the chain's last P V product
+    if (n > 0 && !mbar_wait_warp(bar.s_free(I), (sc - 1) & 1, abort, p.flags, lim)) return;
+    tc_fence_after();
+    if (SPLIT && x.n > 0) {
+      two = x.n > 1;  // (chain 1 has a tile)
+      join[I * BM + tile_row] = make_float2(m, l);
+      if (!meet(0)) return;
+      const float2 a = join[tile_row], c = join[BM + tile_row];  // (-inf, 0 without a tile)
+      M = fmaxf(a.x, c.x);
+      const float Ms = M == -INFINITY ? 0.f : M;
+      f0 = ex2((a.x - Ms) * sl2);
+      f1 = ex2((c.x - Ms) * sl2);
+      sum = f0 * a.y + f1 * c.y;
+    } else {
+      f0 = 1.f;
+    }
+    const bool none = sum == 0.f || dead || x.n == 0;  // no key is seen (a NaN is a result)
+    const float inv = bad ? kNan : (none ? 0.f : 1.f / sum);
+    const float lse = bad ? kNan : (none ? -INFINITY : M * p.scale + logf(sum));
+    f0 *= inv;
+    f1 *= inv;
+    const size_t out_row = (static_cast<size_t>(x.r) * p.Hkv + x.kvh) * w.group_rows + row;
+    const int unit_row = row - 256 * x.pair;
+    const size_t part_row = static_cast<size_t>(x.slot < 0 ? 0 : x.slot) * w.unit_rows + unit_row;
+    const bool has_o = SPLIT ? x.n > 0 : n > 0;
+    // SPLIT: each warpgroup writes half of the channels
+    constexpr int COLS = SPLIT ? D / 2 : D;
+    const int c0 = SPLIT ? COLS * I : 0;
+    if (live) {
+#pragma unroll 1
+      for (int c = c0; c < c0 + COLS; c += 16) {
+        uint32_t o[16], o1[16];
+        if (has_o) {
+          tmem_ld16(lane_base + C::o_col(SPLIT ? 0 : I) + c, o);
+          if (SPLIT && two) tmem_ld16(lane_base + C::o_col(1) + c, o1);
+          tmem_wait_ld();
+          reg_fence16(o);
+          if (SPLIT && two) reg_fence16(o1);
+        }
+        float f[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          f[e] = has_o && !none ? __uint_as_float(o[e]) * f0 : (bad ? kNan : 0.f);
+          if (SPLIT && two && !none) f[e] = fmaf(__uint_as_float(o1[e]), f1, f[e]);
+        }
+        if (row_valid && x.slot < 0) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + out_row * D + c);
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+            dst[v] = make_uint4(pack_bf16x2(f[8 * v], f[8 * v + 1]), pack_bf16x2(f[8 * v + 2], f[8 * v + 3]),
+                                pack_bf16x2(f[8 * v + 4], f[8 * v + 5]),
+                                pack_bf16x2(f[8 * v + 6], f[8 * v + 7]));
+        } else if (row_valid) {
+          float4* dst = reinterpret_cast<float4*>(w.part_o + part_row * D + c);
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            dst[v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
+        }
+      }
+    }
+    if (row_valid && (!SPLIT || I == 0)) {
+      if (x.slot >= 0)
+        w.part_lse[part_row] = lse;
+      else if (p.lse != nullptr)
+        p.lse[out_row] = lse;
+    }
+    // the next piece's products may overwrite what the other warpgroup reads here
+    if (SPLIT && x.n > 0) {
+      if (!meet(1)) return;
+      ++jc;
+    }
+  }
+}
+
+// This CTA's range of the steps, found by all threads together (a request a thread).
+__device__ void make_plan(const Work& w, Plan* plan, int* sums) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto block_sum = [&](int v) {  // over all threads, in every thread
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if (lane == 0) sums[warp] = v;
+    __syncthreads();
+    int t = 0;
+    for (int i = 0; i < kThreads / 32; ++i) t += sums[i];
+    return t;
+  };
+  auto steps = [&](int r) { return r < w.p.S ? sizes_of(w.p, r).steps() * w.segs : 0; };
+  const int first = steps(threadIdx.x);  // (the only requests, usually)
+  int mine = first;
+  for (int r = threadIdx.x + kThreads; r < w.p.S; r += kThreads) mine += steps(r);
+  const int total = block_sum(mine);
+  const int W = min(static_cast<int>(gridDim.x), total);
+  const int k = blockIdx.x;
+  const int share = total / W, extra = total - share * W;  // the first `extra` take one more
+  const int lo = k * share + min(k, extra), n = k < W ? share + (k < extra ? 1 : 0) : 0;
+  if (threadIdx.x == 0) *plan = Plan{lo, n, 0, 0, 0, share, extra};
+  int before = 0;
+  for (int r0 = 0; r0 < w.p.S && n > 0; r0 += kThreads) {
+    const int r = r0 + threadIdx.x;
+    const int own = r0 == 0 ? first : steps(r);
+    int incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int all = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) incl += sums[i];
+      all += sums[i];
+    }
+    incl += before;
+    if (own > 0 && incl - own <= lo && lo < incl) {
+      const int per_seg = own / w.segs, rest = lo - (incl - own);
+      plan->r = r;
+      plan->s = rest / per_seg;
+      plan->j = rest - plan->s * per_seg;
+    }
+    before += all;
+    if (before > lo) break;  // (the same in every thread)
+  }
+}
+
+// Notes the segment that begins in this CTA's range and goes on in the next one.
+__device__ void note_cut(const Work& w, const Plan& plan) {
+  Cut cut{0, 0, 0, 0};
+  Walk walk(w, plan);
+  Piece x;
+  int at = plan.lo;  // step that x begins at
+  while (walk.next(x)) {
+    const int steps = x.z.steps();
+    const int n = walk.left > 0 || x.last ? steps - x.j0 : plan.lo + plan.n - at;
+    if (!x.last && x.j0 == 0) {
+      // the range that holds the segment's last step
+      const int e = at + steps - 1, big = plan.extra * (plan.share + 1);
+      const int k1 = e < big ? e / (plan.share + 1) : plan.extra + (e - big) / plan.share;
+      cut = Cut{x.r, x.kvh * w.pairs + x.pair, k1 - static_cast<int>(blockIdx.x) + 1, x.slot};
+    }
+    at += n;
+  }
+  w.cut[blockIdx.x] = cut;
+}
+
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Work w) {
+  using C = Cfg<D, SPLIT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  const Bars<D, SPLIT> bar{sbase + C::OFF_BAR};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  Plan* plan_at = reinterpret_cast<Plan*>(smem + C::OFF_PLAN);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // the merge kernel (or what else follows as a programmatic dependent) waits for this
+  // grid's results
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    mbar_init(bar.q_full(), 1);
+    mbar_init(bar.q_empty(), 1);
+    for (int s = 0; s < C::NSLOT; ++s) {
+      mbar_init(bar.slot_full(s), 1);
+      mbar_init(bar.slot_empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar.s_full(i), 1);
+      mbar_init(bar.s_free(i), 1);
+      mbar_init(bar.p_full(i), 128);
+      mbar_init(bar.mask_full(i), 1);
+      mbar_init(bar.mask_empty(i), 8);
+      mbar_init(bar.joined(i), 256);
+    }
+    mbar_init(bar.teardown(), 1);
+    *abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  // the preceding kernel's writes (an append's) are complete and visible past this point
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!w.direct) make_plan(w, plan_at, reinterpret_cast<int*>(smem + C::OFF_SUMS));
+  tc_fence_before();
   __syncthreads();
-  if (threadIdx.x >= D) return;
-  float M = -INFINITY, tot = 0.f, out = 0.f;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, part_m[w]);
-  const float Ms = M == -INFINITY ? 0.f : M;
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = ex2((part_m[w] - Ms) * p.scale_log2);
-    tot = fmaf(f, part_l[w], tot);
-    out = fmaf(f, part[w][threadIdx.x], out);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Plan plan = *plan_at;  // (not set, nor read, if w.direct)
+
+  if (warp < 4) {
+    regs_decrease<kRegsWg0>();
+    if (warp == 0) {
+      producer_warp<D, SPLIT>(&tmQ, &tmK, &tmV, w, plan, sbase, bar, abort);
+    } else if (warp == 1) {
+      MmaWarp<D, SPLIT> mma(w, bar, abort, sbase, tmem);
+      mma.run(plan);
+      // Every product this warp issued has finished once the teardown barrier flips.
+      mma_commit_warp(bar.teardown());
+      if (lane == 0) mbar_wait_quiet(bar.teardown(), 0, 1000000000ull);
+      __syncwarp();
+    } else if (warp == 2) {
+      mask_warp<D, SPLIT>(w, plan, smem, bar, abort);
+    } else if (!w.direct && lane == 0) {
+      note_cut(w, plan);
+    }
+  } else {
+    regs_increase<kRegsSoftmax>();
+    softmax_wg<D, SPLIT>(w, plan, smem, tmem, bar, abort, warp < 8 ? 0 : 1);
   }
-  const float nan = __int_as_float(0x7fc00000);
-  out = bad ? nan : (tot == 0.f ? 0.f : out / tot);
-  static_cast<uint16_t*>(p.o)[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] =
-      static_cast<uint16_t>(pack_bf16x2(out, 0.f));
-  if (p.lse != nullptr && threadIdx.x == 0)
-    p.lse[blockIdx.x] = bad ? nan : Ms * p.scale + logf(tot);
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// LSE = M + ln sum_j e^{LSE_j - M}, O = sum_j e^{LSE_j - LSE} O_j over the pieces of one row of
+// a cut segment: a warp a row, four pieces in flight.
+constexpr int kMergeWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ Work w) {
+  constexpr int PER = D / 32;  // channels a lane
+  constexpr float kLog2e = 1.4426950408889634f;
+  // launched as a programmatic dependent: the results are complete and visible past this
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Cut cut = w.cut[blockIdx.x];
+  const int lane = threadIdx.x & 31;
+  const int unit_row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int kvh = cut.s / w.pairs;
+  const int row = 256 * (cut.s - kvh * w.pairs) + unit_row;
+  if (cut.pieces == 0 || unit_row >= w.unit_rows || row >= w.group_rows) return;
+  auto slot = [&](int i) { return i == 0 ? cut.slot : 2 * (static_cast<int>(blockIdx.x) + i); };
+  float m = -INFINITY, sum = 0.f, o[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) o[i] = 0.f;
+  for (int j = 0; j < cut.pieces; j += 4) {
+    float lse[4], v[4][PER];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      lse[s] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[s][i] = 0.f;
+      if (j + s < cut.pieces) {
+        const size_t at = static_cast<size_t>(slot(j + s)) * w.unit_rows + unit_row;
+        lse[s] = w.part_lse[at];
+        const float* src = w.part_o + at * D + lane * PER;
+        if constexpr (PER == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(src);
+          v[s][0] = y.x, v[s][1] = y.y, v[s][2] = y.z, v[s][3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(src);
+          v[s][0] = y.x, v[s][1] = y.y;
+        }
+      }
+    }
+    const float mn = fmaxf(fmaxf(m, lse[0]), fmax3(lse[1], lse[2], lse[3]));
+    const float ms = mn == -INFINITY ? 0.f : mn;
+    const float al = ex2((m - ms) * kLog2e);
+    m = mn;
+    sum *= al;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] *= al;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const float f = ex2((lse[s] - ms) * kLog2e);
+      sum += f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] = fmaf(f, v[s][i], o[i]);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (no key is seen)
+  const size_t out = (static_cast<size_t>(cut.r) * w.p.Hkv + kvh) * w.group_rows + row;
+  uint16_t* dst = static_cast<uint16_t*>(w.p.o) + out * D + lane * PER;
+#pragma unroll
+  for (int i = 0; i < PER; i += 2)
+    *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(o[i] * inv, o[i + 1] * inv);
+  if (w.p.lse != nullptr && lane == 0)
+    w.p.lse[out] = sum == 0.f ? -INFINITY : m + logf(sum);
+}
+
+struct Shape {
+  int group_rows, pairs, segs, unit_rows;
+  long long units, steps;  // segments of the batch, and their steps at most
+  bool direct;
+};
+
+Shape shape_of(int S, int Tn, int Hq, int Hkv, int max_seq_len) {
+  Shape s;
+  s.group_rows = Hq / Hkv * Tn;
+  s.pairs = (s.group_rows + 255) / 256;
+  s.segs = Hkv * s.pairs;
+  s.unit_rows = s.group_rows < 256 ? s.group_rows : 256;
+  const long long per_seg = std::max<long long>(1, (max_seq_len + (BN - 1ll)) / BN);
+  s.units = static_cast<long long>(S) * s.segs;
+  s.steps = per_seg * s.units;
+  s.direct = per_seg <= kDirectSteps;
+  return s;
+}
+
+// CTAs of a split launch, which the workspace is laid out for: as many on every device, so
+// that it depends on the sizes alone.
+constexpr int kMaxGrid = 160;
+int grid_of(const Shape& s, int num_sms) {
+  return static_cast<int>(std::min<long long>({num_sms, kMaxGrid, s.direct ? s.units : s.steps}));
+}
+
+struct Layout {
+  size_t off_lse, off_cut, bytes;  // part_o at 0
+};
+Layout layout_of(const Shape& s, int D) {
+  Layout l{};
+  if (s.direct) return l;
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  const size_t grid = static_cast<size_t>(std::min<long long>(s.steps, kMaxGrid));
+  const size_t rows = 2 * grid * s.unit_rows;
+  l.off_lse = up(rows * D * sizeof(float));
+  l.off_cut = l.off_lse + up(rows * sizeof(float));
+  l.bytes = l.off_cut + up(grid * sizeof(Cut));
+  return l;
+}
+
+template <int D, bool SPLIT>
+cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                   const Work& w, int grid, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<D, SPLIT>::SMEM_BYTES;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<D, SPLIT>, tmQ, tmK, tmV, w);
+  if (e != cudaSuccess || w.direct) return e;
+  cfg.gridDim = dim3(grid, (w.unit_rows + kMergeWarps - 1) / kMergeWarps);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, w);
+}
+
+template <int D, bool SPLIT>
+cudaError_t set_smem() {
+  return cudaFuncSetAttribute(tree_attn_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (Cfg<D, SPLIT>::SMEM_BYTES));
 }
 
 }  // namespace
 
-size_t tree_attn_workspace_bytes(int, int, int, int, int, int) { return 0; }
+size_t tree_attn_workspace_bytes(int S, int Tn, int Hq, int Hkv, int D, int max_seq_len) {
+  return layout_of(shape_of(S, Tn, Hq, Hkv, max_seq_len), D).bytes;
+}
 
-cudaError_t prepare_tree_attn() { return cudaSuccess; }
+cudaError_t prepare_tree_attn() {
+  cudaError_t e;
+  if ((e = set_smem<64, true>()) != cudaSuccess) return e;
+  if ((e = set_smem<64, false>()) != cudaSuccess) return e;
+  if ((e = set_smem<128, true>()) != cudaSuccess) return e;
+  return set_smem<128, false>();
+}
 
-cudaError_t launch_tree_attn(const TreeParams& p, int num_sms, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(p.S) * p.Hq * p.Tn;
+cudaError_t launch_tree_attn(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                             const TreeParams& p, void* workspace, int num_sms,
+                             cudaStream_t stream) {
+  const Shape s = shape_of(p.S, p.Tn, p.Hq, p.Hkv, p.max_seq_len);
+  const Layout l = layout_of(s, p.D);
+  char* ws = static_cast<char*>(workspace);
+  Work w{};
+  w.p = p;
+  w.part_o = reinterpret_cast<float*>(ws);
+  w.part_lse = reinterpret_cast<float*>(ws + l.off_lse);
+  w.cut = reinterpret_cast<Cut*>(ws + l.off_cut);
+  w.group_rows = s.group_rows;
+  w.pairs = s.pairs;
+  w.segs = s.segs;
+  w.unit_rows = s.unit_rows;
+  w.direct = s.direct;
+  const int grid = grid_of(s, num_sms);
+  const bool split = s.group_rows <= BM;
   if (p.D == 64)
-    tree_attn_kernel<64><<<grid, kThreads, 0, stream>>>(p);
-  else
-    tree_attn_kernel<128><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+    return split ? launch<64, true>(tmQ, tmK, tmV, w, grid, stream)
+                 : launch<64, false>(tmQ, tmK, tmV, w, grid, stream);
+  return split ? launch<128, true>(tmQ, tmK, tmV, w, grid, stream)
+               : launch<128, false>(tmQ, tmK, tmV, w, grid, stream);
 }
 
 }  // namespace gbattn
