@@ -534,6 +534,9 @@ def _load_quick(torch):
                  "paged_kv4_attn_prefill", "paged_kv4_attn_prefill_workspace_size")
         m.setup(torch.__version__, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
                 *(ctypes.cast(getattr(h, n), ctypes.c_void_p).value for n in names))
+        names = ("paged_attn_tree", "paged_attn_tree_workspace_size", "draft_verify",
+                 "paged_kv_keep")
+        m.setup_tree(*(ctypes.cast(getattr(h, n), ctypes.c_void_p).value for n in names))
     except ImportError as e:  # not built, or against another torch
         warnings.warn(f"_binding cannot be used ({e}): calls go through the interpreter, at about "
                       "20 us more of host time each", RuntimeWarning)
@@ -993,6 +996,11 @@ def paged_attn_tree(q, k_pool, v_pool, block_table, seq_lens, parents, max_seq_l
     """
     if _torch is None:
         _load_torch()
+    if _quick is not None and stream is None:
+        r = _quick.tree(q, k_pool, v_pool, block_table, seq_lens, parents, max_seq_len, tree_lens,
+                        scale, out, lse, workspace, return_lse)
+        if r is not None:
+            return _done("paged_attn_tree", r)
     _first(q)
     device = q.device
     if q.dim() != 4:
@@ -1079,6 +1087,11 @@ def draft_verify(target_probs, draft_probs, draft_tokens, parents, uniforms, tre
     """
     if _torch is None:
         _load_torch()
+    if _quick is not None and stream is None:
+        r = _quick.verify(target_probs, draft_probs, draft_tokens, parents, uniforms, tree_lens,
+                          tokens_out, path, counts)
+        if r is not None:
+            return _done("draft_verify", r)
     _first(target_probs)
     device = target_probs.device
     _check_probs("target_probs", target_probs, None, None, device)
@@ -1149,6 +1162,10 @@ def paged_kv_keep(k_pool, v_pool, block_table, seq_lens, path, counts, new_seq_l
     """
     if _torch is None:
         _load_torch()
+    if _quick is not None and stream is None:
+        r = _quick.keep(k_pool, v_pool, block_table, seq_lens, path, counts, new_seq_lens)
+        if r is not None:
+            return _done("paged_kv_keep", r)[0]
     _first(seq_lens)
     device = seq_lens.device
     kp, shape = _pools("k_pool", k_pool, device)

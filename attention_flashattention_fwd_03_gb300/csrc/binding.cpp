@@ -40,6 +40,13 @@ struct Entry {
   decltype(&::paged_kv4_attn_prefill) prefill;
   decltype(&::paged_kv4_attn_prefill_workspace_size) prefill_ws;
 } g_entry;
+// Those of the operators for trees of drafted tokens.
+struct TreeEntry {
+  decltype(&::paged_attn_tree) attend;
+  decltype(&::paged_attn_tree_workspace_size) attend_ws;
+  decltype(&::draft_verify) verify;
+  decltype(&::paged_kv_keep) keep;
+} g_tree;
 PyObject *g_get_device = nullptr, *g_get_stream = nullptr;
 
 constexpr int64_t kMaxSize = 0x7fffffff;  // the C ABI's sizes are ints
@@ -490,6 +497,133 @@ PyObject* attend(PyObject* const* args, Py_ssize_t n, bool prefill) {
 PyObject* decode(PyObject*, PyObject* const* args, Py_ssize_t n) { return attend(args, n, false); }
 PyObject* prefill(PyObject*, PyObject* const* args, Py_ssize_t n) { return attend(args, n, true); }
 
+// q, k_pool, v_pool, block_table, seq_lens, parents, length bound, tree_lens, scale (None: 1 /
+// sqrt(D)), out, lse, workspace, return_lse
+PyObject* tree(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded(args, n, 13, [&](Call& c) -> PyObject* {
+    const at::Tensor* q = c.need(c.tensor(0));
+    if (!c.ok || q->dim() != 4 || !c.on(*q)) return nullptr;
+    const int64_t S = q->size(0), Hq = q->size(1), Tn = q->size(2), D = q->size(3);
+    c.dense(0, at::kBFloat16, {S, Hq, Tn, D});
+    const at::Tensor* kp = c.need(c.dense(1, at::kBFloat16, {-1, -1, -1, D}));
+    if (!c.ok) return nullptr;
+    const at::Tensor* vp =
+        c.need(c.dense(2, at::kBFloat16, {kp->size(0), kp->size(1), kp->size(2), D}));
+    const at::Tensor* bt = c.need(c.dense(3, at::kInt, {S, -1}));
+    const at::Tensor* sl = c.need(c.dense(4, at::kInt, {S}));
+    const at::Tensor* pa = c.need(c.dense(5, at::kInt, {S, Tn}));
+    const int len = c.integer(6);
+    const at::Tensor* tl = c.dense(7, at::kInt, {S});
+    const float scale = args[8] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)))
+                                           : static_cast<float>(c.real(8));
+    const at::Tensor* out = c.dense(9, at::kBFloat16, {S, Hq, Tn, D});
+    const at::Tensor* lse = c.dense(10, at::kFloat, {S, Hq, Tn});
+    const at::Tensor* ws = c.dense(11, at::kByte, {-1});
+    const int want_lse = c.truth(12);
+    if (!c.ok) return nullptr;
+    const int64_t Hkv = kp->size(1);
+    at::Tensor made_out, made_lse;
+    c10::DataPtr own_ws;
+    size_t bytes = ws ? static_cast<size_t>(ws->numel()) : 0;
+    void* work = ptr(ws);
+    if (!ws) {
+      bytes = g_tree.attend_ws(S, Tn, Hq, Hkv, D, len);
+      if (bytes) {
+        own_ws = scratch(bytes);
+        work = own_ws.get();
+      }
+    }
+    if (!out) {
+      made_out = make(q->sizes(), at::kBFloat16);
+      out = &made_out;
+    }
+    if (!lse && want_lse) {
+      made_lse = make(q->sizes().slice(0, 3), at::kFloat);
+      lse = &made_lse;
+    }
+    const int st = released(g_tree.attend, ptr(q), ptr(kp), ptr(vp), ptr(bt), ptr(sl), ptr(pa),
+                            ptr(tl), kp->size(2), S, Tn, Hq, Hkv, D, bt->size(1), kp->size(0), len,
+                            scale, ptr(out), ptr(lse), work, bytes, c.stream);
+    if (st != ATTN_OK) return PyLong_FromLong(st);
+    return pack({result(args[9], made_out), result(args[10], made_lse)});
+  });
+}
+
+// target_probs, draft_probs, tokens, parents, uniforms, tree_lens, tokens_out, path, counts
+PyObject* verify(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded(args, n, 9, [&](Call& c) -> PyObject* {
+    const at::Tensor *p = c.need(c.tensor(0)), *q = c.tensor(1);
+    if (!c.ok || p->dim() != 3 || !c.on(*p)) return nullptr;
+    const at::ScalarType type = p->scalar_type();
+    if (type != at::kFloat && type != at::kBFloat16) return nullptr;
+    const int64_t S = p->size(0), Tn = p->size(1), V = p->size(2);
+    for (const at::Tensor* t : {p, q})
+      if (t && (t->scalar_type() != type || t->dim() != 3 || t->size(0) != S || t->size(1) != Tn ||
+                t->size(2) != V || (t->stride(2) != 1 && V > 1) || t->get_device() != c.dev))
+        return nullptr;
+    if (S > kMaxSize || Tn > kMaxSize || V > kMaxSize) return nullptr;
+    const at::Tensor* in[3] = {c.need(c.dense(2, at::kInt, {S, Tn})),
+                               c.need(c.dense(3, at::kInt, {S, Tn})),
+                               c.need(c.dense(4, at::kFloat, {S, Tn}))};
+    const at::Tensor* tl = c.dense(5, at::kInt, {S});
+    const at::Tensor* out[3] = {c.dense(6, at::kInt, {S, Tn}), c.dense(7, at::kInt, {S, Tn}),
+                                c.dense(8, at::kInt, {S})};
+    if (!c.ok) return nullptr;
+    at::Tensor made[3];
+    for (int i = 0; i < 3; ++i) {
+      if (out[i]) continue;
+      made[i] = i < 2 ? make({S, Tn}, at::kInt) : make({S}, at::kInt);
+      out[i] = &made[i];
+    }
+    int64_t strides[2][2] = {};
+    for (int i = 0; i < 2; ++i) {
+      strides[0][i] = p->size(i) > 1 ? p->stride(i) : 0;
+      if (q) strides[1][i] = q->size(i) > 1 ? q->stride(i) : 0;
+    }
+    const int st = released(g_tree.verify, ptr(p), ptr(q), strides[0], strides[1],
+                            type == at::kBFloat16 ? 1 : 0, ptr(in[0]), ptr(in[1]), ptr(in[2]), ptr(tl),
+                            S, Tn, V, ptr(out[0]), ptr(out[1]), ptr(out[2]), c.stream);
+    if (st != ATTN_OK) return PyLong_FromLong(st);
+    return pack({result(args[6], made[0]), result(args[7], made[1]), result(args[8], made[2])});
+  });
+}
+
+// k_pool, v_pool (one layer's, or all layers' in one tensor), block_table, seq_lens, path,
+// counts, new_seq_lens
+PyObject* keep(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded(args, n, 7, [&](Call& c) -> PyObject* {
+    if (!THPVariable_CheckExact(args[0]) || !THPVariable_CheckExact(args[1])) return nullptr;
+    const at::Tensor *kp = c.tensor(0), *vp = c.tensor(1), *sl = c.need(c.tensor(3));
+    if (!c.ok || sl->dim() != 1 || !c.on(*sl)) return nullptr;
+    const int64_t dims = kp->dim(), S = sl->size(0);
+    if ((dims != 4 && dims != 5) || kp->sizes() != vp->sizes()) return nullptr;
+    for (const at::Tensor* t : {kp, vp})
+      if (t->scalar_type() != at::kBFloat16 || !t->is_contiguous() || t->get_device() != c.dev)
+        return nullptr;
+    const int64_t layers = dims == 5 ? kp->size(0) : 1, *size = kp->sizes().data() + (dims - 4);
+    constexpr int64_t kLayers = 256;
+    if (layers < 1 || layers > kLayers || size[0] > kMaxSize || size[1] > kMaxSize) return nullptr;
+    c.dense(3, at::kInt, {S});
+    const at::Tensor* bt = c.need(c.dense(2, at::kInt, {S, -1}));
+    const at::Tensor* path = c.need(c.dense(4, at::kInt, {S, -1}));
+    const at::Tensor* counts = c.need(c.dense(5, at::kInt, {S}));
+    const at::Tensor* after = c.dense(6, at::kInt, {S});
+    if (!c.ok) return nullptr;
+    void* pools[2][kLayers];
+    const int64_t step = size[0] * size[1] * size[2] * size[3] * 2;
+    for (int64_t i = 0; i < layers; ++i) {
+      pools[0][i] = static_cast<char*>(ptr(kp)) + i * step;
+      pools[1][i] = static_cast<char*>(ptr(vp)) + i * step;
+    }
+    const int st = released(g_tree.keep, pools[0], pools[1], layers, ptr(bt), ptr(sl), ptr(path),
+                            ptr(counts), ptr(after), size[2], S, path->size(1), size[1], size[3],
+                            bt->size(1), size[0], c.stream);
+    if (st != ATTN_OK) return PyLong_FromLong(st);
+    // (in a tuple, as a result may be None)
+    return pack({result(args[6], at::Tensor())});
+  });
+}
+
 // setup(torch's version, get_device, get_stream, addresses of the entry points in the order
 // of Entry)
 PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -519,11 +653,32 @@ PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// setup_tree(addresses of the entry points in the order of TreeEntry), after setup.
+PyObject* setup_tree(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  constexpr Py_ssize_t kEntries = sizeof(TreeEntry) / sizeof(void*);
+  if (n != kEntries) {
+    PyErr_SetString(PyExc_TypeError, "setup_tree takes the entry points");
+    return nullptr;
+  }
+  void* address[kEntries];
+  for (Py_ssize_t i = 0; i < kEntries; ++i) {
+    address[i] = PyLong_AsVoidPtr(args[i]);
+    if (!address[i]) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an entry point is missing");
+      return nullptr;
+    }
+  }
+  memcpy(&g_tree, address, sizeof g_tree);
+  Py_RETURN_NONE;
+}
+
 #define ENTRY(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {ENTRY(setup),   ENTRY(rope),   ENTRY(rope_bwd),
                            ENTRY(append),  ENTRY(append4), ENTRY(gather),
-                           ENTRY(decode),  ENTRY(prefill), {nullptr, nullptr, 0, nullptr}};
+                           ENTRY(decode),  ENTRY(prefill), ENTRY(setup_tree),
+                           ENTRY(tree),    ENTRY(verify),  ENTRY(keep),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 

@@ -48,8 +48,16 @@ using u64 = unsigned long long;
 constexpr u64 kOne = 1ull << 62;
 
 // A probability (or random number) as a multiple of 2^-62; NaN and negative values are 0.
+// The significand goes to the top of 64 bits and down by the exponent (PTX shifts by 32 and
+// more give 0; the compiler's conversion to 64 bits runs at the rate of 64-bit floating point).
 __device__ __forceinline__ u64 fixed(float v) {
-  return __float2ull_rz(__saturatef(v) * 0x1p62f);
+  const uint32_t bits = __float_as_uint(__saturatef(v));
+  const uint32_t m = (bits << 8) | 0x80000000u, e = bits >> 23;  // v = m 2^(e - 158)
+  uint32_t hi, up, down;
+  asm("shr.u32 %0, %1, %2;" : "=r"(hi) : "r"(m), "r"(128u - e));
+  asm("shl.b32 %0, %1, %2;" : "=r"(up) : "r"(m), "r"(e - 96u));
+  asm("shr.u32 %0, %1, %2;" : "=r"(down) : "r"(m), "r"(96u - e));
+  return static_cast<u64>(hi) << 32 | (up | down);
 }
 __device__ __forceinline__ float value(float v) { return v; }
 __device__ __forceinline__ float value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
