@@ -9,11 +9,15 @@
 // sum falls in the running sum.
 //
 // A token hangs on which side of a border a random number lies, so sums must not depend on
-// an order and must be finer than fp32: probabilities are held as multiples of 2^-62 in 64-bit
-// integers (an fp32 from 2^-38 up exactly), whose sums are exact whatever the order, and
-// products of two are taken in 128 bits.  The kernel is bound by the rows that it reads; 64-bit
-// floating-point arithmetic, of which this GPU does two operations a clock and SM, would
-// be ten times slower than they are.
+// an order and must be finer than fp32: they are sums of integers, which are exact in any
+// order.  A test of a token takes probabilities as multiples of 2^-62 (an fp32 from 2^-38 up
+// exactly) and products in 128 bits.  Sums over a row take the exact p, or max(p - q, 0), rounded
+// to a multiple of 2^-44 (5e-9 of a distribution over 2^17 tokens at the very most, 1e-11 as
+// roundings go): adding 2 to an fp32 below 1 and taking it off again rounds it to 2^-22,
+// what is left over goes the same way to 2^-44, and the bits of the two sums are the integers
+// to be added up.  That is 13 instructions a token, half of them on pairs; integers made by shifts take 45 (64
+// requests x 8 drafts, 131072 tokens: 104 us), the compiler's conversions to 64 bits, which run at the
+// rate of 64-bit floating point, more yet (159).
 //
 // A cluster of CTAs takes a request.  CTA 0 leads: it reads the tree and, for all nodes at
 // once, the two probabilities that a test of the node would need, and walks down the tree
@@ -43,6 +47,8 @@ constexpr int kMaxCtas = 16;   // of a cluster
 constexpr int kPerLane = 16;   // values of a row that a lane reads at once
 constexpr int kSpan = 32 * kPerLane;
 constexpr int kMaxTiles = 256;
+constexpr int kMaxKept = 16384;  // tokens of a CTA whose w is kept from fall to fall (128 KB)
+static_assert(kMaxKept % kSpan == 0, "whole spans");
 
 using u64 = unsigned long long;
 constexpr u64 kOne = 1ull << 62;
@@ -62,9 +68,19 @@ __device__ __forceinline__ u64 fixed(float v) {
 __device__ __forceinline__ float value(float v) { return v; }
 __device__ __forceinline__ float value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 
-// a b 2^-62, rounded down.
-__device__ __forceinline__ u64 product(u64 a, u64 b) { return (__umul64hi(a, b) << 2) | ((a * b) >> 62); }
+// q W for a probability q, rounded down: the 32-bit significand times W, down by the exponent.
+__device__ __forceinline__ u64 product(float q, u64 W) {
+  const uint32_t bits = __float_as_uint(__saturatef(q));
+  const uint32_t m = (bits << 8) | 0x80000000u, e = bits >> 23;
+  const u64 low = static_cast<u64>(m) * static_cast<uint32_t>(W);
+  const u64 high = static_cast<u64>(m) * static_cast<uint32_t>(W >> 32) + (low >> 32);
+  u64 r;
+  asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(high), "r"(126u - e));  // (by 64 and more: 0)
+  return e == 127u ? W : r;
+}
 __device__ __forceinline__ u64 minus(u64 a, u64 b) { return a > b ? a - b : 0; }
+// a b 2^-62, rounded down.
+__device__ __forceinline__ u64 share_of(u64 a, u64 b) { return (__umul64hi(a, b) << 2) | ((a * b) >> 62); }
 // Whether a b 2^-62 < c, exactly.
 __device__ __forceinline__ bool product_below(u64 a, u64 b, u64 c) {
   const u64 hi = __umul64hi(a, b), lo = a * b;
@@ -112,31 +128,95 @@ __device__ __forceinline__ void store_remote(uint32_t a, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
-// What the leader has the cluster do.
-enum : int { kDone, kScan, kRest, kDraw };  // rest: sum of what is left once W q is taken off
+// What the leader has the cluster do.  kRest: sum of what is left once W q is taken off, and
+// kept as there is another child to try; kRestLast: there is none.
+enum : int { kDone, kScan, kRest, kRestLast, kDraw };
 struct Command {
   int op, node, level, count;
   u64 total;  // kRest: W; kDraw: where the random number falls in the running sum
 };
 static_assert(sizeof(Command) == 24, "three words");
 
-// w of one token at `level` falls, and less W q if `rest`.
-__device__ __forceinline__ u64 left(u64 w, u64 q, const u64* W, int level, bool rest) {
+// w of one token after `level` falls, and less W q if `rest`.
+__device__ __forceinline__ u64 left(float p, float q, const u64* W, int level, bool rest) {
+  u64 w = fixed(p);
   const int n = level + (rest ? 1 : 0);
-  for (int i = 0; i < n; ++i) w = minus(w, i == 0 ? q : product(q, W[i]));  // W[0] = 1
+  for (int i = 0; i < n; ++i) w = minus(w, i == 0 ? fixed(q) : product(q, W[i]));  // W[0] = 1
   return w;
+}
+
+// The sums' form of values in [0, 1]: hi 2^-22 + lo 2^-44 (added up modulo 2^32, with an offset
+// for each value).
+struct Halves {
+  uint32_t hi, lo;
+};
+constexpr uint32_t kHiOffset = 0x40000000u, kLoOffset = 0x35400000u;  // 2, 1.5 x 2^-21
+__device__ __forceinline__ u64 whole(Halves h, uint32_t n) {  // of n values, as a multiple of 2^-62
+  const long long hi = h.hi - n * kHiOffset;                  // (below 2^31: n <= 256)
+  const int lo = static_cast<int>(h.lo - n * kLoOffset);
+  return static_cast<u64>((hi << 22) + lo) << 18;
+}
+// Of d + e for a pair of values, |e| half a unit of d's last place at most.
+__device__ __forceinline__ void halves(float2 d, float2 e, Halves& x, Halves& y) {
+  const float2 t = __fadd2_rn(d, make_float2(2.f, 2.f));
+  const float2 back = __fadd2_rn(t, make_float2(-2.f, -2.f));
+  const float2 r = __fadd2_rn(d, make_float2(-back.x, -back.y));  // exact
+  const float2 u = __fadd2_rn(__fadd2_rn(r, e), make_float2(0x1.8p-21f, 0x1.8p-21f));
+  x = Halves{__float_as_uint(t.x), __float_as_uint(u.x)};
+  y = Halves{__float_as_uint(t.y), __float_as_uint(u.y)};
+}
+// Of max(p - q, 0): where p > q, p - q is d + e exactly.
+__device__ __forceinline__ void rest_halves(float2 p, float2 q, Halves& x, Halves& y) {
+  p = make_float2(__saturatef(p.x), __saturatef(p.y));
+  q = make_float2(-__saturatef(q.x), -__saturatef(q.y));
+  float2 d = __fadd2_rn(p, q);
+  float2 e = __fadd2_rn(__fadd2_rn(p, make_float2(-d.x, -d.y)), q);
+  e = make_float2(d.x > 0.f ? e.x : 0.f, d.y > 0.f ? e.y : 0.f);
+  halves(make_float2(fmaxf(d.x, 0.f), fmaxf(d.y, 0.f)), e, x, y);
+}
+__device__ __forceinline__ void prob_halves(float2 p, Halves& x, Halves& y) {
+  halves(make_float2(__saturatef(p.x), __saturatef(p.y)), make_float2(0.f, 0.f), x, y);
+}
+// w of one token in that form, after `level` falls and less W q if `rest`.
+__device__ __forceinline__ u64 left_rounded(float p, float q, const u64* W, int level, bool rest) {
+  const int n = level + (rest ? 1 : 0);
+  Halves x, y;
+  if (n == 0)
+    prob_halves(make_float2(p, 0.f), x, y);
+  else
+    rest_halves(make_float2(p, 0.f), make_float2(q, 0.f), x, y);
+  u64 w = whole(x, 1);
+  for (int i = 1; i < n; ++i) w = minus(w, product(q, W[i]));
+  return w;
+}
+
+// kPerLane values of a row from `i` on, 32 apart; those from `end` on are 0.
+template <typename T>
+__device__ __forceinline__ void read_span(const T* row, int i, int end, bool all, float (&v)[kPerLane]) {
+  if (all) {
+    T x[kPerLane];
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) x[k] = row[i + 32 * k];
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) v[k] = value(x[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) v[k] = i + 32 * k < end ? value(row[i + 32 * k]) : 0.f;
+  }
 }
 
 template <typename T, bool DRAWN>
 __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyParams p) {
   __shared__ int parent[kMaxNodes], token[kMaxNodes], path[kMaxNodes];
-  __shared__ u64 chance[kMaxNodes], pv[kMaxNodes], qv[kMaxNodes];  // u, p and q of every node
+  __shared__ u64 chance[kMaxNodes];                    // u, p and q of every node
+  __shared__ float pv[kMaxNodes], qv[kMaxNodes];
   __shared__ u64 W[kMaxNodes];           // sums of w by level
   __shared__ u64 sums[kMaxTiles];        // of this CTA's tiles
   __shared__ u64 totals[kMaxCtas];       // of all CTAs
   __shared__ u64 part[kWarps];
   __shared__ Command cmd;
   __shared__ u64 gone[DRAWN ? 1 : kMaxNodes], gone_w[DRAWN ? 1 : kMaxNodes];  // fallen tokens
+  extern __shared__ u64 kept[];          // w of the CTA's first p.kept tokens, as of `held` falls
   const uint32_t ctas = cluster_size(), rank = cluster_rank();
   const int r = blockIdx.x / ctas;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -159,13 +239,13 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
       token[tid] = x;
       chance[tid] = fixed(p.uniforms[row + tid]);
       bad = up < -1 || up >= tid;
-      u64 a = 0, b = 0;
+      float a = 0.f, b = 0.f;
       if (!bad && up >= 0 && x >= 0 && x < p.V) {
-        a = fixed(value(p_rows[up * p.p_stride[1] + x]));
-        if (DRAWN) b = fixed(value(q_rows[up * p.q_stride[1] + x]));
+        a = value(p_rows[up * p.p_stride[1] + x]);
+        if (DRAWN) b = value(q_rows[up * p.q_stride[1] + x]);
       }
       pv[tid] = a;
-      qv[tid] = DRAWN ? b : kOne;
+      qv[tid] = DRAWN ? b : 1.f;
     }
     const bool bad_tree = __syncthreads_or(bad);
     if ((bad_n || bad_tree) && tid == 0) raise_flag(p.flags, bad_n ? DEVFLAG_BAD_SEQLEN : DEVFLAG_BAD_TREE);
@@ -181,6 +261,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
   bool summed = false;  // the last sums are those of the present w
   int op = kDone, s_level = 0, s_node = 0;
   bool s_rest = false;
+  int held = 0, held_node = -1;
   const int c0 = rank * p.chunk, c1 = min(p.V, c0 + p.chunk);  // (chunk * ctas < 2^31)
 
   for (;;) {
@@ -218,11 +299,9 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
             }
             at = found;
           }
-          u64 w = pv[at];
-          const u64 q = qv[at];
-          if (DRAWN) {
-            w = left(w, q, W, level, false);
-          } else {
+          const float q = qv[at];
+          u64 w = left(pv[at], q, W, DRAWN ? level : 0, false);
+          if (!DRAWN) {
             const u64 x = static_cast<u64>(token[at]);
             bool hit = false;
             for (int i = lane; i < fallen; i += 32) hit |= gone[i] == x;
@@ -238,7 +317,10 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
             continue;
           }
           if (DRAWN) {
-            next.op = kRest;
+            bool more = false;
+            for (int b = at & ~31; b < n; b += 32)
+              more |= b + lane > at && b + lane < n && parent[b + lane] == cur;
+            next.op = __any_sync(0xffffffffu, more) ? kRest : kRestLast;
             waiting = kRested;
             break;
           }
@@ -247,8 +329,9 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
             waiting = kSummed;
             break;
           }
-          // without a draft the token itself is what falls
+          // without a draft the token itself is what falls, in the sums' form
           again = false;
+          if (w > 0) w = left_rounded(pv[at], 0.f, W, 0, false);
           u64 out = 0;
           for (int i = lane; i < fallen; i += 32) out += gone_w[i];
           all = warp_sum(lane < static_cast<int>(ctas) ? totals[lane] : 0) - warp_sum(out);
@@ -276,7 +359,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
           for (int i = lane; i < fallen; i += 32) out += gone_w[i];
           all -= warp_sum(out);
         }
-        next.total = product(chance[0], all);
+        next.total = share_of(chance[0], all);
         if (all == 0) next.op = kDone;
         if (lane == 0 && all == 0) raise_flag(p.flags, DEVFLAG_NO_MASS);
       }
@@ -297,38 +380,81 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
     // ---- sums of this CTA's tokens ----
     s_level = DRAWN ? c.level : 0;
     s_node = c.node;
-    s_rest = op == kRest;
+    s_rest = op == kRest || op == kRestLast;
     if (s_rest) {
       if (tid == 0) W[c.level] = c.total;
       __syncthreads();
     }
     const T* pr = p_rows + s_node * p.p_stride[1];
     const T* qr = DRAWN ? q_rows + s_node * p.q_stride[1] : nullptr;
-    const bool both = DRAWN && (s_rest || s_level > 0);
+    const int falls = DRAWN ? s_level + (s_rest ? 1 : 0) : 0;
+    const bool go_on = DRAWN && s_level > 0 && held == s_level && held_node == s_node;
+    const u64 total_w = c.total;
     u64 mine = 0;
     for (int t = warp; c0 + t * p.tile < c1; t += kWarps) {
       u64 sum = 0;
       const int end = min(c1, c0 + (t + 1) * p.tile);
       for (int b = c0 + t * p.tile; b < end; b += kSpan) {
-        T a[kPerLane], d[kPerLane];
+        float a[kPerLane], d[kPerLane];
+        const bool all = b + kSpan <= end, fits = DRAWN && b - c0 + kSpan <= p.kept;
+        u64* row_kept = kept + (b - c0 + lane);
+        if (falls == 0) {
+          read_span(pr, b + lane, end, all, a);
+          Halves s{0, 0};
 #pragma unroll
-        for (int k = 0; k < kPerLane; ++k) {
-          const int i = b + 32 * k + lane;
-          a[k] = d[k] = 0;
-          if (i < end) {
-            a[k] = pr[i];
-            if (both) d[k] = qr[i];
+          for (int k = 0; k < kPerLane; k += 2) {
+            Halves x, y;
+            prob_halves(make_float2(a[k], a[k + 1]), x, y);
+            s.hi += x.hi + y.hi;
+            s.lo += x.lo + y.lo;
           }
-        }
+          sum += whole(s, kPerLane);
+        } else if (falls == 1) {
+          read_span(pr, b + lane, end, all, a);
+          read_span(qr, b + lane, end, all, d);
+          Halves s{0, 0};
+          const bool keep = fits && op == kRest;
 #pragma unroll
-        for (int k = 0; k < kPerLane; ++k) {
-          const u64 w = fixed(value(a[k]));
-          sum += both ? left(w, fixed(value(d[k])), W, s_level, s_rest) : w;
+          for (int k = 0; k < kPerLane; k += 2) {
+            Halves x, y;
+            rest_halves(make_float2(a[k], a[k + 1]), make_float2(d[k], d[k + 1]), x, y);
+            s.hi += x.hi + y.hi;
+            s.lo += x.lo + y.lo;
+            if (keep) {
+              row_kept[32 * k] = whole(x, 1);
+              row_kept[32 * k + 32] = whole(y, 1);
+            }
+          }
+          sum += whole(s, kPerLane);
+        } else if (go_on && fits) {
+          read_span(qr, b + lane, end, all, d);
+#pragma unroll
+          for (int k = 0; k < kPerLane; ++k) {
+            u64 w = row_kept[32 * k];
+            if (s_rest) {
+              w = minus(w, product(d[k], total_w));
+              row_kept[32 * k] = w;
+            }
+            sum += w;
+          }
+        } else {
+          read_span(pr, b + lane, end, all, a);
+          read_span(qr, b + lane, end, all, d);
+#pragma unroll
+          for (int k = 0; k < kPerLane; ++k) {
+            const u64 w = left_rounded(a[k], d[k], W, s_level, s_rest);
+            if (fits) row_kept[32 * k] = w;
+            sum += w;
+          }
         }
       }
       sum = warp_sum(sum);
       if (lane == 0) sums[t] = sum;
       mine += sum;
+    }
+    if (falls > 1 || op == kRest) {
+      held = falls;
+      held_node = s_node;
     }
     if (lane == 0) part[warp] = mine;
     __syncthreads();
@@ -392,8 +518,8 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
     for (int k = 0; k < kPerLane; ++k) {
       w[k] = 0;
       if (i0 + k < end) {
-        w[k] = fixed(value(pr[i0 + k]));
-        if (both) w[k] = left(w[k], fixed(value(qr[i0 + k])), W, s_level, s_rest);
+        w[k] = left_rounded(value(pr[i0 + k]), both ? value(qr[i0 + k]) : 0.f, W, DRAWN ? s_level : 0,
+                            DRAWN && s_rest);
         for (int i = 0; i < n_gone; ++i)
           if (gone[i] == static_cast<u64>(i0 + k)) w[k] = 0;
       }
@@ -430,6 +556,7 @@ cudaError_t launch(const VerifyParams& p, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.S) * ctas);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = p.kept * sizeof(u64);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -442,6 +569,8 @@ cudaError_t prepare_draft_verify() {
   cudaError_t e = cudaSuccess;
   auto set = [&](const void* fn) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKept * sizeof(u64));
   };
   set(reinterpret_cast<const void*>(draft_verify_kernel<float, false>));
   set(reinterpret_cast<const void*>(draft_verify_kernel<float, true>));
@@ -452,12 +581,13 @@ cudaError_t prepare_draft_verify() {
 
 cudaError_t launch_draft_verify(VerifyParams p, bool bf16, int num_sms, cudaStream_t stream) {
   if (p.S <= 0) return cudaSuccess;
-  int ctas = p.S * 8 <= num_sms ? kMaxCtas : 8;
+  int ctas = kMaxCtas;
   while (ctas > 1 && p.V <= ctas / 2 * kSpan * kWarps) ctas /= 2;
   auto up = [](long long x, long long m) { return (x + m - 1) / m * m; };
   const long long share = (static_cast<long long>(p.V) + ctas - 1) / ctas;
   p.tile = static_cast<int>(up((share + kMaxTiles - 1) / kMaxTiles, kSpan));
   p.chunk = static_cast<int>(up(share, p.tile));
+  p.kept = p.q ? (p.chunk < kMaxKept ? p.chunk : kMaxKept) : 0;
   if (bf16)
     return p.q ? launch<uint16_t, true>(p, ctas, stream) : launch<uint16_t, false>(p, ctas, stream);
   return p.q ? launch<float, true>(p, ctas, stream) : launch<float, false>(p, ctas, stream);
