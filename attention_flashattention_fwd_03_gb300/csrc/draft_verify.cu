@@ -8,25 +8,28 @@
 // residual), kept without divisions.  The last token is drawn from w by where u times its
 // sum falls in the running sum.
 //
+// After several falls w is still one subtraction from p,
+//   w = max(p - A q, 0),  A = 1 + W_1 + W_2 + ..   (the W of the falls before),
+// as a value that has become 0 stays 0 and the others have only been subtracted from.  So a
+// sum over a row reads p and q and nothing else, whatever came before.
+//
 // A token hangs on which side of a border a random number lies, so sums must not depend on
 // an order and must be finer than fp32: they are sums of integers, which are exact in any
 // order.  A test of a token takes probabilities as multiples of 2^-62 (an fp32 from 2^-38 up
-// exactly) and products in 128 bits.  Sums over a row take the exact p, or max(p - q, 0), rounded
-// to a multiple of 2^-44 (5e-9 of a distribution over 2^17 tokens at the very most, 1e-11 as
-// roundings go): adding 2 to an fp32 below 1 and taking it off again rounds it to 2^-22,
-// what is left over goes the same way to 2^-44, and the bits of the two sums are the integers
-// to be added up.  That is 13 instructions a token, half of them on pairs; integers made by shifts take 45 (64
-// requests x 8 drafts, 131072 tokens: 104 us), the compiler's conversions to 64 bits, which run at the
-// rate of 64-bit floating point, more yet (159).
+// exactly) and products in 128 bits.  Sums over a row take max(p - A q, 0), computed as the sum
+// of two fp32, rounded to a multiple of 2^-44 (roundings of 2^17 tokens add up to 1e-11 as they
+// go, 5e-9 at the very most): adding 2 to an fp32 below 1 and taking it off again rounds it to
+// 2^-22, what is left over goes the same way to 2^-44, and the bits of the two sums are the
+// integers to be added up.  That is some 16 instructions a token, most of them on pairs.
 //
-// A cluster of CTAs takes a request.  CTA 0 leads: it reads the tree and, for all nodes at
-// once, the two probabilities that a test of the node would need, and walks down the tree
-// in registers and shared memory.  Only where a child falls, or at the end, all V values of
-// a row (or two) are needed: CTA c then sums tokens [c chunk, (c + 1) chunk), a warp a tile
-// of them at a time, keeps the tiles' sums, and puts its sum into every CTA's shared memory.
-// The leader tells the others what to do next, so the control flow, and with it the number
-// of cluster barriers that each CTA meets, is decided in one place.  The last token's CTA is found from the CTAs' sums,
-// its tile from the tiles' sums, and only that tile is read again.
+// A cluster of CTAs takes a request.  CTA 0 reads the tree and, for all nodes at once, the two
+// probabilities that a test of the node would need, and writes them into the others' shared
+// memory; every CTA then walks down the tree for itself, from the same data to the same
+// decisions.  Only where a child falls, or at the end, all V values of a row (or two) are
+// needed: CTA c then sums tokens [c chunk, (c + 1) chunk), a warp a tile of them at a time, keeps
+// the tiles' sums, and puts its sum into every CTA's shared memory, with one cluster barrier.
+// The last token's CTA is found from the CTAs' sums, its tile from the tiles' sums, and only
+// that tile is read again.
 #include <cuda_runtime.h>
 
 #include <cstring>
@@ -44,14 +47,15 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxNodes = GBATTN_TREE_MAX_NODES;
 static_assert(kThreads == kMaxNodes, "a thread a node");
 constexpr int kMaxCtas = 16;   // of a cluster
+constexpr int kCtasPerSm = 4;
 constexpr int kPerLane = 16;   // values of a row that a lane reads at once
 constexpr int kSpan = 32 * kPerLane;
 constexpr int kMaxTiles = 256;
-constexpr int kMaxKept = 16384;  // tokens of a CTA whose w is kept from fall to fall (128 KB)
-static_assert(kMaxKept % kSpan == 0, "whole spans");
 
 using u64 = unsigned long long;
-constexpr u64 kOne = 1ull << 62;
+constexpr u64 kOne = 1ull << 62;   // 1 as a multiple of 2^-62 (probabilities, W)
+constexpr u64 kUnit = 1ull << 54;  // 1 as a multiple of 2^-54 (A, which may come to 256)
+constexpr int kToUnit = 8;         // bits between the two
 
 // A probability (or random number) as a multiple of 2^-62; NaN and negative values are 0.
 // The significand goes to the top of 64 bits and down by the exponent (PTX shifts by 32 and
@@ -78,13 +82,17 @@ __device__ __forceinline__ u64 product(float q, u64 W) {
   asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(high), "r"(126u - e));  // (by 64 and more: 0)
   return e == 127u ? W : r;
 }
-__device__ __forceinline__ u64 minus(u64 a, u64 b) { return a > b ? a - b : 0; }
 // a b 2^-62, rounded down.
 __device__ __forceinline__ u64 share_of(u64 a, u64 b) { return (__umul64hi(a, b) << 2) | ((a * b) >> 62); }
 // Whether a b 2^-62 < c, exactly.
 __device__ __forceinline__ bool product_below(u64 a, u64 b, u64 c) {
   const u64 hi = __umul64hi(a, b), lo = a * b;
   return hi < c >> 2 || (hi == c >> 2 && lo < c << 62);
+}
+// max(p - A q, 0) of one token.
+__device__ __forceinline__ u64 left(float p, float q, u64 A) {
+  const u64 w = fixed(p), off = product(q, A);
+  return off >= 2 * kUnit || off << kToUnit >= w ? 0 : w - (off << kToUnit);
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
@@ -127,22 +135,8 @@ __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
 __device__ __forceinline__ void store_remote(uint32_t a, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
-
-// What the leader has the cluster do.  kRest: sum of what is left once W q is taken off, and
-// kept as there is another child to try; kRestLast: there is none.
-enum : int { kDone, kScan, kRest, kRestLast, kDraw };
-struct Command {
-  int op, node, level, count;
-  u64 total;  // kRest: W; kDraw: where the random number falls in the running sum
-};
-static_assert(sizeof(Command) == 24, "three words");
-
-// w of one token after `level` falls, and less W q if `rest`.
-__device__ __forceinline__ u64 left(float p, float q, const u64* W, int level, bool rest) {
-  u64 w = fixed(p);
-  const int n = level + (rest ? 1 : 0);
-  for (int i = 0; i < n; ++i) w = minus(w, i == 0 ? fixed(q) : product(q, W[i]));  // W[0] = 1
-  return w;
+__device__ __forceinline__ void store_remote(uint32_t a, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
 // The sums' form of values in [0, 1]: hi 2^-22 + lo 2^-44 (added up modulo 2^32, with an offset
@@ -156,38 +150,43 @@ __device__ __forceinline__ u64 whole(Halves h, uint32_t n) {  // of n values, as
   const int lo = static_cast<int>(h.lo - n * kLoOffset);
   return static_cast<u64>((hi << 22) + lo) << 18;
 }
-// Of d + e for a pair of values, |e| half a unit of d's last place at most.
+// Of d + e for a pair of values, |e| below 2^-23.
 __device__ __forceinline__ void halves(float2 d, float2 e, Halves& x, Halves& y) {
   const float2 t = __fadd2_rn(d, make_float2(2.f, 2.f));
   const float2 back = __fadd2_rn(t, make_float2(-2.f, -2.f));
-  const float2 r = __fadd2_rn(d, make_float2(-back.x, -back.y));  // exact
+  const float2 r = __fadd2_rn(d, make_float2(-back.x, -back.y));  // exact, 2^-23 at most
   const float2 u = __fadd2_rn(__fadd2_rn(r, e), make_float2(0x1.8p-21f, 0x1.8p-21f));
   x = Halves{__float_as_uint(t.x), __float_as_uint(u.x)};
   y = Halves{__float_as_uint(t.y), __float_as_uint(u.y)};
 }
-// Of max(p - q, 0): where p > q, p - q is d + e exactly.
-__device__ __forceinline__ void rest_halves(float2 p, float2 q, Halves& x, Halves& y) {
+// Of max(p - A q, 0), A as the sum of two fp32 (hi, lo): A q = t + l with l = the product's
+// rounding error + lo q; where p > t, p - t is d + an error that is computed exactly.
+template <bool FALLEN>
+__device__ __forceinline__ void left_halves(float2 p, float2 q, float2 A, Halves& x, Halves& y) {
   p = make_float2(__saturatef(p.x), __saturatef(p.y));
-  q = make_float2(-__saturatef(q.x), -__saturatef(q.y));
-  float2 d = __fadd2_rn(p, q);
-  float2 e = __fadd2_rn(__fadd2_rn(p, make_float2(-d.x, -d.y)), q);
-  e = make_float2(d.x > 0.f ? e.x : 0.f, d.y > 0.f ? e.y : 0.f);
-  halves(make_float2(fmaxf(d.x, 0.f), fmaxf(d.y, 0.f)), e, x, y);
+  if constexpr (!FALLEN) {
+    halves(p, make_float2(0.f, 0.f), x, y);
+  } else {
+    q = make_float2(-__saturatef(q.x), -__saturatef(q.y));
+    const float2 h = make_float2(A.x, A.x), lo = make_float2(A.y, A.y);
+    const float2 t = __fmul2_rn(q, h);
+    const float2 l = __ffma2_rn(q, lo, __ffma2_rn(q, h, make_float2(-t.x, -t.y)));
+    const float2 d = __fadd2_rn(p, t);
+    float2 e = __fadd2_rn(__fadd2_rn(__fadd2_rn(p, make_float2(-d.x, -d.y)), t), l);
+    const float2 s = __fadd2_rn(d, e);
+    const bool x_left = fminf(d.x, s.x) > 0.f, y_left = fminf(d.y, s.y) > 0.f;
+    halves(make_float2(x_left ? d.x : 0.f, y_left ? d.y : 0.f),
+           make_float2(x_left ? e.x : 0.f, y_left ? e.y : 0.f), x, y);
+  }
 }
-__device__ __forceinline__ void prob_halves(float2 p, Halves& x, Halves& y) {
-  halves(make_float2(__saturatef(p.x), __saturatef(p.y)), make_float2(0.f, 0.f), x, y);
-}
-// w of one token in that form, after `level` falls and less W q if `rest`.
-__device__ __forceinline__ u64 left_rounded(float p, float q, const u64* W, int level, bool rest) {
-  const int n = level + (rest ? 1 : 0);
+// The same of one token.
+__device__ __forceinline__ u64 left_rounded(float p, float q, float2 A, bool fallen) {
   Halves x, y;
-  if (n == 0)
-    prob_halves(make_float2(p, 0.f), x, y);
+  if (fallen)
+    left_halves<true>(make_float2(p, 0.f), make_float2(q, 0.f), A, x, y);
   else
-    rest_halves(make_float2(p, 0.f), make_float2(q, 0.f), x, y);
-  u64 w = whole(x, 1);
-  for (int i = 1; i < n; ++i) w = minus(w, product(q, W[i]));
-  return w;
+    left_halves<false>(make_float2(p, 0.f), make_float2(0.f, 0.f), A, x, y);
+  return whole(x, 1);
 }
 
 // kPerLane values of a row from `i` on, 32 apart; those from `end` on are 0.
@@ -205,289 +204,251 @@ __device__ __forceinline__ void read_span(const T* row, int i, int end, bool all
   }
 }
 
+// This warp's part of the sums of a span of tokens.
+template <typename T, bool FALLEN>
+__device__ __forceinline__ u64 span_sum(const T* pr, const T* qr, int b, int end, float2 A) {
+  const int i = b + (threadIdx.x & 31);
+  const bool all = b + kSpan <= end;
+  float a[kPerLane], d[kPerLane];
+  read_span(pr, i, end, all, a);
+  if (FALLEN) read_span(qr, i, end, all, d);
+  Halves s{0, 0};
+#pragma unroll
+  for (int k = 0; k < kPerLane; k += 2) {
+    Halves x, y;
+    left_halves<FALLEN>(make_float2(a[k], a[k + 1]),
+                        FALLEN ? make_float2(d[k], d[k + 1]) : make_float2(0.f, 0.f), A, x, y);
+    s.hi += x.hi + y.hi;
+    s.lo += x.lo + y.lo;
+  }
+  return whole(s, kPerLane);
+}
+
+// What a walk decides: the sums of max(p - A q, 0) at a node, or the draw.
+enum : int { kDone, kSum, kDraw };
+struct Step {
+  int op, node;
+  u64 A;  // kDraw: where the random number falls in the running sum
+};
+
 template <typename T, bool DRAWN>
-__global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(const VerifyParams p) {
   __shared__ int parent[kMaxNodes], token[kMaxNodes], path[kMaxNodes];
-  __shared__ u64 chance[kMaxNodes];                    // u, p and q of every node
+  __shared__ u64 chance[kMaxNodes];            // u, p and q of every node
   __shared__ float pv[kMaxNodes], qv[kMaxNodes];
-  __shared__ u64 W[kMaxNodes];           // sums of w by level
-  __shared__ u64 sums[kMaxTiles];        // of this CTA's tiles
-  __shared__ u64 totals[kMaxCtas];       // of all CTAs
+  __shared__ u64 sums[kMaxTiles];              // of this CTA's tiles
+  __shared__ u64 totals[2][kMaxCtas];          // of all CTAs, of the last two sums
   __shared__ u64 part[kWarps];
-  __shared__ Command cmd;
-  __shared__ u64 gone[DRAWN ? 1 : kMaxNodes], gone_w[DRAWN ? 1 : kMaxNodes];  // fallen tokens
-  extern __shared__ u64 kept[];          // w of the CTA's first p.kept tokens, as of `held` falls
-  const uint32_t ctas = cluster_size(), rank = cluster_rank();
+  __shared__ int nodes;
+  __shared__ Step step;
+  __shared__ u64 gone[DRAWN ? 1 : kMaxNodes];  // without a draft: the tokens that have fallen at
+  __shared__ u64 gone_w[DRAWN ? 1 : kMaxNodes];  // the node, and what they have in the sums
+  const int ctas = cluster_size(), rank = cluster_rank();
   const int r = blockIdx.x / ctas;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  cluster_arrive();  // every CTA's shared memory may be written once all are past the wait
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   const T* p_rows = static_cast<const T*>(p.p) + r * p.p_stride[0];
   const T* q_rows = DRAWN ? static_cast<const T*>(p.q) + r * p.q_stride[0] : nullptr;
-  int n = 0;
+  cluster_arrive();  // (shared memory of another CTA may be written once it has started)
   if (rank == 0) {
-    n = p.tree_lens ? p.tree_lens[r] : p.Tn;
-    const bool bad_n = n < 0 || n > p.Tn;
-    if (bad_n) n = 0;
     const size_t row = static_cast<size_t>(r) * p.Tn;
-    bool bad = false;
-    if (tid < n) {
-      const int up = p.parents[row + tid], x = p.tokens[row + tid];
-      parent[tid] = up;
-      token[tid] = x;
-      chance[tid] = fixed(p.uniforms[row + tid]);
-      bad = up < -1 || up >= tid;
-      float a = 0.f, b = 0.f;
-      if (!bad && up >= 0 && x >= 0 && x < p.V) {
-        a = value(p_rows[up * p.p_stride[1] + x]);
-        if (DRAWN) b = value(q_rows[up * p.q_stride[1] + x]);
-      }
-      pv[tid] = a;
-      qv[tid] = DRAWN ? b : 1.f;
+    int n = p.Tn, up = -1, x = -1;
+    float u = 0.f, a = 0.f, b = DRAWN ? 0.f : 1.f;
+    if (p.tree_lens) n = p.tree_lens[r];
+    if (tid < p.Tn) {
+      up = p.parents[row + tid];
+      x = p.tokens[row + tid];
+      u = p.uniforms[row + tid];
+    }
+    const bool bad_n = n < 0 || n > p.Tn;
+    const bool bad = !bad_n && tid < n && (up < -1 || up >= tid);
+    if (!bad_n && !bad && tid < n && up >= 0 && x >= 0 && x < p.V) {
+      a = value(p_rows[up * p.p_stride[1] + x]);
+      if (DRAWN) b = value(q_rows[up * p.q_stride[1] + x]);
     }
     const bool bad_tree = __syncthreads_or(bad);
     if ((bad_n || bad_tree) && tid == 0) raise_flag(p.flags, bad_n ? DEVFLAG_BAD_SEQLEN : DEVFLAG_BAD_TREE);
-    if (bad_tree) n = 0;
+    if (bad_n || bad_tree) n = 0;
     if (tid == 0) path[0] = 0;
+    cluster_wait();
+    for (int c = 0; c < ctas; ++c) {
+      if (tid == 0) store_remote(remote(&nodes, c), static_cast<uint32_t>(n));
+      if (tid >= n) continue;
+      store_remote(remote(&parent[tid], c), static_cast<uint32_t>(up));
+      store_remote(remote(&token[tid], c), static_cast<uint32_t>(x));
+      store_remote(remote(&chance[tid], c), fixed(u));
+      store_remote(remote(&pv[tid], c), __float_as_uint(a));
+      store_remote(remote(&qv[tid], c), __float_as_uint(b));
+    }
+  } else {
+    cluster_wait();
   }
+  cluster_arrive();
   cluster_wait();
+  const int n = nodes;
 
-  // the leader's walk (warp 0 of CTA 0)
-  int cur = 0, at = 0, level = 0, fallen = 0, count = n > 0 ? 1 : 0;
-  u64 total = kOne;
-  enum { kNothing, kRested, kSummed, kLast } waiting = kNothing;
+  // the walk (warp 0)
+  int cur = 0, at = 0, fallen = 0, count = n > 0 ? 1 : 0;
+  u64 A = 0, W = kOne;
+  enum { kNothing, kAfterFall, kFalls, kLast } waiting = kNothing;
   bool summed = false;  // the last sums are those of the present w
-  int op = kDone, s_level = 0, s_node = 0;
-  bool s_rest = false;
-  int held = 0, held_node = -1;
+  int buffer = 0;       // of totals that the next sums go to
+  Step now{kDone, 0, 0};
+  float2 A2 = make_float2(0.f, 0.f);
   const int c0 = rank * p.chunk, c1 = min(p.V, c0 + p.chunk);  // (chunk * ctas < 2^31)
+  auto all_sum = [&]() {  // over the row, less what has fallen; by a whole warp
+    u64 v = lane < ctas ? totals[buffer ^ 1][lane] : 0;
+    if (!DRAWN)
+      for (int i = lane; i < fallen; i += 32) v -= gone_w[i];  // (modulo 2^64)
+    return warp_sum(v);
+  };
 
   for (;;) {
-    if (rank == 0 && warp == 0) {
-      Command next{kDone, cur, 0, count, 0};
-      u64 all = 0;
-      if (waiting != kNothing) {
-        all = warp_sum(lane < static_cast<int>(ctas) ? totals[lane] : 0);
-        summed = true;
-        if (waiting == kRested) {
-          if (all > 0) {
-            total = all;
-            ++level;
-          } else {
-            summed = false;
-          }
+    if (warp == 0) {
+      Step next{kDone, cur, 0};
+      bool again = waiting == kFalls;  // child `at` is known to fall
+      if (waiting == kAfterFall) {
+        const u64 all = all_sum();
+        summed = all > 0;
+        if (summed) {
+          A += W >> kToUnit;
+          W = all;
         }
+      } else if (waiting != kNothing) {
+        summed = true;
       }
-      bool again = waiting == kSummed;  // child `at` has been found to fall already
       waiting = kNothing;
-      if (n > 0) {
-        for (;;) {
-          if (!again) {
-            // the next child of the node reached
-            int found = -1;
-            for (int b = (at + 1) & ~31; b < n && found < 0; b += 32) {
-              const int i = b + lane;
-              const unsigned hit = __ballot_sync(0xffffffffu, i > at && i < n && parent[i] == cur);
-              if (hit) found = b + __ffs(hit) - 1;
-            }
-            if (found < 0) {
-              next.op = summed ? kDraw : kScan;
-              waiting = kLast;
-              break;
-            }
-            at = found;
+      while (n > 0) {
+        if (!again) {
+          // the next child of the node reached
+          int found = -1;
+          for (int b = (at + 1) & ~31; b < n && found < 0; b += 32) {
+            const int i = b + lane;
+            const unsigned hit = __ballot_sync(0xffffffffu, i > at && i < n && parent[i] == cur);
+            if (hit) found = b + __ffs(hit) - 1;
           }
-          const float q = qv[at];
-          u64 w = left(pv[at], q, W, DRAWN ? level : 0, false);
+          if (found < 0) {
+            next.op = summed ? kDraw : kSum;
+            next.A = A;
+            waiting = kLast;
+            break;
+          }
+          at = found;
+          u64 w = left(pv[at], qv[at], A);
           if (!DRAWN) {
-            const u64 x = static_cast<u64>(token[at]);
             bool hit = false;
-            for (int i = lane; i < fallen; i += 32) hit |= gone[i] == x;
-            if (__any_sync(0xffffffffu, hit)) w = 0;
+            for (int i = lane; i < fallen; i += 32) hit |= gone[i] == static_cast<u64>(token[at]);
+            w = __any_sync(0xffffffffu, hit) ? 0 : fixed(pv[at]);
           }
-          if (!again && product_below(chance[at], product(q, total), w)) {
+          if (product_below(chance[at], product(qv[at], W), w)) {
+            __syncwarp();
             if (lane == 0) path[count] = at;
             ++count;
-            cur = at;
-            level = fallen = 0;
-            total = kOne;
+            cur = next.node = at;
+            fallen = 0;
+            A = 0;
+            W = kOne;
             summed = false;
             continue;
           }
-          if (DRAWN) {
-            bool more = false;
-            for (int b = at & ~31; b < n; b += 32)
-              more |= b + lane > at && b + lane < n && parent[b + lane] == cur;
-            next.op = __any_sync(0xffffffffu, more) ? kRest : kRestLast;
-            waiting = kRested;
-            break;
-          }
-          if (!summed) {
-            next.op = kScan;
-            waiting = kSummed;
-            break;
-          }
-          // without a draft the token itself is what falls, in the sums' form
-          again = false;
-          if (w > 0) w = left_rounded(pv[at], 0.f, W, 0, false);
-          u64 out = 0;
-          for (int i = lane; i < fallen; i += 32) out += gone_w[i];
-          all = warp_sum(lane < static_cast<int>(ctas) ? totals[lane] : 0) - warp_sum(out);
-          if (all > w) {
-            total = all - w;
-            if (w > 0) {
-              if (lane < static_cast<int>(ctas)) {
-                store_remote(remote(&gone[fallen], lane), static_cast<u64>(token[at]));
-                store_remote(remote(&gone_w[fallen], lane), w);
-              }
-              __syncwarp();
-              ++fallen;
+        }
+        again = false;
+        if (DRAWN) {
+          next.op = kSum;
+          next.A = A + (W >> kToUnit);
+          waiting = kAfterFall;
+          break;
+        }
+        if (!summed) {
+          next.op = kSum;
+          waiting = kFalls;
+          break;
+        }
+        // without a draft it is the token itself that falls, with what it has in the sums
+        const u64 x = static_cast<u64>(token[at]);
+        bool hit = false;
+        for (int i = lane; i < fallen; i += 32) hit |= gone[i] == x;
+        const u64 w = __any_sync(0xffffffffu, hit) ? 0 : left_rounded(pv[at], 0.f, A2, false);
+        const u64 all = all_sum();
+        if (all > w) {
+          W = all - w;
+          if (w > 0) {
+            if (lane == 0) {
+              gone[fallen] = x;
+              gone_w[fallen] = w;
             }
+            ++fallen;
+            __syncwarp();
           }
         }
       }
-      next.node = cur;
-      next.count = count;
-      next.level = DRAWN ? level : fallen;
-      next.total = total;
       if (next.op == kDraw) {
-        all = warp_sum(lane < static_cast<int>(ctas) ? totals[lane] : 0);
-        if (!DRAWN) {
-          u64 out = 0;
-          for (int i = lane; i < fallen; i += 32) out += gone_w[i];
-          all -= warp_sum(out);
+        const u64 all = all_sum();
+        next.A = share_of(chance[0], all);
+        if (all == 0) {
+          next.op = kDone;
+          if (rank == 0 && lane == 0) raise_flag(p.flags, DEVFLAG_NO_MASS);
         }
-        next.total = share_of(chance[0], all);
-        if (all == 0) next.op = kDone;
-        if (lane == 0 && all == 0) raise_flag(p.flags, DEVFLAG_NO_MASS);
       }
-      if (lane < static_cast<int>(ctas)) {
-        u64 words[3];
-        memcpy(words, &next, sizeof words);
-        const uint32_t to = remote(&cmd, lane);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) store_remote(to + 8 * i, words[i]);
-      }
+      if (lane == 0) step = next;
     }
-    cluster_arrive();
-    cluster_wait();
-    const Command c = cmd;
-    op = c.op;
-    if (op == kDone || op == kDraw) break;
+    __syncthreads();
+    if (step.op != kSum) break;
 
     // ---- sums of this CTA's tokens ----
-    s_level = DRAWN ? c.level : 0;
-    s_node = c.node;
-    s_rest = op == kRest || op == kRestLast;
-    if (s_rest) {
-      if (tid == 0) W[c.level] = c.total;
-      __syncthreads();
-    }
-    const T* pr = p_rows + s_node * p.p_stride[1];
-    const T* qr = DRAWN ? q_rows + s_node * p.q_stride[1] : nullptr;
-    const int falls = DRAWN ? s_level + (s_rest ? 1 : 0) : 0;
-    const bool go_on = DRAWN && s_level > 0 && held == s_level && held_node == s_node;
-    const u64 total_w = c.total;
+    now = step;
+    A2.x = __ull2float_rn(now.A) * 0x1p-54f;
+    A2.y = __ll2float_rn(static_cast<long long>(now.A) - __float2ll_rn(A2.x * 0x1p54f)) * 0x1p-54f;
+    const T* pr = p_rows + now.node * p.p_stride[1];
+    const T* qr = DRAWN ? q_rows + now.node * p.q_stride[1] : nullptr;
     u64 mine = 0;
     for (int t = warp; c0 + t * p.tile < c1; t += kWarps) {
       u64 sum = 0;
       const int end = min(c1, c0 + (t + 1) * p.tile);
-      for (int b = c0 + t * p.tile; b < end; b += kSpan) {
-        float a[kPerLane], d[kPerLane];
-        const bool all = b + kSpan <= end, fits = DRAWN && b - c0 + kSpan <= p.kept;
-        u64* row_kept = kept + (b - c0 + lane);
-        if (falls == 0) {
-          read_span(pr, b + lane, end, all, a);
-          Halves s{0, 0};
-#pragma unroll
-          for (int k = 0; k < kPerLane; k += 2) {
-            Halves x, y;
-            prob_halves(make_float2(a[k], a[k + 1]), x, y);
-            s.hi += x.hi + y.hi;
-            s.lo += x.lo + y.lo;
-          }
-          sum += whole(s, kPerLane);
-        } else if (falls == 1) {
-          read_span(pr, b + lane, end, all, a);
-          read_span(qr, b + lane, end, all, d);
-          Halves s{0, 0};
-          const bool keep = fits && op == kRest;
-#pragma unroll
-          for (int k = 0; k < kPerLane; k += 2) {
-            Halves x, y;
-            rest_halves(make_float2(a[k], a[k + 1]), make_float2(d[k], d[k + 1]), x, y);
-            s.hi += x.hi + y.hi;
-            s.lo += x.lo + y.lo;
-            if (keep) {
-              row_kept[32 * k] = whole(x, 1);
-              row_kept[32 * k + 32] = whole(y, 1);
-            }
-          }
-          sum += whole(s, kPerLane);
-        } else if (go_on && fits) {
-          read_span(qr, b + lane, end, all, d);
-#pragma unroll
-          for (int k = 0; k < kPerLane; ++k) {
-            u64 w = row_kept[32 * k];
-            if (s_rest) {
-              w = minus(w, product(d[k], total_w));
-              row_kept[32 * k] = w;
-            }
-            sum += w;
-          }
-        } else {
-          read_span(pr, b + lane, end, all, a);
-          read_span(qr, b + lane, end, all, d);
-#pragma unroll
-          for (int k = 0; k < kPerLane; ++k) {
-            const u64 w = left_rounded(a[k], d[k], W, s_level, s_rest);
-            if (fits) row_kept[32 * k] = w;
-            sum += w;
-          }
-        }
-      }
+      for (int b = c0 + t * p.tile; b < end; b += kSpan)
+        sum += DRAWN && now.A != 0 ? span_sum<T, DRAWN>(pr, qr, b, end, A2)
+                                   : span_sum<T, false>(pr, qr, b, end, A2);
       sum = warp_sum(sum);
       if (lane == 0) sums[t] = sum;
       mine += sum;
-    }
-    if (falls > 1 || op == kRest) {
-      held = falls;
-      held_node = s_node;
     }
     if (lane == 0) part[warp] = mine;
     __syncthreads();
     if (warp == 0) {
       mine = warp_sum(lane < kWarps ? part[lane] : 0);
-      if (lane < static_cast<int>(ctas)) store_remote(remote(&totals[rank], lane), mine);
+      if (lane < ctas) store_remote(remote(&totals[buffer][rank], lane), mine);
     }
+    // (a CTA writes a buffer again two sums on: every other one has then read it)
+    buffer ^= 1;
     cluster_arrive();
     cluster_wait();
   }
 
   // ---- results ----
-  const Command c = cmd;
+  const Step last = step;
   const size_t row = static_cast<size_t>(r) * p.Tn;
+  if (warp != 0) return;
   if (rank == 0) {
-    for (int j = tid; j < p.Tn; j += kThreads) {
-      p.path[row + j] = j < c.count ? path[j] : -1;
-      if (op == kDone || j != c.count - 1)  // (the last token is written by its CTA)
-        p.tokens_out[row + j] = j < c.count - 1 ? token[path[j + 1]] : -1;
+    for (int j = lane; j < p.Tn; j += 32) {
+      p.path[row + j] = j < count ? path[j] : -1;
+      if (last.op == kDone || j != count - 1)  // (the last token is written by its CTA)
+        p.tokens_out[row + j] = j < count - 1 ? token[path[j + 1]] : -1;
     }
-    if (tid == 0) p.counts[r] = c.count;
+    if (lane == 0) p.counts[r] = count;
   }
-  if (op != kDraw || warp != 0) return;
-  // the CTA whose tokens the running sum passes c.total in
-  const int n_gone = DRAWN ? 0 : c.level;
-  u64 own = lane < static_cast<int>(ctas) ? totals[lane] : 0;
+  if (last.op != kDraw) return;
+  // the CTA whose tokens the running sum passes the drawn place in
+  const int n_gone = DRAWN ? 0 : fallen;
+  u64 own = lane < ctas ? totals[buffer ^ 1][lane] : 0;
   for (int i = 0; i < n_gone; ++i)
     if (static_cast<int>(gone[i]) / p.chunk == lane) own -= gone_w[i];
-  u64 upto = warp_prefix(own);
+  const u64 upto = warp_prefix(own);
   const u64 begin = __shfl_sync(0xffffffffu, upto - own, rank);
   const u64 stop = __shfl_sync(0xffffffffu, upto, rank);
-  if (c.total < begin || c.total >= stop) return;
-  u64 rest = c.total - begin;
+  if (last.A < begin || last.A >= stop) return;
+  u64 rest = last.A - begin;
   // its tile
   const int tiles = (c1 - c0 + p.tile - 1) / p.tile;
   int t = -1;
@@ -507,9 +468,9 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
     }
   }
   // its token: a lane's values are neighbours
-  const T* pr = p_rows + s_node * p.p_stride[1];
-  const T* qr = DRAWN ? q_rows + s_node * p.q_stride[1] : nullptr;
-  const bool both = DRAWN && (s_rest || s_level > 0);
+  const T* pr = p_rows + now.node * p.p_stride[1];
+  const T* qr = DRAWN ? q_rows + now.node * p.q_stride[1] : nullptr;
+  const bool subtract = DRAWN && now.A != 0;
   const int end = min(c1, c0 + (t + 1) * p.tile);
   for (int b = c0 + t * p.tile; t >= 0 && b < end; b += kSpan) {
     u64 w[kPerLane], sum = 0;
@@ -518,8 +479,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
     for (int k = 0; k < kPerLane; ++k) {
       w[k] = 0;
       if (i0 + k < end) {
-        w[k] = left_rounded(value(pr[i0 + k]), both ? value(qr[i0 + k]) : 0.f, W, DRAWN ? s_level : 0,
-                            DRAWN && s_rest);
+        w[k] = left_rounded(value(pr[i0 + k]), subtract ? value(qr[i0 + k]) : 0.f, A2, subtract);
         for (int i = 0; i < n_gone; ++i)
           if (gone[i] == static_cast<u64>(i0 + k)) w[k] = 0;
       }
@@ -537,7 +497,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
           s += w[k];
           if (before && s > rest) x = i0 + k;
         }
-        p.tokens_out[row + c.count - 1] = x;
+        p.tokens_out[row + count - 1] = x;
       }
       return;
     }
@@ -556,7 +516,6 @@ cudaError_t launch(const VerifyParams& p, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.S) * ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = p.kept * sizeof(u64);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -569,8 +528,6 @@ cudaError_t prepare_draft_verify() {
   cudaError_t e = cudaSuccess;
   auto set = [&](const void* fn) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKept * sizeof(u64));
   };
   set(reinterpret_cast<const void*>(draft_verify_kernel<float, false>));
   set(reinterpret_cast<const void*>(draft_verify_kernel<float, true>));
@@ -582,12 +539,12 @@ cudaError_t prepare_draft_verify() {
 cudaError_t launch_draft_verify(VerifyParams p, bool bf16, int num_sms, cudaStream_t stream) {
   if (p.S <= 0) return cudaSuccess;
   int ctas = kMaxCtas;
+  while (ctas > 1 && static_cast<long long>(p.S) * ctas > kCtasPerSm * num_sms) ctas /= 2;
   while (ctas > 1 && p.V <= ctas / 2 * kSpan * kWarps) ctas /= 2;
   auto up = [](long long x, long long m) { return (x + m - 1) / m * m; };
   const long long share = (static_cast<long long>(p.V) + ctas - 1) / ctas;
   p.tile = static_cast<int>(up((share + kMaxTiles - 1) / kMaxTiles, kSpan));
   p.chunk = static_cast<int>(up(share, p.tile));
-  p.kept = p.q ? (p.chunk < kMaxKept ? p.chunk : kMaxKept) : 0;
   if (bf16)
     return p.q ? launch<uint16_t, true>(p, ctas, stream) : launch<uint16_t, false>(p, ctas, stream);
   return p.q ? launch<float, true>(p, ctas, stream) : launch<float, false>(p, ctas, stream);

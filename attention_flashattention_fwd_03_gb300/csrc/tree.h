@@ -47,7 +47,6 @@ struct VerifyParams {
   int32_t* counts;             // [S]
   int S, Tn, V;
   int chunk, tile;             // tokens of a CTA, and of a sum that it keeps (launcher)
-  int kept;                    // tokens of a CTA whose remainder it keeps (launcher)
   unsigned* flags;
 };
 
