@@ -87,10 +87,10 @@ int encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
 int encode_bf16(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* base,
                 int rank, const uint64_t* dims, const uint64_t* strides_bytes,
                 const uint32_t* box) {
-  cuuint64_t gdim[3];
-  cuuint64_t gstride[2];
-  cuuint32_t bdim[3];
-  cuuint32_t estride[3] = {1, 1, 1};
+  cuuint64_t gdim[4];
+  cuuint64_t gstride[3];
+  cuuint32_t bdim[4];
+  cuuint32_t estride[4] = {1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     gdim[i] = dims[i];
     bdim[i] = box[i];

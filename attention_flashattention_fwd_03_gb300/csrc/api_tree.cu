@@ -25,12 +25,12 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
 }
 
 // Whether the kernels' 32-bit counts hold a call of these sizes: query rows, and steps of
-// 128 keys of every (request, KV head, 256 rows).
+// 128 keys of every (request, KV head, two row tiles).
 bool tree_fits(int S, int Tn, int Hq, int Hkv, int max_seq_len) {
   const unsigned __int128 rows = static_cast<unsigned __int128>(S) * Hq * Tn;
-  const uint64_t group_rows = static_cast<uint64_t>(Hq / Hkv) * Tn;
   const uint64_t tiles = (static_cast<uint64_t>(max_seq_len) + 127) / 128 + 1;
-  const unsigned __int128 segs = static_cast<unsigned __int128>(S) * Hkv * ((group_rows + 255) / 256);
+  const int nodes = Tn > 0 ? tree_tile_nodes(Hq / Hkv, Tn) : 1;
+  const unsigned __int128 segs = static_cast<unsigned __int128>(S) * Hkv * ((Tn + nodes - 1) / nodes);
   return rows < kMaxDim && segs * tiles < kMaxDim;
 }
 
@@ -39,7 +39,7 @@ bool tree_fits(int S, int Tn, int Hq, int Hkv, int max_seq_len) {
 GBATTN_API size_t paged_attn_tree_workspace_size(int num_seqs, int Tn, int Hq, int Hkv, int D,
                                                  int max_seq_len) {
   if (num_seqs <= 0 || Tn <= 0 || Tn > GBATTN_TREE_MAX_NODES || Hq <= 0 || Hkv <= 0 ||
-      Hq % Hkv != 0 || (D != 64 && D != 128) || max_seq_len < 0 ||
+      Hq % Hkv != 0 || Hq / Hkv > 128 || (D != 64 && D != 128) || max_seq_len < 0 ||
       !tree_fits(num_seqs, Tn, Hq, Hkv, max_seq_len))
     return 0;
   return tree_attn_workspace_bytes(num_seqs, Tn, Hq, Hkv, D, max_seq_len);
@@ -56,7 +56,7 @@ GBATTN_API int paged_attn_tree(const void* q, const void* k_pool, const void* v_
       num_pool_blocks <= 0 || max_seq_len < 0)
     return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
-  if (block_size != 16 || (D != 64 && D != 128) || Tn > GBATTN_TREE_MAX_NODES)
+  if (block_size != 16 || (D != 64 && D != 128) || Tn > GBATTN_TREE_MAX_NODES || Hq / Hkv > 128)
     return ATTN_ERR_UNSUPPORTED;
   if (num_seqs == 0 || Tn == 0) return ATTN_OK;
   if (!q || !k_pool || !v_pool || !block_table || !seq_lens || !parents || !o)
@@ -78,13 +78,17 @@ GBATTN_API int paged_attn_tree(const void* q, const void* k_pool, const void* v_
   PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
   if ((st = encoder(&enc)) != ATTN_OK) return st;
   CUtensorMap tmQ, tmK, tmV;
-  const uint64_t row_bytes = static_cast<uint64_t>(D) * 2, rows = static_cast<uint64_t>(Hq / Hkv) * Tn;
-  const uint64_t q_strides[2] = {row_bytes, row_bytes * rows}, pool_strides[1] = {row_bytes};
-  const uint32_t q_box[3] = {64, 128, 1}, pool_box[2] = {64, 16};
-  const uint64_t dq[3] = {static_cast<uint64_t>(D), rows, static_cast<uint64_t>(num_seqs) * Hkv};
+  const uint64_t row_bytes = static_cast<uint64_t>(D) * 2;
+  const uint32_t group = static_cast<uint32_t>(Hq / Hkv);
+  const uint64_t q_strides[3] = {row_bytes * Tn, row_bytes, row_bytes * Tn * group};
+  const uint64_t pool_strides[1] = {row_bytes};
+  const uint32_t q_box[4] = {64, group, static_cast<uint32_t>(tree_tile_nodes(group, Tn)), 1};
+  const uint32_t pool_box[2] = {64, 16};
+  const uint64_t dq[4] = {static_cast<uint64_t>(D), group, static_cast<uint64_t>(Tn),
+                          static_cast<uint64_t>(num_seqs) * Hkv};
   const uint64_t dpool[2] = {static_cast<uint64_t>(D),
                              static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size};
-  if ((st = encode_bf16(enc, &tmQ, q, 3, dq, q_strides, q_box)) != ATTN_OK) return st;
+  if ((st = encode_bf16(enc, &tmQ, q, 4, dq, q_strides, q_box)) != ATTN_OK) return st;
   if ((st = encode_bf16(enc, &tmK, k_pool, 2, dpool, pool_strides, pool_box)) != ATTN_OK) return st;
   if ((st = encode_bf16(enc, &tmV, v_pool, 2, dpool, pool_strides, pool_box)) != ATTN_OK) return st;
   TreeParams p{};

@@ -30,8 +30,10 @@ struct TreeParams {
 
 size_t tree_attn_workspace_bytes(int S, int Tn, int Hq, int Hkv, int D, int max_seq_len);
 cudaError_t prepare_tree_attn();
-// tmQ is a 3-D map over [S * Hkv, Hq / Hkv * Tn, D] with a 64 x 128 x 1 box, tmK and tmV are the
-// decode kernels' 2-D maps over the pools (64 x 16 box); all with the 128-byte swizzle.
+// tmQ is a 4-D map over [S * Hkv, group, Tn, D] with the group's heads next to the channels: a box
+// of 64 channels x group heads x tree_tile_nodes(group, Tn) nodes x 1; tmK and tmV are the decode
+// kernels' 2-D maps over the pools (64 x 16 box); all with the 128-byte swizzle.
+int tree_tile_nodes(int group, int Tn);
 cudaError_t launch_tree_attn(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                              const TreeParams& p, void* workspace, int num_sms,
                              cudaStream_t stream);

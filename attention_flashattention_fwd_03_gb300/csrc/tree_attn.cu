@@ -3,28 +3,31 @@
 //
 // A tree's queries share almost all of their keys: the L cached tokens, which every node
 // sees, and up to 256 nodes behind them, of which node i sees its ancestors and itself.  So
-// the query heads of a KV head and the nodes are rows of one matrix product ([Hq, Tn, D] keeps
-// the group * Tn rows of a KV head together), every key and value is read once for all of
-// them, and only the last tiles of 128 keys need a mask, a bit a (row, node).
+// the query heads of a KV head and the nodes are rows of one matrix product, every key and
+// value is read once for all of them, and only the last tiles of 128 keys need a mask.  A
+// row tile holds as many nodes as 128 rows have room for, node by node with the group's heads
+// side by side (one TMA box takes them from [Hq, Tn, D]), so that the places past a request's
+// last node fill whole tiles, which are not computed.
 //
-// The work is a sequence of segments, (request, KV head, 256 rows) each, of steps of 128
+// The work is a sequence of segments, (request, KV head, two row tiles) each, of steps of 128
 // keys; a CTA an SM takes an equal range of it, so that one long cache and many short ones
 // alike keep every SM busy whatever the lengths.  A segment that is cut between CTAs is put
 // together from partial outputs by the merge kernel; whole ones are written at once.  Where
 // all caches are short, CTAs take whole segments in turn and there is no merge kernel and no
-// workspace.
+// workspace.  Trees of more than two row tiles are taken by teams of CTAs, a pair of tiles
+// each, over the same keys at the same time, which then come from L2.
 //
 // A CTA is a pipeline of warps, as in attn_fwd.cu:
 //   warp 0      producer: Q tiles, then K and V tiles through the block table (16-row TMA
 //               boxes) into a ring
 //   warp 1      issues the products: S = Q K^T into tensor memory, O += P V with P from
 //               tensor memory
-//   warp 2      ancestors of the segment's tree, as bit masks
+//   warp 2      the segment's tree: its parents, checked
 //   warps 4-7, 8-11  softmax, a row a thread, of two chains of tiles that alternate on the
 //               tensor cores
-// Up to 128 rows the two chains take every other key tile of the one row tile, each with its
-// own maximum, sum and output, and are joined when the piece ends; above, they take a row tile
-// each over the same keys.
+// With one row tile the two chains take every other key tile, each with its own maximum, sum
+// and output, and are joined when the piece ends; with two they take a row tile each over the
+// same keys.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -45,9 +48,9 @@ constexpr int BN = 128;  // keys of a step
 constexpr int kBS = kPagedBlock;
 constexpr int kThreads = 384;
 constexpr int kMaxNodes = GBATTN_TREE_MAX_NODES;
-constexpr int kWords = kMaxNodes / 32;
 constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by > 2^8
 constexpr int kDirectSteps = 4;      // caches of so many steps at most are not cut
+constexpr int kMaxTeam = 8;
 // (the block launches with 168 registers a thread)
 constexpr int kRegsLaunch = 168, kRegsWg0 = 104, kRegsSoftmax = 200;
 static_assert(kRegsWg0 + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split exceeds the launch");
@@ -59,10 +62,11 @@ struct Plan {  // this CTA's range of steps
   int share, extra;
 };
 
-// A segment that is cut after range k and begins in it: request, segment of the request,
-// number of pieces and the first one's slot (the others are their ranges' first slots).
+// The rows of a CTA that are cut after its range and begin in it: request, KV head, pair of row
+// tiles and how many of the two there are, number of pieces and the first one's slot (the others
+// are the first slots of the CTAs that go on).
 struct Cut {
-  int r, s, pieces, slot;
+  int r, kvh, pair, tiles, pieces, slot;
 };
 
 struct Work {  // what the kernels share besides the caller's operands
@@ -70,11 +74,20 @@ struct Work {  // what the kernels share besides the caller's operands
   float* part_o;    // [2 grid][unit_rows][D]
   float* part_lse;  // [2 grid][unit_rows]
   Cut* cut;         // [grid]
-  int group_rows;   // query rows of a KV head
-  int pairs;        // units of rows of a KV head
-  int segs;         // Hkv * pairs
+  int group;        // query heads of a KV head
+  int tile_nodes;   // nodes of a row tile
+  int pairs;        // pairs of row tiles of a KV head
+  int team;         // CTAs of a team: pairs that are taken together
+  int rounds;       // teams' turns at a KV head
+  int segs;         // Hkv * rounds
   int unit_rows;    // rows of a partial output
-  int direct;       // CTAs take whole segments in turn
+  int direct;       // teams take whole segments in turn
+};
+
+// A checked tree: the parent of each node + 1, and the first node of the chain of consecutive
+// numbers that ends with it.
+struct Tree {
+  uint8_t parent1[kMaxNodes], start[kMaxNodes];
 };
 
 template <int D, bool SPLIT>
@@ -83,13 +96,12 @@ struct Cfg {
   static constexpr int BOX_BYTES = BM * 128;
   static constexpr int TILE_BYTES = BM * D * 2;
   static constexpr int NQ = SPLIT ? 1 : 2;       // row tiles
-  static constexpr int NSLOT = D == 64 ? 8 : (SPLIT ? 5 : 4);
+  static constexpr int NSLOT = D == 64 ? 8 : 5;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_RING = NQ * TILE_BYTES;
-  static constexpr int OFF_MASK = OFF_RING + NSLOT * TILE_BYTES;  // [2][kWords][kMaxNodes]
-  static constexpr int OFF_UP = OFF_MASK + 2 * kWords * kMaxNodes * 4;
-  static constexpr int OFF_JOIN = OFF_UP + kMaxNodes * 4;         // [2][BM] float2: maximum and sum
-  static constexpr int OFF_BAR = OFF_JOIN + 2 * BM * 8;
+  static constexpr int OFF_TREE = OFF_RING + NSLOT * TILE_BYTES;  // [2] Tree
+  static constexpr int OFF_JOIN = OFF_TREE + 2 * sizeof(Tree);    // SPLIT: [2][BM] float2, maximum and sum
+  static constexpr int OFF_BAR = OFF_JOIN + (SPLIT ? 2 * BM * 8 : 0);
   static constexpr int NBAR = 2 + 2 * NSLOT + 6 + 1 + 4 + 2;
   static constexpr int OFF_PLAN = OFF_BAR + NBAR * 8;
   static constexpr int OFF_SUMS = OFF_PLAN + sizeof(Plan) + 4;    // [12] ints
@@ -118,8 +130,8 @@ struct Bars {
   __device__ uint32_t s_free(int i) const { return at(4 + 2 * C::NSLOT + i); }
   __device__ uint32_t p_full(int i) const { return at(6 + 2 * C::NSLOT + i); }
   __device__ uint32_t teardown() const { return at(8 + 2 * C::NSLOT); }
-  __device__ uint32_t mask_full(int b) const { return at(9 + 2 * C::NSLOT + b); }
-  __device__ uint32_t mask_empty(int b) const { return at(11 + 2 * C::NSLOT + b); }
+  __device__ uint32_t tree_full(int b) const { return at(9 + 2 * C::NSLOT + b); }
+  __device__ uint32_t tree_empty(int b) const { return at(11 + 2 * C::NSLOT + b); }
   __device__ uint32_t joined(int i) const { return at(13 + 2 * C::NSLOT + i); }
 };
 
@@ -129,7 +141,7 @@ struct Sizes {
   int L, n;
   bool bad;
   __device__ int keys() const { return L + n; }
-  __device__ int steps() const { return max(1, (L + n + BN - 1) / BN); }  // (empty: one, to be written)
+  __device__ int tiles() const { return (L + n + BN - 1) / BN; }
 };
 __device__ __forceinline__ Sizes sizes_of(const TreeParams& p, int r) {
   Sizes z{p.seq_lens[r], p.tree_lens ? p.tree_lens[r] : p.Tn, false};
@@ -139,14 +151,29 @@ __device__ __forceinline__ Sizes sizes_of(const TreeParams& p, int r) {
   if (z.bad) z.L = z.n = 0;
   return z;
 }
+// Row tiles of a request that hold nodes, pairs of them, and team rounds with such a pair.
+__device__ __forceinline__ int live_tiles(const Work& w, const Sizes& z) {
+  return (z.n + w.tile_nodes - 1) / w.tile_nodes;
+}
+__device__ __forceinline__ int live_pairs(const Work& w, const Sizes& z) {
+  return (live_tiles(w, z) + 1) / 2;
+}
+__device__ __forceinline__ int live_rounds(const Work& w, const Sizes& z) {
+  return (live_pairs(w, z) + w.team - 1) / w.team;
+}
+// Steps of a segment: without nodes one, in which zeros are written.
+__device__ __forceinline__ int steps_of(const Work& w, const Sizes& z, int round) {
+  return round < live_rounds(w, z) ? z.tiles() : 1;
+}
 
 // The part of a segment that a CTA takes.
 struct Piece {
   Sizes z;
   int r, kvh, pair;
-  int j0, n;          // first key tile and how many (0: no keys at all)
-  int slot;           // of its partial output; -1: the segment is whole
-  bool last;          // holds the segment's last tile
+  int j0, n;      // first key tile and how many (0: nothing to compute)
+  int row_tiles;  // of the pair's two, how many hold nodes
+  int slot;       // of its partial output; -1: the segment is whole
+  bool last;      // holds the segment's last step
   __device__ bool masked(int j) const { return (j + 1) * BN > z.L; }
   __device__ bool tail() const { return n > 0 && masked(j0 + n - 1); }
 };
@@ -154,12 +181,13 @@ struct Piece {
 // Walks over this CTA's pieces; every role does so for itself.
 struct Walk {
   const Work& w;
+  int team, member;
   int left;  // steps, or (direct) the next segment
   int r, s, j, index = 0;
   Sizes z;
   __device__ Walk(const Work& w_, const Plan& plan)
-      : w(w_), left(w_.direct ? static_cast<int>(blockIdx.x) : plan.n), r(w_.direct ? -1 : plan.r),
-        s(plan.s), j(plan.j) {
+      : w(w_), team(blockIdx.x / w_.team), member(blockIdx.x - team * w_.team),
+        left(w_.direct ? team : plan.n), r(w_.direct ? -1 : plan.r), s(plan.s), j(plan.j) {
     if (!w.direct && left > 0) z = sizes_of(w.p, r);
   }
   __device__ bool next(Piece& x) {
@@ -169,19 +197,21 @@ struct Walk {
       if (now != r) z = sizes_of(w.p, now);
       r = now;
       s = left - now * w.segs;
-      left += gridDim.x;
+      left += gridDim.x / w.team;
       j = 0;
     } else if (left <= 0) {
       return false;
     }
-    const int steps = z.steps();
+    x.kvh = s / w.rounds;
+    const int round = s - x.kvh * w.rounds;
+    const int steps = steps_of(w, z, round);
     const int n = w.direct ? steps : min(left, steps - j);
     x.z = z;
     x.r = r;
-    x.kvh = s / w.pairs;
-    x.pair = s - x.kvh * w.pairs;
+    x.pair = round * w.team + member;
+    x.row_tiles = max(0, min(2, live_tiles(w, z) - 2 * x.pair));
     x.j0 = j;
-    x.n = z.keys() > 0 ? n : 0;
+    x.n = x.row_tiles > 0 ? n : 0;
     x.last = j + n == steps;
     x.slot = j == 0 && x.last ? -1 : 2 * static_cast<int>(blockIdx.x) + (index > 0 ? 1 : 0);
     ++index;
@@ -214,7 +244,7 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
   const uint32_t sQ = sbase + C::OFF_Q, sR = sbase + C::OFF_RING;
   const unsigned long long lim = p.wait_limit_ns;
   const uint64_t stream_policy = l2_policy_evict_first();
-  const bool once = w.pairs == 1;  // every K/V byte is read once
+  const bool once = w.team == 1 && w.rounds == 1;  // every K/V byte is read once
   int rc = 0, uc = 0;
   bool ok = true, last_q_issued = false;
   Walk walk(w, plan);
@@ -225,13 +255,12 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
     if (!mbar_wait_warp(bar.q_empty(), (uc & 1) ^ 1, abort, p.flags, lim)) { ok = false; break; }
     last_q_issued = !(p.withhold_copy && uc == 0);  // test hook: withhold the first Q
     if (lane == 0 && last_q_issued) {
-      mbar_arrive_expect_tx(bar.q_full(), C::NQ * C::TILE_BYTES);
-#pragma unroll
-      for (int i = 0; i < C::NQ; ++i)
+      mbar_arrive_expect_tx(bar.q_full(), x.row_tiles * C::KB * w.group * w.tile_nodes * 128);
+      for (int i = 0; i < x.row_tiles; ++i)
 #pragma unroll
         for (int kb = 0; kb < C::KB; ++kb)
-          tma_load_3d(sQ + i * C::TILE_BYTES + kb * C::BOX_BYTES, tmQ, bar.q_full(), kb * 64,
-                      256 * x.pair + BM * i, x.r * p.Hkv + x.kvh);
+          tma_load_4d(sQ + i * C::TILE_BYTES + kb * C::BOX_BYTES, tmQ, bar.q_full(), kb * 64, 0,
+                      (2 * x.pair + i) * w.tile_nodes, x.r * p.Hkv + x.kvh);
     }
     ++uc;
     const int blocks = (x.z.keys() + kBS - 1) / kBS;
@@ -292,74 +321,56 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
 }
 
 // ---------------------------------------------------------------------------
-// warp 2: which nodes each node sees; and where a segment is cut behind this CTA's range
+// warp 2: the trees
 // ---------------------------------------------------------------------------
-// Word w of node i is at mask[w kMaxNodes + i].  A node's set is taken from its parent's by
-// pointer jumping: `up` is the first ancestor not in the set yet.  Nodes go 32 at a time,
-// so that parents in earlier groups are complete; inside a group the sets double with each
-// round.
-__device__ __forceinline__ void ancestors(const int32_t* parents, int n, int places, uint32_t* mask,
-                                          int* up, bool& bad) {
+__device__ __forceinline__ bool read_tree(const int32_t* parents, int n, Tree& tree) {
   const int lane = threadIdx.x & 31;
-  bad = false;
-  for (int i = lane; i < places; i += 32) {
-    const int a = i < n ? parents[i] : -1;
-    bad |= a < -1 || a >= i;
-    up[i] = a;
-  }
-  bad = __any_sync(0xffffffffu, bad);
-  for (int b = 0; 32 * b < places; ++b) {
-    const int i = 32 * b + lane;
+  bool bad = false;
+  int before = 0;  // start of the chain that ends with the node before
+  for (int b = 0; b < n; b += 32) {
+    const int i = b + lane;
+    int a = i < n ? parents[i] : -1;
+    const bool wrong = a < -1 || a >= i;
+    bad |= i < n && wrong;
+    if (wrong) a = -1;
+    int start = a == i - 1 ? 0 : i;  // the largest break so far
 #pragma unroll
-    for (int w = 0; w < kWords; ++w) mask[w * kMaxNodes + i] = w == b && i < n && !bad ? 1u << lane : 0u;
-    int u = bad || i >= n ? -1 : up[i];
-    __syncwarp();
-    while (__any_sync(0xffffffffu, u >= 0)) {
-      uint32_t set[kWords];
-      int above = -1;
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) set[w] = u >= 0 && w <= b ? mask[w * kMaxNodes + u] : 0u;
-      if (u >= 0) above = up[u];
-      __syncwarp();
-      if (u >= 0) {
-#pragma unroll
-        for (int w = 0; w < kWords; ++w)
-          if (w <= b) mask[w * kMaxNodes + i] |= set[w];
-      }
-      u = above;
-      up[i] = u;
-      __syncwarp();
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, start, o);
+      if (lane >= o) start = max(start, v);
     }
-    up[i] = -1;
-    __syncwarp();
+    start = max(start, before);
+    before = __shfl_sync(0xffffffffu, start, 31);
+    if (i < n) {
+      tree.parent1[i] = static_cast<uint8_t>(a + 1);
+      tree.start[i] = static_cast<uint8_t>(start);
+    }
   }
+  return __any_sync(0xffffffffu, bad);
 }
 
 template <int D, bool SPLIT>
-__device__ void mask_warp(const Work& w, const Plan& plan, uint8_t* smem, const Bars<D, SPLIT>& bar,
+__device__ void tree_warp(const Work& w, const Plan& plan, uint8_t* smem, const Bars<D, SPLIT>& bar,
                           volatile int* abort) {
   using C = Cfg<D, SPLIT>;
   const TreeParams& p = w.p;
   const int lane = threadIdx.x & 31;
-  const int places = (p.Tn + 31) / 32 * 32;
   volatile int* bad_tree = reinterpret_cast<volatile int*>(smem + C::OFF_MISC) + 2;
-  int* up = reinterpret_cast<int*>(smem + C::OFF_UP);
   int mc = 0;
   Walk walk(w, plan);
   Piece x;
   while (walk.next(x)) {
     if (!x.tail()) continue;
     const int b = mc & 1;
-    if (!mbar_wait_warp(bar.mask_empty(b), ((mc >> 1) & 1) ^ 1, abort, p.flags, p.wait_limit_ns)) return;
-    uint32_t* mask = reinterpret_cast<uint32_t*>(smem + C::OFF_MASK) + b * kWords * kMaxNodes;
-    bool bad;
-    ancestors(p.parents + static_cast<size_t>(x.r) * p.Tn, x.z.n, places, mask, up, bad);
+    if (!mbar_wait_warp(bar.tree_empty(b), ((mc >> 1) & 1) ^ 1, abort, p.flags, p.wait_limit_ns)) return;
+    const bool bad = read_tree(p.parents + static_cast<size_t>(x.r) * p.Tn, x.z.n,
+                               reinterpret_cast<Tree*>(smem + C::OFF_TREE)[b]);
     if (lane == 0) {
       bad_tree[b] = bad;
       if (bad) raise_flag(p.flags, DEVFLAG_BAD_TREE);
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar.mask_full(b));
+    if (lane == 0) mbar_arrive(bar.tree_full(b));
     ++mc;
   }
 }
@@ -478,7 +489,7 @@ struct MmaWarp {
           }
         }
       } else {
-        const bool two = 256 * x.pair + BM < w.group_rows;  // the second row tile has rows
+        const bool two = x.row_tiles == 2;
         if (!issue_s<0>(0, false)) return;
         if (two && !issue_s<1>(0, true)) return;
         mma_commit_warp(bar.slot_empty(slot(0)));
@@ -500,13 +511,17 @@ struct MmaWarp {
   }
 };
 
-// Bits x .. x + 31 of a node's set, those before node 0 (the cached tokens) set.
-__device__ __forceinline__ uint32_t seen_bits(const uint32_t* set, int x) {
-  if (x <= -32) return 0xffffffffu;
-  if (x >= kMaxNodes) return 0u;
-  if (x < 0) return (set[0] << -x) | ((1u << -x) - 1u);
-  const int i = x >> 5;
-  return __funnelshift_r(set[i * kMaxNodes], i + 1 < kWords ? set[(i + 1) * kMaxNodes] : 0u, x & 31);
+// What node a sees of the 32 keys from x on, x counted from node 0 (the keys before it are the
+// cached tokens); a becomes the first of its ancestors before those keys.
+__device__ __forceinline__ uint32_t seen_bits(const Tree& tree, int& a, int x) {
+  uint32_t bits = x <= -32 ? 0xffffffffu : (x < 0 ? (1u << -x) - 1u : 0u);
+  while (a >= max(x, 0)) {
+    const int s = tree.start[a];  // s .. a are its own or its ancestors
+    const int hi = min(a - x, 31), lo = max(s - x, 0);
+    if (lo <= hi) bits |= (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
+    a = s < x ? x - 1 : tree.parent1[s] - 1;
+  }
+  return bits;
 }
 
 // ---------------------------------------------------------------------------
@@ -539,16 +554,15 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
   Walk walk(w, plan);
   Piece x;
   while (walk.next(x)) {
-    const int row = 256 * x.pair + (SPLIT ? 0 : BM * I) + tile_row;  // of the KV head
-    const bool row_valid = row < w.group_rows;
-    const int node = row % p.Tn;
-    const bool live = __any_sync(0xffffffffu, row_valid);  // else the warp only keeps step
-    const int n = SPLIT ? (x.n + 1 - I) / 2
-                        : (256 * x.pair + BM * I < w.group_rows ? x.n : 0);
+    const int node0 = (2 * x.pair + (SPLIT ? 0 : I)) * w.tile_nodes;  // of the row tile
+    const int tile_node = tile_row / w.group, head = tile_row - tile_node * w.group;
+    const int node = node0 + tile_node;
+    const bool exists = tile_node < w.tile_nodes && node < p.Tn && x.pair < w.pairs;
+    const bool live = __any_sync(0xffffffffu, exists && node < x.z.n);  // else the warp only keeps step
+    const int n = SPLIT ? (x.n + 1 - I) / 2 : (I < x.row_tiles ? x.n : 0);
     const bool tail = x.tail();
     const int b = mc & 1;
-    const uint32_t* set = reinterpret_cast<const uint32_t*>(smem + C::OFF_MASK) +
-                          b * kWords * kMaxNodes + node;
+    const Tree& tree = reinterpret_cast<const Tree*>(smem + C::OFF_TREE)[b];
     bool have_mask = false;
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < n; ++i) {
@@ -572,12 +586,13 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
         const bool masked = x.masked(j);
         if (masked) {
           if (!have_mask &&
-              !mbar_wait_warp(bar.mask_full(b), (mc >> 1) & 1, abort, p.flags, lim))
+              !mbar_wait_warp(bar.tree_full(b), (mc >> 1) & 1, abort, p.flags, lim))
             return;
           have_mask = true;
+          int a = exists && node < x.z.n ? node : -1;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t bits = seen_bits(set, j * BN - x.z.L + 32 * c);
+          for (int c = 3; c >= 0; --c) {
+            const uint32_t bits = seen_bits(tree, a, j * BN - x.z.L + 32 * c);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!(bits >> e & 1u)) s[32 * c + e] = -INFINITY;
@@ -623,15 +638,19 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
     bool bad = x.z.bad;
     if (tail) {
       // (every warp meets every mask, so that none is a buffer ahead)
-      if (!have_mask && !mbar_wait_warp(bar.mask_full(b), (mc >> 1) & 1, abort, p.flags, lim)) return;
+      if (!have_mask && !mbar_wait_warp(bar.tree_full(b), (mc >> 1) & 1, abort, p.flags, lim)) return;
       bad |= bad_trees[b] != 0;
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar.mask_empty(b));
+      if (lane == 0) mbar_arrive(bar.tree_empty(b));
       ++mc;
     }
 
     // ---- results of the piece: O and LSE, or a partial output ----
     const bool dead = node >= x.z.n;  // no node is in this place
+    // a row tile without nodes: zeros (or NaN), once
+    const bool computed = SPLIT ? x.n > 0 : n > 0;
+    const bool whole = computed ? x.slot < 0 : true;
+    const bool write = exists && (computed || x.last);
     float f0 = 0.f, f1 = 0.f;         // factors of O_0 and O_1 (one of them without SPLIT)
     float M = m, sum = l;
     bool two = false;
@@ -651,19 +670,20 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
     } else {
       f0 = 1.f;
     }
-    const bool none = sum == 0.f || dead || x.n == 0;  // no key is seen (a NaN is a result)
-    const float inv = bad ? kNan : (none ? 0.f : 1.f / sum);
-    const float lse = bad ? kNan : (none ? -INFINITY : M * p.scale + logf(sum));
+    const bool none = sum == 0.f || dead || !computed;  // no key is seen (a NaN is a result)
+    const bool nan = x.z.bad || (bad && !dead);
+    const float inv = nan ? kNan : (none ? 0.f : 1.f / sum);
+    const float lse = nan ? kNan : (none ? -INFINITY : M * p.scale + logf(sum));
     f0 *= inv;
     f1 *= inv;
-    const size_t out_row = (static_cast<size_t>(x.r) * p.Hkv + x.kvh) * w.group_rows + row;
-    const int unit_row = row - 256 * x.pair;
-    const size_t part_row = static_cast<size_t>(x.slot < 0 ? 0 : x.slot) * w.unit_rows + unit_row;
-    const bool has_o = SPLIT ? x.n > 0 : n > 0;
+    const size_t out_row =
+        (static_cast<size_t>(x.r) * p.Hq + x.kvh * w.group + head) * p.Tn + node;
+    const size_t part_row = static_cast<size_t>(max(x.slot, 0)) * w.unit_rows + (SPLIT ? 0 : BM * I) + tile_row;
     // SPLIT: each warpgroup writes half of the channels
     constexpr int COLS = SPLIT ? D / 2 : D;
     const int c0 = SPLIT ? COLS * I : 0;
-    if (live) {
+    const bool has_o = live && computed;
+    if (__any_sync(0xffffffffu, write)) {
 #pragma unroll 1
       for (int c = c0; c < c0 + COLS; c += 16) {
         uint32_t o[16], o1[16];
@@ -677,17 +697,17 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
         float f[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          f[e] = has_o && !none ? __uint_as_float(o[e]) * f0 : (bad ? kNan : 0.f);
-          if (SPLIT && two && !none) f[e] = fmaf(__uint_as_float(o1[e]), f1, f[e]);
+          f[e] = has_o && !none ? __uint_as_float(o[e]) * f0 : inv;  // (zero, or NaN)
+          if (SPLIT && two && has_o && !none) f[e] = fmaf(__uint_as_float(o1[e]), f1, f[e]);
         }
-        if (row_valid && x.slot < 0) {
+        if (write && whole) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + out_row * D + c);
 #pragma unroll
           for (int v = 0; v < 2; ++v)
             dst[v] = make_uint4(pack_bf16x2(f[8 * v], f[8 * v + 1]), pack_bf16x2(f[8 * v + 2], f[8 * v + 3]),
                                 pack_bf16x2(f[8 * v + 4], f[8 * v + 5]),
                                 pack_bf16x2(f[8 * v + 6], f[8 * v + 7]));
-        } else if (row_valid) {
+        } else if (write) {
           float4* dst = reinterpret_cast<float4*>(w.part_o + part_row * D + c);
 #pragma unroll
           for (int v = 0; v < 4; ++v)
@@ -695,8 +715,8 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
         }
       }
     }
-    if (row_valid && (!SPLIT || I == 0)) {
-      if (x.slot >= 0)
+    if (write && (!SPLIT || I == 0)) {
+      if (!whole)
         w.part_lse[part_row] = lse;
       else if (p.lse != nullptr)
         p.lse[out_row] = lse;
@@ -722,20 +742,25 @@ __device__ void make_plan(const Work& w, Plan* plan, int* sums) {
     for (int i = 0; i < kThreads / 32; ++i) t += sums[i];
     return t;
   };
-  auto steps = [&](int r) { return r < w.p.S ? sizes_of(w.p, r).steps() * w.segs : 0; };
-  const int first = steps(threadIdx.x);  // (the only requests, usually)
+  // of a KV head: rounds with nodes, then one step for each of the others
+  auto steps = [&](const Sizes& z) {
+    const int live = live_rounds(w, z);
+    return live * z.tiles() + w.rounds - live;
+  };
+  auto steps_at = [&](int r) { return r < w.p.S ? steps(sizes_of(w.p, r)) * w.p.Hkv : 0; };
+  const int first = steps_at(threadIdx.x);  // (the only requests, usually)
   int mine = first;
-  for (int r = threadIdx.x + kThreads; r < w.p.S; r += kThreads) mine += steps(r);
+  for (int r = threadIdx.x + kThreads; r < w.p.S; r += kThreads) mine += steps_at(r);
   const int total = block_sum(mine);
-  const int W = min(static_cast<int>(gridDim.x), total);
-  const int k = blockIdx.x;
+  const int W = min(static_cast<int>(gridDim.x) / w.team, total);
+  const int k = blockIdx.x / w.team;
   const int share = total / W, extra = total - share * W;  // the first `extra` take one more
   const int lo = k * share + min(k, extra), n = k < W ? share + (k < extra ? 1 : 0) : 0;
   if (threadIdx.x == 0) *plan = Plan{lo, n, 0, 0, 0, share, extra};
   int before = 0;
   for (int r0 = 0; r0 < w.p.S && n > 0; r0 += kThreads) {
     const int r = r0 + threadIdx.x;
-    const int own = r0 == 0 ? first : steps(r);
+    const int own = r0 == 0 ? first : steps_at(r);
     int incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -752,32 +777,34 @@ __device__ void make_plan(const Work& w, Plan* plan, int* sums) {
     }
     incl += before;
     if (own > 0 && incl - own <= lo && lo < incl) {
-      const int per_seg = own / w.segs, rest = lo - (incl - own);
+      const Sizes z = sizes_of(w.p, r);
+      const int head = steps(z), live = live_rounds(w, z) * z.tiles();
+      const int kvh = (lo - (incl - own)) / head, rest = lo - (incl - own) - kvh * head;
+      const int round = rest < live ? rest / z.tiles() : live_rounds(w, z) + rest - live;
       plan->r = r;
-      plan->s = rest / per_seg;
-      plan->j = rest - plan->s * per_seg;
+      plan->s = kvh * w.rounds + round;
+      plan->j = rest < live ? rest - round * z.tiles() : 0;
     }
     before += all;
     if (before > lo) break;  // (the same in every thread)
   }
 }
 
-// Notes the segment that begins in this CTA's range and goes on in the next one.
+// Notes the rows that begin in this CTA's range and go on in the next one.
 __device__ void note_cut(const Work& w, const Plan& plan) {
-  Cut cut{0, 0, 0, 0};
+  Cut cut{0, 0, 0, 0, 0, 0};
   Walk walk(w, plan);
   Piece x;
   int at = plan.lo;  // step that x begins at
   while (walk.next(x)) {
-    const int steps = x.z.steps();
-    const int n = walk.left > 0 || x.last ? steps - x.j0 : plan.lo + plan.n - at;
-    if (!x.last && x.j0 == 0) {
+    const int steps = steps_of(w, x.z, x.pair / w.team);
+    if (!x.last && x.j0 == 0 && x.n > 0) {  // (the range's last piece, then)
       // the range that holds the segment's last step
       const int e = at + steps - 1, big = plan.extra * (plan.share + 1);
       const int k1 = e < big ? e / (plan.share + 1) : plan.extra + (e - big) / plan.share;
-      cut = Cut{x.r, x.kvh * w.pairs + x.pair, k1 - static_cast<int>(blockIdx.x) + 1, x.slot};
+      cut = Cut{x.r, x.kvh, x.pair, x.row_tiles, k1 - walk.team + 1, x.slot};
     }
-    at += n;
+    at += steps - x.j0;
   }
   w.cut[blockIdx.x] = cut;
 }
@@ -811,8 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar.s_full(i), 1);
       mbar_init(bar.s_free(i), 1);
       mbar_init(bar.p_full(i), 128);
-      mbar_init(bar.mask_full(i), 1);
-      mbar_init(bar.mask_empty(i), 8);
+      mbar_init(bar.tree_full(i), 1);
+      mbar_init(bar.tree_empty(i), 8);
       mbar_init(bar.joined(i), 256);
     }
     mbar_init(bar.teardown(), 1);
@@ -850,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_wait_quiet(bar.teardown(), 0, 1000000000ull);
       __syncwarp();
     } else if (warp == 2) {
-      mask_warp<D, SPLIT>(w, plan, smem, bar, abort);
+      tree_warp<D, SPLIT>(w, plan, smem, bar, abort);
     } else if (!w.direct && lane == 0) {
       note_cut(w, plan);
     }
@@ -880,10 +907,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
   const Cut cut = w.cut[blockIdx.x];
   const int lane = threadIdx.x & 31;
   const int unit_row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  const int kvh = cut.s / w.pairs;
-  const int row = 256 * (cut.s - kvh * w.pairs) + unit_row;
-  if (cut.pieces == 0 || unit_row >= w.unit_rows || row >= w.group_rows) return;
-  auto slot = [&](int i) { return i == 0 ? cut.slot : 2 * (static_cast<int>(blockIdx.x) + i); };
+  const int tile = unit_row / BM, tile_row = unit_row - tile * BM;
+  const int tile_node = tile_row / w.group, head = tile_row - tile_node * w.group;
+  const int node = (2 * cut.pair + tile) * w.tile_nodes + tile_node;
+  // (a row tile without nodes has been written already)
+  if (cut.pieces == 0 || tile >= cut.tiles || tile_node >= w.tile_nodes || node >= w.p.Tn) return;
+  auto slot = [&](int i) { return i == 0 ? cut.slot : 2 * (static_cast<int>(blockIdx.x) + i * w.team); };
   float m = -INFINITY, sum = 0.f, o[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = 0.f;
@@ -923,7 +952,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (no key is seen)
-  const size_t out = (static_cast<size_t>(cut.r) * w.p.Hkv + kvh) * w.group_rows + row;
+  const size_t out =
+      (static_cast<size_t>(cut.r) * w.p.Hq + cut.kvh * w.group + head) * w.p.Tn + node;
   uint16_t* dst = static_cast<uint16_t*>(w.p.o) + out * D + lane * PER;
 #pragma unroll
   for (int i = 0; i < PER; i += 2)
@@ -933,17 +963,21 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
 }
 
 struct Shape {
-  int group_rows, pairs, segs, unit_rows;
+  int group, tile_nodes, row_tiles, pairs, team, rounds, segs, unit_rows;
   long long units, steps;  // segments of the batch, and their steps at most
   bool direct;
 };
 
 Shape shape_of(int S, int Tn, int Hq, int Hkv, int max_seq_len) {
   Shape s;
-  s.group_rows = Hq / Hkv * Tn;
-  s.pairs = (s.group_rows + 255) / 256;
-  s.segs = Hkv * s.pairs;
-  s.unit_rows = s.group_rows < 256 ? s.group_rows : 256;
+  s.group = Hq / Hkv;
+  s.tile_nodes = tree_tile_nodes(s.group, Tn);
+  s.row_tiles = (Tn + s.tile_nodes - 1) / s.tile_nodes;
+  s.pairs = (s.row_tiles + 1) / 2;
+  s.rounds = (s.pairs + kMaxTeam - 1) / kMaxTeam;
+  s.team = (s.pairs + s.rounds - 1) / s.rounds;
+  s.segs = Hkv * s.rounds;
+  s.unit_rows = s.row_tiles == 1 ? s.tile_nodes * s.group : 2 * BM;
   const long long per_seg = std::max<long long>(1, (max_seq_len + (BN - 1ll)) / BN);
   s.units = static_cast<long long>(S) * s.segs;
   s.steps = per_seg * s.units;
@@ -951,11 +985,12 @@ Shape shape_of(int S, int Tn, int Hq, int Hkv, int max_seq_len) {
   return s;
 }
 
-// CTAs of a split launch, which the workspace is laid out for: as many on every device, so
-// that it depends on the sizes alone.
+// CTAs of a launch: the workspace is laid out for as many on every device, so that it depends on
+// the sizes alone.
 constexpr int kMaxGrid = 160;
 int grid_of(const Shape& s, int num_sms) {
-  return static_cast<int>(std::min<long long>({num_sms, kMaxGrid, s.direct ? s.units : s.steps}));
+  const int teams = std::max(1, std::min(num_sms, kMaxGrid) / s.team);
+  return s.team * static_cast<int>(std::min<long long>(teams, s.direct ? s.units : s.steps));
 }
 
 struct Layout {
@@ -965,7 +1000,7 @@ Layout layout_of(const Shape& s, int D) {
   Layout l{};
   if (s.direct) return l;
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  const size_t grid = static_cast<size_t>(std::min<long long>(s.steps, kMaxGrid));
+  const size_t grid = static_cast<size_t>(grid_of(s, kMaxGrid));
   const size_t rows = 2 * grid * s.unit_rows;
   l.off_lse = up(rows * D * sizeof(float));
   l.off_cut = l.off_lse + up(rows * sizeof(float));
@@ -1002,6 +1037,8 @@ cudaError_t set_smem() {
 
 }  // namespace
 
+int tree_tile_nodes(int group, int Tn) { return std::min(BM / group, Tn); }
+
 size_t tree_attn_workspace_bytes(int S, int Tn, int Hq, int Hkv, int D, int max_seq_len) {
   return layout_of(shape_of(S, Tn, Hq, Hkv, max_seq_len), D).bytes;
 }
@@ -1025,13 +1062,16 @@ cudaError_t launch_tree_attn(const CUtensorMap& tmQ, const CUtensorMap& tmK, con
   w.part_o = reinterpret_cast<float*>(ws);
   w.part_lse = reinterpret_cast<float*>(ws + l.off_lse);
   w.cut = reinterpret_cast<Cut*>(ws + l.off_cut);
-  w.group_rows = s.group_rows;
+  w.group = s.group;
+  w.tile_nodes = s.tile_nodes;
   w.pairs = s.pairs;
+  w.team = s.team;
+  w.rounds = s.rounds;
   w.segs = s.segs;
   w.unit_rows = s.unit_rows;
   w.direct = s.direct;
   const int grid = grid_of(s, num_sms);
-  const bool split = s.group_rows <= BM;
+  const bool split = s.row_tiles == 1;
   if (p.D == 64)
     return split ? launch<64, true>(tmQ, tmK, tmV, w, grid, stream)
                  : launch<64, false>(tmQ, tmK, tmV, w, grid, stream);

@@ -476,14 +476,14 @@ size_t paged_attn_tree_workspace_size(int num_seqs, int Tn, int Hq, int Hkv, int
  *
  * Node i sees the L_r cached tokens, its ancestors and itself.  Places past a tree's nodes
  * get O = 0 and LSE = -inf; what is cached for them is not read.  max_seq_len bounds every
- * L_r + tree_lens[r].  Tn is at most GBATTN_TREE_MAX_NODES, block_size 16, D 64 or 128; any
- * number of query heads may share a KV head.  The split of the work depends on the lengths
+ * L_r + tree_lens[r].  Tn is at most GBATTN_TREE_MAX_NODES, block_size 16, D 64 or 128, Hq /
+ * Hkv <= 128.  The split of the work depends on the lengths
  * of the whole batch, never on the blocks' places: the same inputs give the same bits.
  *
  * Device-side checks: a length or a number of nodes outside its bounds, or L_r +
  * tree_lens[r] outside [0, min(max_seq_len, max_blocks_per_seq * block_size)], makes that
- * request's O and LSE NaN and sets flag bit 2; a parent outside [-1, i) does so with flag
- * bit 16.  A block id outside the pool is read as block 0 and sets flag bit 4 (that
+ * request's O and LSE NaN and sets flag bit 2; a parent outside [-1, i) makes those of all
+ * its nodes NaN and sets flag bit 16.  A block id outside the pool is read as block 0 and sets flag bit 4 (that
  * request's output is then unspecified).  Slots past the tree may hold any bits.  A NaN in a
  * value may reach O of every node of its request, of those too that do not see it.
  */
