@@ -25,13 +25,13 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
 }
 
 // Whether the kernels' 32-bit counts hold a call of these sizes: query rows, and steps of
-// 128 keys of every (request, KV head, two row tiles).
+// 128 keys of every (request, KV head, two row tiles), 20 units each and 20 more a segment.
 bool tree_fits(int S, int Tn, int Hq, int Hkv, int max_seq_len) {
   const unsigned __int128 rows = static_cast<unsigned __int128>(S) * Hq * Tn;
   const uint64_t tiles = (static_cast<uint64_t>(max_seq_len) + 127) / 128 + 1;
   const int nodes = Tn > 0 ? tree_tile_nodes(Hq / Hkv, Tn) : 1;
   const unsigned __int128 segs = static_cast<unsigned __int128>(S) * Hkv * ((Tn + nodes - 1) / nodes);
-  return rows < kMaxDim && segs * tiles < kMaxDim;
+  return rows < kMaxDim && segs * (tiles + 1) * 20 < kMaxDim;
 }
 
 }  // namespace

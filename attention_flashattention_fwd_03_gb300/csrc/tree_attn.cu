@@ -56,9 +56,15 @@ constexpr int kRegsLaunch = 168, kRegsWg0 = 104, kRegsSoftmax = 200;
 static_assert(kRegsWg0 + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split exceeds the launch");
 constexpr float kNan = __builtin_nanf("");
 
-struct Plan {  // this CTA's range of steps
-  int lo, n;   // first step and how many
-  int r, s, j; // the first one's request, segment of the request and step of the segment
+// The steps lie on a line: a segment begins with kSegCost, then its steps follow one another at
+// the distance of what one costs.  A range takes the steps that lie in it.
+constexpr int kSegCost = 20;
+constexpr int kStepCost0 = 4, kStepCost1 = 16, kStepCost2 = 20;  // by row tiles (0: zeros are written)
+constexpr int kMostCost = kSegCost + kStepCost2;  // no range is shorter, so that each holds a step
+
+struct Plan {        // this CTA's range
+  int lo, hi;        // where it begins and ends
+  int pos, r, s, j;  // the first step's place, request, segment of the request and step of that
   int share, extra;
 };
 
@@ -71,7 +77,7 @@ struct Cut {
 
 struct Work {  // what the kernels share besides the caller's operands
   TreeParams p;
-  float* part_o;    // [2 grid][unit_rows][D]
+  float* part_o;    // [2 grid][D / 4][unit_rows][4]: a warp's rows side by side
   float* part_lse;  // [2 grid][unit_rows]
   Cut* cut;         // [grid]
   int group;        // query heads of a KV head
@@ -161,9 +167,13 @@ __device__ __forceinline__ int live_pairs(const Work& w, const Sizes& z) {
 __device__ __forceinline__ int live_rounds(const Work& w, const Sizes& z) {
   return (live_pairs(w, z) + w.team - 1) / w.team;
 }
-// Steps of a segment: without nodes one, in which zeros are written.
+// Steps of a segment (without nodes one, in which zeros are written) and what one costs.
 __device__ __forceinline__ int steps_of(const Work& w, const Sizes& z, int round) {
   return round < live_rounds(w, z) ? z.tiles() : 1;
+}
+__device__ __forceinline__ int step_cost(const Work& w, const Sizes& z, int round) {
+  const int tiles = live_tiles(w, z) - 2 * round * w.team;
+  return tiles <= 0 ? kStepCost0 : (tiles == 1 ? kStepCost1 : kStepCost2);
 }
 
 // The part of a segment that a CTA takes.
@@ -174,6 +184,7 @@ struct Piece {
   int row_tiles;  // of the pair's two, how many hold nodes
   int slot;       // of its partial output; -1: the segment is whole
   bool last;      // holds the segment's last step
+  int end;        // where the segment ends (not if direct)
   __device__ bool masked(int j) const { return (j + 1) * BN > z.L; }
   __device__ bool tail() const { return n > 0 && masked(j0 + n - 1); }
 };
@@ -182,30 +193,29 @@ struct Piece {
 struct Walk {
   const Work& w;
   int team, member;
-  int left;  // steps, or (direct) the next segment
-  int r, s, j, index = 0;
+  int at;  // place of the next step on the line, or (direct) the next segment
+  int hi, r, s, j, index = 0;
   Sizes z;
   __device__ Walk(const Work& w_, const Plan& plan)
       : w(w_), team(blockIdx.x / w_.team), member(blockIdx.x - team * w_.team),
-        left(w_.direct ? team : plan.n), r(w_.direct ? -1 : plan.r), s(plan.s), j(plan.j) {
-    if (!w.direct && left > 0) z = sizes_of(w.p, r);
+        at(w_.direct ? team : plan.pos), hi(w_.direct ? w_.p.S * w_.segs : plan.hi),
+        r(w_.direct ? -1 : plan.r), s(plan.s), j(plan.j) {
+    if (!w.direct && at < hi) z = sizes_of(w.p, r);
   }
   __device__ bool next(Piece& x) {
+    if (at >= hi) return false;
     if (w.direct) {
-      if (left >= w.p.S * w.segs) return false;
-      const int now = left / w.segs;
+      const int now = at / w.segs;
       if (now != r) z = sizes_of(w.p, now);
       r = now;
-      s = left - now * w.segs;
-      left += gridDim.x / w.team;
+      s = at - now * w.segs;
+      at += gridDim.x / w.team;
       j = 0;
-    } else if (left <= 0) {
-      return false;
     }
     x.kvh = s / w.rounds;
     const int round = s - x.kvh * w.rounds;
-    const int steps = steps_of(w, z, round);
-    const int n = w.direct ? steps : min(left, steps - j);
+    const int steps = steps_of(w, z, round), cost = step_cost(w, z, round);
+    const int n = w.direct ? steps : min((hi - at + cost - 1) / cost, steps - j);
     x.z = z;
     x.r = r;
     x.pair = round * w.team + member;
@@ -216,13 +226,15 @@ struct Walk {
     x.slot = j == 0 && x.last ? -1 : 2 * static_cast<int>(blockIdx.x) + (index > 0 ? 1 : 0);
     ++index;
     if (!w.direct) {
-      left -= n;
+      x.end = at + (steps - j) * cost;
+      at += n * cost;
       j += n;
-      if (j == steps && left > 0) {
+      if (j == steps) {
+        at += kSegCost;
         j = 0;
-        if (++s == w.segs) {
+        if (at < hi && ++s == w.segs) {
           s = 0;
-          if (++r >= w.p.S) left = 0;  // (lengths changed under the kernel)
+          if (++r >= w.p.S) at = hi;  // (lengths changed under the kernel)
           else z = sizes_of(w.p, r);
         }
       }
@@ -252,17 +264,6 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
   while (ok && walk.next(x)) {
     if (x.z.bad && lane == 0) raise_flag(p.flags, DEVFLAG_BAD_SEQLEN);
     if (x.n == 0) continue;
-    if (!mbar_wait_warp(bar.q_empty(), (uc & 1) ^ 1, abort, p.flags, lim)) { ok = false; break; }
-    last_q_issued = !(p.withhold_copy && uc == 0);  // test hook: withhold the first Q
-    if (lane == 0 && last_q_issued) {
-      mbar_arrive_expect_tx(bar.q_full(), x.row_tiles * C::KB * w.group * w.tile_nodes * 128);
-      for (int i = 0; i < x.row_tiles; ++i)
-#pragma unroll
-        for (int kb = 0; kb < C::KB; ++kb)
-          tma_load_4d(sQ + i * C::TILE_BYTES + kb * C::BOX_BYTES, tmQ, bar.q_full(), kb * 64, 0,
-                      (2 * x.pair + i) * w.tile_nodes, x.r * p.Hkv + x.kvh);
-    }
-    ++uc;
     const int blocks = (x.z.keys() + kBS - 1) / kBS;
     // lane l < 8 reads the table entry of block l of a tile, one tile ahead of the copies
     auto table_entry = [&](int j) -> int {
@@ -308,6 +309,24 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
         }
         __syncwarp();
         ++rc;
+      }
+      if (ok && j == x.j0) {
+        // the queries go behind the first tile, whose slots are free before the piece before is
+        // done with its own queries
+        if (!mbar_wait_warp(bar.q_empty(), (uc & 1) ^ 1, abort, p.flags, lim)) {
+          ok = false;
+          break;
+        }
+        last_q_issued = !(p.withhold_copy && uc == 0);  // test hook: withhold the first Q
+        if (lane == 0 && last_q_issued) {
+          mbar_arrive_expect_tx(bar.q_full(), x.row_tiles * C::KB * w.group * w.tile_nodes * 128);
+          for (int i = 0; i < x.row_tiles; ++i)
+#pragma unroll
+            for (int kb = 0; kb < C::KB; ++kb)
+              tma_load_4d(sQ + i * C::TILE_BYTES + kb * C::BOX_BYTES, tmQ, bar.q_full(), kb * 64, 0,
+                          (2 * x.pair + i) * w.tile_nodes, x.r * p.Hkv + x.kvh);
+        }
+        ++uc;
       }
     }
   }
@@ -678,7 +697,8 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
     f1 *= inv;
     const size_t out_row =
         (static_cast<size_t>(x.r) * p.Hq + x.kvh * w.group + head) * p.Tn + node;
-    const size_t part_row = static_cast<size_t>(max(x.slot, 0)) * w.unit_rows + (SPLIT ? 0 : BM * I) + tile_row;
+    const int unit_row = (SPLIT ? 0 : BM * I) + tile_row;
+    const size_t part = static_cast<size_t>(max(x.slot, 0)) * w.unit_rows;
     // SPLIT: each warpgroup writes half of the channels
     constexpr int COLS = SPLIT ? D / 2 : D;
     const int c0 = SPLIT ? COLS * I : 0;
@@ -708,16 +728,16 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
                                 pack_bf16x2(f[8 * v + 4], f[8 * v + 5]),
                                 pack_bf16x2(f[8 * v + 6], f[8 * v + 7]));
         } else if (write) {
-          float4* dst = reinterpret_cast<float4*>(w.part_o + part_row * D + c);
+          float4* dst = reinterpret_cast<float4*>(w.part_o + part * D) + (c / 4) * w.unit_rows + unit_row;
 #pragma unroll
           for (int v = 0; v < 4; ++v)
-            dst[v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
+            dst[v * w.unit_rows] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
         }
       }
     }
     if (write && (!SPLIT || I == 0)) {
       if (!whole)
-        w.part_lse[part_row] = lse;
+        w.part_lse[part + unit_row] = lse;
       else if (p.lse != nullptr)
         p.lse[out_row] = lse;
     }
@@ -742,25 +762,27 @@ __device__ void make_plan(const Work& w, Plan* plan, int* sums) {
     for (int i = 0; i < kThreads / 32; ++i) t += sums[i];
     return t;
   };
-  // of a KV head: rounds with nodes, then one step for each of the others
-  auto steps = [&](const Sizes& z) {
-    const int live = live_rounds(w, z);
-    return live * z.tiles() + w.rounds - live;
+  // of a KV head: rounds with nodes, the last of which may cost less, then those without
+  auto line = [&](const Sizes& z) {
+    int sum = 0;
+    for (int i = 0; i < w.rounds; ++i) sum += kSegCost + steps_of(w, z, i) * step_cost(w, z, i);
+    return sum;
   };
-  auto steps_at = [&](int r) { return r < w.p.S ? steps(sizes_of(w.p, r)) * w.p.Hkv : 0; };
-  const int first = steps_at(threadIdx.x);  // (the only requests, usually)
+  auto line_at = [&](int r) { return r < w.p.S ? line(sizes_of(w.p, r)) * w.p.Hkv : 0; };
+  const int first = line_at(threadIdx.x);  // (the only requests, usually)
   int mine = first;
-  for (int r = threadIdx.x + kThreads; r < w.p.S; r += kThreads) mine += steps_at(r);
+  for (int r = threadIdx.x + kThreads; r < w.p.S; r += kThreads) mine += line_at(r);
   const int total = block_sum(mine);
-  const int W = min(static_cast<int>(gridDim.x) / w.team, total);
+  const int W = max(1, min(static_cast<int>(gridDim.x) / w.team, total / kMostCost));
   const int k = blockIdx.x / w.team;
   const int share = total / W, extra = total - share * W;  // the first `extra` take one more
-  const int lo = k * share + min(k, extra), n = k < W ? share + (k < extra ? 1 : 0) : 0;
-  if (threadIdx.x == 0) *plan = Plan{lo, n, 0, 0, 0, share, extra};
+  const int lo = k < W ? k * share + min(k, extra) : total;
+  const int hi = k < W ? lo + share + (k < extra ? 1 : 0) : total;
+  if (threadIdx.x == 0) *plan = Plan{lo, hi, hi, 0, 0, 0, share, extra};
   int before = 0;
-  for (int r0 = 0; r0 < w.p.S && n > 0; r0 += kThreads) {
+  for (int r0 = 0; r0 < w.p.S && lo < hi; r0 += kThreads) {
     const int r = r0 + threadIdx.x;
-    const int own = r0 == 0 ? first : steps_at(r);
+    const int own = r0 == 0 ? first : line_at(r);
     int incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -777,13 +799,33 @@ __device__ void make_plan(const Work& w, Plan* plan, int* sums) {
     }
     incl += before;
     if (own > 0 && incl - own <= lo && lo < incl) {
-      const Sizes z = sizes_of(w.p, r);
-      const int head = steps(z), live = live_rounds(w, z) * z.tiles();
-      const int kvh = (lo - (incl - own)) / head, rest = lo - (incl - own) - kvh * head;
-      const int round = rest < live ? rest / z.tiles() : live_rounds(w, z) + rest - live;
-      plan->r = r;
-      plan->s = kvh * w.rounds + round;
-      plan->j = rest < live ? rest - round * z.tiles() : 0;
+      // the first step at or behind lo
+      Sizes z = sizes_of(w.p, r);
+      const int head = own / w.p.Hkv, kvh = (lo - (incl - own)) / head;
+      int pos = incl - own + kvh * head, round = 0;
+      while (round + 1 < w.rounds) {
+        const int len = kSegCost + steps_of(w, z, round) * step_cost(w, z, round);
+        if (pos + len > lo) break;
+        pos += len;
+        ++round;
+      }
+      pos += kSegCost;
+      const int steps = steps_of(w, z, round), cost = step_cost(w, z, round);
+      int j = lo > pos ? (lo - pos + cost - 1) / cost : 0, rr = r, s = kvh * w.rounds + round;
+      if (j < steps) {
+        pos += j * cost;
+      } else {  // behind the last one: the next segment's first
+        pos += steps * cost + kSegCost;
+        j = 0;
+        if (++s == w.segs) {
+          s = 0;
+          ++rr;
+        }
+      }
+      plan->pos = rr < w.p.S ? pos : hi;
+      plan->r = rr;
+      plan->s = s;
+      plan->j = j;
     }
     before += all;
     if (before > lo) break;  // (the same in every thread)
@@ -795,16 +837,13 @@ __device__ void note_cut(const Work& w, const Plan& plan) {
   Cut cut{0, 0, 0, 0, 0, 0};
   Walk walk(w, plan);
   Piece x;
-  int at = plan.lo;  // step that x begins at
   while (walk.next(x)) {
-    const int steps = steps_of(w, x.z, x.pair / w.team);
     if (!x.last && x.j0 == 0 && x.n > 0) {  // (the range's last piece, then)
       // the range that holds the segment's last step
-      const int e = at + steps - 1, big = plan.extra * (plan.share + 1);
+      const int e = x.end - step_cost(w, x.z, x.pair / w.team), big = plan.extra * (plan.share + 1);
       const int k1 = e < big ? e / (plan.share + 1) : plan.extra + (e - big) / plan.share;
       cut = Cut{x.r, x.kvh, x.pair, x.row_tiles, k1 - walk.team + 1, x.slot};
     }
-    at += steps - x.j0;
   }
   w.cut[blockIdx.x] = cut;
 }
@@ -894,72 +933,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// LSE = M + ln sum_j e^{LSE_j - M}, O = sum_j e^{LSE_j - LSE} O_j over the pieces of one row of
-// a cut segment: a warp a row, four pieces in flight.
-constexpr int kMergeWarps = 8;
-template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ Work w) {
-  constexpr int PER = D / 32;  // channels a lane
+// LSE = M + ln sum_j e^{LSE_j - M}, O = sum_j e^{LSE_j - LSE} O_j over the pieces of a cut
+// segment: a thread 8 channels of a row, the lanes of a warp neighbouring rows, N pieces in
+// flight.
+constexpr int kMergeThreads = 256;
+template <int D, int N>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ Work w) {
+  constexpr int PARTS = D / 8;
   constexpr float kLog2e = 1.4426950408889634f;
   // launched as a programmatic dependent: the results are complete and visible past this
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Cut cut = w.cut[blockIdx.x];
-  const int lane = threadIdx.x & 31;
-  const int unit_row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int row_groups = (w.unit_rows + 31) / 32;
+  const int unit = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);  // (row group, part)
+  const int part = unit / row_groups, unit_row = (unit - part * row_groups) * 32 + (threadIdx.x & 31);
   const int tile = unit_row / BM, tile_row = unit_row - tile * BM;
   const int tile_node = tile_row / w.group, head = tile_row - tile_node * w.group;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Cut cut = w.cut[blockIdx.x];
   const int node = (2 * cut.pair + tile) * w.tile_nodes + tile_node;
   // (a row tile without nodes has been written already)
-  if (cut.pieces == 0 || tile >= cut.tiles || tile_node >= w.tile_nodes || node >= w.p.Tn) return;
-  auto slot = [&](int i) { return i == 0 ? cut.slot : 2 * (static_cast<int>(blockIdx.x) + i * w.team); };
-  float m = -INFINITY, sum = 0.f, o[PER];
+  if (cut.pieces == 0 || part >= PARTS || unit_row >= w.unit_rows || tile >= cut.tiles ||
+      tile_node >= w.tile_nodes || node >= w.p.Tn)
+    return;
+  float m = -INFINITY, sum = 0.f, o[8];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) o[i] = 0.f;
-  for (int j = 0; j < cut.pieces; j += 4) {
-    float lse[4], v[4][PER];
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  for (int j = 0; j < cut.pieces; j += N) {
+    float lse[N];
+    float4 v[N][2];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < N; ++s) {
       lse[s] = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) v[s][i] = 0.f;
+      v[s][0] = v[s][1] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (j + s < cut.pieces) {
-        const size_t at = static_cast<size_t>(slot(j + s)) * w.unit_rows + unit_row;
-        lse[s] = w.part_lse[at];
-        const float* src = w.part_o + at * D + lane * PER;
-        if constexpr (PER == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(src);
-          v[s][0] = y.x, v[s][1] = y.y, v[s][2] = y.z, v[s][3] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(src);
-          v[s][0] = y.x, v[s][1] = y.y;
-        }
+        const int slot = j + s == 0 ? cut.slot : 2 * (static_cast<int>(blockIdx.x) + (j + s) * w.team);
+        const size_t at = static_cast<size_t>(slot) * w.unit_rows;
+        lse[s] = w.part_lse[at + unit_row];
+        const float4* src = reinterpret_cast<const float4*>(w.part_o + at * D) + unit_row;
+        v[s][0] = src[2 * part * w.unit_rows];
+        v[s][1] = src[(2 * part + 1) * w.unit_rows];
       }
     }
-    const float mn = fmaxf(fmaxf(m, lse[0]), fmax3(lse[1], lse[2], lse[3]));
+    float mn = m;
+#pragma unroll
+    for (int s = 0; s < N; ++s) mn = fmaxf(mn, lse[s]);
     const float ms = mn == -INFINITY ? 0.f : mn;
     const float al = ex2((m - ms) * kLog2e);
     m = mn;
     sum *= al;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] *= al;
+    for (int i = 0; i < 8; ++i) o[i] *= al;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < N; ++s) {
       const float f = ex2((lse[s] - ms) * kLog2e);
       sum += f;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) o[i] = fmaf(f, v[s][i], o[i]);
+      for (int h = 0; h < 2; ++h) {
+        o[4 * h] = fmaf(f, v[s][h].x, o[4 * h]);
+        o[4 * h + 1] = fmaf(f, v[s][h].y, o[4 * h + 1]);
+        o[4 * h + 2] = fmaf(f, v[s][h].z, o[4 * h + 2]);
+        o[4 * h + 3] = fmaf(f, v[s][h].w, o[4 * h + 3]);
+      }
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (no key is seen)
   const size_t out =
       (static_cast<size_t>(cut.r) * w.p.Hq + cut.kvh * w.group + head) * w.p.Tn + node;
-  uint16_t* dst = static_cast<uint16_t*>(w.p.o) + out * D + lane * PER;
-#pragma unroll
-  for (int i = 0; i < PER; i += 2)
-    *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(o[i] * inv, o[i + 1] * inv);
-  if (w.p.lse != nullptr && lane == 0)
-    w.p.lse[out] = sum == 0.f ? -INFINITY : m + logf(sum);
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(w.p.o) + out * D + 8 * part) =
+      make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                 pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+  if (w.p.lse != nullptr && part == 0) w.p.lse[out] = sum == 0.f ? -INFINITY : m + logf(sum);
 }
 
 struct Shape {
@@ -1023,10 +1066,13 @@ cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<D, SPLIT>, tmQ, tmK, tmV, w);
   if (e != cudaSuccess || w.direct) return e;
-  cfg.gridDim = dim3(grid, (w.unit_rows + kMergeWarps - 1) / kMergeWarps);
-  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.gridDim = dim3(grid, ((w.unit_rows + 31) / 32 * (D / 8) + kMergeThreads / 32 - 1) / (kMergeThreads / 32));
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, w);
+  // (few segments are cut into many pieces each)
+  const long long units = static_cast<long long>(w.p.S) * w.segs * w.team;
+  return grid > 4 * units ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, 8>, w)
+                          : cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, 2>, w);
 }
 
 template <int D, bool SPLIT>
