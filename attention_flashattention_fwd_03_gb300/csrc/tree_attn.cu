@@ -23,6 +23,8 @@
 //   warp 1      issues the products: S = Q K^T into tensor memory, O += P V with P from
 //               tensor memory
 //   warp 2      the segment's tree: its parents, checked
+//   warp 3      what there is to do, piece after piece, for all the others (the softmax warps,
+//               each thread of which holds a whole score row, have no registers to spare)
 //   warps 4-7, 8-11  softmax, a row a thread, of two chains of tiles that alternate on the
 //               tensor cores
 // With one row tile the two chains take every other key tile, each with its own maximum, sum
@@ -31,6 +33,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstddef>
 
 #include "api.h"
 #include "attn_tile.cuh"
@@ -51,6 +54,8 @@ constexpr int kMaxNodes = GBATTN_TREE_MAX_NODES;
 constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by > 2^8
 constexpr int kDirectSteps = 4;      // caches of so many steps at most are not cut
 constexpr int kMaxTeam = 8;
+constexpr int kPieces = 4;           // pieces told ahead
+constexpr int kRoles = 11;           // warps that are told
 // (the block launches with 168 registers a thread)
 constexpr int kRegsLaunch = 168, kRegsWg0 = 104, kRegsSoftmax = 200;
 static_assert(kRegsWg0 + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split exceeds the launch");
@@ -90,6 +95,18 @@ struct Work {  // what the kernels share besides the caller's operands
   int direct;       // teams take whole segments in turn
 };
 
+// The part of a segment that a CTA takes.
+struct Piece {
+  int r, kvh, pair;
+  int L, nodes;   // of the request: tokens before the tree, nodes of it
+  int j0, n;      // first key tile and how many (0: nothing to compute; -1: no more pieces)
+  int row_tiles;  // of the pair's two, how many hold nodes
+  int slot;       // of its partial output; -1: the segment is whole
+  int last;       // holds the segment's last step
+  int bad;        // the request's sizes are out of bounds
+  int tail;       // some of its tiles hold nodes' keys
+};
+
 // A checked tree: the parent of each node + 1, and the first node of the chain of consecutive
 // numbers that ends with it.
 struct Tree {
@@ -108,11 +125,13 @@ struct Cfg {
   static constexpr int OFF_TREE = OFF_RING + NSLOT * TILE_BYTES;  // [2] Tree
   static constexpr int OFF_JOIN = OFF_TREE + 2 * sizeof(Tree);    // SPLIT: [2][BM] float2, maximum and sum
   static constexpr int OFF_BAR = OFF_JOIN + (SPLIT ? 2 * BM * 8 : 0);
-  static constexpr int NBAR = 2 + 2 * NSLOT + 6 + 1 + 4 + 2;
+  static constexpr int NBAR = 2 + 2 * NSLOT + 6 + 1 + 4 + 2 + 2 * kPieces;
   static constexpr int OFF_PLAN = OFF_BAR + NBAR * 8;
   static constexpr int OFF_SUMS = OFF_PLAN + sizeof(Plan) + 4;    // [12] ints
-  static constexpr int OFF_MISC = (OFF_SUMS + 48 + 15) & ~15;     // TMEM address, abort, bad tree [2]
-  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;         // + slack for 1024-byte alignment
+  static constexpr int OFF_PIECES = OFF_SUMS + 48;                   // [kPieces]
+  static constexpr int OFF_PLACE = OFF_PIECES + kPieces * sizeof(Piece);  // [BM] uint16_t
+  static constexpr int OFF_MISC = (OFF_PLACE + BM * 2 + 15) & ~15;   // TMEM address, abort, bad tree [2]
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;            // + slack for 1024-byte alignment
   static constexpr uint32_t TMEM_COLS = 512;
   // TMEM columns: S_0 [0,128), S_1 [128,256), O_0 and O_1 from 256 (D each).  P_i (bf16
   // pairs, 64 columns) overwrites the upper half of S_i.
@@ -139,6 +158,8 @@ struct Bars {
   __device__ uint32_t tree_full(int b) const { return at(9 + 2 * C::NSLOT + b); }
   __device__ uint32_t tree_empty(int b) const { return at(11 + 2 * C::NSLOT + b); }
   __device__ uint32_t joined(int i) const { return at(13 + 2 * C::NSLOT + i); }
+  __device__ uint32_t piece_full(int i) const { return at(15 + 2 * C::NSLOT + i); }
+  __device__ uint32_t piece_empty(int i) const { return at(15 + 2 * C::NSLOT + kPieces + i); }
 };
 
 // A request's sizes: tokens before the tree, nodes, and whether they are out of bounds (then
@@ -146,7 +167,6 @@ struct Bars {
 struct Sizes {
   int L, n;
   bool bad;
-  __device__ int keys() const { return L + n; }
   __device__ int tiles() const { return (L + n + BN - 1) / BN; }
 };
 __device__ __forceinline__ Sizes sizes_of(const TreeParams& p, int r) {
@@ -176,25 +196,13 @@ __device__ __forceinline__ int step_cost(const Work& w, const Sizes& z, int roun
   return tiles <= 0 ? kStepCost0 : (tiles == 1 ? kStepCost1 : kStepCost2);
 }
 
-// The part of a segment that a CTA takes.
-struct Piece {
-  Sizes z;
-  int r, kvh, pair;
-  int j0, n;      // first key tile and how many (0: nothing to compute)
-  int row_tiles;  // of the pair's two, how many hold nodes
-  int slot;       // of its partial output; -1: the segment is whole
-  bool last;      // holds the segment's last step
-  int end;        // where the segment ends (not if direct)
-  __device__ bool masked(int j) const { return (j + 1) * BN > z.L; }
-  __device__ bool tail() const { return n > 0 && masked(j0 + n - 1); }
-};
-
-// Walks over this CTA's pieces; every role does so for itself.
+// Walks over this CTA's pieces.
 struct Walk {
   const Work& w;
   int team, member;
   int at;  // place of the next step on the line, or (direct) the next segment
   int hi, r, s, j, index = 0;
+  int end = 0;  // where the segment of the last piece ends on the line (not if direct)
   Sizes z;
   __device__ Walk(const Work& w_, const Plan& plan)
       : w(w_), team(blockIdx.x / w_.team), member(blockIdx.x - team * w_.team),
@@ -216,17 +224,21 @@ struct Walk {
     const int round = s - x.kvh * w.rounds;
     const int steps = steps_of(w, z, round), cost = step_cost(w, z, round);
     const int n = w.direct ? steps : min((hi - at + cost - 1) / cost, steps - j);
-    x.z = z;
+    const int tiles = live_tiles(w, z);
     x.r = r;
     x.pair = round * w.team + member;
-    x.row_tiles = max(0, min(2, live_tiles(w, z) - 2 * x.pair));
+    x.L = z.L;
+    x.nodes = z.n;
+    x.row_tiles = max(0, min(2, tiles - 2 * x.pair));
     x.j0 = j;
     x.n = x.row_tiles > 0 ? n : 0;
     x.last = j + n == steps;
+    x.bad = z.bad;
+    x.tail = x.n > 0 && (j + n) * BN > z.L;
     x.slot = j == 0 && x.last ? -1 : 2 * static_cast<int>(blockIdx.x) + (index > 0 ? 1 : 0);
     ++index;
     if (!w.direct) {
-      x.end = at + (steps - j) * cost;
+      end = at + (steps - j) * cost;
       at += n * cost;
       j += n;
       if (j == steps) {
@@ -244,11 +256,74 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------------------
+// warp 3: tells the other roles what to do
+// ---------------------------------------------------------------------------
+template <int D, bool SPLIT>
+__device__ void planner_warp(const Work& w, const Plan& plan, uint8_t* smem, const Bars<D, SPLIT>& bar,
+                             volatile int* abort) {  // (one lane)
+  using C = Cfg<D, SPLIT>;
+  const TreeParams& p = w.p;
+  Piece* pieces = reinterpret_cast<Piece*>(smem + C::OFF_PIECES);
+  Cut cut{0, 0, 0, 0, 0, 0};
+  Walk walk(w, plan);
+  Piece x;
+  for (int i = 0;; ++i) {
+    const bool more = walk.next(x);
+    if (!more) x.n = -1;
+    if (!mbar_wait(bar.piece_empty(i % kPieces), ((i / kPieces) & 1) ^ 1, abort, p.flags, p.wait_limit_ns))
+      return;
+    pieces[i % kPieces] = x;
+    mbar_arrive(bar.piece_full(i % kPieces));
+    if (!more) break;
+    if (x.bad) raise_flag(p.flags, DEVFLAG_BAD_SEQLEN);
+    if (!w.direct && !x.last && x.j0 == 0 && x.n > 0) {  // (the range's last piece, then)
+      // the rows go on up to the range that holds the segment's last step
+      const int e = walk.end - step_cost(w, walk.z, x.pair / w.team), big = plan.extra * (plan.share + 1);
+      const int k1 = e < big ? e / (plan.share + 1) : plan.extra + (e - big) / plan.share;
+      cut = Cut{x.r, x.kvh, x.pair, x.row_tiles, k1 - walk.team + 1, x.slot};
+    }
+  }
+  if (!w.direct) w.cut[blockIdx.x] = cut;
+}
+
+// A field of a piece, by the piece's shared-memory address; the whole warp calls this together.
+// All lanes read the same: the shuffle
+// tells the compiler so, which then keeps loops over it and what the products are issued with in
+// uniform registers (200 nodes: 241 us without).
+__device__ __forceinline__ int field_at(uint32_t x, uint32_t offset) {
+  int v;
+  asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(x + offset) : "memory");
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+#define FIELD(x, name) field_at(x, offsetof(Piece, name))
+
+// A warp's view of the pieces.
+template <int D, bool SPLIT>
+struct Feed {
+  using C = Cfg<D, SPLIT>;
+  const Bars<D, SPLIT>& bar;
+  int i = 0;
+  __device__ explicit Feed(const Bars<D, SPLIT>& b) : bar(b) {}
+  // The next piece's address, or 0 (after the last one, or the CTA is stopping).
+  __device__ uint32_t next(const TreeParams& p, volatile int* abort) {
+    if (!mbar_wait_warp(bar.piece_full(i % kPieces), (i / kPieces) & 1, abort, p.flags, p.wait_limit_ns))
+      return 0;
+    const uint32_t x = bar.base - C::OFF_BAR + C::OFF_PIECES + (i % kPieces) * sizeof(Piece);
+    return FIELD(x, n) < 0 ? 0 : x;
+  }
+  __device__ void done() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar.piece_empty(i % kPieces));
+    ++i;
+  }
+};
+
+// ---------------------------------------------------------------------------
 // producer warp
 // ---------------------------------------------------------------------------
 template <int D, bool SPLIT>
 __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
-                              const CUtensorMap* tmV, const Work& w, const Plan& plan,
+                              const CUtensorMap* tmV, const Work& w,
                               uint32_t sbase, const Bars<D, SPLIT>& bar, volatile int* abort) {
   using C = Cfg<D, SPLIT>;
   const TreeParams& p = w.p;
@@ -259,30 +334,30 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
   const bool once = w.team == 1 && w.rounds == 1;  // every K/V byte is read once
   int rc = 0, uc = 0;
   bool ok = true, last_q_issued = false;
-  Walk walk(w, plan);
-  Piece x;
-  while (ok && walk.next(x)) {
-    if (x.z.bad && lane == 0) raise_flag(p.flags, DEVFLAG_BAD_SEQLEN);
-    if (x.n == 0) continue;
-    const int blocks = (x.z.keys() + kBS - 1) / kBS;
+  Feed<D, SPLIT> feed(bar);
+  for (uint32_t x; ok && (x = feed.next(p, abort)); feed.done()) {
+    const int n = FIELD(x, n), r = FIELD(x, r), kvh = FIELD(x, kvh), j0 = FIELD(x, j0), j1 = j0 + n;
+    if (n == 0) continue;
+    const int row_tiles = FIELD(x, row_tiles), node0 = 2 * FIELD(x, pair) * w.tile_nodes;
+    const int blocks = (FIELD(x, L) + FIELD(x, nodes) + kBS - 1) / kBS;
     // lane l < 8 reads the table entry of block l of a tile, one tile ahead of the copies
     auto table_entry = [&](int j) -> int {
       const int b = j * (BN / kBS) + lane;
       return lane < BN / kBS && b < blocks
-                 ? p.block_table[static_cast<size_t>(x.r) * p.max_blocks + b]
+                 ? p.block_table[static_cast<size_t>(r) * p.max_blocks + b]
                  : 0;
     };
-    int next_phys = table_entry(x.j0);
-    for (int j = x.j0; j < x.j0 + x.n && ok; ++j) {
+    int next_phys = table_entry(j0);
+    for (int j = j0; j < j1 && ok; ++j) {
       const int nblk = min(BN / kBS, blocks - j * (BN / kBS));
       int phys = next_phys, row = 0;
-      if (j + 1 < x.j0 + x.n) next_phys = table_entry(j + 1);
+      if (j + 1 < j1) next_phys = table_entry(j + 1);
       if (lane < nblk) {
         if (phys < 0 || phys >= p.num_pool_blocks) {
           raise_flag(p.flags, DEVFLAG_BAD_BLOCK);
           phys = 0;
         }
-        row = (phys * p.Hkv + x.kvh) * kBS;
+        row = (phys * p.Hkv + kvh) * kBS;
       }
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
@@ -310,7 +385,7 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
         __syncwarp();
         ++rc;
       }
-      if (ok && j == x.j0) {
+      if (ok && j == j0) {
         // the queries go behind the first tile, whose slots are free before the piece before is
         // done with its own queries
         if (!mbar_wait_warp(bar.q_empty(), (uc & 1) ^ 1, abort, p.flags, lim)) {
@@ -319,12 +394,12 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
         }
         last_q_issued = !(p.withhold_copy && uc == 0);  // test hook: withhold the first Q
         if (lane == 0 && last_q_issued) {
-          mbar_arrive_expect_tx(bar.q_full(), x.row_tiles * C::KB * w.group * w.tile_nodes * 128);
-          for (int i = 0; i < x.row_tiles; ++i)
+          mbar_arrive_expect_tx(bar.q_full(), row_tiles * C::KB * w.group * w.tile_nodes * 128);
+          for (int i = 0; i < row_tiles; ++i)
 #pragma unroll
             for (int kb = 0; kb < C::KB; ++kb)
               tma_load_4d(sQ + i * C::TILE_BYTES + kb * C::BOX_BYTES, tmQ, bar.q_full(), kb * 64, 0,
-                          (2 * x.pair + i) * w.tile_nodes, x.r * p.Hkv + x.kvh);
+                          node0 + i * w.tile_nodes, r * p.Hkv + kvh);
         }
         ++uc;
       }
@@ -369,20 +444,19 @@ __device__ __forceinline__ bool read_tree(const int32_t* parents, int n, Tree& t
 }
 
 template <int D, bool SPLIT>
-__device__ void tree_warp(const Work& w, const Plan& plan, uint8_t* smem, const Bars<D, SPLIT>& bar,
+__device__ void tree_warp(const Work& w, uint8_t* smem, const Bars<D, SPLIT>& bar,
                           volatile int* abort) {
   using C = Cfg<D, SPLIT>;
   const TreeParams& p = w.p;
   const int lane = threadIdx.x & 31;
   volatile int* bad_tree = reinterpret_cast<volatile int*>(smem + C::OFF_MISC) + 2;
   int mc = 0;
-  Walk walk(w, plan);
-  Piece x;
-  while (walk.next(x)) {
-    if (!x.tail()) continue;
+  Feed<D, SPLIT> feed(bar);
+  for (uint32_t x; (x = feed.next(p, abort)); feed.done()) {
+    if (!FIELD(x, tail)) continue;
     const int b = mc & 1;
     if (!mbar_wait_warp(bar.tree_empty(b), ((mc >> 1) & 1) ^ 1, abort, p.flags, p.wait_limit_ns)) return;
-    const bool bad = read_tree(p.parents + static_cast<size_t>(x.r) * p.Tn, x.z.n,
+    const bool bad = read_tree(p.parents + static_cast<size_t>(FIELD(x, r)) * p.Tn, FIELD(x, nodes),
                                reinterpret_cast<Tree*>(smem + C::OFF_TREE)[b]);
     if (lane == 0) {
       bad_tree[b] = bad;
@@ -476,18 +550,18 @@ struct MmaWarp {
     return true;
   }
 
-  __device__ void run(const Plan& plan) {
+  __device__ void run() {
     int uc = 0;
-    Walk walk(w, plan);
-    Piece x;
-    while (walk.next(x)) {
-      const int n = x.n;
+    Feed<D, SPLIT> feed(bar);
+    for (uint32_t x; (x = feed.next(w.p, abort)); feed.done()) {
+      const int n = FIELD(x, n);
       if (n == 0) continue;
       if (!wait(bar.q_full(), uc & 1)) return;
       ++uc;
       cleared = -1;
       // row of the last tile from which on there are no keys
-      auto dead_from = [&](int t) { return x.z.keys() - (x.j0 + t) * BN; };
+      const int keys_left = FIELD(x, L) + FIELD(x, nodes) - FIELD(x, j0) * BN;
+      auto dead_from = [&](int t) { return keys_left - t * BN; };
       if (SPLIT) {
         if (!issue_s<0>(0, false)) return;
         mma_commit_warp(bar.slot_empty(slot(0)));
@@ -508,7 +582,7 @@ struct MmaWarp {
           }
         }
       } else {
-        const bool two = x.row_tiles == 2;
+        const bool two = FIELD(x, row_tiles) == 2;
         if (!issue_s<0>(0, false)) return;
         if (two && !issue_s<1>(0, true)) return;
         mma_commit_warp(bar.slot_empty(slot(0)));
@@ -547,7 +621,7 @@ __device__ __forceinline__ uint32_t seen_bits(const Tree& tree, int& a, int x) {
 // softmax warpgroup of chain I (128 threads, one query row each)
 // ---------------------------------------------------------------------------
 template <int D, bool SPLIT>
-__device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint32_t tmem,
+__device__ void softmax_wg(const Work& w, uint8_t* smem, uint32_t tmem,
                            const Bars<D, SPLIT>& bar, volatile int* abort, const int I) {
   using C = Cfg<D, SPLIT>;
   const TreeParams& p = w.p;
@@ -570,22 +644,27 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
     tc_fence_after();
     return true;
   };
-  Walk walk(w, plan);
-  Piece x;
-  while (walk.next(x)) {
-    const int node0 = (2 * x.pair + (SPLIT ? 0 : I)) * w.tile_nodes;  // of the row tile
-    const int tile_node = tile_row / w.group, head = tile_row - tile_node * w.group;
-    const int node = node0 + tile_node;
-    const bool exists = tile_node < w.tile_nodes && node < p.Tn && x.pair < w.pairs;
-    const bool live = __any_sync(0xffffffffu, exists && node < x.z.n);  // else the warp only keeps step
-    const int n = SPLIT ? (x.n + 1 - I) / 2 : (I < x.row_tiles ? x.n : 0);
-    const bool tail = x.tail();
+  // node of the row tile and head of this thread's row
+  auto place = [&]() {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(bar.base - C::OFF_BAR + C::OFF_PLACE + 2 * tile_row) : "memory");
+    return static_cast<int>(v);
+  };
+  const Tree* trees = reinterpret_cast<const Tree*>(smem + C::OFF_TREE);
+  Feed<D, SPLIT> feed(bar);
+  for (uint32_t x; (x = feed.next(p, abort)); feed.done()) {
+    const int total = FIELD(x, n), L = FIELD(x, L);
+    int j = FIELD(x, j0) + (SPLIT ? I : 0);
+    const int n = SPLIT ? (total + 1 - I) / 2 : (I < FIELD(x, row_tiles) ? total : 0);
+    // this row's node (-1: none is in this place); a warp without any only keeps step
+    const int nodes = FIELD(x, nodes), pair = FIELD(x, pair);
+    int node = (2 * pair + (SPLIT ? 0 : I)) * w.tile_nodes + (place() & 255);
+    if (node >= nodes) node = -1;
+    const bool live = __any_sync(0xffffffffu, node >= 0);
     const int b = mc & 1;
-    const Tree& tree = reinterpret_cast<const Tree*>(smem + C::OFF_TREE)[b];
     bool have_mask = false;
     float m = -INFINITY, l = 0.f;
-    for (int i = 0; i < n; ++i) {
-      const int j = x.j0 + (SPLIT ? 2 * i + I : i);
+    for (int i = 0; i < n; ++i, j += SPLIT ? 2 : 1) {
       if (!mbar_wait_warp(bar.s_full(I), sc & 1, abort, p.flags, lim)) return;
       if (live) {
         tc_fence_after();
@@ -602,16 +681,16 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
 #pragma unroll
             for (int e = 0; e < 32; ++e) s[32 * c + e] = __uint_as_float(u32[c][e]);
         }
-        const bool masked = x.masked(j);
+        const bool masked = (j + 1) * BN > L;
         if (masked) {
           if (!have_mask &&
               !mbar_wait_warp(bar.tree_full(b), (mc >> 1) & 1, abort, p.flags, lim))
             return;
           have_mask = true;
-          int a = exists && node < x.z.n ? node : -1;
+          int a = node;
 #pragma unroll
           for (int c = 3; c >= 0; --c) {
-            const uint32_t bits = seen_bits(tree, a, j * BN - x.z.L + 32 * c);
+            const uint32_t bits = seen_bits(trees[b], a, j * BN - L + 32 * c);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!(bits >> e & 1u)) s[32 * c + e] = -INFINITY;
@@ -643,10 +722,8 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
         }
         const float ms = (m == -INFINITY) ? 0.f : m * sl2;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        if (masked)
-          write_p<false>(s, sl2, ms, lane_base + C::p_col(I), sum);
-        else
-          write_p<true>(s, sl2, ms, lane_base + C::p_col(I), sum);
+        // (one copy of this code for all tiles: the roles share one instruction cache)
+        write_p<false>(s, sl2, ms, lane_base + C::p_col(I), sum);
         l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
@@ -654,8 +731,8 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
       mbar_arrive(bar.p_full(I));
       ++sc;
     }
-    bool bad = x.z.bad;
-    if (tail) {
+    bool bad = false;
+    if (FIELD(x, tail)) {
       // (every warp meets every mask, so that none is a buffer ahead)
       if (!have_mask && !mbar_wait_warp(bar.tree_full(b), (mc >> 1) & 1, abort, p.flags, lim)) return;
       bad |= bad_trees[b] != 0;
@@ -665,19 +742,22 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
     }
 
     // ---- results of the piece: O and LSE, or a partial output ----
-    const bool dead = node >= x.z.n;  // no node is in this place
+    const int slot = FIELD(x, slot), pair_now = FIELD(x, pair), last = FIELD(x, last);
+    const int head = place() >> 8, at = (2 * pair_now + (SPLIT ? 0 : I)) * w.tile_nodes + (place() & 255);
+    const bool dead = node < 0;
+    const bool exists = at < p.Tn && head < w.group && pair_now < w.pairs;
     // a row tile without nodes: zeros (or NaN), once
-    const bool computed = SPLIT ? x.n > 0 : n > 0;
-    const bool whole = computed ? x.slot < 0 : true;
-    const bool write = exists && (computed || x.last);
+    const bool computed = SPLIT ? total > 0 : n > 0;
+    const bool whole = computed ? slot < 0 : true;
+    const bool write = exists && (computed || last);
     float f0 = 0.f, f1 = 0.f;         // factors of O_0 and O_1 (one of them without SPLIT)
     float M = m, sum = l;
     bool two = false;
     // the chain's last P V product
     if (n > 0 && !mbar_wait_warp(bar.s_free(I), (sc - 1) & 1, abort, p.flags, lim)) return;
     tc_fence_after();
-    if (SPLIT && x.n > 0) {
-      two = x.n > 1;  // (chain 1 has a tile)
+    if (SPLIT && total > 0) {
+      two = total > 1;  // (chain 1 has a tile)
       join[I * BM + tile_row] = make_float2(m, l);
       if (!meet(0)) return;
       const float2 a = join[tile_row], c = join[BM + tile_row];  // (-inf, 0 without a tile)
@@ -690,15 +770,15 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
       f0 = 1.f;
     }
     const bool none = sum == 0.f || dead || !computed;  // no key is seen (a NaN is a result)
-    const bool nan = x.z.bad || (bad && !dead);
+    const bool nan = FIELD(x, bad) != 0 || (bad && !dead);
     const float inv = nan ? kNan : (none ? 0.f : 1.f / sum);
     const float lse = nan ? kNan : (none ? -INFINITY : M * p.scale + logf(sum));
     f0 *= inv;
     f1 *= inv;
     const size_t out_row =
-        (static_cast<size_t>(x.r) * p.Hq + x.kvh * w.group + head) * p.Tn + node;
+        (static_cast<size_t>(FIELD(x, r)) * p.Hq + FIELD(x, kvh) * w.group + head) * p.Tn + at;
     const int unit_row = (SPLIT ? 0 : BM * I) + tile_row;
-    const size_t part = static_cast<size_t>(max(x.slot, 0)) * w.unit_rows;
+    const size_t part = static_cast<size_t>(max(slot, 0)) * w.unit_rows;
     // SPLIT: each warpgroup writes half of the channels
     constexpr int COLS = SPLIT ? D / 2 : D;
     const int c0 = SPLIT ? COLS * I : 0;
@@ -742,7 +822,7 @@ __device__ void softmax_wg(const Work& w, const Plan& plan, uint8_t* smem, uint3
         p.lse[out_row] = lse;
     }
     // the next piece's products may overwrite what the other warpgroup reads here
-    if (SPLIT && x.n > 0) {
+    if (SPLIT && total > 0) {
       if (!meet(1)) return;
       ++jc;
     }
@@ -832,22 +912,6 @@ __device__ void make_plan(const Work& w, Plan* plan, int* sums) {
   }
 }
 
-// Notes the rows that begin in this CTA's range and go on in the next one.
-__device__ void note_cut(const Work& w, const Plan& plan) {
-  Cut cut{0, 0, 0, 0, 0, 0};
-  Walk walk(w, plan);
-  Piece x;
-  while (walk.next(x)) {
-    if (!x.last && x.j0 == 0 && x.n > 0) {  // (the range's last piece, then)
-      // the range that holds the segment's last step
-      const int e = x.end - step_cost(w, x.z, x.pair / w.team), big = plan.extra * (plan.share + 1);
-      const int k1 = e < big ? e / (plan.share + 1) : plan.extra + (e - big) / plan.share;
-      cut = Cut{x.r, x.kvh, x.pair, x.row_tiles, k1 - walk.team + 1, x.slot};
-    }
-  }
-  w.cut[blockIdx.x] = cut;
-}
-
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -881,10 +945,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar.tree_empty(i), 8);
       mbar_init(bar.joined(i), 256);
     }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(bar.piece_full(i), 1);
+      mbar_init(bar.piece_empty(i), kRoles);
+    }
     mbar_init(bar.teardown(), 1);
     *abort = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
+  }
+  if (threadIdx.x >= BM && threadIdx.x < 2 * BM) {
+    // rows behind the tile's nodes get a head that does not exist
+    const int row = threadIdx.x - BM, node = row / w.group;
+    reinterpret_cast<uint16_t*>(smem + C::OFF_PLACE)[row] = static_cast<uint16_t>(
+        node < w.tile_nodes ? node | (row - node * w.group) << 8 : 255 | 255 << 8);
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmQ);
@@ -902,27 +976,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Plan plan = *plan_at;  // (not set, nor read, if w.direct)
 
   if (warp < 4) {
     regs_decrease<kRegsWg0>();
     if (warp == 0) {
-      producer_warp<D, SPLIT>(&tmQ, &tmK, &tmV, w, plan, sbase, bar, abort);
+      producer_warp<D, SPLIT>(&tmQ, &tmK, &tmV, w, sbase, bar, abort);
     } else if (warp == 1) {
       MmaWarp<D, SPLIT> mma(w, bar, abort, sbase, tmem);
-      mma.run(plan);
+      mma.run();
       // Every product this warp issued has finished once the teardown barrier flips.
       mma_commit_warp(bar.teardown());
       if (lane == 0) mbar_wait_quiet(bar.teardown(), 0, 1000000000ull);
       __syncwarp();
     } else if (warp == 2) {
-      tree_warp<D, SPLIT>(w, plan, smem, bar, abort);
-    } else if (!w.direct && lane == 0) {
-      note_cut(w, plan);
+      tree_warp<D, SPLIT>(w, smem, bar, abort);
+    } else if (lane == 0) {
+      // (the plan is not set, nor read, if w.direct)
+      planner_warp<D, SPLIT>(w, *plan_at, smem, bar, abort);
     }
   } else {
     regs_increase<kRegsSoftmax>();
-    softmax_wg<D, SPLIT>(w, plan, smem, tmem, bar, abort, warp < 8 ? 0 : 1);
+    softmax_wg<D, SPLIT>(w, smem, tmem, bar, abort, warp < 8 ? 0 : 1);
   }
 
   tc_fence_before();
