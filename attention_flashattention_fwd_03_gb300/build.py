@@ -28,7 +28,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgbattn.so")
 SOURCES = ["attn_fwd.cu", "paged_decode.cu", "kv_cache.cu", "norm_rope.cu", "kv4_cache.cu", "kv4_decode.cu",
-           "tree_attn.cu", "draft_verify.cu", "kv_keep.cu", "api.cu", "api_rope.cu", "api_tree.cu",
+           "tree_attn.cu", "tree_short.cu", "draft_verify.cu", "kv_keep.cu", "api.cu", "api_rope.cu", "api_tree.cu",
            "decode_noalloc.cu"]
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))

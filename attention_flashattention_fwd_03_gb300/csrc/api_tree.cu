@@ -92,6 +92,7 @@ GBATTN_API int paged_attn_tree(const void* q, const void* k_pool, const void* v_
   if ((st = encode_bf16(enc, &tmK, k_pool, 2, dpool, pool_strides, pool_box)) != ATTN_OK) return st;
   if ((st = encode_bf16(enc, &tmV, v_pool, 2, dpool, pool_strides, pool_box)) != ATTN_OK) return st;
   TreeParams p{};
+  p.q = q;
   p.block_table = block_table;
   p.seq_lens = seq_lens;
   p.parents = parents;

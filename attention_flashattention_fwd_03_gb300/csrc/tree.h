@@ -10,7 +10,10 @@
 
 namespace gbattn {
 
+constexpr int kTreeShortRows = 64;
+
 struct TreeParams {
+  const void* q;               // [S, Hq, Tn, D] bf16
   const int32_t* block_table;  // [S, max_blocks]
   const int32_t* seq_lens;     // [S]: tokens before the tree
   const int32_t* parents;      // [S, Tn]
@@ -37,6 +40,11 @@ int tree_tile_nodes(int group, int Tn);
 cudaError_t launch_tree_attn(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                              const TreeParams& p, void* workspace, int num_sms,
                              cudaStream_t stream);
+
+// The same for up to kTreeShortRows query rows on a KV head, without a workspace (tree_short.cu).
+cudaError_t prepare_tree_short();
+cudaError_t launch_tree_short(const CUtensorMap& tmK, const CUtensorMap& tmV, const TreeParams& p,
+                              cudaStream_t stream);
 
 struct VerifyParams {
   const void *p, *q;           // rows of V probabilities; q may be nullptr

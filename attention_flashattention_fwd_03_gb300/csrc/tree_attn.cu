@@ -52,7 +52,6 @@ constexpr int kBS = kPagedBlock;
 constexpr int kThreads = 384;
 constexpr int kMaxNodes = GBATTN_TREE_MAX_NODES;
 constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by > 2^8
-constexpr int kDirectSteps = 4;      // caches of so many steps at most are not cut
 constexpr int kMaxTeam = 8;
 constexpr int kPieces = 4;           // pieces told ahead
 constexpr int kRoles = 11;           // warps that are told
@@ -1082,7 +1081,8 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 struct Shape {
   int group, tile_nodes, row_tiles, pairs, team, rounds, segs, unit_rows;
   long long units, steps;  // segments of the batch, and their steps at most
-  bool direct;
+  bool small;   // for tree_short.cu
+  bool direct;  // CTAs take whole segments
 };
 
 Shape shape_of(int S, int Tn, int Hq, int Hkv, int max_seq_len) {
@@ -1098,7 +1098,27 @@ Shape shape_of(int S, int Tn, int Hq, int Hkv, int max_seq_len) {
   const long long per_seg = std::max<long long>(1, (max_seq_len + (BN - 1ll)) / BN);
   s.units = static_cast<long long>(S) * s.segs;
   s.steps = per_seg * s.units;
-  s.direct = per_seg <= kDirectSteps;
+  // Which kernel, by the bound on the keys.  Device time in us, tree_short.cu / whole segments / cut
+  // segments (lengths from half the bound; D 128 but for *):
+  //   requests x heads   rows  100               250               500               800               1200              1800
+  //   1 x 8/2 *            20  3.5 / 7.4 / 13    5.3 / 7.7 / 10    6.9 / 9.2 / 13    9.2 / 9.9 / 11    13 / 12 / 13      16 / 15 / 12
+  //   1 x 32/8             16  4.6 / 8.0 / 15    6.9 / 8.7 / 15    8.7 / 10 / 15     12 / 12 / 13      16 / 15 / 15      21 / 19 / 14
+  //   5 x 12/2             48  7.7 / 8.3 / 15    10 / 9.1 / 15     18 / 12 / 15      26 / 16 / 14      36 / 20 / 15      52 / 26 / 16
+  //   20 x 32/8            32  9.6 / 12 / 16     12 / 14 / 18      18 / 19 / 22      24 / 25 / 26      30 / 26 / 28      44 / 42 / 33
+  //   64 x 12/2            48  9.4 / 9.4 / 16    14 / 12 / 17      21 / 14 / 20      31 / 18 / 23      42 / 22 / 26      60 / 28 / 30
+  //   100 x 16/8           64  27 / 34 / 39      38 / 46 / 55      55 / 59 / 75      75 / 75 / 89      103 / 94 / 101    143 / 128 / 120
+  //   100 x 16/8 *          8  9 / 28 / 32       14 / 32 / 39      21 / 45 / 63      29 / 54 / 76      39 / 67 / 87      54 / 90 / 102
+  //   200 x 8/2            16  9 / 18 / 20       13 / 21 / 27      20 / 33 / 38      27 / 42 / 46      37 / 54 / 53      51 / 72 / 64
+  const int rows = s.group * Tn;
+  const long long heads = static_cast<long long>(S) * Hkv;
+  const bool many = heads >= 304;  // two a SM
+  if (rows <= 16)
+    s.small = per_seg <= 6 || (many && per_seg <= 20);
+  else if (rows <= 32)
+    s.small = per_seg <= 4;
+  else
+    s.small = rows <= kTreeShortRows && (per_seg <= 1 || (many && per_seg <= 4));
+  s.direct = s.small || per_seg <= 6 || (s.units >= 100 && per_seg <= 10);
   return s;
 }
 
@@ -1165,6 +1185,7 @@ size_t tree_attn_workspace_bytes(int S, int Tn, int Hq, int Hkv, int D, int max_
 
 cudaError_t prepare_tree_attn() {
   cudaError_t e;
+  if ((e = prepare_tree_short()) != cudaSuccess) return e;
   if ((e = set_smem<64, true>()) != cudaSuccess) return e;
   if ((e = set_smem<64, false>()) != cudaSuccess) return e;
   if ((e = set_smem<128, true>()) != cudaSuccess) return e;
@@ -1175,6 +1196,7 @@ cudaError_t launch_tree_attn(const CUtensorMap& tmQ, const CUtensorMap& tmK, con
                              const TreeParams& p, void* workspace, int num_sms,
                              cudaStream_t stream) {
   const Shape s = shape_of(p.S, p.Tn, p.Hq, p.Hkv, p.max_seq_len);
+  if (s.small) return launch_tree_short(tmK, tmV, p, stream);
   const Layout l = layout_of(s, p.D);
   char* ws = static_cast<char*>(workspace);
   Work w{};
