@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kThreads) paged_kv_keep_kernel(const __grid_co
   const int32_t* path = p.path + static_cast<size_t>(r) * p.path_len;
   const int at = mine ? path[j] : 0;
   const int before = mine && j > 0 ? path[j - 1] : -1;
-  const bool increases = !mine || at > before;
+  const bool increases = !mine || (at > before && at >= j);
   const bool fits = sizes_ok && static_cast<long long>(L) + (mine ? at : 0) <
                                     static_cast<long long>(p.max_blocks) * kPagedBlock + (mine ? 0 : 1);
   const bool bad_path = __syncthreads_or(!increases);

@@ -222,6 +222,10 @@ struct Walk {
     x.kvh = s / w.rounds;
     const int round = s - x.kvh * w.rounds;
     const int steps = steps_of(w, z, round), cost = step_cost(w, z, round);
+    if (j >= steps) {  // (lengths changed under the kernel)
+      at = hi;
+      return false;
+    }
     const int n = w.direct ? steps : min((hi - at + cost - 1) / cost, steps - j);
     const int tiles = live_tiles(w, z);
     x.r = r;
@@ -269,8 +273,10 @@ __device__ void planner_warp(const Work& w, const Plan& plan, uint8_t* smem, con
   for (int i = 0;; ++i) {
     const bool more = walk.next(x);
     if (!more) x.n = -1;
-    if (!mbar_wait(bar.piece_empty(i % kPieces), ((i / kPieces) & 1) ^ 1, abort, p.flags, p.wait_limit_ns))
-      return;
+    if (!mbar_wait(bar.piece_empty(i % kPieces), ((i / kPieces) & 1) ^ 1, abort, p.flags, p.wait_limit_ns)) {
+      cut.pieces = 0;  // (what there is need not have been computed)
+      break;
+    }
     pieces[i % kPieces] = x;
     mbar_arrive(bar.piece_full(i % kPieces));
     if (!more) break;
@@ -279,7 +285,9 @@ __device__ void planner_warp(const Work& w, const Plan& plan, uint8_t* smem, con
       // the rows go on up to the range that holds the segment's last step
       const int e = walk.end - step_cost(w, walk.z, x.pair / w.team), big = plan.extra * (plan.share + 1);
       const int k1 = e < big ? e / (plan.share + 1) : plan.extra + (e - big) / plan.share;
-      cut = Cut{x.r, x.kvh, x.pair, x.row_tiles, k1 - walk.team + 1, x.slot};
+      // (within the launch, should the lengths have changed under the kernel)
+      const int pieces = min(k1, static_cast<int>(gridDim.x) / w.team - 1) - walk.team + 1;
+      cut = Cut{x.r, x.kvh, x.pair, x.row_tiles, pieces, x.slot};
     }
   }
   if (!w.direct) w.cut[blockIdx.x] = cut;
@@ -1025,7 +1033,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
   const Cut cut = w.cut[blockIdx.x];
   const int node = (2 * cut.pair + tile) * w.tile_nodes + tile_node;
   // (a row tile without nodes has been written already)
-  if (cut.pieces == 0 || part >= PARTS || unit_row >= w.unit_rows || tile >= cut.tiles ||
+  if (cut.pieces <= 0 || part >= PARTS || unit_row >= w.unit_rows || tile >= cut.tiles ||
       tile_node >= w.tile_nodes || node >= w.p.Tn)
     return;
   float m = -INFINITY, sum = 0.f, o[8];
