@@ -241,8 +241,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
   __shared__ u64 part[kWarps];
   __shared__ int nodes;
   __shared__ Step step;
-  __shared__ u64 gone[DRAWN ? 1 : kMaxNodes];  // without a draft: the tokens that have fallen at
-  __shared__ u64 gone_w[DRAWN ? 1 : kMaxNodes];  // the node, and what they have in the sums
+  __shared__ int gone[DRAWN ? 1 : kMaxNodes];  // without a draft: tokens that have fallen at the node
   const int ctas = cluster_size(), rank = cluster_rank();
   const int r = blockIdx.x / ctas;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -298,26 +297,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
   Step now{kDone, 0, 0};
   float2 A2 = make_float2(0.f, 0.f);
   const int c0 = rank * p.chunk, c1 = min(p.V, c0 + p.chunk);  // (chunk * ctas < 2^31)
-  auto all_sum = [&]() {  // over the row, less what has fallen; by a whole warp
-    u64 v = lane < ctas ? totals[buffer ^ 1][lane] : 0;
-    if (!DRAWN)
-      for (int i = lane; i < fallen; i += 32) v -= gone_w[i];  // (modulo 2^64)
-    return warp_sum(v);
+  u64 all = 0;          // the sum over the row as it is now
+  auto fallen_already = [&](int x) {
+    bool hit = false;
+    for (int i = lane; i < fallen; i += 32) hit |= gone[i] == x;
+    return __any_sync(0xffffffffu, hit) != 0;
   };
 
   for (;;) {
     if (warp == 0) {
       Step next{kDone, cur, 0};
       bool again = waiting == kFalls;  // child `at` is known to fall
-      if (waiting == kAfterFall) {
-        const u64 all = all_sum();
-        summed = all > 0;
-        if (summed) {
+      if (waiting != kNothing) {
+        all = warp_sum(lane < ctas ? totals[buffer ^ 1][lane] : 0);
+        summed = waiting != kAfterFall || all > 0;
+        if (waiting == kAfterFall && all > 0) {
           A += W >> kToUnit;
           W = all;
         }
-      } else if (waiting != kNothing) {
-        summed = true;
       }
       waiting = kNothing;
       while (n > 0) {
@@ -336,14 +333,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
             break;
           }
           at = found;
-          u64 w = left(pv[at], qv[at], A);
-          if (!DRAWN) {
-            bool hit = false;
-            for (int i = lane; i < fallen; i += 32) hit |= gone[i] == static_cast<u64>(token[at]);
-            w = __any_sync(0xffffffffu, hit) ? 0 : fixed(pv[at]);
+          u64 w;
+          if (DRAWN) {
+            w = left(pv[at], qv[at], A);
+          } else {
+            w = fallen_already(token[at]) ? 0 : fixed(pv[at]);
           }
-          if (product_below(chance[at], product(qv[at], W), w)) {
-            __syncwarp();
+          if (product_below(chance[at], DRAWN ? product(qv[at], W) : W, w)) {
             if (lane == 0) path[count] = at;
             ++count;
             cur = next.node = at;
@@ -366,18 +362,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
           waiting = kFalls;
           break;
         }
-        // without a draft it is the token itself that falls, with what it has in the sums
-        const u64 x = static_cast<u64>(token[at]);
-        bool hit = false;
-        for (int i = lane; i < fallen; i += 32) hit |= gone[i] == x;
-        const u64 w = __any_sync(0xffffffffu, hit) ? 0 : left_rounded(pv[at], 0.f, A2, false);
-        const u64 all = all_sum();
+        // without a draft it is the token itself that falls: it leaves the sums
+        const int x = token[at];
+        const u64 w = fallen_already(x) ? 0 : left_rounded(pv[at], 0.f, A2, false);
         if (all > w) {
-          W = all - w;
+          all -= w;
+          W = all;
           if (w > 0) {
             if (lane == 0) {
               gone[fallen] = x;
-              gone_w[fallen] = w;
+              const int c = x / p.chunk;
+              totals[buffer ^ 1][c] -= w;
+              if (c == rank) sums[(x - c0) / p.tile] -= w;
             }
             ++fallen;
             __syncwarp();
@@ -385,7 +381,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
         }
       }
       if (next.op == kDraw) {
-        const u64 all = all_sum();
         next.A = share_of(chance[0], all);
         if (all == 0) {
           next.op = kDone;
@@ -441,9 +436,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
   if (last.op != kDraw) return;
   // the CTA whose tokens the running sum passes the drawn place in
   const int n_gone = DRAWN ? 0 : fallen;
-  u64 own = lane < ctas ? totals[buffer ^ 1][lane] : 0;
-  for (int i = 0; i < n_gone; ++i)
-    if (static_cast<int>(gone[i]) / p.chunk == lane) own -= gone_w[i];
+  const u64 own = lane < ctas ? totals[buffer ^ 1][lane] : 0;
   const u64 upto = warp_prefix(own);
   const u64 begin = __shfl_sync(0xffffffffu, upto - own, rank);
   const u64 stop = __shfl_sync(0xffffffffu, upto, rank);
@@ -453,11 +446,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
   const int tiles = (c1 - c0 + p.tile - 1) / p.tile;
   int t = -1;
   for (int b = 0; b < tiles && t < 0; b += 32) {
-    u64 s = b + lane < tiles ? sums[b + lane] : 0;
-    for (int i = 0; i < n_gone; ++i) {
-      const int x = static_cast<int>(gone[i]) - c0;
-      if (x >= 0 && x < p.chunk && x / p.tile == b + lane) s -= gone_w[i];
-    }
+    const u64 s = b + lane < tiles ? sums[b + lane] : 0;
     const u64 incl = warp_prefix(s);
     const unsigned hit = __ballot_sync(0xffffffffu, rest < incl);
     if (hit) {
@@ -473,16 +462,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
   const bool subtract = DRAWN && now.A != 0;
   const int end = min(c1, c0 + (t + 1) * p.tile);
   for (int b = c0 + t * p.tile; t >= 0 && b < end; b += kSpan) {
-    u64 w[kPerLane], sum = 0;
     const int i0 = b + kPerLane * lane;
+    unsigned out = 0;  // values that have fallen
+    for (int i = 0; i < n_gone; ++i) {
+      const unsigned x = static_cast<unsigned>(gone[i] - i0);
+      if (x < kPerLane) out |= 1u << x;
+    }
+    u64 w[kPerLane], sum = 0;
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
       w[k] = 0;
-      if (i0 + k < end) {
+      if (i0 + k < end && !(out >> k & 1u))
         w[k] = left_rounded(value(pr[i0 + k]), subtract ? value(qr[i0 + k]) : 0.f, A2, subtract);
-        for (int i = 0; i < n_gone; ++i)
-          if (gone[i] == static_cast<u64>(i0 + k)) w[k] = 0;
-      }
       sum += w[k];
     }
     const u64 incl = warp_prefix(sum);
@@ -490,12 +481,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
     if (hit) {
       if (lane == __ffs(hit) - 1) {
         u64 s = incl - sum;
-        int x = i0 + kPerLane - 1;
+        int x = i0;
 #pragma unroll
-        for (int k = 0; k < kPerLane; ++k) {
-          const bool before = s <= rest;
+        for (int k = 0; k < kPerLane; ++k) {  // (as many values as leave the sum at `rest` or below)
           s += w[k];
-          if (before && s > rest) x = i0 + k;
+          if (s <= rest) x = i0 + k + 1;
         }
         p.tokens_out[row + count - 1] = x;
       }

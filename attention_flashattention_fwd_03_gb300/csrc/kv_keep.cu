@@ -22,7 +22,7 @@ namespace gbattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 8;  // rows a lane reads before it stores them
+constexpr int kAhead = 4;  // rows a lane reads before it stores them
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) paged_kv_keep_kernel(const __grid_constant__ KeepParams p) {
@@ -98,8 +98,8 @@ cudaError_t launch_kv_keep(const KeepParams& p, int D, int num_sms, cudaStream_t
   if (p.S <= 0 || p.layers <= 0) return cudaSuccess;
   const int per_cta = kThreads / (D / 8);
   const long long sets = (2ll * p.layers * p.Hkv + per_cta - 1) / per_cta;
-  // some four CTAs an SM in all
-  const long long want = (4ll * num_sms + p.S - 1) / p.S;
+  // some 16 CTAs an SM in all
+  const long long want = (16ll * num_sms + p.S - 1) / p.S;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
