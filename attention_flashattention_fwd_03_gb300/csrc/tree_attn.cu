@@ -1017,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // LSE = M + ln sum_j e^{LSE_j - M}, O = sum_j e^{LSE_j - LSE} O_j over the pieces of a cut
 // segment: a thread 8 channels of a row, the lanes of a warp neighbouring rows, N pieces in
 // flight.
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 128;
 template <int D, int N>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ Work w) {
   constexpr int PARTS = D / 8;

@@ -523,13 +523,13 @@ int paged_attn_tree(const void *q, const void *k_pool, const void *v_pool,
  * search goes on from there.  If it falls, w becomes max(w - W q, 0) and W its sum, unless
  * that is 0, in which case both stay.  Where no child stands, the last token is the first x
  * whose w(0) + .. + w(x) is above u_0 times the sum of w (-1 and flag bit 32 if the sum is
- * 0).  Probabilities and random numbers are taken to [0, 1] (NaN as 0) and held as multiples
- * of 2^-62, so sums do not depend on an order; a row may sum to anything below 4.  Tokens
- * outside [0, V) have probability 0.
+ * 0).  Probabilities and random numbers are taken to [0, 1] (NaN as 0).  Tests take them as
+ * multiples of 2^-62, sums over w as multiples of 2^-44, so that sums do not depend on an
+ * order; a row may sum to anything below 4.  Tokens outside [0, V) have probability 0.
  *
  * A request without nodes gets count 0.  Device-side checks: a number of nodes outside
  * [0, Tn] (flag bit 2) or a parent outside [-1, i) (flag bit 16) gives count 0 as well.
- * Tn is at most GBATTN_TREE_MAX_NODES; strides are non-negative.
+ * Tn is at most GBATTN_TREE_MAX_NODES, V below 2^30; strides are non-negative.
  */
 int draft_verify(const void *target_probs, const void *draft_probs, const int64_t *target_strides,
                  const int64_t *draft_strides, int prob_type, const int32_t *tokens,

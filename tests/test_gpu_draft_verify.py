@@ -94,7 +94,10 @@ def softmax_rows(rng, S, Tn, V, bf16=False):
 @pytest.mark.parametrize("S,Tn,V,kind", [(1, 8, 32000, "chain"), (3, 16, 50257, "random"),
                                          (9, 5, 511, "chain"), (4, 4, 4097, "star"),
                                          (2, 6, 131072, "binary"), (40, 7, 1000, "binary"),
-                                         (1, 3, 300001, "chain"), (1, 256, 100, "random")])
+                                         (1, 3, 300001, "chain"), (1, 256, 100, "random"),
+                                         # fewer CTAs a request, down to one
+                                         (100, 3, 20000, "star"), (300, 3, 9001, "binary"),
+                                         (700, 4, 4099, "star")])
 def test_large_vocabularies(gb, drawn, S, Tn, V, kind):
     rng = np.random.default_rng(V + Tn)
     p, q = softmax_rows(rng, S, Tn, V)

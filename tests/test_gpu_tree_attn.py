@@ -54,6 +54,12 @@ CASES = [
     (3, 3, 128, 130, [0, 126, 254, 1000], "star", [130, 129, 128, 127]),
     (4, 2, 128, 100, [2000, 28, 0, 29], "random", [0, 100, 0, 99]),
     (8, 4, 128, 33, [31, 95, 96, 4000], "binary", None),
+    (128, 1, 64, 3, [70, 0, 2000], "random", [3, 0, 2]),            # a row tile a node
+    (100, 1, 128, 20, [1500, 3], "random", [20, 7]),                # two rounds of teams
+    (16, 16, 128, 1, [50, 700, 1], "chain", None),
+    (6, 2, 128, 5, [700, 0, 64, 63], "comb", None),                 # 15 rows
+    (8, 1, 64, 8, [1, 55, 56, 57, 120], "star", [8, 8, 8, 8, 8]),   # 64 rows
+    (8, 2, 128, 8, [0, 60, 500, 330], "random", [8, 0, 5, 1]),      # 32 rows
 ]
 
 

@@ -31,6 +31,7 @@ def attend(lib, q=A16, k=A16, v=A16, bt=A16, sl=A16, pa=A16, tl=None, bs=16, S=4
 
 @pytest.mark.parametrize("kw,code", [
     (dict(bs=8), UNSUPPORTED), (dict(D=80), UNSUPPORTED), (dict(Tn=257), UNSUPPORTED),
+    (dict(Hq=258, Hkv=2), UNSUPPORTED),  # 129 query heads on a KV head
     (dict(Hq=12, Hkv=5), INVALID), (dict(Hkv=0), INVALID), (dict(S=-1), INVALID),
     (dict(Tn=-1), INVALID), (dict(mb=0), INVALID), (dict(nb=0), INVALID), (dict(msl=-1), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
@@ -54,6 +55,7 @@ def test_attention_workspace(lib):
     size = lib.paged_attn_tree_workspace_size
     assert size(-1, 8, 12, 2, 128, 8192) == 0 and size(4, 0, 12, 2, 128, 8192) == 0
     assert size(4, 257, 12, 2, 128, 8192) == 0 and size(4, 8, 12, 5, 128, 8192) == 0
+    assert size(4, 8, 258, 2, 128, 8192) == 0
     assert size(4, 8, 12, 2, 96, 8192) == 0 and size(1 << 30, 256, 64, 2, 128, 2 ** 31 - 1) == 0
     for S, Tn, Hq, Hkv, D, msl in [(1, 1, 1, 1, 64, 1), (64, 8, 12, 2, 128, 8200), (3, 256, 64, 4, 64, 5000),
                                    (1, 4, 8, 8, 128, 2 ** 31 - 1), (5000, 2, 2, 1, 64, 70000)]:
