@@ -9,7 +9,9 @@
 //
 // Pure data movement, 4 D bytes a row read and as many written.  A CTA translates the rows
 // of a request through the block table once and moves them for some of the request's
-// (layer, K or V, KV head) items.
+// (layer, K or V, KV head) items.  The time is that of a chain of five round trips (lengths, path,
+// table, row in, row out): one layer of 4 requests 3.2 us, 32 layers of 64 requests (13 MB, 2 us at
+// the copy rate) 6.4, with 8 rows ahead 7.2 (fewer warps fit), with 4 CTAs an SM 9.4.
 #include <cuda_runtime.h>
 
 #include "gbattn.h"

@@ -30,6 +30,18 @@
 // With one row tile the two chains take every other key tile, each with its own maximum, sum
 // and output, and are joined when the piece ends; with two they take a row tile each over the
 // same keys.
+//
+// What bounds it.  A step is 64 KB (D 128) and, at the copy rate, 1.5 us of an SM's share of HBM;
+// with one row tile its products and softmax take 0.5 us, so that HBM bounds it: 64 requests of
+// 512 to 8192 tokens x 8 nodes, 12/2 heads (286 MB) take 57.5 us, 73 % of the copy rate, of
+// which some 50 stream; one of 131000 tokens x 32 nodes, 32/8 heads (537 MB) 97 us, 82 %.  With two
+// row tiles a step takes 1.7 us, the pace of attn_fwd.cu (softmax chain and the issue of the
+// products): 8 requests x 200 nodes, 32/4 heads (252 GFLOP) 219 us.  What comes on top: some 5 us
+// until the first tile is there (plan, table entry, copy, each a round trip, and code that
+// is run for the first time), 2 for the last tile and its output, 3 to 10 for the merge.
+//
+// The probabilities are rounded to bf16 before they multiply V, as in attn_fwd.cu; everything
+// else, partial outputs among it, is fp32.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -53,6 +65,7 @@ constexpr int kThreads = 384;
 constexpr int kMaxNodes = GBATTN_TREE_MAX_NODES;
 constexpr float kRescaleLog2 = 8.f;  // move the running max only if it grows by > 2^8
 constexpr int kMaxTeam = 8;
+// (each role walking by itself: 61.9 us instead of 58.3 on 64 requests x 8 nodes)
 constexpr int kPieces = 4;           // pieces told ahead
 constexpr int kRoles = 11;           // warps that are told
 // (the block launches with 168 registers a thread)
@@ -60,8 +73,10 @@ constexpr int kRegsLaunch = 168, kRegsWg0 = 104, kRegsSoftmax = 200;
 static_assert(kRegsWg0 + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split exceeds the launch");
 constexpr float kNan = __builtin_nanf("");
 
-// The steps lie on a line: a segment begins with kSegCost, then its steps follow one another at
-// the distance of what one costs.  A range takes the steps that lie in it.
+// The steps lie on a line: a segment begins with kSegCost (queries to be fetched, an output to be
+// written), then its steps follow one another at the distance of what one costs.  A range takes
+// the steps that lie in it.  With kSegCost 10 / 20 / 32, 64 requests x 8 nodes take 58.1 / 57.6 /
+// 58.7 us, 16 x up to 64 nodes 69.3 / 66.4 / 66.8; with kStepCost2 24 the latter 71.3.
 constexpr int kSegCost = 20;
 constexpr int kStepCost0 = 4, kStepCost1 = 16, kStepCost2 = 20;  // by row tiles (0: zeros are written)
 constexpr int kMostCost = kSegCost + kStepCost2;  // no range is shorter, so that each holds a step
@@ -118,6 +133,7 @@ struct Cfg {
   static constexpr int BOX_BYTES = BM * 128;
   static constexpr int TILE_BYTES = BM * D * 2;
   static constexpr int NQ = SPLIT ? 1 : 2;       // row tiles
+  // (4 slots: 64 requests x 8 nodes 59.8 us instead of 58.0, 131000 tokens 101 instead of 97.4)
   static constexpr int NSLOT = D == 64 ? 8 : 5;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_RING = NQ * TILE_BYTES;
@@ -296,7 +312,7 @@ __device__ void planner_warp(const Work& w, const Plan& plan, uint8_t* smem, con
 // A field of a piece, by the piece's shared-memory address; the whole warp calls this together.
 // All lanes read the same: the shuffle
 // tells the compiler so, which then keeps loops over it and what the products are issued with in
-// uniform registers (200 nodes: 241 us without).
+// uniform registers (8 requests x 200 nodes: 234 us, 242 with plain reads).
 __device__ __forceinline__ int field_at(uint32_t x, uint32_t offset) {
   int v;
   asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(x + offset) : "memory");
@@ -338,7 +354,8 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
   const uint32_t sQ = sbase + C::OFF_Q, sR = sbase + C::OFF_RING;
   const unsigned long long lim = p.wait_limit_ns;
   const uint64_t stream_policy = l2_policy_evict_first();
-  const bool once = w.team == 1 && w.rounds == 1;  // every K/V byte is read once
+  // every K/V byte is read once, and may go first (58.0 us; kept like the rest 59.6)
+  const bool once = w.team == 1 && w.rounds == 1;
   int rc = 0, uc = 0;
   bool ok = true, last_q_issued = false;
   Feed<D, SPLIT> feed(bar);
@@ -729,7 +746,8 @@ __device__ void softmax_wg(const Work& w, uint8_t* smem, uint32_t tmem,
         }
         const float ms = (m == -INFINITY) ? 0.f : m * sl2;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // (one copy of this code for all tiles: the roles share one instruction cache)
+        // (one copy of this code for all tiles, as the roles share one instruction cache: with one
+        // for masked tiles beside it, 200 nodes take 234 us instead of 219)
         write_p<false>(s, sl2, ms, lane_base + C::p_col(I), sum);
         l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
         tmem_wait_st();
@@ -1016,7 +1034,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // LSE = M + ln sum_j e^{LSE_j - M}, O = sum_j e^{LSE_j - LSE} O_j over the pieces of a cut
 // segment: a thread 8 channels of a row, the lanes of a warp neighbouring rows, N pieces in
-// flight.
+// flight.  Bound by latencies: 3 us on 64 requests x 8 nodes (15 MB of partial outputs), 10 on 8 x
+// 200 nodes (39 MB).  A warp a row, its lanes side by side in the channels, with scattered stores
+// of the partial outputs: 13 us on the latter; 16 channels a thread no faster.
 constexpr int kMergeThreads = 128;
 template <int D, int N>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ Work w) {
