@@ -58,8 +58,9 @@ constexpr int kMaxNodes = GBATTN_TREE_MAX_NODES;
 static_assert(kThreads == kMaxNodes, "a thread a node");
 constexpr int kMaxCtas = 16;   // of a cluster
 // All CTAs of a call are on the GPU at once, if the requests are few enough, with as many a request
-// as that leaves.  128 x 5 drafts of 100003 tokens: 4 CTAs an SM 27.4 us (4 a request), 3 29.8, 5 (48
-// registers) 33.5; 8 a request, in two rounds, 32.4, 16 56.8.
+// as that leaves.  128 x 5 drafts of 100003 tokens: 4 CTAs an SM 27.8 us (4 a request), 3 29.8, 5 (48
+// registers) 33.5; 2 a request 31.4, 8 (in two rounds) 33.1, 16 53.5.  64 x 8 of 131072: 8 a request
+// 40.7, 4 53.6, 16 43.5.
 constexpr int kCtasPerSm = 4;
 constexpr int kPerLane = 16;   // values of each row that a lane reads at once
 constexpr int kSpan = 32 * kPerLane;
