@@ -448,18 +448,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
     if (lane == 0) p.counts[r] = count;
   }
   if (last.op != kDraw) return;
-  // the CTA whose tokens the running sum passes the drawn place in
+  // the CTA whose tokens the running sum passes the drawn place in (the first one writes that
+  // there is none, which sums past 64 bits can lead to)
   const int n_gone = DRAWN ? 0 : fallen;
   const u64 own = lane < ctas ? totals[buffer ^ 1][lane] : 0;
-  const u64 upto = warp_prefix(own);
-  const u64 begin = __shfl_sync(0xffffffffu, upto - own, rank);
-  const u64 stop = __shfl_sync(0xffffffffu, upto, rank);
-  if (last.A < begin || last.A >= stop) return;
-  u64 rest = last.A - begin;
+  const u64 upto = warp_prefix(own), before = upto - own;
+  const unsigned passes = __ballot_sync(0xffffffffu, last.A >= before && last.A < upto);
+  const uint32_t owner = passes ? __ffs(passes) - 1 : 0;
+  if (rank != owner) return;
+  u64 rest = last.A - __shfl_sync(0xffffffffu, before, owner);
   // its tile
   const int tiles = (c1 - c0 + p.tile - 1) / p.tile;
   int t = -1;
-  for (int b = 0; b < tiles && t < 0; b += 32) {
+  for (int b = 0; passes != 0 && b < tiles && t < 0; b += 32) {
     const u64 s = b + lane < tiles ? sums[b + lane] : 0;
     const u64 incl = warp_prefix(s);
     const unsigned hit = __ballot_sync(0xffffffffu, rest < incl);
@@ -506,6 +507,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
       return;
     }
     rest -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) {
+    p.tokens_out[row + count - 1] = -1;
+    raise_flag(p.flags, DEVFLAG_NO_MASS);
   }
 }
 

@@ -198,6 +198,32 @@ def test_a_remainder_without_mass_is_left_out(gb):
     check(run(gb, p, None, np.tile([0, 1, 1], (3, 1)), parents, np.tile([0.5, 1.0, 1.0], (3, 1))), want, 3)
 
 
+@pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_rows_that_are_no_distribution_leave_no_output_unwritten(gb, drawn, bf16):
+    """Scores in the place of probabilities: sums past 4 wrap, but every token is one of the V or -1."""
+    rng = np.random.default_rng(5)
+    for S, Tn, V in [(7, 4, 100003), (40, 3, 4999), (9, 5, 40), (3, 2, 7)]:
+        scores = [torch.from_numpy(rng.normal(0, s, (S, Tn, V)).astype(np.float32)).cuda() for s in (3, 9)]
+        scores[0][0] = 1.0
+        if bf16:
+            scores = [x.bfloat16() for x in scores]
+        parents = np.tile(np.arange(Tn) - 1, (S, 1))
+        tokens = rng.integers(0, V, (S, Tn))
+        for u in (0.0, 0.3, 0.999):
+            outs = [torch.full((S, Tn), 1 << 30, dtype=torch.int32, device="cuda") for _ in range(2)]
+            counts = torch.full((S,), 1 << 30, dtype=torch.int32, device="cuda")
+            gb.draft_verify(scores[0], scores[1] if drawn else None, to_dev_i32(tokens), to_dev_i32(parents),
+                            torch.full((S, Tn), u, device="cuda"), tokens_out=outs[0], path=outs[1],
+                            counts=counts)
+            out, path, counts = (t.cpu().numpy() for t in (*outs, counts))
+            assert (out >= -1).all() and (out < V).all()
+            assert (path >= -1).all() and (path < Tn).all()
+            assert (counts >= 1).all() and (counts <= Tn).all()
+    status, flags = gb.attn_device_status()
+    assert flags in (0, 32)
+
+
 def test_bad_trees_and_sizes_are_flagged(gb):
     rng = np.random.default_rng(11)
     p, q = softmax_rows(rng, 3, 4, 50)
