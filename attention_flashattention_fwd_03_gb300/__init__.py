@@ -992,7 +992,8 @@ def paged_attn_tree(q, k_pool, v_pool, block_table, seq_lens, parents, max_seq_l
     A node sees the cached tokens, its ancestors and itself.  ``tree_lens`` [S] int32 says
     how many of the Tn (at most 256) places hold nodes (None: all); the others come back as
     0 and -inf.  ``max_seq_len`` bounds seq_lens + tree_lens.  ``workspace`` (uint8 CUDA
-    tensor) is allocated here when not given.
+    tensor) is allocated here when not given.  Nothing is recorded for automatic
+    differentiation.
     """
     if _torch is None:
         _load_torch()
@@ -1154,7 +1155,8 @@ def paged_kv_keep(k_pool, v_pool, block_table, seq_lens, path, counts, new_seq_l
 
     The row at position seq_lens[r] + path[r,j] goes to seq_lens[r] + j for j < counts[r],
     keys and values, in every layer: k_pool/v_pool are bf16 pools [NB,Hkv,16,D], sequences of
-    such pools (one a layer), or all layers' pools in one tensor [layers,NB,Hkv,16,D].
+    such pools (one a layer), or all layers' pools in one tensor [layers,NB,Hkv,16,D]; they
+    must not share memory (layers that share a cache are given once).
     block_table [S,max_blocks] (shared by the layers), seq_lens [S] (lengths before those
     rows), path [S,n] (strictly increasing, n at most 256), counts [S], all int32.  With
     draft_verify's path and counts that leaves the accepted tokens in the cache.

@@ -2,8 +2,10 @@
 // (include/gbattn.h): argument checks and launches, under the rules of api.cu.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <new>
 
 #include "api.h"
 #include "gbattn.h"
@@ -24,13 +26,39 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   return x < y + b_bytes && y < x + a_bytes;
 }
 
+// Whether two of the pools share memory.  A model's pools, one after another in one tensor or
+// allocated in turn, are often in order: those need no copy.
+bool pools_overlap(void* const* k, void* const* v, int n, size_t bytes, bool* out_of_memory) {
+  auto apart = [&](uintptr_t a, uintptr_t b) { return a + bytes <= b; };
+  auto at = [](void* p) { return reinterpret_cast<uintptr_t>(p); };
+  auto ordered = [&](void* const* x) {
+    for (int i = 1; i < n; ++i)
+      if (!apart(at(x[i - 1]), at(x[i]))) return false;
+    return true;
+  };
+  if (ordered(k) && ordered(v) && (apart(at(k[n - 1]), at(v[0])) || apart(at(v[n - 1]), at(k[0]))))
+    return false;
+  uintptr_t small[256];
+  uintptr_t* all = 2ll * n <= 256 ? small : new (std::nothrow) uintptr_t[2 * static_cast<size_t>(n)];
+  *out_of_memory = all == nullptr;
+  if (!all) return false;
+  for (int i = 0; i < n; ++i) {
+    all[i] = at(k[i]);
+    all[n + i] = at(v[i]);
+  }
+  std::sort(all, all + 2 * static_cast<size_t>(n));
+  bool overlap = false;
+  for (size_t i = 1; i < 2 * static_cast<size_t>(n); ++i) overlap |= !apart(all[i - 1], all[i]);
+  if (all != small) delete[] all;
+  return overlap;
+}
+
 // Whether the kernels' 32-bit counts hold a call of these sizes: query rows, and steps of
-// 128 keys of every (request, KV head, two row tiles), 20 units each and 20 more a segment.
+// 128 keys of every segment, 20 units each and 20 more a segment.
 bool tree_fits(int S, int Tn, int Hq, int Hkv, int max_seq_len) {
   const unsigned __int128 rows = static_cast<unsigned __int128>(S) * Hq * Tn;
   const uint64_t tiles = (static_cast<uint64_t>(max_seq_len) + 127) / 128 + 1;
-  const int nodes = Tn > 0 ? tree_tile_nodes(Hq / Hkv, Tn) : 1;
-  const unsigned __int128 segs = static_cast<unsigned __int128>(S) * Hkv * ((Tn + nodes - 1) / nodes);
+  const unsigned __int128 segs = static_cast<unsigned __int128>(S) * Hkv * tree_rounds(Hq / Hkv, Tn);
   return rows < kMaxDim && segs * (tiles + 1) * 20 < kMaxDim;
 }
 
@@ -188,6 +216,10 @@ GBATTN_API int paged_kv_keep(void* const* k_pools, void* const* v_pools, int num
   if (static_cast<uint64_t>(num_pool_blocks) * Hkv * block_size >= kMaxDim ||
       static_cast<uint64_t>(max_blocks_per_seq) * block_size >= kMaxDim)
     return ATTN_ERR_UNSUPPORTED;
+  const size_t pool_bytes = static_cast<size_t>(num_pool_blocks) * Hkv * block_size * D * 2;
+  bool out_of_memory = false;
+  if (pools_overlap(k_pools, v_pools, num_layers, pool_bytes, &out_of_memory)) return ATTN_ERR_INVALID_ARG;
+  if (out_of_memory) return ATTN_ERR_UNSUPPORTED;
   const size_t S = static_cast<size_t>(num_seqs);
   if (new_seq_lens &&
       (overlap(new_seq_lens, S * 4, seq_lens, S * 4) || overlap(new_seq_lens, S * 4, counts, S * 4) ||

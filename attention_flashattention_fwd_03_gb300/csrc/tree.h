@@ -37,6 +37,8 @@ cudaError_t prepare_tree_attn();
 // of 64 channels x group heads x tree_tile_nodes(group, Tn) nodes x 1; tmK and tmV are the decode
 // kernels' 2-D maps over the pools (64 x 16 box); all with the 128-byte swizzle.
 int tree_tile_nodes(int group, int Tn);
+// Segments of a KV head: how often a team of CTAs turns to it.
+int tree_rounds(int group, int Tn);
 cudaError_t launch_tree_attn(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                              const TreeParams& p, void* workspace, int num_sms,
                              cudaStream_t stream);

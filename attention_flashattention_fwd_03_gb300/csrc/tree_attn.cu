@@ -1119,7 +1119,7 @@ Shape shape_of(int S, int Tn, int Hq, int Hkv, int max_seq_len) {
   s.tile_nodes = tree_tile_nodes(s.group, Tn);
   s.row_tiles = (Tn + s.tile_nodes - 1) / s.tile_nodes;
   s.pairs = (s.row_tiles + 1) / 2;
-  s.rounds = (s.pairs + kMaxTeam - 1) / kMaxTeam;
+  s.rounds = tree_rounds(s.group, Tn);
   s.team = (s.pairs + s.rounds - 1) / s.rounds;
   s.segs = Hkv * s.rounds;
   s.unit_rows = s.row_tiles == 1 ? s.tile_nodes * s.group : 2 * BM;
@@ -1206,6 +1206,11 @@ cudaError_t set_smem() {
 }  // namespace
 
 int tree_tile_nodes(int group, int Tn) { return std::min(BM / group, Tn); }
+int tree_rounds(int group, int Tn) {
+  if (Tn <= 0) return 0;
+  const int nodes = tree_tile_nodes(group, Tn), pairs = ((Tn + nodes - 1) / nodes + 1) / 2;
+  return (pairs + kMaxTeam - 1) / kMaxTeam;
+}
 
 size_t tree_attn_workspace_bytes(int S, int Tn, int Hq, int Hkv, int D, int max_seq_len) {
   return layout_of(shape_of(S, Tn, Hq, Hkv, max_seq_len), D).bytes;

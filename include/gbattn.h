@@ -477,7 +477,9 @@ size_t paged_attn_tree_workspace_size(int num_seqs, int Tn, int Hq, int Hkv, int
  * Node i sees the L_r cached tokens, its ancestors and itself.  Places past a tree's nodes
  * get O = 0 and LSE = -inf; what is cached for them is not read.  max_seq_len bounds every
  * L_r + tree_lens[r].  Tn is at most GBATTN_TREE_MAX_NODES, block_size 16, D 64 or 128, Hq /
- * Hkv <= 128.  The split of the work depends on the lengths
+ * Hkv <= 128; with s = the segments num_seqs * Hkv (times 2, 3, .. where the nodes' rows make
+ * more than 16, 32, .. tiles of 128), s * (max_seq_len / 128 + 3) * 20 has to stay below 2^31
+ * (ATTN_ERR_UNSUPPORTED otherwise).  The split of the work depends on the lengths
  * of the whole batch, never on the blocks' places: the same inputs give the same bits.
  *
  * Device-side checks: a length or a number of nodes outside its bounds, or L_r +
@@ -545,7 +547,7 @@ int draft_verify(const void *target_probs, const void *draft_probs, const int64_
  *
  *   k_pools, v_pools  HOST arrays of num_layers device pointers, each to a pool
  *                 [num_pool_blocks, Hkv, block_size, D] bf16 (changed in place); the pools
- *                 must not overlap
+ *                 must not overlap (ATTN_ERR_INVALID_ARG: rows would move twice)
  *   block_table   [num_seqs, max_blocks_per_seq] int32, shared by the layers
  *   seq_lens      [num_seqs] int32 (device): L_r, the tokens before those rows
  *   path          [num_seqs, path_len] int32: strictly increasing (entries past counts[r]

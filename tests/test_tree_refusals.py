@@ -96,8 +96,9 @@ def test_verify(lib, kw, code):
 def keep(lib, layers=2, k=None, v=None, bt=A16, sl=A16 + (1 << 16), path=A16 + (2 << 16),
          counts=A16 + (3 << 16), new=A16 + (4 << 16), bs=16, S=4, n=8, Hkv=2, D=128, mb=10, nb=100,
          null=False):
-    arr = lambda x: (ctypes.c_void_p * max(layers, 1))(*(x or [A16 + i * 4096 for i in range(max(layers, 1))]))  # noqa: E731
-    return lib.paged_kv_keep(None if null else arr(k), arr(v), layers, bt, sl, path, counts, new, bs,
+    arr = lambda x, at: (ctypes.c_void_p * max(layers, 1))(  # noqa: E731
+        *(x or [(at << 40) + (i << 20) for i in range(max(layers, 1))]))
+    return lib.paged_kv_keep(None if null else arr(k, 1), arr(v, 2), layers, bt, sl, path, counts, new, bs,
                              S, n, Hkv, D, mb, nb, None)
 
 
@@ -127,6 +128,36 @@ def test_valid_calls_without_a_device_are_errors(lib):
     assert verify(lib, Tn=0, p=None, tok=None, pa=None, u=None, out=None, path=None) == gb.ATTN_ERR_CUDA
     assert keep(lib) == gb.ATTN_ERR_CUDA and keep(lib, new=None) == gb.ATTN_ERR_CUDA
     assert keep(lib, n=0, path=None) == gb.ATTN_ERR_CUDA
+
+
+@NO_DEVICE
+def test_pools_that_share_memory(lib):
+    """A pool of nb 100, Hkv 2, D 128 has 819200 bytes."""
+    at, pool = 1 << 40, 819200
+    k, v = [at + i * pool for i in range(3)], [at + (3 + i) * pool for i in range(3)]
+    for x, y in ((k, v), (v, k), (k[::-1], v), (k, v[::-1]), (k[::2] + v[1:2], v[::2] + k[1:2])):
+        assert keep(lib, layers=3, k=x, v=y) == gb.ATTN_ERR_CUDA
+    paired = [at + 2 * i * pool for i in range(3)]
+    assert keep(lib, layers=3, k=paired, v=[x + pool for x in paired]) == gb.ATTN_ERR_CUDA
+    assert keep(lib, layers=1, k=k[:1], v=k[1:2]) == gb.ATTN_ERR_CUDA
+    many = [at + i * pool for i in range(600)]
+    assert keep(lib, layers=300, k=many[::2], v=many[1::2]) == gb.ATTN_ERR_CUDA
+    assert keep(lib, layers=300, k=many[::2], v=many[1::2][:-1] + many[:1]) == INVALID
+    for x, y in ((k, k), ([k[0], k[0], k[2]], v), (k, [v[0], v[1], v[0]]), (k, v[:2] + k[2:]),
+                 (k, [v[0] - 16, v[1], v[2]]), ([k[0], k[1], k[2] + 16], v),
+                 ([k[0], k[0] + pool - 16, k[2]], v)):
+        assert keep(lib, layers=3, k=x, v=y) == INVALID
+    assert keep(lib, layers=1, k=k[:1], v=k[:1]) == INVALID
+
+
+def test_long_bounds_on_many_requests(lib):
+    """What the counts hold: segments x (key tiles + 2) x 20 below 2^31."""
+    size = lib.paged_attn_tree_workspace_size
+    assert size(4000, 8, 32, 8, 128, 400000) > 0 and size(1000, 200, 64, 8, 128, 1 << 20) > 0
+    tiles = (2 ** 31 - 1) // (20 * 32000) - 2
+    assert size(4000, 8, 32, 8, 128, 128 * tiles) > 0
+    assert size(4000, 8, 32, 8, 128, 128 * tiles + 1) == 0
+    assert attend(lib, S=4000, Tn=8, Hq=32, Hkv=8, msl=128 * tiles + 1) == UNSUPPORTED
 
 
 # --------------------------------------------------------------------------- #
