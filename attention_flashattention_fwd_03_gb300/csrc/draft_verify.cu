@@ -33,11 +33,11 @@
 // The last token's CTA is found from the CTAs' sums, its tile from the tiles' sums, and only
 // that tile is read again.
 //
-// What bounds it.  One request (8 drafts, 32000 tokens) takes 8.2 us: 2 until the tree and its
+// What bounds it.  One request (8 drafts, 32000 tokens) takes 8.3 us: 2 until the tree and its
 // probabilities are there (two round trips), 1 for the walk, 1.2 for the sum, 1 for the barrier,
 // then the draw.  128 requests x 5 drafts of 100003 tokens (102 MB, each row pair summed once) take
-// 27 us, 55 % of the copy rate: the sums themselves 12, in which every request starts and ends
-// at about the same time.  64 x 8 drafts of 131072 tokens take 41 us, as long as the request with
+// 25.5 us, 59 % of the copy rate: the sums themselves 12, in which every request starts and ends
+// at about the same time.  64 x 8 drafts of 131072 tokens take 40 us, as long as the request with
 // the most children that fall: 7 us for the first sum of all, 6 for every further one of a few
 // (4 of them reading from L2, the loads of 8 warps an SM in flight).
 #include <cuda_runtime.h>
@@ -58,11 +58,13 @@ constexpr int kMaxNodes = GBATTN_TREE_MAX_NODES;
 static_assert(kThreads == kMaxNodes, "a thread a node");
 constexpr int kMaxCtas = 16;   // of a cluster
 // All CTAs of a call are on the GPU at once, if the requests are few enough, with as many a request
-// as that leaves.  128 x 5 drafts of 100003 tokens: 4 CTAs an SM 27.8 us (4 a request), 3 29.8, 5 (48
-// registers) 33.5; 2 a request 31.4, 8 (in two rounds) 33.1, 16 53.5.  64 x 8 of 131072: 8 a request
-// 40.7, 4 53.6, 16 43.5.
+// as that leaves.  128 x 5 drafts of 100003 tokens: 4 CTAs an SM 25.5 us (4 a request), 5 (48 registers)
+// 33.2; and, measured when the first of these took 27.8: 3 an SM 29.8, 2 a request 31.4, 8 (in two
+// rounds) 33.1, 16 53.5.  64 x 8 of 131072 then: 8 a request 40.7, 4 53.6, 16 43.5.
 constexpr int kCtasPerSm = 4;
-constexpr int kPerLane = 16;   // values of each row that a lane reads at once
+// Values of each row that a lane reads at once (8: 64 x 8 drafts 42.7 us instead of 39.8, one request
+// 7.8 instead of 8.3).
+constexpr int kPerLane = 16;
 constexpr int kSpan = 32 * kPerLane;
 constexpr int kMaxTiles = 256;
 
@@ -255,6 +257,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
   __shared__ u64 part[kWarps];
   __shared__ int nodes;
   __shared__ Step step;
+  // A and W of the walk, kept here as the sums need the registers (128 x 5 drafts 27.8 us -> 25.5)
+  __shared__ u64 walk[2];
   __shared__ int gone[DRAWN ? 1 : kMaxNodes];  // without a draft: tokens that have fallen at the node
   const int ctas = cluster_size(), rank = cluster_rank();
   const int r = blockIdx.x / ctas;
@@ -264,6 +268,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
 
   const T* p_rows = static_cast<const T*>(p.p) + r * p.p_stride[0];
   const T* q_rows = DRAWN ? static_cast<const T*>(p.q) + r * p.q_stride[0] : nullptr;
+  if (tid == 0) {
+    walk[0] = 0;
+    walk[1] = kOne;
+  }
   cluster_arrive();  // (shared memory of another CTA may be written once it has started)
   if (rank == 0) {
     const size_t row = static_cast<size_t>(r) * p.Tn;
@@ -304,14 +312,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
 
   // the walk (warp 0)
   int cur = 0, at = 0, fallen = 0, count = n > 0 ? 1 : 0;
-  u64 A = 0, W = kOne;
   enum { kNothing, kAfterFall, kFalls, kLast } waiting = kNothing;
   bool summed = false;  // the last sums are those of the present w
   int buffer = 0;       // of totals that the next sums go to
   Step now{kDone, 0, 0};
   float2 A2 = make_float2(0.f, 0.f);
   const int c0 = rank * p.chunk, c1 = min(p.V, c0 + p.chunk);  // (chunk * ctas < 2^31)
-  u64 all = 0;          // the sum over the row as it is now
   auto fallen_already = [&](int x) {
     bool hit = false;
     for (int i = lane; i < fallen; i += 32) hit |= gone[i] == x;
@@ -320,7 +326,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
 
   for (;;) {
     if (warp == 0) {
+      u64 A = walk[0], W = walk[1];
       Step next{kDone, cur, 0};
+      u64 all = 0;  // the sum over the row as it is now (once there is one)
       bool again = waiting == kFalls;  // child `at` is known to fall
       if (waiting != kNothing) {
         all = warp_sum(lane < ctas ? totals[buffer ^ 1][lane] : 0);
@@ -401,7 +409,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
           if (rank == 0 && lane == 0) raise_flag(p.flags, DEVFLAG_NO_MASS);
         }
       }
-      if (lane == 0) step = next;
+      __syncwarp();
+      if (lane == 0) {
+        step = next;
+        walk[0] = A;
+        walk[1] = W;
+      }
     }
     __syncthreads();
     if (step.op != kSum) break;
@@ -452,11 +465,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
   // there is none, which sums past 64 bits can lead to)
   const int n_gone = DRAWN ? 0 : fallen;
   const u64 own = lane < ctas ? totals[buffer ^ 1][lane] : 0;
-  const u64 upto = warp_prefix(own), before = upto - own;
-  const unsigned passes = __ballot_sync(0xffffffffu, last.A >= before && last.A < upto);
-  const uint32_t owner = passes ? __ffs(passes) - 1 : 0;
-  if (rank != owner) return;
-  u64 rest = last.A - __shfl_sync(0xffffffffu, before, owner);
+  const u64 upto = warp_prefix(own);
+  const unsigned passes = __ballot_sync(0xffffffffu, last.A - (upto - own) < own);
+  if (rank != max(__ffs(passes), 1) - 1) return;  // (1: CTA 0)
+  u64 rest = last.A - __shfl_sync(0xffffffffu, upto - own, rank);
   // its tile
   const int tiles = (c1 - c0 + p.tile - 1) / p.tile;
   int t = -1;
