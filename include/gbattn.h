@@ -530,6 +530,8 @@ int paged_attn_tree(const void *q, const void *k_pool, const void *v_pool,
  * order; a row may sum to anything below 4.  (Sums wrap from there on: the last token of such
  * a row is any of the V, or -1 with flag bit 32.)  Tokens outside [0, V) have probability 0.
  *
+ * tokens_out, path and counts may be tokens, parents and tree_lens.
+ *
  * A request without nodes gets count 0.  Device-side checks: a number of nodes outside
  * [0, Tn] (flag bit 2) or a parent outside [-1, i) (flag bit 16) gives count 0 as well.
  * Tn is at most GBATTN_TREE_MAX_NODES, V below 2^30; strides are non-negative.

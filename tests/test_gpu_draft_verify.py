@@ -280,6 +280,43 @@ def test_given_outputs_graph_and_stream(gb):
 
 
 @pytest.mark.parametrize("drawn", [True, False])
+def test_outputs_in_the_place_of_inputs(gb, drawn):
+    rng = np.random.default_rng(21)
+    S, Tn, V = 50, 9, 5003
+    p, q = softmax_rows(rng, S, Tn, V)
+    q = q if drawn else None
+    parents, tokens = inputs(rng, S, Tn, V, "random", p, q)
+    u = rng.random((S, Tn), dtype=np.float32)
+    nodes = rng.integers(0, Tn + 1, S)
+    want = run(gb, p, q, tokens, parents, u, nodes)
+    t, pa, n = to_dev_i32(tokens), to_dev_i32(parents), to_dev_i32(nodes)
+    got = gb.draft_verify(torch.from_numpy(p).cuda(), None if q is None else torch.from_numpy(q).cuda(), t, pa,
+                          torch.from_numpy(u).cuda(), tree_lens=n, tokens_out=t, path=pa, counts=n)
+    assert got[0] is t and got[1] is pa and got[2] is n
+    assert all((a.cpu().numpy() == b).all() for a, b in zip(got, want))
+
+
+def test_calls_on_two_streams_at_once(gb):
+    rng = np.random.default_rng(22)
+    sets, want = [], []
+    for S, Tn, V, kind, drawn in [(3, 8, 100003, "chain", True), (200, 5, 4001, "star", False),
+                                  (20, 12, 20000, "random", True)]:
+        p, q = softmax_rows(rng, S, Tn, V)
+        parents, tokens = inputs(rng, S, Tn, V, kind, p, q)
+        u = rng.random((S, Tn), dtype=np.float32)
+        want.append(run(gb, p, q if drawn else None, tokens, parents, u))
+        sets.append([torch.from_numpy(p).cuda(), torch.from_numpy(q).cuda() if drawn else None,
+                     to_dev_i32(tokens), to_dev_i32(parents), torch.from_numpy(u).cuda()])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[gb.draft_verify(*a, stream=s) for a in sets] for _ in range(5) for s in streams]
+    torch.cuda.synchronize()
+    for outs in got:
+        for g, w in zip(outs, want):
+            assert all((a.cpu().numpy() == b).all() for a, b in zip(g, w))
+
+
+@pytest.mark.parametrize("drawn", [True, False])
 def test_tokens_follow_the_target(gb, drawn):
     """Over many requests with numbers of their own, the first token put out is distributed as
     the target's row: 2^17 draws, each frequency within 5.5 standard deviations (a false alarm

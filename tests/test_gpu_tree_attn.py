@@ -265,3 +265,61 @@ def test_graph_replays_follow_the_lengths(gb):
         torch.cuda.synchronize()
         assert torch.equal(out, o_less) and torch.equal(out_lse, lse_less)
         lens.copy_(d.lens)
+
+
+# short caches, whole segments, segments cut between CTAs
+KINDS = [(8, 2, 128, 6, [0, 5, 40]), (16, 2, 64, 20, [0, 300, 500]), (12, 2, 128, 8, [3000, 20]),
+         (32, 2, 128, 33, [2500, 3, 900])]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,Tn,lens", KINDS)
+@pytest.mark.parametrize("scale", [1e-38, 1e-6, 1.0, 3.0])
+def test_softmax_scales(gb, Hq, Hkv, D, Tn, lens, scale):
+    c = ref.TreeInputs(Hq, Hkv, D, Tn, lens, "random", None, 83000)
+    c.scale = scale
+    o, lse = Dev(c).run(gb)
+    torch.cuda.synchronize()
+    ref.check_attention(from_dev(o), from_dev(lse), c.ref(), c.nodes, c.keys)
+
+
+def test_more_requests_than_threads(gb):
+    """Ranges of a batch of more requests than a CTA has threads, some without nodes."""
+    rng = np.random.default_rng(6)
+    lens, nodes = rng.integers(0, 1500, 900).tolist(), rng.integers(0, 4, 900).tolist()
+    c = ref.TreeInputs(2, 1, 64, 3, lens, "random", nodes, 84000, slack=3000)
+    o, lse = Dev(c).run(gb)
+    torch.cuda.synchronize()
+    assert gb.attn_device_status() == (gb.ATTN_OK, 0)
+    ref.check_attention(from_dev(o), from_dev(lse), c.ref(), c.nodes, c.keys)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,Tn,lens", KINDS)
+def test_the_loosest_bound_on_the_lengths(gb, Hq, Hkv, D, Tn, lens):
+    c = ref.TreeInputs(Hq, Hkv, D, Tn, lens[:1], "random", None, 85000)
+    o, lse = Dev(c).run(gb, max_seq_len=2 ** 31 - 1)
+    torch.cuda.synchronize()
+    assert gb.attn_device_status() == (gb.ATTN_OK, 0)
+    ref.check_attention(from_dev(o), from_dev(lse), c.ref(), c.nodes, c.keys)
+
+
+def test_calls_on_two_streams_and_a_graph_at_once(gb):
+    cs = [Dev(ref.TreeInputs(*k, "random", None, 86000 + i)) for i, k in enumerate(KINDS)]
+    want = [d.run(gb) for d in cs]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = [d.run(gb) for d in cs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        with torch.cuda.stream(streams[2]):
+            graph.replay()
+        for s in (0, 1):
+            for d in (cs, cs[::-1])[s]:
+                got[s].append(d.run(gb, stream=streams[s]))
+    torch.cuda.synchronize()
+    assert gb.attn_device_status() == (gb.ATTN_OK, 0)
+    n = len(cs)
+    for i, (o, lse) in enumerate(want):
+        for o2, lse2 in got[0][i::n] + got[1][n - 1 - i::n] + [captured[i]]:
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
