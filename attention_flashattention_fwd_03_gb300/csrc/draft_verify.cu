@@ -37,7 +37,7 @@
 // probabilities are there (two round trips), 1 for the walk, 1.2 for the sum, 1 for the barrier,
 // then the draw.  128 requests x 5 drafts of 100003 tokens (102 MB, each row pair summed once) take
 // 25.5 us, 59 % of the copy rate: the sums themselves 12, in which every request starts and ends
-// at about the same time.  64 x 8 drafts of 131072 tokens take 40 us, as long as the request with
+// at about the same time.  64 x 8 drafts of 131072 tokens take 39 us, as long as the request with
 // the most children that fall: 7 us for the first sum of all, 6 for every further one of a few
 // (4 of them reading from L2, the loads of 8 warps an SM in flight).
 #include <cuda_runtime.h>
@@ -162,11 +162,11 @@ struct Halves {
 };
 constexpr uint32_t kHiOffset = 0x40000000u, kLoOffset = 0x35400000u;  // 2, 1.5 x 2^-21
 __device__ __forceinline__ u64 whole(Halves h, uint32_t n) {  // of n values, as a multiple of 2^-62
-  const long long hi = h.hi - n * kHiOffset;                  // (below 2^31: n <= 256)
-  const int lo = static_cast<int>(h.lo - n * kLoOffset);
+  const long long hi = h.hi - n * kHiOffset;                  // (2^22 n at most: n below 1024)
+  const int lo = static_cast<int>(h.lo - n * kLoOffset);      // (1.75 x 2^21 n at most: n up to 512)
   return static_cast<u64>((hi << 22) + lo) << 18;
 }
-// Of d + e for a pair of values, |e| below 2^-23.
+// Of d + e for a pair of values, |e| at most 0.75 x 2^-23.
 __device__ __forceinline__ void halves(float2 d, float2 e, Halves& x, Halves& y) {
   const float2 t = __fadd2_rn(d, make_float2(2.f, 2.f));
   const float2 back = __fadd2_rn(t, make_float2(-2.f, -2.f));
@@ -176,7 +176,8 @@ __device__ __forceinline__ void halves(float2 d, float2 e, Halves& x, Halves& y)
   y = Halves{__float_as_uint(t.y), __float_as_uint(u.y)};
 }
 // Of max(p - A q, 0), A as the sum of two fp32 (hi, lo): A q = t + l with l = the product's
-// rounding error + lo q; where p > t, p - t is d + an error that is computed exactly.
+// rounding error + lo q; where p > t, p - t is d + an error that is computed exactly.  (There t < 1, so
+// |l| is 2^-25 + 2^-24 at most; the error of d is 0 for t >= p / 2, and else 2^-25, with l half as large.)
 template <bool FALLEN>
 __device__ __forceinline__ void left_halves(float2 p, float2 q, float2 A, Halves& x, Halves& y) {
   p = make_float2(__saturatef(p.x), __saturatef(p.y));
@@ -220,7 +221,7 @@ __device__ __forceinline__ void read_span(const T* row, int i, int end, bool all
   }
 }
 
-// This warp's part of the sums of a span of tokens.
+// The sum over a span of tokens, found by a warp together.
 template <typename T, bool FALLEN>
 __device__ __forceinline__ u64 span_sum(const T* pr, const T* qr, int b, int end, float2 A) {
   const int i = b + (threadIdx.x & 31);
@@ -237,7 +238,10 @@ __device__ __forceinline__ u64 span_sum(const T* pr, const T* qr, int b, int end
     s.hi += x.hi + y.hi;
     s.lo += x.lo + y.lo;
   }
-  return whole(s, kPerLane);
+  static_assert(kSpan <= 512, "sums of a span's values in 32 bits");
+  s.hi = __reduce_add_sync(0xffffffffu, s.hi);
+  s.lo = __reduce_add_sync(0xffffffffu, s.lo);
+  return whole(s, kSpan);
 }
 
 // What a walk decides: the sums of max(p - A q, 0) at a node, or the draw.
@@ -432,7 +436,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
       for (int b = c0 + t * p.tile; b < end; b += kSpan)
         sum += DRAWN && now.A != 0 ? span_sum<T, DRAWN>(pr, qr, b, end, A2)
                                    : span_sum<T, false>(pr, qr, b, end, A2);
-      sum = warp_sum(sum);
       if (lane == 0) sums[t] = sum;
       mine += sum;
     }
