@@ -105,6 +105,7 @@ struct Work {  // what the kernels share besides the caller's operands
   float* part_lse;  // [2 grid][unit_rows]
   Cut* cut;         // [grid]
   int group;        // query heads of a KV head
+  int per_group;    // 2^16 / group, rounded up: x per_group >> 16 = x / group for x < 128
   int tile_nodes;   // nodes of a row tile
   int pairs;        // pairs of row tiles of a KV head
   int team;         // CTAs of a team: pairs that are taken together
@@ -128,8 +129,9 @@ struct Piece {
 
 // A checked tree: the parent of each node + 1, and the first node of the chain of consecutive
 // numbers that ends with it.
+template <int N>
 struct Tree {
-  uint8_t parent1[kMaxNodes], start[kMaxNodes];
+  uint8_t parent1[N], start[N];
 };
 
 template <int D, bool SPLIT>
@@ -138,20 +140,26 @@ struct Cfg {
   static constexpr int BOX_BYTES = BM * 128;
   static constexpr int TILE_BYTES = BM * D * 2;
   static constexpr int NQ = SPLIT ? 1 : 2;       // row tiles
-  // (4 slots: 64 requests x 8 nodes 59.8 us instead of 58.0, 131000 tokens 101 instead of 97.4)
-  static constexpr int NSLOT = D == 64 ? 8 : 5;
+  // (D 128, one row tile: 5 slots 57.8 us on 64 requests x 8 nodes, 97.2 on 131000 tokens; 6 slots
+  // 57.4 and 96.4; 4 slots 2 and 4 us more than 5)
+  static constexpr int NSLOT = D == 64 ? 8 : (SPLIT ? 6 : 5);
+  using Nodes = Tree<SPLIT ? BM : kMaxNodes>;    // (in one row tile: 128 at most)
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_RING = NQ * TILE_BYTES;
   static constexpr int OFF_TREE = OFF_RING + NSLOT * TILE_BYTES;  // [2] Tree
-  static constexpr int OFF_JOIN = OFF_TREE + 2 * sizeof(Tree);    // SPLIT: [2][BM] float2, maximum and sum
+  static constexpr int OFF_JOIN = OFF_TREE + 2 * sizeof(Nodes);   // SPLIT: [2][BM] float2, maximum and sum
   static constexpr int OFF_BAR = OFF_JOIN + (SPLIT ? 2 * BM * 8 : 0);
   static constexpr int NBAR = 2 + 2 * NSLOT + 6 + 1 + 4 + 2 + 2 * kPieces;
-  static constexpr int OFF_PLAN = OFF_BAR + NBAR * 8;
-  static constexpr int OFF_SUMS = OFF_PLAN + sizeof(Plan) + 4;    // [12] ints
-  static constexpr int OFF_PIECES = OFF_SUMS + 48;                   // [kPieces]
-  static constexpr int OFF_PLACE = OFF_PIECES + kPieces * sizeof(Piece);  // [BM] uint16_t
-  static constexpr int OFF_MISC = (OFF_PLACE + BM * 2 + 15) & ~15;   // TMEM address, abort, bad tree [2]
-  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;            // + slack for 1024-byte alignment
+  static constexpr int OFF_PIECES = OFF_BAR + NBAR * 8;                   // [kPieces]
+  static constexpr int OFF_MISC = OFF_PIECES + kPieces * sizeof(Piece);   // TMEM address, abort, bad tree [2]
+  // the plan, and sums [12] for it, are over before the first join
+  static constexpr int OFF_PLAN = SPLIT ? OFF_JOIN : OFF_MISC + 16;
+  static constexpr int OFF_SUMS = OFF_PLAN + sizeof(Plan);
+  static constexpr int END = SPLIT ? OFF_MISC + 16 : OFF_SUMS + 48;
+  // Room to align to 1024 bytes by hand, unless there is none: the array is declared with that
+  // alignment, and the kernel checks it.
+  static constexpr int SLACK = END + 1024 <= 232448 ? 1024 : 0;
+  static constexpr int SMEM_BYTES = END + SLACK;
   static constexpr uint32_t TMEM_COLS = 512;
   // TMEM columns: S_0 [0,128), S_1 [128,256), O_0 and O_1 from 256 (D each).  P_i (bf16
   // pairs, 64 columns) overwrites the upper half of S_i.
@@ -283,7 +291,7 @@ struct Walk {
 // warp 3: tells the other roles what to do
 // ---------------------------------------------------------------------------
 template <int D, bool SPLIT>
-__device__ void planner_warp(const Work& w, const Plan& plan, uint8_t* smem, const Bars<D, SPLIT>& bar,
+__device__ void planner_warp(const Work& w, const Plan plan, uint8_t* smem, const Bars<D, SPLIT>& bar,
                              volatile int* abort) {  // (one lane)
   using C = Cfg<D, SPLIT>;
   const TreeParams& p = w.p;
@@ -446,7 +454,8 @@ __device__ void producer_warp(const CUtensorMap* tmQ, const CUtensorMap* tmK,
 // ---------------------------------------------------------------------------
 // warp 2: the trees
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ bool read_tree(const int32_t* parents, int n, Tree& tree) {
+template <int N>
+__device__ __forceinline__ bool read_tree(const int32_t* parents, int n, Tree<N>& tree) {
   const int lane = threadIdx.x & 31;
   bool bad = false;
   int before = 0;  // start of the chain that ends with the node before
@@ -486,7 +495,7 @@ __device__ void tree_warp(const Work& w, uint8_t* smem, const Bars<D, SPLIT>& ba
     const int b = mc & 1;
     if (!mbar_wait_warp(bar.tree_empty(b), ((mc >> 1) & 1) ^ 1, abort, p.flags, p.wait_limit_ns)) return;
     const bool bad = read_tree(p.parents + static_cast<size_t>(FIELD(x, r)) * p.Tn, FIELD(x, nodes),
-                               reinterpret_cast<Tree*>(smem + C::OFF_TREE)[b]);
+                               reinterpret_cast<typename C::Nodes*>(smem + C::OFF_TREE)[b]);
     if (lane == 0) {
       bad_tree[b] = bad;
       if (bad) raise_flag(p.flags, DEVFLAG_BAD_TREE);
@@ -635,7 +644,8 @@ struct MmaWarp {
 
 // What node a sees of the 32 keys from x on, x counted from node 0 (the keys before it are the
 // cached tokens); a becomes the first of its ancestors before those keys.
-__device__ __forceinline__ uint32_t seen_bits(const Tree& tree, int& a, int x) {
+template <int N>
+__device__ __forceinline__ uint32_t seen_bits(const Tree<N>& tree, int& a, int x) {
   uint32_t bits = x <= -32 ? 0xffffffffu : (x < 0 ? (1u << -x) - 1u : 0u);
   while (a >= max(x, 0)) {
     const int s = tree.start[a];  // s .. a are its own or its ancestors
@@ -675,11 +685,11 @@ __device__ void softmax_wg(const Work& w, uint8_t* smem, uint32_t tmem,
   };
   // node of the row tile and head of this thread's row
   auto place = [&]() {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(bar.base - C::OFF_BAR + C::OFF_PLACE + 2 * tile_row) : "memory");
-    return static_cast<int>(v);
+    // (rows behind the tile's nodes get a head that does not exist)
+    const int node = (tile_row * w.per_group) >> 16, head = tile_row - node * w.group;
+    return node < w.tile_nodes ? node | head << 8 : 255 | 255 << 8;
   };
-  const Tree* trees = reinterpret_cast<const Tree*>(smem + C::OFF_TREE);
+  const auto* trees = reinterpret_cast<const typename C::Nodes*>(smem + C::OFF_TREE);
   Feed<D, SPLIT> feed(bar);
   for (uint32_t x; (x = feed.next(p, abort)); feed.done()) {
     const int total = FIELD(x, n), L = FIELD(x, L);
@@ -960,6 +970,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the merge kernel (or what else follows as a programmatic dependent) waits for this
   // grid's results
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (sbase - raw > C::SLACK) {  // (the declaration asks for it)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x == 0) {
+      raise_flag(w.p.flags, DEVFLAG_TIMEOUT);
+      if (!w.direct) w.cut[blockIdx.x].pieces = 0;
+    }
+    return;
+  }
   if (threadIdx.x == 0) {
     mbar_init(bar.q_full(), 1);
     mbar_init(bar.q_empty(), 1);
@@ -983,12 +1001,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
-  }
-  if (threadIdx.x >= BM && threadIdx.x < 2 * BM) {
-    // rows behind the tile's nodes get a head that does not exist
-    const int row = threadIdx.x - BM, node = row / w.group;
-    reinterpret_cast<uint16_t*>(smem + C::OFF_PLACE)[row] = static_cast<uint16_t>(
-        node < w.tile_nodes ? node | (row - node * w.group) << 8 : 255 | 255 << 8);
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmQ);
@@ -1053,7 +1065,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
   const int unit = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);  // (row group, part)
   const int part = unit / row_groups, unit_row = (unit - part * row_groups) * 32 + (threadIdx.x & 31);
   const int tile = unit_row / BM, tile_row = unit_row - tile * BM;
-  const int tile_node = tile_row / w.group, head = tile_row - tile_node * w.group;
+  const int tile_node = (tile_row * w.per_group) >> 16, head = tile_row - tile_node * w.group;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Cut cut = w.cut[blockIdx.x];
   const int node = (2 * cut.pair + tile) * w.tile_nodes + tile_node;
@@ -1243,6 +1255,7 @@ cudaError_t launch_tree_attn(const CUtensorMap& tmQ, const CUtensorMap& tmK, con
   w.part_lse = reinterpret_cast<float*>(ws + l.off_lse);
   w.cut = reinterpret_cast<Cut*>(ws + l.off_cut);
   w.group = s.group;
+  w.per_group = (65536 + s.group - 1) / s.group;
   w.tile_nodes = s.tile_nodes;
   w.pairs = s.pairs;
   w.team = s.team;
