@@ -17,8 +17,9 @@
 // an order and must be finer than fp32: they are sums of integers, which are exact in any
 // order.  A test of a token takes probabilities as multiples of 2^-62 (an fp32 from 2^-38 up
 // exactly) and products in 128 bits.  Sums over a row take max(p - A q, 0), computed as the sum
-// of two fp32, rounded to a multiple of 2^-44 (roundings of 2^17 tokens add up to 1e-11 as they
-// go, 5e-9 at the very most): adding 2 to an fp32 below 1 and taking it off again rounds it to
+// of two fp32, rounded to a multiple of 2^-44 (off by 0.5 of that for A = 0 and else by less than
+// 0.88, see left_halves; 8e7 random tokens came to 0.67.  Roundings of 2^17 tokens add up to 1e-11
+// as they go, 7e-9 at the very most): adding 2 to an fp32 below 1 and taking it off again rounds it to
 // 2^-22, what is left over goes the same way to 2^-44, and the bits of the two sums are the
 // integers to be added up.  That is some 16 instructions a token, most of them on pairs.  (Integers
 // made by shifts take three times as many, and the first kernel, with the compiler's conversions
@@ -164,10 +165,10 @@ struct Halves {
 constexpr uint32_t kHiOffset = 0x40000000u, kLoOffset = 0x35400000u;  // 2, 1.5 x 2^-21
 __device__ __forceinline__ u64 whole(Halves h, uint32_t n) {  // of n values, as a multiple of 2^-62
   const long long hi = h.hi - n * kHiOffset;                  // (2^22 n at most: n below 1024)
-  const int lo = static_cast<int>(h.lo - n * kLoOffset);      // (1.75 x 2^21 n at most: n up to 512)
+  const int lo = static_cast<int>(h.lo - n * kLoOffset);      // (1.25 x 2^21 n at most: n up to 512)
   return static_cast<u64>((hi << 22) + lo) << 18;
 }
-// Of d + e for a pair of values, |e| at most 0.75 x 2^-23.
+// Of d + e for a pair of values, |e| at most 2^-25.
 __device__ __forceinline__ void halves(float2 d, float2 e, Halves& x, Halves& y) {
   const float2 t = __fadd2_rn(d, make_float2(2.f, 2.f));
   const float2 back = __fadd2_rn(t, make_float2(-2.f, -2.f));
@@ -177,8 +178,12 @@ __device__ __forceinline__ void halves(float2 d, float2 e, Halves& x, Halves& y)
   y = Halves{__float_as_uint(t.y), __float_as_uint(u.y)};
 }
 // Of max(p - A q, 0), A as the sum of two fp32 (hi, lo): A q = t + l with l = the product's
-// rounding error + lo q; where p > t, p - t is d + an error that is computed exactly.  (There t < 1, so
-// |l| is 2^-25 + 2^-24 at most; the error of d is 0 for t >= p / 2, and else 2^-25, with l half as large.)
+// rounding error + lo q, and p - t = d + an error that is computed exactly.  Whether something is
+// left, and what, is up to the sum s of d and e: where the product rounds to p or past it, d alone
+// is 0 or negative.  (s, d - s + e) is the same sum with a second part of 2^-25 at most, as s is 1 at
+// most.  Where s is positive t is below 1 + 2^-22, so that |l| is little more than 2^-23 at most, and
+// what is lost is 2^-48 of A q in A's two parts, 2^-47 in l and e, 2^-48 in the second part, and 2^-47
+// in halves before its rounding to 2^-44.
 template <bool FALLEN>
 __device__ __forceinline__ void left_halves(float2 p, float2 q, float2 A, Halves& x, Halves& y) {
   p = make_float2(__saturatef(p.x), __saturatef(p.y));
@@ -192,9 +197,10 @@ __device__ __forceinline__ void left_halves(float2 p, float2 q, float2 A, Halves
     const float2 d = __fadd2_rn(p, t);
     float2 e = __fadd2_rn(__fadd2_rn(__fadd2_rn(p, make_float2(-d.x, -d.y)), t), l);
     const float2 s = __fadd2_rn(d, e);
-    const bool x_left = fminf(d.x, s.x) > 0.f, y_left = fminf(d.y, s.y) > 0.f;
-    halves(make_float2(x_left ? d.x : 0.f, y_left ? d.y : 0.f),
-           make_float2(x_left ? e.x : 0.f, y_left ? e.y : 0.f), x, y);
+    const float2 rest = __fadd2_rn(__fadd2_rn(d, make_float2(-s.x, -s.y)), e);
+    const bool x_left = s.x > 0.f, y_left = s.y > 0.f;
+    halves(make_float2(x_left ? s.x : 0.f, y_left ? s.y : 0.f),
+           make_float2(x_left ? rest.x : 0.f, y_left ? rest.y : 0.f), x, y);
   }
 }
 // The same of one token.

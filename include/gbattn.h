@@ -526,9 +526,10 @@ int paged_attn_tree(const void *q, const void *k_pool, const void *v_pool,
  * that is 0, in which case both stay.  Where no child stands, the last token is the first x
  * whose w(0) + .. + w(x) is above u_0 times the sum of w (-1 and flag bit 32 if the sum is
  * 0).  Probabilities and random numbers are taken to [0, 1] (NaN as 0).  Tests take them as
- * multiples of 2^-62, sums over w as multiples of 2^-44, so that sums do not depend on an
- * order; a row may sum to anything below 4.  (Sums wrap from there on: the last token of such
- * a row is any of the V, or -1 with flag bit 32.)  Tokens outside [0, V) have probability 0.
+ * multiples of 2^-62, sums over w as multiples of 2^-44 (each value off by less than one of
+ * them), so that sums do not depend on an order; a row may sum to anything below 4.  (Sums wrap
+ * from there on: the last token of such a row is any of the V, or -1 with flag bit 32.)  Tokens
+ * outside [0, V) have probability 0.
  *
  * tokens_out, path and counts may be tokens, parents and tree_lens.
  *

@@ -1,0 +1,59 @@
+"""draft_verify where what a fall leaves of a token is small beside the token's probabilities,
+against the rule in rational numbers."""
+
+from __future__ import annotations
+
+from fractions import Fraction
+
+import numpy as np
+import pytest
+
+import tree_ref as ref
+from test_gpu_draft_verify import check, gb, run  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+def want_of(p, q, tokens, parents, u):
+    S, Tn, V = p.shape
+    return [ref.verify_exact(p[r].tolist(), None if q is None else q[r].tolist(), tokens[r], parents[r],
+                             np.asarray(u[r], dtype=np.float32).tolist(), Tn, V) for r in range(S)]
+
+
+def test_a_remainder_below_the_rounding_of_its_product(gb):
+    """Both children fall; what is left is 2.3e-8 on token 1 alone, where the product in fp32
+    rounds past p."""
+    p = np.tile(np.float32([float.fromhex("0x1.944ea0p-4"), float.fromhex("0x1.cd762cp-1"), 0]), (1, 3, 1))
+    q = np.tile(np.float32([float.fromhex("0x1.9442p-4"), float.fromhex("0x1.cd67cp-1"), 2.0 ** -13]), (1, 3, 1))
+    tokens, parents, u = np.array([[0, 2, 2]]), np.array([[-1, 0, 0]]), [[0.05, 0.5, 0.5]]
+    want = want_of(p, q, tokens, parents, u)
+    assert want == [([1], [0])]
+    check(run(gb, p, q, tokens, parents, u), want, 3)
+
+
+@pytest.mark.parametrize("S,V", [(500, 3), (40, 4099)])
+def test_remainders_next_to_nothing(gb, S, V):
+    """Rows that sum to 1 in steps of 2^-24, with p = q (1 + 2^-13) but for less than a step:
+    the first fall leaves W = 2^-13, the second rem and 1/4 - rem steps on two tokens, or one of
+    them on one token.  The kernel's sums are off by less than 2^-43 a token, 2^-17 of the 2^-26
+    that is left."""
+    rng = np.random.default_rng(V)
+    p, q = np.zeros((2, S, 3, V), dtype=np.float32)
+    tokens = np.zeros((S, 3), dtype=np.int64)
+    u = np.full((S, 3), 0.5)
+    for r in range(S):
+        x, y, z = rng.choice(V, 3, replace=False)
+        a = int(rng.integers(1 << 16, (1 << 24) - (1 << 16)))
+        up = a * (1 + 2.0 ** -13)  # (exact)
+        b = int(np.floor(up)) + int(rng.integers(0, 2))
+        rem = b - up
+        q[r, :, [x, y, z]] = np.array([[a], [(1 << 24) - a - (1 << 11)], [1 << 11]]) * 2.0 ** -24
+        p[r, :, [x, y]] = np.array([[b], [(1 << 24) - b]]) * 2.0 ** -24
+        tokens[r] = z
+        border = (rem if x < y else 0.25 - rem) / 0.25  # between the two tokens, if in (0, 1)
+        u[r, 0] = max((0.25, 0.5, 0.75), key=lambda v: abs(v - border))
+    parents = np.tile([-1, 0, 0], (S, 1))
+    assert all(Fraction(float(s)) == 1 for s in p[:, 0].astype(np.float64).sum(-1))
+    check(run(gb, p, q, tokens, parents, u), want_of(p, q, tokens, parents, u), 3)
