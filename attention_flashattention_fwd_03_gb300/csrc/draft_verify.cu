@@ -72,7 +72,7 @@ constexpr int kMaxTiles = 256;
 
 using u64 = unsigned long long;
 constexpr u64 kOne = 1ull << 62;   // 1 as a multiple of 2^-62 (probabilities, W)
-constexpr u64 kUnit = 1ull << 54;  // 1 as a multiple of 2^-54 (A, which may come to 256)
+constexpr u64 kUnit = 1ull << 54;  // 1 as a multiple of 2^-54 (A: 1 + 254 W below 4 at most, 1017)
 constexpr int kToUnit = 8;         // bits between the two
 
 // A probability (or random number) as a multiple of 2^-62; NaN and negative values are 0.
@@ -433,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
     // ---- sums of this CTA's tokens ----
     now = step;
     A2.x = __ull2float_rn(now.A) * 0x1p-54f;
-    A2.y = __ll2float_rn(static_cast<long long>(now.A) - __float2ll_rn(A2.x * 0x1p54f)) * 0x1p-54f;
+    // (both are below 2^64, and their difference is small)
+    A2.y = __ll2float_rn(static_cast<long long>(now.A - __float2ull_rn(A2.x * 0x1p54f))) * 0x1p-54f;
     const T* pr = p_rows + now.node * p.p_stride[1];
     const T* qr = DRAWN ? q_rows + now.node * p.q_stride[1] : nullptr;
     u64 mine = 0;

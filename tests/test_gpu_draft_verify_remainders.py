@@ -57,3 +57,27 @@ def test_remainders_next_to_nothing(gb, S, V):
     parents = np.tile([-1, 0, 0], (S, 1))
     assert all(Fraction(float(s)) == 1 for s in p[:, 0].astype(np.float64).sum(-1))
     check(run(gb, p, q, tokens, parents, u), want_of(p, q, tokens, parents, u), 3)
+
+
+@pytest.mark.parametrize("n", [130, 180, 256])
+def test_many_falls_over_rows_that_sum_to_almost_4(gb, n):
+    """What the siblings have taken off comes to A = 1 + 3.9 a fall or so, to 446, 595 and 799."""
+    S, V = 64, 5
+    p = np.tile(np.float32([1, 1, 1, 0.875, 0]), (S, n, 1))
+    q = np.tile(np.float32([2.0 ** -10, 2.0 ** -12, 2.0 ** -11, 0, 2.0 ** -20]), (S, n, 1))
+    tokens, parents = np.full((S, n), 4), np.tile([-1] + [0] * (n - 1), (S, 1))
+    u = np.full((S, n), 0.5)
+    u[:, 0] = (np.arange(S) + 0.5) / S
+    want = ref.verify_exact(p[0].tolist(), q[0].tolist(), tokens[0], parents[0], u[0].tolist(), n, V)
+    # (requests differ in the last draw alone: the falls are those of the first request)
+    w, W, A = [Fraction(float(x)) for x in p[0, 0]], Fraction(1), Fraction(0)
+    row = [Fraction(float(x)) for x in q[0, 0]]
+    for _ in range(n - 1):
+        A += W
+        w = [max(Fraction(float(a)) - A * b, Fraction(0)) for a, b in zip(p[0, 0], row)]
+        W = sum(w)
+    runs = np.cumsum([float(x) for x in w]) / float(W)
+    assert np.abs(runs[:, None] - u[:, 0]).min() > 2.0 ** -20  # no number next to a border
+    tokens_last = [int(np.searchsorted(runs, x, side="right")) for x in u[:, 0]]
+    assert tokens_last[0] == want[0][0] and (n < 180 or A > 512)
+    check(run(gb, p, q, tokens, parents, u), [([x], [0]) for x in tokens_last], n)
