@@ -395,18 +395,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
           waiting = kFalls;
           break;
         }
-        // without a draft it is the token itself that falls: it leaves the sums
+        // without a draft it is the token itself that falls: it leaves the sums, and is gone for
+        // the node's other children even where it is too small for the sums
         const int x = token[at];
-        const u64 w = fallen_already(x) ? 0 : left_rounded(pv[at], 0.f, A2, false);
+        const bool before = fallen_already(x);
+        const u64 w = before ? 0 : left_rounded(pv[at], 0.f, A2, false);
         if (all > w) {
           all -= w;
           W = all;
-          if (w > 0) {
+          if (!before && pv[at] > 0.f) {  // (x is one of the V)
             if (lane == 0) {
               gone[fallen] = x;
-              const int c = x / p.chunk;
-              totals[buffer ^ 1][c] -= w;
-              if (c == rank) sums[(x - c0) / p.tile] -= w;
+              if (w > 0) {
+                const int c = x / p.chunk;
+                totals[buffer ^ 1][c] -= w;
+                if (c == rank) sums[(x - c0) / p.tile] -= w;
+              }
             }
             ++fallen;
             __syncwarp();

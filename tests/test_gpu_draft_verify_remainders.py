@@ -81,3 +81,18 @@ def test_many_falls_over_rows_that_sum_to_almost_4(gb, n):
     tokens_last = [int(np.searchsorted(runs, x, side="right")) for x in u[:, 0]]
     assert tokens_last[0] == want[0][0] and (n < 180 or A > 512)
     check(run(gb, p, q, tokens, parents, u), [([x], [0]) for x in tokens_last], n)
+
+
+def test_a_token_that_fell_falls_again_however_small(gb):
+    """Without a draft: a token below the sums' step is gone all the same once it has fallen."""
+    S, V = 4, 6
+    tokens = np.array([[0, 1, 1], [0, 5, 5], [0, 3, 3], [0, 0, 0]])
+    parents = np.tile([-1, 0, 0], (S, 1))
+    p = np.zeros((S, 3, V), dtype=np.float32)
+    p[:3, :, 0], p[3, :, 1] = 1, 1
+    for r, small in enumerate((2.0 ** -50, 2.0 ** -46, 2.0 ** -60, 2.0 ** -49)):
+        p[r, :, tokens[r, 1]] = small
+    u = np.tile([0.5, 0.25, 0.0], (S, 1))
+    want = want_of(p, None, tokens, parents, u)
+    assert all(path == [0] for _, path in want)
+    check(run(gb, p, None, tokens, parents, u), want, 3)
