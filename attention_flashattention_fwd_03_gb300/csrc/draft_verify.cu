@@ -73,7 +73,7 @@ constexpr int kMaxTiles = 256;
 using u64 = unsigned long long;
 constexpr u64 kOne = 1ull << 62;   // 1 as a multiple of 2^-62 (probabilities, W)
 constexpr u64 kUnit = 1ull << 54;  // 1 as a multiple of 2^-54 (A: 1 + 254 W below 4 at most, 1017)
-constexpr int kToUnit = 8;         // bits between the two
+constexpr int kToUnit = 8;         // bits between the two (W and A are multiples of 2^-44: none is lost)
 
 // A probability (or random number) as a multiple of 2^-62; NaN and negative values are 0.
 // The significand goes to the top of 64 bits and down by the exponent (PTX shifts by 32 and
@@ -107,10 +107,15 @@ __device__ __forceinline__ bool product_below(u64 a, u64 b, u64 c) {
   const u64 hi = __umul64hi(a, b), lo = a * b;
   return hi < c >> 2 || (hi == c >> 2 && lo < c << 62);
 }
-// max(p - A q, 0) of one token.
+// max(p - A q, 0) of one token, A q rounded down to a multiple of 2^-62 (so that nothing is left
+// where A q is p or more).
 __device__ __forceinline__ u64 left(float p, float q, u64 A) {
-  const u64 w = fixed(p), off = product(q, A);
-  return off >= 2 * kUnit || off << kToUnit >= w ? 0 : w - (off << kToUnit);
+  if (product(q, A) >= 2 * kUnit) return 0;
+  const uint32_t bits = __float_as_uint(__saturatef(q));
+  const uint32_t m = (bits << 8) | 0x80000000u, e = bits >> 23;  // q = m 2^(e - 158)
+  const u64 w = fixed(p);
+  const u64 off = e < 55u ? 0 : static_cast<u64>((static_cast<unsigned __int128>(A) * m) >> (150u - e));
+  return off >= w ? 0 : w - off;
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {

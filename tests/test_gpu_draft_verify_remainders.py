@@ -96,3 +96,16 @@ def test_a_token_that_fell_falls_again_however_small(gb):
     want = want_of(p, None, tokens, parents, u)
     assert all(path == [0] for _, path in want)
     check(run(gb, p, None, tokens, parents, u), want, 3)
+
+
+@pytest.mark.parametrize("small", [2.0 ** -33, 2.0 ** -35, 2.0 ** -38])
+def test_a_child_of_nothing_falls(gb, small):
+    """p is below q by a step of 2^-56 and less at the fallen token: nothing is left there, and a
+    second child of it falls even for the number 0."""
+    step = small * 2.0 ** -23
+    p = np.tile(np.float32([small + step, 0.75, 0.25]), (1, 3, 1))
+    q = np.tile(np.float32([small + 2 * step, 0.25, 0.75]), (1, 3, 1))
+    tokens, parents, u = np.array([[0, 0, 0]]), np.array([[-1, 0, 0]]), [[0.5, 1 - 2.0 ** -24, 0.0]]
+    want = want_of(p, q, tokens, parents, u)
+    assert want == [([1], [0])]
+    check(run(gb, p, q, tokens, parents, u), want, 3)
