@@ -195,7 +195,8 @@ struct Bars {
 struct Sizes {
   int L, n;
   bool bad;
-  __device__ int tiles() const { return (L + n + BN - 1) / BN; }
+  // (unsigned: the keys may come to 2^31 - 16)
+  __device__ int tiles() const { return static_cast<int>((static_cast<unsigned>(L + n) + (BN - 1)) / BN); }
 };
 __device__ __forceinline__ Sizes sizes_of(const TreeParams& p, int r) {
   Sizes z{p.seq_lens[r], p.tree_lens ? p.tree_lens[r] : p.Tn, false};
@@ -266,7 +267,7 @@ struct Walk {
     x.n = x.row_tiles > 0 ? n : 0;
     x.last = j + n == steps;
     x.bad = z.bad;
-    x.tail = x.n > 0 && (j + n) * BN > z.L;
+    x.tail = x.n > 0 && z.L - (j + n - 1) * BN < BN;
     x.slot = j == 0 && x.last ? -1 : 2 * static_cast<int>(blockIdx.x) + (index > 0 ? 1 : 0);
     ++index;
     if (!w.direct) {
@@ -720,7 +721,7 @@ __device__ void softmax_wg(const Work& w, uint8_t* smem, uint32_t tmem,
 #pragma unroll
             for (int e = 0; e < 32; ++e) s[32 * c + e] = __uint_as_float(u32[c][e]);
         }
-        const bool masked = (j + 1) * BN > L;
+        const bool masked = L - j * BN < BN;
         if (masked) {
           if (!have_mask &&
               !mbar_wait_warp(bar.tree_full(b), (mc >> 1) & 1, abort, p.flags, lim))
