@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
           at = found;
           u64 w;
           if (DRAWN) {
-            w = left(pv[at], qv[at], A);
+            w = A == 0 ? fixed(pv[at]) : left(pv[at], qv[at], A);
           } else {
             w = fallen_already(token[at]) ? 0 : fixed(pv[at]);
           }
@@ -403,19 +403,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
         // without a draft it is the token itself that falls: it leaves the sums, and is gone for
         // the node's other children even where it is too small for the sums
         const int x = token[at];
-        const bool before = fallen_already(x);
-        const u64 w = before ? 0 : left_rounded(pv[at], 0.f, A2, false);
+        const float px = fallen_already(x) ? 0.f : pv[at];
+        const u64 w = left_rounded(px, 0.f, A2, false);
         if (all > w) {
           all -= w;
           W = all;
-          if (!before && pv[at] > 0.f) {  // (x is one of the V)
+          if (px > 0.f) {  // (x is one of the V)
             if (lane == 0) {
               gone[fallen] = x;
-              if (w > 0) {
-                const int c = x / p.chunk;
-                totals[buffer ^ 1][c] -= w;
-                if (c == rank) sums[(x - c0) / p.tile] -= w;
-              }
+              const int c = x / p.chunk;
+              totals[buffer ^ 1][c] -= w;
+              if (c == rank) sums[(x - c0) / p.tile] -= w;
             }
             ++fallen;
             __syncwarp();
