@@ -33,8 +33,8 @@
 //
 // What bounds it.  A step is 64 KB (D 128) and, at the copy rate, 1.5 us of an SM's share of HBM;
 // with one row tile its products and softmax take 0.5 us, so that HBM bounds it: 64 requests of
-// 512 to 8192 tokens x 8 nodes, 12/2 heads (286 MB) take 57.5 us, 73 % of the copy rate, of
-// which some 50 stream; one of 131000 tokens x 32 nodes, 32/8 heads (537 MB) 97 us, 82 %.  With two
+// 512 to 8192 tokens x 8 nodes, 12/2 heads (286 MB) take 56.5 us, 75 % of the copy rate, of
+// which some 50 stream; one of 131000 tokens x 32 nodes, 32/8 heads (537 MB) 95.5 us, 83 %.  With two
 // row tiles a step takes 1.7 us, the pace of attn_fwd.cu (softmax chain and the issue of the
 // products): 8 requests x 200 nodes, 32/4 heads (252 GFLOP) 219 us.  What comes on top: some 5 us
 // until the first tile is there (plan, table entry, copy, each a round trip, and code that
@@ -1145,16 +1145,22 @@ Shape shape_of(int S, int Tn, int Hq, int Hkv, int max_seq_len) {
   s.units = static_cast<long long>(S) * s.segs;
   s.steps = per_seg * s.units;
   // Which kernel, by the bound on the keys.  Device time in us, tree_short.cu / whole segments / cut
-  // segments (lengths from half the bound; D 128 but for *):
+  // segments (batches: lengths from half the bound to it; one request: as long as the bound; D 128
+  // but for *):
   //   requests x heads   rows  100               250               500               800               1200              1800
-  //   1 x 8/2 *            20  3.5 / 7.4 / 13    5.3 / 7.7 / 10    6.9 / 9.2 / 13    9.2 / 9.9 / 11    13 / 12 / 13      16 / 15 / 12
-  //   1 x 32/8             16  4.6 / 8.0 / 15    6.9 / 8.7 / 15    8.7 / 10 / 15     12 / 12 / 13      16 / 15 / 15      21 / 19 / 14
-  //   5 x 12/2             48  7.7 / 8.3 / 15    10 / 9.1 / 15     18 / 12 / 15      26 / 16 / 14      36 / 20 / 15      52 / 26 / 16
-  //   20 x 32/8            32  9.6 / 12 / 16     12 / 14 / 18      18 / 19 / 22      24 / 25 / 26      30 / 26 / 28      44 / 42 / 33
-  //   64 x 12/2            48  9.4 / 9.4 / 16    14 / 12 / 17      21 / 14 / 20      31 / 18 / 23      42 / 22 / 26      60 / 28 / 30
-  //   100 x 16/8           64  27 / 34 / 39      38 / 46 / 55      55 / 59 / 75      75 / 75 / 89      103 / 94 / 101    143 / 128 / 120
-  //   100 x 16/8 *          8  9 / 28 / 32       14 / 32 / 39      21 / 45 / 63      29 / 54 / 76      39 / 67 / 87      54 / 90 / 102
-  //   200 x 8/2            16  9 / 18 / 20       13 / 21 / 27      20 / 33 / 38      27 / 42 / 46      37 / 54 / 53      51 / 72 / 64
+  //   1 x 8/2 *            20  4.4 / 6.9 / 13    6.0 / 7.5 / 9.9   9.1 / 9.6 / 11    13 / 12 / 11      18 / 16 / 11      26 / 20 / 12
+  //   1 x 32/8             16  5.6 / 8.2 / 14    7.8 / 8.9 / 14    12 / 12 / 12      17 / 16 / 14      23 / 20 / 14      33 / 28 / 14
+  //   1 x 32/8             32  7.1 / 8.2 / 14    9.4 / 8.9 / 14    14 / 12 / 12      20 / 16 / 14      27 / 20 / 14      39 / 28 / 15
+  //   1 x 12/2             48  6.6 / 8.0 / 14    10 / 8.7 / 11     17 / 12 / 12      26 / 16 / 13      36 / 20 / 13      54 / 28 / 13
+  //   5 x 12/2             48  7.8 / 8.2 / 14    10 / 8.9 / 14     18 / 12 / 14      26 / 16 / 14      36 / 20 / 14      53 / 26 / 15
+  //   20 x 32/8            32  9.5 / 12 / 15     13 / 14 / 18      18 / 18 / 21      24 / 24 / 25      30 / 25 / 27      44 / 41 / 33
+  //   64 x 12/2            48  9.4 / 9.1 / 15    14 / 11 / 17      21 / 13 / 19      31 / 18 / 23      42 / 22 / 25      60 / 28 / 29
+  //   100 x 16/8           64  27 / 32 / 38      38 / 42 / 53      55 / 54 / 71      75 / 70 / 85      103 / 89 / 97     142 / 124 / 115
+  //   100 x 16/8 *          8  9 / 28 / 32       14 / 32 / 38      21 / 43 / 59      29 / 52 / 74      39 / 65 / 84      54 / 88 / 96
+  //   200 x 8/2            16  9 / 17 / 20       14 / 21 / 26      20 / 31 / 37      27 / 39 / 45      37 / 52 / 51      52 / 71 / 62
+  // The rule takes the better one but for one request of 32 rows (250 keys: 9.4 where whole segments
+  // take 8.9, 500: 14 and 12) and 64 requests of 48 (100 keys: 9.4 and 9.1; 1800: 29 and 28).  At its
+  // own edge, one request of 16 rows and 768 keys takes 16 where cut segments take 14.
   const int rows = s.group * Tn;
   const long long heads = static_cast<long long>(S) * Hkv;
   const bool many = heads >= 304;  // two a SM

@@ -486,8 +486,9 @@ size_t paged_attn_tree_workspace_size(int num_seqs, int Tn, int Hq, int Hkv, int
  * tree_lens[r] outside [0, min(max_seq_len, max_blocks_per_seq * block_size)], makes that
  * request's O and LSE NaN and sets flag bit 2; a parent outside [-1, i) makes those of all
  * its nodes NaN and sets flag bit 16.  A block id outside the pool is read as block 0 and sets flag bit 4 (that
- * request's output is then unspecified).  Slots past the tree may hold any bits.  A NaN in a
- * value may reach O of every node of its request, of those too that do not see it.
+ * request's output is then unspecified).  Slots past the tree may hold any bits.  A NaN or an
+ * infinity in a value may reach O of every node of its request, of those too that do not see it
+ * (in a key it does not).
  */
 int paged_attn_tree(const void *q, const void *k_pool, const void *v_pool,
                     const int32_t *block_table, const int32_t *seq_lens, const int32_t *parents,
