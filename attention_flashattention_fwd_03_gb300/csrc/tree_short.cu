@@ -12,11 +12,11 @@
 // A tile of 64 keys takes some 0.45 us with up to 16 rows, latencies of its loads and products,
 // and 1.9 with 64 (D 128: 128 products a warp, whose accumulators and queries leave three CTAs an
 // SM 56 bytes a thread too few registers: with two, which spill nothing, one request of 48 rows and
-// 100 keys takes 6.2 us instead of 7.6, 64 of them 7.7 instead of 9.4, 100 of 64 rows and 250 keys
-// 37.1 instead of 37.8), where tree_attn.cu takes 1.6 for 128 keys and up to 128 rows.  shape_of in tree_attn.cu has the sizes up to which this kernel is taken, both
-// sides measured.  Eight warps a CTA and four tiles in flight for calls of at most a CTA an SM
-// were no faster up to those sizes (12 heads x 8 nodes on 2 KV heads, 5 requests of 100 tokens:
-// 8.5 us, four warps 7.7).
+// 66 keys takes 6.2 us instead of 7.6, 64 of up to 100 keys 7.7 instead of 9.4, 100 of 64 rows and up
+// to 280 keys 37.1 instead of 37.8), where tree_attn.cu takes 1.6 for 128 keys and up to 128 rows.
+// shape_of in tree_attn.cu has the sizes up to which this kernel is taken, both sides measured.
+// Eight warps a CTA and four tiles in flight for calls of at most a CTA an SM were no faster up to
+// those sizes (12 heads x 8 nodes on 2 KV heads, 5 requests of 100 tokens: 8.5 us, four warps 7.7).
 #include <cuda_runtime.h>
 
 #include "gbattn.h"
